@@ -346,6 +346,133 @@ prn_status prn_head_newton_forward(const void* xproj, const prn_params* params, 
 prn_status prn_head_sequential_forward(const void* xproj, const prn_params* params, const float* A,
                                        int32_t d_head, const void* h0, void* H_out);
 
+/* ---- A token model around the recurrence: lookup, norms, loss ----------
+ * The operators between token ids and the recurrence's inputs, between two
+ * blocks, and between the last block and the loss.  They are not on the
+ * pages; they follow the conventions above (device pointers, caller-owned
+ * buffers and workspace, params->stream, no host synchronisation, argument
+ * checks before anything is enqueued, prn_last_error).  Rows are dense; a row
+ * is one token.  Arithmetic is fp32, each stored value is rounded once to the
+ * storage dtype, every sum over tokens is taken in a fixed order (two calls
+ * give the same bits).  N = 0 is allowed. */
+
+/* no pad id (prn_embed_params.pad_id) */
+#define PRN_NO_PAD INT64_MIN
+
+typedef struct {
+  int32_t dtype;           /* PRN_F32 | PRN_BF16: table, out, dout, dtable              */
+  int32_t token_bytes;     /* 4 or 8: signed token ids                                  */
+  int64_t N;               /* tokens, below 2^31                                        */
+  int64_t V;               /* rows of the table, below 2^31 - 1                         */
+  int64_t d;               /* channels                                                  */
+  float scale;             /* s                                                         */
+  int64_t pad_id;          /* tokens equal to it give rows of zeros and no gradient
+                              (whether or not it is a row of the table); or PRN_NO_PAD  */
+  void* workspace;         /* backward: 256-byte aligned scratch                        */
+  size_t workspace_bytes;  /* >= prn_embed_backward_workspace_bytes(params)             */
+  void* stream;            /* hipStream_t                                               */
+} prn_embed_params;
+
+/* out[n] = s table[tokens[n]]: tokens (N), table (V, d), out (N, d).  A token
+ * outside the table (and not the pad id) gives a row of NaN: its contents are
+ * not read on the host, and nothing is read out of bounds.  Pointers need
+ * only the alignment of their elements; a launch per call, no workspace. */
+prn_status prn_embed(const void* tokens, const void* table, const prn_embed_params* params, void* out);
+
+/* dtable[v] = s * the sum of dout[n] over the n with tokens[n] = v, in order of
+ * n, in fp32: every row of dtable (V, d) is written, the ones of absent tokens
+ * with zeros.  Tokens that are the pad id or outside the table add nothing.
+ * dtable must be 16-byte aligned. */
+prn_status prn_embed_backward(const void* tokens, const void* dout, const prn_embed_params* params,
+                              void* dtable_out);
+size_t prn_embed_backward_workspace_bytes(const prn_embed_params* params);
+
+/* gate activations: silu(g) = g sig(g), or sig(g) */
+enum { PRN_ACT_SILU = 0, PRN_ACT_SIGMOID = 1 };
+
+typedef struct {
+  int32_t dtype;           /* PRN_F32 | PRN_BF16: every N x d tensor                    */
+  int32_t act;             /* PRN_ACT_SILU | PRN_ACT_SIGMOID                            */
+  int64_t N;               /* rows                                                      */
+  int64_t d;               /* channels, 1 .. 8192                                       */
+  float eps;               /* >= 0                                                      */
+  const float* w_post;     /* (d) fp32, or NULL: no norm of h                           */
+  const float* w_pre;      /* (d) fp32, or NULL: no norm of r                           */
+  const float* alpha;      /* (d) fp32 residual scale, or NULL for 1                    */
+  void* workspace;         /* backward: 256-byte aligned scratch                        */
+  size_t workspace_bytes;  /* >= prn_block_norm_backward_workspace_bytes(params)        */
+  void* stream;            /* hipStream_t                                               */
+} prn_block_norm_params;
+
+/* The boundary between two blocks: the norm after a block with its gate and
+ * residual scale, the residual sum, and the norm before the next block.
+ *   u = h rstd(h) w_post    rstd(y) = 1 / sqrt(mean over channels of y^2 + eps)
+ *   v = u act(gate)
+ *   r = x + alpha v
+ *   n = r rstd(r) w_pre     (of r before it is rounded)
+ *   h       (N, d) the block's output (or, with the other parts absent, the
+ *           stream itself: n alone is the norm before the first block)
+ *   gate    (N, d) or NULL (no gate)
+ *   x       (N, d) the residual stream, or NULL (zeros)
+ *   r_out   (N, d) or NULL; n_out (N, d), given exactly when w_pre is
+ * All N x d pointers must be 16-byte aligned.  r_out may alias h or x, n_out
+ * may alias h, gate or x (every row is read before it is written). */
+prn_status prn_block_norm(const void* h, const void* gate, const void* x, const prn_block_norm_params* params,
+                          void* r_out, void* n_out);
+
+/* Gradients at the forward's inputs, given dr = dL/dr (the gradient arriving
+ * along the stream, NULL for zero) and dn = dL/dn (given exactly when w_pre
+ * is).  dh_out, dgate_out, dx_out (N, d), and the fp32 sums over rows
+ * dw_post_out, dw_pre_out, dalpha_out (d): each optional, and NULL where its
+ * input is absent.  The forward's statistics are recomputed, nothing is saved
+ * between the passes.  All N x d pointers must be 16-byte aligned. */
+prn_status prn_block_norm_backward(const void* h, const void* gate, const void* x, const void* dr, const void* dn,
+                                   const prn_block_norm_params* params, void* dh_out, void* dgate_out, void* dx_out,
+                                   float* dw_post_out, float* dw_pre_out, float* dalpha_out);
+size_t prn_block_norm_backward_workspace_bytes(const prn_block_norm_params* params);
+
+typedef struct {
+  int32_t dtype;           /* PRN_F32 | PRN_BF16: x, W, dx, dW                          */
+  int32_t target_bytes;    /* 4 or 8: signed target ids                                 */
+  int64_t N;               /* tokens, below 2^31                                        */
+  int64_t V;               /* vocabulary, 1 .. 2^31 - 1024                              */
+  int64_t d;               /* channels, below 2^20                                      */
+  float scale;             /* s > 0: factor of the logits                               */
+  int64_t ignore_index;    /* rows with this target have loss 0 and no gradient of it   */
+  void* workspace;         /* 256-byte aligned scratch                                  */
+  size_t workspace_bytes;  /* >= prn_vocab_loss_workspace_bytes(params), backward:
+                              >= prn_vocab_loss_backward_workspace_bytes(params)        */
+  void* stream;            /* hipStream_t                                               */
+} prn_vocab_loss_params;
+
+/* Softmax cross entropy over a vocabulary, without the N x V logits in memory:
+ *   z = s x W^T    lse_n = log(sum over v of exp(z_nv))    loss_n = lse_n - z_n,t(n)
+ *   x (N, d), W (V, d) storage dtype, targets (N)
+ *   loss_out (N), lse_out (N) fp32
+ * Logits are fp32 sums of exact bf16 products (bf16), or of products good to
+ * fp32 rounding (fp32 data: six products of its exact three-term bf16 split);
+ * non-finite inputs give non-finite results in their rows.  A target that is
+ * neither ignore_index nor in 0 .. V - 1 gives a NaN loss (nothing is read out
+ * of bounds).  x and W must be 16-byte aligned. */
+prn_status prn_vocab_loss(const void* x, const void* W, const void* targets, const prn_vocab_loss_params* params,
+                          float* loss_out, float* lse_out);
+
+/* Its gradients, in pieces of the vocabulary (the logits are formed again):
+ *   dz = s ((dloss + dlse) p - dloss onehot(t)), p = exp(z - lse); dloss counts as 0 in ignored rows
+ *   dx_out (N, d) = dz W, dW_out (V, d) = dz^T x: storage dtype, each optional
+ *   lse     the forward's lse_out; dloss (N) fp32; dlse (N) fp32 or NULL: the
+ *           gradients arriving at loss_out and lse_out
+ * With bf16 storage dz is rounded once to bf16, relative to the largest
+ * coefficient of the call, for the matrix cores.  A target out of range gives
+ * NaN in its row of dx and in dW.  x, W, dx_out and dW_out must be 16-byte
+ * aligned.  The workspace holds one piece of dz (about 256 MB at most, or 512
+ * bytes per token where that is more) and fp32 sums of dx and of a piece of dW. */
+prn_status prn_vocab_loss_backward(const void* x, const void* W, const void* targets, const float* lse,
+                                   const float* dloss, const float* dlse, const prn_vocab_loss_params* params,
+                                   void* dx_out, void* dW_out);
+size_t prn_vocab_loss_workspace_bytes(const prn_vocab_loss_params* params);
+size_t prn_vocab_loss_backward_workspace_bytes(const prn_vocab_loss_params* params);
+
 /* Host-side check of ragged offsets (the validate_cu_seqlens contract of
  * the shapes/layout page): cu_host has n_seqs + 1 entries, cu[0] = 0,
  * non-decreasing, cu[n_seqs] = N.  cu_host is a HOST pointer. */

@@ -31,7 +31,14 @@ EXPORTS = ("prn_input_proj", "prn_newton_forward", "prn_newton_forward_fused", "
            "prn_newton_backward", "prn_backward_workspace_bytes", "prn_decode_step", "prn_head_newton_forward",
            "prn_head_sequential_forward", "prn_head_workspace_bytes", "prn_validate_cu_seqlens",
            "prn_last_error", "prn_version", "prn_newton_forward_noalloc", "prn_input_proj_backward",
-           "prn_input_proj_backward_workspace_bytes")
+           "prn_input_proj_backward_workspace_bytes",
+           "prn_embed", "prn_embed_backward", "prn_embed_backward_workspace_bytes",
+           "prn_block_norm", "prn_block_norm_backward", "prn_block_norm_backward_workspace_bytes",
+           "prn_vocab_loss", "prn_vocab_loss_backward", "prn_vocab_loss_workspace_bytes",
+           "prn_vocab_loss_backward_workspace_bytes")
+ACTS = {"silu": 0, "sigmoid": 1}
+NO_PAD = -(1 << 63)   # PRN_NO_PAD
+ID_DTYPES = {torch.int32: 4, torch.int64: 8}
 NOALLOC_SCRATCH_BYTES = 32 << 20   # PRN_NOALLOC_SCRATCH_BYTES
 
 
@@ -70,6 +77,52 @@ class prn_params(ctypes.Structure):
     ]
 
 
+class prn_embed_params(ctypes.Structure):
+    _fields_ = [
+        ("dtype", ctypes.c_int32),
+        ("token_bytes", ctypes.c_int32),
+        ("N", ctypes.c_int64),
+        ("V", ctypes.c_int64),
+        ("d", ctypes.c_int64),
+        ("scale", ctypes.c_float),
+        ("pad_id", ctypes.c_int64),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
+        ("stream", ctypes.c_void_p),
+    ]
+
+
+class prn_block_norm_params(ctypes.Structure):
+    _fields_ = [
+        ("dtype", ctypes.c_int32),
+        ("act", ctypes.c_int32),
+        ("N", ctypes.c_int64),
+        ("d", ctypes.c_int64),
+        ("eps", ctypes.c_float),
+        ("w_post", ctypes.c_void_p),
+        ("w_pre", ctypes.c_void_p),
+        ("alpha", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
+        ("stream", ctypes.c_void_p),
+    ]
+
+
+class prn_vocab_loss_params(ctypes.Structure):
+    _fields_ = [
+        ("dtype", ctypes.c_int32),
+        ("target_bytes", ctypes.c_int32),
+        ("N", ctypes.c_int64),
+        ("V", ctypes.c_int64),
+        ("d", ctypes.c_int64),
+        ("scale", ctypes.c_float),
+        ("ignore_index", ctypes.c_int64),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
+        ("stream", ctypes.c_void_p),
+    ]
+
+
 _LIB = None
 
 
@@ -104,6 +157,20 @@ def lib() -> ctypes.CDLL:
         L.prn_validate_cu_seqlens.argtypes = [vp, i64, i64]
         L.prn_last_error.restype = ctypes.c_char_p
         L.prn_version.restype = i32
+        PE, PB, PV = (ctypes.POINTER(c) for c in (prn_embed_params, prn_block_norm_params, prn_vocab_loss_params))
+        L.prn_embed.argtypes = [vp, vp, PE, vp]
+        L.prn_embed_backward.argtypes = [vp, vp, PE, vp]
+        L.prn_block_norm.argtypes = [vp, vp, vp, PB, vp, vp]
+        L.prn_block_norm_backward.argtypes = [vp, vp, vp, vp, vp, PB, vp, vp, vp, vp, vp, vp]
+        L.prn_vocab_loss.argtypes = [vp, vp, vp, PV, vp, vp]
+        L.prn_vocab_loss_backward.argtypes = [vp, vp, vp, vp, vp, vp, PV, vp, vp]
+        for name, ptr in (("prn_embed_backward_workspace_bytes", PE), ("prn_block_norm_backward_workspace_bytes", PB),
+                          ("prn_vocab_loss_workspace_bytes", PV), ("prn_vocab_loss_backward_workspace_bytes", PV)):
+            getattr(L, name).argtypes = [ptr]
+            getattr(L, name).restype = ctypes.c_size_t
+        for name in ("prn_embed", "prn_embed_backward", "prn_block_norm", "prn_block_norm_backward",
+                     "prn_vocab_loss", "prn_vocab_loss_backward"):
+            getattr(L, name).restype = ctypes.c_int
         for name in ("prn_input_proj", "prn_input_proj_backward", "prn_newton_forward", "prn_newton_forward_fused",
                      "prn_newton_forward_noalloc",
                      "prn_sequential_forward",
@@ -462,3 +529,181 @@ def prn_head_sequential_forward(xproj, A, H_out, *, d_head: int = 16, h0=None, s
     Bn, T, d_h = _head_common(xproj, A, H_out, h0, state_last_out, d_head)
     p = make_params("gru", xproj.dtype, Bn, T, d_h, state_last_out=state_last_out, stream=stream)
     _check(lib().prn_head_sequential_forward(_ptr(xproj), ctypes.byref(p), _ptr(A), d_head, _ptr(h0), _ptr(H_out)))
+
+
+# ------------------------------------------------ a token model around the recurrence ---
+
+def _storage(dtype) -> int:
+    if dtype not in DTYPES:
+        raise TypeError(f"unsupported storage dtype {dtype}")
+    return DTYPES[dtype]
+
+
+def _ids(t, name) -> int:
+    _dev(t, name)
+    if t.dtype not in ID_DTYPES:
+        raise TypeError(f"{name} must be int32 or int64, got {t.dtype}")
+    return ID_DTYPES[t.dtype]
+
+
+def _same_device(t, *others) -> None:
+    for o in others:
+        if o is not None and o.device != t.device:
+            raise ValueError(f"tensors on different devices: {t.device} and {o.device}")
+
+
+def _finish_params(p, t, workspace, stream):
+    """Workspace and stream; the stream defaults to the current one of the tensor's device."""
+    if workspace is not None:
+        p.workspace, p.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if stream is None:
+        stream = torch.cuda.current_stream(t.device)
+    p.stream = int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+    return p
+
+
+def _bytes(fn, p) -> int:
+    n = int(fn(ctypes.byref(p)))
+    if n == 0 and prn_last_error():
+        raise PrnError(PRN_ERR_INVALID_ARG, prn_last_error())
+    return n
+
+
+def _embed_params(dtype, id_bytes: int, N: int, V: int, d: int, scale: float, pad_id) -> prn_embed_params:
+    return prn_embed_params(_storage(dtype), id_bytes, N, V, d, scale, NO_PAD if pad_id is None else pad_id)
+
+
+def prn_embed(tokens, table, out, *, scale: float = 1.0, pad_id=None, stream=None) -> None:
+    """out (N, d) = scale * table (V, d) [tokens (N) int32 or int64]."""
+    size = _ids(tokens, "tokens")
+    _dev(table, "table")
+    _dev(out, "out", table.dtype)
+    _same_device(table, tokens, out)
+    V, d = table.shape
+    N = tokens.numel()
+    if tokens.dim() != 1 or out.shape != (N, d):
+        raise ValueError(f"shape mismatch: tokens {tuple(tokens.shape)} table {(V, d)} out {tuple(out.shape)}")
+    p = _finish_params(_embed_params(table.dtype, size, N, V, d, scale, pad_id), table, None, stream)
+    _check(lib().prn_embed(_ptr(tokens), _ptr(table), ctypes.byref(p), _ptr(out)))
+
+
+def prn_embed_backward_workspace_bytes(dtype: torch.dtype, N: int, V: int, d: int) -> int:
+    return _bytes(lib().prn_embed_backward_workspace_bytes, _embed_params(dtype, 8, N, V, d, 1.0, None))
+
+
+def prn_embed_backward(tokens, dout, dtable_out, *, scale: float = 1.0, pad_id=None, workspace=None,
+                       stream=None) -> None:
+    """dtable_out (V, d) = scale * the sums of dout (N, d) over equal tokens (N)."""
+    size = _ids(tokens, "tokens")
+    _dev(dout, "dout")
+    _dev(dtable_out, "dtable_out", dout.dtype)
+    _same_device(dout, tokens, dtable_out, workspace)
+    V, d = dtable_out.shape
+    N = tokens.numel()
+    if tokens.dim() != 1 or dout.shape != (N, d):
+        raise ValueError(f"shape mismatch: tokens {tuple(tokens.shape)} dout {tuple(dout.shape)} dtable {(V, d)}")
+    p = _finish_params(_embed_params(dout.dtype, size, N, V, d, scale, pad_id), dout, workspace, stream)
+    _check(lib().prn_embed_backward(_ptr(tokens), _ptr(dout), ctypes.byref(p), _ptr(dtable_out)))
+
+
+def _norm_params(h, w_post, w_pre, alpha, act, eps, workspace, stream) -> prn_block_norm_params:
+    if act not in ACTS:
+        raise ValueError(f"unknown gate activation {act!r}")
+    N, d = h.shape
+    for t, name in ((w_post, "w_post"), (w_pre, "w_pre"), (alpha, "alpha")):
+        _dev(t, name, torch.float32)
+        if t is not None and t.shape != (d,):
+            raise ValueError(f"{name} must be ({d},), got {tuple(t.shape)}")
+    _same_device(h, w_post, w_pre, alpha, workspace)
+    p = prn_block_norm_params(_storage(h.dtype), ACTS[act], N, d, eps, _ptr(w_post), _ptr(w_pre), _ptr(alpha))
+    return _finish_params(p, h, workspace, stream)
+
+
+def _norm_rows(h, **tensors) -> None:
+    _dev(h, "h")
+    if h.dim() != 2:
+        raise ValueError(f"h must be (N, d), got {tuple(h.shape)}")
+    for name, t in tensors.items():
+        _dev(t, name, h.dtype)
+        if t is not None and t.shape != h.shape:
+            raise ValueError(f"{name} must be {tuple(h.shape)}, got {tuple(t.shape)}")
+    _same_device(h, *tensors.values())
+
+
+def prn_block_norm(h, gate, x, r_out, n_out, *, w_post=None, w_pre=None, alpha=None, act: str = "silu",
+                   eps: float = 1e-6, stream=None) -> None:
+    """r_out = x + alpha * (h rstd(h) w_post) act(gate), n_out = r rstd(r) w_pre: rows of h (N, d); gate, x and
+    the weights (d) fp32 may be None, n_out is given exactly when w_pre is."""
+    _norm_rows(h, gate=gate, x=x, r_out=r_out, n_out=n_out)
+    p = _norm_params(h, w_post, w_pre, alpha, act, eps, None, stream)
+    _check(lib().prn_block_norm(_ptr(h), _ptr(gate), _ptr(x), ctypes.byref(p), _ptr(r_out), _ptr(n_out)))
+
+
+def prn_block_norm_backward_workspace_bytes(dtype: torch.dtype, N: int, d: int) -> int:
+    return _bytes(lib().prn_block_norm_backward_workspace_bytes,
+                  prn_block_norm_params(_storage(dtype), 0, N, d, 0.0))
+
+
+def prn_block_norm_backward(h, gate, x, dr, dn, *, w_post=None, w_pre=None, alpha=None, act: str = "silu",
+                            eps: float = 1e-6, dh_out=None, dgate_out=None, dx_out=None, dw_post_out=None,
+                            dw_pre_out=None, dalpha_out=None, workspace=None, stream=None) -> None:
+    """Gradients at prn_block_norm's inputs from dr (N, d) or None and dn (N, d) (given exactly when w_pre is);
+    every output optional."""
+    _norm_rows(h, gate=gate, x=x, dr=dr, dn=dn, dh_out=dh_out, dgate_out=dgate_out, dx_out=dx_out)
+    p = _norm_params(h, w_post, w_pre, alpha, act, eps, workspace, stream)
+    for t, name in ((dw_post_out, "dw_post_out"), (dw_pre_out, "dw_pre_out"), (dalpha_out, "dalpha_out")):
+        _dev(t, name, torch.float32)
+        if t is not None and t.shape != (h.shape[1],):
+            raise ValueError(f"{name} must be ({h.shape[1]},), got {tuple(t.shape)}")
+    _same_device(h, dw_post_out, dw_pre_out, dalpha_out)
+    _check(lib().prn_block_norm_backward(_ptr(h), _ptr(gate), _ptr(x), _ptr(dr), _ptr(dn), ctypes.byref(p),
+                                         _ptr(dh_out), _ptr(dgate_out), _ptr(dx_out), _ptr(dw_post_out),
+                                         _ptr(dw_pre_out), _ptr(dalpha_out)))
+
+
+def _loss_params(dtype, id_bytes: int, N: int, V: int, d: int, scale: float, ignore_index) -> prn_vocab_loss_params:
+    return prn_vocab_loss_params(_storage(dtype), id_bytes, N, V, d, scale, ignore_index)
+
+
+def _loss_shapes(x, W, targets, **rows):
+    size = _ids(targets, "targets")
+    _dev(x, "x")
+    _dev(W, "W", x.dtype)
+    if x.dim() != 2 or W.dim() != 2 or W.shape[1] != x.shape[1] or targets.shape != (x.shape[0],):
+        raise ValueError(f"shape mismatch: x {tuple(x.shape)} W {tuple(W.shape)} targets {tuple(targets.shape)}")
+    for name, t in rows.items():
+        _dev(t, name, torch.float32)
+        if t is not None and t.shape != (x.shape[0],):
+            raise ValueError(f"{name} must be ({x.shape[0]},), got {tuple(t.shape)}")
+    _same_device(x, W, targets, *rows.values())
+    return size, x.shape[0], W.shape[0], x.shape[1]
+
+
+def prn_vocab_loss_workspace_bytes(dtype: torch.dtype, N: int, V: int, d: int) -> int:
+    return _bytes(lib().prn_vocab_loss_workspace_bytes, _loss_params(dtype, 8, N, V, d, 1.0, -100))
+
+
+def prn_vocab_loss(x, W, targets, loss_out, lse_out, *, scale: float = 1.0, ignore_index: int = -100,
+                   workspace=None, stream=None) -> None:
+    """Softmax cross entropy of the logits scale * x (N, d) W (V, d)^T: loss_out, lse_out (N) fp32."""
+    size, N, V, d = _loss_shapes(x, W, targets, loss_out=loss_out, lse_out=lse_out)
+    p = _finish_params(_loss_params(x.dtype, size, N, V, d, scale, ignore_index), x, workspace, stream)
+    _check(lib().prn_vocab_loss(_ptr(x), _ptr(W), _ptr(targets), ctypes.byref(p), _ptr(loss_out), _ptr(lse_out)))
+
+
+def prn_vocab_loss_backward_workspace_bytes(dtype: torch.dtype, N: int, V: int, d: int) -> int:
+    return _bytes(lib().prn_vocab_loss_backward_workspace_bytes, _loss_params(dtype, 8, N, V, d, 1.0, -100))
+
+
+def prn_vocab_loss_backward(x, W, targets, lse, dloss, *, dlse=None, scale: float = 1.0, ignore_index: int = -100,
+                            dx_out=None, dW_out=None, workspace=None, stream=None) -> None:
+    """dx_out (N, d) and dW_out (V, d), each optional, from dloss (N) and dlse (N) or None."""
+    size, N, V, d = _loss_shapes(x, W, targets, lse=lse, dloss=dloss, dlse=dlse)
+    for t, like, name in ((dx_out, x, "dx_out"), (dW_out, W, "dW_out")):
+        _dev(t, name, x.dtype)
+        if t is not None and t.shape != like.shape:
+            raise ValueError(f"{name} must be {tuple(like.shape)}, got {tuple(t.shape)}")
+    _same_device(x, dx_out, dW_out, workspace)
+    p = _finish_params(_loss_params(x.dtype, size, N, V, d, scale, ignore_index), x, workspace, stream)
+    _check(lib().prn_vocab_loss_backward(_ptr(x), _ptr(W), _ptr(targets), _ptr(lse), _ptr(dloss), _ptr(dlse),
+                                         ctypes.byref(p), _ptr(dx_out), _ptr(dW_out)))

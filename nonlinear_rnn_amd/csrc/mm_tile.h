@@ -1,0 +1,280 @@
+// Matrix-core tiles over bf16 operands of either orientation, for the
+// vocabulary loss: acc = sum over k of A(r, k) B(c, k).
+//
+// Each wave owns WM x WN blocks of 32 x 32; WR x WC waves make a workgroup's
+// tile of BM x BN.  K is walked in stages of BK values, NST stages in LDS,
+// the next ones in flight while one is multiplied.  An operand lies in memory
+// as rows of K ("rows": element (r, k) at r ld + k) or as rows of the other
+// index ("cols": element (r, k) at k ld + r); neither is transposed or copied
+// on the way: both land in LDS as they are, and the "cols" fragments come
+// through ds_read_b64_tr_b16.
+//
+// Loads go straight into LDS (global_load_lds_dwordx4: lane l of a wave's
+// load lands at LDS base + 16 l), 1 KB a wave load.  In LDS the 16-byte
+// chunks of a row are permuted, so that the rows one fragment read touches
+// fall on all banks:
+//   rows: BK = 64: 128-byte rows, chunk c of row r at c ^ ((r / 2) % 8);
+//         BK = 32: 64-byte rows, chunk c at c ^ ((r / 4) % 4)
+//   cols: rows of 2 BM bytes, chunk c of row k at c ^ swz(k); swz keeps the
+//         eight rows of one transposed read (k0 .. k0 + 3 and k0 + 8 ..
+//         k0 + 11) on different banks.
+// A wait for a wave's own loads and a bare barrier make a stage complete (a
+// fence would drain the stages still in flight too).
+//
+// Fragment layout of v_mfma_f32_32x32x16_bf16: lane l feeds row l % 32 of A
+// and column l % 32 of B with the k values 8 (l / 32) .. + 7; accumulator r
+// of lane l holds row 8 (r / 4) + 4 (l / 32) + r % 4, column l % 32.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace prn {
+
+typedef __attribute__((ext_vector_type(8))) __bf16 mm_bf16x8;
+typedef __attribute__((ext_vector_type(16))) float mm_f32x16;
+typedef __attribute__((ext_vector_type(4))) short mm_s16x4;
+typedef __attribute__((ext_vector_type(8))) short mm_s16x8;
+typedef __attribute__((address_space(3))) void* mm_lds_t;
+
+__device__ __attribute__((aligned(16))) const uint32_t kMmZero[4] = {0, 0, 0, 0};
+
+__device__ __forceinline__ uint32_t mm_lds_addr(const void* p) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((mm_lds_t) const_cast<void*>(p)));
+}
+
+// One direct-to-LDS load of 16 bytes per lane to LDS byte lds + 16 lane (lds
+// wave-uniform, through M0, which nothing else here uses; one wait state
+// between the scalar write of M0 and its use).  In asm, so that the compiler
+// does not make every later LDS read wait for it; the stage loop waits.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"   // M0 is a reserved register
+__device__ __forceinline__ void mm_dma(const void* g, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(g), "s"(lds) : "memory", "m0");
+}
+// the same from a wave-uniform base and a byte offset per lane
+__device__ __forceinline__ const void* mm_uniform(const void* p) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
+  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v >> 32));
+  return reinterpret_cast<const void*>(static_cast<uint64_t>(hi) << 32 | lo);
+}
+__device__ __forceinline__ void mm_dma_off(const void* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+               :
+               : "v"(off), "s"(base), "s"(lds)
+               : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+// wait until at most n of this wave's loads are in flight (n <= 15), and for all its LDS reads
+template <int n>
+__device__ __forceinline__ void mm_wait_loads() {
+  static_assert(n >= 0 && n <= 15, "four bits of the load counter");
+  __builtin_amdgcn_s_waitcnt((n & 15) | (7 << 4));
+}
+
+// An operand: `planes` 16-bit matrices `plane` elements apart (one for bf16
+// data, the three terms of fp32 data split by split3), rows ld elements
+// apart, ld a multiple of 8, base 16-byte aligned.  R rows of the tile's
+// index, K values of the summed one.  Along its contiguous index the memory
+// holds a multiple of 8 values per row (the ones past the extent are zeros
+// where that index is k, anything otherwise).
+struct MmOperand {
+  const uint16_t* base;
+  int64_t ld, plane;
+};
+
+// the term pairs of a product: one for bf16, the six of weight 2^-16 or more
+// (bf16split.h) for fp32
+__device__ __forceinline__ int mm_term_a(int t) { return (0x210100 >> (4 * t)) & 3; }   // 0 0 1 0 1 2
+__device__ __forceinline__ int mm_term_b(int t) { return (0x012010 >> (4 * t)) & 3; }   // 0 1 0 2 1 0
+
+template <int WR_, int WC_, int WM_, int WN_, int BK_, int NST_>
+struct MmTile {
+  static constexpr int WR = WR_, WC = WC_, WM = WM_, WN = WN_, BK = BK_, NST = NST_;
+  static constexpr int NW = WR * WC, NTHR = 64 * NW;
+  static constexpr int BM = WR * WM * 32, BN = WC * WN * 32;
+  static constexpr int ABYTES = BM * BK * 2, BBYTES = BN * BK * 2, STAGE = ABYTES + BBYTES;
+  static constexpr int LDS = NST * STAGE;
+  static constexpr int NLA = ABYTES / 1024 / NW, NLB = BBYTES / 1024 / NW;   // wave loads of a wave per stage
+  static_assert(ABYTES % (1024 * NW) == 0 && BBYTES % (1024 * NW) == 0, "stages split evenly over the waves");
+  static_assert(BK == 32 || BK == 64, "row layouts of 64 and 128 bytes");
+  static_assert((NST - 2) * (NLA + NLB) <= 15, "load counter");
+
+  mm_f32x16 acc[WM][WN];
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < WM; ++i)
+#pragma unroll
+      for (int j = 0; j < WN; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+  }
+
+  static __device__ __forceinline__ int row_pos(int r, int c) {
+    return BK == 64 ? c ^ ((r >> 1) & 7) : c ^ ((r >> 2) & 3);
+  }
+  static __device__ __forceinline__ int swz(int k) { return 4 * ((k & 3) | (((k >> 3) & 1) << 2)); }
+
+  // lane's source chunk of wave load li of an operand with BR rows of the
+  // tile index: (row or k within the stage, first element along the contiguous index)
+  template <bool COLS, int BR>
+  static __device__ __forceinline__ void source(int li, int lane, int& slow, int& fast) {
+    const int v = li * 64 + lane;
+    if constexpr (!COLS) {
+      constexpr int CPR = BK / 8;
+      slow = v / CPR;
+      fast = 8 * row_pos(slow, v % CPR);
+    } else {
+      constexpr int CPR = BR / 8;
+      slow = v / CPR;
+      fast = 8 * ((v % CPR) ^ (swz(slow) & (CPR - 1)));
+    }
+  }
+
+  // acc += the product of rows r0 .. of A (R_a of them in all) and c0 .. of B
+  // over k in [k0, k1), for every term pair.  lds: LDS bytes.  k0 a multiple
+  // of 8.  Ends with every wave done reading LDS only after the next barrier.
+  template <bool TA, bool TB>
+  __device__ __forceinline__ void run(uint8_t* lds, const MmOperand& A, int64_t r0, int64_t Ra, const MmOperand& B,
+                                      int64_t c0, int64_t Rb, int64_t k0, int64_t k1, int terms) {
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wr = wave / WC, wc = wave % WC;
+    const int half = lane >> 5, l32 = lane & 31;
+    const int64_t nk = (k1 - k0 + BK - 1) / BK, nfull = (k1 - k0) / BK;
+    const int64_t stages = nk * terms;
+
+    // byte offsets from the tile's first element (rows past the end read the
+    // last row; columns past the end the last chunk: their products are not used)
+    uint32_t offa[NLA], offb[NLB];
+#pragma unroll
+    for (int p = 0; p < NLA; ++p) {
+      int s, f;
+      source<TA, BM>(wave * NLA + p, lane, s, f);
+      const int64_t lim = TA ? (((Ra + 7) & ~int64_t(7)) - 8 - r0) : Ra - 1 - r0;
+      if constexpr (TA) {
+        f = f < lim ? f : static_cast<int>(lim);
+        offa[p] = static_cast<uint32_t>((s * A.ld + f) * 2);
+      } else {
+        s = s < lim ? s : static_cast<int>(lim);
+        offa[p] = static_cast<uint32_t>((s * A.ld + f) * 2);
+      }
+    }
+#pragma unroll
+    for (int p = 0; p < NLB; ++p) {
+      int s, f;
+      source<TB, BN>(wave * NLB + p, lane, s, f);
+      const int64_t lim = TB ? (((Rb + 7) & ~int64_t(7)) - 8 - c0) : Rb - 1 - c0;
+      if constexpr (TB) {
+        f = f < lim ? f : static_cast<int>(lim);
+        offb[p] = static_cast<uint32_t>((s * B.ld + f) * 2);
+      } else {
+        s = s < lim ? s : static_cast<int>(lim);
+        offb[p] = static_cast<uint32_t>((s * B.ld + f) * 2);
+      }
+    }
+    const uint8_t* const a0 = reinterpret_cast<const uint8_t*>(A.base + (TA ? k0 * A.ld + r0 : r0 * A.ld + k0));
+    const uint8_t* const b0 = reinterpret_cast<const uint8_t*>(B.base + (TB ? k0 * B.ld + c0 : c0 * B.ld + k0));
+    const int64_t stepa = 2 * BK * (TA ? A.ld : 1), stepb = 2 * BK * (TB ? B.ld : 1);
+
+    int64_t is_k = 0;   // k tile and term of the next stage to load
+    int is_t = 0;
+    auto issue = [&](int buf) {
+      const uint8_t* ab = a0 + 2 * A.plane * mm_term_a(is_t) + is_k * stepa;
+      const uint8_t* bb = b0 + 2 * B.plane * mm_term_b(is_t) + is_k * stepb;
+      uint8_t* const la = lds + buf * STAGE + wave * NLA * 1024;
+      uint8_t* const lb = lds + buf * STAGE + ABYTES + wave * NLB * 1024;
+      if (is_k < nfull) {
+#pragma unroll
+        for (int p = 0; p < NLA; ++p) mm_dma_off(mm_uniform(ab), offa[p], mm_lds_addr(la + p * 1024));
+#pragma unroll
+        for (int p = 0; p < NLB; ++p) mm_dma_off(mm_uniform(bb), offb[p], mm_lds_addr(lb + p * 1024));
+      } else {
+        // the last, partial stage: chunks past k1 come from the zero chunk
+        const int left = static_cast<int>(k1 - k0 - is_k * BK);
+#pragma unroll
+        for (int p = 0; p < NLA; ++p) {
+          int s, f;
+          source<TA, BM>(wave * NLA + p, lane, s, f);
+          const void* g = (TA ? s : f) < left ? static_cast<const void*>(ab + offa[p]) : static_cast<const void*>(kMmZero);
+          mm_dma(g, mm_lds_addr(la + p * 1024));
+        }
+#pragma unroll
+        for (int p = 0; p < NLB; ++p) {
+          int s, f;
+          source<TB, BN>(wave * NLB + p, lane, s, f);
+          const void* g = (TB ? s : f) < left ? static_cast<const void*>(bb + offb[p]) : static_cast<const void*>(kMmZero);
+          mm_dma(g, mm_lds_addr(lb + p * 1024));
+        }
+      }
+      if (++is_k == nk) {
+        is_k = 0;
+        ++is_t;
+      }
+    };
+
+    // fragment of 32 tile rows from row `at`, k = 16 kb ..
+    const int grp = lane >> 4, jl = lane & 15;
+    const int ksub = 8 * (grp >> 1) + (jl >> 2), csub = 16 * (grp & 1) + 4 * (jl & 3);
+    auto frag_rows = [&](const uint8_t* st, int at, int kb) {
+      const int r = at + l32;
+      return *reinterpret_cast<const mm_bf16x8*>(st + r * (2 * BK) + 16 * row_pos(r, 2 * kb + half));
+    };
+    auto frag_cols = [&](const uint8_t* st, int at, int kb, int rowbytes) {
+      mm_s16x8 v;
+#pragma unroll
+      for (int call = 0; call < 2; ++call) {
+        const int k = 16 * kb + ksub + 4 * call, col = at + csub;
+        const uint8_t* a = st + k * rowbytes + 16 * ((col >> 3) ^ (swz(k) & (rowbytes / 16 - 1))) + 2 * (col & 7);
+        const mm_s16x4 r = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) mm_s16x4*)(a));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[4 * call + e] = r[e];
+      }
+      return __builtin_bit_cast(mm_bf16x8, v);
+    };
+
+    // LDS may still be read by other waves (an earlier tile's last stage)
+    __syncthreads();
+#pragma unroll
+    for (int s = 0; s < NST - 1; ++s)
+      if (s < stages) issue(s);
+    for (int64_t st = 0; st < stages; ++st) {
+      // stage st has landed; every wave is done with the buffer that stage
+      // st + NST - 1 fills
+      asm volatile("" ::: "memory");
+      if (st + NST - 2 < stages)
+        mm_wait_loads<(NST - 2) * (NLA + NLB)>();
+      else
+        mm_wait_loads<0>();
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      if (st + NST - 1 < stages) issue(static_cast<int>((st + NST - 1) % NST));
+      const uint8_t* sa = lds + static_cast<int>(st % NST) * STAGE;
+      const uint8_t* sb = sa + ABYTES;
+#pragma unroll
+      for (int kb = 0; kb < BK / 16; ++kb) {
+        mm_bf16x8 av[WM], bv[WN];
+#pragma unroll
+        for (int j = 0; j < WN; ++j) {
+          const int at = (wc * WN + j) * 32;
+          bv[j] = TB ? frag_cols(sb, at, kb, 2 * BN) : frag_rows(sb, at, kb);
+        }
+#pragma unroll
+        for (int i = 0; i < WM; ++i) {
+          const int at = (wr * WM + i) * 32;
+          av[i] = TA ? frag_cols(sa, at, kb, 2 * BM) : frag_rows(sa, at, kb);
+        }
+#pragma unroll
+        for (int i = 0; i < WM; ++i)
+#pragma unroll
+          for (int j = 0; j < WN; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(av[i], bv[j], acc[i][j], 0, 0, 0);
+      }
+    }
+  }
+};
+
+}  // namespace prn

@@ -1,0 +1,579 @@
+// Softmax cross entropy over a vocabulary, and its gradients, without the
+// N x V logits in memory.
+//
+//   z = s x W^T          lse_n = log sum_v exp z_nv     loss_n = lse_n - z_n,t(n)
+//   dz_nv = s ((dloss_n + dlse_n) p_nv - dloss_n [v = t(n)])     p = exp(z - lse)
+//   dx = dz W            dW = dz^T x
+//
+// Forward: a workgroup keeps a tile of tokens and walks a range of the
+// vocabulary; every tile of logits stays in the matrix-core accumulators
+// and is folded into a running maximum and sum of the lane's token (the
+// tile is W rows x tokens, so that a lane holds one token and many vocabulary
+// entries).  The ranges' (maximum, sum) pairs are joined per token.
+// Backward, in pieces of the vocabulary: the tile of logits is formed again,
+// turned into dz and stored (bf16; fp32 data: as its three bf16 terms); then
+// dx += dz W and dW = dz^T x of the piece.  8 N V d operations in all, two of
+// them for the logits' second time.
+//
+// fp32 data runs as its exact three-term bf16 split (bf16split.h), six term
+// products each: the planes are laid out once per call.
+// dz is stored divided by the largest |dloss|, |dlse|, |dloss + dlse| of the
+// call, so that the usual coefficients (all equal, p - 1 near -1) round to
+// bf16 without loss; the factor comes back, in fp32, where dx and dW are
+// rounded.  Everything else is summed in fp32 in a fixed order.
+#include "vocab_loss.h"
+
+#include <algorithm>
+
+#include "bf16split.h"
+#include "mm_tile.h"
+#include "prn_device.h"
+
+namespace prn {
+namespace {
+
+constexpr int kTerms = 6;
+
+// 4 waves, 256 x 128, 72 KB: two workgroups per CU, so that one's epilogue runs beside the other's products
+using Big = MmTile<2, 2, 4, 2, 32, 3>;
+// few tokens: 128 x 64
+using Few = MmTile<4, 1, 1, 2, 64, 3>;
+
+// ------------------------------------------------------------ operands ---
+
+// The three bf16 terms of fp32 rows (planes R x ldp apart), or a copy of bf16
+// rows; columns d .. ldp - 1 are zeros.  One thread per 8 columns.
+template <bool BF16>
+__global__ void __launch_bounds__(256) k_loss_planes(const void* __restrict__ in, int64_t R, int64_t d, int64_t ldp,
+                                                     uint16_t* __restrict__ out) {
+  const int64_t C = ldp / 8;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= R * C) return;
+  const int64_t r = i / C;
+  const int c0 = static_cast<int>(i - r * C) * 8;
+  if constexpr (BF16) {
+    const uint16_t* p = static_cast<const uint16_t*>(in) + r * d;
+    mm_s16x8 v;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = c0 + e < d ? static_cast<short>(p[c0 + e]) : short(0);
+    *reinterpret_cast<mm_s16x8*>(out + r * ldp + c0) = v;
+  } else {
+    const float* p = static_cast<const float*>(in) + r * d;
+    sp_f32x4 a, b;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      a[e] = c0 + e < d ? p[c0 + e] : 0.0f;
+      b[e] = c0 + 4 + e < d ? p[c0 + 4 + e] : 0.0f;
+    }
+    sp_bf16x8 t[3];
+    split3(a, b, t[0], t[1], t[2]);
+#pragma unroll
+    for (int u = 0; u < 3; ++u) *reinterpret_cast<sp_bf16x8*>(out + (u * R + r) * ldp + c0) = t[u];
+  }
+}
+
+// ------------------------------------------------------------- forward ---
+
+// part[split][n] = (maximum, sum of 2^(c (z - maximum))) of token n over the
+// split's vocabulary tiles, z the plain products x W^T, c = s log2(e) > 0
+template <class Tl>
+__global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_lse(MmOperand W, MmOperand X, int64_t N, int64_t V, int64_t d,
+                                                          int terms, float c, int n_tok, int64_t tiles_per_split,
+                                                          float2* __restrict__ part) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[Tl::LDS];
+  __shared__ float2 hand[Tl::WR][Tl::BN];
+  const int64_t tok = blockIdx.x % n_tok, split = blockIdx.x / n_tok;
+  const int64_t n0 = tok * Tl::BN;
+  const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, l32 = lane & 31;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wr = wave / Tl::WC, wc = wave % Tl::WC;
+  const int64_t v_tiles = (V + Tl::BM - 1) / Tl::BM;
+  const int64_t t0 = split * tiles_per_split, t1 = imin(t0 + tiles_per_split, v_tiles);
+  float m[Tl::WN], s[Tl::WN];
+#pragma unroll
+  for (int j = 0; j < Tl::WN; ++j) {
+    m[j] = -__builtin_inff();
+    s[j] = 0.0f;
+  }
+  for (int64_t t = t0; t < t1; ++t) {
+    const int64_t v0 = t * Tl::BM;
+    Tl tile;
+    tile.clear();
+    tile.template run<false, false>(lds, W, v0, V, X, n0, N, 0, d, terms);
+    if (v0 + Tl::BM > V) {
+#pragma unroll
+      for (int i = 0; i < Tl::WM; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int64_t v = v0 + (wr * Tl::WM + i) * 32 + 8 * (r >> 2) + 4 * half + (r & 3);
+#pragma unroll
+          for (int j = 0; j < Tl::WN; ++j) tile.acc[i][j][r] = v < V ? tile.acc[i][j][r] : -__builtin_inff();
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < Tl::WN; ++j) {
+      float mx = m[j];
+#pragma unroll
+      for (int i = 0; i < Tl::WM; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) mx = fmaxf(mx, tile.acc[i][j][r]);
+      // nothing above -inf yet: any finite reference leaves the sum 0
+      const float ref = mx == -__builtin_inff() ? 0.0f : mx;
+      const float off = -ref * c;
+      float sum = s[j] * ex2(fmaf(m[j], c, off));
+#pragma unroll
+      for (int i = 0; i < Tl::WM; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) sum += ex2(fmaf(tile.acc[i][j][r], c, off));
+      m[j] = mx;
+      s[j] = sum;
+    }
+  }
+  // the two halves of a lane pair hold other rows of the same token, and so
+  // do the waves above one another
+#pragma unroll
+  for (int j = 0; j < Tl::WN; ++j) {
+    const float mo = __shfl_xor(m[j], 32, 64), so = __shfl_xor(s[j], 32, 64);
+    const float mx = fmaxf(m[j], mo), ref = mx == -__builtin_inff() ? 0.0f : mx;
+    const float a = s[j] * ex2((m[j] - ref) * c), b = so * ex2((mo - ref) * c);
+    if (half == 0) hand[wr][(wc * Tl::WN + j) * 32 + l32] = make_float2(mx, a + b);
+  }
+  __syncthreads();
+  for (int i = tid; i < Tl::BN; i += Tl::NTHR) {
+    float mx = hand[0][i].x;
+#pragma unroll
+    for (int w = 1; w < Tl::WR; ++w) mx = fmaxf(mx, hand[w][i].x);
+    const float ref = mx == -__builtin_inff() ? 0.0f : mx;
+    float sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < Tl::WR; ++w) sum += hand[w][i].y * ex2((hand[w][i].x - ref) * c);
+    if (n0 + i < N) part[split * N + n0 + i] = make_float2(mx, sum);
+  }
+}
+
+template <class T>
+__device__ __forceinline__ int64_t target_at(const void* targets, int64_t n) {
+  return static_cast<int64_t>(static_cast<const T*>(targets)[n]);
+}
+__device__ __forceinline__ int64_t target_of(const void* targets, int bytes, int64_t n) {
+  return bytes == 4 ? target_at<int32_t>(targets, n) : target_at<int64_t>(targets, n);
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o, 64);
+  return v;
+}
+
+// One wave per token: joins the splits' pairs; the target's logit is a plain
+// fp32 dot product.  A target outside the vocabulary gives a NaN loss.
+template <bool BF16>
+__global__ void __launch_bounds__(256) k_loss_join(const float2* __restrict__ part, int splits, const void* __restrict__ x,
+                                                   const void* __restrict__ W, const void* __restrict__ targets,
+                                                   int target_bytes, int64_t N, int64_t V, int64_t d, float scale,
+                                                   int64_t ignore, float* __restrict__ loss, float* __restrict__ lse) {
+  using S = Storage<BF16 ? kBF16 : kF32>;
+  const int64_t n = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63;
+  if (n >= N) return;
+  const float c = scale * kLog2e;
+  float m = -__builtin_inff();
+  for (int i = lane; i < splits; i += 64) m = fmaxf(m, part[static_cast<int64_t>(i) * N + n].x);
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
+  const float ref = m == -__builtin_inff() ? 0.0f : m;
+  float s = 0.0f;
+  for (int i = lane; i < splits; i += 64) {
+    const float2 p = part[static_cast<int64_t>(i) * N + n];
+    s += p.y * ex2((p.x - ref) * c);
+  }
+  s = wave_sum(s);
+  const int64_t t = target_of(targets, target_bytes, n);
+  float dot = 0.0f;
+  const bool in = t >= 0 && t < V;
+  if (in && t != ignore) {
+    const typename S::T* xr = static_cast<const typename S::T*>(x) + n * d;
+    const typename S::T* wr = static_cast<const typename S::T*>(W) + t * d;
+    for (int64_t i = lane; i < d; i += 64) dot = fmaf(S::load(xr + i), S::load(wr + i), dot);
+    dot = wave_sum(dot);
+  }
+  if (lane == 0) {
+    const float ln = logf(s);
+    lse[n] = fmaf(ref, scale, ln);
+    loss[n] = t == ignore ? 0.0f : in ? fmaf(ref - dot, scale, ln) : __builtin_nanf("");
+  }
+}
+
+// ------------------------------------------------------------ backward ---
+
+// coefficients of a token's row of dz, divided by the call's largest
+struct RowCoef {
+  float p, one, lse2;   // dz / (s g) = p 2^(c z - lse2) - one at the target
+  int32_t target;       // -1: none
+};
+
+// g[0] = the largest finite |dloss|, |dloss + dlse| (1 if there is none above 0); one workgroup
+__global__ void __launch_bounds__(1024) k_loss_gmax(const float* __restrict__ dloss, const float* __restrict__ dlse,
+                                                    const void* __restrict__ targets, int target_bytes, int64_t ignore,
+                                                    int64_t N, float* __restrict__ g) {
+  __shared__ float w[16];
+  float m = 0.0f;
+  for (int64_t n = threadIdx.x; n < N; n += 1024) {
+    const float one = target_of(targets, target_bytes, n) == ignore ? 0.0f : dloss[n];
+    const float a = fabsf(one), b = dlse ? fabsf(one + dlse[n]) : 0.0f;
+    m = a < __builtin_inff() ? fmaxf(m, a) : m;
+    m = b < __builtin_inff() ? fmaxf(m, b) : m;
+  }
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
+  if ((threadIdx.x & 63) == 0) w[threadIdx.x >> 6] = m;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) m = fmaxf(m, w[i]);
+    g[0] = m > 0.0f ? m : 1.0f;
+  }
+}
+
+__global__ void __launch_bounds__(256) k_loss_coef(const float* __restrict__ dloss, const float* __restrict__ dlse,
+                                                   const float* __restrict__ lse, const void* __restrict__ targets,
+                                                   int target_bytes, int64_t ignore, int64_t N, int64_t V,
+                                                   const float* __restrict__ g, RowCoef* __restrict__ coef) {
+  const int64_t n = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (n >= N) return;
+  const int64_t t = target_of(targets, target_bytes, n);
+  const float gm = g[0];
+  const float one = t == ignore ? 0.0f : dloss[n];
+  RowCoef r;
+  r.p = (dlse ? one + dlse[n] : one) / gm;
+  r.one = one / gm;
+  r.lse2 = lse[n] * kLog2e;
+  r.target = t == ignore ? -1 : static_cast<int32_t>(t);
+  if (t != ignore && (t < 0 || t >= V)) {   // no such entry: the loss was NaN, and so is its gradient
+    r.p = __builtin_nanf("");
+    r.target = -1;
+  }
+  coef[n] = r;
+}
+
+// dz of a tile of W rows x tokens, stored by token rows (ldz apart; planes
+// N ldz apart), through LDS so that the stores are whole 512-byte rows
+template <class Tl, bool BF16>
+__global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_dz(MmOperand W, MmOperand X, int64_t N, int64_t V, int64_t d,
+                                                         int terms, float c, int64_t piece0, int64_t piece1, int n_tok,
+                                                         const RowCoef* __restrict__ coef, uint16_t* __restrict__ dz,
+                                                         int64_t ldz) {
+  constexpr int OUT = Tl::BM * Tl::BN * 2;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[OUT > Tl::LDS ? OUT : Tl::LDS];
+  const int64_t tok = blockIdx.x % n_tok, n0 = tok * Tl::BN;
+  const int64_t v0 = piece0 + blockIdx.x / n_tok * Tl::BM;
+  const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, l32 = lane & 31;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wr = wave / Tl::WC, wc = wave % Tl::WC;
+  Tl tile;
+  tile.clear();
+  tile.template run<false, false>(lds, W, v0, V, X, n0, N, 0, d, terms);
+#pragma unroll
+  for (int j = 0; j < Tl::WN; ++j) {
+    const int64_t n = n0 + (wc * Tl::WN + j) * 32 + l32;
+    const RowCoef rc = coef[n < N ? n : N - 1];
+#pragma unroll
+    for (int i = 0; i < Tl::WM; ++i) {
+      const int64_t vb = v0 + (wr * Tl::WM + i) * 32;
+      const int at = rc.target - static_cast<int>(vb);   // the target's row of this block, if in [0, 32)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) tile.acc[i][j][r] = rc.p * ex2(fmaf(tile.acc[i][j][r], c, -rc.lse2));
+      if (__any(rc.target >= 0 && at >= 0 && at < 32)) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          tile.acc[i][j][r] -= (rc.target >= 0 && at == 8 * (r >> 2) + 4 * half + (r & 3)) ? rc.one : 0.0f;
+      }
+      if (vb + 32 > V) {   // the columns past the vocabulary are zeros (dx sums over them)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          if (vb + 8 * (r >> 2) + 4 * half + (r & 3) >= V) tile.acc[i][j][r] = 0.0f;
+      }
+    }
+  }
+  constexpr int CPR = Tl::BM / 8;   // 16-byte chunks of a token's row
+#pragma unroll
+  for (int u = 0; u < (BF16 ? 1 : 3); ++u) {
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < Tl::WN; ++j) {
+      const int tr = (wc * Tl::WN + j) * 32 + l32;
+#pragma unroll
+      for (int i = 0; i < Tl::WM; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          mm_s16x4 o;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float v = tile.acc[i][j][4 * q + e];
+            if constexpr (BF16) {
+              o[e] = static_cast<short>(Storage<kBF16>::pack(v));
+            } else {
+              const uint32_t b = __float_as_uint(v) & 0xffff0000u;   // the next term of the exact split
+              o[e] = static_cast<short>(b >> 16);
+              tile.acc[i][j][4 * q + e] = v - __uint_as_float(b);
+            }
+          }
+          const int ch = (wr * Tl::WM + i) * 4 + q;
+          *reinterpret_cast<mm_s16x4*>(lds + tr * (2 * Tl::BM) + 16 * (ch ^ (tr & (CPR - 1))) + 8 * half) = o;
+        }
+    }
+    __syncthreads();
+    uint16_t* const out = dz + u * N * ldz + (v0 - piece0);
+    for (int e = tid; e < Tl::BN * CPR; e += Tl::NTHR) {
+      const int tr = e / CPR, ch = e % CPR;
+      if (n0 + tr < N && v0 + 8 * ch < piece1)
+        *reinterpret_cast<mm_s16x8*>(out + (n0 + tr) * ldz + 8 * ch) =
+            *reinterpret_cast<const mm_s16x8*>(lds + tr * (2 * Tl::BM) + 16 * (ch ^ (tr & (CPR - 1))));
+    }
+  }
+}
+
+// P[z][r][c] (+)= sum over k of slice z of A(r, k) B(c, k), fp32; C columns
+template <class Tl, bool TA>
+__global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_mm(MmOperand A, MmOperand B, int64_t R, int64_t C, int64_t K,
+                                                         int64_t k_slice, int terms, int n_col, int add,
+                                                         float* __restrict__ P) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[Tl::LDS];
+  const int64_t c0 = static_cast<int64_t>(blockIdx.x % n_col) * Tl::BN, r0 = static_cast<int64_t>(blockIdx.x / n_col) * Tl::BM;
+  const int64_t z = blockIdx.y, k0 = z * k_slice, k1 = imin(k0 + k_slice, K);
+  const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, l32 = lane & 31;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wr = wave / Tl::WC, wc = wave % Tl::WC;
+  Tl tile;
+  tile.clear();
+  tile.template run<TA, true>(lds, A, r0, R, B, c0, C, k0, k1, terms);
+  // a uniform base and 32-bit offsets within the tile
+  uint8_t* const base = reinterpret_cast<uint8_t*>(P + (z * R + r0) * C + c0);
+  const int rows = static_cast<int>(imin(R - r0, Tl::BM)), cols = static_cast<int>(imin(C - c0, Tl::BN));
+  const uint32_t ldb = static_cast<uint32_t>(C) * 4;
+  const int rl = wr * Tl::WM * 32 + 4 * half, cl = wc * Tl::WN * 32 + l32;
+  const uint32_t at = rl * ldb + cl * 4;
+#pragma unroll
+  for (int i = 0; i < Tl::WM; ++i)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const int ri = 32 * i + 8 * (r >> 2) + (r & 3);
+#pragma unroll
+      for (int j = 0; j < Tl::WN; ++j) {
+        if (rl + ri < rows && cl + 32 * j < cols) {
+          float* const p = reinterpret_cast<float*>(base + (at + ri * ldb + 128 * j));
+          *p = add ? *p + tile.acc[i][j][r] : tile.acc[i][j][r];
+        }
+      }
+    }
+}
+
+// out[i] = the sum over z, in order, of P[z][i], times s g, rounded once
+template <bool BF16>
+__global__ void __launch_bounds__(256) k_loss_out(const float* __restrict__ P, int S, int64_t n,
+                                                  const float* __restrict__ g, float scale,
+                                                  typename Storage<BF16 ? kBF16 : kF32>::T* __restrict__ out) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= n) return;
+  float sum = 0.0f;
+  for (int z = 0; z < S; ++z) sum += P[z * n + i];
+  out[i] = Storage<BF16 ? kBF16 : kF32>::pack(sum * (g[0] * scale));
+}
+
+template <class T>
+__global__ void __launch_bounds__(256) k_loss_zero(T* __restrict__ out, int64_t n) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i < n) out[i] = T(0);
+}
+
+// ---------------------------------------------------------------- plan ---
+
+constexpr int64_t kCus = 256;
+constexpr size_t kPieceBytes = size_t(256) << 20;   // of dz
+
+size_t up(size_t x) { return (x + 255) / 256 * 256; }
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+struct Plan {
+  bool copy;             // x and W are laid out anew (fp32 terms; bf16 rows of no multiple of 8)
+  int planes;
+  int64_t ldp;
+  size_t x_off, w_off, end;
+};
+Plan plan_operands(const LossArgs& a) {
+  Plan p{};
+  p.planes = a.bf16 ? 1 : 3;
+  p.ldp = cdiv(a.d, 8) * 8;
+  p.copy = !a.bf16 || a.d % 8 != 0;
+  p.x_off = 0;
+  p.w_off = p.copy ? up(size_t(p.planes) * a.N * p.ldp * 2) : 0;
+  p.end = p.copy ? p.w_off + up(size_t(p.planes) * a.V * p.ldp * 2) : 0;
+  return p;
+}
+
+struct PlanFw {
+  Plan op;
+  bool few;
+  int64_t n_tok, v_tiles, per_split, splits;
+  size_t part_off, total;
+};
+PlanFw plan_fw(const LossArgs& a) {
+  PlanFw f{};
+  f.op = plan_operands(a);
+  f.few = a.N <= Few::BN;
+  const int64_t bm = f.few ? Few::BM : Big::BM, bn = f.few ? Few::BN : Big::BN;
+  f.n_tok = cdiv(a.N, bn);
+  f.v_tiles = cdiv(a.V, bm);
+  // two workgroups per CU, and whole rounds of them
+  const int64_t want = std::max<int64_t>(1, cdiv(2 * kCus, f.n_tok));
+  f.per_split = std::max<int64_t>(1, f.v_tiles / want);
+  f.splits = cdiv(f.v_tiles, f.per_split);
+  f.part_off = f.op.end;
+  f.total = f.part_off + up(size_t(f.splits) * a.N * sizeof(float2));
+  return f;
+}
+
+struct PlanBw {
+  Plan op;
+  int64_t piece, pieces, ldz;
+  int64_t sx, kx, sw, kw;   // slices of dx's sum (over the piece) and dW's (over the tokens), and their lengths
+  size_t coef_off, g_off, dz_off, px_off, pw_off, total;
+};
+PlanBw plan_bw(const LossArgs& a) {
+  PlanBw b{};
+  b.op = plan_operands(a);
+  const int64_t v_tiles = cdiv(a.V, Big::BM);
+  const size_t row = size_t(a.N) * b.op.planes * 2 * Big::BM;
+  int64_t per = std::max<int64_t>(1, int64_t(kPieceBytes / row));
+  b.pieces = cdiv(v_tiles, per);
+  per = cdiv(v_tiles, b.pieces);
+  b.piece = per * Big::BM;
+  b.pieces = cdiv(a.V, b.piece);
+  b.ldz = b.piece;
+  auto slices = [&](int64_t rows, int64_t K, int64_t* len) {
+    const int64_t tiles = cdiv(rows, Big::BM) * cdiv(a.d, Big::BN);
+    int64_t s = std::max<int64_t>(1, 2 * kCus / tiles);
+    s = std::min<int64_t>(s, std::max<int64_t>(1, K / 512));
+    *len = cdiv(cdiv(K, s), 64) * 64;
+    return cdiv(K, *len);
+  };
+  b.sx = slices(a.N, std::min(b.piece, a.V), &b.kx);
+  b.sw = slices(std::min(b.piece, a.V), a.N, &b.kw);
+  b.coef_off = b.op.end;
+  b.g_off = b.coef_off + up(size_t(a.N) * sizeof(RowCoef));
+  b.dz_off = b.g_off + 256;
+  b.px_off = b.dz_off + up(size_t(a.N) * b.op.planes * b.ldz * 2);
+  b.pw_off = b.px_off + up(size_t(b.sx) * a.N * a.d * 4);
+  b.total = b.pw_off + up(size_t(b.sw) * std::min(b.piece, a.V) * a.d * 4);
+  return b;
+}
+
+void operands(const LossArgs& a, const Plan& p, const void* x, const void* W, MmOperand* X, MmOperand* Wo) {
+  if (!p.copy) {
+    *X = {static_cast<const uint16_t*>(x), a.d, 0};
+    *Wo = {static_cast<const uint16_t*>(W), a.d, 0};
+    return;
+  }
+  auto lay = [&](const void* in, int64_t R, size_t off) {
+    uint16_t* out = reinterpret_cast<uint16_t*>(a.ws + off);
+    const unsigned grid = static_cast<unsigned>(cdiv(R * (p.ldp / 8), 256));
+    if (a.bf16)
+      k_loss_planes<true><<<grid, 256, 0, a.stream>>>(in, R, a.d, p.ldp, out);
+    else
+      k_loss_planes<false><<<grid, 256, 0, a.stream>>>(in, R, a.d, p.ldp, out);
+    return MmOperand{out, p.ldp, R * p.ldp};
+  };
+  *X = lay(x, a.N, p.x_off);
+  *Wo = lay(W, a.V, p.w_off);
+}
+
+}  // namespace
+
+bool loss_fits(const LossArgs& a) {
+  // rows x 16-byte chunks of the operands, and tiles of the logits
+  const double tiles = double(cdiv(a.N, Few::BN)) * double(cdiv(a.V, Few::BM));
+  const double lay = double(std::max(a.N, a.V)) * double(a.d / 8 + 1) / 256, out = double(std::max(a.N, a.V)) * double(a.d) / 256;
+  return std::max({tiles, lay, out}) < 2147483647.0;
+}
+size_t loss_workspace(const LossArgs& a) { return a.N ? plan_fw(a).total : 0; }
+size_t loss_backward_workspace(const LossArgs& a) { return a.N ? plan_bw(a).total : 0; }
+
+void launch_loss(const LossArgs& a, const void* x, const void* W, const void* targets, float* loss, float* lse) {
+  const PlanFw f = plan_fw(a);
+  MmOperand X, Wo;
+  operands(a, f.op, x, W, &X, &Wo);
+  const int terms = a.bf16 ? 1 : kTerms;
+  const float c = a.scale * kLog2e;
+  float2* part = reinterpret_cast<float2*>(a.ws + f.part_off);
+  const unsigned grid = static_cast<unsigned>(f.n_tok * f.splits);
+  if (f.few)
+    k_loss_lse<Few><<<grid, Few::NTHR, 0, a.stream>>>(Wo, X, a.N, a.V, f.op.ldp, terms, c, int(f.n_tok), f.per_split, part);
+  else
+    k_loss_lse<Big><<<grid, Big::NTHR, 0, a.stream>>>(Wo, X, a.N, a.V, f.op.ldp, terms, c, int(f.n_tok), f.per_split, part);
+  const unsigned jg = static_cast<unsigned>(cdiv(a.N, 4));
+  if (a.bf16)
+    k_loss_join<true><<<jg, 256, 0, a.stream>>>(part, int(f.splits), x, W, targets, a.target_bytes, a.N, a.V, a.d,
+                                                a.scale, a.ignore, loss, lse);
+  else
+    k_loss_join<false><<<jg, 256, 0, a.stream>>>(part, int(f.splits), x, W, targets, a.target_bytes, a.N, a.V, a.d,
+                                                 a.scale, a.ignore, loss, lse);
+}
+
+void launch_loss_backward(const LossArgs& a, const void* x, const void* W, const void* targets, const float* lse,
+                          const float* dloss, const float* dlse, void* dx, void* dW) {
+  if (a.N == 0) {   // no token: dW is zero
+    const int64_t n = a.V * a.d;
+    if (dW && a.bf16)
+      k_loss_zero<uint16_t><<<unsigned(cdiv(n, 256)), 256, 0, a.stream>>>(static_cast<uint16_t*>(dW), n);
+    else if (dW)
+      k_loss_zero<float><<<unsigned(cdiv(n, 256)), 256, 0, a.stream>>>(static_cast<float*>(dW), n);
+    return;
+  }
+  const PlanBw b = plan_bw(a);
+  MmOperand X, Wo;
+  operands(a, b.op, x, W, &X, &Wo);
+  const int terms = a.bf16 ? 1 : kTerms;
+  const float c = a.scale * kLog2e;
+  RowCoef* coef = reinterpret_cast<RowCoef*>(a.ws + b.coef_off);
+  float* g = reinterpret_cast<float*>(a.ws + b.g_off);
+  uint16_t* dz = reinterpret_cast<uint16_t*>(a.ws + b.dz_off);
+  float* px = reinterpret_cast<float*>(a.ws + b.px_off);
+  float* pw = reinterpret_cast<float*>(a.ws + b.pw_off);
+  k_loss_gmax<<<1, 1024, 0, a.stream>>>(dloss, dlse, targets, a.target_bytes, a.ignore, a.N, g);
+  k_loss_coef<<<unsigned(cdiv(a.N, 256)), 256, 0, a.stream>>>(dloss, dlse, lse, targets, a.target_bytes, a.ignore, a.N,
+                                                              a.V, g, coef);
+  const int64_t n_tok = cdiv(a.N, Big::BN), n_col = cdiv(a.d, Big::BN);
+  auto out = [&](const float* P, int S, int64_t n, void* o, int64_t at) {
+    const unsigned grid = unsigned(cdiv(n, 256));
+    if (a.bf16)
+      k_loss_out<true><<<grid, 256, 0, a.stream>>>(P, S, n, g, a.scale, static_cast<uint16_t*>(o) + at);
+    else
+      k_loss_out<false><<<grid, 256, 0, a.stream>>>(P, S, n, g, a.scale, static_cast<float*>(o) + at);
+  };
+  for (int64_t v0 = 0; v0 < a.V; v0 += b.piece) {
+    const int64_t v1 = std::min(v0 + b.piece, a.V), nv = v1 - v0;
+    // dz rows reach the end of the piece's last tile of 8: zeros past the vocabulary
+    const int64_t pend = v0 + cdiv(nv, 8) * 8;
+    const unsigned grid = unsigned(n_tok * cdiv(nv, Big::BM));
+    if (a.bf16)
+      k_loss_dz<Big, true><<<grid, Big::NTHR, 0, a.stream>>>(Wo, X, a.N, a.V, b.op.ldp, terms, c, v0, pend, int(n_tok),
+                                                             coef, dz, b.ldz);
+    else
+      k_loss_dz<Big, false><<<grid, Big::NTHR, 0, a.stream>>>(Wo, X, a.N, a.V, b.op.ldp, terms, c, v0, pend, int(n_tok),
+                                                              coef, dz, b.ldz);
+    const MmOperand Z{dz, b.ldz, a.N * b.ldz};
+    if (dx) {
+      const MmOperand Wc{Wo.base + v0 * Wo.ld, Wo.ld, Wo.plane};
+      const dim3 gx(unsigned(cdiv(a.N, Big::BM) * n_col), unsigned(b.sx));
+      k_loss_mm<Big, false><<<gx, Big::NTHR, 0, a.stream>>>(Z, Wc, a.N, a.d, nv, b.kx, terms, int(n_col), v0 > 0, px);
+    }
+    if (dW) {
+      const dim3 gw(unsigned(cdiv(nv, Big::BM) * n_col), unsigned(b.sw));
+      k_loss_mm<Big, true><<<gw, Big::NTHR, 0, a.stream>>>(Z, X, nv, a.d, a.N, b.kw, terms, int(n_col), 0, pw);
+      out(pw, int(b.sw), nv * a.d, dW, v0 * a.d);
+    }
+  }
+  if (dx) out(px, int(b.sx), a.N * a.d, dx, 0);
+}
+
+}  // namespace prn
