@@ -35,6 +35,7 @@ typedef __attribute__((ext_vector_type(8))) __bf16 mm_bf16x8;
 typedef __attribute__((ext_vector_type(16))) float mm_f32x16;
 typedef __attribute__((ext_vector_type(4))) short mm_s16x4;
 typedef __attribute__((ext_vector_type(8))) short mm_s16x8;
+typedef __attribute__((ext_vector_type(4))) uint32_t mm_u32x4;
 typedef __attribute__((address_space(3))) void* mm_lds_t;
 
 __device__ __attribute__((aligned(16))) const uint32_t kMmZero[4] = {0, 0, 0, 0};
@@ -52,13 +53,14 @@ __device__ __forceinline__ uint32_t mm_lds_addr(const void* p) {
 __device__ __forceinline__ void mm_dma(const void* g, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(g), "s"(lds) : "memory", "m0");
 }
-// the same from a wave-uniform base and a byte offset per lane
+// a wave-uniform pointer in scalar registers
 __device__ __forceinline__ const void* mm_uniform(const void* p) {
   const uint64_t v = reinterpret_cast<uint64_t>(p);
   const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
   const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v >> 32));
   return reinterpret_cast<const void*>(static_cast<uint64_t>(hi) << 32 | lo);
 }
+// the load from a wave-uniform base and a byte offset per lane
 __device__ __forceinline__ void mm_dma_off(const void* base, uint32_t off, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
                :
@@ -134,145 +136,170 @@ struct MmTile {
     }
   }
 
-  // acc += the product of rows r0 .. of A (R_a of them in all) and c0 .. of B
-  // over k in [k0, k1), for every term pair.  lds: LDS bytes.  k0 a multiple
-  // of 8.  Ends with every wave done reading LDS only after the next barrier.
+  // The stream of stages: tile after tile, each k0 .. k1 for every term pair.
+  // The loads run NST - 1 stages ahead of the products, across tiles too, so
+  // that the next tile's first stages are in flight during an epilogue.
+  uint8_t* lds;
+  MmOperand A, B;
+  int64_t Ra, Rb, k0, k1;   // rows of the operands in all; the summed range (k0 a multiple of 8)
+  int terms, nk, nfull;
+  uint32_t offa[NLA], offb[NLB];
+  const uint8_t *a0, *b0, *ab, *bb;
+  int at_k, at_t;           // the next stage to load
+  bool more;                // there is one
+  int ahead;                // stages loaded and not yet multiplied
+  int buf_load, buf_use;
+
+  __device__ __forceinline__ void open(uint8_t* lds_, const MmOperand& A_, int64_t Ra_, const MmOperand& B_, int64_t Rb_,
+                                       int64_t k0_, int64_t k1_, int terms_) {
+    lds = lds_, A = A_, B = B_, Ra = Ra_, Rb = Rb_, k0 = k0_, k1 = k1_, terms = terms_;
+    nk = k1 > k0 ? static_cast<int>((k1 - k0 + BK - 1) / BK) : 0;
+    nfull = k1 > k0 ? static_cast<int>((k1 - k0) / BK) : 0;
+    more = false;
+    ahead = buf_load = buf_use = 0;
+  }
+
+  // the next tile to load: rows r0 .. of A, c0 .. of B
   template <bool TA, bool TB>
-  __device__ __forceinline__ void run(uint8_t* lds, const MmOperand& A, int64_t r0, int64_t Ra, const MmOperand& B,
-                                      int64_t c0, int64_t Rb, int64_t k0, int64_t k1, int terms) {
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wr = wave / WC, wc = wave % WC;
-    const int half = lane >> 5, l32 = lane & 31;
-    const int64_t nk = (k1 - k0 + BK - 1) / BK, nfull = (k1 - k0) / BK;
-    const int64_t stages = nk * terms;
+  __device__ __forceinline__ void seek(int64_t r0, int64_t c0) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    offsets<TA, BM, NLA>(wave, lane, A.ld, Ra, r0, offa);
+    offsets<TB, BN, NLB>(wave, lane, B.ld, Rb, c0, offb);
+    a0 = ab = reinterpret_cast<const uint8_t*>(A.base + (TA ? k0 * A.ld + r0 : r0 * A.ld + k0));
+    b0 = bb = reinterpret_cast<const uint8_t*>(B.base + (TB ? k0 * B.ld + c0 : c0 * B.ld + k0));
+    at_k = at_t = 0;
+    more = nk > 0;
+  }
 
-    // byte offsets from the tile's first element (rows past the end read the
-    // last row; columns past the end the last chunk: their products are not used)
-    uint32_t offa[NLA], offb[NLB];
+  // Byte offsets of a wave's loads from the tile's first element.  Rows past
+  // the end read the last row, columns past the end the last chunk: what
+  // comes of them is not used.
+  template <bool COLS, int BR, int NL>
+  static __device__ __forceinline__ void offsets(int wave, int lane, int64_t ld, int64_t R, int64_t r0, uint32_t (&off)[NL]) {
+    const int64_t left = COLS ? ((R + 7) & ~int64_t(7)) - 8 - r0 : R - 1 - r0;
+    const int lim = left < BR ? static_cast<int>(left) : BR;
 #pragma unroll
-    for (int p = 0; p < NLA; ++p) {
+    for (int p = 0; p < NL; ++p) {
       int s, f;
-      source<TA, BM>(wave * NLA + p, lane, s, f);
-      const int64_t lim = TA ? (((Ra + 7) & ~int64_t(7)) - 8 - r0) : Ra - 1 - r0;
-      if constexpr (TA) {
-        f = f < lim ? f : static_cast<int>(lim);
-        offa[p] = static_cast<uint32_t>((s * A.ld + f) * 2);
-      } else {
-        s = s < lim ? s : static_cast<int>(lim);
-        offa[p] = static_cast<uint32_t>((s * A.ld + f) * 2);
+      source<COLS, BR>(wave * NL + p, lane, s, f);
+      if constexpr (COLS) f = f < lim ? f : lim; else s = s < lim ? s : lim;
+      off[p] = static_cast<uint32_t>((s * ld + f) * 2);
+    }
+  }
+  // One operand's loads of a stage.  In the last, partial stage (left < BK
+  // values of k) the chunks past the end come from the zero chunk.
+  template <bool COLS, int BR, int NL>
+  static __device__ __forceinline__ void load_operand(const uint8_t* base, const uint32_t (&off)[NL], uint8_t* dst, int wave,
+                                                      int left) {
+    if (left >= BK) {
+#pragma unroll
+      for (int p = 0; p < NL; ++p) mm_dma_off(mm_uniform(base), off[p], mm_lds_addr(dst + p * 1024));
+    } else {
+      const int lane = threadIdx.x & 63;
+#pragma unroll
+      for (int p = 0; p < NL; ++p) {
+        int s, f;
+        source<COLS, BR>(wave * NL + p, lane, s, f);
+        const void* g = (COLS ? s : f) < left ? static_cast<const void*>(base + off[p]) : static_cast<const void*>(kMmZero);
+        mm_dma(g, mm_lds_addr(dst + p * 1024));
       }
     }
-#pragma unroll
-    for (int p = 0; p < NLB; ++p) {
-      int s, f;
-      source<TB, BN>(wave * NLB + p, lane, s, f);
-      const int64_t lim = TB ? (((Rb + 7) & ~int64_t(7)) - 8 - c0) : Rb - 1 - c0;
-      if constexpr (TB) {
-        f = f < lim ? f : static_cast<int>(lim);
-        offb[p] = static_cast<uint32_t>((s * B.ld + f) * 2);
-      } else {
-        s = s < lim ? s : static_cast<int>(lim);
-        offb[p] = static_cast<uint32_t>((s * B.ld + f) * 2);
+  }
+
+  // load the next stage; after a tile's last one, next() seeks another tile or leaves `more` false
+  template <bool TA, bool TB, class Next>
+  __device__ __forceinline__ void load(Next&& next) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    uint8_t* const dst = lds + buf_load * STAGE;
+    const int left = at_k < nfull ? BK : static_cast<int>(k1 - k0) - at_k * BK;
+    load_operand<TA, BM, NLA>(ab, offa, dst + wave * NLA * 1024, wave, left);
+    load_operand<TB, BN, NLB>(bb, offb, dst + ABYTES + wave * NLB * 1024, wave, left);
+    buf_load = buf_load + 1 == NST ? 0 : buf_load + 1;
+    ++ahead;
+    ab += 2 * BK * (TA ? A.ld : 1);
+    bb += 2 * BK * (TB ? B.ld : 1);
+    if (++at_k == nk) {
+      at_k = 0;
+      ++at_t;
+      ab = a0 + 2 * A.plane * mm_term_a(at_t);
+      bb = b0 + 2 * B.plane * mm_term_b(at_t);
+      if (at_t == terms) {
+        more = false;
+        next();
       }
     }
-    const uint8_t* const a0 = reinterpret_cast<const uint8_t*>(A.base + (TA ? k0 * A.ld + r0 : r0 * A.ld + k0));
-    const uint8_t* const b0 = reinterpret_cast<const uint8_t*>(B.base + (TB ? k0 * B.ld + c0 : c0 * B.ld + k0));
-    const int64_t stepa = 2 * BK * (TA ? A.ld : 1), stepb = 2 * BK * (TB ? B.ld : 1);
+  }
 
-    int64_t is_k = 0;   // k tile and term of the next stage to load
-    int is_t = 0;
-    auto issue = [&](int buf) {
-      const uint8_t* ab = a0 + 2 * A.plane * mm_term_a(is_t) + is_k * stepa;
-      const uint8_t* bb = b0 + 2 * B.plane * mm_term_b(is_t) + is_k * stepb;
-      uint8_t* const la = lds + buf * STAGE + wave * NLA * 1024;
-      uint8_t* const lb = lds + buf * STAGE + ABYTES + wave * NLB * 1024;
-      if (is_k < nfull) {
-#pragma unroll
-        for (int p = 0; p < NLA; ++p) mm_dma_off(mm_uniform(ab), offa[p], mm_lds_addr(la + p * 1024));
-#pragma unroll
-        for (int p = 0; p < NLB; ++p) mm_dma_off(mm_uniform(bb), offb[p], mm_lds_addr(lb + p * 1024));
-      } else {
-        // the last, partial stage: chunks past k1 come from the zero chunk
-        const int left = static_cast<int>(k1 - k0 - is_k * BK);
-#pragma unroll
-        for (int p = 0; p < NLA; ++p) {
-          int s, f;
-          source<TA, BM>(wave * NLA + p, lane, s, f);
-          const void* g = (TA ? s : f) < left ? static_cast<const void*>(ab + offa[p]) : static_cast<const void*>(kMmZero);
-          mm_dma(g, mm_lds_addr(la + p * 1024));
-        }
-#pragma unroll
-        for (int p = 0; p < NLB; ++p) {
-          int s, f;
-          source<TB, BN>(wave * NLB + p, lane, s, f);
-          const void* g = (TB ? s : f) < left ? static_cast<const void*>(bb + offb[p]) : static_cast<const void*>(kMmZero);
-          mm_dma(g, mm_lds_addr(lb + p * 1024));
-        }
-      }
-      if (++is_k == nk) {
-        is_k = 0;
-        ++is_t;
-      }
-    };
-
-    // fragment of 32 tile rows from row `at`, k = 16 kb ..
-    const int grp = lane >> 4, jl = lane & 15;
-    const int ksub = 8 * (grp >> 1) + (jl >> 2), csub = 16 * (grp & 1) + 4 * (jl & 3);
-    auto frag_rows = [&](const uint8_t* st, int at, int kb) {
-      const int r = at + l32;
-      return *reinterpret_cast<const mm_bf16x8*>(st + r * (2 * BK) + 16 * row_pos(r, 2 * kb + half));
-    };
-    auto frag_cols = [&](const uint8_t* st, int at, int kb, int rowbytes) {
-      mm_s16x8 v;
-#pragma unroll
-      for (int call = 0; call < 2; ++call) {
-        const int k = 16 * kb + ksub + 4 * call, col = at + csub;
-        const uint8_t* a = st + k * rowbytes + 16 * ((col >> 3) ^ (swz(k) & (rowbytes / 16 - 1))) + 2 * (col & 7);
-        const mm_s16x4 r = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) mm_s16x4*)(a));
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[4 * call + e] = r[e];
-      }
-      return __builtin_bit_cast(mm_bf16x8, v);
-    };
-
-    // LDS may still be read by other waves (an earlier tile's last stage)
-    __syncthreads();
+  // the first stages of the first tile (after seek)
+  template <bool TA, bool TB, class Next>
+  __device__ __forceinline__ void prime(Next&& next) {
 #pragma unroll
     for (int s = 0; s < NST - 1; ++s)
-      if (s < stages) issue(s);
-    for (int64_t st = 0; st < stages; ++st) {
-      // stage st has landed; every wave is done with the buffer that stage
-      // st + NST - 1 fills
+      if (more) load<TA, TB>(next);
+  }
+
+  // fragment of 32 tile rows from row `at`, k = 16 kb .., of a stage's rows / cols
+  static __device__ __forceinline__ mm_bf16x8 frag_rows(const uint8_t* st, int at, int kb) {
+    const int lane = threadIdx.x & 63, r = at + (lane & 31);
+    return *reinterpret_cast<const mm_bf16x8*>(st + r * (2 * BK) + 16 * row_pos(r, 2 * kb + (lane >> 5)));
+  }
+  template <int ROWBYTES>
+  static __device__ __forceinline__ mm_bf16x8 frag_cols(const uint8_t* st, int at, int kb) {
+    const int lane = threadIdx.x & 63, grp = lane >> 4, jl = lane & 15;
+    const int col = at + 16 * (grp & 1) + 4 * (jl & 3);
+    mm_s16x8 v;
+#pragma unroll
+    for (int call = 0; call < 2; ++call) {
+      const int k = 16 * kb + 8 * (grp >> 1) + (jl >> 2) + 4 * call;
+      const uint8_t* a = st + k * ROWBYTES + 16 * ((col >> 3) ^ (swz(k) & (ROWBYTES / 16 - 1))) + 2 * (col & 7);
+      const mm_s16x4 r = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) mm_s16x4*)(a));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[4 * call + e] = r[e];
+    }
+    return __builtin_bit_cast(mm_bf16x8, v);
+  }
+
+  // acc += the next tile's product
+  template <bool TA, bool TB, class Next>
+  __device__ __forceinline__ void multiply(Next&& next) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wr = wave / WC, wc = wave % WC;
+    const int stages = nk * terms;
+    for (int st = 0; st < stages; ++st) {
+      // this stage has landed; every wave is done with the buffer that the
+      // next load fills
       asm volatile("" ::: "memory");
-      if (st + NST - 2 < stages)
+      if (ahead >= NST - 1)
         mm_wait_loads<(NST - 2) * (NLA + NLB)>();
       else
         mm_wait_loads<0>();
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
-      if (st + NST - 1 < stages) issue(static_cast<int>((st + NST - 1) % NST));
-      const uint8_t* sa = lds + static_cast<int>(st % NST) * STAGE;
+      if (more) load<TA, TB>(next);
+      --ahead;
+      const uint8_t* sa = lds + buf_use * STAGE;
       const uint8_t* sb = sa + ABYTES;
+      buf_use = buf_use + 1 == NST ? 0 : buf_use + 1;
+      mm_bf16x8 av[BK / 16][WM], bv[BK / 16][WN];
 #pragma unroll
       for (int kb = 0; kb < BK / 16; ++kb) {
-        mm_bf16x8 av[WM], bv[WN];
 #pragma unroll
         for (int j = 0; j < WN; ++j) {
           const int at = (wc * WN + j) * 32;
-          bv[j] = TB ? frag_cols(sb, at, kb, 2 * BN) : frag_rows(sb, at, kb);
+          if constexpr (TB) bv[kb][j] = frag_cols<2 * BN>(sb, at, kb); else bv[kb][j] = frag_rows(sb, at, kb);
         }
 #pragma unroll
         for (int i = 0; i < WM; ++i) {
           const int at = (wr * WM + i) * 32;
-          av[i] = TA ? frag_cols(sa, at, kb, 2 * BM) : frag_rows(sa, at, kb);
+          if constexpr (TA) av[kb][i] = frag_cols<2 * BM>(sa, at, kb); else av[kb][i] = frag_rows(sa, at, kb);
         }
+      }
+#pragma unroll
+      for (int kb = 0; kb < BK / 16; ++kb)
 #pragma unroll
         for (int i = 0; i < WM; ++i)
 #pragma unroll
           for (int j = 0; j < WN; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(av[i], bv[j], acc[i][j], 0, 0, 0);
-      }
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(av[kb][i], bv[kb][j], acc[i][j], 0, 0, 0);
     }
   }
 };

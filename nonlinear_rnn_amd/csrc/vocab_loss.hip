@@ -24,6 +24,7 @@
 #include "vocab_loss.h"
 
 #include <algorithm>
+#include <type_traits>
 
 #include "bf16split.h"
 #include "mm_tile.h"
@@ -34,10 +35,31 @@ namespace {
 
 constexpr int kTerms = 6;
 
-// 4 waves, 256 x 128, 72 KB: two workgroups per CU, so that one's epilogue runs beside the other's products
-using Big = MmTile<2, 2, 4, 2, 32, 3>;
+// 8 waves, 256 x 256, 128 KB: the least traffic per product; one workgroup a CU
+using Big = MmTile<2, 4, 4, 2, 64, 2>;
+// 4 waves, 256 x 128, 72 KB: two workgroups a CU, and less waste at narrow edges
+using Mid = MmTile<2, 2, 4, 2, 32, 3>;
 // few tokens: 128 x 64
 using Few = MmTile<4, 1, 1, 2, 64, 3>;
+constexpr int kXcd = 8;
+
+// Workgroups are dealt round-robin to the XCDs.  The i-th unit of work of
+// this workgroup (-1: no more), when every XCD takes a contiguous share of
+// the units, in proportion to its workgroups, so that neighbouring units
+// share its L2.
+__device__ __forceinline__ int64_t unit_of(int64_t i, int64_t units) {
+  const int64_t grid = gridDim.x, x = blockIdx.x % kXcd, slot = blockIdx.x / kXcd;
+  const int64_t q = grid / kXcd, rem = grid % kXcd, before = x * q + imin(x, rem), mine = q + (x < rem ? 1 : 0);
+  const int64_t u = units * before / grid + slot + i * mine;
+  return u < units * (before + mine) / grid ? u : -1;
+}
+// tile u of rows x cols in groups of `group` rows, walked down the group's rows first
+__device__ __forceinline__ void tile_of(int64_t u, int rows, int cols, int group, int64_t& r, int64_t& c) {
+  const int64_t per = static_cast<int64_t>(group) * cols, g = u / per, in = u - g * per;
+  const int64_t h = imin(group, rows - g * group);
+  r = g * group + in % h;
+  c = in / h;
+}
 
 // ------------------------------------------------------------ operands ---
 
@@ -74,80 +96,108 @@ __global__ void __launch_bounds__(256) k_loss_planes(const void* __restrict__ in
 
 // ------------------------------------------------------------- forward ---
 
-// part[split][n] = (maximum, sum of 2^(c (z - maximum))) of token n over the
-// split's vocabulary tiles, z the plain products x W^T, c = s log2(e) > 0
+// part[n][split] = (maximum, sum of 2^(c (z - maximum))) of token n over the
+// split's vocabulary tiles, z the plain products x W^T, c = s log2(e) > 0.
+// A unit is a token tile and a split; four token tiles and their splits are
+// neighbours, so that an XCD's workgroups share the W tiles they walk.
 template <class Tl>
 __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_lse(MmOperand W, MmOperand X, int64_t N, int64_t V, int64_t d,
-                                                          int terms, float c, int n_tok, int64_t tiles_per_split,
+                                                          int terms, float c, int n_tok, int splits, int per_split,
                                                           float2* __restrict__ part) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Tl::LDS];
   __shared__ float2 hand[Tl::WR][Tl::BN];
-  const int64_t tok = blockIdx.x % n_tok, split = blockIdx.x / n_tok;
-  const int64_t n0 = tok * Tl::BN;
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, l32 = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wr = wave / Tl::WC, wc = wave % Tl::WC;
-  const int64_t v_tiles = (V + Tl::BM - 1) / Tl::BM;
-  const int64_t t0 = split * tiles_per_split, t1 = imin(t0 + tiles_per_split, v_tiles);
-  float m[Tl::WN], s[Tl::WN];
-#pragma unroll
-  for (int j = 0; j < Tl::WN; ++j) {
-    m[j] = -__builtin_inff();
-    s[j] = 0.0f;
-  }
-  for (int64_t t = t0; t < t1; ++t) {
-    const int64_t v0 = t * Tl::BM;
-    Tl tile;
-    tile.clear();
-    tile.template run<false, false>(lds, W, v0, V, X, n0, N, 0, d, terms);
-    if (v0 + Tl::BM > V) {
-#pragma unroll
-      for (int i = 0; i < Tl::WM; ++i)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int64_t v = v0 + (wr * Tl::WM + i) * 32 + 8 * (r >> 2) + 4 * half + (r & 3);
-#pragma unroll
-          for (int j = 0; j < Tl::WN; ++j) tile.acc[i][j][r] = v < V ? tile.acc[i][j][r] : -__builtin_inff();
-        }
+  const int v_tiles = static_cast<int>((V + Tl::BM - 1) / Tl::BM);
+  const int64_t units = static_cast<int64_t>(n_tok) * splits;
+  Tl tile;
+  tile.open(lds, W, V, X, N, 0, d, terms);
+  // the loads' place: unit, vocabulary tile
+  int64_t li = 0, lt = 0, lt1 = 0, ltok = 0, lsplit = 0;
+  auto enter = [&]() {
+    const int64_t u = unit_of(li, units);
+    if (u < 0) return false;
+    tile_of(u, n_tok, splits, 4, ltok, lsplit);
+    lt = lsplit * per_split;
+    lt1 = imin(lt + per_split, v_tiles);
+    return true;
+  };
+  auto next = [&]() {
+    if (++lt == lt1) {
+      ++li;
+      if (!enter()) return;
     }
+    tile.template seek<false, false>(lt * Tl::BM, ltok * Tl::BN);
+  };
+  if (!enter()) return;
+  tile.template seek<false, false>(lt * Tl::BM, ltok * Tl::BN);
+  tile.template prime<false, false>(next);
+  for (int64_t i = 0;; ++i) {
+    const int64_t u = unit_of(i, units);
+    if (u < 0) break;
+    int64_t tok, split;
+    tile_of(u, n_tok, splits, 4, tok, split);
+    const int64_t n0 = tok * Tl::BN, t0 = split * per_split, t1 = imin(t0 + per_split, v_tiles);
+    float m[Tl::WN], s[Tl::WN];
 #pragma unroll
     for (int j = 0; j < Tl::WN; ++j) {
-      float mx = m[j];
-#pragma unroll
-      for (int i = 0; i < Tl::WM; ++i)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) mx = fmaxf(mx, tile.acc[i][j][r]);
-      // nothing above -inf yet: any finite reference leaves the sum 0
-      const float ref = mx == -__builtin_inff() ? 0.0f : mx;
-      const float off = -ref * c;
-      float sum = s[j] * ex2(fmaf(m[j], c, off));
-#pragma unroll
-      for (int i = 0; i < Tl::WM; ++i)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) sum += ex2(fmaf(tile.acc[i][j][r], c, off));
-      m[j] = mx;
-      s[j] = sum;
+      m[j] = -__builtin_inff();
+      s[j] = 0.0f;
     }
-  }
-  // the two halves of a lane pair hold other rows of the same token, and so
-  // do the waves above one another
+    for (int64_t t = t0; t < t1; ++t) {
+      const int64_t v0 = t * Tl::BM;
+      tile.clear();
+      tile.template multiply<false, false>(next);
+      if (v0 + Tl::BM > V) {
+        const int left = static_cast<int>(V - v0) - wr * Tl::WM * 32 - 4 * half;
 #pragma unroll
-  for (int j = 0; j < Tl::WN; ++j) {
-    const float mo = __shfl_xor(m[j], 32, 64), so = __shfl_xor(s[j], 32, 64);
-    const float mx = fmaxf(m[j], mo), ref = mx == -__builtin_inff() ? 0.0f : mx;
-    const float a = s[j] * ex2((m[j] - ref) * c), b = so * ex2((mo - ref) * c);
-    if (half == 0) hand[wr][(wc * Tl::WN + j) * 32 + l32] = make_float2(mx, a + b);
-  }
-  __syncthreads();
-  for (int i = tid; i < Tl::BN; i += Tl::NTHR) {
-    float mx = hand[0][i].x;
+        for (int i2 = 0; i2 < Tl::WM; ++i2)
 #pragma unroll
-    for (int w = 1; w < Tl::WR; ++w) mx = fmaxf(mx, hand[w][i].x);
-    const float ref = mx == -__builtin_inff() ? 0.0f : mx;
-    float sum = 0.0f;
+          for (int r = 0; r < 16; ++r)
 #pragma unroll
-    for (int w = 0; w < Tl::WR; ++w) sum += hand[w][i].y * ex2((hand[w][i].x - ref) * c);
-    if (n0 + i < N) part[split * N + n0 + i] = make_float2(mx, sum);
+            for (int j = 0; j < Tl::WN; ++j)
+              tile.acc[i2][j][r] = 32 * i2 + 8 * (r >> 2) + (r & 3) < left ? tile.acc[i2][j][r] : -__builtin_inff();
+      }
+#pragma unroll
+      for (int j = 0; j < Tl::WN; ++j) {
+        float mx = m[j];
+#pragma unroll
+        for (int i2 = 0; i2 < Tl::WM; ++i2)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) mx = fmaxf(mx, tile.acc[i2][j][r]);
+        // nothing above -inf yet: any finite reference leaves the sum 0
+        const float off = mx == -__builtin_inff() ? 0.0f : -mx * c;
+        float sum = s[j] * ex2(fmaf(m[j], c, off));
+#pragma unroll
+        for (int i2 = 0; i2 < Tl::WM; ++i2)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) sum += ex2(fmaf(tile.acc[i2][j][r], c, off));
+        m[j] = mx;
+        s[j] = sum;
+      }
+    }
+    // the two halves of a lane pair hold other rows of the same token, and so
+    // do the waves above one another
+#pragma unroll
+    for (int j = 0; j < Tl::WN; ++j) {
+      const float mo = __shfl_xor(m[j], 32, 64), so = __shfl_xor(s[j], 32, 64);
+      const float mx = fmaxf(m[j], mo), ref = mx == -__builtin_inff() ? 0.0f : mx;
+      const float a = s[j] * ex2((m[j] - ref) * c), b = so * ex2((mo - ref) * c);
+      if (half == 0) hand[wr][(wc * Tl::WN + j) * 32 + l32] = make_float2(mx, a + b);
+    }
+    __syncthreads();
+    for (int e = tid; e < Tl::BN; e += Tl::NTHR) {
+      float mx = hand[0][e].x;
+#pragma unroll
+      for (int w = 1; w < Tl::WR; ++w) mx = fmaxf(mx, hand[w][e].x);
+      const float ref = mx == -__builtin_inff() ? 0.0f : mx;
+      float sum = 0.0f;
+#pragma unroll
+      for (int w = 0; w < Tl::WR; ++w) sum += hand[w][e].y * ex2((hand[w][e].x - ref) * c);
+      if (n0 + e < N) part[(n0 + e) * splits + split] = make_float2(mx, sum);
+    }
+    __syncthreads();
   }
 }
 
@@ -178,13 +228,13 @@ __global__ void __launch_bounds__(256) k_loss_join(const float2* __restrict__ pa
   if (n >= N) return;
   const float c = scale * kLog2e;
   float m = -__builtin_inff();
-  for (int i = lane; i < splits; i += 64) m = fmaxf(m, part[static_cast<int64_t>(i) * N + n].x);
+  for (int i = lane; i < splits; i += 64) m = fmaxf(m, part[n * splits + i].x);
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
   const float ref = m == -__builtin_inff() ? 0.0f : m;
   float s = 0.0f;
   for (int i = lane; i < splits; i += 64) {
-    const float2 p = part[static_cast<int64_t>(i) * N + n];
+    const float2 p = part[n * splits + i];
     s += p.y * ex2((p.x - ref) * c);
   }
   s = wave_sum(s);
@@ -212,13 +262,14 @@ struct RowCoef {
   int32_t target;       // -1: none
 };
 
-// g[0] = the largest finite |dloss|, |dloss + dlse| (1 if there is none above 0); one workgroup
+// the largest finite |dloss|, |dloss + dlse| of each workgroup's tokens
+constexpr int kMaxParts = 64;
 __global__ void __launch_bounds__(1024) k_loss_gmax(const float* __restrict__ dloss, const float* __restrict__ dlse,
                                                     const void* __restrict__ targets, int target_bytes, int64_t ignore,
                                                     int64_t N, float* __restrict__ g) {
   __shared__ float w[16];
   float m = 0.0f;
-  for (int64_t n = threadIdx.x; n < N; n += 1024) {
+  for (int64_t n = static_cast<int64_t>(blockIdx.x) * 1024 + threadIdx.x; n < N; n += static_cast<int64_t>(gridDim.x) * 1024) {
     const float one = target_of(targets, target_bytes, n) == ignore ? 0.0f : dloss[n];
     const float a = fabsf(one), b = dlse ? fabsf(one + dlse[n]) : 0.0f;
     m = a < __builtin_inff() ? fmaxf(m, a) : m;
@@ -231,18 +282,22 @@ __global__ void __launch_bounds__(1024) k_loss_gmax(const float* __restrict__ dl
   if (threadIdx.x == 0) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) m = fmaxf(m, w[i]);
-    g[0] = m > 0.0f ? m : 1.0f;
+    g[1 + blockIdx.x] = m;
   }
 }
 
+// the tokens' coefficients; g[0] = the largest of the parts (1 if none is above 0)
 __global__ void __launch_bounds__(256) k_loss_coef(const float* __restrict__ dloss, const float* __restrict__ dlse,
                                                    const float* __restrict__ lse, const void* __restrict__ targets,
                                                    int target_bytes, int64_t ignore, int64_t N, int64_t V,
-                                                   const float* __restrict__ g, RowCoef* __restrict__ coef) {
+                                                   float* __restrict__ g, int parts, RowCoef* __restrict__ coef) {
+  float gm = 0.0f;
+  for (int i = 0; i < parts; ++i) gm = fmaxf(gm, g[1 + i]);
+  if (gm == 0.0f) gm = 1.0f;
   const int64_t n = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (n == 0) g[0] = gm;
   if (n >= N) return;
   const int64_t t = target_of(targets, target_bytes, n);
-  const float gm = g[0];
   const float one = t == ignore ? 0.0f : dloss[n];
   RowCoef r;
   r.p = (dlse ? one + dlse[n] : one) / gm;
@@ -256,103 +311,155 @@ __global__ void __launch_bounds__(256) k_loss_coef(const float* __restrict__ dlo
   coef[n] = r;
 }
 
-// dz of a tile of W rows x tokens, stored by token rows (ldz apart; planes
-// N ldz apart), through LDS so that the stores are whole 512-byte rows
+// dz of the vocabulary tiles of a piece (first entry piece0, rows to be
+// written up to piece1), stored by token rows (ldz apart; planes N ldz
+// apart).  A lane holds four neighbouring entries of its token at a time and
+// the other half of the wave the next four: a swap of the halves makes them
+// eight, 16 bytes a store.
 template <class Tl, bool BF16>
 __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_dz(MmOperand W, MmOperand X, int64_t N, int64_t V, int64_t d,
                                                          int terms, float c, int64_t piece0, int64_t piece1, int n_tok,
                                                          const RowCoef* __restrict__ coef, uint16_t* __restrict__ dz,
                                                          int64_t ldz) {
-  constexpr int OUT = Tl::BM * Tl::BN * 2;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[OUT > Tl::LDS ? OUT : Tl::LDS];
-  const int64_t tok = blockIdx.x % n_tok, n0 = tok * Tl::BN;
-  const int64_t v0 = piece0 + blockIdx.x / n_tok * Tl::BM;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[Tl::LDS];
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, l32 = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wr = wave / Tl::WC, wc = wave % Tl::WC;
+  const int v_tiles = static_cast<int>((piece1 - piece0 + Tl::BM - 1) / Tl::BM);
+  const int64_t units = static_cast<int64_t>(n_tok) * v_tiles;
+  constexpr int kGroup = 8;   // vocabulary tiles that an XCD's workgroups share
   Tl tile;
-  tile.clear();
-  tile.template run<false, false>(lds, W, v0, V, X, n0, N, 0, d, terms);
+  tile.open(lds, W, V, X, N, 0, d, terms);
+  int64_t li = 0;
+  auto next = [&]() {
+    const int64_t u = unit_of(li++, units);
+    if (u < 0) return;
+    int64_t vt, tok;
+    tile_of(u, v_tiles, n_tok, kGroup, vt, tok);
+    tile.template seek<false, false>(piece0 + vt * Tl::BM, tok * Tl::BN);
+  };
+  next();
+  tile.template prime<false, false>(next);
+  for (int64_t i = 0;; ++i) {
+    const int64_t u = unit_of(i, units);
+    if (u < 0) break;
+    int64_t vt, tok;
+    tile_of(u, v_tiles, n_tok, kGroup, vt, tok);
+    const int64_t v0 = piece0 + vt * Tl::BM, n0 = tok * Tl::BN;
+    // this lane's tokens.  Their coefficients are waited for here, beside the
+    // tile's first stage: a wait after the products would drain the next
+    // tile's loads
+    RowCoef rc[Tl::WN];
 #pragma unroll
-  for (int j = 0; j < Tl::WN; ++j) {
-    const int64_t n = n0 + (wc * Tl::WN + j) * 32 + l32;
-    const RowCoef rc = coef[n < N ? n : N - 1];
+    for (int j = 0; j < Tl::WN; ++j) rc[j] = coef[imin(n0 + (wc * Tl::WN + j) * 32 + l32, N - 1)];
 #pragma unroll
-    for (int i = 0; i < Tl::WM; ++i) {
-      const int64_t vb = v0 + (wr * Tl::WM + i) * 32;
-      const int at = rc.target - static_cast<int>(vb);   // the target's row of this block, if in [0, 32)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) tile.acc[i][j][r] = rc.p * ex2(fmaf(tile.acc[i][j][r], c, -rc.lse2));
-      if (__any(rc.target >= 0 && at >= 0 && at < 32)) {
-#pragma unroll
-        for (int r = 0; r < 16; ++r)
-          tile.acc[i][j][r] -= (rc.target >= 0 && at == 8 * (r >> 2) + 4 * half + (r & 3)) ? rc.one : 0.0f;
-      }
-      if (vb + 32 > V) {   // the columns past the vocabulary are zeros (dx sums over them)
-#pragma unroll
-        for (int r = 0; r < 16; ++r)
-          if (vb + 8 * (r >> 2) + 4 * half + (r & 3) >= V) tile.acc[i][j][r] = 0.0f;
-      }
-    }
-  }
-  constexpr int CPR = Tl::BM / 8;   // 16-byte chunks of a token's row
-#pragma unroll
-  for (int u = 0; u < (BF16 ? 1 : 3); ++u) {
-    __syncthreads();
+    for (int j = 0; j < Tl::WN; ++j) asm volatile("" : "+v"(rc[j].p), "+v"(rc[j].one), "+v"(rc[j].lse2), "+v"(rc[j].target));
+    tile.clear();
+    tile.template multiply<false, false>(next);
+    uint8_t* const base = reinterpret_cast<uint8_t*>(dz + n0 * ldz + (v0 - piece0));
+    const int rows = static_cast<int>(imin(piece1 - v0, Tl::BM)), toks = static_cast<int>(imin(N - n0, Tl::BN));
+    const int vocab_left = static_cast<int>(imin(V - v0, Tl::BM));
 #pragma unroll
     for (int j = 0; j < Tl::WN; ++j) {
-      const int tr = (wc * Tl::WN + j) * 32 + l32;
+      const int tl = (wc * Tl::WN + j) * 32 + l32;
+      const uint32_t at_row = static_cast<uint32_t>(tl) * static_cast<uint32_t>(2 * ldz);
+      // the target's row of this tile (negative or past the tile: elsewhere)
+      const int at = rc[j].target < 0 ? -1 : static_cast<int>(imax(imin(rc[j].target - v0, 1 << 20), -1));
 #pragma unroll
-      for (int i = 0; i < Tl::WM; ++i)
+      for (int i2 = 0; i2 < Tl::WM; ++i2) {
+        const int vb = (wr * Tl::WM + i2) * 32;   // the block's first row of the tile
+        float v[16];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          mm_s16x4 o;
+        for (int r = 0; r < 16; ++r) v[r] = rc[j].p * ex2(fmaf(tile.acc[i2][j][r], c, -rc[j].lse2));
+        if (__any(at >= vb && at < vb + 32)) {
+          const int rel = at - vb - 4 * half;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float v = tile.acc[i][j][4 * q + e];
-            if constexpr (BF16) {
-              o[e] = static_cast<short>(Storage<kBF16>::pack(v));
-            } else {
-              const uint32_t b = __float_as_uint(v) & 0xffff0000u;   // the next term of the exact split
-              o[e] = static_cast<short>(b >> 16);
-              tile.acc[i][j][4 * q + e] = v - __uint_as_float(b);
-            }
-          }
-          const int ch = (wr * Tl::WM + i) * 4 + q;
-          *reinterpret_cast<mm_s16x4*>(lds + tr * (2 * Tl::BM) + 16 * (ch ^ (tr & (CPR - 1))) + 8 * half) = o;
+          for (int r = 0; r < 16; ++r) v[r] -= rel == 8 * (r >> 2) + (r & 3) ? rc[j].one : 0.0f;
         }
-    }
-    __syncthreads();
-    uint16_t* const out = dz + u * N * ldz + (v0 - piece0);
-    for (int e = tid; e < Tl::BN * CPR; e += Tl::NTHR) {
-      const int tr = e / CPR, ch = e % CPR;
-      if (n0 + tr < N && v0 + 8 * ch < piece1)
-        *reinterpret_cast<mm_s16x8*>(out + (n0 + tr) * ldz + 8 * ch) =
-            *reinterpret_cast<const mm_s16x8*>(lds + tr * (2 * Tl::BM) + 16 * (ch ^ (tr & (CPR - 1))));
+        if (vb + 32 > vocab_left) {   // the columns past the vocabulary are zeros (dx sums over them)
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            if (vb + 4 * half + 8 * (r >> 2) + (r & 3) >= vocab_left) v[r] = 0.0f;
+        }
+#pragma unroll
+        for (int t = 0; t < (BF16 ? 1 : 3); ++t) {
+          uint32_t w[4][2];
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float &x0 = v[4 * q + 2 * e], &x1 = v[4 * q + 2 * e + 1];
+              if constexpr (BF16) {
+                w[q][e] = Storage<kBF16>::pack(x0) | static_cast<uint32_t>(Storage<kBF16>::pack(x1)) << 16;
+              } else {   // the next terms of the exact split
+                const uint32_t b0 = __float_as_uint(x0) & 0xffff0000u, b1 = __float_as_uint(x1) & 0xffff0000u;
+                w[q][e] = b1 | b0 >> 16;
+                x0 -= __uint_as_float(b0);
+                x1 -= __uint_as_float(b1);
+              }
+            }
+#pragma unroll
+          for (int q = 0; q < 4; q += 2) {
+            const auto s0 = __builtin_amdgcn_permlane32_swap(w[q][0], w[q + 1][0], false, false);
+            const auto s1 = __builtin_amdgcn_permlane32_swap(w[q][1], w[q + 1][1], false, false);
+            const int col = vb + 8 * (q + half);
+            if (tl < toks && col < rows)
+              gstore(reinterpret_cast<mm_u32x4*>(base + t * (2 * N * ldz) + (at_row + 2 * col)),
+                     mm_u32x4{s0[0], s1[0], s0[1], s1[1]});
+          }
+        }
+      }
     }
   }
 }
 
-// P[z][r][c] (+)= sum over k of slice z of A(r, k) B(c, k), fp32; C columns
-template <class Tl, bool TA>
+// P[z][r][c] (+)= sum over k of slice z of A(r, k) B(c, k), fp32, C columns; or,
+// with `out`, the last of the sums times s g, rounded once to out[r][c].
+// One workgroup per tile and slice, neighbours on one XCD.
+template <class Tl, bool TA, bool BF16>
 __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_mm(MmOperand A, MmOperand B, int64_t R, int64_t C, int64_t K,
-                                                         int64_t k_slice, int terms, int n_col, int add,
-                                                         float* __restrict__ P) {
+                                                         int64_t k_slice, int terms, int n_col, int slices, int add,
+                                                         float* __restrict__ P, void* __restrict__ out,
+                                                         const float* __restrict__ g, float scale) {
+  using T = typename Storage<BF16 ? kBF16 : kF32>::T;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Tl::LDS];
-  const int64_t c0 = static_cast<int64_t>(blockIdx.x % n_col) * Tl::BN, r0 = static_cast<int64_t>(blockIdx.x / n_col) * Tl::BM;
-  const int64_t z = blockIdx.y, k0 = z * k_slice, k1 = imin(k0 + k_slice, K);
+  const int64_t u = unit_of(0, gridDim.x);
+  const int64_t tiles = gridDim.x / slices, z = u / tiles, ti = u - z * tiles;
+  const int64_t c0 = ti % n_col * Tl::BN, r0 = ti / n_col * Tl::BM;
+  const int64_t k0 = z * k_slice, k1 = imin(k0 + k_slice, K);
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, l32 = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wr = wave / Tl::WC, wc = wave % Tl::WC;
   Tl tile;
-  tile.clear();
-  tile.template run<TA, true>(lds, A, r0, R, B, c0, C, k0, k1, terms);
+  tile.open(lds, A, R, B, C, k0, k1, terms);
+  auto next = []() {};
+  tile.template seek<TA, true>(r0, c0);
+  tile.template prime<TA, true>(next);
   // a uniform base and 32-bit offsets within the tile
   uint8_t* const base = reinterpret_cast<uint8_t*>(P + (z * R + r0) * C + c0);
   const int rows = static_cast<int>(imin(R - r0, Tl::BM)), cols = static_cast<int>(imin(C - c0, Tl::BN));
   const uint32_t ldb = static_cast<uint32_t>(C) * 4;
   const int rl = wr * Tl::WM * 32 + 4 * half, cl = wc * Tl::WN * 32 + l32;
   const uint32_t at = rl * ldb + cl * 4;
+  if (add) {   // the sums so far, loaded beside the first stage
+#pragma unroll
+    for (int i = 0; i < Tl::WM; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int ri = 32 * i + 8 * (r >> 2) + (r & 3);
+#pragma unroll
+        for (int j = 0; j < Tl::WN; ++j)
+          tile.acc[i][j][r] = rl + ri < rows && cl + 32 * j < cols
+                                  ? *reinterpret_cast<const float*>(base + (at + ri * ldb + 128 * j))
+                                  : 0.0f;
+      }
+  } else {
+    tile.clear();
+  }
+  tile.template multiply<TA, true>(next);
+  const float f = out ? g[0] * scale : 1.0f;
+  T* const obase = static_cast<T*>(out) + r0 * C + c0;
+  const uint32_t oat = rl * static_cast<uint32_t>(C) + cl;
 #pragma unroll
   for (int i = 0; i < Tl::WM; ++i)
 #pragma unroll
@@ -361,8 +468,10 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_mm(MmOperand A, MmOperand 
 #pragma unroll
       for (int j = 0; j < Tl::WN; ++j) {
         if (rl + ri < rows && cl + 32 * j < cols) {
-          float* const p = reinterpret_cast<float*>(base + (at + ri * ldb + 128 * j));
-          *p = add ? *p + tile.acc[i][j][r] : tile.acc[i][j][r];
+          if (out)
+            obase[oat + ri * static_cast<uint32_t>(C) + 32 * j] = Storage<BF16 ? kBF16 : kF32>::pack(tile.acc[i][j][r] * f);
+          else
+            *reinterpret_cast<float*>(base + (at + ri * ldb + 128 * j)) = tile.acc[i][j][r];
         }
       }
     }
@@ -389,7 +498,7 @@ __global__ void __launch_bounds__(256) k_loss_zero(T* __restrict__ out, int64_t 
 // ---------------------------------------------------------------- plan ---
 
 constexpr int64_t kCus = 256;
-constexpr size_t kPieceBytes = size_t(256) << 20;   // of dz
+constexpr size_t kPieceBytes = size_t(512) << 20;   // of dz
 
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -411,23 +520,39 @@ Plan plan_operands(const LossArgs& a) {
   return p;
 }
 
+// The tile for a product whose tile columns run over `cols`: Mid takes about
+// 1.15 times Big's time per product (measured below), which pays where 256
+// columns a tile would waste more.
+bool take_big(int64_t cols) { return cdiv(cols, Big::BN) * Big::BN * 100 <= cdiv(cols, Mid::BN) * Mid::BN * 115; }
+
 struct PlanFw {
   Plan op;
-  bool few;
-  int64_t n_tok, v_tiles, per_split, splits;
+  int kind;   // 0 Few, 1 Mid, 2 Big
+  int64_t n_tok, splits, per_split, grid;
   size_t part_off, total;
 };
 PlanFw plan_fw(const LossArgs& a) {
   PlanFw f{};
   f.op = plan_operands(a);
-  f.few = a.N <= Few::BN;
-  const int64_t bm = f.few ? Few::BM : Big::BM, bn = f.few ? Few::BN : Big::BN;
+  f.kind = a.N <= Few::BN ? 0 : take_big(a.N) ? 2 : 1;
+  const int64_t bm = f.kind == 0 ? Few::BM : Big::BM, bn = f.kind == 0 ? Few::BN : f.kind == 1 ? Mid::BN : Big::BN;
   f.n_tok = cdiv(a.N, bn);
-  f.v_tiles = cdiv(a.V, bm);
-  // two workgroups per CU, and whole rounds of them
-  const int64_t want = std::max<int64_t>(1, cdiv(2 * kCus, f.n_tok));
-  f.per_split = std::max<int64_t>(1, f.v_tiles / want);
-  f.splits = cdiv(f.v_tiles, f.per_split);
+  const int64_t v_tiles = cdiv(a.V, bm), slots = (f.kind == 2 ? 1 : 2) * kCus;
+  // the number of splits whose longest workgroup has the fewest tiles, among
+  // a few and the ones that fill whole rounds of the device
+  int64_t best = -1;
+  for (int64_t r = 1; r <= 8; ++r) {
+    const int64_t want = r <= 4 ? r : (r - 4) * slots / f.n_tok;
+    if (want < 1) continue;
+    const int64_t per = cdiv(v_tiles, std::min(v_tiles, want)), s = cdiv(v_tiles, per);
+    const int64_t longest = cdiv(f.n_tok * s, slots) * per;
+    if (best < 0 || longest < best) {
+      best = longest;
+      f.splits = s;
+      f.per_split = per;
+    }
+  }
+  f.grid = std::min(f.n_tok * f.splits, slots);
   f.part_off = f.op.end;
   f.total = f.part_off + up(size_t(f.splits) * a.N * sizeof(float2));
   return f;
@@ -435,24 +560,27 @@ PlanFw plan_fw(const LossArgs& a) {
 
 struct PlanBw {
   Plan op;
-  int64_t piece, pieces, ldz;
+  bool big_z, big_o;        // tiles of the logits; of dx and dW
+  int64_t piece, ldz;
   int64_t sx, kx, sw, kw;   // slices of dx's sum (over the piece) and dW's (over the tokens), and their lengths
   size_t coef_off, g_off, dz_off, px_off, pw_off, total;
 };
 PlanBw plan_bw(const LossArgs& a) {
   PlanBw b{};
   b.op = plan_operands(a);
+  b.big_z = take_big(a.N);
+  b.big_o = take_big(a.d);
   const int64_t v_tiles = cdiv(a.V, Big::BM);
   const size_t row = size_t(a.N) * b.op.planes * 2 * Big::BM;
   int64_t per = std::max<int64_t>(1, int64_t(kPieceBytes / row));
-  b.pieces = cdiv(v_tiles, per);
-  per = cdiv(v_tiles, b.pieces);
+  per = cdiv(v_tiles, cdiv(v_tiles, per));
   b.piece = per * Big::BM;
-  b.pieces = cdiv(a.V, b.piece);
-  b.ldz = b.piece;
+  // rows of dz are no power of two apart: they would fall on few memory channels
+  b.ldz = b.piece + 64;
+  const int64_t slots = (b.big_o ? 1 : 2) * kCus, bn = b.big_o ? Big::BN : Mid::BN;
   auto slices = [&](int64_t rows, int64_t K, int64_t* len) {
-    const int64_t tiles = cdiv(rows, Big::BM) * cdiv(a.d, Big::BN);
-    int64_t s = std::max<int64_t>(1, 2 * kCus / tiles);
+    const int64_t tiles = cdiv(rows, Big::BM) * cdiv(a.d, bn);
+    int64_t s = std::max<int64_t>(1, slots / tiles);
     s = std::min<int64_t>(s, std::max<int64_t>(1, K / 512));
     *len = cdiv(cdiv(K, s), 64) * 64;
     return cdiv(K, *len);
@@ -461,10 +589,10 @@ PlanBw plan_bw(const LossArgs& a) {
   b.sw = slices(std::min(b.piece, a.V), a.N, &b.kw);
   b.coef_off = b.op.end;
   b.g_off = b.coef_off + up(size_t(a.N) * sizeof(RowCoef));
-  b.dz_off = b.g_off + 256;
+  b.dz_off = b.g_off + up(4 * (1 + kMaxParts));
   b.px_off = b.dz_off + up(size_t(a.N) * b.op.planes * b.ldz * 2);
   b.pw_off = b.px_off + up(size_t(b.sx) * a.N * a.d * 4);
-  b.total = b.pw_off + up(size_t(b.sw) * std::min(b.piece, a.V) * a.d * 4);
+  b.total = b.pw_off + (b.sw > 1 ? up(size_t(b.sw) * std::min(b.piece, a.V) * a.d * 4) : 0);
   return b;
 }
 
@@ -505,11 +633,12 @@ void launch_loss(const LossArgs& a, const void* x, const void* W, const void* ta
   const int terms = a.bf16 ? 1 : kTerms;
   const float c = a.scale * kLog2e;
   float2* part = reinterpret_cast<float2*>(a.ws + f.part_off);
-  const unsigned grid = static_cast<unsigned>(f.n_tok * f.splits);
-  if (f.few)
-    k_loss_lse<Few><<<grid, Few::NTHR, 0, a.stream>>>(Wo, X, a.N, a.V, f.op.ldp, terms, c, int(f.n_tok), f.per_split, part);
-  else
-    k_loss_lse<Big><<<grid, Big::NTHR, 0, a.stream>>>(Wo, X, a.N, a.V, f.op.ldp, terms, c, int(f.n_tok), f.per_split, part);
+  auto go = [&](auto tl) {
+    using Tl = decltype(tl);
+    k_loss_lse<Tl><<<unsigned(f.grid), Tl::NTHR, 0, a.stream>>>(Wo, X, a.N, a.V, f.op.ldp, terms, c, int(f.n_tok),
+                                                                int(f.splits), int(f.per_split), part);
+  };
+  if (f.kind == 0) go(Few{}); else if (f.kind == 1) go(Mid{}); else go(Big{});
   const unsigned jg = static_cast<unsigned>(cdiv(a.N, 4));
   if (a.bf16)
     k_loss_join<true><<<jg, 256, 0, a.stream>>>(part, int(f.splits), x, W, targets, a.target_bytes, a.N, a.V, a.d,
@@ -539,10 +668,10 @@ void launch_loss_backward(const LossArgs& a, const void* x, const void* W, const
   uint16_t* dz = reinterpret_cast<uint16_t*>(a.ws + b.dz_off);
   float* px = reinterpret_cast<float*>(a.ws + b.px_off);
   float* pw = reinterpret_cast<float*>(a.ws + b.pw_off);
-  k_loss_gmax<<<1, 1024, 0, a.stream>>>(dloss, dlse, targets, a.target_bytes, a.ignore, a.N, g);
+  const int parts = int(std::min<int64_t>(kMaxParts, cdiv(a.N, 1024)));
+  k_loss_gmax<<<parts, 1024, 0, a.stream>>>(dloss, dlse, targets, a.target_bytes, a.ignore, a.N, g);
   k_loss_coef<<<unsigned(cdiv(a.N, 256)), 256, 0, a.stream>>>(dloss, dlse, lse, targets, a.target_bytes, a.ignore, a.N,
-                                                              a.V, g, coef);
-  const int64_t n_tok = cdiv(a.N, Big::BN), n_col = cdiv(a.d, Big::BN);
+                                                              a.V, g, parts, coef);
   auto out = [&](const float* P, int S, int64_t n, void* o, int64_t at) {
     const unsigned grid = unsigned(cdiv(n, 256));
     if (a.bf16)
@@ -550,30 +679,48 @@ void launch_loss_backward(const LossArgs& a, const void* x, const void* W, const
     else
       k_loss_out<false><<<grid, 256, 0, a.stream>>>(P, S, n, g, a.scale, static_cast<float*>(o) + at);
   };
+  // one tile shape and storage type of each kernel
+  auto pick = [&](bool big, auto run) {
+    using T_ = std::true_type;
+    using F_ = std::false_type;
+    if (big && a.bf16) run(Big{}, T_{});
+    else if (big) run(Big{}, F_{});
+    else if (a.bf16) run(Mid{}, T_{});
+    else run(Mid{}, F_{});
+  };
+  const size_t elt = a.bf16 ? 2 : 4;
   for (int64_t v0 = 0; v0 < a.V; v0 += b.piece) {
     const int64_t v1 = std::min(v0 + b.piece, a.V), nv = v1 - v0;
+    const bool last = v1 == a.V;
     // dz rows reach the end of the piece's last tile of 8: zeros past the vocabulary
     const int64_t pend = v0 + cdiv(nv, 8) * 8;
-    const unsigned grid = unsigned(n_tok * cdiv(nv, Big::BM));
-    if (a.bf16)
-      k_loss_dz<Big, true><<<grid, Big::NTHR, 0, a.stream>>>(Wo, X, a.N, a.V, b.op.ldp, terms, c, v0, pend, int(n_tok),
-                                                             coef, dz, b.ldz);
-    else
-      k_loss_dz<Big, false><<<grid, Big::NTHR, 0, a.stream>>>(Wo, X, a.N, a.V, b.op.ldp, terms, c, v0, pend, int(n_tok),
-                                                              coef, dz, b.ldz);
+    pick(b.big_z, [&](auto tl, auto bf) {
+      using Tl = decltype(tl);
+      const int64_t n_tok = cdiv(a.N, Tl::BN), units = n_tok * cdiv(nv, Tl::BM), slots = Tl::BN == Big::BN ? kCus : 2 * kCus;
+      k_loss_dz<Tl, decltype(bf)::value><<<unsigned(std::min(units, slots)), Tl::NTHR, 0, a.stream>>>(
+          Wo, X, a.N, a.V, b.op.ldp, terms, c, v0, pend, int(n_tok), coef, dz, b.ldz);
+    });
     const MmOperand Z{dz, b.ldz, a.N * b.ldz};
-    if (dx) {
-      const MmOperand Wc{Wo.base + v0 * Wo.ld, Wo.ld, Wo.plane};
-      const dim3 gx(unsigned(cdiv(a.N, Big::BM) * n_col), unsigned(b.sx));
-      k_loss_mm<Big, false><<<gx, Big::NTHR, 0, a.stream>>>(Z, Wc, a.N, a.d, nv, b.kx, terms, int(n_col), v0 > 0, px);
-    }
+    if (dx)
+      pick(b.big_o, [&](auto tl, auto bf) {
+        using Tl = decltype(tl);
+        const MmOperand Wc{Wo.base + v0 * Wo.ld, Wo.ld, Wo.plane};
+        const int64_t n_col = cdiv(a.d, Tl::BN);
+        k_loss_mm<Tl, false, decltype(bf)::value><<<unsigned(cdiv(a.N, Tl::BM) * n_col * b.sx), Tl::NTHR, 0, a.stream>>>(
+            Z, Wc, a.N, a.d, nv, b.kx, terms, int(n_col), int(b.sx), v0 > 0, px, last && b.sx == 1 ? dx : nullptr, g, a.scale);
+      });
     if (dW) {
-      const dim3 gw(unsigned(cdiv(nv, Big::BM) * n_col), unsigned(b.sw));
-      k_loss_mm<Big, true><<<gw, Big::NTHR, 0, a.stream>>>(Z, X, nv, a.d, a.N, b.kw, terms, int(n_col), 0, pw);
-      out(pw, int(b.sw), nv * a.d, dW, v0 * a.d);
+      void* const dWc = static_cast<uint8_t*>(dW) + v0 * a.d * elt;
+      pick(b.big_o, [&](auto tl, auto bf) {
+        using Tl = decltype(tl);
+        const int64_t n_col = cdiv(a.d, Tl::BN);
+        k_loss_mm<Tl, true, decltype(bf)::value><<<unsigned(cdiv(nv, Tl::BM) * n_col * b.sw), Tl::NTHR, 0, a.stream>>>(
+            Z, X, nv, a.d, a.N, b.kw, terms, int(n_col), int(b.sw), 0, pw, b.sw == 1 ? dWc : nullptr, g, a.scale);
+      });
+      if (b.sw > 1) out(pw, int(b.sw), nv * a.d, dW, v0 * a.d);
     }
   }
-  if (dx) out(px, int(b.sx), a.N * a.d, dx, 0);
+  if (dx && b.sx > 1) out(px, int(b.sx), a.N * a.d, dx, 0);
 }
 
 }  // namespace prn
