@@ -532,34 +532,64 @@ def prn_head_sequential_forward(xproj, A, H_out, *, d_head: int = 16, h0=None, s
 
 
 # ------------------------------------------------ a token model around the recurrence ---
+# These are called once or more per generated token, so the checks of an
+# argument that is right are one expression; _refuse finds the words for one
+# that is not.
 
-def _storage(dtype) -> int:
-    if dtype not in DTYPES:
-        raise TypeError(f"unsupported storage dtype {dtype}")
-    return DTYPES[dtype]
-
-
-def _ids(t, name) -> int:
-    _dev(t, name)
-    if t.dtype not in ID_DTYPES:
-        raise TypeError(f"{name} must be int32 or int64, got {t.dtype}")
-    return ID_DTYPES[t.dtype]
+_raw_stream = torch._C._cuda_getCurrentRawStream   # the handle alone, without a Stream object
 
 
-def _same_device(t, *others) -> None:
-    for o in others:
-        if o is not None and o.device != t.device:
-            raise ValueError(f"tensors on different devices: {t.device} and {o.device}")
+def _refuse(t, name, dtype, shape, dev) -> None:
+    _dev(t, name, dtype)
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on another device")
+    raise AssertionError(f"{name}: refused without a reason")
 
 
-def _finish_params(p, t, workspace, stream):
-    """Workspace and stream; the stream defaults to the current one of the tensor's device."""
-    if workspace is not None:
-        p.workspace, p.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+def _arg(t, name, dtype, shape, dev):
+    """Device address of a dense tensor of this type, shape and device (None for None)."""
+    if t is None:
+        return None
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.shape == shape and t.is_contiguous()
+            and t.get_device() == dev):
+        _refuse(t, name, dtype, shape, dev)
+    return t.data_ptr()
+
+
+def _lead(t, name, dims: int):
+    """(device, storage code) of the tensor that sets a call's device, type and sizes."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda):
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+    code = DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported storage dtype {t.dtype}")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got {tuple(t.shape)}")
+    return t.get_device(), code
+
+
+def _ids(t, name, shape, dev):
+    """(address, bytes per id) of an int32 or int64 id tensor."""
+    size = ID_DTYPES.get(t.dtype) if isinstance(t, torch.Tensor) else None
+    if size is None:
+        raise TypeError(f"{name} must be an int32 or int64 tensor, got {getattr(t, 'dtype', type(t))}")
+    return _arg(t, name, t.dtype, shape, dev), size
+
+
+def _handle(stream, dev) -> int:
+    """Stream handle; the current stream of the tensors' device by default."""
     if stream is None:
-        stream = torch.cuda.current_stream(t.device)
-    p.stream = int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
-    return p
+        return _raw_stream(dev)
+    return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _scratch(workspace, dev):
+    if workspace is None:
+        return None, 0
+    n = workspace.numel() * workspace.element_size()
+    return _arg(workspace, "workspace", workspace.dtype, workspace.shape, dev), n
 
 
 def _bytes(fn, p) -> int:
@@ -569,74 +599,64 @@ def _bytes(fn, p) -> int:
     return n
 
 
-def _embed_params(dtype, id_bytes: int, N: int, V: int, d: int, scale: float, pad_id) -> prn_embed_params:
-    return prn_embed_params(_storage(dtype), id_bytes, N, V, d, scale, NO_PAD if pad_id is None else pad_id)
+def _storage(dtype) -> int:
+    if dtype not in DTYPES:
+        raise TypeError(f"unsupported storage dtype {dtype}")
+    return DTYPES[dtype]
 
 
 def prn_embed(tokens, table, out, *, scale: float = 1.0, pad_id=None, stream=None) -> None:
     """out (N, d) = scale * table (V, d) [tokens (N) int32 or int64]."""
-    size = _ids(tokens, "tokens")
-    _dev(table, "table")
-    _dev(out, "out", table.dtype)
-    _same_device(table, tokens, out)
+    dev, code = _lead(table, "table", 2)
     V, d = table.shape
     N = tokens.numel()
-    if tokens.dim() != 1 or out.shape != (N, d):
-        raise ValueError(f"shape mismatch: tokens {tuple(tokens.shape)} table {(V, d)} out {tuple(out.shape)}")
-    p = _finish_params(_embed_params(table.dtype, size, N, V, d, scale, pad_id), table, None, stream)
-    _check(lib().prn_embed(_ptr(tokens), _ptr(table), ctypes.byref(p), _ptr(out)))
+    ids, size = _ids(tokens, "tokens", (N,), dev)
+    p = prn_embed_params(code, size, N, V, d, scale, NO_PAD if pad_id is None else pad_id, None, 0,
+                         _handle(stream, dev))
+    _check(lib().prn_embed(ids, _arg(table, "table", table.dtype, table.shape, dev), p,
+                           _arg(out, "out", table.dtype, (N, d), dev)))
 
 
 def prn_embed_backward_workspace_bytes(dtype: torch.dtype, N: int, V: int, d: int) -> int:
-    return _bytes(lib().prn_embed_backward_workspace_bytes, _embed_params(dtype, 8, N, V, d, 1.0, None))
+    return _bytes(lib().prn_embed_backward_workspace_bytes, prn_embed_params(_storage(dtype), 8, N, V, d, 1.0, NO_PAD))
 
 
 def prn_embed_backward(tokens, dout, dtable_out, *, scale: float = 1.0, pad_id=None, workspace=None,
                        stream=None) -> None:
     """dtable_out (V, d) = scale * the sums of dout (N, d) over equal tokens (N)."""
-    size = _ids(tokens, "tokens")
-    _dev(dout, "dout")
-    _dev(dtable_out, "dtable_out", dout.dtype)
-    _same_device(dout, tokens, dtable_out, workspace)
+    dev, code = _lead(dtable_out, "dtable_out", 2)
     V, d = dtable_out.shape
     N = tokens.numel()
-    if tokens.dim() != 1 or dout.shape != (N, d):
-        raise ValueError(f"shape mismatch: tokens {tuple(tokens.shape)} dout {tuple(dout.shape)} dtable {(V, d)}")
-    p = _finish_params(_embed_params(dout.dtype, size, N, V, d, scale, pad_id), dout, workspace, stream)
-    _check(lib().prn_embed_backward(_ptr(tokens), _ptr(dout), ctypes.byref(p), _ptr(dtable_out)))
+    ids, size = _ids(tokens, "tokens", (N,), dev)
+    ws, ws_bytes = _scratch(workspace, dev)
+    p = prn_embed_params(code, size, N, V, d, scale, NO_PAD if pad_id is None else pad_id, ws, ws_bytes,
+                         _handle(stream, dev))
+    dt = dtable_out.dtype
+    _check(lib().prn_embed_backward(ids, _arg(dout, "dout", dt, (N, d), dev), p,
+                                    _arg(dtable_out, "dtable_out", dt, (V, d), dev)))
 
 
-def _norm_params(h, w_post, w_pre, alpha, act, eps, workspace, stream) -> prn_block_norm_params:
+def _norm_params(h, code, dev, w_post, w_pre, alpha, act, eps, workspace, stream) -> prn_block_norm_params:
     if act not in ACTS:
         raise ValueError(f"unknown gate activation {act!r}")
     N, d = h.shape
-    for t, name in ((w_post, "w_post"), (w_pre, "w_pre"), (alpha, "alpha")):
-        _dev(t, name, torch.float32)
-        if t is not None and t.shape != (d,):
-            raise ValueError(f"{name} must be ({d},), got {tuple(t.shape)}")
-    _same_device(h, w_post, w_pre, alpha, workspace)
-    p = prn_block_norm_params(_storage(h.dtype), ACTS[act], N, d, eps, _ptr(w_post), _ptr(w_pre), _ptr(alpha))
-    return _finish_params(p, h, workspace, stream)
-
-
-def _norm_rows(h, **tensors) -> None:
-    _dev(h, "h")
-    if h.dim() != 2:
-        raise ValueError(f"h must be (N, d), got {tuple(h.shape)}")
-    for name, t in tensors.items():
-        _dev(t, name, h.dtype)
-        if t is not None and t.shape != h.shape:
-            raise ValueError(f"{name} must be {tuple(h.shape)}, got {tuple(t.shape)}")
-    _same_device(h, *tensors.values())
+    f32 = torch.float32
+    ws, ws_bytes = _scratch(workspace, dev)
+    return prn_block_norm_params(code, ACTS[act], N, d, eps, _arg(w_post, "w_post", f32, (d,), dev),
+                                 _arg(w_pre, "w_pre", f32, (d,), dev), _arg(alpha, "alpha", f32, (d,), dev), ws, ws_bytes,
+                                 _handle(stream, dev))
 
 
 def prn_block_norm(h, gate, x, r_out, n_out, *, w_post=None, w_pre=None, alpha=None, act: str = "silu",
                    eps: float = 1e-6, stream=None) -> None:
     """r_out = x + alpha * (h rstd(h) w_post) act(gate), n_out = r rstd(r) w_pre: rows of h (N, d); gate, x and
     the weights (d) fp32 may be None, n_out is given exactly when w_pre is."""
-    _norm_rows(h, gate=gate, x=x, r_out=r_out, n_out=n_out)
-    p = _norm_params(h, w_post, w_pre, alpha, act, eps, None, stream)
-    _check(lib().prn_block_norm(_ptr(h), _ptr(gate), _ptr(x), ctypes.byref(p), _ptr(r_out), _ptr(n_out)))
+    dev, code = _lead(h, "h", 2)
+    p = _norm_params(h, code, dev, w_post, w_pre, alpha, act, eps, None, stream)
+    dt, shape = h.dtype, h.shape
+    _check(lib().prn_block_norm(_arg(h, "h", dt, shape, dev), _arg(gate, "gate", dt, shape, dev),
+                                _arg(x, "x", dt, shape, dev), p, _arg(r_out, "r_out", dt, shape, dev),
+                                _arg(n_out, "n_out", dt, shape, dev)))
 
 
 def prn_block_norm_backward_workspace_bytes(dtype: torch.dtype, N: int, d: int) -> int:
@@ -649,61 +669,54 @@ def prn_block_norm_backward(h, gate, x, dr, dn, *, w_post=None, w_pre=None, alph
                             dw_pre_out=None, dalpha_out=None, workspace=None, stream=None) -> None:
     """Gradients at prn_block_norm's inputs from dr (N, d) or None and dn (N, d) (given exactly when w_pre is);
     every output optional."""
-    _norm_rows(h, gate=gate, x=x, dr=dr, dn=dn, dh_out=dh_out, dgate_out=dgate_out, dx_out=dx_out)
-    p = _norm_params(h, w_post, w_pre, alpha, act, eps, workspace, stream)
-    for t, name in ((dw_post_out, "dw_post_out"), (dw_pre_out, "dw_pre_out"), (dalpha_out, "dalpha_out")):
-        _dev(t, name, torch.float32)
-        if t is not None and t.shape != (h.shape[1],):
-            raise ValueError(f"{name} must be ({h.shape[1]},), got {tuple(t.shape)}")
-    _same_device(h, dw_post_out, dw_pre_out, dalpha_out)
-    _check(lib().prn_block_norm_backward(_ptr(h), _ptr(gate), _ptr(x), _ptr(dr), _ptr(dn), ctypes.byref(p),
-                                         _ptr(dh_out), _ptr(dgate_out), _ptr(dx_out), _ptr(dw_post_out),
-                                         _ptr(dw_pre_out), _ptr(dalpha_out)))
+    dev, code = _lead(h, "h", 2)
+    p = _norm_params(h, code, dev, w_post, w_pre, alpha, act, eps, workspace, stream)
+    dt, shape, f32, d = h.dtype, h.shape, torch.float32, (h.shape[1],)
+    _check(lib().prn_block_norm_backward(
+        _arg(h, "h", dt, shape, dev), _arg(gate, "gate", dt, shape, dev), _arg(x, "x", dt, shape, dev),
+        _arg(dr, "dr", dt, shape, dev), _arg(dn, "dn", dt, shape, dev), p, _arg(dh_out, "dh_out", dt, shape, dev),
+        _arg(dgate_out, "dgate_out", dt, shape, dev), _arg(dx_out, "dx_out", dt, shape, dev),
+        _arg(dw_post_out, "dw_post_out", f32, d, dev), _arg(dw_pre_out, "dw_pre_out", f32, d, dev),
+        _arg(dalpha_out, "dalpha_out", f32, d, dev)))
 
 
-def _loss_params(dtype, id_bytes: int, N: int, V: int, d: int, scale: float, ignore_index) -> prn_vocab_loss_params:
-    return prn_vocab_loss_params(_storage(dtype), id_bytes, N, V, d, scale, ignore_index)
-
-
-def _loss_shapes(x, W, targets, **rows):
-    size = _ids(targets, "targets")
-    _dev(x, "x")
-    _dev(W, "W", x.dtype)
-    if x.dim() != 2 or W.dim() != 2 or W.shape[1] != x.shape[1] or targets.shape != (x.shape[0],):
-        raise ValueError(f"shape mismatch: x {tuple(x.shape)} W {tuple(W.shape)} targets {tuple(targets.shape)}")
-    for name, t in rows.items():
-        _dev(t, name, torch.float32)
-        if t is not None and t.shape != (x.shape[0],):
-            raise ValueError(f"{name} must be ({x.shape[0]},), got {tuple(t.shape)}")
-    _same_device(x, W, targets, *rows.values())
-    return size, x.shape[0], W.shape[0], x.shape[1]
+def _loss_params(dtype, N: int, V: int, d: int) -> prn_vocab_loss_params:
+    return prn_vocab_loss_params(_storage(dtype), 8, N, V, d, 1.0, -100)
 
 
 def prn_vocab_loss_workspace_bytes(dtype: torch.dtype, N: int, V: int, d: int) -> int:
-    return _bytes(lib().prn_vocab_loss_workspace_bytes, _loss_params(dtype, 8, N, V, d, 1.0, -100))
+    return _bytes(lib().prn_vocab_loss_workspace_bytes, _loss_params(dtype, N, V, d))
 
 
 def prn_vocab_loss(x, W, targets, loss_out, lse_out, *, scale: float = 1.0, ignore_index: int = -100,
                    workspace=None, stream=None) -> None:
     """Softmax cross entropy of the logits scale * x (N, d) W (V, d)^T: loss_out, lse_out (N) fp32."""
-    size, N, V, d = _loss_shapes(x, W, targets, loss_out=loss_out, lse_out=lse_out)
-    p = _finish_params(_loss_params(x.dtype, size, N, V, d, scale, ignore_index), x, workspace, stream)
-    _check(lib().prn_vocab_loss(_ptr(x), _ptr(W), _ptr(targets), ctypes.byref(p), _ptr(loss_out), _ptr(lse_out)))
+    dev, code = _lead(x, "x", 2)
+    _lead(W, "W", 2)
+    (N, d), V = x.shape, W.shape[0]
+    ids, size = _ids(targets, "targets", (N,), dev)
+    ws, ws_bytes = _scratch(workspace, dev)
+    p = prn_vocab_loss_params(code, size, N, V, d, scale, ignore_index, ws, ws_bytes, _handle(stream, dev))
+    f32 = torch.float32
+    _check(lib().prn_vocab_loss(_arg(x, "x", x.dtype, (N, d), dev), _arg(W, "W", x.dtype, (V, d), dev), ids, p,
+                                _arg(loss_out, "loss_out", f32, (N,), dev), _arg(lse_out, "lse_out", f32, (N,), dev)))
 
 
 def prn_vocab_loss_backward_workspace_bytes(dtype: torch.dtype, N: int, V: int, d: int) -> int:
-    return _bytes(lib().prn_vocab_loss_backward_workspace_bytes, _loss_params(dtype, 8, N, V, d, 1.0, -100))
+    return _bytes(lib().prn_vocab_loss_backward_workspace_bytes, _loss_params(dtype, N, V, d))
 
 
 def prn_vocab_loss_backward(x, W, targets, lse, dloss, *, dlse=None, scale: float = 1.0, ignore_index: int = -100,
                             dx_out=None, dW_out=None, workspace=None, stream=None) -> None:
     """dx_out (N, d) and dW_out (V, d), each optional, from dloss (N) and dlse (N) or None."""
-    size, N, V, d = _loss_shapes(x, W, targets, lse=lse, dloss=dloss, dlse=dlse)
-    for t, like, name in ((dx_out, x, "dx_out"), (dW_out, W, "dW_out")):
-        _dev(t, name, x.dtype)
-        if t is not None and t.shape != like.shape:
-            raise ValueError(f"{name} must be {tuple(like.shape)}, got {tuple(t.shape)}")
-    _same_device(x, dx_out, dW_out, workspace)
-    p = _finish_params(_loss_params(x.dtype, size, N, V, d, scale, ignore_index), x, workspace, stream)
-    _check(lib().prn_vocab_loss_backward(_ptr(x), _ptr(W), _ptr(targets), _ptr(lse), _ptr(dloss), _ptr(dlse),
-                                         ctypes.byref(p), _ptr(dx_out), _ptr(dW_out)))
+    dev, code = _lead(x, "x", 2)
+    _lead(W, "W", 2)
+    (N, d), V = x.shape, W.shape[0]
+    ids, size = _ids(targets, "targets", (N,), dev)
+    ws, ws_bytes = _scratch(workspace, dev)
+    p = prn_vocab_loss_params(code, size, N, V, d, scale, ignore_index, ws, ws_bytes, _handle(stream, dev))
+    f32, dt = torch.float32, x.dtype
+    _check(lib().prn_vocab_loss_backward(
+        _arg(x, "x", dt, (N, d), dev), _arg(W, "W", dt, (V, d), dev), ids, _arg(lse, "lse", f32, (N,), dev),
+        _arg(dloss, "dloss", f32, (N,), dev), _arg(dlse, "dlse", f32, (N,), dev), p,
+        _arg(dx_out, "dx_out", dt, (N, d), dev), _arg(dW_out, "dW_out", dt, (V, d), dev)))

@@ -69,11 +69,11 @@ __device__ __forceinline__ void mm_dma_off(const void* base, uint32_t off, uint3
 }
 #pragma clang diagnostic pop
 
-// wait until at most n of this wave's loads are in flight (n <= 15), and for all its LDS reads
+// wait until at most n of this wave's loads are in flight, and for all its LDS reads
 template <int n>
 __device__ __forceinline__ void mm_wait_loads() {
-  static_assert(n >= 0 && n <= 15, "four bits of the load counter");
-  __builtin_amdgcn_s_waitcnt((n & 15) | (7 << 4));
+  static_assert(n >= 0 && n <= 63, "six bits of the load counter, in two places");
+  __builtin_amdgcn_s_waitcnt((n & 15) | (7 << 4) | ((n >> 4) << 14));
 }
 
 // An operand: `planes` 16-bit matrices `plane` elements apart (one for bf16
@@ -102,7 +102,7 @@ struct MmTile {
   static constexpr int NLA = ABYTES / 1024 / NW, NLB = BBYTES / 1024 / NW;   // wave loads of a wave per stage
   static_assert(ABYTES % (1024 * NW) == 0 && BBYTES % (1024 * NW) == 0, "stages split evenly over the waves");
   static_assert(BK == 32 || BK == 64, "row layouts of 64 and 128 bytes");
-  static_assert((NST - 2) * (NLA + NLB) <= 15, "load counter");
+  static_assert((NST - 2) * (NLA + NLB) <= 63, "load counter");
 
   mm_f32x16 acc[WM][WN];
 
@@ -259,8 +259,8 @@ struct MmTile {
     return __builtin_bit_cast(mm_bf16x8, v);
   }
 
-  // acc += the next tile's product
-  template <bool TA, bool TB, class Next>
+  // acc = (or, with ADD, +=) the next tile's product (acc is left alone if the summed range is empty)
+  template <bool TA, bool TB, bool ADD = false, class Next>
   __device__ __forceinline__ void multiply(Next&& next) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wr = wave / WC, wc = wave % WC;
     const int stages = nk * terms;
@@ -293,13 +293,42 @@ struct MmTile {
           if constexpr (TA) av[kb][i] = frag_cols<2 * BM>(sa, at, kb); else av[kb][i] = frag_rows(sa, at, kb);
         }
       }
+      // a tile's first products start from zero (cheaper than clearing acc)
+      if (!ADD && st == 0) {
+        const mm_f32x16 zero = {};
 #pragma unroll
-      for (int kb = 0; kb < BK / 16; ++kb)
+        for (int i = 0; i < WM; ++i)
+#pragma unroll
+          for (int j = 0; j < WN; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(av[0][i], bv[0][j], zero, 0, 0, 0);
+      } else {
+#pragma unroll
+        for (int i = 0; i < WM; ++i)
+#pragma unroll
+          for (int j = 0; j < WN; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(av[0][i], bv[0][j], acc[i][j], 0, 0, 0);
+      }
+#pragma unroll
+      for (int kb = 1; kb < BK / 16; ++kb)
 #pragma unroll
         for (int i = 0; i < WM; ++i)
 #pragma unroll
           for (int j = 0; j < WN; ++j)
             acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(av[kb][i], bv[kb][j], acc[i][j], 0, 0, 0);
+      // order of the stage: the first 16 k's fragments, then every product
+      // with a share of the next fragments behind it.  Left to itself the
+      // compiler reads each fragment just before its use, to save registers.
+      constexpr int kReads = WM * (TA ? 2 : 1) + WN * (TB ? 2 : 1), kProducts = WM * WN;
+      __builtin_amdgcn_sched_group_barrier(0x100, kReads, 0);
+#pragma unroll
+      for (int kb = 0; kb < BK / 16; ++kb)
+#pragma unroll
+        for (int m = 0; m < kProducts; ++m) {
+          constexpr int kMost = (kReads + kProducts - 1) / kProducts;
+          __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+          if (kb + 1 < BK / 16 && (m + 1) * kReads / kProducts > m * kReads / kProducts)
+            __builtin_amdgcn_sched_group_barrier(0x100, kMost, 0);
+        }
     }
   }
 };

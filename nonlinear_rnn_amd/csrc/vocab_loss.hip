@@ -43,22 +43,27 @@ using Mid = MmTile<2, 2, 4, 2, 32, 3>;
 using Few = MmTile<4, 1, 1, 2, 64, 3>;
 constexpr int kXcd = 8;
 
-// Workgroups are dealt round-robin to the XCDs.  The i-th unit of work of
-// this workgroup (-1: no more), when every XCD takes a contiguous share of
-// the units, in proportion to its workgroups, so that neighbouring units
-// share its L2.
-__device__ __forceinline__ int64_t unit_of(int64_t i, int64_t units) {
-  const int64_t grid = gridDim.x, x = blockIdx.x % kXcd, slot = blockIdx.x / kXcd;
-  const int64_t q = grid / kXcd, rem = grid % kXcd, before = x * q + imin(x, rem), mine = q + (x < rem ? 1 : 0);
-  const int64_t u = units * before / grid + slot + i * mine;
-  return u < units * (before + mine) / grid ? u : -1;
-}
+// Workgroups are dealt round-robin to the XCDs.  The units of work of this
+// workgroup, when every XCD takes a contiguous share of them, in proportion
+// to its workgroups, so that neighbouring units share its L2.
+struct Units {
+  uint32_t u, step, end;
+  __device__ __forceinline__ explicit Units(uint32_t units) {
+    const uint32_t grid = gridDim.x, x = blockIdx.x % kXcd, slot = blockIdx.x / kXcd;
+    const uint32_t q = grid / kXcd, rem = grid % kXcd, before = x * q + min(x, rem);
+    step = q + (x < rem ? 1 : 0);
+    u = static_cast<uint32_t>(static_cast<uint64_t>(units) * before / grid) + slot;
+    end = static_cast<uint32_t>(static_cast<uint64_t>(units) * (before + step) / grid);
+  }
+  __device__ __forceinline__ bool valid() const { return u < end; }
+  __device__ __forceinline__ void advance() { u += step; }
+};
 // tile u of rows x cols in groups of `group` rows, walked down the group's rows first
-__device__ __forceinline__ void tile_of(int64_t u, int rows, int cols, int group, int64_t& r, int64_t& c) {
-  const int64_t per = static_cast<int64_t>(group) * cols, g = u / per, in = u - g * per;
-  const int64_t h = imin(group, rows - g * group);
-  r = g * group + in % h;
+__device__ __forceinline__ void tile_of(uint32_t u, uint32_t rows, uint32_t cols, uint32_t group, uint32_t& r, uint32_t& c) {
+  const uint32_t per = group * cols, g = u / per, in = u - g * per;
+  const uint32_t h = min(group, rows - g * group);
   c = in / h;
+  r = g * group + in - c * h;
 }
 
 // ------------------------------------------------------------ operands ---
@@ -109,74 +114,83 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_lse(MmOperand W, MmOperand
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, l32 = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wr = wave / Tl::WC, wc = wave % Tl::WC;
-  const int v_tiles = static_cast<int>((V + Tl::BM - 1) / Tl::BM);
-  const int64_t units = static_cast<int64_t>(n_tok) * splits;
+  const uint32_t v_tiles = static_cast<uint32_t>((V + Tl::BM - 1) / Tl::BM), units = static_cast<uint32_t>(n_tok) * splits;
   Tl tile;
   tile.open(lds, W, V, X, N, 0, d, terms);
   // the loads' place: unit, vocabulary tile
-  int64_t li = 0, lt = 0, lt1 = 0, ltok = 0, lsplit = 0;
+  Units lu(units), cu(units);
+  uint32_t lt = 0, lt1 = 0, ltok = 0;
   auto enter = [&]() {
-    const int64_t u = unit_of(li, units);
-    if (u < 0) return false;
-    tile_of(u, n_tok, splits, 4, ltok, lsplit);
-    lt = lsplit * per_split;
-    lt1 = imin(lt + per_split, v_tiles);
+    if (!lu.valid()) return false;
+    uint32_t split;
+    tile_of(lu.u, n_tok, splits, 4, ltok, split);
+    lt = split * per_split;
+    lt1 = min(lt + per_split, v_tiles);
     return true;
   };
   auto next = [&]() {
     if (++lt == lt1) {
-      ++li;
+      lu.advance();
       if (!enter()) return;
     }
-    tile.template seek<false, false>(lt * Tl::BM, ltok * Tl::BN);
+    tile.template seek<false, false>(static_cast<int64_t>(lt) * Tl::BM, static_cast<int64_t>(ltok) * Tl::BN);
   };
   if (!enter()) return;
-  tile.template seek<false, false>(lt * Tl::BM, ltok * Tl::BN);
+  tile.template seek<false, false>(static_cast<int64_t>(lt) * Tl::BM, static_cast<int64_t>(ltok) * Tl::BN);
   tile.template prime<false, false>(next);
-  for (int64_t i = 0;; ++i) {
-    const int64_t u = unit_of(i, units);
-    if (u < 0) break;
-    int64_t tok, split;
-    tile_of(u, n_tok, splits, 4, tok, split);
-    const int64_t n0 = tok * Tl::BN, t0 = split * per_split, t1 = imin(t0 + per_split, v_tiles);
+  for (; cu.valid(); cu.advance()) {
+    uint32_t tok, split;
+    tile_of(cu.u, n_tok, splits, 4, tok, split);
+    const int64_t n0 = static_cast<int64_t>(tok) * Tl::BN;
+    const uint32_t t0 = split * per_split, t1 = min(t0 + per_split, v_tiles);
+    // a lane's sums are taken against the maximum m of the first tile that
+    // had one; a later maximum replaces it only when the sums grow large
     float m[Tl::WN], s[Tl::WN];
 #pragma unroll
-    for (int j = 0; j < Tl::WN; ++j) {
-      m[j] = -__builtin_inff();
-      s[j] = 0.0f;
-    }
-    for (int64_t t = t0; t < t1; ++t) {
-      const int64_t v0 = t * Tl::BM;
-      tile.clear();
+    for (int j = 0; j < Tl::WN; ++j) m[j] = s[j] = 0.0f;
+    for (uint32_t t = t0; t < t1; ++t) {
+      const int64_t v0 = static_cast<int64_t>(t) * Tl::BM;
       tile.template multiply<false, false>(next);
       if (v0 + Tl::BM > V) {
         const int left = static_cast<int>(V - v0) - wr * Tl::WM * 32 - 4 * half;
 #pragma unroll
-        for (int i2 = 0; i2 < Tl::WM; ++i2)
+        for (int i = 0; i < Tl::WM; ++i)
 #pragma unroll
           for (int r = 0; r < 16; ++r)
 #pragma unroll
             for (int j = 0; j < Tl::WN; ++j)
-              tile.acc[i2][j][r] = 32 * i2 + 8 * (r >> 2) + (r & 3) < left ? tile.acc[i2][j][r] : -__builtin_inff();
+              tile.acc[i][j][r] = 32 * i + 8 * (r >> 2) + (r & 3) < left ? tile.acc[i][j][r] : -__builtin_inff();
       }
 #pragma unroll
       for (int j = 0; j < Tl::WN; ++j) {
-        float mx = m[j];
+        auto sum_against = [&](float off) {
+          float q[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int i2 = 0; i2 < Tl::WM; ++i2)
+          for (int i = 0; i < Tl::WM; ++i)
 #pragma unroll
-          for (int r = 0; r < 16; ++r) mx = fmaxf(mx, tile.acc[i2][j][r]);
-        // nothing above -inf yet: any finite reference leaves the sum 0
-        const float off = mx == -__builtin_inff() ? 0.0f : -mx * c;
-        float sum = s[j] * ex2(fmaf(m[j], c, off));
+            for (int r = 0; r < 16; ++r) q[r & 3] += ex2(fmaf(tile.acc[i][j][r], c, off));
+          return (q[0] + q[1]) + (q[2] + q[3]);
+        };
+        float sum = sum_against(-m[j] * c);
+        // no maximum yet, or this tile's sum is out of proportion (or NaN)
+        if (__builtin_amdgcn_ballot_w64(s[j] == 0.0f || !(sum < 0x1p60f))) {
+          asm volatile("");   // a branch: taken once or twice a unit
+          float mx = tile.acc[0][j][0];
 #pragma unroll
-        for (int i2 = 0; i2 < Tl::WM; ++i2)
+          for (int i = 0; i < Tl::WM; ++i)
 #pragma unroll
-          for (int r = 0; r < 16; ++r) sum += ex2(fmaf(tile.acc[i2][j][r], c, off));
-        m[j] = mx;
-        s[j] = sum;
+            for (int r = 0; r < 16; ++r) mx = fmaxf(mx, tile.acc[i][j][r]);
+          if (s[j] != 0.0f) mx = fmaxf(mx, m[j]);
+          mx = mx == -__builtin_inff() ? 0.0f : mx;   // any finite reference leaves the sum 0
+          s[j] *= ex2((m[j] - mx) * c);
+          m[j] = mx;
+          sum = sum_against(-mx * c);
+        }
+        s[j] += sum;
       }
     }
+#pragma unroll
+    for (int j = 0; j < Tl::WN; ++j) m[j] = s[j] == 0.0f ? -__builtin_inff() : m[j];
     // the two halves of a lane pair hold other rows of the same token, and so
     // do the waves above one another
 #pragma unroll
@@ -256,9 +270,10 @@ __global__ void __launch_bounds__(256) k_loss_join(const float2* __restrict__ pa
 
 // ------------------------------------------------------------ backward ---
 
-// coefficients of a token's row of dz, divided by the call's largest
+// A token's row of dz / (s g): sign 2^(c z - lse2) - one at the target.  The
+// magnitude of (dloss + dlse) / g is folded into the exponent.
 struct RowCoef {
-  float p, one, lse2;   // dz / (s g) = p 2^(c z - lse2) - one at the target
+  float sign, one, lse2;
   int32_t target;       // -1: none
 };
 
@@ -299,15 +314,14 @@ __global__ void __launch_bounds__(256) k_loss_coef(const float* __restrict__ dlo
   if (n >= N) return;
   const int64_t t = target_of(targets, target_bytes, n);
   const float one = t == ignore ? 0.0f : dloss[n];
+  const float p = (dlse ? one + dlse[n] : one) / gm;
   RowCoef r;
-  r.p = (dlse ? one + dlse[n] : one) / gm;
+  r.sign = p < 0.0f ? -1.0f : 1.0f;
   r.one = one / gm;
-  r.lse2 = lse[n] * kLog2e;
-  r.target = t == ignore ? -1 : static_cast<int32_t>(t);
-  if (t != ignore && (t < 0 || t >= V)) {   // no such entry: the loss was NaN, and so is its gradient
-    r.p = __builtin_nanf("");
-    r.target = -1;
-  }
+  // no such entry: the loss was NaN, and so is its gradient
+  const bool lost = t != ignore && (t < 0 || t >= V);
+  r.lse2 = lost ? __builtin_nanf("") : fmaf(lse[n], kLog2e, -log2f(fabsf(p)));   // p = 0: +inf, a row of zeros
+  r.target = t == ignore || lost ? -1 : static_cast<int32_t>(t);
   coef[n] = r;
 }
 
@@ -321,65 +335,78 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_dz(MmOperand W, MmOperand 
                                                          int terms, float c, int64_t piece0, int64_t piece1, int n_tok,
                                                          const RowCoef* __restrict__ coef, uint16_t* __restrict__ dz,
                                                          int64_t ldz) {
+  // the loads are up to NST tiles ahead (tiles of one stage)
+  constexpr int kRing = Tl::NST + 1;
+  static_assert(sizeof(RowCoef) == 16 && Tl::BN % 64 == 0 && Tl::BN / 64 <= Tl::NW, "one coefficient load per wave");
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Tl::LDS];
-  const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, l32 = lane & 31;
+  __shared__ __attribute__((aligned(1024))) RowCoef coefs[kRing][Tl::BN];
+  const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wr = wave / Tl::WC, wc = wave % Tl::WC;
-  const int v_tiles = static_cast<int>((piece1 - piece0 + Tl::BM - 1) / Tl::BM);
-  const int64_t units = static_cast<int64_t>(n_tok) * v_tiles;
-  constexpr int kGroup = 8;   // vocabulary tiles that an XCD's workgroups share
+  const uint32_t v_tiles = static_cast<uint32_t>((piece1 - piece0 + Tl::BM - 1) / Tl::BM);
+  constexpr uint32_t kGroup = 8;   // vocabulary tiles that an XCD's workgroups share
   Tl tile;
   tile.open(lds, W, V, X, N, 0, d, terms);
-  int64_t li = 0;
-  auto next = [&]() {
-    const int64_t u = unit_of(li++, units);
-    if (u < 0) return;
-    int64_t vt, tok;
-    tile_of(u, v_tiles, n_tok, kGroup, vt, tok);
-    tile.template seek<false, false>(piece0 + vt * Tl::BM, tok * Tl::BN);
+  Units lu(v_tiles * n_tok), cu(v_tiles * n_tok);
+  int fill = 0;   // the tokens' coefficients come with the tile's first stage
+  auto go_to = [&]() {
+    uint32_t vt, tok;
+    tile_of(lu.u, v_tiles, n_tok, kGroup, vt, tok);
+    const int64_t n0 = static_cast<int64_t>(tok) * Tl::BN;
+    tile.template seek<false, false>(piece0 + static_cast<int64_t>(vt) * Tl::BM, n0);
+    if (wave < Tl::BN / 64)
+      mm_dma(coef + imin(n0 + wave * 64 + lane, N - 1), mm_lds_addr(coefs[fill] + wave * 64));
+    fill = fill + 1 == kRing ? 0 : fill + 1;
   };
-  next();
+  auto next = [&]() {
+    lu.advance();
+    if (lu.valid()) go_to();
+  };
+  if (!lu.valid()) return;
+  go_to();
   tile.template prime<false, false>(next);
-  for (int64_t i = 0;; ++i) {
-    const int64_t u = unit_of(i, units);
-    if (u < 0) break;
-    int64_t vt, tok;
-    tile_of(u, v_tiles, n_tok, kGroup, vt, tok);
-    const int64_t v0 = piece0 + vt * Tl::BM, n0 = tok * Tl::BN;
-    // this lane's tokens.  Their coefficients are waited for here, beside the
-    // tile's first stage: a wait after the products would drain the next
-    // tile's loads
-    RowCoef rc[Tl::WN];
-#pragma unroll
-    for (int j = 0; j < Tl::WN; ++j) rc[j] = coef[imin(n0 + (wc * Tl::WN + j) * 32 + l32, N - 1)];
-#pragma unroll
-    for (int j = 0; j < Tl::WN; ++j) asm volatile("" : "+v"(rc[j].p), "+v"(rc[j].one), "+v"(rc[j].lse2), "+v"(rc[j].target));
-    tile.clear();
+  for (int use = 0; cu.valid(); cu.advance(), use = use + 1 == kRing ? 0 : use + 1) {
+    uint32_t vt, tok;
+    tile_of(cu.u, v_tiles, n_tok, kGroup, vt, tok);
+    const int64_t v0 = piece0 + static_cast<int64_t>(vt) * Tl::BM, n0 = static_cast<int64_t>(tok) * Tl::BN;
     tile.template multiply<false, false>(next);
     uint8_t* const base = reinterpret_cast<uint8_t*>(dz + n0 * ldz + (v0 - piece0));
     const int rows = static_cast<int>(imin(piece1 - v0, Tl::BM)), toks = static_cast<int>(imin(N - n0, Tl::BN));
     const int vocab_left = static_cast<int>(imin(V - v0, Tl::BM));
+    // opaque, so that the stores' offsets are not kept in registers over the tiles
+    int el = lane;
+    asm volatile("" : "+v"(el));
+    const int eh = el >> 5;
 #pragma unroll
     for (int j = 0; j < Tl::WN; ++j) {
-      const int tl = (wc * Tl::WN + j) * 32 + l32;
+      const int tl = (wc * Tl::WN + j) * 32 + (el & 31);
       const uint32_t at_row = static_cast<uint32_t>(tl) * static_cast<uint32_t>(2 * ldz);
+      const RowCoef rc = coefs[use][tl];
       // the target's row of this tile (negative or past the tile: elsewhere)
-      const int at = rc[j].target < 0 ? -1 : static_cast<int>(imax(imin(rc[j].target - v0, 1 << 20), -1));
+      const int at = rc.target < 0 ? -1 : static_cast<int>(imax(imin(rc.target - v0, 1 << 20), -1));
+      const bool negative = __builtin_amdgcn_ballot_w64(rc.sign < 0.0f) != 0;
 #pragma unroll
       for (int i2 = 0; i2 < Tl::WM; ++i2) {
         const int vb = (wr * Tl::WM + i2) * 32;   // the block's first row of the tile
         float v[16];
 #pragma unroll
-        for (int r = 0; r < 16; ++r) v[r] = rc[j].p * ex2(fmaf(tile.acc[i2][j][r], c, -rc[j].lse2));
-        if (__any(at >= vb && at < vb + 32)) {
-          const int rel = at - vb - 4 * half;
+        for (int r = 0; r < 16; ++r) v[r] = ex2(fmaf(tile.acc[i2][j][r], c, -rc.lse2));
+        if (negative) {
+          asm volatile("");   // branches: rarely taken
 #pragma unroll
-          for (int r = 0; r < 16; ++r) v[r] -= rel == 8 * (r >> 2) + (r & 3) ? rc[j].one : 0.0f;
+          for (int r = 0; r < 16; ++r) v[r] *= rc.sign;
+        }
+        if (__builtin_amdgcn_ballot_w64(at >= vb && at < vb + 32)) {
+          asm volatile("");
+          const int rel = at - vb - 4 * eh;
+#pragma unroll
+          for (int r = 0; r < 16; ++r) v[r] -= rel == 8 * (r >> 2) + (r & 3) ? rc.one : 0.0f;
         }
         if (vb + 32 > vocab_left) {   // the columns past the vocabulary are zeros (dx sums over them)
+          asm volatile("");
 #pragma unroll
           for (int r = 0; r < 16; ++r)
-            if (vb + 4 * half + 8 * (r >> 2) + (r & 3) >= vocab_left) v[r] = 0.0f;
+            if (vb + 4 * eh + 8 * (r >> 2) + (r & 3) >= vocab_left) v[r] = 0.0f;
         }
 #pragma unroll
         for (int t = 0; t < (BF16 ? 1 : 3); ++t) {
@@ -402,7 +429,7 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_dz(MmOperand W, MmOperand 
           for (int q = 0; q < 4; q += 2) {
             const auto s0 = __builtin_amdgcn_permlane32_swap(w[q][0], w[q + 1][0], false, false);
             const auto s1 = __builtin_amdgcn_permlane32_swap(w[q][1], w[q + 1][1], false, false);
-            const int col = vb + 8 * (q + half);
+            const int col = vb + 8 * (q + eh);
             if (tl < toks && col < rows)
               gstore(reinterpret_cast<mm_u32x4*>(base + t * (2 * N * ldz) + (at_row + 2 * col)),
                      mm_u32x4{s0[0], s1[0], s0[1], s1[1]});
@@ -423,10 +450,9 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_mm(MmOperand A, MmOperand 
                                                          const float* __restrict__ g, float scale) {
   using T = typename Storage<BF16 ? kBF16 : kF32>::T;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Tl::LDS];
-  const int64_t u = unit_of(0, gridDim.x);
-  const int64_t tiles = gridDim.x / slices, z = u / tiles, ti = u - z * tiles;
-  const int64_t c0 = ti % n_col * Tl::BN, r0 = ti / n_col * Tl::BM;
-  const int64_t k0 = z * k_slice, k1 = imin(k0 + k_slice, K);
+  const uint32_t u = Units(gridDim.x).u, tiles = gridDim.x / slices, z = u / tiles, ti = u - z * tiles;
+  const int64_t c0 = static_cast<int64_t>(ti % n_col) * Tl::BN, r0 = static_cast<int64_t>(ti / n_col) * Tl::BM;
+  const int64_t k0 = static_cast<int64_t>(z) * k_slice, k1 = imin(k0 + k_slice, K);
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, l32 = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wr = wave / Tl::WC, wc = wave % Tl::WC;
@@ -456,7 +482,7 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_mm(MmOperand A, MmOperand 
   } else {
     tile.clear();
   }
-  tile.template multiply<TA, true>(next);
+  tile.template multiply<TA, true, true>(next);
   const float f = out ? g[0] * scale : 1.0f;
   T* const obase = static_cast<T*>(out) + r0 * C + c0;
   const uint32_t oat = rl * static_cast<uint32_t>(C) + cl;

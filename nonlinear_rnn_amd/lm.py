@@ -15,16 +15,30 @@ import torch
 from . import binding as B_
 
 
-def _dense(t, align: int = 16):
-    """t contiguous and starting on `align` bytes (itself if it is already)."""
+def _rows(t):
+    """t (..., d) as dense rows (N, d) that start on 16 bytes: itself where it is that already."""
     if t is None:
         return None
-    t = t.contiguous()
-    return t.clone() if t.data_ptr() % align else t
+    if t.dim() != 2:
+        t = t.reshape(-1, t.shape[-1])
+    if not t.is_contiguous():
+        t = t.contiguous()
+    return t.clone() if t.data_ptr() % 16 else t
+
+
+def _flat(t):
+    """Ids or fp32 values of any shape as one dense row."""
+    if t.dim() != 1:
+        t = t.reshape(-1)
+    return t if t.is_contiguous() else t.contiguous()
 
 
 def _weight(t):
-    return None if t is None else t.to(torch.float32).contiguous()
+    if t is None:
+        return None
+    if t.dtype != torch.float32:
+        t = t.to(torch.float32)
+    return t if t.is_contiguous() else t.contiguous()
 
 
 def _scratch(n: int, device) -> torch.Tensor:
@@ -37,17 +51,18 @@ def embed(tokens, table, *, scale: float = 1.0, pad_id=None) -> torch.Tensor:
     """scale * table[tokens]: tokens (...) int32 or int64, table (V, d); (..., d).
 
     Tokens equal to pad_id give zeros; a token outside the table gives NaN."""
-    ids = tokens.reshape(-1).contiguous()
-    table = table.contiguous()
-    out = torch.empty((ids.numel(), table.shape[1]), dtype=table.dtype, device=table.device)
+    ids = _flat(tokens)
+    if not table.is_contiguous():
+        table = table.contiguous()
+    out = table.new_empty((ids.shape[0], table.shape[1]))
     B_.prn_embed(ids, table, out, scale=scale, pad_id=pad_id)
-    return out.view(*tokens.shape, table.shape[1])
+    return out if tokens.dim() == 1 else out.view(*tokens.shape, table.shape[1])
 
 
 def embed_backward(dout, tokens, V: int, *, scale: float = 1.0, pad_id=None) -> torch.Tensor:
     """The table's gradient (V, d): scale * the sums of dout (..., d) over equal tokens, each in token order
     and fp32 (bitwise reproducible); rows of absent tokens are zeros."""
-    ids = tokens.reshape(-1).contiguous()
+    ids = _flat(tokens)
     d = dout.shape[-1]
     if dout.shape[:-1] != tokens.shape:
         raise ValueError(f"dout {tuple(dout.shape)} does not belong to tokens {tuple(tokens.shape)}")
@@ -88,7 +103,7 @@ def block_norm(h, x=None, *, gate=None, w_post=None, w_pre=None, alpha=None, act
     identity, n is None without w_pre).  With w_pre alone r is h itself: the
     norm before the first block."""
     shape = h.shape
-    h2, x2, g2 = (None if t is None else _dense(t.reshape(-1, shape[-1])) for t in (h, x, gate))
+    h2, x2, g2 = _rows(h), _rows(x), _rows(gate)
     w_post, w_pre, alpha = _weight(w_post), _weight(w_pre), _weight(alpha)
     same = x2 is None and g2 is None and w_post is None and alpha is None
     if same and w_pre is None:
@@ -96,6 +111,8 @@ def block_norm(h, x=None, *, gate=None, w_post=None, w_pre=None, alpha=None, act
     r = h2 if same else torch.empty_like(h2)
     n = None if w_pre is None else torch.empty_like(h2)
     B_.prn_block_norm(h2, g2, x2, None if same else r, n, w_post=w_post, w_pre=w_pre, alpha=alpha, act=act, eps=eps)
+    if len(shape) == 2:
+        return (h if same else r), n
     return (h if same else r.view(shape)), (None if n is None else n.view(shape))
 
 
@@ -104,7 +121,7 @@ def block_norm_backward(dr, dn, h, x=None, *, gate=None, w_post=None, w_pre=None
     """Gradients of block_norm from dr = dL/dr (None for zero) and dn = dL/dn (None without w_pre):
     (dh, dx, dgate, dw_post, dw_pre, dalpha), None where the input is absent; the weights' are fp32."""
     shape = h.shape
-    h2, x2, g2, dr2, dn2 = (None if t is None else _dense(t.reshape(-1, shape[-1])) for t in (h, x, gate, dr, dn))
+    h2, x2, g2, dr2, dn2 = _rows(h), _rows(x), _rows(gate), _rows(dr), _rows(dn)
     w_post, w_pre, alpha = _weight(w_post), _weight(w_pre), _weight(alpha)
     dh, dx, dgate = (None if t is None else torch.empty_like(h2) for t in (h2, x2, g2))
     dw_post, dw_pre, dalpha = (None if t is None else torch.empty_like(t) for t in (w_post, w_pre, alpha))
@@ -151,10 +168,10 @@ def vocab_loss(x, W, targets, *, scale: float = 1.0, ignore_index: int = -100):
     x (..., d), W (V, d), targets (...) int32 or int64.  Returns (loss, lse), fp32, shaped like targets; loss is 0
     where targets == ignore_index and NaN where a target is out of range; lse is the log of the summed
     exponentials (-loss is the target's log probability)."""
-    x2, W = _dense(x.reshape(-1, x.shape[-1])), _dense(W)
-    ids = targets.reshape(-1).contiguous()
+    x2, W, ids = _rows(x), _rows(W), _flat(targets)
     N = x2.shape[0]
-    loss, lse = (torch.empty(N, dtype=torch.float32, device=x2.device) for _ in range(2))
+    loss = torch.empty(N, dtype=torch.float32, device=x2.device)
+    lse = torch.empty_like(loss)
     ws = _scratch(B_.prn_vocab_loss_workspace_bytes(x2.dtype, N, *W.shape), x2.device)
     B_.prn_vocab_loss(x2, W, ids, loss, lse, scale=scale, ignore_index=ignore_index, workspace=ws)
     return loss.view(targets.shape), lse.view(targets.shape)
@@ -164,10 +181,9 @@ def vocab_loss_backward(dloss, x, W, targets, lse, *, dlse=None, scale: float = 
                         want_x: bool = True, want_W: bool = True):
     """Gradients (dx, dW) of vocab_loss from dloss and dlse (None for zero), both shaped like targets; each only if
     wanted, else None.  The logits are formed again, a piece of the vocabulary at a time."""
-    x2, W = _dense(x.reshape(-1, x.shape[-1])), _dense(W)
-    ids = targets.reshape(-1).contiguous()
-    dloss, lse = (t.reshape(-1).to(torch.float32).contiguous() for t in (dloss, lse))
-    dlse = None if dlse is None else dlse.reshape(-1).to(torch.float32).contiguous()
+    x2, W, ids = _rows(x), _rows(W), _flat(targets)
+    dloss, lse = _flat(_weight(dloss)), _flat(_weight(lse))
+    dlse = None if dlse is None else _flat(_weight(dlse))
     dx = torch.empty_like(x2) if want_x else None
     dW = torch.empty_like(W) if want_W else None
     ws = _scratch(B_.prn_vocab_loss_backward_workspace_bytes(x2.dtype, x2.shape[0], *W.shape), x2.device)
