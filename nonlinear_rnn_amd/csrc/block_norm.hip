@@ -78,38 +78,13 @@ struct RowSum {
   }
 };
 
-// VEC consecutive channels of a row
+// VEC elements (16 bytes, or one where a row is shorter) at any element's
+// address: rows of odd widths start anywhere, and global memory takes
+// unaligned vector accesses.
 template <int DT, int VEC>
-__device__ __forceinline__ void load_vec(const typename Storage<DT>::T* p, float* o) {
-  if constexpr (VEC == 1) {
-    o[0] = Storage<DT>::load(p);
-  } else if constexpr (DT == kF32) {
-    const float4 q = *reinterpret_cast<const float4*>(p);
-    o[0] = q.x, o[1] = q.y, o[2] = q.z, o[3] = q.w;
-  } else {
-    const uint4 q = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      o[2 * e] = __uint_as_float(w[e] << 16);
-      o[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-    }
-  }
-}
-template <int DT, int VEC>
-__device__ __forceinline__ void store_vec(typename Storage<DT>::T* p, const float* o) {
-  if constexpr (VEC == 1) {
-    *p = Storage<DT>::pack(o[0]);
-  } else if constexpr (DT == kF32) {
-    *reinterpret_cast<float4*>(p) = make_float4(o[0], o[1], o[2], o[3]);
-  } else {
-    uint32_t w[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      w[e] = Storage<kBF16>::pack(o[2 * e]) | static_cast<uint32_t>(Storage<kBF16>::pack(o[2 * e + 1])) << 16;
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-  }
-}
+struct __attribute__((packed, aligned(sizeof(typename Storage<DT>::T)))) Vec {
+  typename Storage<DT>::T v[VEC];
+};
 
 struct NormDev {
   const void *h, *gate, *x, *dr, *dn;
@@ -122,95 +97,142 @@ struct NormDev {
 };
 
 // A lane's channels: chunk v of VEC channels starts at (v TPR + lane) VEC.
-template <int DT, int VEC, int NV, int TPR>
+// TAIL (d no multiple of VEC): the row's last chunk is moved back to end with
+// the row; the channels it then shares with the chunk before it get the same
+// values from both lanes, and count in sums only once (`fresh`).
+template <int DT, int VEC, int NV, int TPR, bool TAIL>
 struct Row {
   static constexpr int E = VEC * NV;
+  using T = typename Storage<DT>::T;
+  struct Raw {
+    Vec<DT, VEC> v[NV];
+  };
   int lane, d;
-  __device__ __forceinline__ int at(int v) const { return (v * TPR + lane) * VEC; }
-  __device__ __forceinline__ void load(const void* p, int64_t row, float* o) const {
-    const typename Storage<DT>::T* q = static_cast<const typename Storage<DT>::T*>(p) + row * d;
+  __device__ __forceinline__ int chunk(int v) const { return (v * TPR + lane) * VEC; }
+  __device__ __forceinline__ bool in(int v) const { return chunk(v) < d; }
+  __device__ __forceinline__ int at(int v) const { return TAIL ? min(chunk(v), d - VEC) : chunk(v); }
+  // does element e of chunk v count in sums?
+  __device__ __forceinline__ bool fresh(int v, int e) const { return !TAIL || chunk(v) <= d - VEC || at(v) + e >= chunk(v); }
+  __device__ __forceinline__ void fetch(const void* p, int64_t row, Raw& o) const {
+    const T* q = static_cast<const T*>(p) + row * d;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      if (at(v) < d) {
-        load_vec<DT, VEC>(q + at(v), o + v * VEC);
+      if (in(v)) {
+        o.v[v] = *reinterpret_cast<const Vec<DT, VEC>*>(q + at(v));
       } else {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) o[v * VEC + e] = 0.0f;
+        for (int e = 0; e < VEC; ++e) o.v[v].v[e] = T(0);
       }
     }
   }
-  __device__ __forceinline__ void store(void* p, int64_t row, const float* o) const {
-    typename Storage<DT>::T* q = static_cast<typename Storage<DT>::T*>(p) + row * d;
+  __device__ __forceinline__ void unpack(const Raw& q, float* o) const {
 #pragma unroll
     for (int v = 0; v < NV; ++v)
-      if (at(v) < d) store_vec<DT, VEC>(q + at(v), o + v * VEC);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) o[v * VEC + e] = Storage<DT>::load(&q.v[v].v[e]);
+  }
+  __device__ __forceinline__ void load(const void* p, int64_t row, float* o) const {
+    Raw q;
+    fetch(p, row, q);
+    unpack(q, o);
+  }
+  __device__ __forceinline__ void store(void* p, int64_t row, const float* o) const {
+    T* q = static_cast<T*>(p) + row * d;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      if (in(v)) {
+        Vec<DT, VEC> t;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) t.v[e] = Storage<DT>::pack(o[v * VEC + e]);
+        *reinterpret_cast<Vec<DT, VEC>*>(q + at(v)) = t;
+      }
+    }
   }
   // fp32 weights of the lane's channels; absent: ones
   __device__ __forceinline__ void weights(const float* p, float* o) const {
 #pragma unroll
     for (int v = 0; v < NV; ++v)
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) o[v * VEC + e] = (p && at(v) < d) ? p[at(v) + e] : 1.0f;
+      for (int e = 0; e < VEC; ++e) o[v * VEC + e] = (p && in(v)) ? p[at(v) + e] : 1.0f;
+  }
+  // sums of squares and the like: adds f(i) for every element that counts
+  template <class F>
+  __device__ __forceinline__ float sum(F f) const {
+    float s = 0.0f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) s += fresh(v, e) ? f(v * VEC + e) : 0.0f;
+    return s;
   }
 };
 
 __device__ __forceinline__ float sig(float g) { return rcp(1.0f + ex2(kSigScale * g)); }
 
-template <int DT, int VEC, int NV, int TPR, int NTHR>
+template <int DT, int VEC, int NV, int TPR, int NTHR, bool TAIL>
 __global__ void __launch_bounds__(NTHR) k_block_norm(NormDev a) {
-  using R = Row<DT, VEC, NV, TPR>;
-  constexpr int E = R::E;
+  using R = Row<DT, VEC, NV, TPR, TAIL>;
+  using Raw = typename R::Raw;
+  constexpr int E = R::E, GROUPS = NTHR / TPR;
+  static_assert(GROUPS == 1 || TPR <= 64, "a row of several waves is its workgroup's only one (barriers)");
   __shared__ float red[2][1][TPR > 64 ? TPR / 64 : 1];
   const R row{static_cast<int>(threadIdx.x) % TPR, a.d};
-  const int64_t n = static_cast<int64_t>(blockIdx.x) * (NTHR / TPR) + threadIdx.x / TPR;
-  if (TPR <= 64 && n >= a.N) return;   // a row of several waves is the workgroup's only one
   RowSum<TPR, 1> total{red};
   const float inv_d = 1.0f / static_cast<float>(a.d);
-  float h[E], g[E], x[E];
-  row.load(a.h, n, h);
-  if (a.gate) row.load(a.gate, n, g);
-  if (a.x) row.load(a.x, n, x);
-  if (a.w_post) {
-    float s = 0.0f, w[E];
+  float w_post[E], w_pre[E], alpha[E];
+  row.weights(a.w_post, w_post);
+  row.weights(a.w_pre, w_pre);
+  row.weights(a.alpha, alpha);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * GROUPS;
+  // the next row's operands are in flight while a row is worked on
+  Raw rh, rg, rx;
+  auto fetch = [&](int64_t n) {
+    row.fetch(a.h, n, rh);
+    if (a.gate) row.fetch(a.gate, n, rg);
+    if (a.x) row.fetch(a.x, n, rx);
+  };
+  int64_t n = static_cast<int64_t>(blockIdx.x) * GROUPS + threadIdx.x / TPR;
+  if (n < a.N) fetch(n);
+  for (; n < a.N; n += step) {
+    float h[E], g[E], x[E];
+    row.unpack(rh, h);
+    if (a.gate) row.unpack(rg, g);
+    if (a.x) row.unpack(rx, x);
+    if (n + step < a.N) fetch(n + step);
+    if (a.w_post) {
+      float s = row.sum([&](int i) { return h[i] * h[i]; });
+      total(&s);
+      const float rstd = __builtin_amdgcn_rsqf(fmaf(s, inv_d, a.eps));
 #pragma unroll
-    for (int e = 0; e < E; ++e) s = fmaf(h[e], h[e], s);
-    row.weights(a.w_post, w);
-    total(&s);
-    const float rstd = __builtin_amdgcn_rsqf(fmaf(s, inv_d, a.eps));
+      for (int e = 0; e < E; ++e) h[e] *= rstd * w_post[e];
+    }
+    if (a.gate) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) h[e] *= rstd * w[e];
-  }
-  if (a.gate) {
+      for (int e = 0; e < E; ++e) h[e] *= a.act == 0 ? g[e] * sig(g[e]) : sig(g[e]);
+    }
+    if (a.x) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) h[e] *= a.act == 0 ? g[e] * sig(g[e]) : sig(g[e]);
-  }
-  if (a.alpha) {
-    float w[E];
-    row.weights(a.alpha, w);
+      for (int e = 0; e < E; ++e) h[e] = fmaf(alpha[e], h[e], x[e]);
+    } else if (a.alpha) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) h[e] *= w[e];
-  }
-  if (a.x) {
+      for (int e = 0; e < E; ++e) h[e] *= alpha[e];
+    }
+    if (a.o0) row.store(a.o0, n, h);
+    if (a.w_pre) {
+      float s = row.sum([&](int i) { return h[i] * h[i]; });
+      total(&s);
+      const float rstd = __builtin_amdgcn_rsqf(fmaf(s, inv_d, a.eps));
 #pragma unroll
-    for (int e = 0; e < E; ++e) h[e] += x[e];
-  }
-  if (a.o0) row.store(a.o0, n, h);
-  if (a.w_pre) {
-    float s = 0.0f, w[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) s = fmaf(h[e], h[e], s);
-    row.weights(a.w_pre, w);
-    total(&s);
-    const float rstd = __builtin_amdgcn_rsqf(fmaf(s, inv_d, a.eps));
-#pragma unroll
-    for (int e = 0; e < E; ++e) h[e] *= rstd * w[e];
-    row.store(a.o1, n, h);
+      for (int e = 0; e < E; ++e) h[e] *= rstd * w_pre[e];
+      row.store(a.o1, n, h);
+    }
   }
 }
 
-template <int DT, int VEC, int NV, int TPR, int NTHR>
+template <int DT, int VEC, int NV, int TPR, int NTHR, bool TAIL>
 __global__ void __launch_bounds__(NTHR) k_block_norm_backward(NormDev a) {
-  using R = Row<DT, VEC, NV, TPR>;
+  using R = Row<DT, VEC, NV, TPR, TAIL>;
+  using Raw = typename R::Raw;
   constexpr int E = R::E, GROUPS = NTHR / TPR;
   __shared__ float red1[2][1][TPR > 64 ? TPR / 64 : 1];
   __shared__ float red2[2][2][TPR > 64 ? TPR / 64 : 1];
@@ -226,29 +248,41 @@ __global__ void __launch_bounds__(NTHR) k_block_norm_backward(NormDev a) {
 #pragma unroll
   for (int e = 0; e < E; ++e) s_post[e] = s_pre[e] = s_alpha[e] = 0.0f;
   const int64_t step = static_cast<int64_t>(gridDim.x) * GROUPS;
-  for (int64_t n = static_cast<int64_t>(blockIdx.x) * GROUPS + threadIdx.x / TPR; n < a.N; n += step) {
+  // the next row's operands are in flight while a row is worked on
+  Raw rh, rg, rx, rr, rn;
+  auto fetch = [&](int64_t n) {
+    row.fetch(a.h, n, rh);
+    if (a.gate) row.fetch(a.gate, n, rg);
+    if (a.x) row.fetch(a.x, n, rx);
+    if (a.dr) row.fetch(a.dr, n, rr);
+    if (a.w_pre) row.fetch(a.dn, n, rn);
+  };
+  constexpr bool AHEAD = NTHR < 1024;   // 128 registers a lane have no room for them
+  int64_t n = static_cast<int64_t>(blockIdx.x) * GROUPS + threadIdx.x / TPR;
+  if (AHEAD && n < a.N) fetch(n);
+  for (; n < a.N; n += step) {
+    if (!AHEAD) fetch(n);
     float h[E], g[E], x[E], dr[E], dn[E];
-    row.load(a.h, n, h);
-    if (a.gate) row.load(a.gate, n, g);
-    if (a.x) row.load(a.x, n, x);
+    row.unpack(rh, h);
+    if (a.gate) row.unpack(rg, g);
+    if (a.x) row.unpack(rx, x);
+    if (a.w_pre) row.unpack(rn, dn);
     if (a.dr) {
-      row.load(a.dr, n, dr);
+      row.unpack(rr, dr);
     } else {
 #pragma unroll
       for (int e = 0; e < E; ++e) dr[e] = 0.0f;
     }
-    if (a.w_pre) row.load(a.dn, n, dn);
+    if (AHEAD && n + step < a.N) fetch(n + step);
     float rstd_h = 1.0f;
     if (a.w_post) {
-      float s = 0.0f;
-#pragma unroll
-      for (int e = 0; e < E; ++e) s = fmaf(h[e], h[e], s);
+      float s = row.sum([&](int i) { return h[i] * h[i]; });
       total(&s);
       rstd_h = __builtin_amdgcn_rsqf(fmaf(s, inv_d, a.eps));
 #pragma unroll
       for (int e = 0; e < E; ++e) h[e] *= rstd_h;
     }
-    // h is hn from here on; u = hn w_post, f = act(gate)
+    // h is hn from here on; f = act(gate), g = act'(gate), v = hn w_post f
     float f[E], v[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) {
@@ -256,32 +290,30 @@ __global__ void __launch_bounds__(NTHR) k_block_norm_backward(NormDev a) {
       if (a.gate) {
         const float sg = sig(g[e]);
         f[e] = a.act == 0 ? g[e] * sg : sg;
-        // act'(g)
         g[e] = a.act == 0 ? sg * fmaf(g[e], 1.0f - sg, 1.0f) : sg * (1.0f - sg);
       }
       v[e] = h[e] * w_post[e] * f[e];
     }
     if (a.w_pre) {
-      float s[2] = {0.0f, 0.0f}, r[E];
+      float r[E], s[2];
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         r[e] = a.x ? fmaf(alpha[e], v[e], x[e]) : alpha[e] * v[e];
-        s[0] = fmaf(r[e], r[e], s[0]);
-        s[1] = fmaf(dn[e] * w_pre[e], r[e], s[1]);
       }
+      s[0] = row.sum([&](int i) { return r[i] * r[i]; });
+      s[1] = row.sum([&](int i) { return dn[i] * w_pre[i] * r[i]; });
       total2(s);
       const float rstd = __builtin_amdgcn_rsqf(fmaf(s[0], inv_d, a.eps));
       const float mean = s[1] * rstd * inv_d;   // mean(q rn)
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const float rn = r[e] * rstd;
-        s_pre[e] = fmaf(dn[e], rn, s_pre[e]);
-        dr[e] = fmaf(rstd, fmaf(dn[e], w_pre[e], -rn * mean), dr[e]);
+        const float rn_ = r[e] * rstd;
+        s_pre[e] = fmaf(dn[e], rn_, s_pre[e]);
+        dr[e] = fmaf(rstd, fmaf(dn[e], w_pre[e], -rn_ * mean), dr[e]);
       }
     }
     if (a.o2) row.store(a.o2, n, dr);
     float dg[E];
-    float s = 0.0f;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       s_alpha[e] = fmaf(dr[e], v[e], s_alpha[e]);
@@ -290,10 +322,10 @@ __global__ void __launch_bounds__(NTHR) k_block_norm_backward(NormDev a) {
       const float du = dv * f[e];
       s_post[e] = fmaf(du, h[e], s_post[e]);
       dr[e] = du * w_post[e];
-      s = fmaf(dr[e], h[e], s);
     }
     if (a.o1) row.store(a.o1, n, dg);
     if (a.w_post) {
+      float s = row.sum([&](int i) { return dr[i] * h[i]; });
       total(&s);
       const float mean = s * inv_d;
 #pragma unroll
@@ -312,7 +344,8 @@ __global__ void __launch_bounds__(NTHR) k_block_norm_backward(NormDev a) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
           const int i = v * VEC + e;
-          hand[(threadIdx.x / TPR) * (TPR * E) + row.at(v) + e] = k == 0 ? s_post[i] : k == 1 ? s_pre[i] : s_alpha[i];
+          if (row.in(v) && row.fresh(v, e))
+            hand[(threadIdx.x / TPR) * (TPR * E) + row.at(v) + e] = k == 0 ? s_post[i] : k == 1 ? s_pre[i] : s_alpha[i];
         }
       __syncthreads();
       for (int c = threadIdx.x; c < a.d; c += NTHR) {
@@ -326,7 +359,7 @@ __global__ void __launch_bounds__(NTHR) k_block_norm_backward(NormDev a) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
           const int i = v * VEC + e;
-          if (row.at(v) < a.d) out[row.at(v) + e] = k == 0 ? s_post[i] : k == 1 ? s_pre[i] : s_alpha[i];
+          if (row.in(v) && row.fresh(v, e)) out[row.at(v) + e] = k == 0 ? s_post[i] : k == 1 ? s_pre[i] : s_alpha[i];
         }
     }
   }
@@ -355,71 +388,74 @@ __global__ void __launch_bounds__(1024) k_block_norm_weights(const float* __rest
   }
 }
 
-// lanes per row, chunks per lane, workgroup: at most 8 channels a lane (16
-// take the backward pass past 256 registers)
+// Lanes per row, chunks per lane, workgroup: at most 8 channels a lane (16
+// take the backward pass past 256 registers).  Rows shorter than 16 bytes go
+// by single elements, rows of no multiple of 16 bytes with a moved-back tail.
 struct Geo {
   int tpr, nv, nthr;
-  bool vec;
+  bool vec, tail;
 };
 Geo geo(bool bf16, int64_t d) {
   const int64_t vec = bf16 ? 8 : 4;
-  const bool v = d % vec == 0;
-  const int64_t w = v ? vec : 1, most = 8 / w;
-  for (int tpr : {16, 64, 256, 512, 1024}) {
+  const bool v = d >= vec;
+  const int64_t w = v ? vec : 1, most = v ? 8 / vec : 1;
+  for (int tpr : {16, 64, 128, 256, 512, 1024}) {
     const int64_t need = (d + tpr * w - 1) / (tpr * w);
     if (need > most) continue;
-    int nv = 1;
-    while (nv < need) nv *= 2;
-    if (!v && nv < 4) nv = 4;
-    return {tpr, nv, tpr > 256 ? tpr : 256, v};
+    return {tpr, int(need), tpr > 64 ? tpr : 256, v, v && d % vec != 0};
   }
-  return {0, 0, 0, false};
+  return {0, 0, 0, false, false};
 }
 
 int64_t groups_of(const Geo& g) { return g.nthr / g.tpr; }
-// workgroups of the backward pass: enough to fill the device four times over
-int64_t bw_grid(const Geo& g, int64_t N) {
+// Workgroups: 2 waves a SIMD at 8 channels a lane, 4 at 4 (what the backward
+// kernels' registers allow; more bring nothing forward either), or one per
+// group of rows where those are fewer.  Measured at 262144 x 512 bf16 with
+// every part: 2, 4, 8 waves a SIMD forward 233, 262, 273 us; one workgroup per
+// four rows, without the row ahead, 311 us; backward 2 or 4 waves 401, 425 us,
+// without the row ahead 610 us.
+int64_t grid_of(const Geo& g, bool bf16, int64_t N) {
   const int64_t need = (N + groups_of(g) - 1) / groups_of(g);
-  return std::min<int64_t>(need, g.nthr > 256 ? 512 : 1024);
+  const int64_t waves = 256 * 4 * ((bf16 || g.nv == 2) ? 2 : 4);
+  return std::min<int64_t>(need, std::max<int64_t>(256, waves / (g.nthr / 64)));
 }
 
-template <bool BACK, int DT, int VEC, int NV, int TPR>
+template <bool BACK, int DT, int VEC, int NV, int TPR, bool TAIL>
 void go(const NormDev& a, unsigned grid, hipStream_t st) {
-  constexpr int NTHR = TPR > 256 ? TPR : 256;
+  constexpr int NTHR = TPR > 64 ? TPR : 256;
   if constexpr (BACK)
-    k_block_norm_backward<DT, VEC, NV, TPR, NTHR><<<grid, NTHR, 0, st>>>(a);
+    k_block_norm_backward<DT, VEC, NV, TPR, NTHR, TAIL><<<grid, NTHR, 0, st>>>(a);
   else
-    k_block_norm<DT, VEC, NV, TPR, NTHR><<<grid, NTHR, 0, st>>>(a);
+    k_block_norm<DT, VEC, NV, TPR, NTHR, TAIL><<<grid, NTHR, 0, st>>>(a);
 }
-template <bool BACK, int DT, int VEC, int NV>
+template <bool BACK, int DT, int VEC, int NV, bool TAIL>
 void go_tpr(const Geo& g, const NormDev& a, unsigned grid, hipStream_t st) {
   switch (g.tpr) {
-    case 16: return go<BACK, DT, VEC, NV, 16>(a, grid, st);
-    case 64: return go<BACK, DT, VEC, NV, 64>(a, grid, st);
-    case 256: return go<BACK, DT, VEC, NV, 256>(a, grid, st);
-    case 512: return go<BACK, DT, VEC, NV, 512>(a, grid, st);
-    default: return go<BACK, DT, VEC, NV, 1024>(a, grid, st);
+    case 16: return go<BACK, DT, VEC, NV, 16, TAIL>(a, grid, st);
+    case 64: return go<BACK, DT, VEC, NV, 64, TAIL>(a, grid, st);
+    case 128: return go<BACK, DT, VEC, NV, 128, TAIL>(a, grid, st);
+    case 256: return go<BACK, DT, VEC, NV, 256, TAIL>(a, grid, st);
+    case 512: return go<BACK, DT, VEC, NV, 512, TAIL>(a, grid, st);
+    default: return go<BACK, DT, VEC, NV, 1024, TAIL>(a, grid, st);
   }
+}
+template <bool BACK, int DT>
+void go_vec(const Geo& g, const NormDev& a, unsigned grid, hipStream_t st) {
+  constexpr int VEC = 16 / sizeof(typename Storage<DT>::T);
+  if (!g.vec) return go<BACK, DT, 1, 1, 16, false>(a, grid, st);
+  if (g.nv == 1) return g.tail ? go_tpr<BACK, DT, VEC, 1, true>(g, a, grid, st) : go_tpr<BACK, DT, VEC, 1, false>(g, a, grid, st);
+  if constexpr (VEC == 4)
+    return g.tail ? go_tpr<BACK, DT, VEC, 2, true>(g, a, grid, st) : go_tpr<BACK, DT, VEC, 2, false>(g, a, grid, st);
 }
 template <bool BACK>
 void go_all(bool bf16, const Geo& g, const NormDev& a, unsigned grid, hipStream_t st) {
-  if (g.vec && bf16) return go_tpr<BACK, kBF16, 8, 1>(g, a, grid, st);
-  if (g.vec) {
-    if (g.nv == 1) return go_tpr<BACK, kF32, 4, 1>(g, a, grid, st);
-    return go_tpr<BACK, kF32, 4, 2>(g, a, grid, st);
-  }
-  if (bf16) {
-    if (g.nv == 4) return go_tpr<BACK, kBF16, 1, 4>(g, a, grid, st);
-    return go_tpr<BACK, kBF16, 1, 8>(g, a, grid, st);
-  }
-  if (g.nv == 4) return go_tpr<BACK, kF32, 1, 4>(g, a, grid, st);
-  return go_tpr<BACK, kF32, 1, 8>(g, a, grid, st);
+  if (bf16) go_vec<BACK, kBF16>(g, a, grid, st); else go_vec<BACK, kF32>(g, a, grid, st);
 }
 
 }  // namespace
 
 size_t block_norm_backward_workspace(bool bf16, int64_t N, int64_t d) {
-  return size_t(3) * std::max<int64_t>(1, bw_grid(geo(bf16, d), N)) * d * 4;
+  return size_t(3) * std::max<int64_t>(1, grid_of(geo(bf16, d), bf16, N)) * d * 4;
 }
 
 void launch_block_norm(const BlockNormArgs& a) {
@@ -429,12 +465,12 @@ void launch_block_norm(const BlockNormArgs& a) {
   n.o0 = a.r_out, n.o1 = a.n_out;
   n.w_post = a.w_post, n.w_pre = a.w_pre, n.alpha = a.alpha;
   n.N = a.N, n.d = int(a.d), n.act = a.act, n.eps = a.eps;
-  go_all<false>(a.bf16, g, n, unsigned((a.N + groups_of(g) - 1) / groups_of(g)), a.stream);
+  go_all<false>(a.bf16, g, n, unsigned(grid_of(g, a.bf16, a.N)), a.stream);
 }
 
 void launch_block_norm_backward(const BlockNormArgs& a) {
   const Geo g = geo(a.bf16, a.d);
-  const int64_t G = bw_grid(g, a.N);
+  const int64_t G = grid_of(g, a.bf16, a.N);
   NormDev n{};
   n.h = a.h, n.gate = a.gate, n.x = a.x, n.dr = a.dr, n.dn = a.dn;
   n.o0 = a.dh, n.o1 = a.dgate, n.o2 = a.dx;

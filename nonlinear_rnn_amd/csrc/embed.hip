@@ -13,47 +13,44 @@
 #include "embed.h"
 
 #include <algorithm>
+#include <type_traits>
 
 #include "prn_device.h"
 
 namespace prn {
 namespace {
 
-constexpr int kTile = 2048;     // positions a workgroup sorts
-constexpr int kSortThr = 256;
-constexpr int kItems = kTile / kSortThr;
+constexpr int kSortThr = 512;
 constexpr int kMaxBits = 9;     // of a radix pass
 constexpr int kBins = 1 << kMaxBits;
 constexpr int kBlock = 16;      // sorted positions a group of lanes starts from
-constexpr int kLong = 64;       // rows of a chunk of a frequent token (a multiple of kBlock)
+constexpr int kLong = 16;       // rows of a chunk of a frequent token (a multiple of kBlock)
 
-template <int DT, int VEC> struct Pack;
-template <> struct Pack<kF32, 4> { using T = uint4; };
-template <> struct Pack<kF32, 2> { using T = uint2; };
-template <> struct Pack<kF32, 1> { using T = uint32_t; };
-template <> struct Pack<kBF16, 8> { using T = uint4; };
-template <> struct Pack<kBF16, 4> { using T = uint2; };
-template <> struct Pack<kBF16, 2> { using T = uint32_t; };
-template <> struct Pack<kBF16, 1> { using T = uint16_t; };
+// VEC elements (16 bytes, or one element where a row is shorter than that) at
+// any element's address: global memory takes unaligned vector accesses, so
+// odd widths need no narrower path.  A row's last vector is moved back to end
+// with the row; the channels two lanes then share get the same value from both.
+template <int DT, int VEC>
+struct __attribute__((packed, aligned(sizeof(typename Storage<DT>::T)))) Vec {
+  typename Storage<DT>::T v[VEC];
+};
+template <int DT> constexpr int kVec = 16 / sizeof(typename Storage<DT>::T);
 
 template <int DT, int VEC>
-__device__ __forceinline__ void load_vec(const typename Storage<DT>::T* p, float* o) {
-  using P = typename Pack<DT, VEC>::T;
-  const P q = *reinterpret_cast<const P*>(p);
-  typename Storage<DT>::T t[VEC];
-  __builtin_memcpy(t, &q, sizeof(q));
+__device__ __forceinline__ void unpack(const Vec<DT, VEC>& q, float* o) {
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) o[e] = Storage<DT>::load(&t[e]);
+  for (int e = 0; e < VEC; ++e) o[e] = Storage<DT>::load(&q.v[e]);
+}
+template <int DT, int VEC>
+__device__ __forceinline__ Vec<DT, VEC> load_vec(const typename Storage<DT>::T* p) {
+  return *reinterpret_cast<const Vec<DT, VEC>*>(p);
 }
 template <int DT, int VEC>
 __device__ __forceinline__ void store_vec(typename Storage<DT>::T* p, const float* o) {
-  using P = typename Pack<DT, VEC>::T;
-  typename Storage<DT>::T t[VEC];
+  Vec<DT, VEC> q;
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) t[e] = Storage<DT>::pack(o[e]);
-  P q;
-  __builtin_memcpy(&q, t, sizeof(q));
-  *reinterpret_cast<P*>(p) = q;
+  for (int e = 0; e < VEC; ++e) q.v[e] = Storage<DT>::pack(o[e]);
+  *reinterpret_cast<Vec<DT, VEC>*>(p) = q;
 }
 
 __device__ __forceinline__ int64_t token_at(const void* tokens, int bytes, int64_t n) {
@@ -61,25 +58,36 @@ __device__ __forceinline__ int64_t token_at(const void* tokens, int bytes, int64
                     : static_cast<const int64_t*>(tokens)[n];
 }
 
-// TPR lanes per row.  The pad token's rows are zeros, a token outside the
-// table gives NaN.
+// TPR lanes per row, kRows rows of a group in flight.  The pad token's rows
+// are zeros, a token outside the table gives NaN.
+constexpr int kRows = 4;
 template <int DT, int VEC, int TPR>
 __global__ void __launch_bounds__(256) k_embed(const void* __restrict__ tokens, int token_bytes,
                                                const typename Storage<DT>::T* __restrict__ table, int64_t N, int64_t V,
                                                int64_t d, float scale, int64_t pad,
                                                typename Storage<DT>::T* __restrict__ out) {
-  const int64_t n = static_cast<int64_t>(blockIdx.x) * (256 / TPR) + threadIdx.x / TPR;
-  if (n >= N) return;
-  const int64_t t = token_at(tokens, token_bytes, n);
-  const bool in = t >= 0 && t < V && t != pad;
-  const float fill = t == pad ? 0.0f : __builtin_nanf("");
-  const typename Storage<DT>::T* src = table + (in ? t : 0) * d;
-  for (int64_t c = static_cast<int64_t>(threadIdx.x % TPR) * VEC; c < d; c += TPR * VEC) {
-    float v[VEC];
-    load_vec<DT, VEC>(src + c, v);
+  const int64_t n0 = (static_cast<int64_t>(blockIdx.x) * (256 / TPR) + threadIdx.x / TPR) * kRows;
+  int64_t tok[kRows];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) v[e] = in ? v[e] * scale : fill;
-    store_vec<DT, VEC>(out + n * d + c, v);
+  for (int q = 0; q < kRows; ++q) tok[q] = n0 + q < N ? token_at(tokens, token_bytes, n0 + q) : -1;
+  for (int64_t c = static_cast<int64_t>(threadIdx.x % TPR) * VEC; c < d; c += TPR * VEC) {
+    const int64_t cc = imin(c, d - VEC);
+    Vec<DT, VEC> raw[kRows];
+#pragma unroll
+    for (int q = 0; q < kRows; ++q) {
+      const bool in = tok[q] >= 0 && tok[q] < V && tok[q] != pad;
+      raw[q] = load_vec<DT, VEC>(table + (in ? tok[q] : 0) * d + cc);
+    }
+#pragma unroll
+    for (int q = 0; q < kRows; ++q) {
+      const bool in = tok[q] >= 0 && tok[q] < V && tok[q] != pad;
+      const float fill = tok[q] == pad ? 0.0f : __builtin_nanf("");
+      float v[VEC];
+      unpack<DT, VEC>(raw[q], v);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) v[e] = in ? v[e] * scale : fill;
+      if (n0 + q < N) store_vec<DT, VEC>(out + (n0 + q) * d + cc, v);
+    }
   }
 }
 
@@ -104,7 +112,7 @@ __device__ __forceinline__ uint32_t sort_key(const SortIn& in, int64_t i) {
 
 // Workgroups below n_tiles: the tile's count of every digit.  The others
 // clear their part of dtable (words of 16 bytes).
-template <bool FIRST>
+template <bool FIRST, int ITEMS>
 __global__ void __launch_bounds__(kSortThr) k_embed_count(SortIn in, int64_t N, int shift, int bits, int n_tiles,
                                                           uint32_t* __restrict__ counts, uint4* __restrict__ clear,
                                                           int64_t n_clear, uint8_t* __restrict__ tail, int n_tail) {
@@ -118,9 +126,9 @@ __global__ void __launch_bounds__(kSortThr) k_embed_count(SortIn in, int64_t N, 
   __shared__ uint32_t hist[kBins];
   for (int b = threadIdx.x; b < kBins; b += kSortThr) hist[b] = 0;
   __syncthreads();
-  const int64_t at = static_cast<int64_t>(blockIdx.x) * kTile;
+  const int64_t at = static_cast<int64_t>(blockIdx.x) * (ITEMS * kSortThr);
 #pragma unroll
-  for (int j = 0; j < kItems; ++j) {
+  for (int j = 0; j < ITEMS; ++j) {
     const int64_t i = at + j * kSortThr + threadIdx.x;
     if (i < N) atomicAdd(&hist[(sort_key<FIRST>(in, i) >> shift) & ((1u << bits) - 1)], 1u);
   }
@@ -129,88 +137,107 @@ __global__ void __launch_bounds__(kSortThr) k_embed_count(SortIn in, int64_t N, 
     counts[static_cast<int64_t>(blockIdx.x) * kBins + b] = hist[b];
 }
 
-// Stable scatter by one digit: wave w of a tile holds its positions 512 w ..
-// + 511 in order; a position's rank among the equal digits before it in the
-// wave comes from ballots, the counts of earlier waves, tiles and digits are
-// added to it.
-template <bool FIRST>
+// The lanes of the wave that hold the same digit (of `bits` bits), this one
+// among them; live lanes only.
+__device__ __forceinline__ unsigned long long same_digit(uint32_t dg, int bits, bool live) {
+  unsigned long long same = __ballot(live);
+#pragma unroll
+  for (int b = 0; b < kMaxBits; ++b) {
+    if (b < bits) {
+      const bool on = (dg >> b) & 1;
+      const unsigned long long m = __ballot(on);
+      same &= on ? m : ~m;
+    }
+  }
+  return same;
+}
+// inclusive sum over the wave
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const uint32_t up = __shfl_up(v, o, 64);
+    if (lane >= o) v += up;
+  }
+  return v;
+}
+
+// Stable scatter by one digit.  A wave of a tile holds 64 ITEMS positions in
+// order; a position's rank among the equal digits before it in the wave comes
+// from ballots, the counts of earlier waves, tiles and digits are added to it.
+template <bool FIRST, int ITEMS>
 __global__ void __launch_bounds__(kSortThr) k_embed_scatter(SortIn in, int64_t N, int shift, int bits, int n_tiles,
                                                             const uint32_t* __restrict__ counts,
                                                             uint32_t* __restrict__ keys_out,
                                                             uint32_t* __restrict__ pos_out) {
   constexpr int NW = kSortThr / 64;
-  __shared__ uint32_t start[kBins];        // where the tile's first position of a digit goes
+  static_assert(kBins == kSortThr, "a digit a thread");
   __shared__ uint32_t wave_hist[NW][kBins];
   __shared__ uint32_t scan[NW];
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-  const int nb = 1 << bits;
-  for (int b = lane; b < nb; b += 64) wave_hist[w][b] = 0;
-  __syncthreads();
-  const int64_t at = static_cast<int64_t>(blockIdx.x) * kTile + w * (kTile / NW);
-  // other lanes of the wave write it between two reads
-  volatile uint32_t* const mine_hist = wave_hist[w];
-  uint32_t key[kItems], pos[kItems], rank[kItems];
+  const int nb = 1 << bits, me = static_cast<int>(blockIdx.x);
+  const int64_t at = (static_cast<int64_t>(me) * NW + w) * (64 * ITEMS);
+  uint32_t key[ITEMS], pos[ITEMS], rank[ITEMS];
 #pragma unroll
-  for (int j = 0; j < kItems; ++j) {
+  for (int j = 0; j < ITEMS; ++j) {
     const int64_t i = at + j * 64 + lane;
     key[j] = i < N ? sort_key<FIRST>(in, i) : 0;
     pos[j] = FIRST ? static_cast<uint32_t>(i) : i < N ? in.pos[i] : 0;
   }
+  // this thread's digit: its count in all tiles, and in the tiles before this one
+  uint32_t total = 0, before = 0;
+  if (tid < nb) {
+    int t = 0;
+    for (; t + 32 <= n_tiles; t += 32) {
+      uint32_t c[32];
 #pragma unroll
-  for (int j = 0; j < kItems; ++j) {
-    const bool live = at + j * 64 + lane < N;
-    const uint32_t dg = (key[j] >> shift) & (nb - 1);
-    unsigned long long same = __ballot(live);
-    for (int b = 0; b < bits; ++b) {
-      const unsigned long long m = __ballot((dg >> b) & 1);
-      same &= (dg >> b) & 1 ? m : ~m;
-    }
-    if (live) {
-      const unsigned long long below = same & ((1ull << lane) - 1);
-      const uint32_t before = mine_hist[dg];
-      rank[j] = before + __popcll(below);
-      // the last lane of the digit counts them all (a wave's LDS accesses are done in order)
-      if ((same >> lane) == 1ull) mine_hist[dg] = before + __popcll(same);
-    }
-  }
-  // digit totals, and those of the tiles before this one
-  uint32_t total[kBins / kSortThr], before[kBins / kSortThr];
+      for (int q = 0; q < 32; ++q) c[q] = counts[static_cast<int64_t>(t + q) * kBins + tid];
 #pragma unroll
-  for (int q = 0; q < kBins / kSortThr; ++q) {
-    const int b = 2 * tid + q;
-    uint32_t all = 0, less = 0;
-    if (b < nb) {
-#pragma unroll 8
-      for (int t = 0; t < n_tiles; ++t) {
-        const uint32_t c = counts[static_cast<int64_t>(t) * kBins + b];
-        all += c;
-        less += t < static_cast<int>(blockIdx.x) ? c : 0;
+      for (int q = 0; q < 32; ++q) {
+        total += c[q];
+        before += t + q < me ? c[q] : 0;
       }
     }
-    total[q] = all;
-    before[q] = less;
+#pragma unroll 8
+    for (; t < n_tiles; ++t) {
+      const uint32_t c = counts[static_cast<int64_t>(t) * kBins + tid];
+      total += c;
+      before += t < me ? c : 0;
+    }
   }
-  // exclusive sum of the totals over the digits (two neighbouring digits a thread)
-  const uint32_t mine = total[0] + total[1];
-  uint32_t incl = mine;
+  for (int b = lane; b < nb; b += 64) wave_hist[w][b] = 0;
+  // other lanes of the wave write it between two reads; a wave's LDS accesses are done in order
+  volatile uint32_t* const mine_hist = wave_hist[w];
 #pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const uint32_t up = __shfl_up(incl, o, 64);
-    if (lane >= o) incl += up;
+  for (int j = 0; j < ITEMS; ++j) {
+    const bool live = at + j * 64 + lane < N;
+    const uint32_t dg = (key[j] >> shift) & (nb - 1);
+    const unsigned long long same = same_digit(dg, bits, live);
+    if (live) {
+      const uint32_t sofar = mine_hist[dg];
+      rank[j] = sofar + __popcll(same & ((1ull << lane) - 1));
+      if ((same >> lane) == 1ull) mine_hist[dg] = sofar + __popcll(same);   // the last lane of the digit counts them all
+    }
   }
+  // exclusive sum of the totals over the digits
+  const uint32_t incl = wave_scan(total);
   if (lane == 63) scan[w] = incl;
   __syncthreads();   // also: every wave's histogram is complete
-  uint32_t base = incl - mine;
+  uint32_t base = incl - total + before;
   for (int q = 0; q < w; ++q) base += scan[q];
-  start[2 * tid] = base + before[0];
-  start[2 * tid + 1] = base + total[0] + before[1];
+  if (tid < nb) {    // where each wave's first position of the digit goes
+#pragma unroll
+    for (int q = 0; q < NW; ++q) {
+      const uint32_t c = wave_hist[q][tid];
+      wave_hist[q][tid] = base;
+      base += c;
+    }
+  }
   __syncthreads();
 #pragma unroll
-  for (int j = 0; j < kItems; ++j) {
+  for (int j = 0; j < ITEMS; ++j) {
     if (at + j * 64 + lane < N) {
-      const uint32_t dg = (key[j] >> shift) & (nb - 1);
-      uint32_t to = start[dg] + rank[j];
-      for (int q = 0; q < w; ++q) to += wave_hist[q][dg];
+      const uint32_t to = wave_hist[w][(key[j] >> shift) & (nb - 1)] + rank[j];
       keys_out[to] = key[j];
       pos_out[to] = pos[j];
     }
@@ -243,17 +270,19 @@ __device__ __forceinline__ void walk_rows(const typename Storage<DT>::T* dout, i
 #pragma unroll
   for (int e = 0; e < VEC; ++e) acc[e] = 0.0f;
   for (int i = i0; i < i1; i += kBatch) {
-    float v[kBatch][VEC];
+    Vec<DT, VEC> raw[kBatch];
 #pragma unroll
     for (int q = 0; q < kBatch; ++q) {
-      if (i + q < i1 && mine) load_vec<DT, VEC>(dout + static_cast<int64_t>(where(i + q)) * d + c, v[q]);
+      if (i + q < i1 && mine) raw[q] = load_vec<DT, VEC>(dout + static_cast<int64_t>(where(i + q)) * d + c);
     }
 #pragma unroll
     for (int q = 0; q < kBatch; ++q) {
       if (i + q < i1) {
         emit(i + q, acc);
+        float v[VEC];
+        unpack<DT, VEC>(raw[q], v);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) acc[e] += v[q][e];
+        for (int e = 0; e < VEC; ++e) acc[e] += v[e];
       }
     }
   }
@@ -263,8 +292,9 @@ __device__ __forceinline__ void walk_rows(const typename Storage<DT>::T* dout, i
 // every token whose rows start there, and the chunk of a frequent token from
 // an earlier block that starts there (at most one: chunks are kLong >= kBlock
 // apart).  A frequent token's chunks go to part: its first to row 2 block + 1,
-// the others to row 2 block.  The keys and positions of the 127 sorted places
-// a wave may need are loaded at once; every decision after that is a ballot.
+// the others to row 2 block.  The keys and positions of the 64 sorted places a
+// wave may need (kBlock - 1 + kLong of them) are loaded at once; every decision
+// after that is a ballot.
 template <int DT, int VEC>
 __global__ void __launch_bounds__(256) k_embed_sum(const uint32_t* __restrict__ keys, const uint32_t* __restrict__ pos,
                                                    const typename Storage<DT>::T* __restrict__ dout, int64_t N, int64_t V,
@@ -275,19 +305,17 @@ __global__ void __launch_bounds__(256) k_embed_sum(const uint32_t* __restrict__ 
   const int64_t block = static_cast<int64_t>(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t p0 = block * kBlock;
   if (p0 >= N) return;
-  const int64_t c = (static_cast<int64_t>(blockIdx.y) * 64 + lane) * VEC;
-  const bool mine = c < d;
-  // place t (position p0 + t): lane t + 1 of the first window for t < 63, lane t - 63 of the second
-  const int64_t ia = p0 - 1 + lane, ib = p0 + 63 + lane;
-  const uint32_t ka = ia >= 0 && ia < N ? keys[ia] : kNone, kb = ib < N ? keys[ib] : kNone;
-  const uint32_t qa = ia >= 0 && ia < N ? pos[ia] : 0, qb = ib < N ? pos[ib] : 0;
-  const uint32_t prev_a = __shfl_up(ka, 1, 64), last_a = __shfl(ka, 63, 64), prev_b = __shfl_up(kb, 1, 64);
-  const uint32_t kb_at = __shfl_up(kb, 1, 64);   // lane t + 1: the key kLong - 1 places after place t
-  // bit t: place t holds another key than place t - 1; bit l of the second: place 63 + l
-  const unsigned long long turn_a = __ballot(lane >= 1 && ka != prev_a) >> 1;
-  const unsigned long long turn_b = __ballot(kb != (lane == 0 ? last_a : prev_b));
-  const unsigned own = static_cast<unsigned>(turn_a & __ballot(ka < V) >> 1) & ((1u << kBlock) - 1);
-  const unsigned frequent = own & static_cast<unsigned>(__ballot(ka == kb_at) >> 1);
+  const int64_t c0 = (static_cast<int64_t>(blockIdx.y) * 64 + lane) * VEC, c = imin(c0, d - VEC);
+  const bool mine = c0 < d;
+  // lane t + 1: place t (position p0 + t), the place before p0 in lane 0
+  static_assert(kBlock + kLong <= 63, "the places fit a wave");
+  const int64_t ia = p0 - 1 + lane;
+  const uint32_t ka = ia >= 0 && ia < N ? keys[ia] : kNone, qa = ia >= 0 && ia < N ? pos[ia] : 0;
+  const uint32_t prev = __shfl_up(ka, 1, 64), later = __shfl_down(ka, kLong - 1, 64);
+  // bit t: place t holds another key than place t - 1
+  const unsigned long long turn = __ballot(lane >= 1 && ka != prev) >> 1;
+  const unsigned own = static_cast<unsigned>(turn & __ballot(ka < V) >> 1) & ((1u << kBlock) - 1);
+  const unsigned frequent = own & static_cast<unsigned>(__ballot(ka == later) >> 1);
   float acc[VEC];
   auto to_part = [&](int64_t row) {
     if (mine) {
@@ -297,15 +325,16 @@ __global__ void __launch_bounds__(256) k_embed_sum(const uint32_t* __restrict__ 
   };
 
   const uint32_t k0 = __shfl(ka, 1, 64);
-  if (!(turn_a & 1) && k0 < V) {
+  if (!(turn & 1) && k0 < V) {
     // a token from an earlier block: its chunk that starts here, if it is a frequent one
     const int64_t s = lower_bound(keys, p0, k0);
     if (s + kLong <= N && keys[s + kLong - 1] == k0) {
       const int64_t b = s + (p0 - s + kLong - 1) / kLong * kLong;
-      const unsigned long long run = __ballot(b + lane < N && keys[b + lane < N ? b + lane : N - 1] == k0);
-      const uint32_t at = b + lane < N ? pos[b + lane] : 0;
+      const bool in = lane < kLong && b + lane < N;
+      const unsigned long long run = __ballot(in && keys[in ? b + lane : 0] == k0);
+      const uint32_t at = in ? pos[b + lane] : 0;
       if (b < p0 + kBlock && (run & 1)) {
-        const int n = ~run == 0 ? 64 : __builtin_ctzll(~run);
+        const int n = __builtin_ctzll(~run);   // up to kLong
         walk_rows<DT, VEC>(dout, d, c, mine, 0, n, [&](int i) { return __builtin_amdgcn_readlane(at, i); },
                            [](int, float*) {}, acc);
         to_part(2 * block);
@@ -315,9 +344,8 @@ __global__ void __launch_bounds__(256) k_embed_sum(const uint32_t* __restrict__ 
   if (!own) return;
   const int t0 = __builtin_ctz(own), t1 = 31 - __builtin_clz(own);   // first and last token that starts here
   const bool last_frequent = (frequent >> t1) & 1;
-  const unsigned long long rest = turn_a >> (t1 + 1);
-  // the next turn, in the first window or (a shorter run ends by place t1 + kLong - 1) the second
-  const int end = last_frequent ? t1 + kLong : rest ? t1 + 1 + __builtin_ctzll(rest) : 63 + __builtin_ctzll(turn_b);
+  // a shorter run ends within kLong places
+  const int end = last_frequent ? t1 + kLong : t1 + 1 + __builtin_ctzll(turn >> (t1 + 1));
   uint32_t token = __builtin_amdgcn_readlane(ka, t0 + 1);
   auto to_table = [&]() {
     if (mine) {
@@ -329,7 +357,7 @@ __global__ void __launch_bounds__(256) k_embed_sum(const uint32_t* __restrict__ 
   };
   walk_rows<DT, VEC>(
       dout, d, c, mine, t0, end,
-      [&](int t) { return t < 63 ? __builtin_amdgcn_readlane(qa, t + 1) : __builtin_amdgcn_readlane(qb, t - 63); },
+      [&](int t) { return __builtin_amdgcn_readlane(qa, t + 1); },
       [&](int t, float* s) {
         if (t > t0 && t <= t1 && ((own >> t) & 1)) {
           to_table();
@@ -346,46 +374,164 @@ __global__ void __launch_bounds__(256) k_embed_sum(const uint32_t* __restrict__ 
 }
 
 // The frequent tokens that start among kJoin sorted positions: their chunks'
-// sums, added in order by 16 waves (every 16th chunk each, then the waves in
-// order), 64 channels at a time.
-constexpr int kJoin = 1024;
-template <int DT>
-__global__ void __launch_bounds__(1024) k_embed_join(const uint32_t* __restrict__ keys, const float* __restrict__ part,
-                                                     int64_t N, int64_t V, int64_t d, float scale,
-                                                     typename Storage<DT>::T* __restrict__ dtable) {
+// sums at 64 CPT channels (blockIdx.y), added in order by 16 waves (every 16th
+// chunk each, then the waves in order).
+constexpr int kJoin = 256, kJoinThr = 1024, kJoinBatch = 8;
+template <int DT, int CPT>
+__global__ void __launch_bounds__(kJoinThr) k_embed_join(const uint32_t* __restrict__ keys, const float* __restrict__ part,
+                                                         int64_t N, int64_t V, int64_t d, float scale,
+                                                         typename Storage<DT>::T* __restrict__ dtable) {
+  using F = Vec<kF32, CPT>;
+  constexpr int NW = kJoinThr / 64;
   __shared__ uint32_t n_found;
   __shared__ uint32_t found[kJoin / kLong + 1];
-  __shared__ float hand[16][64];
-  if (threadIdx.x == 0) n_found = 0;
-  __syncthreads();
+  __shared__ float hand[NW][64 * CPT];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int64_t at = static_cast<int64_t>(blockIdx.x) * kJoin;
   const int64_t p = at + threadIdx.x;
-  if (p + kLong <= N) {
+  bool starts = false;
+  if (threadIdx.x < kJoin && p + kLong <= N) {
     const uint32_t k = keys[p];
-    if (k < V && keys[p + kLong - 1] == k && (p == 0 || keys[p - 1] != k)) found[atomicAdd(&n_found, 1u)] = threadIdx.x;
+    starts = k < V && keys[p + kLong - 1] == k && (p == 0 || keys[p - 1] != k);
   }
+  if (threadIdx.x == 0) n_found = 0;
   __syncthreads();
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  if (starts) found[atomicAdd(&n_found, 1u)] = threadIdx.x;
+  __syncthreads();
+  const int64_t c0 = (static_cast<int64_t>(blockIdx.y) * 64 + lane) * CPT, c = imin(c0, d - CPT);
+  const bool mine = c0 < d;
   for (uint32_t f = 0; f < n_found; ++f) {   // in any order: each writes its own row
     const int64_t s = at + found[f];
     const uint32_t k = keys[s];
-    const int64_t len = lower_bound(keys, N, k + 1) - s, chunks = (len + kLong - 1) / kLong;
-    for (int64_t c0 = 0; c0 < d; c0 += 64) {
-      const int64_t c = c0 + lane;
-      float acc = 0.0f;
-      if (c < d) {
-#pragma unroll 4
-        for (int64_t q = w; q < chunks; q += 16) acc += part[(2 * ((s + q * kLong) / kBlock) + (q == 0)) * d + c];
-      }
-      hand[w][lane] = acc;
-      __syncthreads();
-      if (w == 0 && c < d) {
+    float acc[CPT];
 #pragma unroll
-        for (int q = 1; q < 16; ++q) acc += hand[q][lane];
-        dtable[static_cast<int64_t>(k) * d + c] = Storage<DT>::pack(acc * scale);
+    for (int e = 0; e < CPT; ++e) acc[e] = 0.0f;
+    // the token's chunks, 64 at a time: chunk q is there if its first position holds the token
+    for (int64_t q0 = 0;; q0 += 64) {
+      const int64_t i = s + (q0 + lane) * kLong;
+      const unsigned long long there = __ballot(i < N && keys[i < N ? i : s] == k);
+      const int n = ~there == 0 ? 64 : __builtin_ctzll(~there);
+      if (mine) {
+        for (int q = w; q < n; q += NW * kJoinBatch) {
+          F v[kJoinBatch];
+#pragma unroll
+          for (int b = 0; b < kJoinBatch; ++b) {
+            const int64_t qq = q0 + q + b * NW;
+            if (q + b * NW < n) v[b] = *reinterpret_cast<const F*>(part + (2 * ((s + qq * kLong) / kBlock) + (qq == 0)) * d + c);
+          }
+#pragma unroll
+          for (int b = 0; b < kJoinBatch; ++b)
+            if (q + b * NW < n) {
+#pragma unroll
+              for (int e = 0; e < CPT; ++e) acc[e] += v[b].v[e];
+            }
+        }
       }
-      __syncthreads();
+      if (n < 64) break;
     }
+#pragma unroll
+    for (int e = 0; e < CPT; ++e) hand[w][lane * CPT + e] = acc[e];
+    __syncthreads();
+    if (w == 0 && mine) {
+#pragma unroll
+      for (int q = 1; q < NW; ++q)
+#pragma unroll
+        for (int e = 0; e < CPT; ++e) acc[e] += hand[q][lane * CPT + e];
+#pragma unroll
+      for (int e = 0; e < CPT; ++e) acc[e] *= scale;
+      store_vec<DT, CPT>(dtable + static_cast<int64_t>(k) * d + c, acc);
+    }
+    __syncthreads();
+  }
+}
+
+// ------------------------------------------------------------ small sort ---
+
+// The whole sort in one workgroup's LDS, for up to kSmall positions whose key
+// and position fit one word (key above, position below): the other workgroups
+// of the launch clear dtable meanwhile.  A wave holds its positions in
+// order and ranks equal digits by ballots, as k_embed_scatter does.
+constexpr int kSmall = 8192, kSmallThr = 1024, kSmallItems = kSmall / kSmallThr;
+__global__ void __launch_bounds__(kSmallThr) k_embed_sort(SortIn in, int N, int pos_bits, int bits, int passes,
+                                                          uint32_t* __restrict__ keys, uint32_t* __restrict__ pos,
+                                                          uint4* __restrict__ clear, int64_t n_clear,
+                                                          uint8_t* __restrict__ tail, int n_tail) {
+  constexpr int NW = kSmallThr / 64;
+  __shared__ uint32_t word[kSmall];
+  __shared__ uint16_t wave_hist[NW][kBins];
+  __shared__ uint32_t start[kBins];
+  __shared__ uint32_t scan[NW];
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  if (blockIdx.x > 0) {
+    const int64_t me = (static_cast<int64_t>(blockIdx.x) - 1) * kSmallThr + tid;
+    const int64_t all = (static_cast<int64_t>(gridDim.x) - 1) * kSmallThr;
+    for (int64_t i = me; i < n_clear; i += all) clear[i] = make_uint4(0, 0, 0, 0);
+    if (me < n_tail) tail[me] = 0;
+    return;
+  }
+  const int items = (N + kSmallThr - 1) / kSmallThr;   // of each lane; a wave's are together
+  const int at = w * items * 64;
+  const int nb = 1 << bits;
+  volatile uint16_t* const mine_hist = wave_hist[w];
+  uint32_t v[kSmallItems];
+  uint16_t rank[kSmallItems];
+#pragma unroll
+  for (int j = 0; j < kSmallItems; ++j) {
+    const int i = at + j * 64 + lane;
+    if (j < items && i < N) v[j] = sort_key<true>(in, i) << pos_bits | static_cast<uint32_t>(i);
+  }
+  for (int p = 0; p < passes; ++p) {
+    const int shift = pos_bits + p * bits;
+    for (int b = lane; b < nb; b += 64) wave_hist[w][b] = 0;
+    // (a wave's LDS accesses are done in order)
+#pragma unroll
+    for (int j = 0; j < kSmallItems; ++j) {
+      const int i = at + j * 64 + lane;
+      if (j < items) {
+        if (p > 0 && i < N) v[j] = word[i];
+        const bool live = i < N;
+        const uint32_t dg = (v[j] >> shift) & (nb - 1);
+        const unsigned long long same = same_digit(dg, bits, live);
+        if (live) {
+          const uint16_t before = mine_hist[dg];
+          rank[j] = static_cast<uint16_t>(before + __popcll(same & ((1ull << lane) - 1)));
+          if ((same >> lane) == 1ull) mine_hist[dg] = static_cast<uint16_t>(before + __popcll(same));
+        }
+      }
+    }
+    __syncthreads();   // every wave's counts are there, and every word is in a register
+    // counts of earlier waves, and the digits' totals
+    uint32_t total = 0;
+    if (tid < nb) {
+#pragma unroll
+      for (int q = 0; q < NW; ++q) {
+        const uint32_t c = wave_hist[q][tid];
+        wave_hist[q][tid] = static_cast<uint16_t>(total);
+        total += c;
+      }
+    }
+    const uint32_t incl = wave_scan(total);
+    if (lane == 63) scan[w] = incl;
+    __syncthreads();
+    if (tid < nb) {
+      uint32_t base = incl - total;
+      for (int q = 0; q < w; ++q) base += scan[q];
+      start[tid] = base;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kSmallItems; ++j) {
+      const int i = at + j * 64 + lane;
+      if (j < items && i < N) {
+        const uint32_t dg = (v[j] >> shift) & (nb - 1);
+        word[start[dg] + wave_hist[w][dg] + rank[j]] = v[j];
+      }
+    }
+    __syncthreads();
+  }
+  for (int i = tid; i < N; i += kSmallThr) {
+    keys[i] = word[i] >> pos_bits;
+    pos[i] = word[i] & ((1u << pos_bits) - 1);
   }
 }
 
@@ -395,7 +541,7 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
 
 struct Plan {
-  int passes, bits;
+  int key_bits, passes, bits, items;
   int64_t tiles;
   size_t counts_off, key_off[2], pos_off[2], part_off, total;
 };
@@ -403,9 +549,12 @@ Plan plan(const EmbedArgs& a) {
   Plan p{};
   int bits = 1;
   while ((a.V >> bits) != 0) ++bits;   // keys 0 .. V
+  p.key_bits = bits;
   p.passes = (bits + kMaxBits - 1) / kMaxBits;
   p.bits = (bits + p.passes - 1) / p.passes;
-  p.tiles = cdiv(a.N, kTile);
+  // small tiles while they are few: every tile adds up the counts of all
+  p.items = a.N <= 64 * 2 * kSortThr ? 2 : 4;
+  p.tiles = cdiv(a.N, p.items * kSortThr);
   size_t off = up(size_t(p.tiles) * kBins * 4);
   for (int i = 0; i < 2; ++i) {
     p.key_off[i] = off;
@@ -418,15 +567,12 @@ Plan plan(const EmbedArgs& a) {
   return p;
 }
 
-// elements per access: the largest power of two that divides a row and its
-// 16 bytes and keeps every base aligned
-int vec_of(bool bf16, int64_t d, const void* p, const void* q) {
-  const int elt = bf16 ? 2 : 4;
-  int v = 16 / elt;
-  while (v > 1 && (d % v != 0 || reinterpret_cast<uintptr_t>(p) % (v * elt) != 0 ||
-                   reinterpret_cast<uintptr_t>(q) % (v * elt) != 0))
-    v /= 2;
-  return v;
+// does one workgroup sort them all?
+bool small_sort(const EmbedArgs& a, int key_bits, int* pos_bits) {
+  int pb = 1;
+  while (((a.N - 1) >> pb) != 0) ++pb;
+  *pos_bits = pb;
+  return a.N <= kSmall && key_bits + pb <= 32;
 }
 
 template <int DT, int VEC>
@@ -434,7 +580,7 @@ void embed_vec(const EmbedArgs& a, const void* tokens, const void* table, void* 
   using T = typename Storage<DT>::T;
   auto run = [&](auto tpr) {
     constexpr int TPR = decltype(tpr)::value;
-    k_embed<DT, VEC, TPR><<<unsigned(cdiv(a.N, 256 / TPR)), 256, 0, a.stream>>>(
+    k_embed<DT, VEC, TPR><<<unsigned(cdiv(a.N, 256 / TPR * kRows)), 256, 0, a.stream>>>(
         tokens, a.token_bytes, static_cast<const T*>(table), a.N, a.V, a.d, a.scale, a.pad, static_cast<T*>(out));
   };
   if (a.d <= 16 * VEC) run(std::integral_constant<int, 16>{});
@@ -444,12 +590,14 @@ void embed_vec(const EmbedArgs& a, const void* tokens, const void* table, void* 
 template <int DT, int VEC>
 void sum_vec(const EmbedArgs& a, const Plan& p, const uint32_t* keys, const uint32_t* pos, const void* dout, void* dtable) {
   using T = typename Storage<DT>::T;
+  constexpr int CPT = VEC > 4 ? 4 : VEC;
   float* part = reinterpret_cast<float*>(a.ws + p.part_off);
   const dim3 grid(unsigned(cdiv(cdiv(a.N, kBlock), 4)), unsigned(cdiv(a.d, 64 * VEC)));
   k_embed_sum<DT, VEC><<<grid, 256, 0, a.stream>>>(keys, pos, static_cast<const T*>(dout), a.N, a.V, a.d, a.scale,
                                                    static_cast<T*>(dtable), part);
-  k_embed_join<DT><<<unsigned(cdiv(a.N, kJoin)), 1024, 0, a.stream>>>(keys, part, a.N, a.V, a.d, a.scale,
-                                                                       static_cast<T*>(dtable));
+  if (a.N < kLong) return;
+  const dim3 jgrid(unsigned(cdiv(a.N, kJoin)), unsigned(cdiv(a.d, 64 * CPT)));
+  k_embed_join<DT, CPT><<<jgrid, kJoinThr, 0, a.stream>>>(keys, part, a.N, a.V, a.d, a.scale, static_cast<T*>(dtable));
 }
 
 }  // namespace
@@ -457,16 +605,9 @@ void sum_vec(const EmbedArgs& a, const Plan& p, const uint32_t* keys, const uint
 size_t embed_backward_workspace(const EmbedArgs& a) { return a.N ? plan(a).total : 0; }
 
 void launch_embed(const EmbedArgs& a, const void* tokens, const void* table, void* out) {
-  const int v = vec_of(a.bf16, a.d, table, out);
-  if (a.bf16) {
-    if (v == 8) return embed_vec<kBF16, 8>(a, tokens, table, out);
-    if (v == 4) return embed_vec<kBF16, 4>(a, tokens, table, out);
-    if (v == 2) return embed_vec<kBF16, 2>(a, tokens, table, out);
-    return embed_vec<kBF16, 1>(a, tokens, table, out);
-  }
-  if (v == 4) return embed_vec<kF32, 4>(a, tokens, table, out);
-  if (v == 2) return embed_vec<kF32, 2>(a, tokens, table, out);
-  return embed_vec<kF32, 1>(a, tokens, table, out);
+  if (a.bf16)
+    return a.d >= kVec<kBF16> ? embed_vec<kBF16, kVec<kBF16>>(a, tokens, table, out) : embed_vec<kBF16, 1>(a, tokens, table, out);
+  return a.d >= kVec<kF32> ? embed_vec<kF32, kVec<kF32>>(a, tokens, table, out) : embed_vec<kF32, 1>(a, tokens, table, out);
 }
 
 void launch_embed_backward(const EmbedArgs& a, const void* tokens, const void* dout, void* dtable) {
@@ -480,36 +621,46 @@ void launch_embed_backward(const EmbedArgs& a, const void* tokens, const void* d
   const size_t bytes = size_t(a.V) * a.d * (a.bf16 ? 2 : 4);
   uint8_t* const lo = static_cast<uint8_t*>(dtable);   // 16-byte aligned
   const int64_t words = int64_t(bytes / 16);
+  uint4* const clear = reinterpret_cast<uint4*>(lo);
+  uint8_t* const tail = lo + words * 16;
+  const int n_tail = int(bytes % 16);
   SortIn in{tokens, a.token_bytes, a.V, a.pad, nullptr, nullptr};
-  int cur = 0;
-  for (int s = 0; s < p.passes; ++s) {
-    const int shift = s * p.bits;
-    const unsigned tiles = unsigned(p.tiles);
-    if (s == 0) {
-      const unsigned clear = unsigned(std::min<int64_t>(1024, cdiv(words, kSortThr) + 1));
-      k_embed_count<true><<<tiles + clear, kSortThr, 0, a.stream>>>(in, a.N, shift, p.bits, int(tiles), counts,
-                                                                    reinterpret_cast<uint4*>(lo), words, lo + words * 16,
-                                                                    int(bytes % 16));
-      if (a.N == 0) return;
-      k_embed_scatter<true><<<tiles, kSortThr, 0, a.stream>>>(in, a.N, shift, p.bits, int(tiles), counts, keys[0], pos[0]);
-    } else {
-      in.keys = keys[cur];
-      in.pos = pos[cur];
-      k_embed_count<false><<<tiles, kSortThr, 0, a.stream>>>(in, a.N, shift, p.bits, int(tiles), counts, nullptr, 0, nullptr, 0);
-      k_embed_scatter<false><<<tiles, kSortThr, 0, a.stream>>>(in, a.N, shift, p.bits, int(tiles), counts, keys[cur ^ 1],
-                                                               pos[cur ^ 1]);
-      cur ^= 1;
-    }
+  int cur = 0, pos_bits;
+  if (a.N > 0 && small_sort(a, p.key_bits, &pos_bits)) {
+    const unsigned others = unsigned(std::min<int64_t>(255, cdiv(words, kSmallThr) + 1));
+    k_embed_sort<<<1 + others, kSmallThr, 0, a.stream>>>(in, int(a.N), pos_bits, p.bits, p.passes, keys[0], pos[0], clear,
+                                                         words, tail, n_tail);
+  } else {
+    auto sort = [&](auto items) {
+      constexpr int IT = decltype(items)::value;
+      const unsigned tiles = unsigned(p.tiles), others = unsigned(std::min<int64_t>(1024, cdiv(words, kSortThr) + 1));
+      for (int s = 0; s < p.passes; ++s) {
+        const int shift = s * p.bits;
+        if (s == 0) {
+          k_embed_count<true, IT><<<tiles + others, kSortThr, 0, a.stream>>>(in, a.N, shift, p.bits, int(tiles), counts,
+                                                                             clear, words, tail, n_tail);
+          if (a.N == 0) return;
+          k_embed_scatter<true, IT><<<tiles, kSortThr, 0, a.stream>>>(in, a.N, shift, p.bits, int(tiles), counts, keys[0],
+                                                                      pos[0]);
+          continue;
+        }
+        in.keys = keys[cur];
+        in.pos = pos[cur];
+        k_embed_count<false, IT><<<tiles, kSortThr, 0, a.stream>>>(in, a.N, shift, p.bits, int(tiles), counts, nullptr, 0,
+                                                                   nullptr, 0);
+        k_embed_scatter<false, IT><<<tiles, kSortThr, 0, a.stream>>>(in, a.N, shift, p.bits, int(tiles), counts,
+                                                                     keys[cur ^ 1], pos[cur ^ 1]);
+        cur ^= 1;
+      }
+    };
+    if (p.items == 2) sort(std::integral_constant<int, 2>{}); else sort(std::integral_constant<int, 4>{});
+    if (a.N == 0) return;
   }
-  const int v = vec_of(a.bf16, a.d, dout, dtable);
   if (a.bf16) {
-    if (v == 8) return sum_vec<kBF16, 8>(a, p, keys[cur], pos[cur], dout, dtable);
-    if (v == 4) return sum_vec<kBF16, 4>(a, p, keys[cur], pos[cur], dout, dtable);
-    if (v == 2) return sum_vec<kBF16, 2>(a, p, keys[cur], pos[cur], dout, dtable);
+    if (a.d >= kVec<kBF16>) return sum_vec<kBF16, kVec<kBF16>>(a, p, keys[cur], pos[cur], dout, dtable);
     return sum_vec<kBF16, 1>(a, p, keys[cur], pos[cur], dout, dtable);
   }
-  if (v == 4) return sum_vec<kF32, 4>(a, p, keys[cur], pos[cur], dout, dtable);
-  if (v == 2) return sum_vec<kF32, 2>(a, p, keys[cur], pos[cur], dout, dtable);
+  if (a.d >= kVec<kF32>) return sum_vec<kF32, kVec<kF32>>(a, p, keys[cur], pos[cur], dout, dtable);
   return sum_vec<kF32, 1>(a, p, keys[cur], pos[cur], dout, dtable);
 }
 
