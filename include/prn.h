@@ -462,11 +462,13 @@ prn_status prn_vocab_loss(const void* x, const void* W, const void* targets, con
  *   dx_out (N, d) = dz W, dW_out (V, d) = dz^T x: storage dtype, each optional
  *   lse     the forward's lse_out; dloss (N) fp32; dlse (N) fp32 or NULL: the
  *           gradients arriving at loss_out and lse_out
- * With bf16 storage dz is rounded once to bf16, relative to the largest
- * coefficient of the call, for the matrix cores.  A target out of range gives
- * NaN in its row of dx and in dW.  x, W, dx_out and dW_out must be 16-byte
- * aligned.  The workspace holds one piece of dz (about 256 MB at most, or 512
- * bytes per token where that is more) and fp32 sums of dx and of a piece of dW. */
+ * With bf16 storage dz is rounded once, to fp16 in units of the call's largest
+ * coefficient, for the matrix cores (x and W go there as fp16 too, scaled by
+ * powers of two).  A target out of range gives NaN in its row of dx and in
+ * dW.  x, W, dx_out and dW_out must be 16-byte aligned.  The workspace holds
+ * one piece of dz (about 512 MB at most, or 512 bytes per token where that is
+ * more; fp32 three times as much per entry), x and W once more in the matrix
+ * cores' terms, and fp32 sums of dx and of a piece of dW. */
 prn_status prn_vocab_loss_backward(const void* x, const void* W, const void* targets, const float* lse,
                                    const float* dloss, const float* dlse, const prn_vocab_loss_params* params,
                                    void* dx_out, void* dW_out);

@@ -1,4 +1,4 @@
-// Matrix-core tiles over bf16 operands of either orientation, for the
+// Matrix-core tiles over bf16 or fp16 operands of either orientation, for the
 // vocabulary loss: acc = sum over k of A(r, k) B(c, k).
 //
 // Each wave owns WM x WN blocks of 32 x 32; WR x WC waves make a workgroup's
@@ -21,7 +21,7 @@
 // A wait for a wave's own loads and a bare barrier make a stage complete (a
 // fence would drain the stages still in flight too).
 //
-// Fragment layout of v_mfma_f32_32x32x16_bf16: lane l feeds row l % 32 of A
+// Fragment layout of v_mfma_f32_32x32x16_bf16 and _f16: lane l feeds row l % 32 of A
 // and column l % 32 of B with the k values 8 (l / 32) .. + 7; accumulator r
 // of lane l holds row 8 (r / 4) + 4 (l / 32) + r % 4, column l % 32.
 #pragma once
@@ -32,6 +32,8 @@
 namespace prn {
 
 typedef __attribute__((ext_vector_type(8))) __bf16 mm_bf16x8;
+typedef __attribute__((ext_vector_type(2))) _Float16 mm_f16x2;
+typedef __attribute__((ext_vector_type(8))) _Float16 mm_f16x8;
 typedef __attribute__((ext_vector_type(16))) float mm_f32x16;
 typedef __attribute__((ext_vector_type(4))) short mm_s16x4;
 typedef __attribute__((ext_vector_type(8))) short mm_s16x8;
@@ -74,6 +76,15 @@ template <int n>
 __device__ __forceinline__ void mm_wait_loads() {
   static_assert(n >= 0 && n <= 63, "six bits of the load counter, in two places");
   __builtin_amdgcn_s_waitcnt((n & 15) | (7 << 4) | ((n >> 4) << 14));
+}
+
+// one product of two fragments of bf16 or fp16 values
+template <bool F16>
+__device__ __forceinline__ mm_f32x16 mm_product(mm_bf16x8 a, mm_bf16x8 b, mm_f32x16 c) {
+  if constexpr (F16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(mm_f16x8, a), __builtin_bit_cast(mm_f16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
 // An operand: `planes` 16-bit matrices `plane` elements apart (one for bf16
@@ -260,7 +271,7 @@ struct MmTile {
   }
 
   // acc = (or, with ADD, +=) the next tile's product (acc is left alone if the summed range is empty)
-  template <bool TA, bool TB, bool ADD = false, class Next>
+  template <bool TA, bool TB, bool ADD = false, bool F16 = false, class Next>
   __device__ __forceinline__ void multiply(Next&& next) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wr = wave / WC, wc = wave % WC;
     const int stages = nk * terms;
@@ -300,13 +311,13 @@ struct MmTile {
         for (int i = 0; i < WM; ++i)
 #pragma unroll
           for (int j = 0; j < WN; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(av[0][i], bv[0][j], zero, 0, 0, 0);
+            acc[i][j] = mm_product<F16>(av[0][i], bv[0][j], zero);
       } else {
 #pragma unroll
         for (int i = 0; i < WM; ++i)
 #pragma unroll
           for (int j = 0; j < WN; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(av[0][i], bv[0][j], acc[i][j], 0, 0, 0);
+            acc[i][j] = mm_product<F16>(av[0][i], bv[0][j], acc[i][j]);
       }
 #pragma unroll
       for (int kb = 1; kb < BK / 16; ++kb)
@@ -314,7 +325,7 @@ struct MmTile {
         for (int i = 0; i < WM; ++i)
 #pragma unroll
           for (int j = 0; j < WN; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(av[kb][i], bv[kb][j], acc[i][j], 0, 0, 0);
+            acc[i][j] = mm_product<F16>(av[kb][i], bv[kb][j], acc[i][j]);
       // order of the stage: the first 16 k's fragments, then every product
       // with a share of the next fragments behind it.  Left to itself the
       // compiler reads each fragment just before its use, to save registers.

@@ -17,10 +17,15 @@
 //
 // fp32 data runs as its exact three-term bf16 split (bf16split.h), six term
 // products each: the planes are laid out once per call.
-// dz is stored divided by the largest |dloss|, |dlse|, |dloss + dlse| of the
-// call, so that the usual coefficients (all equal, p - 1 near -1) round to
-// bf16 without loss; the factor comes back, in fp32, where dx and dW are
-// rounded.  Everything else is summed in fp32 in a fixed order.
+// dz is stored in units of the call's largest |dloss|, |dloss + dlse|.  With
+// bf16 data it is rounded to fp16, not bf16: an entry of a row near 1 in size
+// is then off by 2^-12 of itself at most, where bf16's 2^-9 would double the
+// error that the outputs' own rounding makes (the entry of the target can
+// carry the whole row).  W and x are laid out as fp16 for these products,
+// scaled by the power of two that takes their largest value to 2^14 .. 2^15;
+// bf16's eight bits fit fp16's eleven exactly down to 2^-28 of that largest
+// value.  The units come back, in fp32, where dx and dW are rounded.
+// Everything else is summed in fp32 in a fixed order.
 #include "vocab_loss.h"
 
 #include <algorithm>
@@ -277,55 +282,148 @@ struct RowCoef {
   int32_t target;       // -1: none
 };
 
-// the largest finite |dloss|, |dloss + dlse| of each workgroup's tokens
-constexpr int kMaxParts = 64;
-__global__ void __launch_bounds__(1024) k_loss_gmax(const float* __restrict__ dloss, const float* __restrict__ dlse,
-                                                    const void* __restrict__ targets, int target_bytes, int64_t ignore,
-                                                    int64_t N, float* __restrict__ g) {
-  __shared__ float w[16];
-  float m = 0.0f;
-  for (int64_t n = static_cast<int64_t>(blockIdx.x) * 1024 + threadIdx.x; n < N; n += static_cast<int64_t>(gridDim.x) * 1024) {
-    const float one = target_of(targets, target_bytes, n) == ignore ? 0.0f : dloss[n];
-    const float a = fabsf(one), b = dlse ? fabsf(one + dlse[n]) : 0.0f;
-    m = a < __builtin_inff() ? fmaxf(m, a) : m;
-    m = b < __builtin_inff() ? fmaxf(m, b) : m;
-  }
+constexpr int kMaxParts = 256;
+constexpr int kUnit = 13;   // dz is stored times 2^13: fp16 has entries down to 2^-37
+
+// The units of a backward call: dz / (s g) is stored times 2^kUnit (bf16
+// data; as it is with fp32), x and W times 2^ex and 2^ew.
+struct LossUnits {
+  float g, back_x, back_w;         // dx = acc back_x (s g), dW = acc back_w (s g)
+  float parts[3][kMaxParts];       // the workgroups' maxima: of dloss and dlse, x, W
+};
+
+__device__ __forceinline__ float block_max(float m, float* w) {
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
+  __syncthreads();
   if ((threadIdx.x & 63) == 0) w[threadIdx.x >> 6] = m;
   __syncthreads();
-  if (threadIdx.x == 0) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) m = fmaxf(m, w[i]);
-    g[1 + blockIdx.x] = m;
-  }
+  for (int i = 0; i < static_cast<int>(blockDim.x >> 6); ++i) m = fmaxf(m, w[i]);
+  return m;
+}
+__device__ __forceinline__ float finite_max(float m, float v) {
+  v = fabsf(v);
+  return v < __builtin_inff() ? fmaxf(m, v) : m;
 }
 
-// the tokens' coefficients; g[0] = the largest of the parts (1 if none is above 0)
+// The maxima: workgroups [0, n0) of |dloss|, |dloss + dlse|, the next n1 of x
+// and the last n2 of W (bf16 data only; values that are not finite do not
+// set a unit, they go through as they are).
+__global__ void __launch_bounds__(1024) k_loss_maxima(const float* __restrict__ dloss, const float* __restrict__ dlse,
+                                                      const void* __restrict__ targets, int target_bytes, int64_t ignore,
+                                                      int64_t N, int64_t V, int64_t d, const uint16_t* __restrict__ x,
+                                                      const uint16_t* __restrict__ W, int n0, int n1, int n2,
+                                                      LossUnits* __restrict__ u) {
+  __shared__ float w[16];
+  int b = static_cast<int>(blockIdx.x);
+  float m = 0.0f;
+  if (b < n0) {
+    for (int64_t n = static_cast<int64_t>(b) * 1024 + threadIdx.x; n < N; n += static_cast<int64_t>(n0) * 1024) {
+      const float one = target_of(targets, target_bytes, n) == ignore ? 0.0f : dloss[n];
+      m = finite_max(m, one);
+      if (dlse) m = finite_max(m, one + dlse[n]);
+    }
+    m = block_max(m, w);
+    if (threadIdx.x == 0) u->parts[0][b] = m;
+    return;
+  }
+  b -= n0;
+  const bool is_x = b < n1;
+  if (!is_x) b -= n1;
+  const uint16_t* p = is_x ? x : W;
+  const int64_t n = (is_x ? N : V) * d, step = static_cast<int64_t>(is_x ? n1 : n2) * 8192;
+  for (int64_t i = (static_cast<int64_t>(b) * 1024 + threadIdx.x) * 8; i < n; i += step) {
+    if (i + 8 <= n) {
+      const mm_s16x8 v = *reinterpret_cast<const mm_s16x8*>(p + i);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m = finite_max(m, __uint_as_float(static_cast<uint32_t>(static_cast<uint16_t>(v[e])) << 16));
+    } else {
+      for (int64_t q = i; q < n; ++q) m = finite_max(m, __uint_as_float(static_cast<uint32_t>(p[q]) << 16));
+    }
+  }
+  m = block_max(m, w);
+  if (threadIdx.x == 0) u->parts[is_x ? 1 : 2][b] = m;
+}
+
+// the power of two that takes a largest value m to 2^14 .. 2^15, and its inverse
+__device__ __forceinline__ float unit_of(float m, float* inverse) {
+  const int e = m > 0.0f ? static_cast<int>(__float_as_uint(m) >> 23) - 127 : 14;
+  const int k = min(max(14 - e, -126), 126);
+  *inverse = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+  return __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
+}
+
+// Workgroups [0, nc): the tokens' coefficients; then (bf16 data) n1 that lay
+// out x and n2 that lay out W in fp16, rows of ldp values, zeros past d.
 __global__ void __launch_bounds__(256) k_loss_coef(const float* __restrict__ dloss, const float* __restrict__ dlse,
                                                    const float* __restrict__ lse, const void* __restrict__ targets,
-                                                   int target_bytes, int64_t ignore, int64_t N, int64_t V,
-                                                   float* __restrict__ g, int parts, RowCoef* __restrict__ coef) {
-  float gm = 0.0f;
-  for (int i = 0; i < parts; ++i) gm = fmaxf(gm, g[1 + i]);
-  if (gm == 0.0f) gm = 1.0f;
-  const int64_t n = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (n == 0) g[0] = gm;
-  if (n >= N) return;
-  const int64_t t = target_of(targets, target_bytes, n);
-  const float one = t == ignore ? 0.0f : dloss[n];
-  const float p = (dlse ? one + dlse[n] : one) / gm;
-  RowCoef r;
-  r.sign = p < 0.0f ? -1.0f : 1.0f;
-  r.one = one / gm;
-  // no such entry: the loss was NaN, and so is its gradient
-  const bool lost = t != ignore && (t < 0 || t >= V);
-  r.lse2 = lost ? __builtin_nanf("") : fmaf(lse[n], kLog2e, -log2f(fabsf(p)));   // p = 0: +inf, a row of zeros
-  r.target = t == ignore || lost ? -1 : static_cast<int32_t>(t);
-  coef[n] = r;
+                                                   int target_bytes, int64_t ignore, int64_t N, int64_t V, int64_t d,
+                                                   int64_t ldp, const uint16_t* __restrict__ x,
+                                                   const uint16_t* __restrict__ W, int nc, int n1, int parts0, int parts1,
+                                                   int parts2, LossUnits* __restrict__ u, RowCoef* __restrict__ coef,
+                                                   uint16_t* __restrict__ xh, uint16_t* __restrict__ wh) {
+  __shared__ float w[4];
+  int b = static_cast<int>(blockIdx.x);
+  const int tid = threadIdx.x;
+  auto maximum = [&](int k, int parts) { return block_max(tid < parts ? u->parts[k][tid] : 0.0f, w); };
+  if (b < nc) {
+    float g = maximum(0, parts0);
+    if (g == 0.0f) g = 1.0f;
+    if (b == 0) {
+      float ix = 1.0f, iw = 1.0f, unit = 1.0f;
+      if (x) {
+        unit_of(maximum(1, parts1), &ix);
+        unit_of(maximum(2, parts2), &iw);
+        unit = 1.0f / (1 << kUnit);
+      }
+      if (tid == 0) {
+        u->g = g;
+        u->back_x = iw * unit;
+        u->back_w = ix * unit;
+      }
+    }
+    const int64_t n = static_cast<int64_t>(b) * 256 + tid;
+    if (n >= N) return;
+    const int64_t t = target_of(targets, target_bytes, n);
+    const float one = t == ignore ? 0.0f : dloss[n], unit = x ? static_cast<float>(kUnit) : 0.0f;
+    const float p = (dlse ? one + dlse[n] : one) / g;
+    RowCoef r;
+    r.sign = p < 0.0f ? -1.0f : 1.0f;
+    r.one = one / g * (x ? static_cast<float>(1 << kUnit) : 1.0f);
+    // no such entry: the loss was NaN, and so is its gradient
+    const bool lost = t != ignore && (t < 0 || t >= V);
+    r.lse2 = lost ? __builtin_nanf("") : fmaf(lse[n], kLog2e, -log2f(fabsf(p))) - unit;   // p = 0: +inf, a row of zeros
+    r.target = t == ignore || lost ? -1 : static_cast<int32_t>(t);
+    coef[n] = r;
+    return;
+  }
+  b -= nc;
+  const bool is_x = b < n1;
+  if (!is_x) b -= n1;
+  float inv;
+  const float unit = unit_of(is_x ? maximum(1, parts1) : maximum(2, parts2), &inv);
+  const uint16_t* in = is_x ? x : W;
+  uint16_t* out = is_x ? xh : wh;
+  const int64_t R = is_x ? N : V, C = ldp / 8;
+  const int64_t i = static_cast<int64_t>(b) * 256 + tid;
+  if (i >= R * C) return;
+  const int64_t r = C == 1 ? i : i / C, c0 = (i - r * C) * 8;
+  mm_f16x8 o;
+  if (d == ldp) {
+    const mm_s16x8 v = *reinterpret_cast<const mm_s16x8*>(in + r * d + c0);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      o[e] = static_cast<_Float16>(__uint_as_float(static_cast<uint32_t>(static_cast<uint16_t>(v[e])) << 16) * unit);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      o[e] = c0 + e < d ? static_cast<_Float16>(__uint_as_float(static_cast<uint32_t>(in[r * d + c0 + e]) << 16) * unit)
+                        : static_cast<_Float16>(0.0f);
+  }
+  *reinterpret_cast<mm_f16x8*>(out + r * ldp + c0) = o;
 }
 
-// dz of the vocabulary tiles of a piece (first entry piece0, rows to be
+// dz (in units of its call) of the vocabulary tiles of a piece (first entry piece0, rows to be
 // written up to piece1), stored by token rows (ldz apart; planes N ldz
 // apart).  A lane holds four neighbouring entries of its token at a time and
 // the other half of the wave the next four: a swap of the halves makes them
@@ -417,7 +515,7 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_dz(MmOperand W, MmOperand 
             for (int e = 0; e < 2; ++e) {
               float &x0 = v[4 * q + 2 * e], &x1 = v[4 * q + 2 * e + 1];
               if constexpr (BF16) {
-                w[q][e] = Storage<kBF16>::pack(x0) | static_cast<uint32_t>(Storage<kBF16>::pack(x1)) << 16;
+                w[q][e] = __builtin_bit_cast(uint32_t, mm_f16x2{static_cast<_Float16>(x0), static_cast<_Float16>(x1)});
               } else {   // the next terms of the exact split
                 const uint32_t b0 = __float_as_uint(x0) & 0xffff0000u, b1 = __float_as_uint(x1) & 0xffff0000u;
                 w[q][e] = b1 | b0 >> 16;
@@ -441,13 +539,13 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_dz(MmOperand W, MmOperand 
 }
 
 // P[z][r][c] (+)= sum over k of slice z of A(r, k) B(c, k), fp32, C columns; or,
-// with `out`, the last of the sums times s g, rounded once to out[r][c].
+// with `out`, the last of the sums times its units, rounded once to out[r][c].
 // One workgroup per tile and slice, neighbours on one XCD.
 template <class Tl, bool TA, bool BF16>
 __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_mm(MmOperand A, MmOperand B, int64_t R, int64_t C, int64_t K,
                                                          int64_t k_slice, int terms, int n_col, int slices, int add,
                                                          float* __restrict__ P, void* __restrict__ out,
-                                                         const float* __restrict__ g, float scale) {
+                                                         const LossUnits* __restrict__ units, float scale) {
   using T = typename Storage<BF16 ? kBF16 : kF32>::T;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Tl::LDS];
   const uint32_t u = Units(gridDim.x).u, tiles = gridDim.x / slices, z = u / tiles, ti = u - z * tiles;
@@ -482,8 +580,8 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_mm(MmOperand A, MmOperand 
   } else {
     tile.clear();
   }
-  tile.template multiply<TA, true, true>(next);
-  const float f = out ? g[0] * scale : 1.0f;
+  tile.template multiply<TA, true, true, BF16>(next);
+  const float back = out ? (TA ? units->back_w : units->back_x) : 1.0f, f = out ? units->g * scale : 1.0f;
   T* const obase = static_cast<T*>(out) + r0 * C + c0;
   const uint32_t oat = rl * static_cast<uint32_t>(C) + cl;
 #pragma unroll
@@ -495,7 +593,7 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_mm(MmOperand A, MmOperand 
       for (int j = 0; j < Tl::WN; ++j) {
         if (rl + ri < rows && cl + 32 * j < cols) {
           if (out)
-            obase[oat + ri * static_cast<uint32_t>(C) + 32 * j] = Storage<BF16 ? kBF16 : kF32>::pack(tile.acc[i][j][r] * f);
+            obase[oat + ri * static_cast<uint32_t>(C) + 32 * j] = Storage<BF16 ? kBF16 : kF32>::pack(tile.acc[i][j][r] * back * f);
           else
             *reinterpret_cast<float*>(base + (at + ri * ldb + 128 * j)) = tile.acc[i][j][r];
         }
@@ -503,16 +601,16 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_mm(MmOperand A, MmOperand 
     }
 }
 
-// out[i] = the sum over z, in order, of P[z][i], times s g, rounded once
+// out[i] = the sum over z, in order, of P[z][i], times its units, rounded once
 template <bool BF16>
 __global__ void __launch_bounds__(256) k_loss_out(const float* __restrict__ P, int S, int64_t n,
-                                                  const float* __restrict__ g, float scale,
+                                                  const LossUnits* __restrict__ units, int is_w, float scale,
                                                   typename Storage<BF16 ? kBF16 : kF32>::T* __restrict__ out) {
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (i >= n) return;
   float sum = 0.0f;
   for (int z = 0; z < S; ++z) sum += P[z * n + i];
-  out[i] = Storage<BF16 ? kBF16 : kF32>::pack(sum * (g[0] * scale));
+  out[i] = Storage<BF16 ? kBF16 : kF32>::pack(sum * (is_w ? units->back_w : units->back_x) * (units->g * scale));
 }
 
 template <class T>
@@ -589,7 +687,7 @@ struct PlanBw {
   bool big_z, big_o;        // tiles of the logits; of dx and dW
   int64_t piece, ldz;
   int64_t sx, kx, sw, kw;   // slices of dx's sum (over the piece) and dW's (over the tokens), and their lengths
-  size_t coef_off, g_off, dz_off, px_off, pw_off, total;
+  size_t coef_off, units_off, xh_off, wh_off, dz_off, px_off, pw_off, total;
 };
 PlanBw plan_bw(const LossArgs& a) {
   PlanBw b{};
@@ -614,8 +712,10 @@ PlanBw plan_bw(const LossArgs& a) {
   b.sx = slices(a.N, std::min(b.piece, a.V), &b.kx);
   b.sw = slices(std::min(b.piece, a.V), a.N, &b.kw);
   b.coef_off = b.op.end;
-  b.g_off = b.coef_off + up(size_t(a.N) * sizeof(RowCoef));
-  b.dz_off = b.g_off + up(4 * (1 + kMaxParts));
+  b.units_off = b.coef_off + up(size_t(a.N) * sizeof(RowCoef));
+  b.xh_off = b.units_off + up(sizeof(LossUnits));
+  b.wh_off = b.xh_off + (a.bf16 ? up(size_t(a.N) * b.op.ldp * 2) : 0);
+  b.dz_off = b.wh_off + (a.bf16 ? up(size_t(a.V) * b.op.ldp * 2) : 0);
   b.px_off = b.dz_off + up(size_t(a.N) * b.op.planes * b.ldz * 2);
   b.pw_off = b.px_off + up(size_t(b.sx) * a.N * a.d * 4);
   b.total = b.pw_off + (b.sw > 1 ? up(size_t(b.sw) * std::min(b.piece, a.V) * a.d * 4) : 0);
@@ -690,20 +790,37 @@ void launch_loss_backward(const LossArgs& a, const void* x, const void* W, const
   const int terms = a.bf16 ? 1 : kTerms;
   const float c = a.scale * kLog2e;
   RowCoef* coef = reinterpret_cast<RowCoef*>(a.ws + b.coef_off);
-  float* g = reinterpret_cast<float*>(a.ws + b.g_off);
+  LossUnits* units = reinterpret_cast<LossUnits*>(a.ws + b.units_off);
+  uint16_t* xh = reinterpret_cast<uint16_t*>(a.ws + b.xh_off);
+  uint16_t* wh = reinterpret_cast<uint16_t*>(a.ws + b.wh_off);
   uint16_t* dz = reinterpret_cast<uint16_t*>(a.ws + b.dz_off);
   float* px = reinterpret_cast<float*>(a.ws + b.px_off);
   float* pw = reinterpret_cast<float*>(a.ws + b.pw_off);
-  const int parts = int(std::min<int64_t>(kMaxParts, cdiv(a.N, 1024)));
-  k_loss_gmax<<<parts, 1024, 0, a.stream>>>(dloss, dlse, targets, a.target_bytes, a.ignore, a.N, g);
-  k_loss_coef<<<unsigned(cdiv(a.N, 256)), 256, 0, a.stream>>>(dloss, dlse, lse, targets, a.target_bytes, a.ignore, a.N,
-                                                              a.V, g, parts, coef);
-  auto out = [&](const float* P, int S, int64_t n, void* o, int64_t at) {
+  // the operands of dx and dW
+  MmOperand Xo = X, Wp = Wo;
+  {
+    auto parts = [](int64_t n) { return int(std::min<int64_t>(kMaxParts, cdiv(n, 1024))); };
+    const int p0 = parts(a.N), p1 = a.bf16 ? parts(cdiv(a.N * a.d, 8)) : 0, p2 = a.bf16 ? parts(cdiv(a.V * a.d, 8)) : 0;
+    const uint16_t* x16 = a.bf16 ? static_cast<const uint16_t*>(x) : nullptr;
+    const uint16_t* w16 = a.bf16 ? static_cast<const uint16_t*>(W) : nullptr;
+    k_loss_maxima<<<unsigned(p0 + p1 + p2), 1024, 0, a.stream>>>(dloss, dlse, targets, a.target_bytes, a.ignore, a.N, a.V,
+                                                                 a.d, x16, w16, p0, p1, p2, units);
+    const int64_t nc = cdiv(a.N, 256), C = b.op.ldp / 8;
+    const int64_t n1 = a.bf16 ? cdiv(a.N * C, 256) : 0, n2 = a.bf16 ? cdiv(a.V * C, 256) : 0;
+    k_loss_coef<<<unsigned(nc + n1 + n2), 256, 0, a.stream>>>(dloss, dlse, lse, targets, a.target_bytes, a.ignore, a.N, a.V,
+                                                              a.d, b.op.ldp, x16, w16, int(nc), int(n1), p0, p1, p2, units,
+                                                              coef, xh, wh);
+    if (a.bf16) {
+      Xo = {xh, b.op.ldp, 0};
+      Wp = {wh, b.op.ldp, 0};
+    }
+  }
+  auto out = [&](const float* P, int S, int64_t n, int is_w, void* o, int64_t at) {
     const unsigned grid = unsigned(cdiv(n, 256));
     if (a.bf16)
-      k_loss_out<true><<<grid, 256, 0, a.stream>>>(P, S, n, g, a.scale, static_cast<uint16_t*>(o) + at);
+      k_loss_out<true><<<grid, 256, 0, a.stream>>>(P, S, n, units, is_w, a.scale, static_cast<uint16_t*>(o) + at);
     else
-      k_loss_out<false><<<grid, 256, 0, a.stream>>>(P, S, n, g, a.scale, static_cast<float*>(o) + at);
+      k_loss_out<false><<<grid, 256, 0, a.stream>>>(P, S, n, units, is_w, a.scale, static_cast<float*>(o) + at);
   };
   // one tile shape and storage type of each kernel
   auto pick = [&](bool big, auto run) {
@@ -730,10 +847,10 @@ void launch_loss_backward(const LossArgs& a, const void* x, const void* W, const
     if (dx)
       pick(b.big_o, [&](auto tl, auto bf) {
         using Tl = decltype(tl);
-        const MmOperand Wc{Wo.base + v0 * Wo.ld, Wo.ld, Wo.plane};
+        const MmOperand Wc{Wp.base + v0 * Wp.ld, Wp.ld, Wp.plane};
         const int64_t n_col = cdiv(a.d, Tl::BN);
         k_loss_mm<Tl, false, decltype(bf)::value><<<unsigned(cdiv(a.N, Tl::BM) * n_col * b.sx), Tl::NTHR, 0, a.stream>>>(
-            Z, Wc, a.N, a.d, nv, b.kx, terms, int(n_col), int(b.sx), v0 > 0, px, last && b.sx == 1 ? dx : nullptr, g, a.scale);
+            Z, Wc, a.N, a.d, nv, b.kx, terms, int(n_col), int(b.sx), v0 > 0, px, last && b.sx == 1 ? dx : nullptr, units, a.scale);
       });
     if (dW) {
       void* const dWc = static_cast<uint8_t*>(dW) + v0 * a.d * elt;
@@ -741,12 +858,12 @@ void launch_loss_backward(const LossArgs& a, const void* x, const void* W, const
         using Tl = decltype(tl);
         const int64_t n_col = cdiv(a.d, Tl::BN);
         k_loss_mm<Tl, true, decltype(bf)::value><<<unsigned(cdiv(nv, Tl::BM) * n_col * b.sw), Tl::NTHR, 0, a.stream>>>(
-            Z, X, nv, a.d, a.N, b.kw, terms, int(n_col), int(b.sw), 0, pw, b.sw == 1 ? dWc : nullptr, g, a.scale);
+            Z, Xo, nv, a.d, a.N, b.kw, terms, int(n_col), int(b.sw), 0, pw, b.sw == 1 ? dWc : nullptr, units, a.scale);
       });
-      if (b.sw > 1) out(pw, int(b.sw), nv * a.d, dW, v0 * a.d);
+      if (b.sw > 1) out(pw, int(b.sw), nv * a.d, 1, dW, v0 * a.d);
     }
   }
-  if (dx && b.sx > 1) out(px, int(b.sx), a.N * a.d, dx, 0);
+  if (dx && b.sx > 1) out(px, int(b.sx), a.N * a.d, 0, dx, 0);
 }
 
 }  // namespace prn
