@@ -450,8 +450,8 @@ typedef struct {
  *   x (N, d), W (V, d) storage dtype, targets (N)
  *   loss_out (N), lse_out (N) fp32
  * Logits are fp32 sums of exact bf16 products (bf16), or of products good to
- * fp32 rounding (fp32 data: six products of its exact three-term bf16 split);
- * non-finite inputs give non-finite results in their rows.  A target that is
+ * 2^-20 (fp32 data: two fp16 terms of each value, three products; values below
+ * 2^-17 of their tensor's largest one are held to 2^-40 of that); non-finite inputs give non-finite results in their rows.  A target that is
  * neither ignore_index nor in 0 .. V - 1 gives a NaN loss (nothing is read out
  * of bounds).  x and W must be 16-byte aligned. */
 prn_status prn_vocab_loss(const void* x, const void* W, const void* targets, const prn_vocab_loss_params* params,

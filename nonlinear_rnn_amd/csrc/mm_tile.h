@@ -87,21 +87,20 @@ __device__ __forceinline__ mm_f32x16 mm_product(mm_bf16x8 a, mm_bf16x8 b, mm_f32
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
-// An operand: `planes` 16-bit matrices `plane` elements apart (one for bf16
-// data, the three terms of fp32 data split by split3), rows ld elements
-// apart, ld a multiple of 8, base 16-byte aligned.  R rows of the tile's
-// index, K values of the summed one.  Along its contiguous index the memory
-// holds a multiple of 8 values per row (the ones past the extent are zeros
-// where that index is k, anything otherwise).
+// An operand: 16-bit matrices `plane` elements apart (one, or the two terms of
+// fp32 data), rows ld elements apart, ld a multiple of 8, base 16-byte
+// aligned.  Along its contiguous index the memory holds a multiple of 8 values
+// per row (the ones past the extent are zeros where that index is k, anything
+// otherwise).
 struct MmOperand {
   const uint16_t* base;
   int64_t ld, plane;
 };
 
-// the term pairs of a product: one for bf16, the six of weight 2^-16 or more
-// (bf16split.h) for fp32
-__device__ __forceinline__ int mm_term_a(int t) { return (0x210100 >> (4 * t)) & 3; }   // 0 0 1 0 1 2
-__device__ __forceinline__ int mm_term_b(int t) { return (0x012010 >> (4 * t)) & 3; }   // 0 1 0 2 1 0
+// the term pairs of a product of two-term operands: the low terms' own
+// product is left out
+__device__ __forceinline__ int mm_term_a(int t) { return t >> 1; }   // 0 0 1
+__device__ __forceinline__ int mm_term_b(int t) { return t & 1; }    // 0 1 0
 
 template <int WR_, int WC_, int WM_, int WN_, int BK_, int NST_>
 struct MmTile {

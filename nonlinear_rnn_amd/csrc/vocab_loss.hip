@@ -15,30 +15,34 @@
 // dx += dz W and dW = dz^T x of the piece.  8 N V d operations in all, two of
 // them for the logits' second time.
 //
-// fp32 data runs as its exact three-term bf16 split (bf16split.h), six term
-// products each: the planes are laid out once per call.
-// dz is stored in units of the call's largest |dloss|, |dloss + dlse|.  With
-// bf16 data it is rounded to fp16, not bf16: an entry of a row near 1 in size
-// is then off by 2^-12 of itself at most, where bf16's 2^-9 would double the
-// error that the outputs' own rounding makes (the entry of the target can
-// carry the whole row).  W and x are laid out as fp16 for these products,
-// scaled by the power of two that takes their largest value to 2^14 .. 2^15;
-// bf16's eight bits fit fp16's eleven exactly down to 2^-28 of that largest
-// value.  The units come back, in fp32, where dx and dW are rounded.
-// Everything else is summed in fp32 in a fixed order.
+// The matrix cores take 16-bit operands.
+// bf16 data: the logits are exact products of bf16 values.  dz is rounded to
+// fp16, not bf16: an entry is then off by 2^-12 of itself at most, where
+// bf16's 2^-9 would double the error that the outputs' own rounding makes (the
+// entry of the target can carry the whole row).  W and x are laid out as fp16
+// for dx and dW, which holds bf16's eight bits exactly.
+// fp32 data: x, W and dz run as two fp16 terms, v = hi + lo to 2^-22 |v|, three
+// products each (lo lo, below 2^-22, is left out).  That is four fp32
+// roundings a product, below what the fp32 sums over them make; the exact
+// three-term bf16 split (bf16split.h) took twice the products and 1.74 ms
+// where this takes 1.0 (4096 x 256 x 32000).
+// For fp16's range a call's x and W are scaled by the power of two that takes
+// their largest value to 2^14 .. 2^15 (values below 2^-17 of that lose the low
+// bits of lo: at most 2^-40 of the largest value), and dz, in units of the
+// largest |dloss|, |dloss + dlse|, by 2^13.  The units come back, in fp32,
+// where they are used.  Everything is summed in fp32 in a fixed order.
 #include "vocab_loss.h"
 
 #include <algorithm>
 #include <type_traits>
 
-#include "bf16split.h"
 #include "mm_tile.h"
 #include "prn_device.h"
 
 namespace prn {
 namespace {
 
-constexpr int kTerms = 6;
+constexpr int kTerms = 3;   // products of two-term operands
 
 // 8 waves, 256 x 256, 128 KB: the least traffic per product; one workgroup a CU
 using Big = MmTile<2, 4, 4, 2, 64, 2>;
@@ -73,57 +77,221 @@ __device__ __forceinline__ void tile_of(uint32_t u, uint32_t rows, uint32_t cols
 
 // ------------------------------------------------------------ operands ---
 
-// The three bf16 terms of fp32 rows (planes R x ldp apart), or a copy of bf16
-// rows; columns d .. ldp - 1 are zeros.  One thread per 8 columns.
-template <bool BF16>
-__global__ void __launch_bounds__(256) k_loss_planes(const void* __restrict__ in, int64_t R, int64_t d, int64_t ldp,
-                                                     uint16_t* __restrict__ out) {
+// A copy of bf16 rows of d values as rows of ldp, zeros past d.  One thread
+// per 8 columns.
+__global__ void __launch_bounds__(256) k_loss_pad(const uint16_t* __restrict__ in, int64_t R, int64_t d, int64_t ldp,
+                                                  uint16_t* __restrict__ out) {
   const int64_t C = ldp / 8;
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (i >= R * C) return;
   const int64_t r = i / C;
   const int c0 = static_cast<int>(i - r * C) * 8;
-  if constexpr (BF16) {
-    const uint16_t* p = static_cast<const uint16_t*>(in) + r * d;
-    mm_s16x8 v;
+  mm_s16x8 v;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = c0 + e < d ? static_cast<short>(p[c0 + e]) : short(0);
-    *reinterpret_cast<mm_s16x8*>(out + r * ldp + c0) = v;
+  for (int e = 0; e < 8; ++e) v[e] = c0 + e < d ? static_cast<short>(in[r * d + c0 + e]) : short(0);
+  *reinterpret_cast<mm_s16x8*>(out + r * ldp + c0) = v;
+}
+
+constexpr int kMaxParts = 256;
+constexpr int kUnit = 13;   // dz is stored times 2^13: fp16 has entries down to 2^-37
+
+// The units of a call
+struct LossUnits {
+  float g;                         // dz is stored as 2^kUnit dz / (s g)
+  float back_z;                    // z = acc back_z s (1 with bf16 data)
+  float back_x, back_w;            // dx = acc back_x (s g), dW = acc back_w (s g)
+  float parts[3][kMaxParts];       // the workgroups' maxima: of dloss and dlse, x, W
+};
+
+template <class T>
+__device__ __forceinline__ int64_t target_at(const void* targets, int64_t n) {
+  return static_cast<int64_t>(static_cast<const T*>(targets)[n]);
+}
+__device__ __forceinline__ int64_t target_of(const void* targets, int bytes, int64_t n) {
+  return bytes == 4 ? target_at<int32_t>(targets, n) : target_at<int64_t>(targets, n);
+}
+
+__device__ __forceinline__ float block_max(float m, float* w) {
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) w[threadIdx.x >> 6] = m;
+  __syncthreads();
+  for (int i = 0; i < static_cast<int>(blockDim.x >> 6); ++i) m = fmaxf(m, w[i]);
+  return m;
+}
+__device__ __forceinline__ float finite_max(float m, float v) {
+  v = fabsf(v);
+  return v < __builtin_inff() ? fmaxf(m, v) : m;
+}
+
+// eight values of a dense array of n from place i on (16-byte aligned, i a
+// multiple of 8); zeros past the end
+template <bool BF16>
+__device__ __forceinline__ void load8(const void* p, int64_t i, int64_t n, float* o) {
+  using S = Storage<BF16 ? kBF16 : kF32>;
+  const typename S::T* q = static_cast<const typename S::T*>(p) + i;
+  if (i + 8 <= n) {
+    typename S::T t[8];
+    __builtin_memcpy(t, __builtin_assume_aligned(q, 16), sizeof(t));
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = S::load(&t[e]);
   } else {
-    const float* p = static_cast<const float*>(in) + r * d;
-    sp_f32x4 a, b;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      a[e] = c0 + e < d ? p[c0 + e] : 0.0f;
-      b[e] = c0 + 4 + e < d ? p[c0 + 4 + e] : 0.0f;
-    }
-    sp_bf16x8 t[3];
-    split3(a, b, t[0], t[1], t[2]);
-#pragma unroll
-    for (int u = 0; u < 3; ++u) *reinterpret_cast<sp_bf16x8*>(out + (u * R + r) * ldp + c0) = t[u];
+    for (int e = 0; e < 8; ++e) o[e] = i + e < n ? S::load(q + e) : 0.0f;
   }
+}
+
+// The maxima: workgroups [0, n0) of |dloss|, |dloss + dlse|, the next n1 of x
+// and the last n2 of W.  Values that are not finite do not set a unit, they go
+// through as they are.
+template <bool BF16>
+__global__ void __launch_bounds__(1024) k_loss_maxima(const float* __restrict__ dloss, const float* __restrict__ dlse,
+                                                      const void* __restrict__ targets, int target_bytes, int64_t ignore,
+                                                      int64_t N, int64_t V, int64_t d, const void* __restrict__ x,
+                                                      const void* __restrict__ W, int n0, int n1, int n2,
+                                                      LossUnits* __restrict__ u) {
+  __shared__ float w[16];
+  int b = static_cast<int>(blockIdx.x);
+  float m = 0.0f;
+  if (b < n0) {
+    for (int64_t n = static_cast<int64_t>(b) * 1024 + threadIdx.x; n < N; n += static_cast<int64_t>(n0) * 1024) {
+      const float one = target_of(targets, target_bytes, n) == ignore ? 0.0f : dloss[n];
+      m = finite_max(m, one);
+      if (dlse) m = finite_max(m, one + dlse[n]);
+    }
+    m = block_max(m, w);
+    if (threadIdx.x == 0) u->parts[0][b] = m;
+    return;
+  }
+  b -= n0;
+  const bool is_x = b < n1;
+  if (!is_x) b -= n1;
+  const int64_t n = (is_x ? N : V) * d, step = static_cast<int64_t>(is_x ? n1 : n2) * 8192;
+  for (int64_t i = (static_cast<int64_t>(b) * 1024 + threadIdx.x) * 8; i < n; i += step) {
+    float v[8];
+    load8<BF16>(is_x ? x : W, i, n, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = finite_max(m, v[e]);
+  }
+  m = block_max(m, w);
+  if (threadIdx.x == 0) u->parts[is_x ? 1 : 2][b] = m;
+}
+
+// the power of two that takes a largest value m to 2^14 .. 2^15, and its inverse
+__device__ __forceinline__ float unit_of(float m, float* inverse) {
+  const int e = m > 0.0f ? static_cast<int>(__float_as_uint(m) >> 23) - 127 : 14;
+  const int k = min(max(14 - e, -126), 126);
+  *inverse = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+  return __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
+}
+
+// A token's row of dz in its units: sign 2^(c z - lse2) - one at the target.
+// The magnitude of (dloss + dlse) / g is folded into the exponent.
+struct RowCoef {
+  float sign, one, lse2;
+  int32_t target;       // -1: none
+};
+
+// Workgroups [0, nc): the tokens' coefficients; then n1 that lay out x and the
+// rest W in fp16 terms (BF16: one, else two, R ldp apart), rows of ldp values,
+// zeros past d.  The first writes the units.
+template <bool BF16>
+__global__ void __launch_bounds__(256) k_loss_layout(const float* __restrict__ dloss, const float* __restrict__ dlse,
+                                                     const float* __restrict__ lse, const void* __restrict__ targets,
+                                                     int target_bytes, int64_t ignore, int64_t N, int64_t V, int64_t d,
+                                                     int64_t ldp, const void* __restrict__ x, const void* __restrict__ W,
+                                                     int nc, int n1, int parts0, int parts1, int parts2,
+                                                     LossUnits* __restrict__ u, RowCoef* __restrict__ coef,
+                                                     uint16_t* __restrict__ xh, uint16_t* __restrict__ wh) {
+  __shared__ float w[4];
+  int b = static_cast<int>(blockIdx.x);
+  const int tid = threadIdx.x;
+  auto maximum = [&](int k, int parts) { return block_max(tid < parts ? u->parts[k][tid] : 0.0f, w); };
+  float g = 1.0f;
+  if (b < nc) {
+    g = maximum(0, parts0);
+    if (g == 0.0f) g = 1.0f;
+  }
+  if (b == 0) {
+    float ix, iw;
+    unit_of(maximum(1, parts1), &ix);
+    unit_of(maximum(2, parts2), &iw);
+    if (tid == 0) {
+      u->g = g;
+      u->back_z = BF16 ? 1.0f : ix * iw;
+      u->back_x = iw / (1 << kUnit);
+      u->back_w = ix / (1 << kUnit);
+    }
+  }
+  if (b < nc) {
+    const int64_t n = static_cast<int64_t>(b) * 256 + tid;
+    if (n >= N) return;
+    const int64_t t = target_of(targets, target_bytes, n);
+    const float one = t == ignore ? 0.0f : dloss[n];
+    const float p = (dlse ? one + dlse[n] : one) / g;
+    RowCoef r;
+    r.sign = p < 0.0f ? -1.0f : 1.0f;
+    r.one = one / g * (1 << kUnit);
+    // no such entry: the loss was NaN, and so is its gradient
+    const bool lost = t != ignore && (t < 0 || t >= V);
+    r.lse2 = lost ? __builtin_nanf("") : fmaf(lse[n], kLog2e, -log2f(fabsf(p))) - kUnit;   // p = 0: +inf, a row of zeros
+    r.target = t == ignore || lost ? -1 : static_cast<int32_t>(t);
+    coef[n] = r;
+    return;
+  }
+  b -= nc;
+  const bool is_x = b < n1;
+  if (!is_x) b -= n1;
+  float inv;
+  const float unit = unit_of(is_x ? maximum(1, parts1) : maximum(2, parts2), &inv);
+  const int64_t R = is_x ? N : V, C = ldp / 8, i = static_cast<int64_t>(b) * 256 + tid;
+  if (i >= R * C) return;
+  const int64_t r = i / C, c0 = (i - r * C) * 8;
+  float v[8];
+  if (d == ldp) {
+    load8<BF16>(is_x ? x : W, r * d + c0, R * d, v);
+  } else {
+    using S = Storage<BF16 ? kBF16 : kF32>;
+    const typename S::T* q = static_cast<const typename S::T*>(is_x ? x : W) + r * d + c0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = c0 + e < d ? S::load(q + e) : 0.0f;
+  }
+  mm_f16x8 hi, lo;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float s = v[e] * unit;
+    hi[e] = static_cast<_Float16>(s);
+    lo[e] = static_cast<_Float16>(s - static_cast<float>(hi[e]));
+  }
+  uint16_t* const out = (is_x ? xh : wh) + r * ldp + c0;
+  *reinterpret_cast<mm_f16x8*>(out) = hi;
+  if constexpr (!BF16) *reinterpret_cast<mm_f16x8*>(out + R * ldp) = lo;
 }
 
 // ------------------------------------------------------------- forward ---
 
 // part[n][split] = (maximum, sum of 2^(c (z - maximum))) of token n over the
-// split's vocabulary tiles, z the plain products x W^T, c = s log2(e) > 0.
+// split's vocabulary tiles, z the plain products x W^T (F16: of the operands
+// in their units), c = s log2(e) > 0 (in those units).
 // A unit is a token tile and a split; four token tiles and their splits are
 // neighbours, so that an XCD's workgroups share the W tiles they walk.
-template <class Tl>
+template <class Tl, bool F16>
 __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_lse(MmOperand W, MmOperand X, int64_t N, int64_t V, int64_t d,
-                                                          int terms, float c, int n_tok, int splits, int per_split,
+                                                          int terms, float c, const LossUnits* __restrict__ units,
+                                                          int n_tok, int splits, int per_split,
                                                           float2* __restrict__ part) {
+  if constexpr (F16) c *= units->back_z;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Tl::LDS];
   __shared__ float2 hand[Tl::WR][Tl::BN];
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, l32 = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wr = wave / Tl::WC, wc = wave % Tl::WC;
-  const uint32_t v_tiles = static_cast<uint32_t>((V + Tl::BM - 1) / Tl::BM), units = static_cast<uint32_t>(n_tok) * splits;
+  const uint32_t v_tiles = static_cast<uint32_t>((V + Tl::BM - 1) / Tl::BM);
   Tl tile;
   tile.open(lds, W, V, X, N, 0, d, terms);
   // the loads' place: unit, vocabulary tile
-  Units lu(units), cu(units);
+  Units lu(static_cast<uint32_t>(n_tok) * splits), cu(lu);
   uint32_t lt = 0, lt1 = 0, ltok = 0;
   auto enter = [&]() {
     if (!lu.valid()) return false;
@@ -155,7 +323,7 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_lse(MmOperand W, MmOperand
     for (int j = 0; j < Tl::WN; ++j) m[j] = s[j] = 0.0f;
     for (uint32_t t = t0; t < t1; ++t) {
       const int64_t v0 = static_cast<int64_t>(t) * Tl::BM;
-      tile.template multiply<false, false>(next);
+      tile.template multiply<false, false, false, F16>(next);
       if (v0 + Tl::BM > V) {
         const int left = static_cast<int>(V - v0) - wr * Tl::WM * 32 - 4 * half;
 #pragma unroll
@@ -220,14 +388,6 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_lse(MmOperand W, MmOperand
   }
 }
 
-template <class T>
-__device__ __forceinline__ int64_t target_at(const void* targets, int64_t n) {
-  return static_cast<int64_t>(static_cast<const T*>(targets)[n]);
-}
-__device__ __forceinline__ int64_t target_of(const void* targets, int bytes, int64_t n) {
-  return bytes == 4 ? target_at<int32_t>(targets, n) : target_at<int64_t>(targets, n);
-}
-
 __device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o, 64);
@@ -240,12 +400,13 @@ template <bool BF16>
 __global__ void __launch_bounds__(256) k_loss_join(const float2* __restrict__ part, int splits, const void* __restrict__ x,
                                                    const void* __restrict__ W, const void* __restrict__ targets,
                                                    int target_bytes, int64_t N, int64_t V, int64_t d, float scale,
-                                                   int64_t ignore, float* __restrict__ loss, float* __restrict__ lse) {
+                                                   const LossUnits* __restrict__ units, int64_t ignore,
+                                                   float* __restrict__ loss, float* __restrict__ lse) {
   using S = Storage<BF16 ? kBF16 : kF32>;
   const int64_t n = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
   if (n >= N) return;
-  const float c = scale * kLog2e;
+  const float back = BF16 ? 1.0f : units->back_z, c = scale * kLog2e * back;
   float m = -__builtin_inff();
   for (int i = lane; i < splits; i += 64) m = fmaxf(m, part[n * splits + i].x);
 #pragma unroll
@@ -268,160 +429,12 @@ __global__ void __launch_bounds__(256) k_loss_join(const float2* __restrict__ pa
   }
   if (lane == 0) {
     const float ln = logf(s);
-    lse[n] = fmaf(ref, scale, ln);
-    loss[n] = t == ignore ? 0.0f : in ? fmaf(ref - dot, scale, ln) : __builtin_nanf("");
+    lse[n] = fmaf(ref * back, scale, ln);
+    loss[n] = t == ignore ? 0.0f : in ? fmaf(fmaf(ref, back, -dot), scale, ln) : __builtin_nanf("");
   }
 }
 
 // ------------------------------------------------------------ backward ---
-
-// A token's row of dz / (s g): sign 2^(c z - lse2) - one at the target.  The
-// magnitude of (dloss + dlse) / g is folded into the exponent.
-struct RowCoef {
-  float sign, one, lse2;
-  int32_t target;       // -1: none
-};
-
-constexpr int kMaxParts = 256;
-constexpr int kUnit = 13;   // dz is stored times 2^13: fp16 has entries down to 2^-37
-
-// The units of a backward call: dz / (s g) is stored times 2^kUnit (bf16
-// data; as it is with fp32), x and W times 2^ex and 2^ew.
-struct LossUnits {
-  float g, back_x, back_w;         // dx = acc back_x (s g), dW = acc back_w (s g)
-  float parts[3][kMaxParts];       // the workgroups' maxima: of dloss and dlse, x, W
-};
-
-__device__ __forceinline__ float block_max(float m, float* w) {
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) w[threadIdx.x >> 6] = m;
-  __syncthreads();
-  for (int i = 0; i < static_cast<int>(blockDim.x >> 6); ++i) m = fmaxf(m, w[i]);
-  return m;
-}
-__device__ __forceinline__ float finite_max(float m, float v) {
-  v = fabsf(v);
-  return v < __builtin_inff() ? fmaxf(m, v) : m;
-}
-
-// The maxima: workgroups [0, n0) of |dloss|, |dloss + dlse|, the next n1 of x
-// and the last n2 of W (bf16 data only; values that are not finite do not
-// set a unit, they go through as they are).
-__global__ void __launch_bounds__(1024) k_loss_maxima(const float* __restrict__ dloss, const float* __restrict__ dlse,
-                                                      const void* __restrict__ targets, int target_bytes, int64_t ignore,
-                                                      int64_t N, int64_t V, int64_t d, const uint16_t* __restrict__ x,
-                                                      const uint16_t* __restrict__ W, int n0, int n1, int n2,
-                                                      LossUnits* __restrict__ u) {
-  __shared__ float w[16];
-  int b = static_cast<int>(blockIdx.x);
-  float m = 0.0f;
-  if (b < n0) {
-    for (int64_t n = static_cast<int64_t>(b) * 1024 + threadIdx.x; n < N; n += static_cast<int64_t>(n0) * 1024) {
-      const float one = target_of(targets, target_bytes, n) == ignore ? 0.0f : dloss[n];
-      m = finite_max(m, one);
-      if (dlse) m = finite_max(m, one + dlse[n]);
-    }
-    m = block_max(m, w);
-    if (threadIdx.x == 0) u->parts[0][b] = m;
-    return;
-  }
-  b -= n0;
-  const bool is_x = b < n1;
-  if (!is_x) b -= n1;
-  const uint16_t* p = is_x ? x : W;
-  const int64_t n = (is_x ? N : V) * d, step = static_cast<int64_t>(is_x ? n1 : n2) * 8192;
-  for (int64_t i = (static_cast<int64_t>(b) * 1024 + threadIdx.x) * 8; i < n; i += step) {
-    if (i + 8 <= n) {
-      const mm_s16x8 v = *reinterpret_cast<const mm_s16x8*>(p + i);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) m = finite_max(m, __uint_as_float(static_cast<uint32_t>(static_cast<uint16_t>(v[e])) << 16));
-    } else {
-      for (int64_t q = i; q < n; ++q) m = finite_max(m, __uint_as_float(static_cast<uint32_t>(p[q]) << 16));
-    }
-  }
-  m = block_max(m, w);
-  if (threadIdx.x == 0) u->parts[is_x ? 1 : 2][b] = m;
-}
-
-// the power of two that takes a largest value m to 2^14 .. 2^15, and its inverse
-__device__ __forceinline__ float unit_of(float m, float* inverse) {
-  const int e = m > 0.0f ? static_cast<int>(__float_as_uint(m) >> 23) - 127 : 14;
-  const int k = min(max(14 - e, -126), 126);
-  *inverse = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
-  return __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
-}
-
-// Workgroups [0, nc): the tokens' coefficients; then (bf16 data) n1 that lay
-// out x and n2 that lay out W in fp16, rows of ldp values, zeros past d.
-__global__ void __launch_bounds__(256) k_loss_coef(const float* __restrict__ dloss, const float* __restrict__ dlse,
-                                                   const float* __restrict__ lse, const void* __restrict__ targets,
-                                                   int target_bytes, int64_t ignore, int64_t N, int64_t V, int64_t d,
-                                                   int64_t ldp, const uint16_t* __restrict__ x,
-                                                   const uint16_t* __restrict__ W, int nc, int n1, int parts0, int parts1,
-                                                   int parts2, LossUnits* __restrict__ u, RowCoef* __restrict__ coef,
-                                                   uint16_t* __restrict__ xh, uint16_t* __restrict__ wh) {
-  __shared__ float w[4];
-  int b = static_cast<int>(blockIdx.x);
-  const int tid = threadIdx.x;
-  auto maximum = [&](int k, int parts) { return block_max(tid < parts ? u->parts[k][tid] : 0.0f, w); };
-  if (b < nc) {
-    float g = maximum(0, parts0);
-    if (g == 0.0f) g = 1.0f;
-    if (b == 0) {
-      float ix = 1.0f, iw = 1.0f, unit = 1.0f;
-      if (x) {
-        unit_of(maximum(1, parts1), &ix);
-        unit_of(maximum(2, parts2), &iw);
-        unit = 1.0f / (1 << kUnit);
-      }
-      if (tid == 0) {
-        u->g = g;
-        u->back_x = iw * unit;
-        u->back_w = ix * unit;
-      }
-    }
-    const int64_t n = static_cast<int64_t>(b) * 256 + tid;
-    if (n >= N) return;
-    const int64_t t = target_of(targets, target_bytes, n);
-    const float one = t == ignore ? 0.0f : dloss[n], unit = x ? static_cast<float>(kUnit) : 0.0f;
-    const float p = (dlse ? one + dlse[n] : one) / g;
-    RowCoef r;
-    r.sign = p < 0.0f ? -1.0f : 1.0f;
-    r.one = one / g * (x ? static_cast<float>(1 << kUnit) : 1.0f);
-    // no such entry: the loss was NaN, and so is its gradient
-    const bool lost = t != ignore && (t < 0 || t >= V);
-    r.lse2 = lost ? __builtin_nanf("") : fmaf(lse[n], kLog2e, -log2f(fabsf(p))) - unit;   // p = 0: +inf, a row of zeros
-    r.target = t == ignore || lost ? -1 : static_cast<int32_t>(t);
-    coef[n] = r;
-    return;
-  }
-  b -= nc;
-  const bool is_x = b < n1;
-  if (!is_x) b -= n1;
-  float inv;
-  const float unit = unit_of(is_x ? maximum(1, parts1) : maximum(2, parts2), &inv);
-  const uint16_t* in = is_x ? x : W;
-  uint16_t* out = is_x ? xh : wh;
-  const int64_t R = is_x ? N : V, C = ldp / 8;
-  const int64_t i = static_cast<int64_t>(b) * 256 + tid;
-  if (i >= R * C) return;
-  const int64_t r = C == 1 ? i : i / C, c0 = (i - r * C) * 8;
-  mm_f16x8 o;
-  if (d == ldp) {
-    const mm_s16x8 v = *reinterpret_cast<const mm_s16x8*>(in + r * d + c0);
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      o[e] = static_cast<_Float16>(__uint_as_float(static_cast<uint32_t>(static_cast<uint16_t>(v[e])) << 16) * unit);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      o[e] = c0 + e < d ? static_cast<_Float16>(__uint_as_float(static_cast<uint32_t>(in[r * d + c0 + e]) << 16) * unit)
-                        : static_cast<_Float16>(0.0f);
-  }
-  *reinterpret_cast<mm_f16x8*>(out + r * ldp + c0) = o;
-}
 
 // dz (in units of its call) of the vocabulary tiles of a piece (first entry piece0, rows to be
 // written up to piece1), stored by token rows (ldz apart; planes N ldz
@@ -430,9 +443,11 @@ __global__ void __launch_bounds__(256) k_loss_coef(const float* __restrict__ dlo
 // eight, 16 bytes a store.
 template <class Tl, bool BF16>
 __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_dz(MmOperand W, MmOperand X, int64_t N, int64_t V, int64_t d,
-                                                         int terms, float c, int64_t piece0, int64_t piece1, int n_tok,
+                                                         int terms, float c, const LossUnits* __restrict__ units,
+                                                         int64_t piece0, int64_t piece1, int n_tok,
                                                          const RowCoef* __restrict__ coef, uint16_t* __restrict__ dz,
                                                          int64_t ldz) {
+  if constexpr (!BF16) c *= units->back_z;
   // the loads are up to NST tiles ahead (tiles of one stage)
   constexpr int kRing = Tl::NST + 1;
   static_assert(sizeof(RowCoef) == 16 && Tl::BN % 64 == 0 && Tl::BN / 64 <= Tl::NW, "one coefficient load per wave");
@@ -445,7 +460,7 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_dz(MmOperand W, MmOperand 
   constexpr uint32_t kGroup = 8;   // vocabulary tiles that an XCD's workgroups share
   Tl tile;
   tile.open(lds, W, V, X, N, 0, d, terms);
-  Units lu(v_tiles * n_tok), cu(v_tiles * n_tok);
+  Units lu(v_tiles * n_tok), cu(lu);
   int fill = 0;   // the tokens' coefficients come with the tile's first stage
   auto go_to = [&]() {
     uint32_t vt, tok;
@@ -467,7 +482,7 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_dz(MmOperand W, MmOperand 
     uint32_t vt, tok;
     tile_of(cu.u, v_tiles, n_tok, kGroup, vt, tok);
     const int64_t v0 = piece0 + static_cast<int64_t>(vt) * Tl::BM, n0 = static_cast<int64_t>(tok) * Tl::BN;
-    tile.template multiply<false, false>(next);
+    tile.template multiply<false, false, false, !BF16>(next);
     uint8_t* const base = reinterpret_cast<uint8_t*>(dz + n0 * ldz + (v0 - piece0));
     const int rows = static_cast<int>(imin(piece1 - v0, Tl::BM)), toks = static_cast<int>(imin(N - n0, Tl::BN));
     const int vocab_left = static_cast<int>(imin(V - v0, Tl::BM));
@@ -507,20 +522,18 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_dz(MmOperand W, MmOperand 
             if (vb + 4 * eh + 8 * (r >> 2) + (r & 3) >= vocab_left) v[r] = 0.0f;
         }
 #pragma unroll
-        for (int t = 0; t < (BF16 ? 1 : 3); ++t) {
+        for (int t = 0; t < (BF16 ? 1 : 2); ++t) {
           uint32_t w[4][2];
 #pragma unroll
           for (int q = 0; q < 4; ++q)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               float &x0 = v[4 * q + 2 * e], &x1 = v[4 * q + 2 * e + 1];
-              if constexpr (BF16) {
-                w[q][e] = __builtin_bit_cast(uint32_t, mm_f16x2{static_cast<_Float16>(x0), static_cast<_Float16>(x1)});
-              } else {   // the next terms of the exact split
-                const uint32_t b0 = __float_as_uint(x0) & 0xffff0000u, b1 = __float_as_uint(x1) & 0xffff0000u;
-                w[q][e] = b1 | b0 >> 16;
-                x0 -= __uint_as_float(b0);
-                x1 -= __uint_as_float(b1);
+              const mm_f16x2 p{static_cast<_Float16>(x0), static_cast<_Float16>(x1)};
+              w[q][e] = __builtin_bit_cast(uint32_t, p);
+              if (!BF16 && t == 0) {   // what is left for the second term
+                x0 -= static_cast<float>(p[0]);
+                x1 -= static_cast<float>(p[1]);
               }
             }
 #pragma unroll
@@ -580,7 +593,7 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_mm(MmOperand A, MmOperand 
   } else {
     tile.clear();
   }
-  tile.template multiply<TA, true, true, BF16>(next);
+  tile.template multiply<TA, true, true, true>(next);
   const float back = out ? (TA ? units->back_w : units->back_x) : 1.0f, f = out ? units->g * scale : 1.0f;
   T* const obase = static_cast<T*>(out) + r0 * C + c0;
   const uint32_t oat = rl * static_cast<uint32_t>(C) + cl;
@@ -627,20 +640,32 @@ constexpr size_t kPieceBytes = size_t(512) << 20;   // of dz
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// Operands laid out anew: bf16 rows of no multiple of 8 (for the logits), and
+// the fp16 terms (fp32 data: for every product; bf16: for dx and dW).
 struct Plan {
-  bool copy;             // x and W are laid out anew (fp32 terms; bf16 rows of no multiple of 8)
-  int planes;
+  bool pad;
+  int planes;            // terms of x, W and dz
   int64_t ldp;
-  size_t x_off, w_off, end;
+  size_t units_off, xp_off, wp_off, xh_off, wh_off, end;
 };
-Plan plan_operands(const LossArgs& a) {
+Plan plan_operands(const LossArgs& a, bool back) {
   Plan p{};
-  p.planes = a.bf16 ? 1 : 3;
+  p.planes = a.bf16 ? 1 : 2;
   p.ldp = cdiv(a.d, 8) * 8;
-  p.copy = !a.bf16 || a.d % 8 != 0;
-  p.x_off = 0;
-  p.w_off = p.copy ? up(size_t(p.planes) * a.N * p.ldp * 2) : 0;
-  p.end = p.copy ? p.w_off + up(size_t(p.planes) * a.V * p.ldp * 2) : 0;
+  p.pad = a.bf16 && a.d % 8 != 0;
+  const bool terms = back || !a.bf16;
+  size_t off = 0;
+  auto take = [&](bool on, size_t bytes) {
+    const size_t at = off;
+    if (on) off += up(bytes);
+    return at;
+  };
+  p.units_off = take(terms, sizeof(LossUnits));
+  p.xp_off = take(p.pad, size_t(a.N) * p.ldp * 2);
+  p.wp_off = take(p.pad, size_t(a.V) * p.ldp * 2);
+  p.xh_off = take(terms, size_t(p.planes) * a.N * p.ldp * 2);
+  p.wh_off = take(terms, size_t(p.planes) * a.V * p.ldp * 2);
+  p.end = off;
   return p;
 }
 
@@ -657,7 +682,7 @@ struct PlanFw {
 };
 PlanFw plan_fw(const LossArgs& a) {
   PlanFw f{};
-  f.op = plan_operands(a);
+  f.op = plan_operands(a, false);
   f.kind = a.N <= Few::BN ? 0 : take_big(a.N) ? 2 : 1;
   const int64_t bm = f.kind == 0 ? Few::BM : Big::BM, bn = f.kind == 0 ? Few::BN : f.kind == 1 ? Mid::BN : Big::BN;
   f.n_tok = cdiv(a.N, bn);
@@ -687,11 +712,11 @@ struct PlanBw {
   bool big_z, big_o;        // tiles of the logits; of dx and dW
   int64_t piece, ldz;
   int64_t sx, kx, sw, kw;   // slices of dx's sum (over the piece) and dW's (over the tokens), and their lengths
-  size_t coef_off, units_off, xh_off, wh_off, dz_off, px_off, pw_off, total;
+  size_t coef_off, dz_off, px_off, pw_off, total;
 };
 PlanBw plan_bw(const LossArgs& a) {
   PlanBw b{};
-  b.op = plan_operands(a);
+  b.op = plan_operands(a, true);
   b.big_z = take_big(a.N);
   b.big_o = take_big(a.d);
   const int64_t v_tiles = cdiv(a.V, Big::BM);
@@ -712,33 +737,56 @@ PlanBw plan_bw(const LossArgs& a) {
   b.sx = slices(a.N, std::min(b.piece, a.V), &b.kx);
   b.sw = slices(std::min(b.piece, a.V), a.N, &b.kw);
   b.coef_off = b.op.end;
-  b.units_off = b.coef_off + up(size_t(a.N) * sizeof(RowCoef));
-  b.xh_off = b.units_off + up(sizeof(LossUnits));
-  b.wh_off = b.xh_off + (a.bf16 ? up(size_t(a.N) * b.op.ldp * 2) : 0);
-  b.dz_off = b.wh_off + (a.bf16 ? up(size_t(a.V) * b.op.ldp * 2) : 0);
+  b.dz_off = b.coef_off + up(size_t(a.N) * sizeof(RowCoef));
   b.px_off = b.dz_off + up(size_t(a.N) * b.op.planes * b.ldz * 2);
   b.pw_off = b.px_off + up(size_t(b.sx) * a.N * a.d * 4);
   b.total = b.pw_off + (b.sw > 1 ? up(size_t(b.sw) * std::min(b.piece, a.V) * a.d * 4) : 0);
   return b;
 }
 
-void operands(const LossArgs& a, const Plan& p, const void* x, const void* W, MmOperand* X, MmOperand* Wo) {
-  if (!p.copy) {
-    *X = {static_cast<const uint16_t*>(x), a.d, 0};
-    *Wo = {static_cast<const uint16_t*>(W), a.d, 0};
-    return;
+// The operands: X and Wo of the logits, Xh and Wh (fp16 terms) of dx and dW;
+// with `coef`, the tokens' coefficients.  For the forward dloss .. coef are null.
+struct Operands {
+  MmOperand X, Wo, Xh, Wh;
+  LossUnits* units;
+};
+Operands lay_out(const LossArgs& a, const Plan& p, const void* x, const void* W, const void* targets, const float* lse,
+                 const float* dloss, const float* dlse, RowCoef* coef) {
+  Operands o{};
+  auto at = [&](size_t off) { return reinterpret_cast<uint16_t*>(a.ws + off); };
+  if (coef || !a.bf16) {
+    auto parts = [](int64_t n) { return int(std::min<int64_t>(kMaxParts, cdiv(n, 1024))); };
+    o.units = reinterpret_cast<LossUnits*>(a.ws + p.units_off);
+    o.Xh = {at(p.xh_off), p.ldp, a.N * p.ldp};
+    o.Wh = {at(p.wh_off), p.ldp, a.V * p.ldp};
+    const int p0 = coef ? parts(a.N) : 0, p1 = parts(cdiv(a.N * a.d, 8)), p2 = parts(cdiv(a.V * a.d, 8));
+    const int64_t nc = coef ? cdiv(a.N, 256) : 0, n1 = cdiv(a.N * (p.ldp / 8), 256), n2 = cdiv(a.V * (p.ldp / 8), 256);
+    auto go = [&](auto bf) {
+      constexpr bool BF = decltype(bf)::value;
+      k_loss_maxima<BF><<<unsigned(p0 + p1 + p2), 1024, 0, a.stream>>>(dloss, dlse, targets, a.target_bytes, a.ignore, a.N,
+                                                                       a.V, a.d, x, W, p0, p1, p2, o.units);
+      k_loss_layout<BF><<<unsigned(nc + n1 + n2), 256, 0, a.stream>>>(
+          dloss, dlse, lse, targets, a.target_bytes, a.ignore, a.N, a.V, a.d, p.ldp, x, W, int(nc), int(n1), p0, p1, p2,
+          o.units, coef, at(p.xh_off), at(p.wh_off));
+    };
+    if (a.bf16) go(std::true_type{}); else go(std::false_type{});
   }
-  auto lay = [&](const void* in, int64_t R, size_t off) {
-    uint16_t* out = reinterpret_cast<uint16_t*>(a.ws + off);
-    const unsigned grid = static_cast<unsigned>(cdiv(R * (p.ldp / 8), 256));
-    if (a.bf16)
-      k_loss_planes<true><<<grid, 256, 0, a.stream>>>(in, R, a.d, p.ldp, out);
-    else
-      k_loss_planes<false><<<grid, 256, 0, a.stream>>>(in, R, a.d, p.ldp, out);
-    return MmOperand{out, p.ldp, R * p.ldp};
-  };
-  *X = lay(x, a.N, p.x_off);
-  *Wo = lay(W, a.V, p.w_off);
+  if (!a.bf16) {
+    o.X = o.Xh;
+    o.Wo = o.Wh;
+  } else if (p.pad) {
+    auto pad = [&](const void* in, int64_t R, size_t off) {
+      k_loss_pad<<<unsigned(cdiv(R * (p.ldp / 8), 256)), 256, 0, a.stream>>>(static_cast<const uint16_t*>(in), R, a.d, p.ldp,
+                                                                             at(off));
+      return MmOperand{at(off), p.ldp, 0};
+    };
+    o.X = pad(x, a.N, p.xp_off);
+    o.Wo = pad(W, a.V, p.wp_off);
+  } else {
+    o.X = {static_cast<const uint16_t*>(x), a.d, 0};
+    o.Wo = {static_cast<const uint16_t*>(W), a.d, 0};
+  }
+  return o;
 }
 
 }  // namespace
@@ -754,24 +802,26 @@ size_t loss_backward_workspace(const LossArgs& a) { return a.N ? plan_bw(a).tota
 
 void launch_loss(const LossArgs& a, const void* x, const void* W, const void* targets, float* loss, float* lse) {
   const PlanFw f = plan_fw(a);
-  MmOperand X, Wo;
-  operands(a, f.op, x, W, &X, &Wo);
+  const Operands o = lay_out(a, f.op, x, W, targets, nullptr, nullptr, nullptr, nullptr);
   const int terms = a.bf16 ? 1 : kTerms;
   const float c = a.scale * kLog2e;
   float2* part = reinterpret_cast<float2*>(a.ws + f.part_off);
-  auto go = [&](auto tl) {
+  auto go = [&](auto tl, auto f16) {
     using Tl = decltype(tl);
-    k_loss_lse<Tl><<<unsigned(f.grid), Tl::NTHR, 0, a.stream>>>(Wo, X, a.N, a.V, f.op.ldp, terms, c, int(f.n_tok),
-                                                                int(f.splits), int(f.per_split), part);
+    k_loss_lse<Tl, decltype(f16)::value><<<unsigned(f.grid), Tl::NTHR, 0, a.stream>>>(
+        o.Wo, o.X, a.N, a.V, f.op.ldp, terms, c, o.units, int(f.n_tok), int(f.splits), int(f.per_split), part);
   };
-  if (f.kind == 0) go(Few{}); else if (f.kind == 1) go(Mid{}); else go(Big{});
+  auto go_type = [&](auto tl) {
+    if (a.bf16) go(tl, std::false_type{}); else go(tl, std::true_type{});
+  };
+  if (f.kind == 0) go_type(Few{}); else if (f.kind == 1) go_type(Mid{}); else go_type(Big{});
   const unsigned jg = static_cast<unsigned>(cdiv(a.N, 4));
   if (a.bf16)
     k_loss_join<true><<<jg, 256, 0, a.stream>>>(part, int(f.splits), x, W, targets, a.target_bytes, a.N, a.V, a.d,
-                                                a.scale, a.ignore, loss, lse);
+                                                a.scale, o.units, a.ignore, loss, lse);
   else
     k_loss_join<false><<<jg, 256, 0, a.stream>>>(part, int(f.splits), x, W, targets, a.target_bytes, a.N, a.V, a.d,
-                                                 a.scale, a.ignore, loss, lse);
+                                                 a.scale, o.units, a.ignore, loss, lse);
 }
 
 void launch_loss_backward(const LossArgs& a, const void* x, const void* W, const void* targets, const float* lse,
@@ -785,42 +835,20 @@ void launch_loss_backward(const LossArgs& a, const void* x, const void* W, const
     return;
   }
   const PlanBw b = plan_bw(a);
-  MmOperand X, Wo;
-  operands(a, b.op, x, W, &X, &Wo);
   const int terms = a.bf16 ? 1 : kTerms;
   const float c = a.scale * kLog2e;
   RowCoef* coef = reinterpret_cast<RowCoef*>(a.ws + b.coef_off);
-  LossUnits* units = reinterpret_cast<LossUnits*>(a.ws + b.units_off);
-  uint16_t* xh = reinterpret_cast<uint16_t*>(a.ws + b.xh_off);
-  uint16_t* wh = reinterpret_cast<uint16_t*>(a.ws + b.wh_off);
   uint16_t* dz = reinterpret_cast<uint16_t*>(a.ws + b.dz_off);
   float* px = reinterpret_cast<float*>(a.ws + b.px_off);
   float* pw = reinterpret_cast<float*>(a.ws + b.pw_off);
-  // the operands of dx and dW
-  MmOperand Xo = X, Wp = Wo;
-  {
-    auto parts = [](int64_t n) { return int(std::min<int64_t>(kMaxParts, cdiv(n, 1024))); };
-    const int p0 = parts(a.N), p1 = a.bf16 ? parts(cdiv(a.N * a.d, 8)) : 0, p2 = a.bf16 ? parts(cdiv(a.V * a.d, 8)) : 0;
-    const uint16_t* x16 = a.bf16 ? static_cast<const uint16_t*>(x) : nullptr;
-    const uint16_t* w16 = a.bf16 ? static_cast<const uint16_t*>(W) : nullptr;
-    k_loss_maxima<<<unsigned(p0 + p1 + p2), 1024, 0, a.stream>>>(dloss, dlse, targets, a.target_bytes, a.ignore, a.N, a.V,
-                                                                 a.d, x16, w16, p0, p1, p2, units);
-    const int64_t nc = cdiv(a.N, 256), C = b.op.ldp / 8;
-    const int64_t n1 = a.bf16 ? cdiv(a.N * C, 256) : 0, n2 = a.bf16 ? cdiv(a.V * C, 256) : 0;
-    k_loss_coef<<<unsigned(nc + n1 + n2), 256, 0, a.stream>>>(dloss, dlse, lse, targets, a.target_bytes, a.ignore, a.N, a.V,
-                                                              a.d, b.op.ldp, x16, w16, int(nc), int(n1), p0, p1, p2, units,
-                                                              coef, xh, wh);
-    if (a.bf16) {
-      Xo = {xh, b.op.ldp, 0};
-      Wp = {wh, b.op.ldp, 0};
-    }
-  }
-  auto out = [&](const float* P, int S, int64_t n, int is_w, void* o, int64_t at) {
+  const Operands o = lay_out(a, b.op, x, W, targets, lse, dloss, dlse, coef);
+  LossUnits* const units = o.units;
+  auto out = [&](const float* P, int S, int64_t n, int is_w, void* to, int64_t at) {
     const unsigned grid = unsigned(cdiv(n, 256));
     if (a.bf16)
-      k_loss_out<true><<<grid, 256, 0, a.stream>>>(P, S, n, units, is_w, a.scale, static_cast<uint16_t*>(o) + at);
+      k_loss_out<true><<<grid, 256, 0, a.stream>>>(P, S, n, units, is_w, a.scale, static_cast<uint16_t*>(to) + at);
     else
-      k_loss_out<false><<<grid, 256, 0, a.stream>>>(P, S, n, units, is_w, a.scale, static_cast<float*>(o) + at);
+      k_loss_out<false><<<grid, 256, 0, a.stream>>>(P, S, n, units, is_w, a.scale, static_cast<float*>(to) + at);
   };
   // one tile shape and storage type of each kernel
   auto pick = [&](bool big, auto run) {
@@ -839,15 +867,15 @@ void launch_loss_backward(const LossArgs& a, const void* x, const void* W, const
     const int64_t pend = v0 + cdiv(nv, 8) * 8;
     pick(b.big_z, [&](auto tl, auto bf) {
       using Tl = decltype(tl);
-      const int64_t n_tok = cdiv(a.N, Tl::BN), units = n_tok * cdiv(nv, Tl::BM), slots = Tl::BN == Big::BN ? kCus : 2 * kCus;
-      k_loss_dz<Tl, decltype(bf)::value><<<unsigned(std::min(units, slots)), Tl::NTHR, 0, a.stream>>>(
-          Wo, X, a.N, a.V, b.op.ldp, terms, c, v0, pend, int(n_tok), coef, dz, b.ldz);
+      const int64_t n_tok = cdiv(a.N, Tl::BN), tiles = n_tok * cdiv(nv, Tl::BM), slots = Tl::BN == Big::BN ? kCus : 2 * kCus;
+      k_loss_dz<Tl, decltype(bf)::value><<<unsigned(std::min(tiles, slots)), Tl::NTHR, 0, a.stream>>>(
+          o.Wo, o.X, a.N, a.V, b.op.ldp, terms, c, units, v0, pend, int(n_tok), coef, dz, b.ldz);
     });
     const MmOperand Z{dz, b.ldz, a.N * b.ldz};
     if (dx)
       pick(b.big_o, [&](auto tl, auto bf) {
         using Tl = decltype(tl);
-        const MmOperand Wc{Wp.base + v0 * Wp.ld, Wp.ld, Wp.plane};
+        const MmOperand Wc{o.Wh.base + v0 * o.Wh.ld, o.Wh.ld, o.Wh.plane};
         const int64_t n_col = cdiv(a.d, Tl::BN);
         k_loss_mm<Tl, false, decltype(bf)::value><<<unsigned(cdiv(a.N, Tl::BM) * n_col * b.sx), Tl::NTHR, 0, a.stream>>>(
             Z, Wc, a.N, a.d, nv, b.kx, terms, int(n_col), int(b.sx), v0 > 0, px, last && b.sx == 1 ? dx : nullptr, units, a.scale);
@@ -858,7 +886,7 @@ void launch_loss_backward(const LossArgs& a, const void* x, const void* W, const
         using Tl = decltype(tl);
         const int64_t n_col = cdiv(a.d, Tl::BN);
         k_loss_mm<Tl, true, decltype(bf)::value><<<unsigned(cdiv(nv, Tl::BM) * n_col * b.sw), Tl::NTHR, 0, a.stream>>>(
-            Z, Xo, nv, a.d, a.N, b.kw, terms, int(n_col), int(b.sw), 0, pw, b.sw == 1 ? dWc : nullptr, units, a.scale);
+            Z, o.Xh, nv, a.d, a.N, b.kw, terms, int(n_col), int(b.sw), 0, pw, b.sw == 1 ? dWc : nullptr, units, a.scale);
       });
       if (b.sw > 1) out(pw, int(b.sw), nv * a.d, 1, dW, v0 * a.d);
     }

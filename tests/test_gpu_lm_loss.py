@@ -143,6 +143,30 @@ def test_large_logits_and_bad_values_stay_in_their_rows():
     assert dx2[9].isnan().all() and torch.equal(dx2[keep], dx[keep])
 
 
+def test_values_far_below_the_largest():
+    """fp32 rows from 1 down to 1e-9 of the largest value: on top of the usual band the operands may be off by
+    2^-39 of their tensor's largest value (two fp16 terms in units of that value)."""
+    N, V, d = 160, 200, 48
+    x, W, t, dloss, _ = _inputs(N, V, d, "f32", 12)
+    x *= 10.0 ** -(torch.arange(N, device="cuda") % 10)[:, None].float()
+    W *= 10.0 ** -(torch.arange(V, device="cuda") % 7)[:, None].float()
+    loss, lse = prn.vocab_loss(x, W, t)
+    dx, dW = prn.vocab_loss_backward(dloss, x, W, t, lse)
+    x64, W64, tn, dl = to_f64(x), to_f64(W), t.cpu().numpy(), to_f64(dloss)
+    ref, band = _bands(x64, W64, tn, dl, None, "f32", 1.0)
+    ux, uw = 2.0 ** -39 * np.abs(x64).max(), 2.0 ** -39 * np.abs(W64).max()
+    bz = (ux * np.abs(W64).sum(1)[None, :] + uw * np.abs(x64).sum(1)[:, None])
+    one = np.where(tn == -100, 0.0, np.abs(dl))
+    dz = 2 * one[:, None] * bz            # through p and the target's entry
+    u = 2.0 ** -39 * one.max()            # dz's own terms
+    extra = (2 * bz.max(-1), bz.max(-1), dz @ np.abs(W64) + u * np.abs(W64).sum(0) + uw * 2 * one[:, None],
+             dz.T @ np.abs(x64) + u * np.abs(x64).sum(0) + ux * 2 * one.sum())
+    for name, got, r, b, e in zip(("loss", "lse", "dx", "dW"), (loss, lse, dx, dW), ref, band, extra):
+        worst = float((np.abs(to_f64(got) - r) / (b + e)).max())
+        say(f"  {name}: of the band {worst:.3f}")
+        assert worst <= 1.0, name
+
+
 def test_gradients_that_are_zero_or_one_sided():
     x, W, t, dloss, dlse = _inputs(90, 200, 24, "bf16", 3)
     loss, lse = prn.vocab_loss(x, W, t)
