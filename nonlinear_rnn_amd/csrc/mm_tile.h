@@ -128,7 +128,15 @@ struct MmTile {
   static __device__ __forceinline__ int row_pos(int r, int c) {
     return BK == 64 ? c ^ ((r >> 1) & 7) : c ^ ((r >> 2) & 3);
   }
-  static __device__ __forceinline__ int swz(int k) { return 4 * ((k & 3) | (((k >> 3) & 1) << 2)); }
+  // where the chunks of row k (of CPR) go: c ^ swz
+  template <int CPR>
+  static __device__ __forceinline__ int swz(int k) {
+    static_assert(CPR == 24 || (CPR & (CPR - 1)) == 0, "XOR stays within a row");
+    if constexpr (CPR == 24)
+      return 4 * ((k >> 1) & 1);   // rows of 384 bytes: neighbours are half of the banks apart by themselves
+    else
+      return 4 * ((k & 3) | (((k >> 3) & 1) << 2)) & (CPR - 1);
+  }
 
   // lane's source chunk of wave load li of an operand with BR rows of the
   // tile index: (row or k within the stage, first element along the contiguous index)
@@ -142,7 +150,7 @@ struct MmTile {
     } else {
       constexpr int CPR = BR / 8;
       slow = v / CPR;
-      fast = 8 * ((v % CPR) ^ (swz(slow) & (CPR - 1)));
+      fast = 8 * ((v % CPR) ^ swz<CPR>(slow));
     }
   }
 
@@ -261,7 +269,7 @@ struct MmTile {
 #pragma unroll
     for (int call = 0; call < 2; ++call) {
       const int k = 16 * kb + 8 * (grp >> 1) + (jl >> 2) + 4 * call;
-      const uint8_t* a = st + k * ROWBYTES + 16 * ((col >> 3) ^ (swz(k) & (ROWBYTES / 16 - 1))) + 2 * (col & 7);
+      const uint8_t* a = st + k * ROWBYTES + 16 * ((col >> 3) ^ swz<ROWBYTES / 16>(k)) + 2 * (col & 7);
       const mm_s16x4 r = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) mm_s16x4*)(a));
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[4 * call + e] = r[e];

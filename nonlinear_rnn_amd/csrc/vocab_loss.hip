@@ -16,11 +16,12 @@
 // them for the logits' second time.
 //
 // The matrix cores take 16-bit operands.
-// bf16 data: the logits are exact products of bf16 values.  dz is rounded to
-// fp16, not bf16: an entry is then off by 2^-12 of itself at most, where
-// bf16's 2^-9 would double the error that the outputs' own rounding makes (the
-// entry of the target can carry the whole row).  W and x are laid out as fp16
-// for dx and dW, which holds bf16's eight bits exactly.
+// bf16 data: the forward's logits are products of the values as they are.  dz
+// is rounded to fp16, not bf16: an entry is then off by 2^-12 of itself at
+// most, where bf16's 2^-9 would double the error that the outputs' own rounding
+// makes (the entry of the target can carry the whole row).  W and x are laid
+// out as fp16 for the backward's products, which holds bf16's eight bits
+// exactly (down to 2^-31 of the largest value, below that to 2^-40 of it).
 // fp32 data: x, W and dz run as two fp16 terms, v = hi + lo to 2^-22 |v|, three
 // products each (lo lo, below 2^-22, is left out).  That is four fp32
 // roundings a product, below what the fp32 sums over them make; the exact
@@ -46,8 +47,10 @@ constexpr int kTerms = 3;   // products of two-term operands
 
 // 8 waves, 256 x 256, 128 KB: the least traffic per product; one workgroup a CU
 using Big = MmTile<2, 4, 4, 2, 64, 2>;
-// 4 waves, 256 x 128, 72 KB: two workgroups a CU, and less waste at narrow edges
+// 4 waves, 256 x 128, 72 KB, two workgroups a CU: for the logits of few tokens
 using Mid = MmTile<2, 2, 4, 2, 32, 3>;
+// 8 waves, 256 x 192, 112 KB: for dx and dW where 256 columns a tile would be wider than the rows
+using Wide = MmTile<4, 2, 2, 3, 64, 2>;
 // few tokens: 128 x 64
 using Few = MmTile<4, 1, 1, 2, 64, 3>;
 constexpr int kXcd = 8;
@@ -87,8 +90,12 @@ __global__ void __launch_bounds__(256) k_loss_pad(const uint16_t* __restrict__ i
   const int64_t r = i / C;
   const int c0 = static_cast<int>(i - r * C) * 8;
   mm_s16x8 v;
+  if (c0 + 8 <= d) {   // one load, aligned or not
+    __builtin_memcpy(&v, in + r * d + c0, sizeof(v));
+  } else {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = c0 + e < d ? static_cast<short>(in[r * d + c0 + e]) : short(0);
+    for (int e = 0; e < 8; ++e) v[e] = c0 + e < d ? static_cast<short>(in[r * d + c0 + e]) : short(0);
+  }
   *reinterpret_cast<mm_s16x8*>(out + r * ldp + c0) = v;
 }
 
@@ -98,7 +105,7 @@ constexpr int kUnit = 13;   // dz is stored times 2^13: fp16 has entries down to
 // The units of a call
 struct LossUnits {
   float g;                         // dz is stored as 2^kUnit dz / (s g)
-  float back_z;                    // z = acc back_z s (1 with bf16 data)
+  float back_z;                    // z = acc back_z s
   float back_x, back_w;            // dx = acc back_x (s g), dW = acc back_w (s g)
   float parts[3][kMaxParts];       // the workgroups' maxima: of dloss and dlse, x, W
 };
@@ -219,7 +226,7 @@ __global__ void __launch_bounds__(256) k_loss_layout(const float* __restrict__ d
     unit_of(maximum(2, parts2), &iw);
     if (tid == 0) {
       u->g = g;
-      u->back_z = BF16 ? 1.0f : ix * iw;
+      u->back_z = ix * iw;
       u->back_x = iw / (1 << kUnit);
       u->back_w = ix / (1 << kUnit);
     }
@@ -447,7 +454,7 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_dz(MmOperand W, MmOperand 
                                                          int64_t piece0, int64_t piece1, int n_tok,
                                                          const RowCoef* __restrict__ coef, uint16_t* __restrict__ dz,
                                                          int64_t ldz) {
-  if constexpr (!BF16) c *= units->back_z;
+  c *= units->back_z;
   // the loads are up to NST tiles ahead (tiles of one stage)
   constexpr int kRing = Tl::NST + 1;
   static_assert(sizeof(RowCoef) == 16 && Tl::BN % 64 == 0 && Tl::BN / 64 <= Tl::NW, "one coefficient load per wave");
@@ -482,7 +489,7 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_dz(MmOperand W, MmOperand 
     uint32_t vt, tok;
     tile_of(cu.u, v_tiles, n_tok, kGroup, vt, tok);
     const int64_t v0 = piece0 + static_cast<int64_t>(vt) * Tl::BM, n0 = static_cast<int64_t>(tok) * Tl::BN;
-    tile.template multiply<false, false, false, !BF16>(next);
+    tile.template multiply<false, false, false, true>(next);
     uint8_t* const base = reinterpret_cast<uint8_t*>(dz + n0 * ldz + (v0 - piece0));
     const int rows = static_cast<int>(imin(piece1 - v0, Tl::BM)), toks = static_cast<int>(imin(N - n0, Tl::BN));
     const int vocab_left = static_cast<int>(imin(V - v0, Tl::BM));
@@ -648,12 +655,22 @@ struct Plan {
   int64_t ldp;
   size_t units_off, xp_off, wp_off, xh_off, wh_off, end;
 };
+// Rows laid out anew are whole lines of 128 bytes, or an even part of one: a
+// stage reads 128 bytes of every row, which other rows have in two lines (a
+// forward call of 5003 x 1001 x 50021 took 587 us with rows of 2016 bytes and
+// takes 534).  bf16 rows of a multiple of 8 are read where they are: at
+// 5003 x 520 x 50021 the copy costs what it gains, 323 us to 318.
+int64_t row_of(int64_t d) {
+  for (int64_t n = 8; n < 64; n *= 2)
+    if (d <= n) return n;
+  return cdiv(d, 64) * 64;
+}
 Plan plan_operands(const LossArgs& a, bool back) {
   Plan p{};
   p.planes = a.bf16 ? 1 : 2;
-  p.ldp = cdiv(a.d, 8) * 8;
-  p.pad = a.bf16 && a.d % 8 != 0;
   const bool terms = back || !a.bf16;
+  p.pad = !terms && a.d % 8 != 0;
+  p.ldp = row_of(a.d);
   size_t off = 0;
   auto take = [&](bool on, size_t bytes) {
     const size_t at = off;
@@ -709,7 +726,8 @@ PlanFw plan_fw(const LossArgs& a) {
 
 struct PlanBw {
   Plan op;
-  bool big_z, big_o;        // tiles of the logits; of dx and dW
+  bool big_z;               // tile of the logits
+  int out;                  // tile columns of dx and dW
   int64_t piece, ldz;
   int64_t sx, kx, sw, kw;   // slices of dx's sum (over the piece) and dW's (over the tokens), and their lengths
   size_t coef_off, dz_off, px_off, pw_off, total;
@@ -718,7 +736,6 @@ PlanBw plan_bw(const LossArgs& a) {
   PlanBw b{};
   b.op = plan_operands(a, true);
   b.big_z = take_big(a.N);
-  b.big_o = take_big(a.d);
   const int64_t v_tiles = cdiv(a.V, Big::BM);
   const size_t row = size_t(a.N) * b.op.planes * 2 * Big::BM;
   int64_t per = std::max<int64_t>(1, int64_t(kPieceBytes / row));
@@ -726,16 +743,24 @@ PlanBw plan_bw(const LossArgs& a) {
   b.piece = per * Big::BM;
   // rows of dz are no power of two apart: they would fall on few memory channels
   b.ldz = b.piece + 64;
-  const int64_t slots = (b.big_o ? 1 : 2) * kCus, bn = b.big_o ? Big::BN : Mid::BN;
-  auto slices = [&](int64_t rows, int64_t K, int64_t* len) {
-    const int64_t tiles = cdiv(rows, Big::BM) * cdiv(a.d, bn);
-    int64_t s = std::max<int64_t>(1, slots / tiles);
-    s = std::min<int64_t>(s, std::max<int64_t>(1, K / 512));
-    *len = cdiv(cdiv(K, s), 64) * 64;
-    return cdiv(K, *len);
+  // the products' tile: the shorter of the two plans.  256 columns a tile are
+  // faster than 192 per column, those waste less at the edge and may fill the
+  // device's rounds better: 16384 x 520 x 16384 took 1118 us with 192 and 1194
+  // with 256, x 512 1076 and 921.  (128, two workgroups a CU, was never faster
+  // than 192: dz is read once for every column of tiles.)
+  auto out_plan = [&](int64_t bn) {
+    auto slices = [&](int64_t rows, int64_t K, int64_t* s, int64_t* len) {
+      const int64_t tiles = cdiv(rows, Big::BM) * cdiv(a.d, bn);
+      *s = std::min(std::max<int64_t>(1, kCus / tiles), std::max<int64_t>(1, K / 512));
+      *len = cdiv(cdiv(K, *s), 64) * 64;
+      *s = cdiv(K, *len);
+      return cdiv(tiles * *s, kCus) * *len * (bn == Big::BN ? bn * 100 : bn * 112);
+    };
+    const int64_t nv = std::min(b.piece, a.V);
+    b.out = static_cast<int>(bn);
+    return slices(a.N, nv, &b.sx, &b.kx) + slices(nv, a.N, &b.sw, &b.kw);
   };
-  b.sx = slices(a.N, std::min(b.piece, a.V), &b.kx);
-  b.sw = slices(std::min(b.piece, a.V), a.N, &b.kw);
+  if (out_plan(Wide::BN) < out_plan(Big::BN)) out_plan(Wide::BN);
   b.coef_off = b.op.end;
   b.dz_off = b.coef_off + up(size_t(a.N) * sizeof(RowCoef));
   b.px_off = b.dz_off + up(size_t(a.N) * b.op.planes * b.ldz * 2);
@@ -771,7 +796,7 @@ Operands lay_out(const LossArgs& a, const Plan& p, const void* x, const void* W,
     };
     if (a.bf16) go(std::true_type{}); else go(std::false_type{});
   }
-  if (!a.bf16) {
+  if (o.units) {
     o.X = o.Xh;
     o.Wo = o.Wh;
   } else if (p.pad) {
@@ -809,7 +834,7 @@ void launch_loss(const LossArgs& a, const void* x, const void* W, const void* ta
   auto go = [&](auto tl, auto f16) {
     using Tl = decltype(tl);
     k_loss_lse<Tl, decltype(f16)::value><<<unsigned(f.grid), Tl::NTHR, 0, a.stream>>>(
-        o.Wo, o.X, a.N, a.V, f.op.ldp, terms, c, o.units, int(f.n_tok), int(f.splits), int(f.per_split), part);
+        o.Wo, o.X, a.N, a.V, a.d, terms, c, o.units, int(f.n_tok), int(f.splits), int(f.per_split), part);
   };
   auto go_type = [&](auto tl) {
     if (a.bf16) go(tl, std::false_type{}); else go(tl, std::true_type{});
@@ -851,13 +876,11 @@ void launch_loss_backward(const LossArgs& a, const void* x, const void* W, const
       k_loss_out<false><<<grid, 256, 0, a.stream>>>(P, S, n, units, is_w, a.scale, static_cast<float*>(to) + at);
   };
   // one tile shape and storage type of each kernel
-  auto pick = [&](bool big, auto run) {
-    using T_ = std::true_type;
-    using F_ = std::false_type;
-    if (big && a.bf16) run(Big{}, T_{});
-    else if (big) run(Big{}, F_{});
-    else if (a.bf16) run(Mid{}, T_{});
-    else run(Mid{}, F_{});
+  auto typed = [&](auto tl, auto run) {
+    if (a.bf16) run(tl, std::true_type{}); else run(tl, std::false_type{});
+  };
+  auto product = [&](auto run) {
+    if (b.out == Big::BN) typed(Big{}, run); else typed(Wide{}, run);
   };
   const size_t elt = a.bf16 ? 2 : 4;
   for (int64_t v0 = 0; v0 < a.V; v0 += b.piece) {
@@ -865,15 +888,16 @@ void launch_loss_backward(const LossArgs& a, const void* x, const void* W, const
     const bool last = v1 == a.V;
     // dz rows reach the end of the piece's last tile of 8: zeros past the vocabulary
     const int64_t pend = v0 + cdiv(nv, 8) * 8;
-    pick(b.big_z, [&](auto tl, auto bf) {
+    auto logits = [&](auto tl, auto bf) {
       using Tl = decltype(tl);
       const int64_t n_tok = cdiv(a.N, Tl::BN), tiles = n_tok * cdiv(nv, Tl::BM), slots = Tl::BN == Big::BN ? kCus : 2 * kCus;
       k_loss_dz<Tl, decltype(bf)::value><<<unsigned(std::min(tiles, slots)), Tl::NTHR, 0, a.stream>>>(
-          o.Wo, o.X, a.N, a.V, b.op.ldp, terms, c, units, v0, pend, int(n_tok), coef, dz, b.ldz);
-    });
+          o.Wo, o.X, a.N, a.V, a.d, terms, c, units, v0, pend, int(n_tok), coef, dz, b.ldz);
+    };
+    if (b.big_z) typed(Big{}, logits); else typed(Mid{}, logits);
     const MmOperand Z{dz, b.ldz, a.N * b.ldz};
     if (dx)
-      pick(b.big_o, [&](auto tl, auto bf) {
+      product( [&](auto tl, auto bf) {
         using Tl = decltype(tl);
         const MmOperand Wc{o.Wh.base + v0 * o.Wh.ld, o.Wh.ld, o.Wh.plane};
         const int64_t n_col = cdiv(a.d, Tl::BN);
@@ -882,7 +906,7 @@ void launch_loss_backward(const LossArgs& a, const void* x, const void* W, const
       });
     if (dW) {
       void* const dWc = static_cast<uint8_t*>(dW) + v0 * a.d * elt;
-      pick(b.big_o, [&](auto tl, auto bf) {
+      product( [&](auto tl, auto bf) {
         using Tl = decltype(tl);
         const int64_t n_col = cdiv(a.d, Tl::BN);
         k_loss_mm<Tl, true, decltype(bf)::value><<<unsigned(cdiv(nv, Tl::BM) * n_col * b.sw), Tl::NTHR, 0, a.stream>>>(
