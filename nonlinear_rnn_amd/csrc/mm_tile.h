@@ -19,7 +19,15 @@
 //         eight rows of one transposed read (k0 .. k0 + 3 and k0 + 8 ..
 //         k0 + 11) on different banks.
 // A wait for a wave's own loads and a bare barrier make a stage complete (a
-// fence would drain the stages still in flight too).
+// fence would drain the stages still in flight too).  They come before a
+// stage's last 16 k: its fragments are in registers by then, so its buffer is
+// free for the next load, and the next stage's first fragments are read while
+// the last products run.  (With the wait at the head of a stage the cores
+// stood still for it and the reads behind it: the logits of 32768 x 512 x 32768
+// took 1.17 ms, now 1.05.)
+// What bounds it: power.  At 256 x 256 the loop runs at 1.0 .. 1.15 PFLOP/s of
+// random data (the matrix cores busy 53 .. 58% of the cycles, at 1.85 GHz of
+// 2.4) and at 1.76 of zeros.
 //
 // Fragment layout of v_mfma_f32_32x32x16_bf16 and _f16: lane l feeds row l % 32 of A
 // and column l % 32 of B with the k values 8 (l / 32) .. + 7; accumulator r
@@ -28,6 +36,8 @@
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 namespace prn {
 
@@ -277,16 +287,25 @@ struct MmTile {
     return __builtin_bit_cast(mm_bf16x8, v);
   }
 
-  // acc = (or, with ADD, +=) the next tile's product (acc is left alone if the summed range is empty)
-  template <bool TA, bool TB, bool ADD = false, bool F16 = false, class Next>
-  __device__ __forceinline__ void multiply(Next&& next) {
+  // acc = (or, with ADD, +=) the next tile's product (acc is left alone if the
+  // summed range is empty).  `stored`: this wave has issued STORES stores, no
+  // fewer, since the last stage was loaded; they may stay in flight (the
+  // counter goes down in the order of issue).
+  template <bool TA, bool TB, bool ADD = false, bool F16 = false, int STORES = 0, class Next>
+  __device__ __forceinline__ void multiply(Next&& next, bool stored = false) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wr = wave / WC, wc = wave % WC;
+    constexpr int KB = BK / 16;
+    static_assert(KB % 2 == 0, "two sets of fragments in turn");
     const int stages = nk * terms;
-    for (int st = 0; st < stages; ++st) {
-      // this stage has landed; every wave is done with the buffer that the
-      // next load fills
+    if (stages == 0) return;
+    const uint8_t* sa;
+    // the next stage has landed, and every wave is done with the buffer that
+    // the load after it fills
+    auto arrive = [&](bool after_stores) {
       asm volatile("" ::: "memory");
-      if (ahead >= NST - 1)
+      if (STORES && after_stores)
+        mm_wait_loads<STORES>();
+      else if (ahead >= NST - 1)
         mm_wait_loads<(NST - 2) * (NLA + NLB)>();
       else
         mm_wait_loads<0>();
@@ -294,60 +313,70 @@ struct MmTile {
       asm volatile("" ::: "memory");
       if (more) load<TA, TB>(next);
       --ahead;
-      const uint8_t* sa = lds + buf_use * STAGE;
-      const uint8_t* sb = sa + ABYTES;
+      sa = lds + buf_use * STAGE;
       buf_use = buf_use + 1 == NST ? 0 : buf_use + 1;
-      mm_bf16x8 av[BK / 16][WM], bv[BK / 16][WN];
+    };
+    mm_bf16x8 av[2][WM], bv[2][WN];
+    auto fragments = [&](int kb, mm_bf16x8 (&a)[WM], mm_bf16x8 (&b)[WN]) {
+      const uint8_t* sb = sa + ABYTES;
 #pragma unroll
-      for (int kb = 0; kb < BK / 16; ++kb) {
-#pragma unroll
-        for (int j = 0; j < WN; ++j) {
-          const int at = (wc * WN + j) * 32;
-          if constexpr (TB) bv[kb][j] = frag_cols<2 * BN>(sb, at, kb); else bv[kb][j] = frag_rows(sb, at, kb);
-        }
-#pragma unroll
-        for (int i = 0; i < WM; ++i) {
-          const int at = (wr * WM + i) * 32;
-          if constexpr (TA) av[kb][i] = frag_cols<2 * BM>(sa, at, kb); else av[kb][i] = frag_rows(sa, at, kb);
-        }
+      for (int j = 0; j < WN; ++j) {
+        const int at = (wc * WN + j) * 32;
+        if constexpr (TB) b[j] = frag_cols<2 * BN>(sb, at, kb); else b[j] = frag_rows(sb, at, kb);
       }
-      // a tile's first products start from zero (cheaper than clearing acc)
-      if (!ADD && st == 0) {
+#pragma unroll
+      for (int i = 0; i < WM; ++i) {
+        const int at = (wr * WM + i) * 32;
+        if constexpr (TA) a[i] = frag_cols<2 * BM>(sa, at, kb); else a[i] = frag_rows(sa, at, kb);
+      }
+    };
+    // every product with a share of the next fragments behind it (left to
+    // itself the compiler reads each fragment just before its use)
+    auto in_order = [&](int reads) {
+      constexpr int kReads = WM * (TA ? 2 : 1) + WN * (TB ? 2 : 1), kProducts = WM * WN, kMost = (kReads + kProducts - 1) / kProducts;
+#pragma unroll
+      for (int m = 0; m < kProducts; ++m) {
+        __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+        if (reads && (m + 1) * kReads / kProducts > m * kReads / kProducts) __builtin_amdgcn_sched_group_barrier(0x100, kMost, 0);
+      }
+    };
+    auto products = [&](int set) {
+#pragma unroll
+      for (int i = 0; i < WM; ++i)
+#pragma unroll
+        for (int j = 0; j < WN; ++j) acc[i][j] = mm_product<F16>(av[set][i], bv[set][j], acc[i][j]);
+    };
+    // a stage whose first fragments are in set 0; but after the last one, the
+    // next stage's are on their way there while the last products run
+    auto stage = [&](bool first, auto last) {
+      fragments(1, av[1], bv[1]);
+      if (first) {   // a tile's first products start from zero (cheaper than clearing acc)
         const mm_f32x16 zero = {};
 #pragma unroll
         for (int i = 0; i < WM; ++i)
 #pragma unroll
-          for (int j = 0; j < WN; ++j)
-            acc[i][j] = mm_product<F16>(av[0][i], bv[0][j], zero);
+          for (int j = 0; j < WN; ++j) acc[i][j] = mm_product<F16>(av[0][i], bv[0][j], zero);
       } else {
-#pragma unroll
-        for (int i = 0; i < WM; ++i)
-#pragma unroll
-          for (int j = 0; j < WN; ++j)
-            acc[i][j] = mm_product<F16>(av[0][i], bv[0][j], acc[i][j]);
+        products(0);
       }
 #pragma unroll
-      for (int kb = 1; kb < BK / 16; ++kb)
-#pragma unroll
-        for (int i = 0; i < WM; ++i)
-#pragma unroll
-          for (int j = 0; j < WN; ++j)
-            acc[i][j] = mm_product<F16>(av[kb][i], bv[kb][j], acc[i][j]);
-      // order of the stage: the first 16 k's fragments, then every product
-      // with a share of the next fragments behind it.  Left to itself the
-      // compiler reads each fragment just before its use, to save registers.
-      constexpr int kReads = WM * (TA ? 2 : 1) + WN * (TB ? 2 : 1), kProducts = WM * WN;
-      __builtin_amdgcn_sched_group_barrier(0x100, kReads, 0);
-#pragma unroll
-      for (int kb = 0; kb < BK / 16; ++kb)
-#pragma unroll
-        for (int m = 0; m < kProducts; ++m) {
-          constexpr int kMost = (kReads + kProducts - 1) / kProducts;
-          __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
-          if (kb + 1 < BK / 16 && (m + 1) * kReads / kProducts > m * kReads / kProducts)
-            __builtin_amdgcn_sched_group_barrier(0x100, kMost, 0);
+      for (int kb = 1; kb < KB; ++kb) {
+        if (kb + 1 < KB) {
+          fragments(kb + 1, av[(kb + 1) & 1], bv[(kb + 1) & 1]);
+        } else if (!decltype(last)::value) {
+          __builtin_amdgcn_sched_barrier(0);
+          arrive(false);
+          fragments(0, av[0], bv[0]);
         }
-    }
+        products(kb & 1);
+        in_order(kb + 1 < KB || !decltype(last)::value);
+      }
+    };
+    arrive(stored);
+    fragments(0, av[0], bv[0]);
+    for (int st = 0; st + 1 < stages; ++st) stage(!ADD && st == 0, std::false_type{});
+    stage(!ADD && stages == 1, std::true_type{});
+    __builtin_amdgcn_sched_barrier(0);   // an epilogue begins after the products: mixed with them it spills
   }
 };
 
