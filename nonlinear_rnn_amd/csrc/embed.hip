@@ -447,91 +447,53 @@ __global__ void __launch_bounds__(kJoinThr) k_embed_join(const uint32_t* __restr
 
 // ------------------------------------------------------------ small sort ---
 
-// The whole sort in one workgroup's LDS, for up to kSmall positions whose key
-// and position fit one word (key above, position below): the other workgroups
-// of the launch clear dtable meanwhile.  A wave holds its positions in
-// order and ranks equal digits by ballots, as k_embed_scatter does.
-constexpr int kSmall = 8192, kSmallThr = 1024, kSmallItems = kSmall / kSmallThr;
-__global__ void __launch_bounds__(kSmallThr) k_embed_sort(SortIn in, int N, int pos_bits, int bits, int passes,
+// The whole sort in one launch, for up to kSmall positions whose key and
+// position fit one word (key above, position below; no two are alike): a
+// word's place is the number of words below it.  A workgroup has all words in
+// LDS and ranks kRanked of them: lane l has word l % 16, and counts among four
+// words at a time of its quarter of the wave's share.  The other workgroups of
+// the launch clear dtable meanwhile.  N^2 comparisons, but spread over the
+// device: a whole gradient of d = 250, V = 50021 takes 22 us at N = 4099, 28 at
+// 8192 and 47 at 16384; with the radix sort's launches 34, 35 and 37.
+constexpr int kSmall = 8192, kSmallThr = 1024, kRanked = 16;
+__global__ void __launch_bounds__(kSmallThr) k_embed_rank(SortIn in, int N, int pos_bits, int n_rank,
                                                           uint32_t* __restrict__ keys, uint32_t* __restrict__ pos,
                                                           uint4* __restrict__ clear, int64_t n_clear,
                                                           uint8_t* __restrict__ tail, int n_tail) {
   constexpr int NW = kSmallThr / 64;
-  __shared__ uint32_t word[kSmall];
-  __shared__ uint16_t wave_hist[NW][kBins];
-  __shared__ uint32_t start[kBins];
-  __shared__ uint32_t scan[NW];
+  __shared__ __attribute__((aligned(16))) uint32_t word[kSmall];
+  __shared__ uint32_t below[NW][kRanked];
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-  if (blockIdx.x > 0) {
-    const int64_t me = (static_cast<int64_t>(blockIdx.x) - 1) * kSmallThr + tid;
-    const int64_t all = (static_cast<int64_t>(gridDim.x) - 1) * kSmallThr;
+  if (static_cast<int>(blockIdx.x) >= n_rank) {
+    const int64_t me = (static_cast<int64_t>(blockIdx.x) - n_rank) * kSmallThr + tid;
+    const int64_t all = (static_cast<int64_t>(gridDim.x) - n_rank) * kSmallThr;
     for (int64_t i = me; i < n_clear; i += all) clear[i] = make_uint4(0, 0, 0, 0);
     if (me < n_tail) tail[me] = 0;
     return;
   }
-  const int items = (N + kSmallThr - 1) / kSmallThr;   // of each lane; a wave's are together
-  const int at = w * items * 64;
-  const int nb = 1 << bits;
-  volatile uint16_t* const mine_hist = wave_hist[w];
-  uint32_t v[kSmallItems];
-  uint16_t rank[kSmallItems];
-#pragma unroll
-  for (int j = 0; j < kSmallItems; ++j) {
-    const int i = at + j * 64 + lane;
-    if (j < items && i < N) v[j] = sort_key<true>(in, i) << pos_bits | static_cast<uint32_t>(i);
+  constexpr uint32_t kNone = 0xffffffffu;   // below no word
+  const int quads = (N + 3) / 4;
+  for (int i = tid; i < 4 * quads; i += kSmallThr)
+    word[i] = i < N ? sort_key<true>(in, i) << pos_bits | static_cast<uint32_t>(i) : kNone;
+  __syncthreads();
+  const int at = static_cast<int>(blockIdx.x) * kRanked + lane % kRanked;
+  const uint32_t mine = at < N ? word[at] : 0;
+  uint32_t n = 0;
+#pragma unroll 4
+  for (int q = w * 4 + lane / kRanked; q < quads; q += 4 * NW) {
+    const uint4 o = *reinterpret_cast<const uint4*>(word + 4 * q);
+    n += (o.x < mine) + (o.y < mine) + (o.z < mine) + (o.w < mine);
   }
-  for (int p = 0; p < passes; ++p) {
-    const int shift = pos_bits + p * bits;
-    for (int b = lane; b < nb; b += 64) wave_hist[w][b] = 0;
-    // (a wave's LDS accesses are done in order)
+  n += __shfl_xor(n, 16, 64);
+  n += __shfl_xor(n, 32, 64);
+  if (lane < kRanked) below[w][lane] = n;
+  __syncthreads();
+  if (tid < kRanked && at < N) {
+    uint32_t to = 0;
 #pragma unroll
-    for (int j = 0; j < kSmallItems; ++j) {
-      const int i = at + j * 64 + lane;
-      if (j < items) {
-        if (p > 0 && i < N) v[j] = word[i];
-        const bool live = i < N;
-        const uint32_t dg = (v[j] >> shift) & (nb - 1);
-        const unsigned long long same = same_digit(dg, bits, live);
-        if (live) {
-          const uint16_t before = mine_hist[dg];
-          rank[j] = static_cast<uint16_t>(before + __popcll(same & ((1ull << lane) - 1)));
-          if ((same >> lane) == 1ull) mine_hist[dg] = static_cast<uint16_t>(before + __popcll(same));
-        }
-      }
-    }
-    __syncthreads();   // every wave's counts are there, and every word is in a register
-    // counts of earlier waves, and the digits' totals
-    uint32_t total = 0;
-    if (tid < nb) {
-#pragma unroll
-      for (int q = 0; q < NW; ++q) {
-        const uint32_t c = wave_hist[q][tid];
-        wave_hist[q][tid] = static_cast<uint16_t>(total);
-        total += c;
-      }
-    }
-    const uint32_t incl = wave_scan(total);
-    if (lane == 63) scan[w] = incl;
-    __syncthreads();
-    if (tid < nb) {
-      uint32_t base = incl - total;
-      for (int q = 0; q < w; ++q) base += scan[q];
-      start[tid] = base;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < kSmallItems; ++j) {
-      const int i = at + j * 64 + lane;
-      if (j < items && i < N) {
-        const uint32_t dg = (v[j] >> shift) & (nb - 1);
-        word[start[dg] + wave_hist[w][dg] + rank[j]] = v[j];
-      }
-    }
-    __syncthreads();
-  }
-  for (int i = tid; i < N; i += kSmallThr) {
-    keys[i] = word[i] >> pos_bits;
-    pos[i] = word[i] & ((1u << pos_bits) - 1);
+    for (int q = 0; q < NW; ++q) to += below[q][tid];
+    keys[to] = mine >> pos_bits;
+    pos[to] = static_cast<uint32_t>(at);
   }
 }
 
@@ -567,7 +529,7 @@ Plan plan(const EmbedArgs& a) {
   return p;
 }
 
-// does one workgroup sort them all?
+// are they sorted in one launch?
 bool small_sort(const EmbedArgs& a, int key_bits, int* pos_bits) {
   int pb = 1;
   while (((a.N - 1) >> pb) != 0) ++pb;
@@ -627,9 +589,9 @@ void launch_embed_backward(const EmbedArgs& a, const void* tokens, const void* d
   SortIn in{tokens, a.token_bytes, a.V, a.pad, nullptr, nullptr};
   int cur = 0, pos_bits;
   if (a.N > 0 && small_sort(a, p.key_bits, &pos_bits)) {
-    const unsigned others = unsigned(std::min<int64_t>(255, cdiv(words, kSmallThr) + 1));
-    k_embed_sort<<<1 + others, kSmallThr, 0, a.stream>>>(in, int(a.N), pos_bits, p.bits, p.passes, keys[0], pos[0], clear,
-                                                         words, tail, n_tail);
+    const unsigned ranks = unsigned(cdiv(a.N, kRanked)), others = unsigned(std::min<int64_t>(512, cdiv(words, kSmallThr) + 1));
+    k_embed_rank<<<ranks + others, kSmallThr, 0, a.stream>>>(in, int(a.N), pos_bits, int(ranks), keys[0], pos[0], clear, words,
+                                                             tail, n_tail);
   } else {
     auto sort = [&](auto items) {
       constexpr int IT = decltype(items)::value;

@@ -414,26 +414,35 @@ __global__ void __launch_bounds__(256) k_loss_join(const float2* __restrict__ pa
   const int lane = threadIdx.x & 63;
   if (n >= N) return;
   const float back = BF16 ? 1.0f : units->back_z, c = scale * kLog2e * back;
-  float m = -__builtin_inff();
-  for (int i = lane; i < splits; i += 64) m = fmaxf(m, part[n * splits + i].x);
+  const int64_t t = target_of(targets, target_bytes, n);
+  const bool in = t >= 0 && t < V;
+  // the pairs are on their way while the dot product waits for the target
+  constexpr int kHeld = 4;
+  const float2* const mine = part + n * splits;
+  float2 held[kHeld];
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k)
+    held[k] = lane + 64 * k < splits ? mine[lane + 64 * k] : make_float2(-__builtin_inff(), 0.0f);
+  float dot = 0.0f;
+  if (in && t != ignore) {
+    const typename S::T* xr = static_cast<const typename S::T*>(x) + n * d;
+    const typename S::T* wr = static_cast<const typename S::T*>(W) + t * d;
+#pragma unroll 8
+    for (int64_t i = lane; i < d; i += 64) dot = fmaf(S::load(xr + i), S::load(wr + i), dot);
+    dot = wave_sum(dot);
+  }
+  float m = held[0].x;
+#pragma unroll
+  for (int k = 1; k < kHeld; ++k) m = fmaxf(m, held[k].x);
+  for (int i = lane + 64 * kHeld; i < splits; i += 64) m = fmaxf(m, mine[i].x);
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
   const float ref = m == -__builtin_inff() ? 0.0f : m;
   float s = 0.0f;
-  for (int i = lane; i < splits; i += 64) {
-    const float2 p = part[n * splits + i];
-    s += p.y * ex2((p.x - ref) * c);
-  }
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k) s += held[k].y * ex2((held[k].x - ref) * c);
+  for (int i = lane + 64 * kHeld; i < splits; i += 64) s += mine[i].y * ex2((mine[i].x - ref) * c);
   s = wave_sum(s);
-  const int64_t t = target_of(targets, target_bytes, n);
-  float dot = 0.0f;
-  const bool in = t >= 0 && t < V;
-  if (in && t != ignore) {
-    const typename S::T* xr = static_cast<const typename S::T*>(x) + n * d;
-    const typename S::T* wr = static_cast<const typename S::T*>(W) + t * d;
-    for (int64_t i = lane; i < d; i += 64) dot = fmaf(S::load(xr + i), S::load(wr + i), dot);
-    dot = wave_sum(dot);
-  }
   if (lane == 0) {
     const float ln = logf(s);
     lse[n] = fmaf(ref * back, scale, ln);
