@@ -365,25 +365,31 @@ __global__ void __launch_bounds__(NTHR) k_block_norm_backward(NormDev a) {
   }
 }
 
-// out_k[c] = the sum over the G workgroups' partials: 16 waves take every
-// 16th partial of 64 channels in order, their sums are added in order
+// out_k[c] = the sum over the G workgroups' partials, for 16 channels: 64
+// groups of 16 lanes take every 64th partial in order, their sums are added in
+// a fixed order.  (64 channels a workgroup fill too few CUs: at d = 1001 and
+// 1024 partials 5.7 us where this takes 5.0.)
+constexpr int kWeightCols = 16;
 __global__ void __launch_bounds__(1024) k_block_norm_weights(const float* __restrict__ part, int G, int d,
                                                              float* o0, float* o1, float* o2) {
-  __shared__ float hand[16][64];
-  const int k = blockIdx.y, lane = threadIdx.x & 63, w = threadIdx.x >> 6, c = blockIdx.x * 64 + lane;
+  __shared__ float hand[16][kWeightCols];
+  const int k = blockIdx.y, col = threadIdx.x % kWeightCols, c = blockIdx.x * kWeightCols + col;
   float* const out = k == 0 ? o0 : k == 1 ? o1 : o2;
   if (!out) return;
   const float* p = part + static_cast<int64_t>(k) * G * d;
   float s = 0.0f;
   if (c < d) {
 #pragma unroll 8
-    for (int g = w; g < G; g += 16) s += p[static_cast<int64_t>(g) * d + c];
+    for (int g = threadIdx.x / kWeightCols; g < G; g += 1024 / kWeightCols) s += p[static_cast<int64_t>(g) * d + c];
   }
-  hand[w][lane] = s;
+  s += __shfl_xor(s, 16, 64);
+  s += __shfl_xor(s, 32, 64);
+  if ((threadIdx.x & 63) < kWeightCols) hand[threadIdx.x >> 6][col] = s;
   __syncthreads();
-  if (w == 0 && c < d) {
+  if (threadIdx.x < kWeightCols && c < d) {
+    s = hand[0][col];
 #pragma unroll
-    for (int q = 1; q < 16; ++q) s += hand[q][lane];
+    for (int q = 1; q < 16; ++q) s += hand[q][col];
     out[c] = s;
   }
 }
@@ -479,7 +485,7 @@ void launch_block_norm_backward(const BlockNormArgs& a) {
   n.N = a.N, n.d = int(a.d), n.act = a.act, n.eps = a.eps;
   if (G > 0) go_all<true>(a.bf16, g, n, unsigned(G), a.stream);
   if (a.dw_post || a.dw_pre || a.dalpha) {
-    const dim3 grid(unsigned((a.d + 63) / 64), 3);
+    const dim3 grid(unsigned((a.d + kWeightCols - 1) / kWeightCols), 3);
     k_block_norm_weights<<<grid, 1024, 0, a.stream>>>(n.part, int(G), int(a.d), a.dw_post, a.dw_pre, a.dalpha);
   }
 }
