@@ -374,19 +374,23 @@ __global__ void __launch_bounds__(256) k_embed_sum(const uint32_t* __restrict__ 
 }
 
 // The frequent tokens that start among kJoin sorted positions: their chunks'
-// sums at 64 CPT channels (blockIdx.y), added in order by 16 waves (every 16th
-// chunk each, then the waves in order).
-constexpr int kJoin = 256, kJoinThr = 1024, kJoinBatch = 8;
+// sums at 64 CPT channels (blockIdx.y), added in order, a wave per token; a
+// token of kMany chunks or more by all 16 waves (every 16th chunk each, then
+// the waves in order).  All waves for every token took 37 us at 262144 tokens
+// over 131072, where up to 16 tokens start in one workgroup; this takes 30, most
+// of it the 22000 rows of the most frequent token in one workgroup.
+constexpr int kJoin = 256, kJoinThr = 1024, kJoinBatch = 8, kMany = 33;
 template <int DT, int CPT>
 __global__ void __launch_bounds__(kJoinThr) k_embed_join(const uint32_t* __restrict__ keys, const float* __restrict__ part,
                                                          int64_t N, int64_t V, int64_t d, float scale,
                                                          typename Storage<DT>::T* __restrict__ dtable) {
   using F = Vec<kF32, CPT>;
   constexpr int NW = kJoinThr / 64;
-  __shared__ uint32_t n_found;
-  __shared__ uint32_t found[kJoin / kLong + 1];
+  static_assert(kMany <= 64, "a wave counts its chunks at once");
+  __shared__ uint32_t n_found, n_many;
+  __shared__ uint32_t found[kJoin / kLong + 1], many[kJoin / kLong + 1];
   __shared__ float hand[NW][64 * CPT];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t at = static_cast<int64_t>(blockIdx.x) * kJoin;
   const int64_t p = at + threadIdx.x;
   bool starts = false;
@@ -394,52 +398,74 @@ __global__ void __launch_bounds__(kJoinThr) k_embed_join(const uint32_t* __restr
     const uint32_t k = keys[p];
     starts = k < V && keys[p + kLong - 1] == k && (p == 0 || keys[p - 1] != k);
   }
-  if (threadIdx.x == 0) n_found = 0;
+  if (threadIdx.x == 0) n_found = n_many = 0;
   __syncthreads();
   if (starts) found[atomicAdd(&n_found, 1u)] = threadIdx.x;
   __syncthreads();
   const int64_t c0 = (static_cast<int64_t>(blockIdx.y) * 64 + lane) * CPT, c = imin(c0, d - CPT);
   const bool mine = c0 < d;
-  for (uint32_t f = 0; f < n_found; ++f) {   // in any order: each writes its own row
-    const int64_t s = at + found[f];
-    const uint32_t k = keys[s];
-    float acc[CPT];
+  // how many of the token's chunks from q0 on there are, up to 64: chunk q is
+  // there if its first position holds the token
+  auto chunks = [&](int64_t s, uint32_t k, int64_t q0) {
+    const int64_t i = s + (q0 + lane) * kLong;
+    const unsigned long long there = __ballot(i < N && keys[i < N ? i : s] == k);
+    return ~there == 0 ? 64 : __builtin_ctzll(~there);
+  };
+  // acc += the sums of chunks q0 + first, + every .. of q0 + n
+  auto add = [&](int64_t s, int64_t q0, int first, int every, int n, float* acc) {
+    if (!mine) return;
+    for (int q = first; q < n; q += every * kJoinBatch) {
+      F v[kJoinBatch];
 #pragma unroll
-    for (int e = 0; e < CPT; ++e) acc[e] = 0.0f;
-    // the token's chunks, 64 at a time: chunk q is there if its first position holds the token
-    for (int64_t q0 = 0;; q0 += 64) {
-      const int64_t i = s + (q0 + lane) * kLong;
-      const unsigned long long there = __ballot(i < N && keys[i < N ? i : s] == k);
-      const int n = ~there == 0 ? 64 : __builtin_ctzll(~there);
-      if (mine) {
-        for (int q = w; q < n; q += NW * kJoinBatch) {
-          F v[kJoinBatch];
-#pragma unroll
-          for (int b = 0; b < kJoinBatch; ++b) {
-            const int64_t qq = q0 + q + b * NW;
-            if (q + b * NW < n) v[b] = *reinterpret_cast<const F*>(part + (2 * ((s + qq * kLong) / kBlock) + (qq == 0)) * d + c);
-          }
-#pragma unroll
-          for (int b = 0; b < kJoinBatch; ++b)
-            if (q + b * NW < n) {
-#pragma unroll
-              for (int e = 0; e < CPT; ++e) acc[e] += v[b].v[e];
-            }
-        }
+      for (int b = 0; b < kJoinBatch; ++b) {
+        const int64_t qq = q0 + q + b * every;
+        if (q + b * every < n) v[b] = *reinterpret_cast<const F*>(part + (2 * ((s + qq * kLong) / kBlock) + (qq == 0)) * d + c);
       }
+#pragma unroll
+      for (int b = 0; b < kJoinBatch; ++b)
+        if (q + b * every < n) {
+#pragma unroll
+          for (int e = 0; e < CPT; ++e) acc[e] += v[b].v[e];
+        }
+    }
+  };
+  auto finish = [&](uint32_t k, float* acc) {
+    if (!mine) return;
+#pragma unroll
+    for (int e = 0; e < CPT; ++e) acc[e] *= scale;
+    store_vec<DT, CPT>(dtable + static_cast<int64_t>(k) * d + c, acc);
+  };
+  for (uint32_t f = w; f < n_found; f += NW) {   // in any order: each writes its own row
+    const int64_t s = at + __builtin_amdgcn_readfirstlane(found[f]);
+    const uint32_t k = __builtin_amdgcn_readfirstlane(keys[s]);
+    const int n = chunks(s, k, 0);
+    if (n >= kMany) {
+      if (lane == 0) many[atomicAdd(&n_many, 1u)] = found[f];
+      continue;
+    }
+    float acc[CPT] = {};
+    add(s, 0, 0, 1, n, acc);
+    finish(k, acc);
+  }
+  __syncthreads();
+  for (uint32_t f = 0; f < n_many; ++f) {
+    const int64_t s = at + __builtin_amdgcn_readfirstlane(many[f]);
+    const uint32_t k = __builtin_amdgcn_readfirstlane(keys[s]);
+    float acc[CPT] = {};
+    for (int64_t q0 = 0;; q0 += 64) {
+      const int n = chunks(s, k, q0);
+      add(s, q0, w, NW, n, acc);
       if (n < 64) break;
     }
 #pragma unroll
     for (int e = 0; e < CPT; ++e) hand[w][lane * CPT + e] = acc[e];
     __syncthreads();
-    if (w == 0 && mine) {
+    if (w == 0) {
 #pragma unroll
       for (int q = 1; q < NW; ++q)
 #pragma unroll
         for (int e = 0; e < CPT; ++e) acc[e] += hand[q][lane * CPT + e];
-#pragma unroll
-      for (int e = 0; e < CPT; ++e) acc[e] *= scale;
-      store_vec<DT, CPT>(dtable + static_cast<int64_t>(k) * d + c, acc);
+      finish(k, acc);
     }
     __syncthreads();
   }
