@@ -169,12 +169,11 @@ def vocab_loss(x, W, targets, *, scale: float = 1.0, ignore_index: int = -100):
     where targets == ignore_index and NaN where a target is out of range; lse is the log of the summed
     exponentials (-loss is the target's log probability)."""
     x2, W, ids = _rows(x), _rows(W), _flat(targets)
-    N = x2.shape[0]
-    loss = torch.empty(N, dtype=torch.float32, device=x2.device)
+    loss = torch.empty(x2.shape[0], dtype=torch.float32, device=x2.device)
     lse = torch.empty_like(loss)
-    ws = _scratch(B_.prn_vocab_loss_workspace_bytes(x2.dtype, N, *W.shape), x2.device)
+    ws = _scratch(B_.prn_vocab_loss_workspace_bytes(x2.dtype, x2.shape[0], *W.shape), x2.device)
     B_.prn_vocab_loss(x2, W, ids, loss, lse, scale=scale, ignore_index=ignore_index, workspace=ws)
-    return loss.view(targets.shape), lse.view(targets.shape)
+    return (loss, lse) if targets.dim() == 1 else (loss.view(targets.shape), lse.view(targets.shape))
 
 
 def vocab_loss_backward(dloss, x, W, targets, lse, *, dlse=None, scale: float = 1.0, ignore_index: int = -100,
