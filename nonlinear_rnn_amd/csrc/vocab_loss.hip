@@ -756,12 +756,48 @@ PlanFw plan_fw(const LossArgs& a) {
   return f;
 }
 
+// A product's work: the rows whose tiles fill whole rounds of the device run
+// over the whole sum each; the sum of the rest is cut in slices, joined after.
+// The fewest microseconds of a few slice counts, with and without a head.
+struct Cut {
+  int64_t head;       // rows of the first kind
+  int64_t s, len;     // slices of the rest's sum, and their length
+};
+Cut cut_of(int64_t rows, int64_t K, int64_t d, int terms, int64_t bn, double* us) {
+  // microseconds of a CU for a tile over k of the sum (256 x 256 at 1.05
+  // PFLOP/s of the device), and of storing fp32 sums and reading them again at
+  // 4 TB/s, weighed half as much again: CUs that idle in a round leave the others
+  // their power (16384 x 520 x 16384 with dx's 192 tiles in four slices of the
+  // sum took 1093 us, in one 1066; 5003 x 520 x 50021 without the rest's slices
+  // 1056, with them 1016)
+  auto tile = [&](int64_t k) { return double(k) * terms * Big::BM * bn * (bn == Big::BN ? 1.0 : 1.12) * 2 / 4.1e6; };
+  auto join = [&](int64_t n, int64_t s) { return s > 1 ? 4 + double(s) * n * d * 8 * 1.5 / 4e6 : 0.0; };
+  const int64_t n_col = cdiv(d, bn), blocks = cdiv(rows, Big::BM), whole = blocks * n_col / kCus * kCus;
+  Cut best{};
+  *us = -1;
+  for (int64_t head = 0;; head = std::min(whole / n_col * Big::BM, rows)) {
+    const int64_t rest = rows - head, tiles = cdiv(rest, Big::BM) * n_col;
+    const double first = cdiv(cdiv(head, Big::BM) * n_col, kCus) * tile(K) + (head > 0 && rest > 0 ? 3 : 0);
+    for (int64_t want : {int64_t(1), int64_t(2), int64_t(3), int64_t(4), int64_t(6), int64_t(8), tiles ? std::min(kCus / tiles, K / 512) : 1}) {
+      if (want < 1 || (want > 1 && K / want < 512)) continue;
+      const int64_t len = cdiv(cdiv(K, want), 64) * 64, n = cdiv(K, len);
+      const double t = first + cdiv(tiles * n, kCus) * tile(len) + join(rest, n);
+      if (*us < 0 || t < *us) {
+        *us = t;
+        best = {head, n, len};
+      }
+    }
+    if (head > 0 || whole / n_col == 0) break;
+  }
+  return best;
+}
+
 struct PlanBw {
   Plan op;
   bool big_z;               // tile of the logits
   int out;                  // tile columns of dx and dW
   int64_t piece, ldz;
-  int64_t sx, kx, sw, kw;   // slices of dx's sum (over the piece) and dW's (over the tokens), and their lengths
+  Cut x, w;                 // of dx's sum (over the piece), and dW's (over the tokens)
   size_t coef_off, dz_off, px_off, pw_off, total;
 };
 PlanBw plan_bw(const LossArgs& a) {
@@ -780,24 +816,22 @@ PlanBw plan_bw(const LossArgs& a) {
   // device's rounds better: 16384 x 520 x 16384 took 1118 us with 192 and 1194
   // with 256, x 512 1076 and 921.  (128, two workgroups a CU, was never faster
   // than 192: dz is read once for every column of tiles.)
-  auto out_plan = [&](int64_t bn) {
-    auto slices = [&](int64_t rows, int64_t K, int64_t* s, int64_t* len) {
-      const int64_t tiles = cdiv(rows, Big::BM) * cdiv(a.d, bn);
-      *s = std::min(std::max<int64_t>(1, kCus / tiles), std::max<int64_t>(1, K / 512));
-      *len = cdiv(cdiv(K, *s), 64) * 64;
-      *s = cdiv(K, *len);
-      return cdiv(tiles * *s, kCus) * *len * (bn == Big::BN ? bn * 100 : bn * 112);
-    };
-    const int64_t nv = std::min(b.piece, a.V);
-    b.out = static_cast<int>(bn);
-    return slices(a.N, nv, &b.sx, &b.kx) + slices(nv, a.N, &b.sw, &b.kw);
-  };
-  if (out_plan(Wide::BN) < out_plan(Big::BN)) out_plan(Wide::BN);
+  const int64_t nv = std::min(b.piece, a.V);
+  const int terms = a.bf16 ? 1 : kTerms;
+  double best = -1;
+  for (int bn : {int(Big::BN), int(Wide::BN)}) {
+    double tx, tw;
+    const Cut x = cut_of(a.N, nv, a.d, terms, bn, &tx), w = cut_of(nv, a.N, a.d, terms, bn, &tw);
+    if (best >= 0 && tx + tw >= best) continue;
+    best = tx + tw;
+    b.out = bn, b.x = x, b.w = w;
+  }
+  auto sums = [&](int64_t rows, const Cut& c) { return up((size_t(c.head) + size_t(c.s) * (rows - c.head)) * a.d * 4); };
   b.coef_off = b.op.end;
   b.dz_off = b.coef_off + up(size_t(a.N) * sizeof(RowCoef));
   b.px_off = b.dz_off + up(size_t(a.N) * b.op.planes * b.ldz * 2);
-  b.pw_off = b.px_off + up(size_t(b.sx) * a.N * a.d * 4);
-  b.total = b.pw_off + (b.sw > 1 ? up(size_t(b.sw) * std::min(b.piece, a.V) * a.d * 4) : 0);
+  b.pw_off = b.px_off + sums(a.N, b.x);
+  b.total = b.pw_off + (b.w.s > 1 ? sums(nv, b.w) : 0);
   return b;
 }
 
@@ -900,19 +934,16 @@ void launch_loss_backward(const LossArgs& a, const void* x, const void* W, const
   float* pw = reinterpret_cast<float*>(a.ws + b.pw_off);
   const Operands o = lay_out(a, b.op, x, W, targets, lse, dloss, dlse, coef);
   LossUnits* const units = o.units;
-  auto out = [&](const float* P, int S, int64_t n, int is_w, void* to, int64_t at) {
+  auto out = [&](const float* P, int S, int64_t n, int is_w, void* to) {
     const unsigned grid = unsigned(cdiv(n, 256));
     if (a.bf16)
-      k_loss_out<true><<<grid, 256, 0, a.stream>>>(P, S, n, units, is_w, a.scale, static_cast<uint16_t*>(to) + at);
+      k_loss_out<true><<<grid, 256, 0, a.stream>>>(P, S, n, units, is_w, a.scale, static_cast<uint16_t*>(to));
     else
-      k_loss_out<false><<<grid, 256, 0, a.stream>>>(P, S, n, units, is_w, a.scale, static_cast<float*>(to) + at);
+      k_loss_out<false><<<grid, 256, 0, a.stream>>>(P, S, n, units, is_w, a.scale, static_cast<float*>(to));
   };
   // one tile shape and storage type of each kernel
   auto typed = [&](auto tl, auto run) {
     if (a.bf16) run(tl, std::true_type{}); else run(tl, std::false_type{});
-  };
-  auto product = [&](auto run) {
-    if (b.out == Big::BN) typed(Big{}, run); else typed(Wide{}, run);
   };
   const size_t elt = a.bf16 ? 2 : 4;
   for (int64_t v0 = 0; v0 < a.V; v0 += b.piece) {
@@ -928,26 +959,34 @@ void launch_loss_backward(const LossArgs& a, const void* x, const void* W, const
     };
     if (b.big_z) typed(Big{}, logits); else typed(Mid{}, logits);
     const MmOperand Z{dz, b.ldz, a.N * b.ldz};
-    if (dx)
-      product( [&](auto tl, auto bf) {
-        using Tl = decltype(tl);
-        const MmOperand Wc{o.Wh.base + v0 * o.Wh.ld, o.Wh.ld, o.Wh.plane};
-        const int64_t n_col = cdiv(a.d, Tl::BN);
-        k_loss_mm<Tl, false, decltype(bf)::value><<<unsigned(cdiv(a.N, Tl::BM) * n_col * b.sx), Tl::NTHR, 0, a.stream>>>(
-            Z, Wc, a.N, a.d, nv, b.kx, terms, int(n_col), int(b.sx), v0 > 0, px, last && b.sx == 1 ? dx : nullptr, units, a.scale);
-      });
-    if (dW) {
-      void* const dWc = static_cast<uint8_t*>(dW) + v0 * a.d * elt;
-      product( [&](auto tl, auto bf) {
-        using Tl = decltype(tl);
-        const int64_t n_col = cdiv(a.d, Tl::BN);
-        k_loss_mm<Tl, true, decltype(bf)::value><<<unsigned(cdiv(nv, Tl::BM) * n_col * b.sw), Tl::NTHR, 0, a.stream>>>(
-            Z, o.Xh, nv, a.d, a.N, b.kw, terms, int(n_col), int(b.sw), 0, pw, b.sw == 1 ? dWc : nullptr, units, a.scale);
-      });
-      if (b.sw > 1) out(pw, int(b.sw), nv * a.d, 1, dW, v0 * a.d);
+    // head rows, then the rest, of a product whose rows lie `step` apart in Z
+    auto product = [&](auto ta, const Cut& c, int64_t step, const MmOperand& B, int64_t rows, int64_t K, bool add, float* P,
+                       bool finish, void* to) {
+      constexpr bool TA = decltype(ta)::value;
+      auto part = [&](int64_t r0, int64_t n, int64_t s, int64_t len, float* sums) {
+        if (n <= 0) return;
+        MmOperand A = Z;
+        A.base += r0 * step;
+        uint8_t* const dst = static_cast<uint8_t*>(to) + size_t(r0) * a.d * elt;
+        auto run = [&](auto tl, auto bf) {
+          using Tl = decltype(tl);
+          const int64_t n_col = cdiv(a.d, Tl::BN);
+          k_loss_mm<Tl, TA, decltype(bf)::value><<<unsigned(cdiv(n, Tl::BM) * n_col * s), Tl::NTHR, 0, a.stream>>>(
+              A, B, n, a.d, K, len, terms, int(n_col), int(s), add, sums, finish && s == 1 ? dst : nullptr, units, a.scale);
+        };
+        if (b.out == Big::BN) typed(Big{}, run); else typed(Wide{}, run);
+        if (finish && s > 1) out(sums, int(s), n * a.d, TA, dst);
+      };
+      const int64_t head = std::min(c.head, rows);
+      part(0, head, 1, cdiv(K, 64) * 64, P);
+      part(head, rows - head, c.s, c.len, P + head * a.d);
+    };
+    if (dx) {
+      const MmOperand Wc{o.Wh.base + v0 * o.Wh.ld, o.Wh.ld, o.Wh.plane};
+      product(std::false_type{}, b.x, b.ldz, Wc, a.N, nv, v0 > 0, px, last, dx);
     }
+    if (dW) product(std::true_type{}, b.w, 1, o.Xh, nv, a.N, false, pw, true, static_cast<uint8_t*>(dW) + v0 * a.d * elt);
   }
-  if (dx && b.sx > 1) out(px, int(b.sx), a.N * a.d, 0, dx, 0);
 }
 
 }  // namespace prn

@@ -104,6 +104,12 @@ def test_several_pieces_of_the_vocabulary(dtype, N, V):
     _check(N, V, 16, dtype)
 
 
+@pytest.mark.parametrize("dtype,N,V", [("bf16", 1030, 66000), ("f32", 1030, 66000), ("bf16", 66000, 1030)])
+def test_rest_of_the_rounds_in_slices(dtype, N, V):
+    """258 row tiles: 256 over the whole sum, the sum of the last two in slices (of dW, or of dx)."""
+    _check(N, V, 16, dtype)
+
+
 def test_rows_without_a_loss_and_targets_out_of_range():
     x, W, t, dloss, dlse = _inputs(150, 300, 40, "f32", 1)
     t[:] = -100                                     # nothing to learn from
