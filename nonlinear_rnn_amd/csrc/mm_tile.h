@@ -170,7 +170,7 @@ struct MmTile {
   uint8_t* lds;
   MmOperand A, B;
   int64_t Ra, Rb, k0, k1;   // rows of the operands in all; the summed range (k0 a multiple of 8)
-  int terms, nk, nfull;
+  int terms, nk, nfull, ntail;   // stages of a term, full ones, the last one's blocks of 16 k
   uint32_t offa[NLA], offb[NLB];
   const uint8_t *a0, *b0, *ab, *bb;
   int at_k, at_t;           // the next stage to load
@@ -183,6 +183,7 @@ struct MmTile {
     lds = lds_, A = A_, B = B_, Ra = Ra_, Rb = Rb_, k0 = k0_, k1 = k1_, terms = terms_;
     nk = k1 > k0 ? static_cast<int>((k1 - k0 + BK - 1) / BK) : 0;
     nfull = k1 > k0 ? static_cast<int>((k1 - k0) / BK) : 0;
+    ntail = nk > 0 ? static_cast<int>((k1 - k0 - static_cast<int64_t>(nk - 1) * BK + 15) / 16) : 0;
     more = false;
     ahead = buf_load = buf_use = 0;
   }
@@ -347,8 +348,10 @@ struct MmTile {
         for (int j = 0; j < WN; ++j) acc[i][j] = mm_product<F16>(av[set][i], bv[set][j], acc[i][j]);
     };
     // a stage whose first fragments are in set 0; but after the last one, the
-    // next stage's are on their way there while the last products run
+    // next stage's are on their way there while the last products run.  The
+    // last one stops at its blocks of 16 k (the rest are zeros).
     auto stage = [&](bool first, auto last) {
+      constexpr bool LAST = decltype(last)::value;
       fragments(1, av[1], bv[1]);
       if (first) {   // a tile's first products start from zero (cheaper than clearing acc)
         const mm_f32x16 zero = {};
@@ -361,15 +364,16 @@ struct MmTile {
       }
 #pragma unroll
       for (int kb = 1; kb < KB; ++kb) {
+        if (LAST && kb >= ntail) break;
         if (kb + 1 < KB) {
           fragments(kb + 1, av[(kb + 1) & 1], bv[(kb + 1) & 1]);
-        } else if (!decltype(last)::value) {
+        } else if (!LAST) {
           __builtin_amdgcn_sched_barrier(0);
           arrive(false);
           fragments(0, av[0], bv[0]);
         }
         products(kb & 1);
-        in_order(kb + 1 < KB || !decltype(last)::value);
+        in_order(kb + 1 < KB || !LAST);
       }
     };
     arrive(stored);
