@@ -97,24 +97,28 @@ __device__ __forceinline__ mm_f32x16 mm_product(mm_bf16x8 a, mm_bf16x8 b, mm_f32
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
-// An operand: 16-bit matrices `plane` elements apart (one, or the two terms of
-// fp32 data), rows ld elements apart, ld a multiple of 8, base 16-byte
-// aligned.  Along its contiguous index the memory holds a multiple of 8 values
-// per row (the ones past the extent are zeros where that index is k, anything
-// otherwise).
+// An operand: a 16-bit matrix, rows ld elements apart, ld a multiple of 8, base
+// 16-byte aligned.  Along its contiguous index the memory holds a multiple of 8
+// values per row (the ones past the extent are zeros where that index is k,
+// anything otherwise).  Of two-term data (PAIR) every 32 values along that
+// index are 64: the 32 high terms, then the 32 low ones.
 struct MmOperand {
   const uint16_t* base;
-  int64_t ld, plane;
+  int64_t ld;
 };
 
-// the term pairs of a product of two-term operands: the low terms' own
-// product is left out
-__device__ __forceinline__ int mm_term_a(int t) { return t >> 1; }   // 0 0 1
-__device__ __forceinline__ int mm_term_b(int t) { return t & 1; }    // 0 1 0
-
-template <int WR_, int WC_, int WM_, int WN_, int BK_, int NST_>
+// PAIR: two-term operands.  A stage holds both terms of BK / 2 = 32 values of
+// k, the high ones in the first half of its k places; the product takes high
+// high, high low and low high (the low terms' own product is left out).  Every
+// term is loaded and read once for its two products, where a pass per pair of
+// terms loads and reads half as much again (4096 x 256 x 32000, each way: 955
+// us; this takes 855).
+template <int WR_, int WC_, int WM_, int WN_, int BK_, int NST_, bool PAIR_ = false>
 struct MmTile {
   static constexpr int WR = WR_, WC = WC_, WM = WM_, WN = WN_, BK = BK_, NST = NST_;
+  static constexpr bool PAIR = PAIR_;
+  static constexpr int KS = PAIR ? BK / 2 : BK;   // k of a stage
+  static_assert(!PAIR || BK == 64, "32 and 32");
   static constexpr int NW = WR * WC, NTHR = 64 * NW;
   static constexpr int BM = WR * WM * 32, BN = WC * WN * 32;
   static constexpr int ABYTES = BM * BK * 2, BBYTES = BN * BK * 2, STAGE = ABYTES + BBYTES;
@@ -164,26 +168,26 @@ struct MmTile {
     }
   }
 
-  // The stream of stages: tile after tile, each k0 .. k1 for every term pair.
+  // The stream of stages: tile after tile, each k0 .. k1.
   // The loads run NST - 1 stages ahead of the products, across tiles too, so
   // that the next tile's first stages are in flight during an epilogue.
   uint8_t* lds;
   MmOperand A, B;
-  int64_t Ra, Rb, k0, k1;   // rows of the operands in all; the summed range (k0 a multiple of 8)
-  int terms, nk, nfull, ntail;   // stages of a term, full ones, the last one's blocks of 16 k
+  int64_t Ra, Rb, k0, k1;   // rows of the operands in all; the summed range (k0 a multiple of 8, PAIR: 32)
+  int nk, nfull, ntail;     // stages, full ones, the last one's blocks of 16 k
   uint32_t offa[NLA], offb[NLB];
-  const uint8_t *a0, *b0, *ab, *bb;
-  int at_k, at_t;           // the next stage to load
+  const uint8_t *ab, *bb;
+  int at_k;                 // the next stage to load
   bool more;                // there is one
   int ahead;                // stages loaded and not yet multiplied
   int buf_load, buf_use;
 
   __device__ __forceinline__ void open(uint8_t* lds_, const MmOperand& A_, int64_t Ra_, const MmOperand& B_, int64_t Rb_,
-                                       int64_t k0_, int64_t k1_, int terms_) {
-    lds = lds_, A = A_, B = B_, Ra = Ra_, Rb = Rb_, k0 = k0_, k1 = k1_, terms = terms_;
-    nk = k1 > k0 ? static_cast<int>((k1 - k0 + BK - 1) / BK) : 0;
-    nfull = k1 > k0 ? static_cast<int>((k1 - k0) / BK) : 0;
-    ntail = nk > 0 ? static_cast<int>((k1 - k0 - static_cast<int64_t>(nk - 1) * BK + 15) / 16) : 0;
+                                       int64_t k0_, int64_t k1_) {
+    lds = lds_, A = A_, B = B_, Ra = Ra_, Rb = Rb_, k0 = k0_, k1 = k1_;
+    nk = k1 > k0 ? static_cast<int>((k1 - k0 + KS - 1) / KS) : 0;
+    nfull = k1 > k0 ? static_cast<int>((k1 - k0) / KS) : 0;
+    ntail = nk > 0 ? static_cast<int>((k1 - k0 - static_cast<int64_t>(nk - 1) * KS + 15) / 16) : 0;
     more = false;
     ahead = buf_load = buf_use = 0;
   }
@@ -194,9 +198,10 @@ struct MmTile {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     offsets<TA, BM, NLA>(wave, lane, A.ld, Ra, r0, offa);
     offsets<TB, BN, NLB>(wave, lane, B.ld, Rb, c0, offb);
-    a0 = ab = reinterpret_cast<const uint8_t*>(A.base + (TA ? k0 * A.ld + r0 : r0 * A.ld + k0));
-    b0 = bb = reinterpret_cast<const uint8_t*>(B.base + (TB ? k0 * B.ld + c0 : c0 * B.ld + k0));
-    at_k = at_t = 0;
+    constexpr int F = PAIR ? 2 : 1;
+    ab = reinterpret_cast<const uint8_t*>(A.base + (TA ? k0 * A.ld + F * r0 : r0 * A.ld + F * k0));
+    bb = reinterpret_cast<const uint8_t*>(B.base + (TB ? k0 * B.ld + F * c0 : c0 * B.ld + F * k0));
+    at_k = 0;
     more = nk > 0;
   }
 
@@ -212,15 +217,19 @@ struct MmTile {
       int s, f;
       source<COLS, BR>(wave * NL + p, lane, s, f);
       if constexpr (COLS) f = f < lim ? f : lim; else s = s < lim ? s : lim;
+      if constexpr (COLS && PAIR) {
+        f = 2 * (f & ~31) + (f & 31) + 32 * (s / KS);
+        s %= KS;
+      }
       off[p] = static_cast<uint32_t>((s * ld + f) * 2);
     }
   }
-  // One operand's loads of a stage.  In the last, partial stage (left < BK
+  // One operand's loads of a stage.  In the last, partial stage (left < KS
   // values of k) the chunks past the end come from the zero chunk.
   template <bool COLS, int BR, int NL>
   static __device__ __forceinline__ void load_operand(const uint8_t* base, const uint32_t (&off)[NL], uint8_t* dst, int wave,
                                                       int left) {
-    if (left >= BK) {
+    if (left >= KS) {
 #pragma unroll
       for (int p = 0; p < NL; ++p) mm_dma_off(mm_uniform(base), off[p], mm_lds_addr(dst + p * 1024));
     } else {
@@ -229,7 +238,7 @@ struct MmTile {
       for (int p = 0; p < NL; ++p) {
         int s, f;
         source<COLS, BR>(wave * NL + p, lane, s, f);
-        const void* g = (COLS ? s : f) < left ? static_cast<const void*>(base + off[p]) : static_cast<const void*>(kMmZero);
+        const void* g = (COLS ? s : f) % KS < left ? static_cast<const void*>(base + off[p]) : static_cast<const void*>(kMmZero);
         mm_dma(g, mm_lds_addr(dst + p * 1024));
       }
     }
@@ -240,22 +249,16 @@ struct MmTile {
   __device__ __forceinline__ void load(Next&& next) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     uint8_t* const dst = lds + buf_load * STAGE;
-    const int left = at_k < nfull ? BK : static_cast<int>(k1 - k0) - at_k * BK;
+    const int left = at_k < nfull ? KS : static_cast<int>(k1 - k0) - at_k * KS;
     load_operand<TA, BM, NLA>(ab, offa, dst + wave * NLA * 1024, wave, left);
     load_operand<TB, BN, NLB>(bb, offb, dst + ABYTES + wave * NLB * 1024, wave, left);
     buf_load = buf_load + 1 == NST ? 0 : buf_load + 1;
     ++ahead;
-    ab += 2 * BK * (TA ? A.ld : 1);
-    bb += 2 * BK * (TB ? B.ld : 1);
+    ab += TA ? 2 * KS * A.ld : 2 * BK;
+    bb += TB ? 2 * KS * B.ld : 2 * BK;
     if (++at_k == nk) {
-      at_k = 0;
-      ++at_t;
-      ab = a0 + 2 * A.plane * mm_term_a(at_t);
-      bb = b0 + 2 * B.plane * mm_term_b(at_t);
-      if (at_t == terms) {
-        more = false;
-        next();
-      }
+      more = false;
+      next();
     }
   }
 
@@ -297,7 +300,7 @@ struct MmTile {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wr = wave / WC, wc = wave % WC;
     constexpr int KB = BK / 16;
     static_assert(KB % 2 == 0, "two sets of fragments in turn");
-    const int stages = nk * terms;
+    const int stages = nk;
     if (stages == 0) return;
     const uint8_t* sa;
     // the next stage has landed, and every wave is done with the buffer that
@@ -318,41 +321,44 @@ struct MmTile {
       buf_use = buf_use + 1 == NST ? 0 : buf_use + 1;
     };
     mm_bf16x8 av[2][WM], bv[2][WN];
-    auto fragments = [&](int kb, mm_bf16x8 (&a)[WM], mm_bf16x8 (&b)[WN]) {
-      const uint8_t* sb = sa + ABYTES;
-#pragma unroll
-      for (int j = 0; j < WN; ++j) {
-        const int at = (wc * WN + j) * 32;
-        if constexpr (TB) b[j] = frag_cols<2 * BN>(sb, at, kb); else b[j] = frag_rows(sb, at, kb);
-      }
+    auto fragments_a = [&](int kb, mm_bf16x8 (&a)[WM]) {
 #pragma unroll
       for (int i = 0; i < WM; ++i) {
         const int at = (wr * WM + i) * 32;
         if constexpr (TA) a[i] = frag_cols<2 * BM>(sa, at, kb); else a[i] = frag_rows(sa, at, kb);
       }
     };
+    auto fragments_b = [&](int kb, mm_bf16x8 (&b)[WN]) {
+      const uint8_t* sb = sa + ABYTES;
+#pragma unroll
+      for (int j = 0; j < WN; ++j) {
+        const int at = (wc * WN + j) * 32;
+        if constexpr (TB) b[j] = frag_cols<2 * BN>(sb, at, kb); else b[j] = frag_rows(sb, at, kb);
+      }
+    };
+    constexpr int kReadsA = WM * (TA ? 2 : 1), kReadsB = WN * (TB ? 2 : 1);
     // every product with a share of the next fragments behind it (left to
     // itself the compiler reads each fragment just before its use)
-    auto in_order = [&](int reads) {
-      constexpr int kReads = WM * (TA ? 2 : 1) + WN * (TB ? 2 : 1), kProducts = WM * WN, kMost = (kReads + kProducts - 1) / kProducts;
+    auto in_order = [&](auto n) {
+      constexpr int kReads = decltype(n)::value, kProducts = WM * WN, kMost = (kReads + kProducts - 1) / kProducts;
 #pragma unroll
       for (int m = 0; m < kProducts; ++m) {
         __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
-        if (reads && (m + 1) * kReads / kProducts > m * kReads / kProducts) __builtin_amdgcn_sched_group_barrier(0x100, kMost, 0);
+        if (kReads > 0 && (m + 1) * kReads / kProducts > m * kReads / kProducts)
+          __builtin_amdgcn_sched_group_barrier(0x100, kMost, 0);
       }
     };
-    auto products = [&](int set) {
+    using None = std::integral_constant<int, 0>;
+    using OfA = std::integral_constant<int, kReadsA>;
+    using OfB = std::integral_constant<int, kReadsB>;
+    using Both = std::integral_constant<int, kReadsA + kReadsB>;
+    auto products = [&](int sa_, int sb_) {
 #pragma unroll
       for (int i = 0; i < WM; ++i)
 #pragma unroll
-        for (int j = 0; j < WN; ++j) acc[i][j] = mm_product<F16>(av[set][i], bv[set][j], acc[i][j]);
+        for (int j = 0; j < WN; ++j) acc[i][j] = mm_product<F16>(av[sa_][i], bv[sb_][j], acc[i][j]);
     };
-    // a stage whose first fragments are in set 0; but after the last one, the
-    // next stage's are on their way there while the last products run.  The
-    // last one stops at its blocks of 16 k (the rest are zeros).
-    auto stage = [&](bool first, auto last) {
-      constexpr bool LAST = decltype(last)::value;
-      fragments(1, av[1], bv[1]);
+    auto first_products = [&](bool first) {
       if (first) {   // a tile's first products start from zero (cheaper than clearing acc)
         const mm_f32x16 zero = {};
 #pragma unroll
@@ -360,24 +366,65 @@ struct MmTile {
 #pragma unroll
           for (int j = 0; j < WN; ++j) acc[i][j] = mm_product<F16>(av[0][i], bv[0][j], zero);
       } else {
-        products(0);
+        products(0, 0);
       }
-#pragma unroll
-      for (int kb = 1; kb < KB; ++kb) {
-        if (LAST && kb >= ntail) break;
-        if (kb + 1 < KB) {
-          fragments(kb + 1, av[(kb + 1) & 1], bv[(kb + 1) & 1]);
-        } else if (!LAST) {
-          __builtin_amdgcn_sched_barrier(0);
-          arrive(false);
-          fragments(0, av[0], bv[0]);
+    };
+    auto next_stage = [&]() {
+      __builtin_amdgcn_sched_barrier(0);
+      arrive(false);
+      fragments_a(0, av[0]);
+      fragments_b(0, bv[0]);
+    };
+    // a stage whose first fragments are in sets 0; but after the last one, the
+    // next stage's are on their way there while the last products run.  The
+    // last one stops at its blocks of 16 k (the rest are zeros).
+    auto stage = [&](bool first, auto last) {
+      constexpr bool LAST = decltype(last)::value;
+      if constexpr (PAIR) {
+        fragments_b(2, bv[1]);
+        first_products(first);   // high high, k 0 .. 15
+        fragments_a(2, av[1]);
+        products(0, 1);          // high low
+        in_order(OfA{});
+        const bool more_k = !LAST || ntail > 1;
+        if (more_k) {
+          fragments_a(1, av[0]);
+          fragments_b(1, bv[1]);
         }
-        products(kb & 1);
-        in_order(kb + 1 < KB || !LAST);
+        products(1, 0);          // low high
+        if (!LAST) in_order(Both{});
+        if (more_k) {            // k 16 .. 31
+          fragments_b(3, bv[0]);
+          products(0, 1);
+          in_order(OfB{});
+          fragments_a(3, av[1]);
+          products(0, 0);
+          in_order(OfA{});
+          if constexpr (!LAST) next_stage();
+          products(1, 1);
+          in_order(std::conditional_t<LAST, None, Both>{});
+        }
+      } else {
+        fragments_a(1, av[1]);
+        fragments_b(1, bv[1]);
+        first_products(first);
+#pragma unroll
+        for (int kb = 1; kb < KB; ++kb) {
+          if (LAST && kb >= ntail) break;
+          if (kb + 1 < KB) {
+            fragments_a(kb + 1, av[(kb + 1) & 1]);
+            fragments_b(kb + 1, bv[(kb + 1) & 1]);
+          } else if constexpr (!LAST) {
+            next_stage();
+          }
+          products(kb & 1, kb & 1);
+          if (kb + 1 < KB || !LAST) in_order(Both{}); else in_order(None{});
+        }
       }
     };
     arrive(stored);
-    fragments(0, av[0], bv[0]);
+    fragments_a(0, av[0]);
+    fragments_b(0, bv[0]);
     for (int st = 0; st + 1 < stages; ++st) stage(!ADD && st == 0, std::false_type{});
     stage(!ADD && stages == 1, std::true_type{});
     __builtin_amdgcn_sched_barrier(0);   // an epilogue begins after the products: mixed with them it spills

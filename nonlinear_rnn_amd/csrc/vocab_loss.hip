@@ -26,7 +26,7 @@
 // products each (lo lo, below 2^-22, is left out).  That is four fp32
 // roundings a product, below what the fp32 sums over them make; the exact
 // three-term bf16 split (bf16split.h) took twice the products and 1.74 ms
-// where this takes 1.0 (4096 x 256 x 32000).
+// where this takes 0.855 (4096 x 256 x 32000).
 // For fp16's range a call's x and W are scaled by the power of two that takes
 // their largest value to 2^14 .. 2^15 (values below 2^-17 of that lose the low
 // bits of lo: at most 2^-40 of the largest value), and dz, in units of the
@@ -46,13 +46,19 @@ namespace {
 constexpr int kTerms = 3;   // products of two-term operands
 
 // 8 waves, 256 x 256, 128 KB: the least traffic per product; one workgroup a CU
-using Big = MmTile<2, 4, 4, 2, 64, 2>;
-// 4 waves, 256 x 128, 72 KB, two workgroups a CU: for the logits of few tokens
-using Mid = MmTile<2, 2, 4, 2, 32, 3>;
+template <bool PAIR> using Big = MmTile<2, 4, 4, 2, 64, 2, PAIR>;
+// 256 x 128 for the logits of few tokens: bf16 data 4 waves, 72 KB, two
+// workgroups a CU; fp32 data 8 waves, 96 KB
+template <bool PAIR>
+using Mid = std::conditional_t<PAIR, MmTile<4, 2, 2, 2, 64, 2, true>, MmTile<2, 2, 4, 2, 32, 3, false>>;
 // 8 waves, 256 x 192, 112 KB: for dx and dW where 256 columns a tile would be wider than the rows
-using Wide = MmTile<4, 2, 2, 3, 64, 2>;
+template <bool PAIR> using Wide = MmTile<4, 2, 2, 3, 64, 2, PAIR>;
 // few tokens: 128 x 64
-using Few = MmTile<4, 1, 1, 2, 64, 3>;
+template <bool PAIR> using Few = MmTile<4, 1, 1, 2, 64, 3, PAIR>;
+// tiles' extents, and workgroups of Mid on a CU
+constexpr int64_t kBM = Big<false>::BM, kBig = Big<false>::BN, kMid = Mid<false>::BN, kWide = Wide<false>::BN;
+constexpr int64_t kFewM = Few<false>::BM, kFewN = Few<false>::BN;
+int64_t mid_slots(bool bf16) { return bf16 ? 2 : 1; }
 constexpr int kXcd = 8;
 
 // Workgroups are dealt round-robin to the XCDs.  The units of work of this
@@ -201,8 +207,8 @@ struct RowCoef {
 };
 
 // Workgroups [0, nc): the tokens' coefficients; then n1 that lay out x and the
-// rest W in fp16 terms (BF16: one, else two, R ldp apart), rows of ldp values,
-// zeros past d.  The first writes the units.
+// rest W in fp16 terms, rows of ldp values (fp32 data: 2 ldp, every 32 high
+// terms and their 32 low ones), zeros past d.  The first writes the units.
 template <bool BF16>
 __global__ void __launch_bounds__(256) k_loss_layout(const float* __restrict__ dloss, const float* __restrict__ dlse,
                                                      const float* __restrict__ lse, const void* __restrict__ targets,
@@ -271,9 +277,14 @@ __global__ void __launch_bounds__(256) k_loss_layout(const float* __restrict__ d
     hi[e] = static_cast<_Float16>(s);
     lo[e] = static_cast<_Float16>(s - static_cast<float>(hi[e]));
   }
-  uint16_t* const out = (is_x ? xh : wh) + r * ldp + c0;
-  *reinterpret_cast<mm_f16x8*>(out) = hi;
-  if constexpr (!BF16) *reinterpret_cast<mm_f16x8*>(out + R * ldp) = lo;
+  uint16_t* const to = is_x ? xh : wh;
+  if constexpr (BF16) {
+    *reinterpret_cast<mm_f16x8*>(to + r * ldp + c0) = hi;
+  } else {
+    uint16_t* const out = to + 2 * (r * ldp + (c0 & ~int64_t(31))) + (c0 & 31);
+    *reinterpret_cast<mm_f16x8*>(out) = hi;
+    *reinterpret_cast<mm_f16x8*>(out + 32) = lo;
+  }
 }
 
 // ------------------------------------------------------------- forward ---
@@ -285,8 +296,7 @@ __global__ void __launch_bounds__(256) k_loss_layout(const float* __restrict__ d
 // neighbours, so that an XCD's workgroups share the W tiles they walk.
 template <class Tl, bool F16>
 __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_lse(MmOperand W, MmOperand X, int64_t N, int64_t V, int64_t d,
-                                                          int terms, float c, const LossUnits* __restrict__ units,
-                                                          int n_tok, int splits, int per_split,
+                                                          float c, const LossUnits* __restrict__ units, int n_tok, int splits, int per_split,
                                                           float2* __restrict__ part) {
   if constexpr (F16) c *= units->back_z;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Tl::LDS];
@@ -296,7 +306,7 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_lse(MmOperand W, MmOperand
   const int wr = wave / Tl::WC, wc = wave % Tl::WC;
   const uint32_t v_tiles = static_cast<uint32_t>((V + Tl::BM - 1) / Tl::BM);
   Tl tile;
-  tile.open(lds, W, V, X, N, 0, d, terms);
+  tile.open(lds, W, V, X, N, 0, d);
   // the loads' place: unit, vocabulary tile
   Units lu(static_cast<uint32_t>(n_tok) * splits), cu(lu);
   uint32_t lt = 0, lt1 = 0, ltok = 0;
@@ -453,10 +463,10 @@ __global__ void __launch_bounds__(256) k_loss_join(const float2* __restrict__ pa
 // ------------------------------------------------------------ backward ---
 
 // dz (in units of its call) of the vocabulary tiles of a piece (first entry piece0, rows to be
-// written up to piece1), stored by token rows (ldz apart; planes N ldz
-// apart).  A lane holds four neighbouring entries of its token at a time and
-// the other half of the wave the next four: a swap of the halves makes them
-// eight, 16 bytes a store, and a swap of the halves' halves puts 64 bytes of
+// written up to piece1), stored by token rows ldz apart (fp32 data:
+// every 32 high terms and their 32 low ones).  A lane holds four neighbouring
+// entries of its token at a time and the other half of the wave the next four:
+// a swap of the halves makes them eight, 16 bytes a store, and a swap of the halves' halves puts 64 bytes of
 // 16 tokens into one store of the wave (32 bytes of 32 tokens: 377 us for
 // 32768 x 512 x 8192 instead of 366).  dz is as large as the last-level cache
 // or larger, so the stores leave W and x in the caches: 354 us, and the dx
@@ -464,7 +474,7 @@ __global__ void __launch_bounds__(256) k_loss_join(const float2* __restrict__ pa
 // products alone 245.
 template <class Tl, bool BF16>
 __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_dz(MmOperand W, MmOperand X, int64_t N, int64_t V, int64_t d,
-                                                         int terms, float c, const LossUnits* __restrict__ units,
+                                                         float c, const LossUnits* __restrict__ units,
                                                          int64_t piece0, int64_t piece1, int n_tok,
                                                          const RowCoef* __restrict__ coef, uint16_t* __restrict__ dz,
                                                          int64_t ldz) {
@@ -480,7 +490,7 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_dz(MmOperand W, MmOperand 
   const uint32_t v_tiles = static_cast<uint32_t>((piece1 - piece0 + Tl::BM - 1) / Tl::BM);
   constexpr uint32_t kGroup = 8;   // vocabulary tiles that an XCD's workgroups share
   Tl tile;
-  tile.open(lds, W, V, X, N, 0, d, terms);
+  tile.open(lds, W, V, X, N, 0, d);
   Units lu(v_tiles * n_tok), cu(lu);
   int fill = 0;   // the tokens' coefficients come with the tile's first stage
   auto go_to = [&]() {
@@ -499,14 +509,15 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_dz(MmOperand W, MmOperand 
   if (!lu.valid()) return;
   go_to();
   tile.template prime<false, false>(next);
-  constexpr int kStores = std::min(63, Tl::WM * Tl::WN * (BF16 ? 2 : 4));   // of a wave and whole tile
+  constexpr int TERMS = BF16 ? 1 : 2;
+  constexpr int kStores = std::min(63, Tl::WM * Tl::WN * 2 * TERMS);   // of a wave and whole tile
   bool whole = false;   // the tile before was
   for (int use = 0; cu.valid(); cu.advance(), use = use + 1 == kRing ? 0 : use + 1) {
     uint32_t vt, tok;
     tile_of(cu.u, v_tiles, n_tok, kGroup, vt, tok);
     const int64_t v0 = piece0 + static_cast<int64_t>(vt) * Tl::BM, n0 = static_cast<int64_t>(tok) * Tl::BN;
     tile.template multiply<false, false, false, true, kStores>(next, whole);
-    uint8_t* const base = reinterpret_cast<uint8_t*>(dz + n0 * ldz + (v0 - piece0));
+    uint8_t* const base = reinterpret_cast<uint8_t*>(dz + n0 * ldz + TERMS * (v0 - piece0));
     const int rows = static_cast<int>(imin(piece1 - v0, Tl::BM)), toks = static_cast<int>(imin(N - n0, Tl::BN));
     const int vocab_left = static_cast<int>(imin(V - v0, Tl::BM));
     whole = vocab_left == Tl::BM && toks == Tl::BN;
@@ -550,7 +561,7 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_dz(MmOperand W, MmOperand 
               if (vb + 4 * eh + 8 * (r >> 2) + (r & 3) >= vocab_left) v[r] = 0.0f;
           }
 #pragma unroll
-          for (int t = 0; t < (BF16 ? 1 : 2); ++t) {
+          for (int t = 0; t < TERMS; ++t) {
             uint32_t w[4][2];
 #pragma unroll
             for (int q = 0; q < 4; ++q)
@@ -581,7 +592,7 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_dz(MmOperand W, MmOperand 
             for (int k = 0; k < 2; ++k)
               if (!EDGE || (tb + 16 * k < toks && vb + eb < rows))
                 __builtin_nontemporal_store(
-                    o[k], reinterpret_cast<mm_u32x4*>(base + t * (2 * N * ldz) + (at_row + 16 * k * ld2 + 2 * vb)));
+                    o[k], reinterpret_cast<mm_u32x4*>(base + (at_row + 16 * k * ld2 + 2 * TERMS * vb + 64 * t)));
           }
         }
       }
@@ -595,7 +606,7 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_dz(MmOperand W, MmOperand 
 // One workgroup per tile and slice, neighbours on one XCD.
 template <class Tl, bool TA, bool BF16>
 __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_mm(MmOperand A, MmOperand B, int64_t R, int64_t C, int64_t K,
-                                                         int64_t k_slice, int terms, int n_col, int slices, int add,
+                                                         int64_t k_slice, int n_col, int slices, int add,
                                                          float* __restrict__ P, void* __restrict__ out,
                                                          const LossUnits* __restrict__ units, float scale) {
   using T = typename Storage<BF16 ? kBF16 : kF32>::T;
@@ -607,7 +618,7 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_mm(MmOperand A, MmOperand 
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wr = wave / Tl::WC, wc = wave % Tl::WC;
   Tl tile;
-  tile.open(lds, A, R, B, C, k0, k1, terms);
+  tile.open(lds, A, R, B, C, k0, k1);
   auto next = []() {};
   tile.template seek<TA, true>(r0, c0);
   tile.template prime<TA, true>(next);
@@ -692,7 +703,8 @@ struct Plan {
 // forward call of 5003 x 1001 x 50021 took 587 us with rows of 2016 bytes and
 // takes 534).  bf16 rows of a multiple of 8 are read where they are: at
 // 5003 x 520 x 50021 the copy costs what it gains, 323 us to 318.
-int64_t row_of(int64_t d) {
+int64_t row_of(int64_t d, bool pair) {
+  if (pair) return cdiv(d, 32) * 32;   // of both terms
   for (int64_t n = 8; n < 64; n *= 2)
     if (d <= n) return n;
   return cdiv(d, 64) * 64;
@@ -702,7 +714,7 @@ Plan plan_operands(const LossArgs& a, bool back) {
   p.planes = a.bf16 ? 1 : 2;
   const bool terms = back || !a.bf16;
   p.pad = !terms && a.d % 8 != 0;
-  p.ldp = row_of(a.d);
+  p.ldp = row_of(a.d, !a.bf16);
   size_t off = 0;
   auto take = [&](bool on, size_t bytes) {
     const size_t at = off;
@@ -721,7 +733,7 @@ Plan plan_operands(const LossArgs& a, bool back) {
 // The logits' tile: Mid takes about 1.15 times Big's time per product (32768 x
 // 512 x 8192: dz 395 and 360 us), which pays where 256 tokens a tile would
 // waste more.
-bool take_big(int64_t cols) { return cdiv(cols, Big::BN) * Big::BN * 100 <= cdiv(cols, Mid::BN) * Mid::BN * 115; }
+bool take_big(int64_t cols) { return cdiv(cols, kBig) * kBig * 100 <= cdiv(cols, kMid) * kMid * 115; }
 
 struct PlanFw {
   Plan op;
@@ -732,10 +744,10 @@ struct PlanFw {
 PlanFw plan_fw(const LossArgs& a) {
   PlanFw f{};
   f.op = plan_operands(a, false);
-  f.kind = a.N <= Few::BN ? 0 : take_big(a.N) ? 2 : 1;
-  const int64_t bm = f.kind == 0 ? Few::BM : Big::BM, bn = f.kind == 0 ? Few::BN : f.kind == 1 ? Mid::BN : Big::BN;
+  f.kind = a.N <= kFewN ? 0 : take_big(a.N) ? 2 : 1;
+  const int64_t bm = f.kind == 0 ? kFewM : kBM, bn = f.kind == 0 ? kFewN : f.kind == 1 ? kMid : kBig;
   f.n_tok = cdiv(a.N, bn);
-  const int64_t v_tiles = cdiv(a.V, bm), slots = (f.kind == 2 ? 1 : 2) * kCus;
+  const int64_t v_tiles = cdiv(a.V, bm), slots = (f.kind == 2 ? 1 : f.kind == 1 ? mid_slots(a.bf16) : 2) * kCus;
   // the number of splits whose longest workgroup has the fewest tiles, among
   // a few and the ones that fill whole rounds of the device
   int64_t best = -1;
@@ -770,14 +782,14 @@ Cut cut_of(int64_t rows, int64_t K, int64_t d, int terms, int64_t bn, double* us
   // their power (16384 x 520 x 16384 with dx's 192 tiles in four slices of the
   // sum took 1093 us, in one 1066; 5003 x 520 x 50021 without the rest's slices
   // 1056, with them 1016)
-  auto tile = [&](int64_t k) { return double(k) * terms * Big::BM * bn * (bn == Big::BN ? 1.0 : 1.12) * 2 / 4.1e6; };
+  auto tile = [&](int64_t k) { return double(k) * terms * kBM * bn * (bn == kBig ? 1.0 : 1.12) * 2 / 4.1e6; };
   auto join = [&](int64_t n, int64_t s) { return s > 1 ? 4 + double(s) * n * d * 8 * 1.5 / 4e6 : 0.0; };
-  const int64_t n_col = cdiv(d, bn), blocks = cdiv(rows, Big::BM), whole = blocks * n_col / kCus * kCus;
+  const int64_t n_col = cdiv(d, bn), blocks = cdiv(rows, kBM), whole = blocks * n_col / kCus * kCus;
   Cut best{};
   *us = -1;
-  for (int64_t head = 0;; head = std::min(whole / n_col * Big::BM, rows)) {
-    const int64_t rest = rows - head, tiles = cdiv(rest, Big::BM) * n_col;
-    const double first = cdiv(cdiv(head, Big::BM) * n_col, kCus) * tile(K) + (head > 0 && rest > 0 ? 3 : 0);
+  for (int64_t head = 0;; head = std::min(whole / n_col * kBM, rows)) {
+    const int64_t rest = rows - head, tiles = cdiv(rest, kBM) * n_col;
+    const double first = cdiv(cdiv(head, kBM) * n_col, kCus) * tile(K) + (head > 0 && rest > 0 ? 3 : 0);
     for (int64_t want : {int64_t(1), int64_t(2), int64_t(3), int64_t(4), int64_t(6), int64_t(8), tiles ? std::min(kCus / tiles, K / 512) : 1}) {
       if (want < 1 || (want > 1 && K / want < 512)) continue;
       const int64_t len = cdiv(cdiv(K, want), 64) * 64, n = cdiv(K, len);
@@ -795,7 +807,7 @@ Cut cut_of(int64_t rows, int64_t K, int64_t d, int terms, int64_t bn, double* us
 struct PlanBw {
   Plan op;
   bool big_z;               // tile of the logits
-  int out;                  // tile columns of dx and dW
+  int64_t out;              // tile columns of dx and dW
   int64_t piece, ldz;
   Cut x, w;                 // of dx's sum (over the piece), and dW's (over the tokens)
   size_t coef_off, dz_off, px_off, pw_off, total;
@@ -804,13 +816,13 @@ PlanBw plan_bw(const LossArgs& a) {
   PlanBw b{};
   b.op = plan_operands(a, true);
   b.big_z = take_big(a.N);
-  const int64_t v_tiles = cdiv(a.V, Big::BM);
-  const size_t row = size_t(a.N) * b.op.planes * 2 * Big::BM;
+  const int64_t v_tiles = cdiv(a.V, kBM);
+  const size_t row = size_t(a.N) * b.op.planes * 2 * kBM;
   int64_t per = std::max<int64_t>(1, int64_t(kPieceBytes / row));
   per = cdiv(v_tiles, cdiv(v_tiles, per));
-  b.piece = per * Big::BM;
+  b.piece = per * kBM;
   // rows of dz are no power of two apart: they would fall on few memory channels
-  b.ldz = b.piece + 64;
+  b.ldz = b.op.planes * b.piece + 64;
   // the products' tile: the shorter of the two plans.  256 columns a tile are
   // faster than 192 per column, those waste less at the edge and may fill the
   // device's rounds better: 16384 x 520 x 16384 took 1118 us with 192 and 1194
@@ -819,7 +831,7 @@ PlanBw plan_bw(const LossArgs& a) {
   const int64_t nv = std::min(b.piece, a.V);
   const int terms = a.bf16 ? 1 : kTerms;
   double best = -1;
-  for (int bn : {int(Big::BN), int(Wide::BN)}) {
+  for (int64_t bn : {kBig, kWide}) {
     double tx, tw;
     const Cut x = cut_of(a.N, nv, a.d, terms, bn, &tx), w = cut_of(nv, a.N, a.d, terms, bn, &tw);
     if (best >= 0 && tx + tw >= best) continue;
@@ -829,7 +841,7 @@ PlanBw plan_bw(const LossArgs& a) {
   auto sums = [&](int64_t rows, const Cut& c) { return up((size_t(c.head) + size_t(c.s) * (rows - c.head)) * a.d * 4); };
   b.coef_off = b.op.end;
   b.dz_off = b.coef_off + up(size_t(a.N) * sizeof(RowCoef));
-  b.px_off = b.dz_off + up(size_t(a.N) * b.op.planes * b.ldz * 2);
+  b.px_off = b.dz_off + up(size_t(a.N) * b.ldz * 2);
   b.pw_off = b.px_off + sums(a.N, b.x);
   b.total = b.pw_off + (b.w.s > 1 ? sums(nv, b.w) : 0);
   return b;
@@ -848,8 +860,8 @@ Operands lay_out(const LossArgs& a, const Plan& p, const void* x, const void* W,
   if (coef || !a.bf16) {
     auto parts = [](int64_t n) { return int(std::min<int64_t>(kMaxParts, cdiv(n, 1024))); };
     o.units = reinterpret_cast<LossUnits*>(a.ws + p.units_off);
-    o.Xh = {at(p.xh_off), p.ldp, a.N * p.ldp};
-    o.Wh = {at(p.wh_off), p.ldp, a.V * p.ldp};
+    o.Xh = {at(p.xh_off), p.planes * p.ldp};
+    o.Wh = {at(p.wh_off), p.planes * p.ldp};
     const int p0 = coef ? parts(a.N) : 0, p1 = parts(cdiv(a.N * a.d, 8)), p2 = parts(cdiv(a.V * a.d, 8));
     const int64_t nc = coef ? cdiv(a.N, 256) : 0, n1 = cdiv(a.N * (p.ldp / 8), 256), n2 = cdiv(a.V * (p.ldp / 8), 256);
     auto go = [&](auto bf) {
@@ -869,13 +881,13 @@ Operands lay_out(const LossArgs& a, const Plan& p, const void* x, const void* W,
     auto pad = [&](const void* in, int64_t R, size_t off) {
       k_loss_pad<<<unsigned(cdiv(R * (p.ldp / 8), 256)), 256, 0, a.stream>>>(static_cast<const uint16_t*>(in), R, a.d, p.ldp,
                                                                              at(off));
-      return MmOperand{at(off), p.ldp, 0};
+      return MmOperand{at(off), p.ldp};
     };
     o.X = pad(x, a.N, p.xp_off);
     o.Wo = pad(W, a.V, p.wp_off);
   } else {
-    o.X = {static_cast<const uint16_t*>(x), a.d, 0};
-    o.Wo = {static_cast<const uint16_t*>(W), a.d, 0};
+    o.X = {static_cast<const uint16_t*>(x), a.d};
+    o.Wo = {static_cast<const uint16_t*>(W), a.d};
   }
   return o;
 }
@@ -884,7 +896,7 @@ Operands lay_out(const LossArgs& a, const Plan& p, const void* x, const void* W,
 
 bool loss_fits(const LossArgs& a) {
   // rows x 16-byte chunks of the operands, and tiles of the logits
-  const double tiles = double(cdiv(a.N, Few::BN)) * double(cdiv(a.V, Few::BM));
+  const double tiles = double(cdiv(a.N, kFewN)) * double(cdiv(a.V, kFewM));
   const double lay = double(std::max(a.N, a.V)) * double(a.d / 8 + 1) / 256, out = double(std::max(a.N, a.V)) * double(a.d) / 256;
   return std::max({tiles, lay, out}) < 2147483647.0;
 }
@@ -894,18 +906,18 @@ size_t loss_backward_workspace(const LossArgs& a) { return a.N ? plan_bw(a).tota
 void launch_loss(const LossArgs& a, const void* x, const void* W, const void* targets, float* loss, float* lse) {
   const PlanFw f = plan_fw(a);
   const Operands o = lay_out(a, f.op, x, W, targets, nullptr, nullptr, nullptr, nullptr);
-  const int terms = a.bf16 ? 1 : kTerms;
   const float c = a.scale * kLog2e;
   float2* part = reinterpret_cast<float2*>(a.ws + f.part_off);
-  auto go = [&](auto tl, auto f16) {
-    using Tl = decltype(tl);
-    k_loss_lse<Tl, decltype(f16)::value><<<unsigned(f.grid), Tl::NTHR, 0, a.stream>>>(
-        o.Wo, o.X, a.N, a.V, a.d, terms, c, o.units, int(f.n_tok), int(f.splits), int(f.per_split), part);
+  auto go = [&](auto pair) {
+    constexpr bool PAIR = decltype(pair)::value;
+    auto run = [&](auto tl) {
+      using Tl = decltype(tl);
+      k_loss_lse<Tl, PAIR><<<unsigned(f.grid), Tl::NTHR, 0, a.stream>>>(o.Wo, o.X, a.N, a.V, a.d, c, o.units, int(f.n_tok),
+                                                                       int(f.splits), int(f.per_split), part);
+    };
+    if (f.kind == 0) run(Few<PAIR>{}); else if (f.kind == 1) run(Mid<PAIR>{}); else run(Big<PAIR>{});
   };
-  auto go_type = [&](auto tl) {
-    if (a.bf16) go(tl, std::false_type{}); else go(tl, std::true_type{});
-  };
-  if (f.kind == 0) go_type(Few{}); else if (f.kind == 1) go_type(Mid{}); else go_type(Big{});
+  if (a.bf16) go(std::false_type{}); else go(std::true_type{});
   const unsigned jg = static_cast<unsigned>(cdiv(a.N, 4));
   if (a.bf16)
     k_loss_join<true><<<jg, 256, 0, a.stream>>>(part, int(f.splits), x, W, targets, a.target_bytes, a.N, a.V, a.d,
@@ -926,7 +938,6 @@ void launch_loss_backward(const LossArgs& a, const void* x, const void* W, const
     return;
   }
   const PlanBw b = plan_bw(a);
-  const int terms = a.bf16 ? 1 : kTerms;
   const float c = a.scale * kLog2e;
   RowCoef* coef = reinterpret_cast<RowCoef*>(a.ws + b.coef_off);
   uint16_t* dz = reinterpret_cast<uint16_t*>(a.ws + b.dz_off);
@@ -941,9 +952,8 @@ void launch_loss_backward(const LossArgs& a, const void* x, const void* W, const
     else
       k_loss_out<false><<<grid, 256, 0, a.stream>>>(P, S, n, units, is_w, a.scale, static_cast<float*>(to));
   };
-  // one tile shape and storage type of each kernel
-  auto typed = [&](auto tl, auto run) {
-    if (a.bf16) run(tl, std::true_type{}); else run(tl, std::false_type{});
+  auto typed = [&](auto run) {
+    if (a.bf16) run(std::true_type{}); else run(std::false_type{});
   };
   const size_t elt = a.bf16 ? 2 : 4;
   for (int64_t v0 = 0; v0 < a.V; v0 += b.piece) {
@@ -951,14 +961,17 @@ void launch_loss_backward(const LossArgs& a, const void* x, const void* W, const
     const bool last = v1 == a.V;
     // dz rows reach the end of the piece's last tile of 8: zeros past the vocabulary
     const int64_t pend = v0 + cdiv(nv, 8) * 8;
-    auto logits = [&](auto tl, auto bf) {
-      using Tl = decltype(tl);
-      const int64_t n_tok = cdiv(a.N, Tl::BN), tiles = n_tok * cdiv(nv, Tl::BM), slots = Tl::BN == Big::BN ? kCus : 2 * kCus;
-      k_loss_dz<Tl, decltype(bf)::value><<<unsigned(std::min(tiles, slots)), Tl::NTHR, 0, a.stream>>>(
-          o.Wo, o.X, a.N, a.V, a.d, terms, c, units, v0, pend, int(n_tok), coef, dz, b.ldz);
-    };
-    if (b.big_z) typed(Big{}, logits); else typed(Mid{}, logits);
-    const MmOperand Z{dz, b.ldz, a.N * b.ldz};
+    typed([&](auto bf) {
+      constexpr bool BF = decltype(bf)::value;
+      auto run = [&](auto tl) {
+        using Tl = decltype(tl);
+        const int64_t n_tok = cdiv(a.N, Tl::BN), tiles = n_tok * cdiv(nv, kBM), slots = (b.big_z ? 1 : mid_slots(BF)) * kCus;
+        k_loss_dz<Tl, BF><<<unsigned(std::min(tiles, slots)), Tl::NTHR, 0, a.stream>>>(
+            o.Wo, o.X, a.N, a.V, a.d, c, units, v0, pend, int(n_tok), coef, dz, b.ldz);
+      };
+      if (b.big_z) run(Big<!BF>{}); else run(Mid<!BF>{});
+    });
+    const MmOperand Z{dz, b.ldz};
     // head rows, then the rest, of a product whose rows lie `step` apart in Z
     auto product = [&](auto ta, const Cut& c, int64_t step, const MmOperand& B, int64_t rows, int64_t K, bool add, float* P,
                        bool finish, void* to) {
@@ -968,13 +981,16 @@ void launch_loss_backward(const LossArgs& a, const void* x, const void* W, const
         MmOperand A = Z;
         A.base += r0 * step;
         uint8_t* const dst = static_cast<uint8_t*>(to) + size_t(r0) * a.d * elt;
-        auto run = [&](auto tl, auto bf) {
-          using Tl = decltype(tl);
-          const int64_t n_col = cdiv(a.d, Tl::BN);
-          k_loss_mm<Tl, TA, decltype(bf)::value><<<unsigned(cdiv(n, Tl::BM) * n_col * s), Tl::NTHR, 0, a.stream>>>(
-              A, B, n, a.d, K, len, terms, int(n_col), int(s), add, sums, finish && s == 1 ? dst : nullptr, units, a.scale);
-        };
-        if (b.out == Big::BN) typed(Big{}, run); else typed(Wide{}, run);
+        typed([&](auto bf) {
+          constexpr bool BF = decltype(bf)::value;
+          auto run = [&](auto tl) {
+            using Tl = decltype(tl);
+            const int64_t n_col = cdiv(a.d, Tl::BN);
+            k_loss_mm<Tl, TA, BF><<<unsigned(cdiv(n, kBM) * n_col * s), Tl::NTHR, 0, a.stream>>>(
+                A, B, n, a.d, K, len, int(n_col), int(s), add, sums, finish && s == 1 ? dst : nullptr, units, a.scale);
+          };
+          if (b.out == kBig) run(Big<!BF>{}); else run(Wide<!BF>{});
+        });
         if (finish && s > 1) out(sums, int(s), n * a.d, TA, dst);
       };
       const int64_t head = std::min(c.head, rows);
@@ -982,10 +998,10 @@ void launch_loss_backward(const LossArgs& a, const void* x, const void* W, const
       part(head, rows - head, c.s, c.len, P + head * a.d);
     };
     if (dx) {
-      const MmOperand Wc{o.Wh.base + v0 * o.Wh.ld, o.Wh.ld, o.Wh.plane};
+      const MmOperand Wc{o.Wh.base + v0 * o.Wh.ld, o.Wh.ld};
       product(std::false_type{}, b.x, b.ldz, Wc, a.N, nv, v0 > 0, px, last, dx);
     }
-    if (dW) product(std::true_type{}, b.w, 1, o.Xh, nv, a.N, false, pw, true, static_cast<uint8_t*>(dW) + v0 * a.d * elt);
+    if (dW) product(std::true_type{}, b.w, b.op.planes, o.Xh, nv, a.N, false, pw, true, static_cast<uint8_t*>(dW) + v0 * a.d * elt);
   }
 }
 
