@@ -262,11 +262,14 @@ __global__ void __launch_bounds__(256) k_loss_layout(const float* __restrict__ d
   if (i >= R * C) return;
   const int64_t r = i / C, c0 = (i - r * C) * 8;
   float v[8];
-  if (d == ldp) {
-    load8<BF16>(is_x ? x : W, r * d + c0, R * d, v);
+  using S = Storage<BF16 ? kBF16 : kF32>;
+  const typename S::T* const q = static_cast<const typename S::T*>(is_x ? x : W) + r * d + c0;
+  if (c0 + 8 <= d) {   // at once, aligned or not
+    typename S::T t[8];
+    __builtin_memcpy(t, q, sizeof(t));
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = S::load(&t[e]);
   } else {
-    using S = Storage<BF16 ? kBF16 : kF32>;
-    const typename S::T* q = static_cast<const typename S::T*>(is_x ? x : W) + r * d + c0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = c0 + e < d ? S::load(q + e) : 0.0f;
   }
