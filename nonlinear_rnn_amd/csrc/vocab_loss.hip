@@ -733,9 +733,9 @@ Plan plan_operands(const LossArgs& a, bool back) {
   return p;
 }
 
-// The logits' tile: Mid takes about 1.15 times Big's time per product (32768 x
-// 512 x 8192: dz 395 and 360 us), which pays where 256 tokens a tile would
-// waste more.
+// The logits' tile: Mid takes about 1.15 times Big's time per product (16384 x
+// 512 x 16384: 285 and 245 us), which pays where 256 tokens a tile would waste
+// more (100 x 512 x 32768: 18 and 21 us, fp32 58 and 70).
 bool take_big(int64_t cols) { return cdiv(cols, kBig) * kBig * 100 <= cdiv(cols, kMid) * kMid * 115; }
 
 struct PlanFw {
@@ -828,8 +828,8 @@ PlanBw plan_bw(const LossArgs& a) {
   b.ldz = b.op.planes * b.piece + 64;
   // the products' tile: the shorter of the two plans.  256 columns a tile are
   // faster than 192 per column, those waste less at the edge and may fill the
-  // device's rounds better: 16384 x 520 x 16384 took 1118 us with 192 and 1194
-  // with 256, x 512 1076 and 921.  (128, two workgroups a CU, was never faster
+  // device's rounds better: 16384 x 520 x 16384 takes 1127 us with 192 and 1251
+  // with 256, x 512 1025 and 873.  (128, two workgroups a CU, was never faster
   // than 192: dz is read once for every column of tiles.)
   const int64_t nv = std::min(b.piece, a.V);
   const int terms = a.bf16 ? 1 : kTerms;
