@@ -29,6 +29,9 @@ def _draw(kind, N, V, rng):
         return np.full(N, V // 2)
     if kind == "skewed":
         return np.minimum((V ** rng.random(N)).astype(np.int64) - 1, V - 1).clip(0)
+    if kind == "many":   # run lengths around the cuts of a very frequent token's chunks
+        lengths = [511, 512, 513, 527, 528, 529, 1023, 1024, 1025, 1040, 2049]
+        return rng.permutation(np.concatenate([np.repeat(np.arange(len(lengths)), lengths), rng.integers(20, V, N)])[:N])
     # "runs": run lengths around the cut of a frequent token's rows, then shuffled
     lengths = [1, 2, 15, 16, 17, 62, 63, 64, 65, 66, 127, 128, 129, 191, 192, 193, 300]
     ids = np.repeat(np.arange(len(lengths)), lengths)[:N]
@@ -69,6 +72,16 @@ def _check(N, V, d, dtype, kind, ids=np.int64, scale=1.5, pad=None, odd=False):
     (9000, 131075, 8, "skewed"), (4100, 300000, 16, "uniform"), (5000, 1000, 256, "same"), (20000, 700, 33, "skewed"),
 ])
 def test_embed_matches_oracle(N, V, d, kind, dtype):
+    _check(N, V, d, dtype, kind)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,V,d,kind", [
+    (8191, 700, 12, "skewed"), (8192, 9000, 8, "uniform"), (8193, 9000, 8, "uniform"),   # both sorts
+    (8192, 524287, 4, "uniform"), (8192, 524288, 4, "uniform"),                           # a word for key and position, or not
+    (8190, 60, 24, "many"), (12000, 3000, 260, "many"),
+])
+def test_embed_gradient_at_the_cuts(N, V, d, kind, dtype):
     _check(N, V, d, dtype, kind)
 
 

@@ -3,11 +3,11 @@
 Bands, first-order, per element, e = 2^-24, u = half a step of the storage
 type, A = |x| |W|^T (the size of a logit's products):
   logits  dz_ = (2 d + 8) e s A: d fp32 additions of exact products (two
-          roundings each allowed for the matrix cores' order), or of products
-          good to 3 e (fp32 data, six terms each: 12 d + 8 instead)
+          roundings each allowed for the matrix cores' order); fp32 data, whose
+          values go as two terms good to 2^-22 each: 12 d + 8 instead
   lse     max dz_ of the row + (V / 2 + 64) e (sums of positive terms) + 8 e (|lse| + max|z|)
   loss    lse's band + the target's logit's
-  dz      relative 2^-8 (its bf16 rounding; bf16 storage only) + the error of
+  dz      relative 2^-8 (one rounding to 8 bits; bf16 storage only) + the error of
           p's exponent: dz_ + lse's band + 4 e (|z| + |lse|) + 16 e, against
           q = s (|dloss + dlse| p + |dloss| onehot)
   dx      u |dx| + sum of dz's band |W| + 2 (V + 64) e sum q |W|; dW likewise with N
