@@ -465,16 +465,19 @@ __global__ void __launch_bounds__(256) k_loss_join(const float2* __restrict__ pa
 
 // ------------------------------------------------------------ backward ---
 
-// dz (in units of its call) of the vocabulary tiles of a piece (first entry piece0, rows to be
-// written up to piece1), stored by token rows ldz apart (fp32 data:
-// every 32 high terms and their 32 low ones).  A lane holds four neighbouring
-// entries of its token at a time and the other half of the wave the next four:
-// a swap of the halves makes them eight, 16 bytes a store, and a swap of the halves' halves puts 64 bytes of
-// 16 tokens into one store of the wave (32 bytes of 32 tokens: 377 us for
-// 32768 x 512 x 8192 instead of 366).  dz is as large as the last-level cache
-// or larger, so the stores leave W and x in the caches: 354 us, and the dx
-// that reads it 275 instead of 291.  Without any store it would be 295, the
-// products alone 245.
+// dz (in units of its call) of the vocabulary tiles of a piece (first entry
+// piece0, rows to be written up to piece1), stored by token rows ldz apart
+// (fp32 data: every 32 high terms and their 32 low ones).  A lane holds four
+// neighbouring entries of its token at a time and the other half of the wave
+// the next four: a swap of the halves makes them eight, 16 bytes, a swap of the
+// halves' halves puts 64 bytes of 16 tokens into four lanes of one register, and
+// a permutation of the lanes puts these side by side (32768 x 512 x 8192: stores
+// of 16 bytes a row in a quarter of a wave 354 us, this 336; without any store
+// 295 at the time, the products alone 245).
+// bf16 data goes past the caches, so that W and x stay in them: 336 us and 283
+// for the dx that reads it, against 340 and 299, though half lines count for
+// more there (694 MB written for 537).  fp32 data, whose two terms fill a line,
+// does not: 4096 x 256 x 32000 252, dx 215, dW 229 us against 287, 209, 225.
 template <class Tl, bool BF16>
 __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_dz(MmOperand W, MmOperand X, int64_t N, int64_t V, int64_t d,
                                                          float c, const LossUnits* __restrict__ units,
@@ -501,8 +504,9 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_dz(MmOperand W, MmOperand 
     tile_of(lu.u, v_tiles, n_tok, kGroup, vt, tok);
     const int64_t n0 = static_cast<int64_t>(tok) * Tl::BN;
     tile.template seek<false, false>(piece0 + static_cast<int64_t>(vt) * Tl::BM, n0);
-    if (wave < Tl::BN / 64)
-      mm_dma(coef + imin(n0 + wave * 64 + lane, N - 1), mm_lds_addr(coefs[fill] + wave * 64));
+    int l = lane;
+    asm volatile("" : "+v"(l));
+    if (wave < Tl::BN / 64) mm_dma(coef + imin(n0 + wave * 64 + l, N - 1), mm_lds_addr(coefs[fill] + wave * 64));
     fill = fill + 1 == kRing ? 0 : fill + 1;
   };
   auto next = [&]() {
@@ -524,17 +528,21 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_dz(MmOperand W, MmOperand 
     const int rows = static_cast<int>(imin(piece1 - v0, Tl::BM)), toks = static_cast<int>(imin(N - n0, Tl::BN));
     const int vocab_left = static_cast<int>(imin(V - v0, Tl::BM));
     whole = vocab_left == Tl::BM && toks == Tl::BN;
-    // opaque, so that the stores' offsets are not kept in registers over the tiles
-    int el = lane;
-    asm volatile("" : "+v"(el));
-    const int eh = el >> 5, eb = 8 * eh + 16 * ((el >> 4) & 1);
+    // opaque, so that what follows from them is not kept in registers over the tiles
+    int el = lane, first_row = wr * Tl::WM * 32;
+    asm volatile("" : "+v"(el), "+s"(first_row));
+    const int eh = el >> 5;
+    // this lane's place in a store: token el / 4 of 16, entries 8 (el % 4) ..; they
+    // are in the lane of that token and chunk (chunks 0, 16, 8, 24 by lane / 16)
+    const int eb = 8 * (el & 3), et = el >> 2;
+    const int from = 4 * (et + 16 * ((el & 3) == 1 ? 2 : (el & 3) == 2 ? 1 : el & 3));
     const uint32_t ld2 = static_cast<uint32_t>(2 * ldz);
     auto finish = [&](auto edge) {
       constexpr bool EDGE = decltype(edge)::value;
 #pragma unroll
       for (int j = 0; j < Tl::WN; ++j) {
         const int tl = (wc * Tl::WN + j) * 32 + (el & 31);
-        const int tb = (wc * Tl::WN + j) * 32 + (el & 15);
+        const int tb = (wc * Tl::WN + j) * 32 + et;
         const uint32_t at_row = static_cast<uint32_t>(tb) * ld2 + 2 * eb;
         const RowCoef rc = coefs[use][tl];
         // the target's row of this tile (negative or past the tile: elsewhere)
@@ -542,7 +550,7 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_dz(MmOperand W, MmOperand 
         const bool negative = __builtin_amdgcn_ballot_w64(rc.sign < 0.0f) != 0;
 #pragma unroll
         for (int i2 = 0; i2 < Tl::WM; ++i2) {
-          const int vb = (wr * Tl::WM + i2) * 32;   // the block's first row of the tile
+          const int vb = first_row + i2 * 32;   // the block's first row of the tile
           float v[16];
 #pragma unroll
           for (int r = 0; r < 16; ++r) v[r] = ex2(fmaf(tile.acc[i2][j][r], c, -rc.lse2));
@@ -578,7 +586,7 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_dz(MmOperand W, MmOperand 
                   x1 -= static_cast<float>(p[1]);
                 }
               }
-            // places: entry 8 (lane / 32) + 16 (lane / 16 % 2) of the block, token 16 k + lane % 16
+            // entry 8 (lane / 32) + 16 (lane / 16 % 2) of the block, token 16 k + lane % 16
             mm_u32x4 o[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -593,9 +601,14 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_dz(MmOperand W, MmOperand 
             }
 #pragma unroll
             for (int k = 0; k < 2; ++k)
-              if (!EDGE || (tb + 16 * k < toks && vb + eb < rows))
-                __builtin_nontemporal_store(
-                    o[k], reinterpret_cast<mm_u32x4*>(base + (at_row + 16 * k * ld2 + 2 * TERMS * vb + 64 * t)));
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[k][e] = __builtin_amdgcn_ds_bpermute(from, o[k][e]);
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              if (!EDGE || (tb + 16 * k < toks && vb + eb < rows)) {
+                mm_u32x4* const to = reinterpret_cast<mm_u32x4*>(base + (at_row + 16 * k * ld2 + 2 * TERMS * vb + 64 * t));
+                if constexpr (BF16) __builtin_nontemporal_store(o[k], to); else gstore(to, o[k]);
+              }
           }
         }
       }
