@@ -296,7 +296,8 @@ __global__ void __launch_bounds__(256) k_loss_layout(const float* __restrict__ d
 // split's vocabulary tiles, z the plain products x W^T (F16: of the operands
 // in their units), c = s log2(e) > 0 (in those units).
 // A unit is a token tile and a split; four token tiles and their splits are
-// neighbours, so that an XCD's workgroups share the W tiles they walk.
+// neighbours, so that an XCD's workgroups share the W tiles they walk (8 or 16
+// were 1 to 5% slower).
 template <class Tl, bool F16>
 __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_lse(MmOperand W, MmOperand X, int64_t N, int64_t V, int64_t d,
                                                           float c, const LossUnits* __restrict__ units, int n_tok, int splits, int per_split,
