@@ -415,8 +415,9 @@ typedef struct {
  *   gate    (N, d) or NULL (no gate)
  *   x       (N, d) the residual stream, or NULL (zeros)
  *   r_out   (N, d) or NULL; n_out (N, d), given exactly when w_pre is
- * All N x d pointers must be 16-byte aligned.  r_out may alias h or x, n_out
- * may alias h, gate or x (every row is read before it is written). */
+ * All N x d pointers must be 16-byte aligned.  r_out may be h or x itself, n_out
+ * h, gate or x itself (every row is read before it is written), not otherwise
+ * overlap them; r_out and n_out are different arrays. */
 prn_status prn_block_norm(const void* h, const void* gate, const void* x, const prn_block_norm_params* params,
                           void* r_out, void* n_out);
 

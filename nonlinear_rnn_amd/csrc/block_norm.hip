@@ -94,6 +94,7 @@ struct NormDev {
   int64_t N;
   int d, act;
   float eps;
+  bool in_place;        // forward: r is written over h or x
 };
 
 // A lane's channels: chunk v of VEC channels starts at (v TPR + lane) VEC.
@@ -216,6 +217,12 @@ __global__ void __launch_bounds__(NTHR) k_block_norm(NormDev a) {
     } else if (a.alpha) {
 #pragma unroll
       for (int e = 0; e < E; ++e) h[e] *= alpha[e];
+    }
+    // r over h or x: a moved-back last chunk reads channels that another wave
+    // of the row writes, so every wave has read the row before one writes it
+    // (behind the first norm's sum they have; n's stores are behind the second's)
+    if constexpr (TAIL && TPR > 64) {
+      if (a.in_place && !a.w_post) __syncthreads();
     }
     if (a.o0) row.store(a.o0, n, h);
     if (a.w_pre) {
@@ -471,6 +478,7 @@ void launch_block_norm(const BlockNormArgs& a) {
   n.o0 = a.r_out, n.o1 = a.n_out;
   n.w_post = a.w_post, n.w_pre = a.w_pre, n.alpha = a.alpha;
   n.N = a.N, n.d = int(a.d), n.act = a.act, n.eps = a.eps;
+  n.in_place = a.r_out && (a.r_out == a.h || a.r_out == a.x);
   go_all<false>(a.bf16, g, n, unsigned(grid_of(g, a.bf16, a.N)), a.stream);
 }
 

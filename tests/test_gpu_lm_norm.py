@@ -201,3 +201,28 @@ def test_another_stream_and_a_graph():
         torch.cuda.synchronize()
         want = prn.block_norm(h, x, **kw) + prn.block_norm_backward(dr, dn, h, x, **kw)
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 513), ("bf16", 519), ("bf16", 1025), ("bf16", 2049), ("bf16", 4099), ("bf16", 8185),
+                                     ("bf16", 1001), ("f32", 515), ("f32", 769), ("f32", 1025), ("f32", 2051), ("f32", 513)])
+@pytest.mark.parametrize("N", [3, 2500])
+def test_in_place_at_widths_whose_last_chunk_crosses_waves(N, d, dtype):
+    """The moved-back last chunk of a row reads channels of another wave: with no norm of h there is no sum, and
+    so no barrier, between reading the row and writing r over it, unless the kernel puts one there."""
+    kw, _, _ = _inputs(N, d, dtype, FULL, N + d)
+    h, x = kw.pop("h"), kw.pop("x")
+    for parts in ((), ("gate",), ("alpha",), ("w_pre",), ("gate", "alpha", "w_pre"), ("gate", "w_post", "w_pre")):
+        p = {k: kw[k] if k in parts else None for k in kw}
+        g, weights = p.pop("gate"), p
+        n = None if weights["w_pre"] is None else torch.empty_like(h)
+        want = prn.block_norm(h, x, gate=g, **weights)
+        for over in ("h", "x"):
+            hh, xx = h.clone(), x.clone()
+            r = hh if over == "h" else xx
+            B.prn_block_norm(hh, g, xx, r, n, **weights)
+            assert torch.equal(r, want[0]) and (n is None or torch.equal(n, want[1])), (parts, over)
+            if n is not None:      # n over the other input
+                hh, xx = h.clone(), x.clone()
+                r, m = (hh, xx) if over == "h" else (xx, hh)
+                B.prn_block_norm(hh, g, xx, r, m, **weights)
+                assert torch.equal(r, want[0]) and torch.equal(m, want[1]), (parts, over)
