@@ -1,0 +1,105 @@
+"""The vocabulary loss where its 16-bit terms could run out of range: tokens of
+very unequal weight or size, products below fp32's range, several pieces of
+two-term gradients, and the one fp16 rounding of bf16 data's dz.
+
+Bands, first-order, per element, e = 2^-24, u = half a step of the storage
+type, A = |x| |W|^T, g_n = max(|dloss_n|, |dloss_n + dlse_n|):
+  operands  x is held to 2^-39 of its token's largest value, W to 2^-39 of the
+            tensor's (a largest value of 2^14 .. 2^15 and half a step of 2^-24);
+            above that bf16 data exactly, fp32 data to 2^-22 of itself, which
+            the logits' count has
+  logits    bz = (2 d + 8) e s A (fp32 data 12 d + 8) + s times the operands' floors
+  lse       max bz of the row + (V / 2 + 64) e + 8 e (|lse| + max|z|)
+  loss      lse's band + the target's logit's
+  dz        relative 2^-11 (bf16 data: one fp16 rounding) or 4 e (two terms);
+            2^-38 s g_n (half a step of 2^-24 over 2^13); p's exponent: bz + lse's
+            band + 4 e (|z| + |lse|) + 16 e, against q = s (|dloss + dlse| p + |dloss| onehot)
+  dx        u |dx| + sum of dz's band |W| + 2 (V + 64) e sum q |W| + W's floor sum q
+  dW        u |dW| + sum of dz's band |x| + 2 (N + 64) e sum q |x|, and x, in it times
+            a power of two in (g_n / 2, g_n], is held to 2^-39 max(g_n |x|): 2^-38 max(g_n |x|) sum q / g_n
+"""
+import numpy as np
+import pytest
+import torch
+
+import nonlinear_rnn_amd as prn
+from gpu_helpers import TORCH_DT, say, to_f64
+from nonlinear_rnn_amd import binding as B
+from oracle import lm as olm
+
+pytestmark = pytest.mark.gpu
+E = 2.0 ** -24
+
+
+def _inputs(N, V, d, dtype, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    dt = TORCH_DT[dtype]
+    W = torch.randn(V, d, generator=g, device="cuda") / d ** 0.5
+    t = torch.randint(0, V, (N,), generator=g, device="cuda")
+    x = torch.randn(N, d, generator=g, device="cuda") + 4 * W[t]
+    t[torch.rand(N, generator=g, device="cuda") < 0.1] = -100
+    dloss = torch.rand(N, generator=g, device="cuda") + 0.5
+    dlse = 0.1 * torch.randn(N, generator=g, device="cuda")
+    return x.to(dt), W.to(dt), t, dloss, dlse
+
+
+def _bands(x, W, t, dloss, dlse, dtype, scale):
+    """(loss, lse, dx, dW) of the oracle and their bands."""
+    (N, d), V = x.shape, W.shape[0]
+    u = torch.finfo(TORCH_DT[dtype]).eps / 2
+    loss, lse, z = olm.vocab_loss(x, W, t, scale)
+    fx, fW = 2.0 ** -39 * np.abs(x).max(-1), 2.0 ** -39 * np.abs(W).max()
+    bz = np.abs(x) @ np.abs(W).T
+    bz *= ((2 * d + 8) if dtype == "bf16" else (12 * d + 8)) * E * scale
+    bz += scale * (fx[:, None] * np.abs(W).sum(1)[None, :] + fW * np.abs(x).sum(1)[:, None])
+    b_lse = bz.max(-1) + (V / 2 + 64) * E + 8 * E * (np.abs(lse) + np.abs(z).max(-1))
+    at, rows = np.where((t >= 0) & (t < V), t, 0), np.arange(N)
+    b_loss = b_lse + bz[rows, at] + 8 * E * np.abs(z[rows, at])
+    dz = olm.vocab_loss_dz(dloss, dlse, z, lse, t, scale)
+    one = np.where(t == -100, 0.0, dloss)
+    both = one if dlse is None else one + dlse
+    g = np.maximum(np.abs(one), np.abs(both))
+    q = np.exp(z - lse[:, None]) * np.abs(both)[:, None]
+    b_dz = (bz + b_lse[:, None] + 4 * E * (np.abs(z) + np.abs(lse)[:, None]) + 16 * E) * q
+    q[rows, at] += np.abs(one)
+    b_dz[rows, at] += 16 * E * np.abs(one)
+    b_dz += (2.0 ** -11 if dtype == "bf16" else 4 * E) * np.abs(dz) / scale + 2.0 ** -38 * g[:, None]
+    b_dz, q = scale * b_dz, scale * q
+    dx, dW = dz @ W, dz.T @ x
+    b_dx = u * np.abs(dx) + b_dz @ np.abs(W) + 2 * (V + 64) * E * (q @ np.abs(W)) + fW * q.sum(-1)[:, None]
+    inv = np.divide(1.0, g, out=np.zeros_like(g), where=g > 0)
+    b_dW = u * np.abs(dW) + b_dz.T @ np.abs(x) + 2 * (N + 64) * E * (q.T @ np.abs(x))
+    b_dW += 2.0 ** -38 * (g * np.abs(x).max(-1)).max() * (q.T @ inv)[:, None]
+    return (loss, lse, dx, dW), (b_loss, b_lse, b_dx, b_dW)
+
+
+def _check(x, W, t, dloss, dlse, dtype, scale=1.0, names=("loss", "lse", "dx", "dW"), rows=None):
+    """Every output in its band; of `names` only, and of the tokens `rows` only (not for dW)."""
+    loss, lse = prn.vocab_loss(x, W, t, scale=scale)
+    dx, dW = prn.vocab_loss_backward(dloss, x, W, t, lse, dlse=dlse, scale=scale)
+    ref, band = _bands(to_f64(x), to_f64(W), t.cpu().numpy(), to_f64(dloss), None if dlse is None else to_f64(dlse), dtype, scale)
+    for name, got, r, b in zip(("loss", "lse", "dx", "dW"), (loss, lse, dx, dW), ref, band):
+        if name not in names:
+            continue
+        part = slice(None) if rows is None or name == "dW" else rows
+        err = np.abs(to_f64(got) - r)[part] / np.maximum(b[part], 1e-300)
+        worst = float(np.nan_to_num(err, nan=np.inf).max())
+        say(f"  {name}: of the band {worst:.3g}")
+        assert worst <= 1.0, name
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,V,d", [(64, 128, 64), (65, 129, 65), (2, 5000, 40), (257, 2048, 256), (700, 513, 129)])
+def test_dz_is_rounded_once_to_fp16(N, V, d, dtype):
+    say(f"[case] vocab loss N={N} V={V} d={d} {dtype}")
+    _check(*_inputs(N, V, d, dtype, N + V), dtype)
+
+
+@pytest.mark.parametrize("N,V", [(9000, 16001), (66000, 2100)])
+def test_several_pieces_of_two_terms(N, V):
+    """More than 512 MB of fp32 data's dz: dx adds up over pieces, the last one short and of no multiple of 8; in the
+    second case 258 row tiles, the last two's sums in slices."""
+    whole = N * V * 4
+    assert B.prn_vocab_loss_backward_workspace_bytes(torch.float32, N, V, 16) < whole
+    say(f"[case] vocab loss N={N} V={V} f32, several pieces")
+    _check(*_inputs(N, V, 16, "f32", 4), "f32")
