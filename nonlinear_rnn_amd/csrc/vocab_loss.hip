@@ -61,6 +61,11 @@ constexpr int64_t kFewM = Few<false>::BM, kFewN = Few<false>::BN;
 int64_t mid_slots(bool bf16) { return bf16 ? 2 : 1; }
 constexpr int kXcd = 8;
 
+// A factor of the logits, above 0 also where their operands' units are so small
+// that it underflows: an entry past the vocabulary is -inf times it, and the
+// logits, below 2^60 in these units, are zero all the same.
+__device__ __forceinline__ float above_zero(float c) { return fmaxf(c, 0x1p-126f); }
+
 // Workgroups are dealt round-robin to the XCDs.  The units of work of this
 // workgroup, when every XCD takes a contiguous share of them, in proportion
 // to its workgroups, so that neighbouring units share its L2.
@@ -302,7 +307,7 @@ template <class Tl, bool F16>
 __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_lse(MmOperand W, MmOperand X, int64_t N, int64_t V, int64_t d,
                                                           float c, const LossUnits* __restrict__ units, int n_tok, int splits, int per_split,
                                                           float2* __restrict__ part) {
-  if constexpr (F16) c *= units->back_z;
+  if constexpr (F16) c = above_zero(c * units->back_z);
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Tl::LDS];
   __shared__ float2 hand[Tl::WR][Tl::BN];
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, l32 = lane & 31;
@@ -427,7 +432,7 @@ __global__ void __launch_bounds__(256) k_loss_join(const float2* __restrict__ pa
   const int64_t n = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
   if (n >= N) return;
-  const float back = BF16 ? 1.0f : units->back_z, c = scale * kLog2e * back;
+  const float back = BF16 ? 1.0f : units->back_z, c = above_zero(scale * kLog2e * back);
   const int64_t t = target_of(targets, target_bytes, n);
   const bool in = t >= 0 && t < V;
   // the pairs are on their way while the dot product waits for the target

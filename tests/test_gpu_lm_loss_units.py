@@ -95,6 +95,19 @@ def test_dz_is_rounded_once_to_fp16(N, V, d, dtype):
     _check(*_inputs(N, V, d, dtype, N + V), dtype)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("sx,sw", [(1e-20, 1e-20), (1e-30, 1e-12), (1e-38, 1.0), (0.0, 1e-30), (1e-36, 1e-36)])
+def test_logits_below_the_range(dtype, sx, sw):
+    """The logits are zero but for what fp32 cannot hold: the loss is log V."""
+    x, W, t, dloss, dlse = _inputs(70, 300, 40, dtype, 3)
+    x, W = x * sx, W * sw
+    loss, lse = prn.vocab_loss(x, W, t)
+    assert (np.abs(to_f64(lse) - np.log(300)) <= (150 + 64) * E + 8 * E * 6).all()
+    assert torch.equal(loss[t != -100], lse[t != -100])
+    dx, dW = prn.vocab_loss_backward(dloss, x, W, t, lse, dlse=dlse)
+    assert dx.isfinite().all() and dW.isfinite().all()
+
+
 @pytest.mark.parametrize("N,V", [(9000, 16001), (66000, 2100)])
 def test_several_pieces_of_two_terms(N, V):
     """More than 512 MB of fp32 data's dz: dx adds up over pieces, the last one short and of no multiple of 8; in the
