@@ -451,8 +451,9 @@ typedef struct {
  *   x (N, d), W (V, d) storage dtype, targets (N)
  *   loss_out (N), lse_out (N) fp32
  * Logits are fp32 sums of exact bf16 products (bf16), or of products good to
- * 2^-20 (fp32 data: two fp16 terms of each value, three products; values below
- * 2^-17 of their tensor's largest one are held to 2^-40 of that).  Non-finite
+ * 2^-20 (fp32 data: two fp16 terms of each value, three products; x's values
+ * below 2^-17 of their token's largest one, and W's below 2^-17 of W's largest
+ * one, are held to 2^-39 of that).  Non-finite
  * inputs give non-finite results in their rows.  A target that is neither
  * ignore_index nor in 0 .. V - 1 gives a NaN loss (nothing is read out of
  * bounds).  x and W must be 16-byte aligned. */
@@ -466,11 +467,12 @@ prn_status prn_vocab_loss(const void* x, const void* W, const void* targets, con
  *           gradients arriving at loss_out and lse_out
  * With bf16 storage dz is rounded once, to fp16 in units of the call's largest
  * coefficient, for the matrix cores; x and W go there as fp16 too, scaled by
- * powers of two (exactly; values below 2^-31 of their tensor's largest one are
- * held to 2^-40 of that).  A target out of range gives NaN in its row of dx and in
+ * powers of two (exactly; values below 2^-31 of the largest one are held to 2^-39
+ * of that).  The logits take x in units of each token, dW takes it in x's, and W
+ * goes in W's.  A target out of range gives NaN in its row of dx and in
  * dW.  x, W, dx_out and dW_out must be 16-byte aligned.  The workspace holds
  * one piece of dz (about 512 MB at most, or 512 bytes per token where that is
- * more; twice as much per entry with fp32), x and W once more in the matrix
+ * more; twice as much per entry with fp32), x twice and W once more in the matrix
  * cores' terms, and fp32 sums of dx and of a piece of dW. */
 prn_status prn_vocab_loss_backward(const void* x, const void* W, const void* targets, const float* lse,
                                    const float* dloss, const float* dlse, const prn_vocab_loss_params* params,

@@ -21,17 +21,19 @@
 // most, not 2^-8 (the entry of the target can carry the whole row); bf16 took
 // the error of dx and dW, 0.0017 from their own rounding, to 0.0019.  W and x
 // are laid out as fp16 for the backward's products, which holds bf16's eight
-// bits exactly (down to 2^-31 of the largest value, below that to 2^-40 of it).
+// bits exactly (down to 2^-31 of the largest value, below that to 2^-39 of it).
 // fp32 data: x, W and dz run as two fp16 terms, v = hi + lo to 2^-22 |v|, three
 // products each (lo lo, below 2^-22, is left out).  That is four fp32
 // roundings a product, below what the fp32 sums over them make; the exact
 // three-term bf16 split (bf16split.h) took twice the products and 1.74 ms
 // where this takes 0.855 (4096 x 256 x 32000).
-// For fp16's range a call's x and W are scaled by the power of two that takes
-// their largest value to 2^14 .. 2^15 (values below 2^-17 of that lose the low
-// bits of lo: at most 2^-40 of the largest value), and dz, in units of the
-// largest |dloss|, |dloss + dlse|, by 2^13.  The units come back, in fp32,
-// where they are used.  Everything is summed in fp32 in a fixed order.
+// For fp16's range W is scaled by the power of two that takes its largest value
+// to 2^14 .. 2^15, every token's x by that of its own (so that a large token
+// leaves the others' logits alone; for dW, which sums over tokens, by x's), and
+// dz, in units of the largest |dloss|, |dloss + dlse|, by 2^13.  Values below
+// 2^-17 of the largest one lose the low bits of lo: at most 2^-39 of the largest,
+// half a step of 2^-24 over 2^14.  The units come back, in fp32, where they are
+// used.  Everything is summed in fp32 in a fixed order.
 #include "vocab_loss.h"
 
 #include <algorithm>
@@ -116,7 +118,7 @@ constexpr int kUnit = 13;   // dz is stored times 2^13: fp16 has entries down to
 // The units of a call
 struct LossUnits {
   float g;                         // dz is stored as 2^kUnit dz / (s g)
-  float back_z;                    // z = acc back_z s
+  float iw;                        // z = acc iw s times the token's inverse unit
   float back_x, back_w;            // dx = acc back_x (s g), dW = acc back_w (s g)
   float parts[3][kMaxParts];       // the workgroups' maxima: of dloss and dlse, x, W
 };
@@ -161,7 +163,7 @@ __device__ __forceinline__ void load8(const void* p, int64_t i, int64_t n, float
 }
 
 // The maxima: workgroups [0, n0) of |dloss|, |dloss + dlse|, the next n1 of x
-// and the last n2 of W.  Values that are not finite do not set a unit, they go
+// (for dW) and the last n2 of W.  Values that are not finite do not set a unit, they go
 // through as they are.
 template <bool BF16>
 __global__ void __launch_bounds__(1024) k_loss_maxima(const float* __restrict__ dloss, const float* __restrict__ dlse,
@@ -204,71 +206,19 @@ __device__ __forceinline__ float unit_of(float m, float* inverse) {
   return __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
 }
 
-// A token's row of dz in its units: sign 2^(c z - lse2) - one at the target.
+// A token's row of dz in its units: sign 2^(|c| acc - lse2) - one at the target.
 // The magnitude of (dloss + dlse) / g is folded into the exponent.
 struct RowCoef {
-  float sign, one, lse2;
+  float c;              // s log2(e) times the units of its logits; the sign is that of (dloss + dlse)
+  float one, lse2;
   int32_t target;       // -1: none
 };
 
-// Workgroups [0, nc): the tokens' coefficients; then n1 that lay out x and the
-// rest W in fp16 terms, rows of ldp values (fp32 data: 2 ldp, every 32 high
-// terms and their 32 low ones), zeros past d.  The first writes the units.
+// eight values of row r from column c0 on, zeros past d
 template <bool BF16>
-__global__ void __launch_bounds__(256) k_loss_layout(const float* __restrict__ dloss, const float* __restrict__ dlse,
-                                                     const float* __restrict__ lse, const void* __restrict__ targets,
-                                                     int target_bytes, int64_t ignore, int64_t N, int64_t V, int64_t d,
-                                                     int64_t ldp, const void* __restrict__ x, const void* __restrict__ W,
-                                                     int nc, int n1, int parts0, int parts1, int parts2,
-                                                     LossUnits* __restrict__ u, RowCoef* __restrict__ coef,
-                                                     uint16_t* __restrict__ xh, uint16_t* __restrict__ wh) {
-  __shared__ float w[4];
-  int b = static_cast<int>(blockIdx.x);
-  const int tid = threadIdx.x;
-  auto maximum = [&](int k, int parts) { return block_max(tid < parts ? u->parts[k][tid] : 0.0f, w); };
-  float g = 1.0f;
-  if (b < nc) {
-    g = maximum(0, parts0);
-    if (g == 0.0f) g = 1.0f;
-  }
-  if (b == 0) {
-    float ix, iw;
-    unit_of(maximum(1, parts1), &ix);
-    unit_of(maximum(2, parts2), &iw);
-    if (tid == 0) {
-      u->g = g;
-      u->back_z = ix * iw;
-      u->back_x = iw / (1 << kUnit);
-      u->back_w = ix / (1 << kUnit);
-    }
-  }
-  if (b < nc) {
-    const int64_t n = static_cast<int64_t>(b) * 256 + tid;
-    if (n >= N) return;
-    const int64_t t = target_of(targets, target_bytes, n);
-    const float one = t == ignore ? 0.0f : dloss[n];
-    const float p = (dlse ? one + dlse[n] : one) / g;
-    RowCoef r;
-    r.sign = p < 0.0f ? -1.0f : 1.0f;
-    r.one = one / g * (1 << kUnit);
-    // no such entry: the loss was NaN, and so is its gradient
-    const bool lost = t != ignore && (t < 0 || t >= V);
-    r.lse2 = lost ? __builtin_nanf("") : fmaf(lse[n], kLog2e, -log2f(fabsf(p))) - kUnit;   // p = 0: +inf, a row of zeros
-    r.target = t == ignore || lost ? -1 : static_cast<int32_t>(t);
-    coef[n] = r;
-    return;
-  }
-  b -= nc;
-  const bool is_x = b < n1;
-  if (!is_x) b -= n1;
-  float inv;
-  const float unit = unit_of(is_x ? maximum(1, parts1) : maximum(2, parts2), &inv);
-  const int64_t R = is_x ? N : V, C = ldp / 8, i = static_cast<int64_t>(b) * 256 + tid;
-  if (i >= R * C) return;
-  const int64_t r = i / C, c0 = (i - r * C) * 8;
-  float v[8];
+__device__ __forceinline__ void row8(const void* p, int64_t r, int64_t d, int64_t c0, float* v) {
   using S = Storage<BF16 ? kBF16 : kF32>;
-  const typename S::T* const q = static_cast<const typename S::T*>(is_x ? x : W) + r * d + c0;
+  const typename S::T* const q = static_cast<const typename S::T*>(p) + r * d + c0;
   if (c0 + 8 <= d) {   // at once, aligned or not
     typename S::T t[8];
     __builtin_memcpy(t, q, sizeof(t));
@@ -278,6 +228,10 @@ __global__ void __launch_bounds__(256) k_loss_layout(const float* __restrict__ d
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = c0 + e < d ? S::load(q + e) : 0.0f;
   }
+}
+// their fp16 terms, in units
+template <bool BF16>
+__device__ __forceinline__ void store_terms(const float* v, float unit, uint16_t* to, int64_t r, int64_t ldp, int64_t c0) {
   mm_f16x8 hi, lo;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
@@ -285,7 +239,6 @@ __global__ void __launch_bounds__(256) k_loss_layout(const float* __restrict__ d
     hi[e] = static_cast<_Float16>(s);
     lo[e] = static_cast<_Float16>(s - static_cast<float>(hi[e]));
   }
-  uint16_t* const to = is_x ? xh : wh;
   if constexpr (BF16) {
     *reinterpret_cast<mm_f16x8*>(to + r * ldp + c0) = hi;
   } else {
@@ -295,19 +248,98 @@ __global__ void __launch_bounds__(256) k_loss_layout(const float* __restrict__ d
   }
 }
 
+// Lays out x and W in fp16 terms, rows of ldp values (fp32 data: 2 ldp, every
+// 32 high terms and their 32 low ones), zeros past d.  Workgroups [0, n1):
+// tokens, `lanes` lanes each: xh in units of the token (its inverse to ix), and
+// for the gradients xg, for dW, in the call's, and the token's coefficients.
+// The others W, 8 columns a thread.  The first writes the units.
+template <bool BF16>
+__global__ void __launch_bounds__(256) k_loss_layout(const float* __restrict__ dloss, const float* __restrict__ dlse,
+                                                     const float* __restrict__ lse, const void* __restrict__ targets,
+                                                     int target_bytes, int64_t ignore, int64_t N, int64_t V, int64_t d,
+                                                     float c, int64_t ldp, const void* __restrict__ x,
+                                                     const void* __restrict__ W, int n1, int lanes, int parts0, int parts1,
+                                                     int parts2, LossUnits* __restrict__ u, float* __restrict__ ix,
+                                                     RowCoef* __restrict__ coef, uint16_t* __restrict__ xh,
+                                                     uint16_t* __restrict__ xg, uint16_t* __restrict__ wh) {
+  __shared__ float w[4];
+  const int b = static_cast<int>(blockIdx.x), tid = threadIdx.x;
+  auto maximum = [&](int k, int parts) { return block_max(tid < parts ? u->parts[k][tid] : 0.0f, w); };
+  float iw;
+  const float unit_w = unit_of(maximum(2, parts2), &iw);
+  if (b >= n1) {
+    const int64_t C = ldp / 8, i = static_cast<int64_t>(b - n1) * 256 + tid;
+    if (i >= V * C) return;
+    const int64_t r = i / C, c0 = (i - r * C) * 8;
+    float v[8];
+    row8<BF16>(W, r, d, c0, v);
+    store_terms<BF16>(v, unit_w, wh, r, ldp, c0);
+    return;
+  }
+  float g = 1.0f, unit_g = 1.0f, ig = 1.0f;
+  if (xg) {
+    g = maximum(0, parts0);
+    if (g == 0.0f) g = 1.0f;
+    unit_g = unit_of(maximum(1, parts1), &ig);
+  }
+  if (b == 0 && tid == 0) {
+    u->g = g;
+    u->iw = iw;
+    u->back_x = iw / (1 << kUnit);
+    u->back_w = ig / (1 << kUnit);
+  }
+  const int64_t n = static_cast<int64_t>(b) * (256 / lanes) + tid / lanes;
+  if (n >= N) return;   // all lanes of a token
+  const int lane = tid % lanes;
+  float m = 0.0f;
+#pragma unroll 4
+  for (int64_t c0 = 8 * lane; c0 < d; c0 += 8 * lanes) {
+    float v[8];
+    row8<BF16>(x, n, d, c0, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = finite_max(m, v[e]);
+  }
+  for (int o = 1; o < lanes; o <<= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
+  float inverse;
+  const float unit = unit_of(m, &inverse);
+#pragma unroll 4
+  for (int64_t c0 = 8 * lane; c0 < ldp; c0 += 8 * lanes) {
+    float v[8];
+    row8<BF16>(x, n, d, c0, v);
+    store_terms<BF16>(v, unit, xh, n, ldp, c0);
+    if (xg) store_terms<BF16>(v, unit_g, xg, n, ldp, c0);
+  }
+  if (lane != 0) return;
+  ix[n] = inverse;
+  if (!xg) return;
+  const int64_t t = target_of(targets, target_bytes, n);
+  const float one = t == ignore ? 0.0f : dloss[n];
+  const float p = (dlse ? one + dlse[n] : one) / g;
+  RowCoef r;
+  r.c = copysignf(above_zero(c * iw * inverse), p);
+  r.one = one / g * (1 << kUnit);
+  // no such entry: the loss was NaN, and so is its gradient
+  const bool lost = t != ignore && (t < 0 || t >= V);
+  r.lse2 = lost ? __builtin_nanf("") : fmaf(lse[n], kLog2e, -log2f(fabsf(p))) - kUnit;   // p = 0: +inf, a row of zeros
+  r.target = t == ignore || lost ? -1 : static_cast<int32_t>(t);
+  coef[n] = r;
+}
+
 // ------------------------------------------------------------- forward ---
 
 // part[n][split] = (maximum, sum of 2^(c (z - maximum))) of token n over the
 // split's vocabulary tiles, z the plain products x W^T (F16: of the operands
-// in their units), c = s log2(e) > 0 (in those units).
+// in their units), c = s log2(e) > 0 (F16: in those units, the token's own).
 // A unit is a token tile and a split; four token tiles and their splits are
 // neighbours, so that an XCD's workgroups share the W tiles they walk (8 or 16
 // were 1 to 5% slower).
 template <class Tl, bool F16>
 __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_lse(MmOperand W, MmOperand X, int64_t N, int64_t V, int64_t d,
-                                                          float c, const LossUnits* __restrict__ units, int n_tok, int splits, int per_split,
-                                                          float2* __restrict__ part) {
-  if constexpr (F16) c = above_zero(c * units->back_z);
+                                                          float c_, const LossUnits* __restrict__ units,
+                                                          const float* __restrict__ ix, int n_tok, int splits,
+                                                          int per_split, float2* __restrict__ part) {
+  if constexpr (F16) c_ *= units->iw;
+  auto factor = [&](int64_t n) { return F16 ? above_zero(c_ * ix[imin(n, N - 1)]) : c_; };
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Tl::LDS];
   __shared__ float2 hand[Tl::WR][Tl::BN];
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, l32 = lane & 31;
@@ -344,9 +376,12 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_lse(MmOperand W, MmOperand
     const uint32_t t0 = split * per_split, t1 = min(t0 + per_split, v_tiles);
     // a lane's sums are taken against the maximum m of the first tile that
     // had one; a later maximum replaces it only when the sums grow large
-    float m[Tl::WN], s[Tl::WN];
+    float m[Tl::WN], s[Tl::WN], c[Tl::WN];
 #pragma unroll
-    for (int j = 0; j < Tl::WN; ++j) m[j] = s[j] = 0.0f;
+    for (int j = 0; j < Tl::WN; ++j) {
+      m[j] = s[j] = 0.0f;
+      c[j] = factor(n0 + (wc * Tl::WN + j) * 32 + l32);
+    }
     for (uint32_t t = t0; t < t1; ++t) {
       const int64_t v0 = static_cast<int64_t>(t) * Tl::BM;
       tile.template multiply<false, false, false, F16>(next);
@@ -367,10 +402,10 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_lse(MmOperand W, MmOperand
 #pragma unroll
           for (int i = 0; i < Tl::WM; ++i)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) q[r & 3] += ex2(fmaf(tile.acc[i][j][r], c, off));
+            for (int r = 0; r < 16; ++r) q[r & 3] += ex2(fmaf(tile.acc[i][j][r], c[j], off));
           return (q[0] + q[1]) + (q[2] + q[3]);
         };
-        float sum = sum_against(-m[j] * c);
+        float sum = sum_against(-m[j] * c[j]);
         // no maximum yet, or this tile's sum is out of proportion (or NaN)
         if (__builtin_amdgcn_ballot_w64(s[j] == 0.0f || !(sum < 0x1p60f))) {
           asm volatile("");   // a branch: taken once or twice a unit
@@ -381,9 +416,9 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_lse(MmOperand W, MmOperand
             for (int r = 0; r < 16; ++r) mx = fmaxf(mx, tile.acc[i][j][r]);
           if (s[j] != 0.0f) mx = fmaxf(mx, m[j]);
           mx = mx == -__builtin_inff() ? 0.0f : mx;   // any finite reference leaves the sum 0
-          s[j] *= ex2((m[j] - mx) * c);
+          s[j] *= ex2((m[j] - mx) * c[j]);
           m[j] = mx;
-          sum = sum_against(-mx * c);
+          sum = sum_against(-mx * c[j]);
         }
         s[j] += sum;
       }
@@ -396,7 +431,7 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_lse(MmOperand W, MmOperand
     for (int j = 0; j < Tl::WN; ++j) {
       const float mo = __shfl_xor(m[j], 32, 64), so = __shfl_xor(s[j], 32, 64);
       const float mx = fmaxf(m[j], mo), ref = mx == -__builtin_inff() ? 0.0f : mx;
-      const float a = s[j] * ex2((m[j] - ref) * c), b = so * ex2((mo - ref) * c);
+      const float a = s[j] * ex2((m[j] - ref) * c[j]), b = so * ex2((mo - ref) * c[j]);
       if (half == 0) hand[wr][(wc * Tl::WN + j) * 32 + l32] = make_float2(mx, a + b);
     }
     __syncthreads();
@@ -405,9 +440,10 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_lse(MmOperand W, MmOperand
 #pragma unroll
       for (int w = 1; w < Tl::WR; ++w) mx = fmaxf(mx, hand[w][e].x);
       const float ref = mx == -__builtin_inff() ? 0.0f : mx;
+      const float ce = factor(n0 + e);
       float sum = 0.0f;
 #pragma unroll
-      for (int w = 0; w < Tl::WR; ++w) sum += hand[w][e].y * ex2((hand[w][e].x - ref) * c);
+      for (int w = 0; w < Tl::WR; ++w) sum += hand[w][e].y * ex2((hand[w][e].x - ref) * ce);
       if (n0 + e < N) part[(n0 + e) * splits + split] = make_float2(mx, sum);
     }
     __syncthreads();
@@ -426,13 +462,14 @@ template <bool BF16>
 __global__ void __launch_bounds__(256) k_loss_join(const float2* __restrict__ part, int splits, const void* __restrict__ x,
                                                    const void* __restrict__ W, const void* __restrict__ targets,
                                                    int target_bytes, int64_t N, int64_t V, int64_t d, float scale,
-                                                   const LossUnits* __restrict__ units, int64_t ignore,
+                                                   const LossUnits* __restrict__ units, const float* __restrict__ ix,
+                                                   int64_t ignore,
                                                    float* __restrict__ loss, float* __restrict__ lse) {
   using S = Storage<BF16 ? kBF16 : kF32>;
   const int64_t n = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
   if (n >= N) return;
-  const float back = BF16 ? 1.0f : units->back_z, c = above_zero(scale * kLog2e * back);
+  const float back = BF16 ? 1.0f : units->iw * ix[n], c = above_zero(scale * kLog2e * back);
   const int64_t t = target_of(targets, target_bytes, n);
   const bool in = t >= 0 && t < V;
   // the pairs are on their way while the dot product waits for the target
@@ -486,11 +523,9 @@ __global__ void __launch_bounds__(256) k_loss_join(const float2* __restrict__ pa
 // does not: 4096 x 256 x 32000 252, dx 215, dW 229 us against 287, 209, 225.
 template <class Tl, bool BF16>
 __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_dz(MmOperand W, MmOperand X, int64_t N, int64_t V, int64_t d,
-                                                         float c, const LossUnits* __restrict__ units,
                                                          int64_t piece0, int64_t piece1, int n_tok,
                                                          const RowCoef* __restrict__ coef, uint16_t* __restrict__ dz,
                                                          int64_t ldz) {
-  c *= units->back_z;
   // the loads are up to NST tiles ahead (tiles of one stage)
   constexpr int kRing = Tl::NST + 1;
   static_assert(sizeof(RowCoef) == 16 && Tl::BN % 64 == 0 && Tl::BN / 64 <= Tl::NW, "one coefficient load per wave");
@@ -553,7 +588,8 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_dz(MmOperand W, MmOperand 
         const RowCoef rc = coefs[use][tl];
         // the target's row of this tile (negative or past the tile: elsewhere)
         const int at = rc.target < 0 ? -1 : static_cast<int>(imax(imin(rc.target - v0, 1 << 20), -1));
-        const bool negative = __builtin_amdgcn_ballot_w64(rc.sign < 0.0f) != 0;
+        const float c = fabsf(rc.c);
+        const bool negative = __builtin_amdgcn_ballot_w64(rc.c < 0.0f) != 0;
 #pragma unroll
         for (int i2 = 0; i2 < Tl::WM; ++i2) {
           const int vb = first_row + i2 * 32;   // the block's first row of the tile
@@ -563,7 +599,7 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_dz(MmOperand W, MmOperand 
           if (negative) {
             asm volatile("");   // branches: rarely taken
 #pragma unroll
-            for (int r = 0; r < 16; ++r) v[r] *= rc.sign;
+            for (int r = 0; r < 16; ++r) v[r] = rc.c < 0.0f ? -v[r] : v[r];
           }
           if (__builtin_amdgcn_ballot_w64(at >= vb && at < vb + 32)) {
             asm volatile("");
@@ -718,7 +754,7 @@ struct Plan {
   bool pad;
   int planes;            // terms of x, W and dz
   int64_t ldp;
-  size_t units_off, xp_off, wp_off, xh_off, wh_off, end;
+  size_t units_off, ix_off, xp_off, wp_off, xh_off, xg_off, wh_off, end;
 };
 // Rows laid out anew are whole lines of 128 bytes, or an even part of one: a
 // stage reads 128 bytes of every row, which other rows have in two lines (a
@@ -744,9 +780,11 @@ Plan plan_operands(const LossArgs& a, bool back) {
     return at;
   };
   p.units_off = take(terms, sizeof(LossUnits));
+  p.ix_off = take(terms, size_t(a.N) * 4);
   p.xp_off = take(p.pad, size_t(a.N) * p.ldp * 2);
   p.wp_off = take(p.pad, size_t(a.V) * p.ldp * 2);
   p.xh_off = take(terms, size_t(p.planes) * a.N * p.ldp * 2);
+  p.xg_off = take(back, size_t(p.planes) * a.N * p.ldp * 2);
   p.wh_off = take(terms, size_t(p.planes) * a.V * p.ldp * 2);
   p.end = off;
   return p;
@@ -869,11 +907,12 @@ PlanBw plan_bw(const LossArgs& a) {
   return b;
 }
 
-// The operands: X and Wo of the logits, Xh and Wh (fp16 terms) of dx and dW;
+// The operands: X and Wo of the logits, Wh of dx and Xg of dW (fp16 terms);
 // with `coef`, the tokens' coefficients.  For the forward dloss .. coef are null.
 struct Operands {
-  MmOperand X, Wo, Xh, Wh;
+  MmOperand X, Wo, Xg, Wh;
   LossUnits* units;
+  float* ix;
 };
 Operands lay_out(const LossArgs& a, const Plan& p, const void* x, const void* W, const void* targets, const float* lse,
                  const float* dloss, const float* dlse, RowCoef* coef) {
@@ -882,24 +921,25 @@ Operands lay_out(const LossArgs& a, const Plan& p, const void* x, const void* W,
   if (coef || !a.bf16) {
     auto parts = [](int64_t n) { return int(std::min<int64_t>(kMaxParts, cdiv(n, 1024))); };
     o.units = reinterpret_cast<LossUnits*>(a.ws + p.units_off);
-    o.Xh = {at(p.xh_off), p.planes * p.ldp};
-    o.Wh = {at(p.wh_off), p.planes * p.ldp};
-    const int p0 = coef ? parts(a.N) : 0, p1 = parts(cdiv(a.N * a.d, 8)), p2 = parts(cdiv(a.V * a.d, 8));
-    const int64_t nc = coef ? cdiv(a.N, 256) : 0, n1 = cdiv(a.N * (p.ldp / 8), 256), n2 = cdiv(a.V * (p.ldp / 8), 256);
+    o.ix = reinterpret_cast<float*>(a.ws + p.ix_off);
+    o.X = {at(p.xh_off), p.planes * p.ldp};
+    o.Xg = {at(p.xg_off), p.planes * p.ldp};
+    o.Wo = o.Wh = {at(p.wh_off), p.planes * p.ldp};
+    const int p0 = coef ? parts(a.N) : 0, p1 = coef ? parts(cdiv(a.N * a.d, 8)) : 0, p2 = parts(cdiv(a.V * a.d, 8));
+    const int lanes = a.d <= 256 ? 16 : 64;
+    const int64_t n1 = cdiv(a.N, 256 / lanes), n2 = cdiv(a.V * (p.ldp / 8), 256);
     auto go = [&](auto bf) {
       constexpr bool BF = decltype(bf)::value;
       k_loss_maxima<BF><<<unsigned(p0 + p1 + p2), 1024, 0, a.stream>>>(dloss, dlse, targets, a.target_bytes, a.ignore, a.N,
                                                                        a.V, a.d, x, W, p0, p1, p2, o.units);
-      k_loss_layout<BF><<<unsigned(nc + n1 + n2), 256, 0, a.stream>>>(
-          dloss, dlse, lse, targets, a.target_bytes, a.ignore, a.N, a.V, a.d, p.ldp, x, W, int(nc), int(n1), p0, p1, p2,
-          o.units, coef, at(p.xh_off), at(p.wh_off));
+      k_loss_layout<BF><<<unsigned(n1 + n2), 256, 0, a.stream>>>(
+          dloss, dlse, lse, targets, a.target_bytes, a.ignore, a.N, a.V, a.d, a.scale * kLog2e, p.ldp, x, W, int(n1), lanes,
+          p0, p1, p2, o.units, o.ix, coef, at(p.xh_off), coef ? at(p.xg_off) : nullptr, at(p.wh_off));
     };
     if (a.bf16) go(std::true_type{}); else go(std::false_type{});
   }
-  if (o.units) {
-    o.X = o.Xh;
-    o.Wo = o.Wh;
-  } else if (p.pad) {
+  if (o.units) return o;
+  if (p.pad) {
     auto pad = [&](const void* in, int64_t R, size_t off) {
       k_loss_pad<<<unsigned(cdiv(R * (p.ldp / 8), 256)), 256, 0, a.stream>>>(static_cast<const uint16_t*>(in), R, a.d, p.ldp,
                                                                              at(off));
@@ -934,7 +974,7 @@ void launch_loss(const LossArgs& a, const void* x, const void* W, const void* ta
     constexpr bool PAIR = decltype(pair)::value;
     auto run = [&](auto tl) {
       using Tl = decltype(tl);
-      k_loss_lse<Tl, PAIR><<<unsigned(f.grid), Tl::NTHR, 0, a.stream>>>(o.Wo, o.X, a.N, a.V, a.d, c, o.units, int(f.n_tok),
+      k_loss_lse<Tl, PAIR><<<unsigned(f.grid), Tl::NTHR, 0, a.stream>>>(o.Wo, o.X, a.N, a.V, a.d, c, o.units, o.ix, int(f.n_tok),
                                                                        int(f.splits), int(f.per_split), part);
     };
     if (f.kind == 0) run(Few<PAIR>{}); else if (f.kind == 1) run(Mid<PAIR>{}); else run(Big<PAIR>{});
@@ -943,10 +983,10 @@ void launch_loss(const LossArgs& a, const void* x, const void* W, const void* ta
   const unsigned jg = static_cast<unsigned>(cdiv(a.N, 4));
   if (a.bf16)
     k_loss_join<true><<<jg, 256, 0, a.stream>>>(part, int(f.splits), x, W, targets, a.target_bytes, a.N, a.V, a.d,
-                                                a.scale, o.units, a.ignore, loss, lse);
+                                                a.scale, o.units, o.ix, a.ignore, loss, lse);
   else
     k_loss_join<false><<<jg, 256, 0, a.stream>>>(part, int(f.splits), x, W, targets, a.target_bytes, a.N, a.V, a.d,
-                                                 a.scale, o.units, a.ignore, loss, lse);
+                                                 a.scale, o.units, o.ix, a.ignore, loss, lse);
 }
 
 void launch_loss_backward(const LossArgs& a, const void* x, const void* W, const void* targets, const float* lse,
@@ -960,7 +1000,6 @@ void launch_loss_backward(const LossArgs& a, const void* x, const void* W, const
     return;
   }
   const PlanBw b = plan_bw(a);
-  const float c = a.scale * kLog2e;
   RowCoef* coef = reinterpret_cast<RowCoef*>(a.ws + b.coef_off);
   uint16_t* dz = reinterpret_cast<uint16_t*>(a.ws + b.dz_off);
   float* px = reinterpret_cast<float*>(a.ws + b.px_off);
@@ -989,7 +1028,7 @@ void launch_loss_backward(const LossArgs& a, const void* x, const void* W, const
         using Tl = decltype(tl);
         const int64_t n_tok = cdiv(a.N, Tl::BN), tiles = n_tok * cdiv(nv, kBM), slots = (b.big_z ? 1 : mid_slots(BF)) * kCus;
         k_loss_dz<Tl, BF><<<unsigned(std::min(tiles, slots)), Tl::NTHR, 0, a.stream>>>(
-            o.Wo, o.X, a.N, a.V, a.d, c, units, v0, pend, int(n_tok), coef, dz, b.ldz);
+            o.Wo, o.X, a.N, a.V, a.d, v0, pend, int(n_tok), coef, dz, b.ldz);
       };
       if (b.big_z) run(Big<!BF>{}); else run(Mid<!BF>{});
     });
@@ -1023,7 +1062,7 @@ void launch_loss_backward(const LossArgs& a, const void* x, const void* W, const
       const MmOperand Wc{o.Wh.base + v0 * o.Wh.ld, o.Wh.ld};
       product(std::false_type{}, b.x, b.ldz, Wc, a.N, nv, v0 > 0, px, last, dx);
     }
-    if (dW) product(std::true_type{}, b.w, b.op.planes, o.Xh, nv, a.N, false, pw, true, static_cast<uint8_t*>(dW) + v0 * a.d * elt);
+    if (dW) product(std::true_type{}, b.w, b.op.planes, o.Xg, nv, a.N, false, pw, true, static_cast<uint8_t*>(dW) + v0 * a.d * elt);
   }
 }
 

@@ -96,6 +96,14 @@ def test_dz_is_rounded_once_to_fp16(N, V, d, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_one_large_token_leaves_the_others(dtype):
+    x, W, t, dloss, dlse = _inputs(140, 200, 64, dtype, 2)
+    x[3] *= 2.0 ** 44
+    rows = np.arange(140) != 3
+    _check(x, W, t, dloss, dlse, dtype, names=("loss", "lse", "dx"), rows=rows)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("sx,sw", [(1e-20, 1e-20), (1e-30, 1e-12), (1e-38, 1.0), (0.0, 1e-30), (1e-36, 1e-36)])
 def test_logits_below_the_range(dtype, sx, sw):
     """The logits are zero but for what fp32 cannot hold: the loss is log V."""
