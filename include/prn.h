@@ -465,11 +465,14 @@ prn_status prn_vocab_loss(const void* x, const void* W, const void* targets, con
  *   dx_out (N, d) = dz W, dW_out (V, d) = dz^T x: storage dtype, each optional
  *   lse     the forward's lse_out; dloss (N) fp32; dlse (N) fp32 or NULL: the
  *           gradients arriving at loss_out and lse_out
- * With bf16 storage dz is rounded once, to fp16 in units of the call's largest
- * coefficient, for the matrix cores; x and W go there as fp16 too, scaled by
- * powers of two (exactly; values below 2^-31 of the largest one are held to 2^-39
- * of that).  The logits take x in units of each token, dW takes it in x's, and W
- * goes in W's.  A target out of range gives NaN in its row of dx and in
+ * Every token's row of dz is held in units of the token's weight, max(|dloss|,
+ * |dloss + dlse|): with bf16 storage dz is rounded once, to fp16 (2^-11 of it),
+ * with fp32 storage to two fp16 terms (2^-22), and in both no finer than 2^-38 s
+ * weight (an entry of less likelihood than that is a zero).  x and W go to the
+ * matrix cores as fp16 too (two terms with fp32), scaled by powers of two: bf16
+ * values exactly; values far below the largest one (2^-31 of it with bf16, 2^-17
+ * with fp32) are held to 2^-39 of that.  The largest is that of the token for the
+ * logits, of W for W, and for dW of weight x over the tokens.  A target out of range gives NaN in its row of dx and in
  * dW.  x, W, dx_out and dW_out must be 16-byte aligned.  The workspace holds
  * one piece of dz (about 512 MB at most, or 512 bytes per token where that is
  * more; twice as much per entry with fp32), x twice and W once more in the matrix

@@ -29,11 +29,15 @@
 // where this takes 0.855 (4096 x 256 x 32000).
 // For fp16's range W is scaled by the power of two that takes its largest value
 // to 2^14 .. 2^15, every token's x by that of its own (so that a large token
-// leaves the others' logits alone; for dW, which sums over tokens, by x's), and
-// dz, in units of the largest |dloss|, |dloss + dlse|, by 2^13.  Values below
-// 2^-17 of the largest one lose the low bits of lo: at most 2^-39 of the largest,
-// half a step of 2^-24 over 2^14.  The units come back, in fp32, where they are
-// used.  Everything is summed in fp32 in a fixed order.
+// leaves the others' logits alone), and every token's row of dz, in units of its
+// weight, the power of two below the larger of |dloss| and |dloss + dlse|, by
+// 2^13 (so that a light token's row of dx is as good as a heavy one's).  dW, which
+// sums over tokens, takes x times the weight, scaled by the power of two of the
+// largest of these.  Values below 2^-17 of the largest one lose the low bits of
+// lo: at most 2^-39 of the largest, half a step of 2^-24 over 2^14; an entry of dz
+// is off by at most 2^-38 of its token's weight, half a step of 2^-24 over 2^13,
+// however small it is.  The units come back, in fp32, where they are used.
+// Everything is summed in fp32 in a fixed order.
 #include "vocab_loss.h"
 
 #include <algorithm>
@@ -117,11 +121,12 @@ constexpr int kUnit = 13;   // dz is stored times 2^13: fp16 has entries down to
 
 // The units of a call
 struct LossUnits {
-  float g;                         // dz is stored as 2^kUnit dz / (s g)
   float iw;                        // z = acc iw s times the token's inverse unit
-  float back_x, back_w;            // dx = acc back_x (s g), dW = acc back_w (s g)
-  float parts[3][kMaxParts];       // the workgroups' maxima: of dloss and dlse, x, W
+  float back_x;                    // dx = acc back_x s u, u the token's weight
+  int32_t back_w;                  // dW = acc 2^back_w s
+  float parts[2][kMaxParts];       // the workgroups' maxima: of the exponents of u x; of |W|
 };
+constexpr float kNoExponent = -1e4f;   // of nothing but zeros
 
 template <class T>
 __device__ __forceinline__ int64_t target_at(const void* targets, int64_t n) {
@@ -162,57 +167,23 @@ __device__ __forceinline__ void load8(const void* p, int64_t i, int64_t n, float
   }
 }
 
-// The maxima: workgroups [0, n0) of |dloss|, |dloss + dlse|, the next n1 of x
-// (for dW) and the last n2 of W.  Values that are not finite do not set a unit, they go
-// through as they are.
-template <bool BF16>
-__global__ void __launch_bounds__(1024) k_loss_maxima(const float* __restrict__ dloss, const float* __restrict__ dlse,
-                                                      const void* __restrict__ targets, int target_bytes, int64_t ignore,
-                                                      int64_t N, int64_t V, int64_t d, const void* __restrict__ x,
-                                                      const void* __restrict__ W, int n0, int n1, int n2,
-                                                      LossUnits* __restrict__ u) {
-  __shared__ float w[16];
-  int b = static_cast<int>(blockIdx.x);
-  float m = 0.0f;
-  if (b < n0) {
-    for (int64_t n = static_cast<int64_t>(b) * 1024 + threadIdx.x; n < N; n += static_cast<int64_t>(n0) * 1024) {
-      const float one = target_of(targets, target_bytes, n) == ignore ? 0.0f : dloss[n];
-      m = finite_max(m, one);
-      if (dlse) m = finite_max(m, one + dlse[n]);
-    }
-    m = block_max(m, w);
-    if (threadIdx.x == 0) u->parts[0][b] = m;
-    return;
-  }
-  b -= n0;
-  const bool is_x = b < n1;
-  if (!is_x) b -= n1;
-  const int64_t n = (is_x ? N : V) * d, step = static_cast<int64_t>(is_x ? n1 : n2) * 8192;
-  for (int64_t i = (static_cast<int64_t>(b) * 1024 + threadIdx.x) * 8; i < n; i += step) {
-    float v[8];
-    load8<BF16>(is_x ? x : W, i, n, v);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) m = finite_max(m, v[e]);
-  }
-  m = block_max(m, w);
-  if (threadIdx.x == 0) u->parts[is_x ? 1 : 2][b] = m;
-}
+__device__ __forceinline__ int exponent_of(float m) { return max(static_cast<int>(__float_as_uint(m) >> 23) - 127, -126); }
 
-// the power of two that takes a largest value m to 2^14 .. 2^15, and its inverse
-__device__ __forceinline__ float unit_of(float m, float* inverse) {
-  const int e = m > 0.0f ? static_cast<int>(__float_as_uint(m) >> 23) - 127 : 14;
-  const int k = min(max(14 - e, -126), 126);
-  *inverse = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
-  return __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
-}
-
-// A token's row of dz in its units: sign 2^(|c| acc - lse2) - one at the target.
-// The magnitude of (dloss + dlse) / g is folded into the exponent.
-struct RowCoef {
-  float c;              // s log2(e) times the units of its logits; the sign is that of (dloss + dlse)
-  float one, lse2;
-  int32_t target;       // -1: none
+// What arrives at a token's loss and at its lse and loss together, and its
+// weight u: the power of two below the larger one (0: neither, or not finite).
+// Its row of dz is stored as 2^kUnit dz / (s u), so that every token's row of
+// dx is as good as it would be alone.
+struct Arriving {
+  float one, both, u;
 };
+__device__ __forceinline__ Arriving arriving(const float* dloss, const float* dlse, int64_t n, bool ignored) {
+  Arriving a;
+  a.one = ignored ? 0.0f : dloss[n];
+  a.both = dlse ? a.one + dlse[n] : a.one;
+  const float m = finite_max(finite_max(0.0f, a.one), a.both);
+  a.u = m > 0.0f ? __uint_as_float(static_cast<uint32_t>(exponent_of(m) + 127) << 23) : 0.0f;
+  return a;
+}
 
 // eight values of row r from column c0 on, zeros past d
 template <bool BF16>
@@ -229,15 +200,74 @@ __device__ __forceinline__ void row8(const void* p, int64_t r, int64_t d, int64_
     for (int e = 0; e < 8; ++e) v[e] = c0 + e < d ? S::load(q + e) : 0.0f;
   }
 }
-// their fp16 terms, in units
+
+// The maxima: workgroups [0, n1) of the exponents of u x (for dW; `lanes`
+// lanes a token), the last n2 of W.  Values that are not finite do not set a
+// unit, they go through as they are.
 template <bool BF16>
-__device__ __forceinline__ void store_terms(const float* v, float unit, uint16_t* to, int64_t r, int64_t ldp, int64_t c0) {
+__global__ void __launch_bounds__(1024) k_loss_maxima(const float* __restrict__ dloss, const float* __restrict__ dlse,
+                                                      const void* __restrict__ targets, int target_bytes, int64_t ignore,
+                                                      int64_t N, int64_t V, int64_t d, const void* __restrict__ x,
+                                                      const void* __restrict__ W, int n1, int lanes, int n2,
+                                                      LossUnits* __restrict__ u) {
+  __shared__ float w[16];
+  int b = static_cast<int>(blockIdx.x);
+  if (b < n1) {
+    float top = kNoExponent;
+    const int lane = threadIdx.x % lanes, per = 1024 / lanes;
+    for (int64_t n = static_cast<int64_t>(b) * per + threadIdx.x / lanes; n < N; n += static_cast<int64_t>(n1) * per) {
+      const Arriving a = arriving(dloss, dlse, n, target_of(targets, target_bytes, n) == ignore);
+      float m = 0.0f;
+#pragma unroll 1
+      for (int64_t c0 = 8 * lane; c0 < d; c0 += 8 * lanes) {
+        float v[8];
+        row8<BF16>(x, n, d, c0, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = finite_max(m, v[e]);
+      }
+      if (m > 0.0f && a.u > 0.0f) top = fmaxf(top, static_cast<float>(exponent_of(m) + exponent_of(a.u)));
+    }
+    top = block_max(top, w);
+    if (threadIdx.x == 0) u->parts[0][b] = top;
+    return;
+  }
+  b -= n1;
+  float m = 0.0f;
+  const int64_t n = V * d;
+  for (int64_t i = (static_cast<int64_t>(b) * 1024 + threadIdx.x) * 8; i < n; i += static_cast<int64_t>(n2) * 8192) {
+    float v[8];
+    load8<BF16>(W, i, n, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = finite_max(m, v[e]);
+  }
+  m = block_max(m, w);
+  if (threadIdx.x == 0) u->parts[1][b] = m;
+}
+
+// the power of two that takes a largest value m to 2^14 .. 2^15, and its inverse
+__device__ __forceinline__ float unit_of(float m, float* inverse) {
+  const int e = m > 0.0f ? static_cast<int>(__float_as_uint(m) >> 23) - 127 : 14;
+  const int k = min(max(14 - e, -126), 126);
+  *inverse = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+  return __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
+}
+
+// A token's row of dz in its units: sign 2^(|c| acc - lse2) - one at the target.
+// The magnitude of (dloss + dlse) / u is folded into the exponent.
+struct RowCoef {
+  float c;              // s log2(e) times the units of its logits; the sign is that of (dloss + dlse)
+  float one, lse2;
+  int32_t target;       // -1: none
+};
+
+// eight values' fp16 terms, to row r from column c0 on
+template <bool BF16>
+__device__ __forceinline__ void store_terms(const float* v, uint16_t* to, int64_t r, int64_t ldp, int64_t c0) {
   mm_f16x8 hi, lo;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const float s = v[e] * unit;
-    hi[e] = static_cast<_Float16>(s);
-    lo[e] = static_cast<_Float16>(s - static_cast<float>(hi[e]));
+    hi[e] = static_cast<_Float16>(v[e]);
+    lo[e] = static_cast<_Float16>(v[e] - static_cast<float>(hi[e]));
   }
   if constexpr (BF16) {
     *reinterpret_cast<mm_f16x8*>(to + r * ldp + c0) = hi;
@@ -251,73 +281,89 @@ __device__ __forceinline__ void store_terms(const float* v, float unit, uint16_t
 // Lays out x and W in fp16 terms, rows of ldp values (fp32 data: 2 ldp, every
 // 32 high terms and their 32 low ones), zeros past d.  Workgroups [0, n1):
 // tokens, `lanes` lanes each: xh in units of the token (its inverse to ix), and
-// for the gradients xg, for dW, in the call's, and the token's coefficients.
-// The others W, 8 columns a thread.  The first writes the units.
+// for the gradients xg, for dW, times the token's weight u and in units of the
+// largest of these, u and the token's coefficients.  The others W, 8 columns a
+// thread.  The first writes the units.
 template <bool BF16>
 __global__ void __launch_bounds__(256) k_loss_layout(const float* __restrict__ dloss, const float* __restrict__ dlse,
                                                      const float* __restrict__ lse, const void* __restrict__ targets,
                                                      int target_bytes, int64_t ignore, int64_t N, int64_t V, int64_t d,
                                                      float c, int64_t ldp, const void* __restrict__ x,
-                                                     const void* __restrict__ W, int n1, int lanes, int parts0, int parts1,
-                                                     int parts2, LossUnits* __restrict__ u, float* __restrict__ ix,
-                                                     RowCoef* __restrict__ coef, uint16_t* __restrict__ xh,
+                                                     const void* __restrict__ W, int n1, int lanes, int parts1, int parts2,
+                                                     LossUnits* __restrict__ units, float* __restrict__ ix,
+                                                     float* __restrict__ weight, RowCoef* __restrict__ coef, uint16_t* __restrict__ xh,
                                                      uint16_t* __restrict__ xg, uint16_t* __restrict__ wh) {
   __shared__ float w[4];
   const int b = static_cast<int>(blockIdx.x), tid = threadIdx.x;
-  auto maximum = [&](int k, int parts) { return block_max(tid < parts ? u->parts[k][tid] : 0.0f, w); };
+  auto maximum = [&](int k, int parts, float least) { return block_max(tid < parts ? units->parts[k][tid] : least, w); };
   float iw;
-  const float unit_w = unit_of(maximum(2, parts2), &iw);
+  const float unit_w = unit_of(maximum(1, parts2, 0.0f), &iw);
   if (b >= n1) {
     const int64_t C = ldp / 8, i = static_cast<int64_t>(b - n1) * 256 + tid;
     if (i >= V * C) return;
     const int64_t r = i / C, c0 = (i - r * C) * 8;
     float v[8];
     row8<BF16>(W, r, d, c0, v);
-    store_terms<BF16>(v, unit_w, wh, r, ldp, c0);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= unit_w;
+    store_terms<BF16>(v, wh, r, ldp, c0);
     return;
   }
-  float g = 1.0f, unit_g = 1.0f, ig = 1.0f;
+  int shift = 0;   // xg = u x 2^shift
   if (xg) {
-    g = maximum(0, parts0);
-    if (g == 0.0f) g = 1.0f;
-    unit_g = unit_of(maximum(1, parts1), &ig);
+    const float top = maximum(0, parts1, kNoExponent);
+    shift = top > kNoExponent ? 14 - static_cast<int>(top) : 0;
   }
   if (b == 0 && tid == 0) {
-    u->g = g;
-    u->iw = iw;
-    u->back_x = iw / (1 << kUnit);
-    u->back_w = ig / (1 << kUnit);
+    units->iw = iw;
+    units->back_x = iw / (1 << kUnit);
+    units->back_w = -shift - kUnit;
   }
   const int64_t n = static_cast<int64_t>(b) * (256 / lanes) + tid / lanes;
   if (n >= N) return;   // all lanes of a token
   const int lane = tid % lanes;
-  float m = 0.0f;
-#pragma unroll 4
-  for (int64_t c0 = 8 * lane; c0 < d; c0 += 8 * lanes) {
-    float v[8];
-    row8<BF16>(x, n, d, c0, v);
+  float m = 0.0f, v[8];
+  row8<BF16>(x, n, d, 8 * lane, v);   // kept: most rows have no more
 #pragma unroll
-    for (int e = 0; e < 8; ++e) m = finite_max(m, v[e]);
+  for (int e = 0; e < 8; ++e) m = finite_max(m, v[e]);
+#pragma unroll 2
+  for (int64_t c0 = 8 * (lane + lanes); c0 < d; c0 += 8 * lanes) {
+    float o[8];
+    row8<BF16>(x, n, d, c0, o);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = finite_max(m, o[e]);
   }
   for (int o = 1; o < lanes; o <<= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
   float inverse;
   const float unit = unit_of(m, &inverse);
-#pragma unroll 4
+  Arriving in{};
+  int64_t t = 0;
+  if (xg) {
+    t = target_of(targets, target_bytes, n);
+    in = arriving(dloss, dlse, n, t == ignore);
+    shift += exponent_of(in.u);
+  }
+#pragma unroll 2
   for (int64_t c0 = 8 * lane; c0 < ldp; c0 += 8 * lanes) {
-    float v[8];
-    row8<BF16>(x, n, d, c0, v);
-    store_terms<BF16>(v, unit, xh, n, ldp, c0);
-    if (xg) store_terms<BF16>(v, unit_g, xg, n, ldp, c0);
+    float s[8];
+    if (c0 >= 8 * lanes) row8<BF16>(x, n, d, c0, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[e] = v[e] * unit;
+    store_terms<BF16>(s, xh, n, ldp, c0);
+    if (xg) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s[e] = in.u > 0.0f ? ldexpf(v[e], shift) : v[e] * 0.0f;
+      store_terms<BF16>(s, xg, n, ldp, c0);
+    }
   }
   if (lane != 0) return;
   ix[n] = inverse;
   if (!xg) return;
-  const int64_t t = target_of(targets, target_bytes, n);
-  const float one = t == ignore ? 0.0f : dloss[n];
-  const float p = (dlse ? one + dlse[n] : one) / g;
+  weight[n] = in.u;
+  const float u = in.u > 0.0f ? in.u : 1.0f, p = in.both / u;
   RowCoef r;
   r.c = copysignf(above_zero(c * iw * inverse), p);
-  r.one = one / g * (1 << kUnit);
+  r.one = in.one / u * (1 << kUnit);
   // no such entry: the loss was NaN, and so is its gradient
   const bool lost = t != ignore && (t < 0 || t >= V);
   r.lse2 = lost ? __builtin_nanf("") : fmaf(lse[n], kLog2e, -log2f(fabsf(p))) - kUnit;   // p = 0: +inf, a row of zeros
@@ -659,6 +705,15 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_dz(MmOperand W, MmOperand 
   }
 }
 
+// a sum of dx (or dW) from its units: dx's are the token's, of weight u
+template <bool IS_W>
+__device__ __forceinline__ float loss_finish(float v, const LossUnits* units, float u, float scale) {
+  if constexpr (IS_W)
+    return ldexpf(v * scale, units->back_w);
+  else
+    return v * units->back_x * (u * scale);
+}
+
 // P[z][r][c] (+)= sum over k of slice z of A(r, k) B(c, k), fp32, C columns; or,
 // with `out`, the last of the sums times its units, rounded once to out[r][c].
 // One workgroup per tile and slice, neighbours on one XCD.
@@ -666,7 +721,8 @@ template <class Tl, bool TA, bool BF16>
 __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_mm(MmOperand A, MmOperand B, int64_t R, int64_t C, int64_t K,
                                                          int64_t k_slice, int n_col, int slices, int add,
                                                          float* __restrict__ P, void* __restrict__ out,
-                                                         const LossUnits* __restrict__ units, float scale) {
+                                                         const LossUnits* __restrict__ units,
+                                                         const float* __restrict__ weight, float scale) {
   using T = typename Storage<BF16 ? kBF16 : kF32>::T;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Tl::LDS];
   const uint32_t u = Units(gridDim.x).u, tiles = gridDim.x / slices, z = u / tiles, ti = u - z * tiles;
@@ -702,11 +758,16 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_mm(MmOperand A, MmOperand 
     tile.clear();
   }
   tile.template multiply<TA, true, true, true>(next);
-  const float back = out ? (TA ? units->back_w : units->back_x) : 1.0f, f = out ? units->g * scale : 1.0f;
   T* const obase = static_cast<T*>(out) + r0 * C + c0;
   const uint32_t oat = rl * static_cast<uint32_t>(C) + cl;
 #pragma unroll
-  for (int i = 0; i < Tl::WM; ++i)
+  for (int i = 0; i < Tl::WM; ++i) {
+    float u[16];   // the rows' weights (there are some for a whole tile)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float4 f = !TA && out ? *reinterpret_cast<const float4*>(weight + r0 + rl + 32 * i + 8 * q) : float4{};
+      u[4 * q] = f.x, u[4 * q + 1] = f.y, u[4 * q + 2] = f.z, u[4 * q + 3] = f.w;
+    }
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
       const int ri = 32 * i + 8 * (r >> 2) + (r & 3);
@@ -714,24 +775,27 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_mm(MmOperand A, MmOperand 
       for (int j = 0; j < Tl::WN; ++j) {
         if (rl + ri < rows && cl + 32 * j < cols) {
           if (out)
-            obase[oat + ri * static_cast<uint32_t>(C) + 32 * j] = Storage<BF16 ? kBF16 : kF32>::pack(tile.acc[i][j][r] * back * f);
+            obase[oat + ri * static_cast<uint32_t>(C) + 32 * j] =
+                Storage<BF16 ? kBF16 : kF32>::pack(loss_finish<TA>(tile.acc[i][j][r], units, u[r], scale));
           else
             *reinterpret_cast<float*>(base + (at + ri * ldb + 128 * j)) = tile.acc[i][j][r];
         }
       }
     }
+  }
 }
 
-// out[i] = the sum over z, in order, of P[z][i], times its units, rounded once
-template <bool BF16>
-__global__ void __launch_bounds__(256) k_loss_out(const float* __restrict__ P, int S, int64_t n,
-                                                  const LossUnits* __restrict__ units, int is_w, float scale,
+// out[i] = the sum over z, in order, of P[z][i], from its units, rounded once
+template <bool BF16, bool IS_W>
+__global__ void __launch_bounds__(256) k_loss_out(const float* __restrict__ P, int S, int64_t n, int64_t d,
+                                                  const LossUnits* __restrict__ units,
+                                                  const float* __restrict__ weight, float scale,
                                                   typename Storage<BF16 ? kBF16 : kF32>::T* __restrict__ out) {
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (i >= n) return;
   float sum = 0.0f;
   for (int z = 0; z < S; ++z) sum += P[z * n + i];
-  out[i] = Storage<BF16 ? kBF16 : kF32>::pack(sum * (is_w ? units->back_w : units->back_x) * (units->g * scale));
+  out[i] = Storage<BF16 ? kBF16 : kF32>::pack(loss_finish<IS_W>(sum, units, IS_W ? 1.0f : weight[i / d], scale));
 }
 
 template <class T>
@@ -754,7 +818,7 @@ struct Plan {
   bool pad;
   int planes;            // terms of x, W and dz
   int64_t ldp;
-  size_t units_off, ix_off, xp_off, wp_off, xh_off, xg_off, wh_off, end;
+  size_t units_off, ix_off, weight_off, xp_off, wp_off, xh_off, xg_off, wh_off, end;
 };
 // Rows laid out anew are whole lines of 128 bytes, or an even part of one: a
 // stage reads 128 bytes of every row, which other rows have in two lines (a
@@ -781,6 +845,7 @@ Plan plan_operands(const LossArgs& a, bool back) {
   };
   p.units_off = take(terms, sizeof(LossUnits));
   p.ix_off = take(terms, size_t(a.N) * 4);
+  p.weight_off = take(back, size_t(cdiv(a.N, kBM)) * kBM * 4);
   p.xp_off = take(p.pad, size_t(a.N) * p.ldp * 2);
   p.wp_off = take(p.pad, size_t(a.V) * p.ldp * 2);
   p.xh_off = take(terms, size_t(p.planes) * a.N * p.ldp * 2);
@@ -912,7 +977,7 @@ PlanBw plan_bw(const LossArgs& a) {
 struct Operands {
   MmOperand X, Wo, Xg, Wh;
   LossUnits* units;
-  float* ix;
+  float *ix, *weight;
 };
 Operands lay_out(const LossArgs& a, const Plan& p, const void* x, const void* W, const void* targets, const float* lse,
                  const float* dloss, const float* dlse, RowCoef* coef) {
@@ -922,19 +987,20 @@ Operands lay_out(const LossArgs& a, const Plan& p, const void* x, const void* W,
     auto parts = [](int64_t n) { return int(std::min<int64_t>(kMaxParts, cdiv(n, 1024))); };
     o.units = reinterpret_cast<LossUnits*>(a.ws + p.units_off);
     o.ix = reinterpret_cast<float*>(a.ws + p.ix_off);
+    o.weight = reinterpret_cast<float*>(a.ws + p.weight_off);
     o.X = {at(p.xh_off), p.planes * p.ldp};
     o.Xg = {at(p.xg_off), p.planes * p.ldp};
     o.Wo = o.Wh = {at(p.wh_off), p.planes * p.ldp};
-    const int p0 = coef ? parts(a.N) : 0, p1 = coef ? parts(cdiv(a.N * a.d, 8)) : 0, p2 = parts(cdiv(a.V * a.d, 8));
-    const int lanes = a.d <= 256 ? 16 : 64;
+    const int lanes = a.d <= 128 ? 16 : 64;
+    const int p1 = coef ? parts(a.N * lanes) : 0, p2 = parts(cdiv(a.V * a.d, 8));
     const int64_t n1 = cdiv(a.N, 256 / lanes), n2 = cdiv(a.V * (p.ldp / 8), 256);
     auto go = [&](auto bf) {
       constexpr bool BF = decltype(bf)::value;
-      k_loss_maxima<BF><<<unsigned(p0 + p1 + p2), 1024, 0, a.stream>>>(dloss, dlse, targets, a.target_bytes, a.ignore, a.N,
-                                                                       a.V, a.d, x, W, p0, p1, p2, o.units);
+      k_loss_maxima<BF><<<unsigned(p1 + p2), 1024, 0, a.stream>>>(dloss, dlse, targets, a.target_bytes, a.ignore, a.N,
+                                                                       a.V, a.d, x, W, p1, lanes, p2, o.units);
       k_loss_layout<BF><<<unsigned(n1 + n2), 256, 0, a.stream>>>(
           dloss, dlse, lse, targets, a.target_bytes, a.ignore, a.N, a.V, a.d, a.scale * kLog2e, p.ldp, x, W, int(n1), lanes,
-          p0, p1, p2, o.units, o.ix, coef, at(p.xh_off), coef ? at(p.xg_off) : nullptr, at(p.wh_off));
+          p1, p2, o.units, o.ix, o.weight, coef, at(p.xh_off), coef ? at(p.xg_off) : nullptr, at(p.wh_off));
     };
     if (a.bf16) go(std::true_type{}); else go(std::false_type{});
   }
@@ -1006,12 +1072,10 @@ void launch_loss_backward(const LossArgs& a, const void* x, const void* W, const
   float* pw = reinterpret_cast<float*>(a.ws + b.pw_off);
   const Operands o = lay_out(a, b.op, x, W, targets, lse, dloss, dlse, coef);
   LossUnits* const units = o.units;
-  auto out = [&](const float* P, int S, int64_t n, int is_w, void* to) {
-    const unsigned grid = unsigned(cdiv(n, 256));
-    if (a.bf16)
-      k_loss_out<true><<<grid, 256, 0, a.stream>>>(P, S, n, units, is_w, a.scale, static_cast<uint16_t*>(to));
-    else
-      k_loss_out<false><<<grid, 256, 0, a.stream>>>(P, S, n, units, is_w, a.scale, static_cast<float*>(to));
+  auto out = [&](auto bf, auto is_w, const float* P, int S, int64_t n, const float* weight, void* to) {
+    constexpr bool BF = decltype(bf)::value, IS_W = decltype(is_w)::value;
+    k_loss_out<BF, IS_W><<<unsigned(cdiv(n, 256)), 256, 0, a.stream>>>(P, S, n, a.d, units, weight, a.scale,
+                                                                       static_cast<typename Storage<BF ? kBF16 : kF32>::T*>(to));
   };
   auto typed = [&](auto run) {
     if (a.bf16) run(std::true_type{}); else run(std::false_type{});
@@ -1048,11 +1112,11 @@ void launch_loss_backward(const LossArgs& a, const void* x, const void* W, const
             using Tl = decltype(tl);
             const int64_t n_col = cdiv(a.d, Tl::BN);
             k_loss_mm<Tl, TA, BF><<<unsigned(cdiv(n, kBM) * n_col * s), Tl::NTHR, 0, a.stream>>>(
-                A, B, n, a.d, K, len, int(n_col), int(s), add, sums, finish && s == 1 ? dst : nullptr, units, a.scale);
+                A, B, n, a.d, K, len, int(n_col), int(s), add, sums, finish && s == 1 ? dst : nullptr, units, o.weight + r0, a.scale);
           };
           if (b.out == kBig) run(Big<!BF>{}); else run(Wide<!BF>{});
+          if (finish && s > 1) out(bf, ta, sums, int(s), n * a.d, o.weight + r0, dst);
         });
-        if (finish && s > 1) out(sums, int(s), n * a.d, TA, dst);
       };
       const int64_t head = std::min(c.head, rows);
       part(0, head, 1, cdiv(K, 64) * 64, P);

@@ -96,6 +96,17 @@ def test_dz_is_rounded_once_to_fp16(N, V, d, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("with_dlse", [False, True])
+def test_tokens_of_unequal_weight(dtype, with_dlse):
+    """dloss from 1 down to 1e-12, and one token without any: every row of dx is as good as alone."""
+    x, W, t, dloss, dlse = _inputs(260, 700, 48, dtype, 1)
+    w = 10.0 ** -(torch.arange(260, device="cuda") % 13).float()
+    w[7] = 0
+    _check(x, W, t, dloss * w, dlse * w if with_dlse else None, dtype)
+    _check(x, W, t, -dloss * w * 2.0 ** 20, dlse * w if with_dlse else None, dtype, scale=0.3)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_one_large_token_leaves_the_others(dtype):
     x, W, t, dloss, dlse = _inputs(140, 200, 64, dtype, 2)
     x[3] *= 2.0 ** 44
