@@ -41,6 +41,14 @@ def _weight(t):
     return t if t.is_contiguous() else t.contiguous()
 
 
+def _shaped(shape, **tensors):
+    """Refuses a tensor of another shape: rows are flattened, so that one of as many rows in another order would
+    be taken for the right one."""
+    for name, t in tensors.items():
+        if t is not None and t.shape != shape:
+            raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+
+
 def _scratch(n: int, device) -> torch.Tensor:
     return torch.empty(max(n, 1), dtype=torch.uint8, device=device)
 
@@ -64,8 +72,7 @@ def embed_backward(dout, tokens, V: int, *, scale: float = 1.0, pad_id=None) -> 
     and fp32 (bitwise reproducible); rows of absent tokens are zeros."""
     ids = _flat(tokens)
     d = dout.shape[-1]
-    if dout.shape[:-1] != tokens.shape:
-        raise ValueError(f"dout {tuple(dout.shape)} does not belong to tokens {tuple(tokens.shape)}")
+    _shaped((*tokens.shape, d), dout=dout)
     dout = dout.reshape(-1, d).contiguous()
     dtable = torch.empty((V, d), dtype=dout.dtype, device=dout.device)
     ws = _scratch(B_.prn_embed_backward_workspace_bytes(dout.dtype, ids.numel(), V, d), dout.device)
@@ -103,6 +110,7 @@ def block_norm(h, x=None, *, gate=None, w_post=None, w_pre=None, alpha=None, act
     identity, n is None without w_pre).  With w_pre alone r is h itself: the
     norm before the first block."""
     shape = h.shape
+    _shaped(shape, x=x, gate=gate)
     h2, x2, g2 = _rows(h), _rows(x), _rows(gate)
     w_post, w_pre, alpha = _weight(w_post), _weight(w_pre), _weight(alpha)
     same = x2 is None and g2 is None and w_post is None and alpha is None
@@ -121,6 +129,7 @@ def block_norm_backward(dr, dn, h, x=None, *, gate=None, w_post=None, w_pre=None
     """Gradients of block_norm from dr = dL/dr (None for zero) and dn = dL/dn (None without w_pre):
     (dh, dx, dgate, dw_post, dw_pre, dalpha), None where the input is absent; the weights' are fp32."""
     shape = h.shape
+    _shaped(shape, x=x, gate=gate, dr=dr, dn=dn)
     h2, x2, g2, dr2, dn2 = _rows(h), _rows(x), _rows(gate), _rows(dr), _rows(dn)
     w_post, w_pre, alpha = _weight(w_post), _weight(w_pre), _weight(alpha)
     dh, dx, dgate = (None if t is None else torch.empty_like(h2) for t in (h2, x2, g2))
@@ -168,6 +177,9 @@ def vocab_loss(x, W, targets, *, scale: float = 1.0, ignore_index: int = -100):
     x (..., d), W (V, d), targets (...) int32 or int64.  Returns (loss, lse), fp32, shaped like targets; loss is 0
     where targets == ignore_index and NaN where a target is out of range; lse is the log of the summed
     exponentials (-loss is the target's log probability)."""
+    _shaped(x.shape[:-1], targets=targets)
+    if W.dim() != 2:
+        raise ValueError(f"W must have 2 dimensions, got {tuple(W.shape)}")
     x2, W, ids = _rows(x), _rows(W), _flat(targets)
     loss = torch.empty(x2.shape[0], dtype=torch.float32, device=x2.device)
     lse = torch.empty_like(loss)
@@ -180,6 +192,9 @@ def vocab_loss_backward(dloss, x, W, targets, lse, *, dlse=None, scale: float = 
                         want_x: bool = True, want_W: bool = True):
     """Gradients (dx, dW) of vocab_loss from dloss and dlse (None for zero), both shaped like targets; each only if
     wanted, else None.  The logits are formed again, a piece of the vocabulary at a time."""
+    _shaped(x.shape[:-1], targets=targets, lse=lse, dloss=dloss, dlse=dlse)
+    if W.dim() != 2:
+        raise ValueError(f"W must have 2 dimensions, got {tuple(W.shape)}")
     x2, W, ids = _rows(x), _rows(W), _flat(targets)
     dloss, lse = _flat(_weight(dloss)), _flat(_weight(lse))
     dlse = None if dlse is None else _flat(_weight(dlse))

@@ -159,3 +159,25 @@ def test_python_refusals_without_a_gpu():
         lm.vocab_loss(cpu, cpu, ids)
     with pytest.raises(ValueError):
         lm.embed_backward(torch.zeros(3, 8), ids, 4)
+
+
+def test_tensors_of_as_many_rows_in_another_order_are_refused():
+    """Rows are flattened: a (T, B) tensor beside a (B, T) one would pair the wrong rows."""
+    x, W, t = torch.zeros(2, 3, 8), torch.zeros(5, 8), torch.zeros(3, 2, dtype=torch.int64)
+    good = torch.zeros(2, 3, dtype=torch.int64)
+    for call in (lambda: lm.vocab_loss(x, W, t), lambda: lm.vocab_loss(x, W, good.view(-1)),
+                 lambda: lm.vocab_loss(x, W.view(5, 1, 8), good), lambda: lm.vocab_loss_apply(x, W, t)):
+        with pytest.raises(ValueError):
+            call()
+    f = torch.zeros(2, 3)
+    for dloss, targets, lse, dlse in ((f.t(), good, f, None), (f, t, f, None), (f, good, f.t(), None), (f, good, f, f.t())):
+        with pytest.raises(ValueError):
+            lm.vocab_loss_backward(dloss, x, W, targets, lse, dlse=dlse)
+    y, w = x.transpose(0, 1), torch.ones(8)
+    for call in (lambda: lm.block_norm(x, y), lambda: lm.block_norm(x, gate=y), lambda: lm.block_norm_apply(x, y, w_pre=w),
+                 lambda: lm.block_norm_backward(y, None, x, gate=x), lambda: lm.block_norm_backward(None, y, x, w_pre=w),
+                 lambda: lm.block_norm_backward(x, None, x, y), lambda: lm.block_norm_backward(x, None, x, gate=y)):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(ValueError):
+        lm.embed_backward(y, good, 5)
