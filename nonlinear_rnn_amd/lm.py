@@ -149,7 +149,7 @@ class _BlockNormFunction(torch.autograd.Function):
         ctx.act, ctx.eps = act, eps
         ctx.set_materialize_grads(False)
         r, n = block_norm(h, x, gate=gate, w_post=w_post, w_pre=w_pre, alpha=alpha, act=act, eps=eps)
-        return (r.clone() if r is h else r), n
+        return (None if r is h else r), n   # the stream itself is not an output
 
     @staticmethod
     def backward(ctx, dr, dn):

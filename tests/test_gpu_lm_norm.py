@@ -226,3 +226,16 @@ def test_in_place_at_widths_whose_last_chunk_crosses_waves(N, d, dtype):
                 r, m = (hh, xx) if over == "h" else (xx, hh)
                 B.prn_block_norm(hh, g, xx, r, m, **weights)
                 assert torch.equal(r, want[0]) and torch.equal(m, want[1]), (parts, over)
+
+
+def test_the_norm_before_the_first_block_copies_nothing():
+    """n is all that the differentiable form allocates: the stream goes on as it is."""
+    y, w = torch.randn(4096, 512, device="cuda", requires_grad=True), torch.ones(512, device="cuda")
+    prn.block_norm_apply(y, w_pre=w)
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    r, n = prn.block_norm_apply(y, w_pre=w)
+    assert r is y and torch.cuda.max_memory_allocated() - before < 1.5 * y.numel() * 4
+    (n * 2).sum().backward()
+    assert torch.equal(y.grad, prn.block_norm_backward(None, torch.full_like(n, 2.0), y.detach(), w_pre=w)[0])
