@@ -6,7 +6,7 @@ As in ``api``: strided views (and views that do not start on 16 bytes) are
 copied to a dense layout first, outputs and workspaces are allocated here, the
 arithmetic is the library's.  Leading dimensions are rows: tokens of any
 shape, activations (..., d).  The plain functions compute one direction; the
-``*_apply`` functions are differentiable.
+``*_apply`` functions are differentiable, once: a second derivative raises.
 """
 from __future__ import annotations
 
@@ -53,6 +53,29 @@ def _scratch(n: int, device) -> torch.Tensor:
     return torch.empty(max(n, 1), dtype=torch.uint8, device=device)
 
 
+class _FirstDerivatives(torch.autograd.Function):
+    """Copies of gradients, and an error where a derivative of theirs is asked for."""
+
+    @staticmethod
+    def forward(ctx, count, *tensors):
+        return tuple(t.clone() for t in tensors[:count])
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("the token-model operators have first derivatives only")
+
+
+def _first(grads, *sources):
+    """A backward pass's gradients.  Under create_graph they would come without a graph, and a derivative of theirs
+    would silently lack this operator's part: it raises instead."""
+    sources = [s for s in sources if s is not None and s.requires_grad]
+    if not torch.is_grad_enabled() or not sources:
+        return grads
+    given = [g for g in grads if g is not None]
+    tied = iter(_FirstDerivatives.apply(len(given), *given, *sources))
+    return tuple(None if g is None else next(tied) for g in grads)
+
+
 # ------------------------------------------------------------------ embedding lookup ---
 
 def embed(tokens, table, *, scale: float = 1.0, pad_id=None) -> torch.Tensor:
@@ -90,7 +113,8 @@ class _EmbedFunction(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dout):
         tokens, = ctx.saved_tensors
-        return None, embed_backward(dout.to(ctx.dtype), tokens, ctx.V, scale=ctx.scale, pad_id=ctx.pad_id), None, None
+        dtable = embed_backward(dout.to(ctx.dtype), tokens, ctx.V, scale=ctx.scale, pad_id=ctx.pad_id)
+        return None, *_first((dtable,), dout), None, None
 
 
 def embed_apply(tokens, table, *, scale: float = 1.0, pad_id=None) -> torch.Tensor:
@@ -157,8 +181,10 @@ class _BlockNormFunction(torch.autograd.Function):
         if w_pre is not None and dn is None:
             dn = torch.zeros_like(h)
         dr, dn = (None if t is None else t.to(h.dtype) for t in (dr, dn))
-        return (*block_norm_backward(dr, dn, h, x, gate=gate, w_post=w_post, w_pre=w_pre, alpha=alpha, act=ctx.act,
-                                     eps=ctx.eps), None, None)
+        dh, dx, dgate, dw_post, dw_pre, dalpha = _first(
+            block_norm_backward(dr, dn, h, x, gate=gate, w_post=w_post, w_pre=w_pre, alpha=alpha, act=ctx.act,
+                                eps=ctx.eps), dr, dn, h, x, gate, w_post, w_pre, alpha)
+        return dh, dx, dgate, dw_post, dw_pre, dalpha, None, None
 
 
 def block_norm_apply(h, x=None, *, gate=None, w_post=None, w_pre=None, alpha=None, act: str = "silu",
@@ -223,7 +249,7 @@ class _VocabLossFunction(torch.autograd.Function):
         dx, dW = vocab_loss_backward(dloss, x, W, targets, lse, dlse=dlse, scale=ctx.scale,
                                      ignore_index=ctx.ignore_index, want_x=ctx.needs_input_grad[0],
                                      want_W=ctx.needs_input_grad[1])
-        return dx, dW, None, None, None
+        return *_first((dx, dW), dloss, dlse, x, W), None, None, None
 
 
 def vocab_loss_apply(x, W, targets, *, scale: float = 1.0, ignore_index: int = -100):

@@ -101,3 +101,37 @@ def test_a_few_steps_learn(dtype):
     tokens, targets = ex.chain(8, 128, 200, torch.Generator(device="cuda").manual_seed(6))
     losses = ex.train(model, tokens, targets, 40)
     assert losses[-1] < 0.7 * losses[0]
+
+
+def _losses():
+    """(name, leaves, loss) of each differentiable operator."""
+    import nonlinear_rnn_amd as prn
+    g = torch.Generator(device="cuda").manual_seed(7)
+    new = lambda *s: torch.randn(*s, generator=g, device="cuda", requires_grad=True)   # noqa: E731
+    ids = torch.randint(0, 30, (12,), generator=g, device="cuda")
+    table, x, h, gate, w = new(30, 16), new(12, 16), new(12, 16), new(12, 16), new(16)
+    yield "embed", (table,), lambda: prn.embed_apply(ids, table).square().sum()
+    yield "norm", (x, h, gate, w), lambda: sum(y.square().sum() for y in prn.block_norm_apply(
+        h, x, gate=gate, w_post=w, w_pre=w, alpha=w))
+    yield "norm before", (h, w), lambda: prn.block_norm_apply(h, w_pre=w)[1].square().sum()
+    # a gradient that arrives without a graph of its own
+    yield "loss", (x, table), lambda: prn.vocab_loss_apply(x, table, ids)[0].sum()
+    yield "lse", (x, table), lambda: prn.vocab_loss_apply(x, table, ids)[1].square().sum()
+
+
+def test_a_second_derivative_raises():
+    """It would lack the operators' parts of it without a sign; the first derivatives are the same either way."""
+    for name, leaves, loss in _losses():
+        plain = torch.autograd.grad(loss(), leaves)
+        total = loss()
+        grads = torch.autograd.grad(total, leaves, create_graph=True)
+        assert all(torch.equal(a, b) for a, b in zip(plain, grads)), name
+        with pytest.raises(RuntimeError, match="first derivatives only"):
+            (total + sum(g.square().sum() for g in grads)).backward()
+        # gradients that are only kept
+        loss().backward(create_graph=True)
+        for p, g in zip(leaves, plain):
+            with torch.no_grad():
+                p.grad.mul_(0.5)
+            assert torch.equal(p.grad, 0.5 * g), name
+            p.grad = None
