@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(256) k_embed(const void* __restrict__ tokens, 
                                                const typename Storage<DT>::T* __restrict__ table, int64_t N, int64_t V,
                                                int64_t d, float scale, int64_t pad,
                                                typename Storage<DT>::T* __restrict__ out) {
-  const int64_t n0 = (static_cast<int64_t>(blockIdx.x) * (256 / TPR) + threadIdx.x / TPR) * kRows;
+  const int64_t n0 = (block_in_rows() * (256 / TPR) + threadIdx.x / TPR) * kRows;
   int64_t tok[kRows];
 #pragma unroll
   for (int q = 0; q < kRows; ++q) tok[q] = n0 + q < N ? token_at(tokens, token_bytes, n0 + q) : -1;
@@ -288,7 +288,7 @@ __device__ __forceinline__ void walk_rows(const typename Storage<DT>::T* dout, i
   }
 }
 
-// A wave per kBlock sorted positions and 64 VEC channels (blockIdx.y): sums
+// A wave per kBlock sorted positions and 64 VEC channels (blockIdx.z): sums
 // every token whose rows start there, and the chunk of a frequent token from
 // an earlier block that starts there (at most one: chunks are kLong >= kBlock
 // apart).  A frequent token's chunks go to part: its first to row 2 block + 1,
@@ -302,10 +302,10 @@ __global__ void __launch_bounds__(256) k_embed_sum(const uint32_t* __restrict__ 
                                                    float* __restrict__ part) {
   constexpr uint32_t kNone = 0xffffffffu;   // above every key
   const int lane = threadIdx.x & 63;
-  const int64_t block = static_cast<int64_t>(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t block = block_in_rows() * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t p0 = block * kBlock;
   if (p0 >= N) return;
-  const int64_t c0 = (static_cast<int64_t>(blockIdx.y) * 64 + lane) * VEC, c = imin(c0, d - VEC);
+  const int64_t c0 = (static_cast<int64_t>(blockIdx.z) * 64 + lane) * VEC, c = imin(c0, d - VEC);
   const bool mine = c0 < d;
   // lane t + 1: place t (position p0 + t), the place before p0 in lane 0
   static_assert(kBlock + kLong <= 63, "the places fit a wave");
@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(256) k_embed_sum(const uint32_t* __restrict__ 
 }
 
 // The frequent tokens that start among kJoin sorted positions: their chunks'
-// sums at 64 CPT channels (blockIdx.y), added in order, a wave per token; a
+// sums at 64 CPT channels (blockIdx.z), added in order, a wave per token; a
 // token of kMany chunks or more by all 16 waves (every 16th chunk each, then
 // the waves in order).  All waves for every token took 37 us at 262144 tokens
 // over 131072, where up to 16 tokens start in one workgroup; this takes 30, most
@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(kJoinThr) k_embed_join(const uint32_t* __restr
   __shared__ uint32_t found[kJoin / kLong + 1], many[kJoin / kLong + 1];
   __shared__ float hand[NW][64 * CPT];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t at = static_cast<int64_t>(blockIdx.x) * kJoin;
+  const int64_t at = block_in_rows() * kJoin;
   const int64_t p = at + threadIdx.x;
   bool starts = false;
   if (threadIdx.x < kJoin && p + kLong <= N) {
@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(kJoinThr) k_embed_join(const uint32_t* __restr
   __syncthreads();
   if (starts) found[atomicAdd(&n_found, 1u)] = threadIdx.x;
   __syncthreads();
-  const int64_t c0 = (static_cast<int64_t>(blockIdx.y) * 64 + lane) * CPT, c = imin(c0, d - CPT);
+  const int64_t c0 = (static_cast<int64_t>(blockIdx.z) * 64 + lane) * CPT, c = imin(c0, d - CPT);
   const bool mine = c0 < d;
   // how many of the token's chunks from q0 on there are, up to 64: chunk q is
   // there if its first position holds the token
@@ -568,7 +568,7 @@ void embed_vec(const EmbedArgs& a, const void* tokens, const void* table, void* 
   using T = typename Storage<DT>::T;
   auto run = [&](auto tpr) {
     constexpr int TPR = decltype(tpr)::value;
-    k_embed<DT, VEC, TPR><<<unsigned(cdiv(a.N, 256 / TPR * kRows)), 256, 0, a.stream>>>(
+    k_embed<DT, VEC, TPR><<<rows_of_blocks(cdiv(a.N, 256 / TPR * kRows)), 256, 0, a.stream>>>(
         tokens, a.token_bytes, static_cast<const T*>(table), a.N, a.V, a.d, a.scale, a.pad, static_cast<T*>(out));
   };
   if (a.d <= 16 * VEC) run(std::integral_constant<int, 16>{});
@@ -580,11 +580,11 @@ void sum_vec(const EmbedArgs& a, const Plan& p, const uint32_t* keys, const uint
   using T = typename Storage<DT>::T;
   constexpr int CPT = VEC > 4 ? 4 : VEC;
   float* part = reinterpret_cast<float*>(a.ws + p.part_off);
-  const dim3 grid(unsigned(cdiv(cdiv(a.N, kBlock), 4)), unsigned(cdiv(a.d, 64 * VEC)));
+  const dim3 grid = rows_of_blocks(cdiv(cdiv(a.N, kBlock), 4), cdiv(a.d, 64 * VEC));
   k_embed_sum<DT, VEC><<<grid, 256, 0, a.stream>>>(keys, pos, static_cast<const T*>(dout), a.N, a.V, a.d, a.scale,
                                                    static_cast<T*>(dtable), part);
   if (a.N < kLong) return;
-  const dim3 jgrid(unsigned(cdiv(a.N, kJoin)), unsigned(cdiv(a.d, 64 * CPT)));
+  const dim3 jgrid = rows_of_blocks(cdiv(a.N, kJoin), cdiv(a.d, 64 * CPT));
   k_embed_join<DT, CPT><<<jgrid, kJoinThr, 0, a.stream>>>(keys, part, a.N, a.V, a.d, a.scale, static_cast<T*>(dtable));
 }
 

@@ -102,7 +102,7 @@ __device__ __forceinline__ void tile_of(uint32_t u, uint32_t rows, uint32_t cols
 __global__ void __launch_bounds__(256) k_loss_pad(const uint16_t* __restrict__ in, int64_t R, int64_t d, int64_t ldp,
                                                   uint16_t* __restrict__ out) {
   const int64_t C = ldp / 8;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t i = block_in_rows() * 256 + threadIdx.x;
   if (i >= R * C) return;
   const int64_t r = i / C;
   const int c0 = static_cast<int>(i - r * C) * 8;
@@ -294,12 +294,13 @@ __global__ void __launch_bounds__(256) k_loss_layout(const float* __restrict__ d
                                                      float* __restrict__ weight, RowCoef* __restrict__ coef, uint16_t* __restrict__ xh,
                                                      uint16_t* __restrict__ xg, uint16_t* __restrict__ wh) {
   __shared__ float w[4];
-  const int b = static_cast<int>(blockIdx.x), tid = threadIdx.x;
+  const int64_t b = block_in_rows();
+  const int tid = threadIdx.x;
   auto maximum = [&](int k, int parts, float least) { return block_max(tid < parts ? units->parts[k][tid] : least, w); };
   float iw;
   const float unit_w = unit_of(maximum(1, parts2, 0.0f), &iw);
   if (b >= n1) {
-    const int64_t C = ldp / 8, i = static_cast<int64_t>(b - n1) * 256 + tid;
+    const int64_t C = ldp / 8, i = (b - n1) * 256 + tid;
     if (i >= V * C) return;
     const int64_t r = i / C, c0 = (i - r * C) * 8;
     float v[8];
@@ -319,7 +320,7 @@ __global__ void __launch_bounds__(256) k_loss_layout(const float* __restrict__ d
     units->back_x = iw / (1 << kUnit);
     units->back_w = -shift - kUnit;
   }
-  const int64_t n = static_cast<int64_t>(b) * (256 / lanes) + tid / lanes;
+  const int64_t n = b * (256 / lanes) + tid / lanes;
   if (n >= N) return;   // all lanes of a token
   const int lane = tid % lanes;
   float m = 0.0f, v[8];
@@ -512,7 +513,7 @@ __global__ void __launch_bounds__(256) k_loss_join(const float2* __restrict__ pa
                                                    int64_t ignore,
                                                    float* __restrict__ loss, float* __restrict__ lse) {
   using S = Storage<BF16 ? kBF16 : kF32>;
-  const int64_t n = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  const int64_t n = block_in_rows() * 4 + (threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
   if (n >= N) return;
   const float back = BF16 ? 1.0f : units->iw * ix[n], c = above_zero(scale * kLog2e * back);
@@ -791,7 +792,7 @@ __global__ void __launch_bounds__(256) k_loss_out(const float* __restrict__ P, i
                                                   const LossUnits* __restrict__ units,
                                                   const float* __restrict__ weight, float scale,
                                                   typename Storage<BF16 ? kBF16 : kF32>::T* __restrict__ out) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t i = block_in_rows() * 256 + threadIdx.x;
   if (i >= n) return;
   float sum = 0.0f;
   for (int z = 0; z < S; ++z) sum += P[z * n + i];
@@ -800,7 +801,7 @@ __global__ void __launch_bounds__(256) k_loss_out(const float* __restrict__ P, i
 
 template <class T>
 __global__ void __launch_bounds__(256) k_loss_zero(T* __restrict__ out, int64_t n) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t i = block_in_rows() * 256 + threadIdx.x;
   if (i < n) out[i] = T(0);
 }
 
@@ -998,7 +999,7 @@ Operands lay_out(const LossArgs& a, const Plan& p, const void* x, const void* W,
       constexpr bool BF = decltype(bf)::value;
       k_loss_maxima<BF><<<unsigned(p1 + p2), 1024, 0, a.stream>>>(dloss, dlse, targets, a.target_bytes, a.ignore, a.N,
                                                                        a.V, a.d, x, W, p1, lanes, p2, o.units);
-      k_loss_layout<BF><<<unsigned(n1 + n2), 256, 0, a.stream>>>(
+      k_loss_layout<BF><<<rows_of_blocks(n1 + n2), 256, 0, a.stream>>>(
           dloss, dlse, lse, targets, a.target_bytes, a.ignore, a.N, a.V, a.d, a.scale * kLog2e, p.ldp, x, W, int(n1), lanes,
           p1, p2, o.units, o.ix, o.weight, coef, at(p.xh_off), coef ? at(p.xg_off) : nullptr, at(p.wh_off));
     };
@@ -1007,7 +1008,7 @@ Operands lay_out(const LossArgs& a, const Plan& p, const void* x, const void* W,
   if (o.units) return o;
   if (p.pad) {
     auto pad = [&](const void* in, int64_t R, size_t off) {
-      k_loss_pad<<<unsigned(cdiv(R * (p.ldp / 8), 256)), 256, 0, a.stream>>>(static_cast<const uint16_t*>(in), R, a.d, p.ldp,
+      k_loss_pad<<<rows_of_blocks(cdiv(R * (p.ldp / 8), 256)), 256, 0, a.stream>>>(static_cast<const uint16_t*>(in), R, a.d, p.ldp,
                                                                              at(off));
       return MmOperand{at(off), p.ldp};
     };
@@ -1046,7 +1047,7 @@ void launch_loss(const LossArgs& a, const void* x, const void* W, const void* ta
     if (f.kind == 0) run(Few<PAIR>{}); else if (f.kind == 1) run(Mid<PAIR>{}); else run(Big<PAIR>{});
   };
   if (a.bf16) go(std::false_type{}); else go(std::true_type{});
-  const unsigned jg = static_cast<unsigned>(cdiv(a.N, 4));
+  const dim3 jg = rows_of_blocks(cdiv(a.N, 4));
   if (a.bf16)
     k_loss_join<true><<<jg, 256, 0, a.stream>>>(part, int(f.splits), x, W, targets, a.target_bytes, a.N, a.V, a.d,
                                                 a.scale, o.units, o.ix, a.ignore, loss, lse);
@@ -1060,9 +1061,9 @@ void launch_loss_backward(const LossArgs& a, const void* x, const void* W, const
   if (a.N == 0) {   // no token: dW is zero
     const int64_t n = a.V * a.d;
     if (dW && a.bf16)
-      k_loss_zero<uint16_t><<<unsigned(cdiv(n, 256)), 256, 0, a.stream>>>(static_cast<uint16_t*>(dW), n);
+      k_loss_zero<uint16_t><<<rows_of_blocks(cdiv(n, 256)), 256, 0, a.stream>>>(static_cast<uint16_t*>(dW), n);
     else if (dW)
-      k_loss_zero<float><<<unsigned(cdiv(n, 256)), 256, 0, a.stream>>>(static_cast<float*>(dW), n);
+      k_loss_zero<float><<<rows_of_blocks(cdiv(n, 256)), 256, 0, a.stream>>>(static_cast<float*>(dW), n);
     return;
   }
   const PlanBw b = plan_bw(a);
@@ -1074,7 +1075,7 @@ void launch_loss_backward(const LossArgs& a, const void* x, const void* W, const
   LossUnits* const units = o.units;
   auto out = [&](auto bf, auto is_w, const float* P, int S, int64_t n, const float* weight, void* to) {
     constexpr bool BF = decltype(bf)::value, IS_W = decltype(is_w)::value;
-    k_loss_out<BF, IS_W><<<unsigned(cdiv(n, 256)), 256, 0, a.stream>>>(P, S, n, a.d, units, weight, a.scale,
+    k_loss_out<BF, IS_W><<<rows_of_blocks(cdiv(n, 256)), 256, 0, a.stream>>>(P, S, n, a.d, units, weight, a.scale,
                                                                        static_cast<typename Storage<BF ? kBF16 : kF32>::T*>(to));
   };
   auto typed = [&](auto run) {

@@ -165,3 +165,12 @@ def test_binding_checks_shapes_and_types():
         B.prn_embed(tok, table, out.t().contiguous().t())
     with pytest.raises(B.PrnError, match="workspace"):
         B.prn_embed_backward(tok, out, table)
+
+
+def test_more_tokens_than_one_row_of_a_grid():
+    """2^30 tokens and a few, one channel: more threads than one dimension of a launch may have."""
+    table = torch.randn(5, 1, device="cuda").bfloat16()
+    tok = torch.arange(5, device="cuda", dtype=torch.int32).repeat((1 << 30) // 5 + 2)[:(1 << 30) + 3]
+    out = prn.embed(tok, table)
+    n = out.shape[0] // 5
+    assert torch.equal(out[:5 * n].view(n, 5), table[:, 0].expand(n, 5)) and torch.equal(out[5 * n:], table[:len(out) - 5 * n])

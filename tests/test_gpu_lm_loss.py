@@ -253,3 +253,14 @@ def test_another_stream_and_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, run()))
+
+
+def test_more_tokens_than_one_row_of_a_grid():
+    """2^26 tokens and a few: a wave each is more threads than one dimension of a launch may have."""
+    x, W, t, _, _ = _inputs(1024, 16, 8, "bf16", 9)
+    loss, lse = prn.vocab_loss(x, W, t)
+    n = (1 << 16) + 1
+    big = prn.vocab_loss(x.repeat(n, 1)[:-700], W, t.repeat(n)[:-700])
+    for got, want in zip(big, (loss, lse)):
+        assert torch.equal(got[:1024 * (n - 1)].view(n - 1, 1024), want.expand(n - 1, 1024))
+        assert torch.equal(got[1024 * (n - 1):], want[:324])
