@@ -174,3 +174,21 @@ def test_more_tokens_than_one_row_of_a_grid():
     out = prn.embed(tok, table)
     n = out.shape[0] // 5
     assert torch.equal(out[:5 * n].view(n, 5), table[:, 0].expand(n, 5)) and torch.equal(out[5 * n:], table[:len(out) - 5 * n])
+
+
+@pytest.mark.parametrize("dtype,N,V,d,kind", [("f32", 640 * 2048, 70000, 2, "skewed"), ("f32", 640 * 2048 + 1, 3000, 2, "uniform"),
+                                             ("bf16", 1400007, 300000, 3, "skewed"), ("f32", 2097153, 500, 1, "uniform")])
+def test_embed_gradient_of_many_tiles(dtype, N, V, d, kind):
+    """640 tiles of 2048 tokens, and more of them, whose counts are summed up in groups of 256 before the scatter."""
+    _check(N, V, d, dtype, kind)
+
+
+def test_embed_gradient_of_a_billion_tokens():
+    """2^30 tokens and a few, each 1024 times, one channel: sums of ones are exact.  (Adding up the counts of all
+    tiles in every tile would read 600 TB.)"""
+    V, n = 1 << 20, (1 << 30) + 5
+    tok = torch.arange(n, device="cuda", dtype=torch.int32).bitwise_and_(V - 1)
+    grad = prn.embed_backward(torch.ones(n, 1, device="cuda", dtype=torch.bfloat16), tok, V)
+    want = torch.full((V, 1), 1024.0, device="cuda")
+    want[:5] += 1
+    assert torch.equal(grad, want.bfloat16())
