@@ -20,6 +20,7 @@
 namespace prn {
 namespace {
 
+constexpr int64_t kNoPad = INT64_MIN;
 constexpr int kSortThr = 512;
 constexpr int kMaxBits = 9;     // of a radix pass
 constexpr int kBins = 1 << kMaxBits;
@@ -81,7 +82,7 @@ __global__ void __launch_bounds__(256) k_embed(const void* __restrict__ tokens, 
 #pragma unroll
     for (int q = 0; q < kRows; ++q) {
       const bool in = tok[q] >= 0 && tok[q] < V && tok[q] != pad;
-      const float fill = tok[q] == pad ? 0.0f : __builtin_nanf("");
+      const float fill = tok[q] == pad && pad != kNoPad ? 0.0f : __builtin_nanf("");
       float v[VEC];
       unpack<DT, VEC>(raw[q], v);
 #pragma unroll

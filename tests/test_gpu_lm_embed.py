@@ -192,3 +192,9 @@ def test_embed_gradient_of_a_billion_tokens():
     want = torch.full((V, 1), 1024.0, device="cuda")
     want[:5] += 1
     assert torch.equal(grad, want.bfloat16())
+
+
+def test_the_value_that_stands_for_no_pad_id_is_no_pad_id():
+    tok = torch.tensor([-2 ** 63, 1], device="cuda")
+    out = prn.embed(tok, torch.ones(4, 24, device="cuda"))
+    assert out[0].isnan().all() and (out[1] == 1).all()
