@@ -135,3 +135,33 @@ def test_several_pieces_of_two_terms(N, V):
     assert B.prn_vocab_loss_backward_workspace_bytes(torch.float32, N, V, 16) < whole
     say(f"[case] vocab loss N={N} V={V} f32, several pieces")
     _check(*_inputs(N, V, 16, "f32", 4), "f32")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_values_that_are_not_finite(dtype, bad):
+    """In x: in their tokens' rows, and in dW; in W: in every token whose logit of it is not -inf."""
+    x, W, t, dloss, dlse = _inputs(150, 200, 40, dtype, 5)
+    t[20] = -100
+    loss, lse = prn.vocab_loss(x, W, t)
+    dx, _ = prn.vocab_loss_backward(dloss, x, W, t, lse, dlse=dlse)
+    y = x.clone()
+    y[9, 3] = y[20, 0] = bad
+    rows = torch.zeros(150, dtype=torch.bool, device="cuda")
+    rows[9] = rows[20] = True
+    loss2, lse2 = prn.vocab_loss(y, W, t)
+    dx2, dW2 = prn.vocab_loss_backward(dloss, y, W, t, lse2, dlse=dlse)
+    assert loss2[20] == 0 and not loss2[9].isfinite() and not lse2[rows].isfinite().any()
+    assert torch.equal(loss2[~rows], loss[~rows]) and torch.equal(lse2[~rows], lse[~rows])
+    assert dx2[rows].isnan().all() and torch.equal(dx2[~rows], dx[~rows]) and dW2.isnan().all()
+    U = W.clone()
+    U[30, 5] = bad
+    loss3, lse3 = prn.vocab_loss(x, U, t)
+    high = ~(x[:, 5] * bad == -float("inf"))
+    assert not lse3[high].isfinite().any() and not loss3[high & (t != -100)].isfinite().any()
+    if dtype == "bf16":   # the others have no share of entry 30
+        keep = torch.arange(200, device="cuda") != 30
+        _, want, z = olm.vocab_loss(to_f64(x), to_f64(W[keep]), np.full(150, -100))
+        size = (np.abs(to_f64(x)) @ np.abs(to_f64(W[keep])).T).max(-1)
+        band = (2 * 40 + 8) * E * size + (100 + 64) * E + 8 * E * (np.abs(want) + np.abs(z).max(-1))
+        assert (np.abs(to_f64(lse3) - want) <= band)[~high.cpu().numpy()].all()
