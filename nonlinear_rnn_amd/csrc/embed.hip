@@ -15,6 +15,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "grid_rows.h"
 #include "prn_device.h"
 
 namespace prn {

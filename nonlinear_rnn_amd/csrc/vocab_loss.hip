@@ -43,6 +43,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "grid_rows.h"
 #include "mm_tile.h"
 #include "prn_device.h"
 
