@@ -73,6 +73,11 @@ constexpr int kXcd = 8;
 // logits, below 2^60 in these units, are zero all the same.
 __device__ __forceinline__ float above_zero(float c) { return fmaxf(c, 0x1p-126f); }
 
+// Exponents (of 2) of this size and more are formed as the factor times a
+// difference: the fused product less the rounded other one, an instruction
+// shorter, is off by 2^-12 there, and by whole powers of 2 at logits of 1e7.
+constexpr float kFar = 0x1p12f;
+
 // Workgroups are dealt round-robin to the XCDs.  The units of work of this
 // workgroup, when every XCD takes a contiguous share of them, in proportion
 // to its workgroups, so that neighbouring units share its L2.
@@ -445,18 +450,32 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_lse(MmOperand W, MmOperand
       }
 #pragma unroll
       for (int j = 0; j < Tl::WN; ++j) {
-        auto sum_against = [&](float off) {
+        auto sum_against = [&](float ref) {
           float q[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          const float off = -ref * c[j];
+          const bool far = fabsf(off) >= kFar;
+          if (__builtin_amdgcn_ballot_w64(far)) {
+            asm volatile("");   // a branch, for some lane's token; the others' exponents are as without it
 #pragma unroll
-          for (int i = 0; i < Tl::WM; ++i)
+            for (int i = 0; i < Tl::WM; ++i)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) q[r & 3] += ex2(fmaf(tile.acc[i][j][r], c[j], off));
+              for (int r = 0; r < 16; ++r) {
+                const float a = tile.acc[i][j][r];
+                q[r & 3] += ex2(far ? (a - ref) * c[j] : fmaf(a, c[j], off));
+              }
+          } else {
+#pragma unroll
+            for (int i = 0; i < Tl::WM; ++i)
+#pragma unroll
+              for (int r = 0; r < 16; ++r) q[r & 3] += ex2(fmaf(tile.acc[i][j][r], c[j], off));
+          }
           return (q[0] + q[1]) + (q[2] + q[3]);
         };
-        float sum = sum_against(-m[j] * c[j]);
+        float sum = sum_against(m[j]);
         // no maximum yet, or this tile's sum is out of proportion (or NaN)
-        if (__builtin_amdgcn_ballot_w64(s[j] == 0.0f || !(sum < 0x1p60f))) {
-          asm volatile("");   // a branch: taken once or twice a unit
+        const bool renew = s[j] == 0.0f || !(sum < 0x1p60f);
+        if (__builtin_amdgcn_ballot_w64(renew)) {
+          asm volatile("");   // a branch: taken once or twice a unit; for these lanes only
           float mx = tile.acc[0][j][0];
 #pragma unroll
           for (int i = 0; i < Tl::WM; ++i)
@@ -464,9 +483,11 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_lse(MmOperand W, MmOperand
             for (int r = 0; r < 16; ++r) mx = fmaxf(mx, tile.acc[i][j][r]);
           if (s[j] != 0.0f) mx = fmaxf(mx, m[j]);
           mx = mx == -__builtin_inff() ? 0.0f : mx;   // any finite reference leaves the sum 0
-          s[j] *= ex2((m[j] - mx) * c[j]);
+          if (!renew) mx = m[j];
+          // (no sum yet: m is no maximum, and mx may lie far below it)
+          if (s[j] != 0.0f) s[j] *= ex2((m[j] - mx) * c[j]);
           m[j] = mx;
-          sum = sum_against(-mx * c[j]);
+          sum = sum_against(mx);
         }
         s[j] += sum;
       }

@@ -165,3 +165,22 @@ def test_values_that_are_not_finite(dtype, bad):
         size = (np.abs(to_f64(x)) @ np.abs(to_f64(W[keep])).T).max(-1)
         band = (2 * 40 + 8) * E * size + (100 + 64) * E + 8 * E * (np.abs(want) + np.abs(z).max(-1))
         assert (np.abs(to_f64(lse3) - want) <= band)[~high.cpu().numpy()].all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,V", [(64, 1000), (300, 3000)])
+@pytest.mark.parametrize("size", [80.0, 100.0, 1e3, 1e5, 1e7, 2e9, 1e12, 1e18])
+def test_logits_far_from_zero(dtype, N, V, size):
+    """All of a token's logits around -size or size, or spread over that: loss and lse against the oracle.  The
+    tokens beside them in a wave are ordinary ones."""
+    x, W, t, _, _ = _inputs(N, V, 40, dtype, 7)
+    W[:, 0] = 1.0
+    x[0:60:4, 0] = -size
+    x[1:60:4, 0] = size
+    x[2:60:4] *= size
+    loss, lse = prn.vocab_loss(x, W, t)
+    (ref, ref_lse, _, _), (b_loss, b_lse, _, _) = _bands(to_f64(x), to_f64(W), t.cpu().numpy(), np.ones(N), None, dtype, 1.0)
+    for name, got, r, b in (("loss", loss, ref, b_loss), ("lse", lse, ref_lse, b_lse)):
+        worst = np.nan_to_num(np.abs(to_f64(got) - r) / b, nan=np.inf).max()
+        say(f"  {name}: of the band {worst:.3g}")
+        assert worst <= 1.0, name
