@@ -783,27 +783,35 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_mm(MmOperand A, MmOperand 
   tile.template multiply<TA, true, true, true>(next);
   T* const obase = static_cast<T*>(out) + r0 * C + c0;
   const uint32_t oat = rl * static_cast<uint32_t>(C) + cl;
+  if (!out) {
+#pragma unroll
+    for (int i = 0; i < Tl::WM; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int ri = 32 * i + 8 * (r >> 2) + (r & 3);
+#pragma unroll
+        for (int j = 0; j < Tl::WN; ++j)
+          if (rl + ri < rows && cl + 32 * j < cols)
+            *reinterpret_cast<float*>(base + (at + ri * ldb + 128 * j)) = tile.acc[i][j][r];
+      }
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < Tl::WM; ++i) {
     float u[16];   // the rows' weights (there are some for a whole tile)
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const float4 f = !TA && out ? *reinterpret_cast<const float4*>(weight + r0 + rl + 32 * i + 8 * q) : float4{};
+      const float4 f = TA ? float4{} : *reinterpret_cast<const float4*>(weight + r0 + rl + 32 * i + 8 * q);
       u[4 * q] = f.x, u[4 * q + 1] = f.y, u[4 * q + 2] = f.z, u[4 * q + 3] = f.w;
     }
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
       const int ri = 32 * i + 8 * (r >> 2) + (r & 3);
 #pragma unroll
-      for (int j = 0; j < Tl::WN; ++j) {
-        if (rl + ri < rows && cl + 32 * j < cols) {
-          if (out)
-            obase[oat + ri * static_cast<uint32_t>(C) + 32 * j] =
-                Storage<BF16 ? kBF16 : kF32>::pack(loss_finish<TA>(tile.acc[i][j][r], units, u[r], scale));
-          else
-            *reinterpret_cast<float*>(base + (at + ri * ldb + 128 * j)) = tile.acc[i][j][r];
-        }
-      }
+      for (int j = 0; j < Tl::WN; ++j)
+        if (rl + ri < rows && cl + 32 * j < cols)
+          obase[oat + ri * static_cast<uint32_t>(C) + 32 * j] =
+              Storage<BF16 ? kBF16 : kF32>::pack(loss_finish<TA>(tile.acc[i][j][r], units, u[r], scale));
     }
   }
 }
