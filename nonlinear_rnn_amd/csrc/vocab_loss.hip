@@ -130,6 +130,7 @@ struct LossUnits {
   float iw;                        // z = acc iw s times the token's inverse unit
   float back_x;                    // dx = acc back_x s u, u the token's weight
   int32_t back_w;                  // dW = acc 2^back_w s
+  int32_t any_far;                 // is a token's lse2 kFar or more? (RowFar)
   float parts[2][kMaxParts];       // the workgroups' maxima: of the exponents of u x; of |W|
 };
 constexpr float kNoExponent = -1e4f;   // of nothing but zeros
@@ -218,6 +219,7 @@ __global__ void __launch_bounds__(1024) k_loss_maxima(const float* __restrict__ 
                                                       LossUnits* __restrict__ u) {
   __shared__ float w[16];
   int b = static_cast<int>(blockIdx.x);
+  if (b == 0 && threadIdx.x == 0) u->any_far = 0;
   if (b < n1) {
     float top = kNoExponent;
     const int lane = threadIdx.x % lanes, per = 1024 / lanes;
@@ -266,6 +268,14 @@ struct RowCoef {
   int32_t target;       // -1: none
 };
 
+// The same for a token whose lse2 is kFar and more, where it holds little of a
+// fraction: sign 2^((acc back - lse) log2(e) + log2p).  acc back - lse, both as
+// the forward had them, is at most what lse's rounding makes it.
+struct RowFar {
+  float back, lse, log2p, unused;
+};
+__device__ __forceinline__ bool is_far(float lse2) { return fabsf(lse2) >= kFar && fabsf(lse2) < __builtin_inff(); }
+
 // eight values' fp16 terms, to row r from column c0 on
 template <bool BF16>
 __device__ __forceinline__ void store_terms(const float* v, uint16_t* to, int64_t r, int64_t ldp, int64_t c0) {
@@ -294,10 +304,11 @@ template <bool BF16>
 __global__ void __launch_bounds__(256) k_loss_layout(const float* __restrict__ dloss, const float* __restrict__ dlse,
                                                      const float* __restrict__ lse, const void* __restrict__ targets,
                                                      int target_bytes, int64_t ignore, int64_t N, int64_t V, int64_t d,
-                                                     float c, int64_t ldp, const void* __restrict__ x,
+                                                     float scale, int64_t ldp, const void* __restrict__ x,
                                                      const void* __restrict__ W, int n1, int lanes, int parts1, int parts2,
                                                      LossUnits* __restrict__ units, float* __restrict__ ix,
-                                                     float* __restrict__ weight, RowCoef* __restrict__ coef, uint16_t* __restrict__ xh,
+                                                     float* __restrict__ weight, RowCoef* __restrict__ coef,
+                                                     RowFar* __restrict__ far, uint16_t* __restrict__ xh,
                                                      uint16_t* __restrict__ xg, uint16_t* __restrict__ wh) {
   __shared__ float w[4];
   const int64_t b = block_in_rows();
@@ -369,13 +380,16 @@ __global__ void __launch_bounds__(256) k_loss_layout(const float* __restrict__ d
   weight[n] = in.u;
   const float u = in.u > 0.0f ? in.u : 1.0f, p = in.both / u;
   RowCoef r;
-  r.c = copysignf(above_zero(c * iw * inverse), p);
+  r.c = copysignf(above_zero(scale * kLog2e * iw * inverse), p);
   r.one = in.one / u * (1 << kUnit);
   // no such entry: the loss was NaN, and so is its gradient
   const bool lost = t != ignore && (t < 0 || t >= V);
-  r.lse2 = lost ? __builtin_nanf("") : fmaf(lse[n], kLog2e, -log2f(fabsf(p))) - kUnit;   // p = 0: +inf, a row of zeros
+  const float log2p = log2f(fabsf(p)), l = lse[n];
+  r.lse2 = lost ? __builtin_nanf("") : fmaf(l, kLog2e, -log2p) - kUnit;   // p = 0: +inf, a row of zeros
   r.target = t == ignore || lost ? -1 : static_cast<int32_t>(t);
   coef[n] = r;
+  far[n] = {iw * inverse * scale, l, log2p + kUnit, 0.0f};
+  if (is_far(r.lse2)) units->any_far = 1;
 }
 
 // ------------------------------------------------------------- forward ---
@@ -592,9 +606,11 @@ __global__ void __launch_bounds__(256) k_loss_join(const float2* __restrict__ pa
 // does not: 4096 x 256 x 32000 252, dx 215, dW 229 us against 287, 209, 225.
 template <class Tl, bool BF16>
 __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_dz(MmOperand W, MmOperand X, int64_t N, int64_t V, int64_t d,
-                                                         int64_t piece0, int64_t piece1, int n_tok,
-                                                         const RowCoef* __restrict__ coef, uint16_t* __restrict__ dz,
+                                                         const LossUnits* __restrict__ units, int64_t piece0,
+                                                         int64_t piece1, int n_tok, const RowCoef* __restrict__ coef,
+                                                         const RowFar* __restrict__ far, uint16_t* __restrict__ dz,
                                                          int64_t ldz) {
+  const bool any_far = __builtin_amdgcn_readfirstlane(units->any_far) != 0;
   // the loads are up to NST tiles ahead (tiles of one stage)
   constexpr int kRing = Tl::NST + 1;
   static_assert(sizeof(RowCoef) == 16 && Tl::BN % 64 == 0 && Tl::BN / 64 <= Tl::NW, "one coefficient load per wave");
@@ -665,6 +681,15 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_dz(MmOperand W, MmOperand 
           float v[16];
 #pragma unroll
           for (int r = 0; r < 16; ++r) v[r] = ex2(fmaf(tile.acc[i2][j][r], c, -rc.lse2));
+          if (any_far) {   // such tokens' exponents, at most 14 (twice the weight) whatever lse's rounding
+            asm volatile("");
+            const RowFar f = far[imin(n0 + tl, N - 1)];
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+              const float e = fmaf(fmaf(tile.acc[i2][j][r], f.back, -f.lse), kLog2e, f.log2p);
+              v[r] = is_far(rc.lse2) ? ex2(fminf(e, kUnit + 1.0f)) : v[r];
+            }
+          }
           if (negative) {
             asm volatile("");   // branches: rarely taken
 #pragma unroll
@@ -783,37 +808,42 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_mm(MmOperand A, MmOperand 
   tile.template multiply<TA, true, true, true>(next);
   T* const obase = static_cast<T*>(out) + r0 * C + c0;
   const uint32_t oat = rl * static_cast<uint32_t>(C) + cl;
-  if (!out) {
+  auto stores = [&](auto kind) {   // 0: sums that go on, 1: finished ones, 2: as `out` says
+    constexpr int KIND = decltype(kind)::value;
 #pragma unroll
-    for (int i = 0; i < Tl::WM; ++i)
+    for (int i = 0; i < Tl::WM; ++i) {
+      float u[16] = {};   // the rows' weights (there are some for a whole tile)
+      if constexpr (!TA && KIND == 1) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float4 f = *reinterpret_cast<const float4*>(weight + r0 + rl + 32 * i + 8 * q);
+          u[4 * q] = f.x, u[4 * q + 1] = f.y, u[4 * q + 2] = f.z, u[4 * q + 3] = f.w;
+        }
+      }
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
         const int ri = 32 * i + 8 * (r >> 2) + (r & 3);
 #pragma unroll
-        for (int j = 0; j < Tl::WN; ++j)
-          if (rl + ri < rows && cl + 32 * j < cols)
-            *reinterpret_cast<float*>(base + (at + ri * ldb + 128 * j)) = tile.acc[i][j][r];
+        for (int j = 0; j < Tl::WN; ++j) {
+          if (rl + ri < rows && cl + 32 * j < cols) {
+            if (KIND == 1 || (KIND == 2 && out))
+              obase[oat + ri * static_cast<uint32_t>(C) + 32 * j] =
+                  Storage<BF16 ? kBF16 : kF32>::pack(loss_finish<TA>(tile.acc[i][j][r], units, u[r], scale));
+            else
+              *reinterpret_cast<float*>(base + (at + ri * ldb + 128 * j)) = tile.acc[i][j][r];
+          }
+        }
       }
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < Tl::WM; ++i) {
-    float u[16];   // the rows' weights (there are some for a whole tile)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const float4 f = TA ? float4{} : *reinterpret_cast<const float4*>(weight + r0 + rl + 32 * i + 8 * q);
-      u[4 * q] = f.x, u[4 * q + 1] = f.y, u[4 * q + 2] = f.z, u[4 * q + 3] = f.w;
     }
-#pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const int ri = 32 * i + 8 * (r >> 2) + (r & 3);
-#pragma unroll
-      for (int j = 0; j < Tl::WN; ++j)
-        if (rl + ri < rows && cl + 32 * j < cols)
-          obase[oat + ri * static_cast<uint32_t>(C) + 32 * j] =
-              Storage<BF16 ? kBF16 : kF32>::pack(loss_finish<TA>(tile.acc[i][j][r], units, u[r], scale));
-    }
-  }
+  };
+  // dx by a loop of its own for each (4096 x 256 x 32000 fp32: 213 us against 228 with one), dW by one for both
+  // (5003 x 520 x 50021 bf16: 308 against 324)
+  if constexpr (TA)
+    stores(std::integral_constant<int, 2>{});
+  else if (out)
+    stores(std::integral_constant<int, 1>{});
+  else
+    stores(std::integral_constant<int, 0>{});
 }
 
 // out[i] = the sum over z, in order, of P[z][i], from its units, rounded once
@@ -966,7 +996,7 @@ struct PlanBw {
   int64_t out;              // tile columns of dx and dW
   int64_t piece, ldz;
   Cut x, w;                 // of dx's sum (over the piece), and dW's (over the tokens)
-  size_t coef_off, dz_off, px_off, pw_off, total;
+  size_t coef_off, far_off, dz_off, px_off, pw_off, total;
 };
 PlanBw plan_bw(const LossArgs& a) {
   PlanBw b{};
@@ -996,7 +1026,8 @@ PlanBw plan_bw(const LossArgs& a) {
   }
   auto sums = [&](int64_t rows, const Cut& c) { return up((size_t(c.head) + size_t(c.s) * (rows - c.head)) * a.d * 4); };
   b.coef_off = b.op.end;
-  b.dz_off = b.coef_off + up(size_t(a.N) * sizeof(RowCoef));
+  b.far_off = b.coef_off + up(size_t(a.N) * sizeof(RowCoef));
+  b.dz_off = b.far_off + up(size_t(a.N) * sizeof(RowFar));
   b.px_off = b.dz_off + up(size_t(a.N) * b.ldz * 2);
   b.pw_off = b.px_off + sums(a.N, b.x);
   b.total = b.pw_off + (b.w.s > 1 ? sums(nv, b.w) : 0);
@@ -1011,7 +1042,7 @@ struct Operands {
   float *ix, *weight;
 };
 Operands lay_out(const LossArgs& a, const Plan& p, const void* x, const void* W, const void* targets, const float* lse,
-                 const float* dloss, const float* dlse, RowCoef* coef) {
+                 const float* dloss, const float* dlse, RowCoef* coef, RowFar* far) {
   Operands o{};
   auto at = [&](size_t off) { return reinterpret_cast<uint16_t*>(a.ws + off); };
   if (coef || !a.bf16) {
@@ -1030,8 +1061,8 @@ Operands lay_out(const LossArgs& a, const Plan& p, const void* x, const void* W,
       k_loss_maxima<BF><<<unsigned(p1 + p2), 1024, 0, a.stream>>>(dloss, dlse, targets, a.target_bytes, a.ignore, a.N,
                                                                        a.V, a.d, x, W, p1, lanes, p2, o.units);
       k_loss_layout<BF><<<rows_of_blocks(n1 + n2), 256, 0, a.stream>>>(
-          dloss, dlse, lse, targets, a.target_bytes, a.ignore, a.N, a.V, a.d, a.scale * kLog2e, p.ldp, x, W, int(n1), lanes,
-          p1, p2, o.units, o.ix, o.weight, coef, at(p.xh_off), coef ? at(p.xg_off) : nullptr, at(p.wh_off));
+          dloss, dlse, lse, targets, a.target_bytes, a.ignore, a.N, a.V, a.d, a.scale, p.ldp, x, W, int(n1), lanes,
+          p1, p2, o.units, o.ix, o.weight, coef, far, at(p.xh_off), coef ? at(p.xg_off) : nullptr, at(p.wh_off));
     };
     if (a.bf16) go(std::true_type{}); else go(std::false_type{});
   }
@@ -1064,7 +1095,7 @@ size_t loss_backward_workspace(const LossArgs& a) { return a.N ? plan_bw(a).tota
 
 void launch_loss(const LossArgs& a, const void* x, const void* W, const void* targets, float* loss, float* lse) {
   const PlanFw f = plan_fw(a);
-  const Operands o = lay_out(a, f.op, x, W, targets, nullptr, nullptr, nullptr, nullptr);
+  const Operands o = lay_out(a, f.op, x, W, targets, nullptr, nullptr, nullptr, nullptr, nullptr);
   const float c = a.scale * kLog2e;
   float2* part = reinterpret_cast<float2*>(a.ws + f.part_off);
   auto go = [&](auto pair) {
@@ -1098,10 +1129,11 @@ void launch_loss_backward(const LossArgs& a, const void* x, const void* W, const
   }
   const PlanBw b = plan_bw(a);
   RowCoef* coef = reinterpret_cast<RowCoef*>(a.ws + b.coef_off);
+  RowFar* far = reinterpret_cast<RowFar*>(a.ws + b.far_off);
   uint16_t* dz = reinterpret_cast<uint16_t*>(a.ws + b.dz_off);
   float* px = reinterpret_cast<float*>(a.ws + b.px_off);
   float* pw = reinterpret_cast<float*>(a.ws + b.pw_off);
-  const Operands o = lay_out(a, b.op, x, W, targets, lse, dloss, dlse, coef);
+  const Operands o = lay_out(a, b.op, x, W, targets, lse, dloss, dlse, coef, far);
   LossUnits* const units = o.units;
   auto out = [&](auto bf, auto is_w, const float* P, int S, int64_t n, const float* weight, void* to) {
     constexpr bool BF = decltype(bf)::value, IS_W = decltype(is_w)::value;
@@ -1123,7 +1155,7 @@ void launch_loss_backward(const LossArgs& a, const void* x, const void* W, const
         using Tl = decltype(tl);
         const int64_t n_tok = cdiv(a.N, Tl::BN), tiles = n_tok * cdiv(nv, kBM), slots = (b.big_z ? 1 : mid_slots(BF)) * kCus;
         k_loss_dz<Tl, BF><<<unsigned(std::min(tiles, slots)), Tl::NTHR, 0, a.stream>>>(
-            o.Wo, o.X, a.N, a.V, a.d, v0, pend, int(n_tok), coef, dz, b.ldz);
+            o.Wo, o.X, a.N, a.V, a.d, units, v0, pend, int(n_tok), coef, far, dz, b.ldz);
       };
       if (b.big_z) run(Big<!BF>{}); else run(Mid<!BF>{});
     });

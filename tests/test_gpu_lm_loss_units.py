@@ -184,3 +184,39 @@ def test_logits_far_from_zero(dtype, N, V, size):
         worst = np.nan_to_num(np.abs(to_f64(got) - r) / b, nan=np.inf).max()
         say(f"  {name}: of the band {worst:.3g}")
         assert worst <= 1.0, name
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("size", [2.0 ** 20, 2.0 ** 24, 2.0 ** 27, 2.0 ** 32, 2.0 ** 44])
+@pytest.mark.parametrize("shift", [False, True])
+def test_logits_that_hold_no_fraction(dtype, size, shift):
+    """Logits of 1e7 and more, of either sign, or (shift) all of a token's the same: a probability of one entry is at
+    most 1 whatever its exponent's rounding, so dx and dW stay finite and dx within what its coefficients allow;
+    with fp32 data, whose logits are the same bits both ways, it is that of the one entry that counts."""
+    x, W, t, dloss, dlse = _inputs(150, 200, 64, dtype, 6)
+    W[:, 0] = -1.0
+    if shift:
+        x[5:9, 0] = size        # every logit far below zero, their differences lost
+        x[9:12, 0] = -size
+    else:
+        x[5:12] *= size
+    loss, lse = prn.vocab_loss(x, W, t)
+    dx, dW = prn.vocab_loss_backward(dloss, x, W, t, lse, dlse=dlse)
+    assert loss.isfinite().all() and lse.isfinite().all() and dx.isfinite().all() and dW.isfinite().all()
+    W64 = to_f64(W)
+    one = np.where(t.cpu().numpy() == -100, 0.0, to_f64(dloss))
+    both = one + to_f64(dlse)
+    if shift:   # up to 200 entries of up to twice their coefficient's power of two each
+        bound = (200 * 4 + 1) * np.maximum(np.abs(one), np.abs(both))[5:12, None] * np.abs(W64).max(0)
+        assert (np.abs(to_f64(dx)[5:12]) <= bound).all()
+        return
+    z = to_f64(x) @ W64.T
+    top = np.sort(z, -1)
+    A = (np.abs(to_f64(x)) @ np.abs(W64).T).max(-1)
+    alone = top[:, -1] - top[:, -2] > (12 * 64 + 8) * E * A * 2 + 40     # the largest stands out of the logits' errors
+    want = both[:, None] * W64[z.argmax(-1)] - np.where((t.cpu().numpy() >= 0), one, 0.0)[:, None] * W64[t.cpu().numpy().clip(0)]
+    rows = [n for n in range(5, 12) if alone[n]]
+    if dtype == "f32" and size >= 2.0 ** 32:   # lse is the largest logit, without a fraction
+        assert rows
+        size_ = (np.abs(both) + np.abs(one))[:, None] * np.abs(W64).max(0)
+        assert (np.abs(to_f64(dx) - want) <= 2.0 ** -20 * size_)[rows].all()
