@@ -168,6 +168,12 @@ struct Row {
   }
 };
 
+// 1 / sqrt(v); v_rsq_f32 takes a value below 2^-126 for zero
+__device__ __forceinline__ float inverse_root(float v) {
+  const bool tiny = v < 0x1p-96f;
+  return __builtin_amdgcn_rsqf(tiny ? v * 0x1p96f : v) * (tiny ? 0x1p48f : 1.0f);
+}
+
 __device__ __forceinline__ float sig(float g) { return rcp(1.0f + ex2(kSigScale * g)); }
 
 template <int DT, int VEC, int NV, int TPR, int NTHR, bool TAIL>
@@ -203,7 +209,7 @@ __global__ void __launch_bounds__(NTHR) k_block_norm(NormDev a) {
     if (a.w_post) {
       float s = row.sum([&](int i) { return h[i] * h[i]; });
       total(&s);
-      const float rstd = __builtin_amdgcn_rsqf(fmaf(s, inv_d, a.eps));
+      const float rstd = inverse_root(fmaf(s, inv_d, a.eps));
 #pragma unroll
       for (int e = 0; e < E; ++e) h[e] *= rstd * w_post[e];
     }
@@ -228,7 +234,7 @@ __global__ void __launch_bounds__(NTHR) k_block_norm(NormDev a) {
     if (a.w_pre) {
       float s = row.sum([&](int i) { return h[i] * h[i]; });
       total(&s);
-      const float rstd = __builtin_amdgcn_rsqf(fmaf(s, inv_d, a.eps));
+      const float rstd = inverse_root(fmaf(s, inv_d, a.eps));
 #pragma unroll
       for (int e = 0; e < E; ++e) h[e] *= rstd * w_pre[e];
       row.store(a.o1, n, h);
@@ -285,7 +291,7 @@ __global__ void __launch_bounds__(NTHR) k_block_norm_backward(NormDev a) {
     if (a.w_post) {
       float s = row.sum([&](int i) { return h[i] * h[i]; });
       total(&s);
-      rstd_h = __builtin_amdgcn_rsqf(fmaf(s, inv_d, a.eps));
+      rstd_h = inverse_root(fmaf(s, inv_d, a.eps));
 #pragma unroll
       for (int e = 0; e < E; ++e) h[e] *= rstd_h;
     }
@@ -310,7 +316,7 @@ __global__ void __launch_bounds__(NTHR) k_block_norm_backward(NormDev a) {
       s[0] = row.sum([&](int i) { return r[i] * r[i]; });
       s[1] = row.sum([&](int i) { return dn[i] * w_pre[i] * r[i]; });
       total2(s);
-      const float rstd = __builtin_amdgcn_rsqf(fmaf(s[0], inv_d, a.eps));
+      const float rstd = inverse_root(fmaf(s[0], inv_d, a.eps));
       const float mean = s[1] * rstd * inv_d;   // mean(q rn)
 #pragma unroll
       for (int e = 0; e < E; ++e) {

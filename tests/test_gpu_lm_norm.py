@@ -239,3 +239,24 @@ def test_the_norm_before_the_first_block_copies_nothing():
     assert r is y and torch.cuda.max_memory_allocated() - before < 1.5 * y.numel() * 4
     (n * 2).sum().backward()
     assert torch.equal(y.grad, prn.block_norm_backward(None, torch.full_like(n, 2.0), y.detach(), w_pre=w)[0])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("size", [1e-18, 1e-19, 1e-20])
+def test_rows_whose_squares_leave_the_normal_range(size, dtype):
+    """eps = 0: the mean of the squares is below 2^-126, where each square is off by half a step of 2^-149 (relative
+    to the mean: 2^-150 / mean, halved by the root), and its root is not."""
+    d = 96
+    kw, _, dn = _inputs(5, d, dtype, (False, False, True, False, False), 11)
+    h = (kw["h"].float() * size).to(TORCH_DT[dtype])
+    u, h64 = torch.finfo(TORCH_DT[dtype]).eps / 2, to_f64(h)
+    n = prn.block_norm(h, w_pre=kw["w_pre"], eps=0.0)[1]
+    ref = olm.block_norm(h64, w_pre=to_f64(kw["w_pre"]), eps=0.0)[1]
+    mean = (h64 ** 2).mean(-1, keepdims=True)
+    rel = 160 * E24 + 2.0 ** -150 / mean
+    assert (np.abs(to_f64(n) - ref) <= (u + rel) * np.abs(ref)).all()
+    dh = prn.block_norm_backward(None, dn, h, w_pre=kw["w_pre"], eps=0.0)[0]
+    args = (None, to_f64(dn), h64)
+    ref = olm.block_norm_backward(*args, w_pre=to_f64(kw["w_pre"]), eps=0.0)["dh"]
+    band = olm.block_norm_backward(*args, w_pre=to_f64(kw["w_pre"]), eps=0.0, size=True)["dh"]
+    assert (np.abs(to_f64(dh) - ref) <= u * np.abs(ref) + 4 * rel * band).all()
