@@ -451,13 +451,15 @@ typedef struct {
  *   x (N, d), W (V, d) storage dtype, targets (N)
  *   loss_out (N), lse_out (N) fp32
  * Logits are fp32 sums of exact bf16 products (bf16), or of products good to
- * 2^-20 (fp32 data: two fp16 terms of each value, three products; x's values
- * below 2^-17 of their token's largest one, and W's below 2^-17 of W's largest
- * one, are held to 2^-39 of that).  A value of x that is not finite gives its
- * token a non-finite lse (and loss, where it is not ignored) and no other; one of
- * W all tokens, or with bf16 those whose logit of it is not -inf.  A target that is neither
- * ignore_index nor in 0 .. V - 1 gives a NaN loss (nothing is read out of
- * bounds).  x and W must be 16-byte aligned. */
+ * 2^-20 (fp32 data: two fp16 terms of each value, three products; values below
+ * 2^-17 of the largest one are held to 2^-39 of that: of x the token's, of W the
+ * whole tensor's, but a row of more than 2^12 times its smallest eight values,
+ * with a mask's value among its channels, say, counts for itself).
+ * A value of x that is not finite gives its token a non-finite lse (and loss,
+ * where it is not ignored) and no other; one of W all tokens, or with bf16 those
+ * whose logit of it is not -inf.  A target that is neither ignore_index nor in
+ * 0 .. V - 1 gives a NaN loss (nothing is read out of bounds).  x and W must be
+ * 16-byte aligned. */
 prn_status prn_vocab_loss(const void* x, const void* W, const void* targets, const prn_vocab_loss_params* params,
                           float* loss_out, float* lse_out);
 
@@ -472,12 +474,14 @@ prn_status prn_vocab_loss(const void* x, const void* W, const void* targets, con
  * weight (an entry of less likelihood than that is a zero).  x and W go to the
  * matrix cores as fp16 too (two terms with fp32), scaled by powers of two: bf16
  * values exactly; values far below the largest one (2^-31 of it with bf16, 2^-17
- * with fp32) are held to 2^-39 of that.  The largest is that of the token for the
- * logits, of W for W, and for dW of weight x over the tokens.  A target out of range gives NaN in its row of dx and in
- * dW, and so does a value of x that is not finite, in an ignored row too.  x, W, dx_out and dW_out must be 16-byte aligned.  The workspace holds
- * one piece of dz (about 512 MB at most, or 512 bytes per token where that is
- * more; twice as much per entry with fp32), x twice and W once more in the matrix
- * cores' terms, and fp32 sums of dx and of a piece of dW. */
+ * with fp32) are held to 2^-39 of that: in the logits as above, in dW of weight x
+ * over the tokens, in dx of W, or of its column where it has such rows.
+ * A target out of range gives NaN in its row of dx and in dW, and so does a value
+ * of x that is not finite, in an ignored row too.  x, W, dx_out and dW_out must be
+ * 16-byte aligned.  The workspace holds one piece of dz (about 512 MB at most, or
+ * 512 bytes per token where that is more; twice as much per entry with fp32), x and
+ * W twice more in the matrix cores' terms, and fp32 sums of dx and of a piece of
+ * dW. */
 prn_status prn_vocab_loss_backward(const void* x, const void* W, const void* targets, const float* lse,
                                    const float* dloss, const float* dlse, const prn_vocab_loss_params* params,
                                    void* dx_out, void* dW_out);

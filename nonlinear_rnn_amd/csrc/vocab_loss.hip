@@ -33,11 +33,13 @@
 // weight, the power of two below the larger of |dloss| and |dloss + dlse|, by
 // 2^13 (so that a light token's row of dx is as good as a heavy one's).  dW, which
 // sums over tokens, takes x times the weight, scaled by the power of two of the
-// largest of these.  Values below 2^-17 of the largest one lose the low bits of
-// lo: at most 2^-39 of the largest, half a step of 2^-24 over 2^14; an entry of dz
-// is off by at most 2^-38 of its token's weight, half a step of 2^-24 over 2^13,
-// however small it is.  The units come back, in fp32, where they are used.
-// Everything is summed in fp32 in a fixed order.
+// largest of these.  A W of values far apart (kNear) has a unit for each larger
+// row in the logits and for each column in dx, so that a channel of mask values
+// leaves the other entries and channels alone.  Values below 2^-17 of the largest
+// one lose the low bits of lo: at most 2^-39 of the largest, half a step of 2^-24
+// over 2^14; an entry of dz is off by at most 2^-38 of its token's weight, half a
+// step of 2^-24 over 2^13, however small it is.  The units come back, in fp32,
+// where they are used.  Everything is summed in fp32 in a fixed order.
 #include "vocab_loss.h"
 
 #include <algorithm>
@@ -122,18 +124,25 @@ __global__ void __launch_bounds__(256) k_loss_pad(const uint16_t* __restrict__ i
   *reinterpret_cast<mm_s16x8*>(out + r * ldp + c0) = v;
 }
 
-constexpr int kMaxParts = 256;
+constexpr int kMaxParts = 1024;
 constexpr int kUnit = 13;   // dz is stored times 2^13: fp16 has entries down to 2^-37
+
+constexpr float kNoExponent = -1e4f;   // of nothing but zeros
+// W has one unit where every eight neighbouring values have one within 2^kNear
+// of the largest (or none but zeros).  Where not, rows of up to 2^kNear times the
+// smallest of those share one, and each larger row (with a mask's value among its
+// channels, say) has its own in the logits, and every column in dx.
+constexpr float kNear = 12.0f;
 
 // The units of a call
 struct LossUnits {
-  float iw;                        // z = acc iw s times the token's inverse unit
-  float back_x;                    // dx = acc back_x s u, u the token's weight
-  int32_t back_w;                  // dW = acc 2^back_w s
-  int32_t any_far;                 // is a token's lse2 kFar or more? (RowFar)
-  float parts[2][kMaxParts];       // the workgroups' maxima: of the exponents of u x; of |W|
+  float iw;                        // z = acc iw s times the token's inverse unit (and the row's, row_unit)
+  int32_t exponent;                // W's common one
+  int32_t wide;                    // has it others?
+  int32_t shift;                   // xg = u x 2^shift
+  int32_t odd;                     // has a row its own, or is a token's lse2 kFar or more? (RowFar)
+  float parts[3][kMaxParts];       // the workgroups' maxima: of the exponents of u x; of W's eights' and their negatives
 };
-constexpr float kNoExponent = -1e4f;   // of nothing but zeros
 
 template <class T>
 __device__ __forceinline__ int64_t target_at(const void* targets, int64_t n) {
@@ -152,26 +161,15 @@ __device__ __forceinline__ float block_max(float m, float* w) {
   for (int i = 0; i < static_cast<int>(blockDim.x >> 6); ++i) m = fmaxf(m, w[i]);
   return m;
 }
+__device__ __forceinline__ float join_parts(const float* part, int parts, float* w) {
+  float m = kNoExponent;
+  for (int q = threadIdx.x; q < parts; q += blockDim.x) m = fmaxf(m, part[q]);
+  return block_max(m, w);
+}
+__device__ __forceinline__ float two_to(int e) { return ldexpf(1.0f, e); }
 __device__ __forceinline__ float finite_max(float m, float v) {
   v = fabsf(v);
   return v < __builtin_inff() ? fmaxf(m, v) : m;
-}
-
-// eight values of a dense array of n from place i on (16-byte aligned, i a
-// multiple of 8); zeros past the end
-template <bool BF16>
-__device__ __forceinline__ void load8(const void* p, int64_t i, int64_t n, float* o) {
-  using S = Storage<BF16 ? kBF16 : kF32>;
-  const typename S::T* q = static_cast<const typename S::T*>(p) + i;
-  if (i + 8 <= n) {
-    typename S::T t[8];
-    __builtin_memcpy(t, __builtin_assume_aligned(q, 16), sizeof(t));
-#pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] = S::load(&t[e]);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] = i + e < n ? S::load(q + e) : 0.0f;
-  }
 }
 
 __device__ __forceinline__ int exponent_of(float m) { return max(static_cast<int>(__float_as_uint(m) >> 23) - 127, -126); }
@@ -192,72 +190,183 @@ __device__ __forceinline__ Arriving arriving(const float* dloss, const float* dl
   return a;
 }
 
-// eight values of row r from column c0 on, zeros past d
-template <bool BF16>
-__device__ __forceinline__ void row8(const void* p, int64_t r, int64_t d, int64_t c0, float* v) {
-  using S = Storage<BF16 ? kBF16 : kF32>;
-  const typename S::T* const q = static_cast<const typename S::T*>(p) + r * d + c0;
+// eight values of each of M rows (row(q) the q-th) from column c0 on, zeros past d
+template <bool BF16, int M, class Row>
+__device__ __forceinline__ void raw8(const void* p, Row row, int64_t d, int64_t c0,
+                                     typename Storage<BF16 ? kBF16 : kF32>::T (&t)[M][8]) {
+  using T = typename Storage<BF16 ? kBF16 : kF32>::T;
+  const T* const at = static_cast<const T*>(p) + c0;
   if (c0 + 8 <= d) {   // at once, aligned or not
-    typename S::T t[8];
-    __builtin_memcpy(t, q, sizeof(t));
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = S::load(&t[e]);
+    for (int q = 0; q < M; ++q) __builtin_memcpy(t[q], at + row(q) * d, sizeof(t[q]));
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = c0 + e < d ? S::load(q + e) : 0.0f;
+    for (int q = 0; q < M; ++q)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) t[q][e] = c0 + e < d ? at[row(q) * d + e] : T(0);
   }
 }
 
-// The maxima: workgroups [0, n1) of the exponents of u x (for dW; `lanes`
-// lanes a token), the last n2 of W.  Values that are not finite do not set a
-// unit, they go through as they are.
-template <bool BF16>
-__global__ void __launch_bounds__(1024) k_loss_maxima(const float* __restrict__ dloss, const float* __restrict__ dlse,
-                                                      const void* __restrict__ targets, int target_bytes, int64_t ignore,
-                                                      int64_t N, int64_t V, int64_t d, const void* __restrict__ x,
-                                                      const void* __restrict__ W, int n1, int lanes, int n2,
-                                                      LossUnits* __restrict__ u) {
-  __shared__ float w[16];
-  int b = static_cast<int>(blockIdx.x);
-  if (b == 0 && threadIdx.x == 0) u->any_far = 0;
-  if (b < n1) {
-    float top = kNoExponent;
-    const int lane = threadIdx.x % lanes, per = 1024 / lanes;
-    for (int64_t n = static_cast<int64_t>(b) * per + threadIdx.x / lanes; n < N; n += static_cast<int64_t>(n1) * per) {
-      const Arriving a = arriving(dloss, dlse, n, target_of(targets, target_bytes, n) == ignore);
-      float m = 0.0f;
-#pragma unroll 1
-      for (int64_t c0 = 8 * lane; c0 < d; c0 += 8 * lanes) {
-        float v[8];
-        row8<BF16>(x, n, d, c0, v);
+// The largest finite magnitudes of rows r, r + step, .. of R in all, `lanes` lanes
+// a row and two rows in flight (four take registers of which the occupancy
+// suffers): take(row, magnitude), in every lane.
+template <bool BF16, class Take>
+__device__ __forceinline__ void row_maxima(const void* p, int64_t r, int64_t step, int64_t R, int64_t d, int lanes, Take take) {
+  constexpr int kRows = 2;
+  const int lane = threadIdx.x % lanes;
+  for (; r < R; r += kRows * step) {
+    float m[kRows] = {};
+    for (int64_t c0 = 8 * lane; c0 < d; c0 += 8 * lanes) {
+      typename Storage<BF16 ? kBF16 : kF32>::T t[kRows][8];
+      raw8<BF16>(p, [&](int q) { return imin(r + q * step, R - 1); }, d, c0, t);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) m = finite_max(m, v[e]);
-      }
-      if (m > 0.0f && a.u > 0.0f) top = fmaxf(top, static_cast<float>(exponent_of(m) + exponent_of(a.u)));
+      for (int q = 0; q < kRows; ++q)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m[q] = finite_max(m[q], Storage<BF16 ? kBF16 : kF32>::load(&t[q][e]));
     }
+    for (int o = 1; o < lanes; o <<= 1) {
+#pragma unroll
+      for (int q = 0; q < kRows; ++q) m[q] = fmaxf(m[q], __shfl_xor(m[q], o, 64));
+    }
+#pragma unroll
+    for (int q = 0; q < kRows; ++q)
+      if (r + q * step < R) take(r + q * step, m[q]);
+  }
+}
+
+// Workgroups [0, n1): the tokens' largest magnitudes, `lanes` lanes a token, to
+// top_x, and the greatest of the exponents of u x (for dW, where there is a
+// dloss).  The last n2: the greatest and the least exponent of W's eights.  Values
+// that are not finite do not set a unit, they go through as they are.
+template <bool BF16>
+__global__ void __launch_bounds__(256) k_loss_maxima(const float* __restrict__ dloss, const float* __restrict__ dlse,
+                                                     const void* __restrict__ targets, int target_bytes, int64_t ignore,
+                                                     int64_t N, int64_t V, int64_t d, int64_t ldp, const void* __restrict__ x,
+                                                     const void* __restrict__ W, int n1, int lanes, int n2,
+                                                     LossUnits* __restrict__ u, float* __restrict__ top_x,
+                                                     uint32_t* __restrict__ columns) {
+  using S = Storage<BF16 ? kBF16 : kF32>;
+  __shared__ float w[4];
+  int b = static_cast<int>(blockIdx.x);
+  const int per = 256 / lanes;
+  const bool first = threadIdx.x % lanes == 0;
+  if (b == 0) {
+    if (columns)
+      for (int64_t c = threadIdx.x; c < ldp; c += 256) columns[c] = 0;
+  }
+  float top = kNoExponent, low = kNoExponent;
+  if (b < n1) {
+    row_maxima<BF16>(x, static_cast<int64_t>(b) * per + threadIdx.x / lanes, static_cast<int64_t>(n1) * per, N, d, lanes,
+                     [&](int64_t n, float m) {
+                       if (!first) return;
+                       top_x[n] = m;
+                       if (!dloss) return;
+                       const Arriving a = arriving(dloss, dlse, n, target_of(targets, target_bytes, n) == ignore);
+                       if (m > 0.0f && a.u > 0.0f) top = fmaxf(top, static_cast<float>(exponent_of(m) + exponent_of(a.u)));
+                     });
     top = block_max(top, w);
     if (threadIdx.x == 0) u->parts[0][b] = top;
     return;
   }
   b -= n1;
-  float m = 0.0f;
   const int64_t n = V * d;
-  for (int64_t i = (static_cast<int64_t>(b) * 1024 + threadIdx.x) * 8; i < n; i += static_cast<int64_t>(n2) * 8192) {
-    float v[8];
-    load8<BF16>(W, i, n, v);
+#pragma unroll 4
+  for (int64_t i = (static_cast<int64_t>(b) * 256 + threadIdx.x) * 8; i < n; i += static_cast<int64_t>(n2) * 2048) {
+    typename S::T t[8];
+    const typename S::T* const q = static_cast<const typename S::T*>(W) + i;
+    if (i + 8 <= n) {
+      __builtin_memcpy(t, __builtin_assume_aligned(q, 16), sizeof(t));
+    } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) m = finite_max(m, v[e]);
+      for (int e = 0; e < 8; ++e) t[e] = i + e < n ? q[e] : typename S::T(0);
+    }
+    float m = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = finite_max(m, S::load(&t[e]));
+    if (m > 0.0f) {
+      top = fmaxf(top, static_cast<float>(exponent_of(m)));
+      low = fmaxf(low, -static_cast<float>(exponent_of(m)));
+    }
   }
-  m = block_max(m, w);
-  if (threadIdx.x == 0) u->parts[1][b] = m;
+  top = block_max(top, w);
+  low = block_max(low, w);
+  if (threadIdx.x == 0) {
+    u->parts[1][b] = top;
+    u->parts[2][b] = low;
+  }
 }
 
-// the power of two that takes a largest value m to 2^14 .. 2^15, and its inverse
+// Joins the maxima and writes the units (the first workgroup); of a W of more than
+// one unit, workgroups [0, n1) the rows' largest magnitudes, to top_w, the others
+// the columns', as bits (so that it does not matter in which order they meet): 256
+// columns each, 8 a lane, 32 rows at a time of its share.
+template <bool BF16>
+__global__ void __launch_bounds__(1024) k_loss_units(const void* __restrict__ W, int64_t V, int64_t d, int n1, int lanes,
+                                                     int blocks, int64_t share, LossUnits* __restrict__ u, int parts1,
+                                                     int parts2, int gradients, float* __restrict__ top_w,
+                                                     uint32_t* __restrict__ top) {
+  constexpr int kRows = 4;
+  __shared__ float w[16];
+  __shared__ float hand[32][256];
+  const float greatest = join_parts(u->parts[1], parts2, w), least = -join_parts(u->parts[2], parts2, w);
+  const bool wide = greatest > kNoExponent && greatest > least + kNear;
+  if (blockIdx.x == 0) {
+    const float most = gradients ? join_parts(u->parts[0], parts1, w) : kNoExponent;
+    if (threadIdx.x == 0) {
+      u->exponent = greatest > kNoExponent ? static_cast<int>(fmaxf(fminf(greatest, least + kNear), -112.0f)) : 14;
+      u->iw = two_to(u->exponent - 14);
+      u->wide = wide;
+      u->shift = most > kNoExponent ? 14 - static_cast<int>(most) : 0;
+      u->odd = 0;
+    }
+  }
+  if (!wide) return;
+  const int tid = threadIdx.x, b = static_cast<int>(blockIdx.x);
+  if (b < n1) {
+    const int per = 1024 / lanes;
+    row_maxima<BF16>(W, static_cast<int64_t>(b) * per + tid / lanes, static_cast<int64_t>(n1) * per, V, d, lanes,
+                     [&](int64_t r, float m) {
+                       if (tid % lanes == 0) top_w[r] = m;
+                     });
+    return;
+  }
+  const int lane = tid & 31, g = tid >> 5;
+  const int64_t first = static_cast<int64_t>((b - n1) % blocks) * 256, c0 = first + 8 * lane;
+  const int64_t r0 = static_cast<int64_t>((b - n1) / blocks) * share, r1 = imin(r0 + share, V);
+  float m[8] = {};
+  if (c0 < d) {
+    for (int64_t r = r0 + g; r < r1; r += 32 * kRows) {
+      typename Storage<BF16 ? kBF16 : kF32>::T t[kRows][8];
+      raw8<BF16>(W, [&](int q) { return imin(r + 32 * q, r1 - 1); }, d, c0, t);
+#pragma unroll
+      for (int q = 0; q < kRows; ++q)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m[e] = finite_max(m[e], Storage<BF16 ? kBF16 : kF32>::load(&t[q][e]));
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) hand[g][8 * lane + e] = m[e];
+  __syncthreads();
+  if (tid >= 256 || first + tid >= d) return;
+  float t = hand[0][tid];
+#pragma unroll 8
+  for (int q = 1; q < 32; ++q) t = fmaxf(t, hand[q][tid]);
+  atomicMax(top + first + tid, __float_as_uint(t));
+}
+
+// the power of two that takes a largest value m to 2^14 .. 2^15 (a token's of its
+// x), and its inverse
 __device__ __forceinline__ float unit_of(float m, float* inverse) {
   const int e = m > 0.0f ? static_cast<int>(__float_as_uint(m) >> 23) - 127 : 14;
   const int k = min(max(14 - e, -126), 126);
   *inverse = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
   return __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
+}
+
+__device__ __forceinline__ float inverse_unit(float m) {
+  float inverse;
+  unit_of(m, &inverse);
+  return inverse;
 }
 
 // A token's row of dz in its units: sign 2^(|c| acc - lse2) - one at the target.
@@ -295,101 +404,80 @@ __device__ __forceinline__ void store_terms(const float* v, uint16_t* to, int64_
 }
 
 // Lays out x and W in fp16 terms, rows of ldp values (fp32 data: 2 ldp, every
-// 32 high terms and their 32 low ones), zeros past d.  Workgroups [0, n1):
-// tokens, `lanes` lanes each: xh in units of the token (its inverse to ix), and
-// for the gradients xg, for dW, times the token's weight u and in units of the
-// largest of these, u and the token's coefficients.  The others W, 8 columns a
-// thread.  The first writes the units.
+// 32 high terms and their 32 low ones), zeros past d, 8 columns a thread.
+// Workgroups [0, n1): x, to xh in units of the token, and for the gradients to xg,
+// for dW, times the token's weight u and in units of the largest of these; u and
+// the token's coefficients.  The others W, to wh in W's unit, or the row's own
+// (what that is larger to row_unit), and, where it has more than one, for dx to wd
+// in units of the column.
 template <bool BF16>
 __global__ void __launch_bounds__(256) k_loss_layout(const float* __restrict__ dloss, const float* __restrict__ dlse,
                                                      const float* __restrict__ lse, const void* __restrict__ targets,
                                                      int target_bytes, int64_t ignore, int64_t N, int64_t V, int64_t d,
                                                      float scale, int64_t ldp, const void* __restrict__ x,
-                                                     const void* __restrict__ W, int n1, int lanes, int parts1, int parts2,
-                                                     LossUnits* __restrict__ units, float* __restrict__ ix,
-                                                     float* __restrict__ weight, RowCoef* __restrict__ coef,
-                                                     RowFar* __restrict__ far, uint16_t* __restrict__ xh,
-                                                     uint16_t* __restrict__ xg, uint16_t* __restrict__ wh) {
-  __shared__ float w[4];
+                                                     const void* __restrict__ W, int n1, LossUnits* __restrict__ units, const float* __restrict__ top_x,
+                                                     const float* __restrict__ top_w, float* __restrict__ row_unit,
+                                                     const uint32_t* __restrict__ columns, float* __restrict__ weight,
+                                                     RowCoef* __restrict__ coef, RowFar* __restrict__ far,
+                                                     uint16_t* __restrict__ xh, uint16_t* __restrict__ xg,
+                                                     uint16_t* __restrict__ wh, uint16_t* __restrict__ wd) {
+  using S = Storage<BF16 ? kBF16 : kF32>;
   const int64_t b = block_in_rows();
-  const int tid = threadIdx.x;
-  auto maximum = [&](int k, int parts, float least) { return block_max(tid < parts ? units->parts[k][tid] : least, w); };
-  float iw;
-  const float unit_w = unit_of(maximum(1, parts2, 0.0f), &iw);
-  if (b >= n1) {
-    const int64_t C = ldp / 8, i = (b - n1) * 256 + tid;
-    if (i >= V * C) return;
-    const int64_t r = i / C, c0 = (i - r * C) * 8;
-    float v[8];
-    row8<BF16>(W, r, d, c0, v);
+  const bool is_x = b < n1;
+  const int64_t R = is_x ? N : V, C = ldp / 8, i = (is_x ? b : b - n1) * 256 + threadIdx.x;
+  if (i >= R * C) return;
+  const int64_t r = i / C, c0 = (i - r * C) * 8;
+  typename S::T t[1][8];
+  raw8<BF16>(is_x ? x : W, [&](int) { return r; }, d, c0, t);
+  float v[8], s[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] *= unit_w;
-    store_terms<BF16>(v, wh, r, ldp, c0);
+  for (int e = 0; e < 8; ++e) v[e] = S::load(&t[0][e]);
+  if (!is_x) {
+    const bool wide = units->wide != 0;
+    int own = units->exponent;
+    if (wide) own = max(exponent_of(top_w[r]), own);   // (zeros: the common one)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[e] = ldexpf(v[e], 14 - own);
+    store_terms<BF16>(s, wh, r, ldp, c0);
+    if (wd && wide) {
+      uint32_t k[8];
+      __builtin_memcpy(k, __builtin_assume_aligned(columns + c0, 32), sizeof(k));
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s[e] = ldexpf(v[e], 14 - exponent_of(__uint_as_float(k[e])));
+      store_terms<BF16>(s, wd, r, ldp, c0);
+    }
+    if (c0 == 0) {
+      row_unit[r] = two_to(min(own - units->exponent, 127));
+      if (own > units->exponent) units->odd = 1;
+    }
     return;
   }
-  int shift = 0;   // xg = u x 2^shift
-  if (xg) {
-    const float top = maximum(0, parts1, kNoExponent);
-    shift = top > kNoExponent ? 14 - static_cast<int>(top) : 0;
-  }
-  if (b == 0 && tid == 0) {
-    units->iw = iw;
-    units->back_x = iw / (1 << kUnit);
-    units->back_w = -shift - kUnit;
-  }
-  const int64_t n = b * (256 / lanes) + tid / lanes;
-  if (n >= N) return;   // all lanes of a token
-  const int lane = tid % lanes;
-  float m = 0.0f, v[8];
-  row8<BF16>(x, n, d, 8 * lane, v);   // kept: most rows have no more
-#pragma unroll
-  for (int e = 0; e < 8; ++e) m = finite_max(m, v[e]);
-#pragma unroll 2
-  for (int64_t c0 = 8 * (lane + lanes); c0 < d; c0 += 8 * lanes) {
-    float o[8];
-    row8<BF16>(x, n, d, c0, o);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) m = finite_max(m, o[e]);
-  }
-  for (int o = 1; o < lanes; o <<= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
   float inverse;
-  const float unit = unit_of(m, &inverse);
-  Arriving in{};
-  int64_t t = 0;
-  if (xg) {
-    t = target_of(targets, target_bytes, n);
-    in = arriving(dloss, dlse, n, t == ignore);
-    shift += exponent_of(in.u);
-  }
-#pragma unroll 2
-  for (int64_t c0 = 8 * lane; c0 < ldp; c0 += 8 * lanes) {
-    float s[8];
-    if (c0 >= 8 * lanes) row8<BF16>(x, n, d, c0, v);
+  const float unit = unit_of(top_x[r], &inverse);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) s[e] = v[e] * unit;
-    store_terms<BF16>(s, xh, n, ldp, c0);
-    if (xg) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) s[e] = in.u > 0.0f ? ldexpf(v[e], shift) : v[e] * 0.0f;
-      store_terms<BF16>(s, xg, n, ldp, c0);
-    }
-  }
-  if (lane != 0) return;
-  ix[n] = inverse;
+  for (int e = 0; e < 8; ++e) s[e] = v[e] * unit;
+  store_terms<BF16>(s, xh, r, ldp, c0);
   if (!xg) return;
-  weight[n] = in.u;
+  const int64_t target = target_of(targets, target_bytes, r);
+  const Arriving in = arriving(dloss, dlse, r, target == ignore);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) s[e] = in.u > 0.0f ? ldexpf(v[e], units->shift + exponent_of(in.u)) : v[e] * 0.0f;
+  store_terms<BF16>(s, xg, r, ldp, c0);
+  if (c0 != 0) return;
+  weight[r] = in.u;
   const float u = in.u > 0.0f ? in.u : 1.0f, p = in.both / u;
-  RowCoef r;
-  r.c = copysignf(above_zero(scale * kLog2e * iw * inverse), p);
-  r.one = in.one / u * (1 << kUnit);
+  const float iw = units->iw;
+  RowCoef k;
+  k.c = copysignf(above_zero(scale * kLog2e * iw * inverse), p);
+  k.one = in.one / u * (1 << kUnit);
   // no such entry: the loss was NaN, and so is its gradient
-  const bool lost = t != ignore && (t < 0 || t >= V);
-  const float log2p = log2f(fabsf(p)), l = lse[n];
-  r.lse2 = lost ? __builtin_nanf("") : fmaf(l, kLog2e, -log2p) - kUnit;   // p = 0: +inf, a row of zeros
-  r.target = t == ignore || lost ? -1 : static_cast<int32_t>(t);
-  coef[n] = r;
-  far[n] = {iw * inverse * scale, l, log2p + kUnit, 0.0f};
-  if (is_far(r.lse2)) units->any_far = 1;
+  const bool lost = target != ignore && (target < 0 || target >= V);
+  const float log2p = log2f(fabsf(p)), l = lse[r];
+  k.lse2 = lost ? __builtin_nanf("") : fmaf(l, kLog2e, -log2p) - kUnit;   // p = 0: +inf, a row of zeros
+  k.target = target == ignore || lost ? -1 : static_cast<int32_t>(target);
+  coef[r] = k;
+  far[r] = {iw * inverse * scale, l, log2p + kUnit, 0.0f};
+  if (is_far(k.lse2)) units->odd = 1;
 }
 
 // ------------------------------------------------------------- forward ---
@@ -403,10 +491,12 @@ __global__ void __launch_bounds__(256) k_loss_layout(const float* __restrict__ d
 template <class Tl, bool F16>
 __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_lse(MmOperand W, MmOperand X, int64_t N, int64_t V, int64_t d,
                                                           float c_, const LossUnits* __restrict__ units,
-                                                          const float* __restrict__ ix, int n_tok, int splits,
+                                                          const float* __restrict__ top_x,
+                                                          const float* __restrict__ row_unit, int n_tok, int splits,
                                                           int per_split, float2* __restrict__ part) {
   if constexpr (F16) c_ *= units->iw;
-  auto factor = [&](int64_t n) { return F16 ? above_zero(c_ * ix[imin(n, N - 1)]) : c_; };
+  const bool odd = F16 && __builtin_amdgcn_readfirstlane(units->odd) != 0;
+  auto factor = [&](int64_t n) { return F16 ? above_zero(c_ * inverse_unit(top_x[imin(n, N - 1)])) : c_; };
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Tl::LDS];
   __shared__ float2 hand[Tl::WR][Tl::BN];
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, l32 = lane & 31;
@@ -452,6 +542,23 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_lse(MmOperand W, MmOperand
     for (uint32_t t = t0; t < t1; ++t) {
       const int64_t v0 = static_cast<int64_t>(t) * Tl::BM;
       tile.template multiply<false, false, false, F16>(next);
+      if constexpr (F16) {
+        if (odd) {   // rows of W in units of their own
+#pragma unroll
+          for (int i = 0; i < Tl::WM; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const float4 f = *reinterpret_cast<const float4*>(row_unit + v0 + (wr * Tl::WM + i) * 32 + 8 * q + 4 * half);
+#pragma unroll
+              for (int j = 0; j < Tl::WN; ++j) {
+                tile.acc[i][j][4 * q] *= f.x;
+                tile.acc[i][j][4 * q + 1] *= f.y;
+                tile.acc[i][j][4 * q + 2] *= f.z;
+                tile.acc[i][j][4 * q + 3] *= f.w;
+              }
+            }
+        }
+      }
       if (v0 + Tl::BM > V) {
         const int left = static_cast<int>(V - v0) - wr * Tl::WM * 32 - 4 * half;
 #pragma unroll
@@ -545,14 +652,14 @@ template <bool BF16>
 __global__ void __launch_bounds__(256) k_loss_join(const float2* __restrict__ part, int splits, const void* __restrict__ x,
                                                    const void* __restrict__ W, const void* __restrict__ targets,
                                                    int target_bytes, int64_t N, int64_t V, int64_t d, float scale,
-                                                   const LossUnits* __restrict__ units, const float* __restrict__ ix,
+                                                   const LossUnits* __restrict__ units, const float* __restrict__ top_x,
                                                    int64_t ignore,
                                                    float* __restrict__ loss, float* __restrict__ lse) {
   using S = Storage<BF16 ? kBF16 : kF32>;
   const int64_t n = block_in_rows() * 4 + (threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
   if (n >= N) return;
-  const float back = BF16 ? 1.0f : units->iw * ix[n], c = above_zero(scale * kLog2e * back);
+  const float back = BF16 ? 1.0f : units->iw * inverse_unit(top_x[n]), c = above_zero(scale * kLog2e * back);
   const int64_t t = target_of(targets, target_bytes, n);
   const bool in = t >= 0 && t < V;
   // the pairs are on their way while the dot product waits for the target
@@ -608,9 +715,10 @@ template <class Tl, bool BF16>
 __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_dz(MmOperand W, MmOperand X, int64_t N, int64_t V, int64_t d,
                                                          const LossUnits* __restrict__ units, int64_t piece0,
                                                          int64_t piece1, int n_tok, const RowCoef* __restrict__ coef,
-                                                         const RowFar* __restrict__ far, uint16_t* __restrict__ dz,
+                                                         const RowFar* __restrict__ far,
+                                                         const float* __restrict__ row_unit, uint16_t* __restrict__ dz,
                                                          int64_t ldz) {
-  const bool any_far = __builtin_amdgcn_readfirstlane(units->any_far) != 0;
+  const bool odd = __builtin_amdgcn_readfirstlane(units->odd) != 0;
   // the loads are up to NST tiles ahead (tiles of one stage)
   constexpr int kRing = Tl::NST + 1;
   static_assert(sizeof(RowCoef) == 16 && Tl::BN % 64 == 0 && Tl::BN / 64 <= Tl::NW, "one coefficient load per wave");
@@ -681,13 +789,19 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_dz(MmOperand W, MmOperand 
           float v[16];
 #pragma unroll
           for (int r = 0; r < 16; ++r) v[r] = ex2(fmaf(tile.acc[i2][j][r], c, -rc.lse2));
-          if (any_far) {   // such tokens' exponents, at most 14 (twice the weight) whatever lse's rounding
+          if (odd) {   // rows in units of their own; far tokens' exponents, at most 14 (twice the weight) whatever lse's rounding
             asm volatile("");
             const RowFar f = far[imin(n0 + tl, N - 1)];
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-              const float e = fmaf(fmaf(tile.acc[i2][j][r], f.back, -f.lse), kLog2e, f.log2p);
-              v[r] = is_far(rc.lse2) ? ex2(fminf(e, kUnit + 1.0f)) : v[r];
+            for (int q = 0; q < 4; ++q) {
+              const float4 k = *reinterpret_cast<const float4*>(row_unit + v0 + vb + 8 * q + 4 * eh);
+              const float of[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                const float a = tile.acc[i2][j][4 * q + r] * of[r];
+                const float e = fmaf(fmaf(a, f.back, -f.lse), kLog2e, f.log2p);
+                v[4 * q + r] = ex2(is_far(rc.lse2) ? fminf(e, kUnit + 1.0f) : fmaf(a, c, -rc.lse2));
+              }
             }
           }
           if (negative) {
@@ -753,13 +867,18 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_dz(MmOperand W, MmOperand 
   }
 }
 
-// a sum of dx (or dW) from its units: dx's are the token's, of weight u
+// a sum of dx (or dW) from its units: dx's are the token's, of weight u, and the
+// column's
 template <bool IS_W>
-__device__ __forceinline__ float loss_finish(float v, const LossUnits* units, float u, float scale) {
+__device__ __forceinline__ float loss_finish(float v, int shift, float u, float column, float scale) {
   if constexpr (IS_W)
-    return ldexpf(v * scale, units->back_w);
+    return ldexpf(v * scale, -shift - kUnit);
   else
-    return v * units->back_x * (u * scale);
+    return v * column * (u * scale);
+}
+// a column's: wd is W 2^(14 - exponent), dz has 2^kUnit
+__device__ __forceinline__ float column_back(uint32_t top) {
+  return ldexpf(1.0f, exponent_of(__uint_as_float(top)) - 14 - kUnit);
 }
 
 // P[z][r][c] (+)= sum over k of slice z of A(r, k) B(c, k), fp32, C columns; or,
@@ -770,7 +889,9 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_mm(MmOperand A, MmOperand 
                                                          int64_t k_slice, int n_col, int slices, int add,
                                                          float* __restrict__ P, void* __restrict__ out,
                                                          const LossUnits* __restrict__ units,
-                                                         const float* __restrict__ weight, float scale) {
+                                                         const float* __restrict__ weight,
+                                                         const uint32_t* __restrict__ columns,
+                                                         const uint16_t* __restrict__ wide_b, float scale) {
   using T = typename Storage<BF16 ? kBF16 : kF32>::T;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Tl::LDS];
   const uint32_t u = Units(gridDim.x).u, tiles = gridDim.x / slices, z = u / tiles, ti = u - z * tiles;
@@ -779,6 +900,13 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_mm(MmOperand A, MmOperand 
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, l32 = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wr = wave / Tl::WC, wc = wave % Tl::WC;
+  const int shift = units->shift;
+  const float iw = units->iw;
+  bool wide = false;
+  if constexpr (!TA) {   // dx: W in units of its columns, where it has more than one
+    wide = units->wide != 0;
+    B.base = wide ? wide_b : B.base;
+  }
   Tl tile;
   tile.open(lds, A, R, B, C, k0, k1);
   auto next = []() {};
@@ -810,6 +938,15 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_mm(MmOperand A, MmOperand 
   const uint32_t oat = rl * static_cast<uint32_t>(C) + cl;
   auto stores = [&](auto kind) {   // 0: sums that go on, 1: finished ones, 2: as `out` says
     constexpr int KIND = decltype(kind)::value;
+    float column[Tl::WN] = {};
+    if constexpr (!TA && KIND == 1) {
+#pragma unroll
+      for (int j = 0; j < Tl::WN; ++j) column[j] = iw / (1 << kUnit);
+      if (wide) {
+#pragma unroll
+        for (int j = 0; j < Tl::WN; ++j) column[j] = column_back(columns[imin(c0 + cl + 32 * j, C - 1)]);
+      }
+    }
 #pragma unroll
     for (int i = 0; i < Tl::WM; ++i) {
       float u[16] = {};   // the rows' weights (there are some for a whole tile)
@@ -828,7 +965,7 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_mm(MmOperand A, MmOperand 
           if (rl + ri < rows && cl + 32 * j < cols) {
             if (KIND == 1 || (KIND == 2 && out))
               obase[oat + ri * static_cast<uint32_t>(C) + 32 * j] =
-                  Storage<BF16 ? kBF16 : kF32>::pack(loss_finish<TA>(tile.acc[i][j][r], units, u[r], scale));
+                  Storage<BF16 ? kBF16 : kF32>::pack(loss_finish<TA>(tile.acc[i][j][r], shift, u[r], column[j], scale));
             else
               *reinterpret_cast<float*>(base + (at + ri * ldb + 128 * j)) = tile.acc[i][j][r];
           }
@@ -850,13 +987,17 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_loss_mm(MmOperand A, MmOperand 
 template <bool BF16, bool IS_W>
 __global__ void __launch_bounds__(256) k_loss_out(const float* __restrict__ P, int S, int64_t n, int64_t d,
                                                   const LossUnits* __restrict__ units,
-                                                  const float* __restrict__ weight, float scale,
+                                                  const float* __restrict__ weight,
+                                                  const uint32_t* __restrict__ columns, float scale,
                                                   typename Storage<BF16 ? kBF16 : kF32>::T* __restrict__ out) {
   const int64_t i = block_in_rows() * 256 + threadIdx.x;
   if (i >= n) return;
   float sum = 0.0f;
   for (int z = 0; z < S; ++z) sum += P[z * n + i];
-  out[i] = Storage<BF16 ? kBF16 : kF32>::pack(loss_finish<IS_W>(sum, units, IS_W ? 1.0f : weight[i / d], scale));
+  const int64_t r = IS_W ? 0 : i / d;
+  const float column = IS_W ? 1.0f : units->wide ? column_back(columns[i - r * d]) : units->iw / (1 << kUnit);
+  out[i] = Storage<BF16 ? kBF16 : kF32>::pack(
+      loss_finish<IS_W>(sum, units->shift, IS_W ? 1.0f : weight[r], column, scale));
 }
 
 template <class T>
@@ -879,7 +1020,7 @@ struct Plan {
   bool pad;
   int planes;            // terms of x, W and dz
   int64_t ldp;
-  size_t units_off, ix_off, weight_off, xp_off, wp_off, xh_off, xg_off, wh_off, end;
+  size_t units_off, topx_off, topw_off, row_off, col_off, weight_off, xp_off, wp_off, xh_off, xg_off, wh_off, wd_off, end;
 };
 // Rows laid out anew are whole lines of 128 bytes, or an even part of one: a
 // stage reads 128 bytes of every row, which other rows have in two lines (a
@@ -905,13 +1046,17 @@ Plan plan_operands(const LossArgs& a, bool back) {
     return at;
   };
   p.units_off = take(terms, sizeof(LossUnits));
-  p.ix_off = take(terms, size_t(a.N) * 4);
+  p.topx_off = take(terms, size_t(a.N) * 4);
+  p.topw_off = take(terms, size_t(a.V) * 4);
+  p.row_off = take(terms, size_t(cdiv(a.V, kBM)) * kBM * 4);   // whole tiles
+  p.col_off = take(back, size_t(p.ldp) * 4);
   p.weight_off = take(back, size_t(cdiv(a.N, kBM)) * kBM * 4);
   p.xp_off = take(p.pad, size_t(a.N) * p.ldp * 2);
   p.wp_off = take(p.pad, size_t(a.V) * p.ldp * 2);
   p.xh_off = take(terms, size_t(p.planes) * a.N * p.ldp * 2);
   p.xg_off = take(back, size_t(p.planes) * a.N * p.ldp * 2);
   p.wh_off = take(terms, size_t(p.planes) * a.V * p.ldp * 2);
+  p.wd_off = take(back, size_t(p.planes) * a.V * p.ldp * 2);
   p.end = off;
   return p;
 }
@@ -1034,35 +1179,46 @@ PlanBw plan_bw(const LossArgs& a) {
   return b;
 }
 
-// The operands: X and Wo of the logits, Wh of dx and Xg of dW (fp16 terms);
-// with `coef`, the tokens' coefficients.  For the forward dloss .. coef are null.
+// The operands: X and Wo of the logits, Wo or (a W of more than one unit) Wd of dx
+// (with dx_too) and Xg of dW (fp16 terms); with `coef`, the tokens' coefficients.  For the forward dloss ..
+// far are null.
 struct Operands {
-  MmOperand X, Wo, Xg, Wh;
+  MmOperand X, Wo, Xg, Wd;
   LossUnits* units;
-  float *ix, *weight;
+  float *top_x, *top_w, *row, *weight;
+  uint32_t* col;
 };
 Operands lay_out(const LossArgs& a, const Plan& p, const void* x, const void* W, const void* targets, const float* lse,
-                 const float* dloss, const float* dlse, RowCoef* coef, RowFar* far) {
+                 const float* dloss, const float* dlse, RowCoef* coef, RowFar* far, bool dx_too) {
   Operands o{};
   auto at = [&](size_t off) { return reinterpret_cast<uint16_t*>(a.ws + off); };
   if (coef || !a.bf16) {
-    auto parts = [](int64_t n) { return int(std::min<int64_t>(kMaxParts, cdiv(n, 1024))); };
+    auto parts = [](int64_t n) { return int(std::min<int64_t>(kMaxParts, cdiv(n, 256))); };
     o.units = reinterpret_cast<LossUnits*>(a.ws + p.units_off);
-    o.ix = reinterpret_cast<float*>(a.ws + p.ix_off);
+    o.top_x = reinterpret_cast<float*>(a.ws + p.topx_off);
+    o.top_w = reinterpret_cast<float*>(a.ws + p.topw_off);
     o.weight = reinterpret_cast<float*>(a.ws + p.weight_off);
     o.X = {at(p.xh_off), p.planes * p.ldp};
     o.Xg = {at(p.xg_off), p.planes * p.ldp};
-    o.Wo = o.Wh = {at(p.wh_off), p.planes * p.ldp};
-    const int lanes = a.d <= 128 ? 16 : 64;
-    const int p1 = coef ? parts(a.N * lanes) : 0, p2 = parts(cdiv(a.V * a.d, 8));
-    const int64_t n1 = cdiv(a.N, 256 / lanes), n2 = cdiv(a.V * (p.ldp / 8), 256);
+    o.Wo = {at(p.wh_off), p.planes * p.ldp};
+    o.Wd = {at(p.wd_off), p.planes * p.ldp};
+    o.row = reinterpret_cast<float*>(a.ws + p.row_off);
+    o.col = dx_too ? reinterpret_cast<uint32_t*>(a.ws + p.col_off) : nullptr;
+    const int lanes = a.d <= 128 ? 16 : a.d <= 256 ? 32 : 64;
+    const int p1 = parts(a.N * lanes), p2 = parts(cdiv(a.V * a.d, 8));
+    const int64_t n1 = cdiv(a.N * (p.ldp / 8), 256), n2 = cdiv(a.V * (p.ldp / 8), 256);
     auto go = [&](auto bf) {
       constexpr bool BF = decltype(bf)::value;
-      k_loss_maxima<BF><<<unsigned(p1 + p2), 1024, 0, a.stream>>>(dloss, dlse, targets, a.target_bytes, a.ignore, a.N,
-                                                                       a.V, a.d, x, W, p1, lanes, p2, o.units);
+      k_loss_maxima<BF><<<unsigned(p1 + p2), 256, 0, a.stream>>>(dloss, dlse, targets, a.target_bytes, a.ignore, a.N, a.V,
+                                                                 a.d, p.ldp, x, W, p1, lanes, p2, o.units, o.top_x, o.col);
+      const int64_t blocks = cdiv(a.d, 256), share = cdiv(cdiv(a.V, std::max<int64_t>(1, 128 / blocks)), 32) * 32;
+      const int64_t rows = std::min<int64_t>(128, cdiv(a.V * lanes, 1024)), cols = dx_too ? blocks * cdiv(a.V, share) : 0;
+      k_loss_units<BF><<<unsigned(rows + cols), 1024, 0, a.stream>>>(W, a.V, a.d, int(rows), lanes, int(blocks), share, o.units,
+                                                                     p1, p2, coef != nullptr, o.top_w, o.col);
       k_loss_layout<BF><<<rows_of_blocks(n1 + n2), 256, 0, a.stream>>>(
-          dloss, dlse, lse, targets, a.target_bytes, a.ignore, a.N, a.V, a.d, a.scale, p.ldp, x, W, int(n1), lanes,
-          p1, p2, o.units, o.ix, o.weight, coef, far, at(p.xh_off), coef ? at(p.xg_off) : nullptr, at(p.wh_off));
+          dloss, dlse, lse, targets, a.target_bytes, a.ignore, a.N, a.V, a.d, a.scale, p.ldp, x, W, int(n1),
+          o.units, o.top_x, o.top_w, o.row, o.col, o.weight, coef, far, at(p.xh_off), coef ? at(p.xg_off) : nullptr, at(p.wh_off),
+          dx_too ? at(p.wd_off) : nullptr);
     };
     if (a.bf16) go(std::true_type{}); else go(std::false_type{});
   }
@@ -1095,14 +1251,14 @@ size_t loss_backward_workspace(const LossArgs& a) { return a.N ? plan_bw(a).tota
 
 void launch_loss(const LossArgs& a, const void* x, const void* W, const void* targets, float* loss, float* lse) {
   const PlanFw f = plan_fw(a);
-  const Operands o = lay_out(a, f.op, x, W, targets, nullptr, nullptr, nullptr, nullptr, nullptr);
+  const Operands o = lay_out(a, f.op, x, W, targets, nullptr, nullptr, nullptr, nullptr, nullptr, false);
   const float c = a.scale * kLog2e;
   float2* part = reinterpret_cast<float2*>(a.ws + f.part_off);
   auto go = [&](auto pair) {
     constexpr bool PAIR = decltype(pair)::value;
     auto run = [&](auto tl) {
       using Tl = decltype(tl);
-      k_loss_lse<Tl, PAIR><<<unsigned(f.grid), Tl::NTHR, 0, a.stream>>>(o.Wo, o.X, a.N, a.V, a.d, c, o.units, o.ix, int(f.n_tok),
+      k_loss_lse<Tl, PAIR><<<unsigned(f.grid), Tl::NTHR, 0, a.stream>>>(o.Wo, o.X, a.N, a.V, a.d, c, o.units, o.top_x, o.row, int(f.n_tok),
                                                                        int(f.splits), int(f.per_split), part);
     };
     if (f.kind == 0) run(Few<PAIR>{}); else if (f.kind == 1) run(Mid<PAIR>{}); else run(Big<PAIR>{});
@@ -1111,10 +1267,10 @@ void launch_loss(const LossArgs& a, const void* x, const void* W, const void* ta
   const dim3 jg = rows_of_blocks(cdiv(a.N, 4));
   if (a.bf16)
     k_loss_join<true><<<jg, 256, 0, a.stream>>>(part, int(f.splits), x, W, targets, a.target_bytes, a.N, a.V, a.d,
-                                                a.scale, o.units, o.ix, a.ignore, loss, lse);
+                                                a.scale, o.units, o.top_x, a.ignore, loss, lse);
   else
     k_loss_join<false><<<jg, 256, 0, a.stream>>>(part, int(f.splits), x, W, targets, a.target_bytes, a.N, a.V, a.d,
-                                                 a.scale, o.units, o.ix, a.ignore, loss, lse);
+                                                 a.scale, o.units, o.top_x, a.ignore, loss, lse);
 }
 
 void launch_loss_backward(const LossArgs& a, const void* x, const void* W, const void* targets, const float* lse,
@@ -1133,11 +1289,11 @@ void launch_loss_backward(const LossArgs& a, const void* x, const void* W, const
   uint16_t* dz = reinterpret_cast<uint16_t*>(a.ws + b.dz_off);
   float* px = reinterpret_cast<float*>(a.ws + b.px_off);
   float* pw = reinterpret_cast<float*>(a.ws + b.pw_off);
-  const Operands o = lay_out(a, b.op, x, W, targets, lse, dloss, dlse, coef, far);
+  const Operands o = lay_out(a, b.op, x, W, targets, lse, dloss, dlse, coef, far, dx != nullptr);
   LossUnits* const units = o.units;
   auto out = [&](auto bf, auto is_w, const float* P, int S, int64_t n, const float* weight, void* to) {
     constexpr bool BF = decltype(bf)::value, IS_W = decltype(is_w)::value;
-    k_loss_out<BF, IS_W><<<rows_of_blocks(cdiv(n, 256)), 256, 0, a.stream>>>(P, S, n, a.d, units, weight, a.scale,
+    k_loss_out<BF, IS_W><<<rows_of_blocks(cdiv(n, 256)), 256, 0, a.stream>>>(P, S, n, a.d, units, weight, o.col, a.scale,
                                                                        static_cast<typename Storage<BF ? kBF16 : kF32>::T*>(to));
   };
   auto typed = [&](auto run) {
@@ -1155,14 +1311,14 @@ void launch_loss_backward(const LossArgs& a, const void* x, const void* W, const
         using Tl = decltype(tl);
         const int64_t n_tok = cdiv(a.N, Tl::BN), tiles = n_tok * cdiv(nv, kBM), slots = (b.big_z ? 1 : mid_slots(BF)) * kCus;
         k_loss_dz<Tl, BF><<<unsigned(std::min(tiles, slots)), Tl::NTHR, 0, a.stream>>>(
-            o.Wo, o.X, a.N, a.V, a.d, units, v0, pend, int(n_tok), coef, far, dz, b.ldz);
+            o.Wo, o.X, a.N, a.V, a.d, units, v0, pend, int(n_tok), coef, far, o.row, dz, b.ldz);
       };
       if (b.big_z) run(Big<!BF>{}); else run(Mid<!BF>{});
     });
     const MmOperand Z{dz, b.ldz};
     // head rows, then the rest, of a product whose rows lie `step` apart in Z
-    auto product = [&](auto ta, const Cut& c, int64_t step, const MmOperand& B, int64_t rows, int64_t K, bool add, float* P,
-                       bool finish, void* to) {
+    auto product = [&](auto ta, const Cut& c, int64_t step, const MmOperand& B, const uint16_t* wide_b, int64_t rows,
+                       int64_t K, bool add, float* P, bool finish, void* to) {
       constexpr bool TA = decltype(ta)::value;
       auto part = [&](int64_t r0, int64_t n, int64_t s, int64_t len, float* sums) {
         if (n <= 0) return;
@@ -1175,7 +1331,7 @@ void launch_loss_backward(const LossArgs& a, const void* x, const void* W, const
             using Tl = decltype(tl);
             const int64_t n_col = cdiv(a.d, Tl::BN);
             k_loss_mm<Tl, TA, BF><<<unsigned(cdiv(n, kBM) * n_col * s), Tl::NTHR, 0, a.stream>>>(
-                A, B, n, a.d, K, len, int(n_col), int(s), add, sums, finish && s == 1 ? dst : nullptr, units, o.weight + r0, a.scale);
+                A, B, n, a.d, K, len, int(n_col), int(s), add, sums, finish && s == 1 ? dst : nullptr, units, o.weight + r0, o.col, wide_b, a.scale);
           };
           if (b.out == kBig) run(Big<!BF>{}); else run(Wide<!BF>{});
           if (finish && s > 1) out(bf, ta, sums, int(s), n * a.d, o.weight + r0, dst);
@@ -1186,10 +1342,10 @@ void launch_loss_backward(const LossArgs& a, const void* x, const void* W, const
       part(head, rows - head, c.s, c.len, P + head * a.d);
     };
     if (dx) {
-      const MmOperand Wc{o.Wh.base + v0 * o.Wh.ld, o.Wh.ld};
-      product(std::false_type{}, b.x, b.ldz, Wc, a.N, nv, v0 > 0, px, last, dx);
+      const MmOperand Wc{o.Wo.base + v0 * o.Wo.ld, o.Wo.ld};
+      product(std::false_type{}, b.x, b.ldz, Wc, o.Wd.base + v0 * o.Wd.ld, a.N, nv, v0 > 0, px, last, dx);
     }
-    if (dW) product(std::true_type{}, b.w, b.op.planes, o.Xg, nv, a.N, false, pw, true, static_cast<uint8_t*>(dW) + v0 * a.d * elt);
+    if (dW) product(std::true_type{}, b.w, b.op.planes, o.Xg, nullptr, nv, a.N, false, pw, true, static_cast<uint8_t*>(dW) + v0 * a.d * elt);
   }
 }
 

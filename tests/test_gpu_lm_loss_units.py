@@ -220,3 +220,30 @@ def test_logits_that_hold_no_fraction(dtype, size, shift):
         assert rows
         size_ = (np.abs(both) + np.abs(one))[:, None] * np.abs(W64).max(0)
         assert (np.abs(to_f64(dx) - want) <= 2.0 ** -20 * size_)[rows].all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("mask", [-1e9, -1e30, -3.3895314e38])
+@pytest.mark.parametrize("N,V,d", [(64, 700, 40), (150, 1500, 300), (5, 9000, 600)])
+def test_masked_entries(N, V, d, mask, dtype):
+    """A channel of ones in x and of a bias in W, which is a mask's value at some entries (-1e9, or the type's
+    lowest): their probability is 0, and no other entry, token or channel feels how large it is.  The bands are
+    those of the entries that are left, over the other channels."""
+    x, W, t, dloss, dlse = _inputs(N, V, d, dtype, 8)
+    x[:, 0] = 1.0
+    off = torch.zeros(V, dtype=torch.bool, device="cuda")
+    off[torch.randperm(V, generator=torch.Generator().manual_seed(V))[: V // 5].cuda()] = True
+    t = torch.where(off[t.clamp(min=0)], torch.full_like(t, -100), t)
+    W[off, 0] = mask
+    loss, lse = prn.vocab_loss(x, W, t)
+    dx, dW = prn.vocab_loss_backward(dloss, x, W, t, lse, dlse=dlse)
+    keep = (~off).cpu().numpy()
+    new = np.where(keep, np.cumsum(keep) - 1, 0)
+    tn = t.cpu().numpy()
+    ref, band = _bands(to_f64(x), to_f64(W)[keep], np.where(tn < 0, -100, new[tn.clip(0)]), to_f64(dloss), to_f64(dlse), dtype, 1.0)
+    for name, got, r, b in zip(("loss", "lse", "dx", "dW"), (loss, lse, dx[:, 1:], dW[~off]), ref, band):
+        r, b = (r[:, 1:], b[:, 1:]) if name == "dx" else (r, b)
+        worst = np.nan_to_num(np.abs(to_f64(got) - r) / b, nan=np.inf).max()
+        say(f"  {name}: of the band {worst:.3g}")
+        assert worst <= 1.0, name
+    assert not dW[off].any() and dx.isfinite().all()
