@@ -25,9 +25,10 @@
 // the last products run.  (With the wait at the head of a stage the cores
 // stood still for it and the reads behind it: the logits of 32768 x 512 x 32768
 // took 1.17 ms, now 1.05.)
-// What bounds it: power.  At 256 x 256 the loop runs at 1.0 .. 1.15 PFLOP/s of
-// random data (the matrix cores busy 53 .. 58% of the cycles, at 1.85 GHz of
-// 2.4) and at 1.76 of zeros.
+// What bounds it: the energy of a product.  At 256 x 256 the loop runs at 1.0 ..
+// 1.15 PFLOP/s of random data (the matrix cores busy 53 .. 60% of the cycles, at
+// 1.85 GHz of 2.4) and at 1.76 of zeros; a library product of 8192^3, with longer
+// sums and wider waves, has 1.45 under the same power.
 //
 // Fragment layout of v_mfma_f32_32x32x16_bf16 and _f16: lane l feeds row l % 32 of A
 // and column l % 32 of B with the k values 8 (l / 32) .. + 7; accumulator r
@@ -112,7 +113,7 @@ struct MmOperand {
 // high, high low and low high (the low terms' own product is left out).  Every
 // term is loaded and read once for its two products, where a pass per pair of
 // terms loads and reads half as much again (4096 x 256 x 32000, each way: 955
-// us; this takes 855).
+// us; this takes 860).
 template <int WR_, int WC_, int WM_, int WN_, int BK_, int NST_, bool PAIR_ = false>
 struct MmTile {
   static constexpr int WR = WR_, WC = WC_, WM = WM_, WN = WN_, BK = BK_, NST = NST_;

@@ -26,7 +26,7 @@
 // products each (lo lo, below 2^-22, is left out).  That is four fp32
 // roundings a product, below what the fp32 sums over them make; the exact
 // three-term bf16 split (bf16split.h) took twice the products and 1.74 ms
-// where this takes 0.855 (4096 x 256 x 32000).
+// where this takes 0.86 (4096 x 256 x 32000).
 // For fp16's range W is scaled by the power of two that takes its largest value
 // to 2^14 .. 2^15, every token's x by that of its own (so that a large token
 // leaves the others' logits alone), and every token's row of dz, in units of its
@@ -705,8 +705,9 @@ __global__ void __launch_bounds__(256) k_loss_join(const float2* __restrict__ pa
 // the next four: a swap of the halves makes them eight, 16 bytes, a swap of the
 // halves' halves puts 64 bytes of 16 tokens into four lanes of one register, and
 // a permutation of the lanes puts these side by side (32768 x 512 x 8192: stores
-// of 16 bytes a row in a quarter of a wave 354 us, this 336; without any store
-// 295 at the time, the products alone 245).
+// of 16 bytes a row in a quarter of a wave 354 us, this 336, and 345 since x has a
+// copy of its own for dW, which leaves this one out of the caches; without any
+// store 295, the products alone 245).
 // bf16 data goes past the caches, so that W and x stay in them: 336 us and 283
 // for the dx that reads it, against 340 and 299, though half lines count for
 // more there (694 MB written for 537).  fp32 data, whose two terms fill a line,
@@ -1063,7 +1064,7 @@ Plan plan_operands(const LossArgs& a, bool back) {
 
 // The logits' tile: Mid takes about 1.15 times Big's time per product (16384 x
 // 512 x 16384: 285 and 245 us), which pays where 256 tokens a tile would waste
-// more (100 x 512 x 32768: 18 and 21 us, fp32 58 and 70).
+// more (100 x 512 x 32768: 16 and 21 us, fp32 60 and 73).
 bool take_big(int64_t cols) { return cdiv(cols, kBig) * kBig * 100 <= cdiv(cols, kMid) * kMid * 115; }
 
 struct PlanFw {
