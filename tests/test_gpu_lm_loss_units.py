@@ -247,3 +247,30 @@ def test_masked_entries(N, V, d, mask, dtype):
         say(f"  {name}: of the band {worst:.3g}")
         assert worst <= 1.0, name
     assert not dW[off].any() and dx.isfinite().all()
+
+
+@pytest.mark.parametrize("seed", range(48))
+def test_seeded_sweep(seed):
+    """Sizes, types, scales and data of every kind above, drawn."""
+    r = np.random.default_rng(seed)
+    dtype = ("bf16", "f32")[int(r.integers(2))]
+    N, V, d = (int(2 ** r.uniform(0, top)) for top in (10, 12, 9.3))
+    x, W, t, dloss, dlse = _inputs(N, V, d, dtype, seed)
+    scale, kind = 1.0, ("plain", "offset", "weights", "rows", "entries", "scale", "large")[seed % 7]
+    spread = lambda n: 10.0 ** (-8 * torch.from_numpy(r.random((n, 1))).float().cuda())   # noqa: E731
+    if kind == "offset":
+        W[:, 0] = 1.0
+        x[::2, 0] = float(r.choice([-1, 1]) * 10 ** r.uniform(1, 4))
+    elif kind == "weights":
+        w = spread(N)[:, 0]
+        dloss, dlse = dloss * w, dlse * w
+    elif kind == "rows":
+        x = (x.float() * spread(N)).to(x.dtype)
+    elif kind == "entries":
+        W = (W.float() * spread(V)).to(W.dtype)
+    elif kind == "scale":
+        scale = float(10 ** r.uniform(-3, 1))
+    elif kind == "large":
+        x = x * float(r.choice([10, 100]))
+    say(f"[case] {seed} {kind} N={N} V={V} d={d} {dtype} scale={scale:.3g}")
+    _check(x, W, t, dloss, dlse if r.integers(2) else None, dtype, scale=scale)
