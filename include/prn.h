@@ -53,7 +53,7 @@ typedef enum {
   PRN_ERR_DEVICE = 4        /* a HIP call or kernel launch failed            */
 } prn_status;
 
-/* Cells.  Gate order inside a token's projected row:
+/* Cells of the Newton solver.  Gate order inside a token's projected row:
  *   PRN_CELL_DIAG_GRU   G = 3 gates [z | r | c], state S = 1 (h)
  *       z = sig(x_z + a_z h), r = sig(x_r + a_r h), c = tanh(x_c + a_c r h),
  *       h' = (1 - z) h + z c
@@ -63,11 +63,20 @@ typedef enum {
  * (diagonal "mix='diag'" cells of the shapes/layout page's support table) */
 enum { PRN_CELL_DIAG_GRU = 0, PRN_CELL_DIAG_LSTM = 1 };
 
+/* Gated linear cells, which need no Newton iteration (prn_gated_scan): no
+ * recurrent weights, state S = 1 (h), not on the pages.
+ *   PRN_CELL_GATED        G = 2 gates [f | v]       h' = sig(x_f) h + (1 - sig(x_f)) x_v
+ *   PRN_CELL_GATED_INPUT  G = 3 gates [f | i | v]   h' = sig(x_f) h + sig(x_i) x_v
+ * prn_input_proj, prn_input_proj_backward and prn_decode_step take them as well
+ * (params->a is not read); the Newton, sequential and head-mix
+ * entry points return PRN_ERR_UNSUPPORTED. */
+enum { PRN_CELL_GATED = 2, PRN_CELL_GATED_INPUT = 3 };
+
 /* Storage dtypes. */
 enum { PRN_F32 = 0, PRN_BF16 = 1 };
 
 typedef struct {
-  int32_t cell;            /* PRN_CELL_DIAG_GRU | PRN_CELL_DIAG_LSTM                     */
+  int32_t cell;            /* PRN_CELL_*                                                 */
   int32_t dtype;           /* PRN_F32 | PRN_BF16                                          */
   int64_t B;               /* batch rows; must be 1 for a ragged pack                     */
   int64_t T;               /* steps per row; for a ragged pack the total token count N    */
@@ -307,7 +316,9 @@ size_t prn_backward_workspace_bytes(const prn_params* params);
  * params: cell, dtype, B = slots, T = 1, d_in, d_h, a, stream.  One kernel
  * launch, no workspace, no memory set: it can be captured in a HIP graph with
  * its buffers pinned.  The result equals prn_input_proj + prn_sequential_forward
- * on the same token up to the summation order of the projection.
+ * on the same token up to the summation order of the projection.  The gated
+ * linear cells take the projected values in fp32, without rounding them to the
+ * storage dtype in between (a gate next to 1 would lose most of 1 - f).
  * Errors (nothing is launched): PRN_ERR_INVALID_ARG for T != 1, a ragged pack
  * (n_seqs > 0), d_in < 1, NULL x / W / a / state_out, a pointer not aligned
  * to its element size, or state_in == state_out. */
@@ -487,6 +498,97 @@ prn_status prn_vocab_loss_backward(const void* x, const void* W, const void* tar
                                    void* dx_out, void* dW_out);
 size_t prn_vocab_loss_workspace_bytes(const prn_vocab_loss_params* params);
 size_t prn_vocab_loss_backward_workspace_bytes(const prn_vocab_loss_params* params);
+
+/* ---- Gated linear recurrence over time ---------------------------------
+ * h_t = f_t h_{t-1} + in_t v_t for the cells PRN_CELL_GATED and
+ * PRN_CELL_GATED_INPUT above, the state and its maps in fp32, every output
+ * rounded once.  Two calls with the same arguments give the same bits.  No
+ * workgroup waits for another (there is no error_out), no memory has to be
+ * cleared: a call can be captured in a HIP graph with its buffers pinned.
+ *   xproj      (B, T, G, d_h) storage dtype, biases included
+ *   h0         (rows, d_h) storage dtype or NULL for zeros; rows = B, or n_seqs
+ *              for a ragged pack
+ *   cu_seqlens NULL, or a ragged pack's (n_seqs + 1) int32 offsets, as for
+ *              prn_newton_forward.  Whatever a sequence holds, infinities and
+ *              NaN included, reaches no other one
+ *   H_out      (B, T, d_h) storage dtype
+ * params: cell, dtype, B, T (below 2^31), d_h, n_seqs, state_last_out
+ * ((rows, d_h) or NULL; an empty sequence's is its h0), workspace (at least
+ * prn_gated_scan_workspace_bytes(params)), stream; a, states_out, picard_iters
+ * and error_out are not used.  Tensors must be 16-byte aligned. */
+prn_status prn_gated_scan(const void* xproj, const prn_params* params, const void* h0, const int32_t* cu_seqlens,
+                          void* H_out);
+size_t prn_gated_scan_workspace_bytes(const prn_params* params);
+
+/* Its gradients: lam_t = dH_t + f_{t+1} lam_{t+1} (0 past a sequence's end, where
+ * dstate_last arrives too),
+ *   PRN_CELL_GATED        dx_f = lam (h_{t-1} - v) f (1 - f)    dv = lam (1 - f)
+ *   PRN_CELL_GATED_INPUT  dx_f = lam h_{t-1} f (1 - f)    dx_i = lam v i (1 - i)    dv = lam i
+ * and dh0 = f lam at a sequence's first step (an empty one's: its dstate_last).
+ *   xproj, h0, cu_seqlens  as given to the forward; H its H_out
+ *   dH           (B, T, d_h) storage dtype
+ *   dstate_last  (rows, d_h) storage dtype, or NULL for zero
+ *   dxproj_out   (B, T, G, d_h) storage dtype
+ *   dh0_out      (rows, d_h) storage dtype, or NULL
+ * The states are formed again in fp32, from H at every 64th step.  params as for
+ * the forward, its workspace prn_gated_scan_backward_workspace_bytes(params). */
+prn_status prn_gated_scan_backward(const void* xproj, const prn_params* params, const void* h0, const int32_t* cu_seqlens,
+                                   const void* H, const void* dH, const void* dstate_last, void* dxproj_out,
+                                   void* dh0_out);
+size_t prn_gated_scan_backward_workspace_bytes(const prn_params* params);
+
+/* ---- The feed-forward half of a block, and dropout ---------------------
+ * As the operators between token ids and the loss above: rows are dense,
+ * arithmetic fp32, each stored value rounded once, sums in a fixed order,
+ * N = 0 is allowed. */
+
+typedef struct {
+  int32_t dtype;           /* PRN_F32 | PRN_BF16: every tensor                          */
+  int32_t act;             /* PRN_ACT_SILU | PRN_ACT_SIGMOID                            */
+  int64_t N;               /* rows, below 2^31                                          */
+  int64_t d;               /* input channels                                            */
+  int64_t F;               /* output channels; 2 F d below 2^32                         */
+  void* workspace;         /* 256-byte aligned scratch                                  */
+  size_t workspace_bytes;  /* >= prn_gated_ffn_workspace_bytes(params), backward:
+                              >= prn_gated_ffn_backward_workspace_bytes(params)         */
+  void* stream;            /* hipStream_t                                               */
+} prn_gated_ffn_params;
+
+/* out = act(x Wg^T) * (x Wu^T), both products, the activation and their product
+ * in one kernel: x (N, d), W (2 F, d) = [Wg; Wu] (rows gate-major, as the
+ * projection's), out (N, F), storage dtype.  The sums are prn_input_proj's, kept
+ * in fp32.  Tensors must be 16-byte aligned. */
+prn_status prn_gated_ffn(const void* x, const void* W, const prn_gated_ffn_params* params, void* out);
+
+/* Its gradients from dout (N, F): dz = [dout u act'(g) | dout act(g)], with g and u
+ * formed again, rounded once to the storage dtype; dx_out (N, d) = dz W, dW_out
+ * (2 F, d) = dz^T x, each optional.  The workspace holds dz.  Tensors must be
+ * 16-byte aligned. */
+prn_status prn_gated_ffn_backward(const void* x, const void* W, const void* dout, const prn_gated_ffn_params* params,
+                                  void* dx_out, void* dW_out);
+size_t prn_gated_ffn_workspace_bytes(const prn_gated_ffn_params* params);
+size_t prn_gated_ffn_backward_workspace_bytes(const prn_gated_ffn_params* params);
+
+typedef struct {
+  int32_t dtype;           /* PRN_F32 | PRN_BF16: x, residual, out                      */
+  int64_t n;               /* elements                                                  */
+  double p;                /* 0 .. 1: the share that is dropped, held to 2^-16          */
+  uint64_t seed, offset;
+  const int64_t* state;    /* device (seed, offset) to take instead, read when the
+                              kernel runs (a captured graph draws anew when they have
+                              changed), or NULL                                         */
+  void* stream;            /* hipStream_t                                               */
+} prn_dropout_params;
+
+/* out = residual + (kept ? x / (1 - q) : 0), q = round(65536 p) / 65536, a dropped
+ * x counting for nothing whatever it is.  Which elements stay is a function of
+ * (seed, offset, index): element 8 b + 2 j (8 b + 2 j + 1) is dropped if the low
+ * (high) 16 bits of word j of Philox4x32-10 with key seed and counter (b, offset)
+ * are below 65536 q.  Nothing is stored for the backward pass, which is the same
+ * function of the gradient, without residual.
+ *   x, out (n); residual (n) or NULL.  out may be x or residual itself.  16-byte
+ * aligned. */
+prn_status prn_dropout(const void* x, const void* residual, const prn_dropout_params* params, void* out);
 
 /* Host-side check of ragged offsets (the validate_cu_seqlens contract of
  * the shapes/layout page): cu_host has n_seqs + 1 entries, cu[0] = 0,

@@ -23,6 +23,7 @@ import warnings
 import torch
 
 from . import binding as B_
+from .autograd import first as _first
 
 RESIDUAL_FAIL = 1.0
 # warn band: 1e-3 for fp32 storage; bf16 storage rounds every stored state
@@ -359,3 +360,99 @@ def input_proj_apply(x, W, bias=None, *, cell: str):
     matrix cores, with fixed summation orders."""
     return _ProjFunction.apply(x.contiguous(), W.contiguous(),
                                None if bias is None else bias.to(torch.float32).contiguous(), cell)
+
+
+# ------------------------------------------------------------------ gated linear recurrence ---
+# The recurrence that is linear in its state needs no Newton iteration: one scan, exact, without a residual to
+# gate and without a wait that can time out, so no host synchronisation either.
+
+def _aligned(t):
+    """t as a dense tensor that starts on 16 bytes (None for None)."""
+    if t is None:
+        return None
+    t = t.contiguous()
+    return t.clone() if t.data_ptr() % 16 else t
+
+
+def _pack_offsets(cu_seqlens, T: int, device):
+    """int32 offsets on the device are taken as they are (validate_cu_seqlens gives such); others are checked."""
+    if cu_seqlens is None:
+        return None
+    if isinstance(cu_seqlens, torch.Tensor) and cu_seqlens.device == device and cu_seqlens.dtype == torch.int32:
+        return cu_seqlens.contiguous()
+    return validate_cu_seqlens(cu_seqlens, T, device)
+
+
+def _check_gated(xproj, cell: str) -> None:
+    if cell not in B_.GATED_CELLS:
+        raise ValueError(f"a gated scan takes the cells {B_.GATED_CELLS}, not {cell!r}")
+    if xproj.dim() != 4 or xproj.shape[2] != B_.GATES[cell]:
+        raise ValueError(f"xproj of the cell {cell!r} must be (B, T, {B_.GATES[cell]}, d), got {tuple(xproj.shape)}")
+
+
+def _scan_workspace(n: int, device):
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def gated_scan(xproj, *, cell: str, h0=None, cu_seqlens=None, return_state=False):
+    """The gated linear recurrence over projected inputs (B, T, G, d), from input_proj with the same cell:
+
+        "glr"   G = 2, rows f, v:       h' = s(f) h + (1 - s(f)) v
+        "glri"  G = 3, rows f, i, v:    h' = s(f) h + s(i) v
+
+    s the logistic function.  H (B, T, d), with return_state also the final states (rows, 1, d); h0 (rows, 1, d)
+    or None for zeros.  A ragged pack has B = 1 and cu_seqlens: int32 offsets on the device are used without a look
+    at them, anything else is validated first.  The state is fp32 within a call."""
+    _check_gated(xproj, cell)
+    xproj, h0 = _aligned(xproj), _aligned(h0)
+    Bn, T, _, d = xproj.shape
+    cu = _pack_offsets(cu_seqlens, T, xproj.device)
+    n_seqs = 0 if cu is None else cu.numel() - 1
+    H = xproj.new_empty((Bn, T, d))
+    last = xproj.new_empty((n_seqs or Bn, 1, d)) if return_state else None
+    ws = _scan_workspace(B_.prn_gated_scan_workspace_bytes(cell, xproj.dtype, Bn, T, d, n_seqs), xproj.device)
+    B_.prn_gated_scan(xproj, H, cell=cell, h0=h0, cu_seqlens=cu, state_last_out=last, workspace=ws)
+    return (H, last) if return_state else H
+
+
+def gated_scan_backward(dH, xproj, H, *, cell: str, h0=None, cu_seqlens=None, dstate=None, want_h0: bool = True):
+    """Gradients (dxproj, dh0) of gated_scan from dH (B, T, d) and dstate (rows, 1, d), that of the final states, or
+    None for zero; H is the forward's.  dh0 is None without h0, or where it is not wanted."""
+    _check_gated(xproj, cell)
+    xproj, h0, H, dH, dstate = (_aligned(t) for t in (xproj, h0, H, dH, dstate))
+    Bn, T, _, d = xproj.shape
+    cu = _pack_offsets(cu_seqlens, T, xproj.device)
+    n_seqs = 0 if cu is None else cu.numel() - 1
+    dxproj = torch.empty_like(xproj)
+    dh0 = torch.empty_like(h0) if h0 is not None and want_h0 else None
+    ws = _scan_workspace(B_.prn_gated_scan_backward_workspace_bytes(cell, xproj.dtype, Bn, T, d, n_seqs), xproj.device)
+    B_.prn_gated_scan_backward(xproj, H, dH, dxproj, cell=cell, h0=h0, cu_seqlens=cu, dstate_last=dstate, dh0_out=dh0,
+                               workspace=ws)
+    return dxproj, dh0
+
+
+class _GatedScanFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, xproj, h0, cell, cu, with_state):
+        out = gated_scan(xproj, cell=cell, h0=h0, cu_seqlens=cu, return_state=with_state)
+        H = out[0] if with_state else out
+        ctx.save_for_backward(xproj, h0, H, cu)
+        ctx.cell = cell
+        ctx.set_materialize_grads(False)
+        return out
+
+    @staticmethod
+    def backward(ctx, dH, dstate=None):
+        xproj, h0, H, cu = ctx.saved_tensors
+        dH = torch.zeros_like(H) if dH is None else dH.to(xproj.dtype)
+        dstate = None if dstate is None else dstate.to(xproj.dtype)
+        dxproj, dh0 = gated_scan_backward(dH, xproj, H, cell=ctx.cell, h0=h0, cu_seqlens=cu, dstate=dstate,
+                                          want_h0=ctx.needs_input_grad[1])
+        return *_first((dxproj, dh0), dH, dstate, xproj, h0), None, None, None
+
+
+def gated_scan_apply(xproj, *, cell: str, h0=None, cu_seqlens=None, return_state=False):
+    """Differentiable gated_scan: gradients of H and of the final states reach xproj and h0."""
+    _check_gated(xproj, cell)
+    cu = _pack_offsets(cu_seqlens, xproj.shape[1], xproj.device)
+    return _GatedScanFunction.apply(xproj, h0, cell, cu, bool(return_state))

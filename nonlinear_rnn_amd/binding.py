@@ -20,9 +20,11 @@ LIB_PATH = os.environ.get("PRN_LIB", os.path.join(HERE, "libprn.so"))
 PRN_OK, PRN_ERR_INVALID_ARG, PRN_ERR_UNSUPPORTED, PRN_ERR_WORKSPACE, PRN_ERR_DEVICE = range(5)
 STATUS_NAMES = {0: "PRN_OK", 1: "PRN_ERR_INVALID_ARG", 2: "PRN_ERR_UNSUPPORTED",
                 3: "PRN_ERR_WORKSPACE", 4: "PRN_ERR_DEVICE"}
-CELLS = {"gru": 0, "lstm": 1}
-GATES = {"gru": 3, "lstm": 4}
-STATE = {"gru": 1, "lstm": 2}
+# glr, glri: the gated linear cells, of prn_gated_scan, prn_input_proj and prn_decode_step
+CELLS = {"gru": 0, "lstm": 1, "glr": 2, "glri": 3}
+GATES = {"gru": 3, "lstm": 4, "glr": 2, "glri": 3}
+STATE = {"gru": 1, "lstm": 2, "glr": 1, "glri": 1}
+GATED_CELLS = ("glr", "glri")
 DTYPES = {torch.float32: 0, torch.bfloat16: 1}
 
 # every symbol include/prn.h declares
@@ -35,7 +37,11 @@ EXPORTS = ("prn_input_proj", "prn_newton_forward", "prn_newton_forward_fused", "
            "prn_embed", "prn_embed_backward", "prn_embed_backward_workspace_bytes",
            "prn_block_norm", "prn_block_norm_backward", "prn_block_norm_backward_workspace_bytes",
            "prn_vocab_loss", "prn_vocab_loss_backward", "prn_vocab_loss_workspace_bytes",
-           "prn_vocab_loss_backward_workspace_bytes")
+           "prn_vocab_loss_backward_workspace_bytes",
+           "prn_gated_scan", "prn_gated_scan_workspace_bytes", "prn_gated_scan_backward",
+           "prn_gated_scan_backward_workspace_bytes",
+           "prn_gated_ffn", "prn_gated_ffn_workspace_bytes", "prn_gated_ffn_backward",
+           "prn_gated_ffn_backward_workspace_bytes", "prn_dropout")
 ACTS = {"silu": 0, "sigmoid": 1}
 NO_PAD = -(1 << 63)   # PRN_NO_PAD
 ID_DTYPES = {torch.int32: 4, torch.int64: 8}
@@ -123,6 +129,31 @@ class prn_vocab_loss_params(ctypes.Structure):
     ]
 
 
+class prn_gated_ffn_params(ctypes.Structure):
+    _fields_ = [
+        ("dtype", ctypes.c_int32),
+        ("act", ctypes.c_int32),
+        ("N", ctypes.c_int64),
+        ("d", ctypes.c_int64),
+        ("F", ctypes.c_int64),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
+        ("stream", ctypes.c_void_p),
+    ]
+
+
+class prn_dropout_params(ctypes.Structure):
+    _fields_ = [
+        ("dtype", ctypes.c_int32),
+        ("n", ctypes.c_int64),
+        ("p", ctypes.c_double),
+        ("seed", ctypes.c_uint64),
+        ("offset", ctypes.c_uint64),
+        ("state", ctypes.c_void_p),
+        ("stream", ctypes.c_void_p),
+    ]
+
+
 _LIB = None
 
 
@@ -164,12 +195,21 @@ def lib() -> ctypes.CDLL:
         L.prn_block_norm_backward.argtypes = [vp, vp, vp, vp, vp, PB, vp, vp, vp, vp, vp, vp]
         L.prn_vocab_loss.argtypes = [vp, vp, vp, PV, vp, vp]
         L.prn_vocab_loss_backward.argtypes = [vp, vp, vp, vp, vp, vp, PV, vp, vp]
+        PF, PD = ctypes.POINTER(prn_gated_ffn_params), ctypes.POINTER(prn_dropout_params)
+        L.prn_gated_scan.argtypes = [vp, P, vp, vp, vp]
+        L.prn_gated_scan_backward.argtypes = [vp, P, vp, vp, vp, vp, vp, vp, vp]
+        L.prn_gated_ffn.argtypes = [vp, vp, PF, vp]
+        L.prn_gated_ffn_backward.argtypes = [vp, vp, vp, PF, vp, vp]
+        L.prn_dropout.argtypes = [vp, vp, PD, vp]
         for name, ptr in (("prn_embed_backward_workspace_bytes", PE), ("prn_block_norm_backward_workspace_bytes", PB),
-                          ("prn_vocab_loss_workspace_bytes", PV), ("prn_vocab_loss_backward_workspace_bytes", PV)):
+                          ("prn_vocab_loss_workspace_bytes", PV), ("prn_vocab_loss_backward_workspace_bytes", PV),
+                          ("prn_gated_scan_workspace_bytes", P), ("prn_gated_scan_backward_workspace_bytes", P),
+                          ("prn_gated_ffn_workspace_bytes", PF), ("prn_gated_ffn_backward_workspace_bytes", PF)):
             getattr(L, name).argtypes = [ptr]
             getattr(L, name).restype = ctypes.c_size_t
         for name in ("prn_embed", "prn_embed_backward", "prn_block_norm", "prn_block_norm_backward",
-                     "prn_vocab_loss", "prn_vocab_loss_backward"):
+                     "prn_vocab_loss", "prn_vocab_loss_backward", "prn_gated_scan", "prn_gated_scan_backward",
+                     "prn_gated_ffn", "prn_gated_ffn_backward", "prn_dropout"):
             getattr(L, name).restype = ctypes.c_int
         for name in ("prn_input_proj", "prn_input_proj_backward", "prn_newton_forward", "prn_newton_forward_fused",
                      "prn_newton_forward_noalloc",
@@ -466,7 +506,8 @@ def prn_newton_backward(xproj, a, states, dH, dxproj_out, da_out, *, cell: str, 
 
 def prn_decode_step(x, W, bias, a, state_out, *, cell: str, state_in=None, h_out=None, stream=None) -> None:
     """One T = 1 step for B slots: x (B, d_in), W (G*d_h, d_in), bias (G*d_h) fp32 or None,
-    state_in / state_out (B, S, d_h) (distinct buffers), h_out (B, d_h) or None."""
+    state_in / state_out (B, S, d_h) (distinct buffers), h_out (B, d_h) or None.
+    The gated linear cells have no a (None)."""
     _dev(x, "x")
     _dev(W, "W", x.dtype)
     _dev(bias, "bias", torch.float32)
@@ -477,8 +518,12 @@ def prn_decode_step(x, W, bias, a, state_out, *, cell: str, state_in=None, h_out
     Bn, d_in = x.shape
     G, S = GATES[cell], STATE[cell]
     d_h = W.shape[0] // G
-    if W.shape != (G * d_h, d_in) or a.shape != (G, d_h) or state_out.shape != (Bn, S, d_h):
+    if W.shape != (G * d_h, d_in) or (a is not None and a.shape != (G, d_h)) or state_out.shape != (Bn, S, d_h):
         raise ValueError(f"shape mismatch: x {tuple(x.shape)} W {tuple(W.shape)} state_out {tuple(state_out.shape)}")
+    if a is None and cell not in GATED_CELLS:
+        raise ValueError(f"the cell {cell!r} has recurrent weights a")
+    if bias is not None and bias.shape != (G * d_h,):
+        raise ValueError("bias must have G*d_h entries")
     if state_in is not None and state_in.shape != (Bn, S, d_h):
         raise ValueError("state_in must match state_out")
     if h_out is not None and h_out.shape != (Bn, d_h):
@@ -720,3 +765,134 @@ def prn_vocab_loss_backward(x, W, targets, lse, dloss, *, dlse=None, scale: floa
         _arg(x, "x", dt, (N, d), dev), _arg(W, "W", dt, (V, d), dev), ids, _arg(lse, "lse", f32, (N,), dev),
         _arg(dloss, "dloss", f32, (N,), dev), _arg(dlse, "dlse", f32, (N,), dev), p,
         _arg(dx_out, "dx_out", dt, (N, d), dev), _arg(dW_out, "dW_out", dt, (V, d), dev)))
+
+
+class _On:
+    """Makes a device the current one for a launch, where it is not: a stream belongs to its device."""
+
+    def __init__(self, dev):
+        self.guard = None if torch.cuda.current_device() == dev else torch.cuda.device(dev)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *reason):
+        if self.guard is not None:
+            self.guard.__exit__(*reason)
+
+
+def _scan_params(xproj, cell: str, cu_seqlens, state_last_out, workspace, stream):
+    """(device, parameters, the shape of per-sequence states)"""
+    dev, code = _lead(xproj, "xproj", 4)
+    if cell not in GATED_CELLS:
+        raise ValueError(f"a gated scan takes the cells {GATED_CELLS}, not {cell!r}")
+    Bn, T, G, d = xproj.shape
+    if G != GATES[cell]:
+        raise ValueError(f"xproj of the cell {cell!r} must be (B, T, {GATES[cell]}, d), got {tuple(xproj.shape)}")
+    n_seqs = 0
+    if cu_seqlens is not None:
+        if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
+            raise ValueError("cu_seqlens must be 1-D with at least 2 entries")
+        n_seqs = cu_seqlens.shape[0] - 1
+    rows = (n_seqs or Bn, 1, d)
+    p = prn_params()
+    p.cell, p.dtype, p.B, p.T, p.d_h, p.n_seqs = CELLS[cell], code, Bn, T, d, n_seqs
+    p.state_last_out = _arg(state_last_out, "state_last_out", xproj.dtype, rows, dev)
+    p.workspace, p.workspace_bytes = _scratch(workspace, dev)
+    p.stream = _handle(stream, dev)
+    return dev, p, rows
+
+
+def prn_gated_scan_workspace_bytes(cell: str, dtype: torch.dtype, B: int, T: int, d_h: int, n_seqs: int = 0) -> int:
+    p = prn_params(CELLS[cell], _storage(dtype), B, T, 0, d_h, n_seqs)
+    return _bytes(lib().prn_gated_scan_workspace_bytes, p)
+
+
+def prn_gated_scan(xproj, H_out, *, cell: str, h0=None, cu_seqlens=None, state_last_out=None, workspace=None,
+                   stream=None) -> None:
+    """H_out (B, T, d) of the gated linear recurrence over xproj (B, T, G, d); h0 and state_last_out (rows, 1, d)."""
+    dev, p, rows = _scan_params(xproj, cell, cu_seqlens, state_last_out, workspace, stream)
+    Bn, T, _, d = xproj.shape
+    dt = xproj.dtype
+    with _On(dev):
+        _check(lib().prn_gated_scan(
+            _arg(xproj, "xproj", dt, xproj.shape, dev), p, _arg(h0, "h0", dt, rows, dev),
+            _arg(cu_seqlens, "cu_seqlens", torch.int32, None if cu_seqlens is None else cu_seqlens.shape, dev),
+            _arg(H_out, "H_out", dt, (Bn, T, d), dev)))
+
+
+def prn_gated_scan_backward_workspace_bytes(cell: str, dtype: torch.dtype, B: int, T: int, d_h: int,
+                                            n_seqs: int = 0) -> int:
+    p = prn_params(CELLS[cell], _storage(dtype), B, T, 0, d_h, n_seqs)
+    return _bytes(lib().prn_gated_scan_backward_workspace_bytes, p)
+
+
+def prn_gated_scan_backward(xproj, H, dH, dxproj_out, *, cell: str, h0=None, cu_seqlens=None, dstate_last=None,
+                            dh0_out=None, workspace=None, stream=None) -> None:
+    """dxproj_out (B, T, G, d) and, optional, dh0_out (rows, 1, d) from dH (B, T, d) and dstate_last (rows, 1, d)
+    or None; H (B, T, d) the forward's."""
+    dev, p, rows = _scan_params(xproj, cell, cu_seqlens, None, workspace, stream)
+    Bn, T, _, d = xproj.shape
+    dt, states = xproj.dtype, (Bn, T, d)
+    with _On(dev):
+        _check(lib().prn_gated_scan_backward(
+            _arg(xproj, "xproj", dt, xproj.shape, dev), p, _arg(h0, "h0", dt, rows, dev),
+            _arg(cu_seqlens, "cu_seqlens", torch.int32, None if cu_seqlens is None else cu_seqlens.shape, dev),
+            _arg(H, "H", dt, states, dev), _arg(dH, "dH", dt, states, dev),
+            _arg(dstate_last, "dstate_last", dt, rows, dev), _arg(dxproj_out, "dxproj_out", dt, xproj.shape, dev),
+            _arg(dh0_out, "dh0_out", dt, rows, dev)))
+
+
+def _ffn_params(x, W, act: str, workspace, stream):
+    dev, code = _lead(x, "x", 2)
+    _lead(W, "W", 2)
+    if act not in ACTS:
+        raise ValueError(f"unknown gate activation {act!r}")
+    N, d = x.shape
+    if W.shape[0] % 2:
+        raise ValueError(f"W must have gate and up rows, got {tuple(W.shape)}")
+    F = W.shape[0] // 2
+    ws, ws_bytes = _scratch(workspace, dev)
+    return dev, prn_gated_ffn_params(code, ACTS[act], N, d, F, ws, ws_bytes, _handle(stream, dev)), N, d, F
+
+
+def prn_gated_ffn_workspace_bytes(dtype: torch.dtype, N: int, d: int, F: int) -> int:
+    return _bytes(lib().prn_gated_ffn_workspace_bytes, prn_gated_ffn_params(_storage(dtype), 0, N, d, F))
+
+
+def prn_gated_ffn(x, W, out, *, act: str = "silu", workspace=None, stream=None) -> None:
+    """out (N, F) = act(x Wg^T) * (x Wu^T): x (N, d), W (2 F, d) = [Wg; Wu]."""
+    dev, p, N, d, F = _ffn_params(x, W, act, workspace, stream)
+    dt = x.dtype
+    with _On(dev):
+        _check(lib().prn_gated_ffn(_arg(x, "x", dt, (N, d), dev), _arg(W, "W", dt, (2 * F, d), dev), p,
+                                   _arg(out, "out", dt, (N, F), dev)))
+
+
+def prn_gated_ffn_backward_workspace_bytes(dtype: torch.dtype, N: int, d: int, F: int) -> int:
+    return _bytes(lib().prn_gated_ffn_backward_workspace_bytes, prn_gated_ffn_params(_storage(dtype), 0, N, d, F))
+
+
+def prn_gated_ffn_backward(x, W, dout, *, act: str = "silu", dx_out=None, dW_out=None, workspace=None,
+                           stream=None) -> None:
+    """dx_out (N, d) and dW_out (2 F, d), each optional, from dout (N, F)."""
+    dev, p, N, d, F = _ffn_params(x, W, act, workspace, stream)
+    dt = x.dtype
+    with _On(dev):
+        _check(lib().prn_gated_ffn_backward(
+            _arg(x, "x", dt, (N, d), dev), _arg(W, "W", dt, (2 * F, d), dev), _arg(dout, "dout", dt, (N, F), dev), p,
+            _arg(dx_out, "dx_out", dt, (N, d), dev), _arg(dW_out, "dW_out", dt, (2 * F, d), dev)))
+
+
+def prn_dropout(x, out, *, p: float, seed: int = 0, offset: int = 0, state=None, residual=None, stream=None) -> None:
+    """out = residual + dropout(x), tensors of one shape; state an int64 tensor (seed, offset) instead of the two."""
+    if not (isinstance(x, torch.Tensor) and x.is_cuda):
+        raise TypeError("x must be a CUDA (HIP) tensor")
+    dev, dt, shape = x.get_device(), x.dtype, x.shape
+    m = (1 << 64) - 1
+    q = prn_dropout_params(_storage(dt), x.numel(), p, seed & m, offset & m, _arg(state, "state", torch.int64, (2,), dev),
+                           _handle(stream, dev))
+    with _On(dev):
+        _check(lib().prn_dropout(_arg(x, "x", dt, shape, dev), _arg(residual, "residual", dt, shape, dev), q,
+                                 _arg(out, "out", dt, shape, dev)))

@@ -1,0 +1,26 @@
+// Gated feed-forward product: plan and launches (gated_ffn.hip).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace prn {
+
+struct GatedFfnArgs {
+  bool bf16, silu;
+  int64_t N, d, F;
+  uint8_t* ws;
+  hipStream_t stream;
+};
+
+// do the launches fit their grids?
+bool gated_ffn_fits(const GatedFfnArgs& a);
+size_t gated_ffn_workspace(const GatedFfnArgs& a);
+void launch_gated_ffn(const GatedFfnArgs& a, const void* x, const void* W, void* out);
+// the workspace of the gradients of the sums, N x 2 F; dz_at: where in it they lie
+size_t gated_ffn_dz_workspace(const GatedFfnArgs& a, size_t* dz_at);
+// the gradients of the sums, [gate | up], from dout
+void launch_gated_ffn_dz(const GatedFfnArgs& a, const void* x, const void* W, const void* dout);
+
+}  // namespace prn

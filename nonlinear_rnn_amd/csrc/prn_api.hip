@@ -147,9 +147,14 @@ struct Shape {
   bool ragged;
 };
 
-prn_status check_common(const prn_params* p, Shape* sh) {
+bool gated_cell(int cell) { return cell == PRN_CELL_GATED || cell == PRN_CELL_GATED_INPUT; }
+
+// gated: is this one of the entry points that take the gated linear cells too?
+prn_status check_common(const prn_params* p, Shape* sh, bool gated = false) {
   if (!p) return fail(PRN_ERR_INVALID_ARG, "params is NULL");
-  if (p->cell != PRN_CELL_DIAG_GRU && p->cell != PRN_CELL_DIAG_LSTM)
+  if (gated_cell(p->cell) && !gated)
+    return fail(PRN_ERR_UNSUPPORTED, "the gated linear cells need no Newton iteration: prn_gated_scan takes them");
+  if (p->cell != PRN_CELL_DIAG_GRU && p->cell != PRN_CELL_DIAG_LSTM && !gated_cell(p->cell))
     return fail(PRN_ERR_INVALID_ARG, "unknown cell %d", p->cell);
   if (p->dtype != PRN_F32 && p->dtype != PRN_BF16)
     return fail(PRN_ERR_INVALID_ARG, "unknown storage dtype %d", p->dtype);
@@ -161,8 +166,8 @@ prn_status check_common(const prn_params* p, Shape* sh) {
     return fail(PRN_ERR_INVALID_ARG, "a ragged pack (n_seqs > 0) needs B == 1, got B=%lld", (long long)p->B);
   if (p->B > kMaxGrid || p->n_seqs > kMaxGrid || (p->d_h + 63) / 64 > kMaxGrid)
     return fail(PRN_ERR_UNSUPPORTED, "B, n_seqs and d_h/64 must each be <= %lld", (long long)kMaxGrid);
-  sh->G = p->cell == PRN_CELL_DIAG_GRU ? 3 : 4;
-  sh->S = p->cell == PRN_CELL_DIAG_GRU ? 1 : 2;
+  sh->G = p->cell == PRN_CELL_GATED ? 2 : p->cell == PRN_CELL_DIAG_LSTM ? 4 : 3;
+  sh->S = p->cell == PRN_CELL_DIAG_LSTM ? 2 : 1;
   sh->elt = p->dtype == PRN_F32 ? 4 : 2;
   sh->ragged = p->n_seqs > 0;
   sh->rows = sh->ragged ? p->n_seqs : p->B;
@@ -770,12 +775,13 @@ prn_status prn_newton_forward_noalloc(const void* xproj, const prn_params* p, co
 prn_status prn_decode_step(const void* x, const void* W, const float* bias, const prn_params* p,
                            const void* state_in, void* state_out, void* h_out) {
   Shape sh;
-  prn_status s = check_common(p, &sh);
+  prn_status s = check_common(p, &sh, true);
   if (s != PRN_OK) return s;
   if (p->T != 1) return fail(PRN_ERR_INVALID_ARG, "a decode step has T = 1, got T=%lld", (long long)p->T);
   if (sh.ragged) return fail(PRN_ERR_INVALID_ARG, "a decode step takes slots (B), not a ragged pack");
   if (p->d_in < 1) return fail(PRN_ERR_INVALID_ARG, "d_in must be >= 1");
-  if (!x || !W || !p->a || !state_out) return fail(PRN_ERR_INVALID_ARG, "x, W, a or state_out is NULL");
+  if (!x || !W || (!p->a && !gated_cell(p->cell)) || !state_out)
+    return fail(PRN_ERR_INVALID_ARG, "x, W, a or state_out is NULL");
   if (misaligned(x, sh.elt) || misaligned(W, sh.elt) || misaligned(bias, 4) || misaligned(p->a, 4) ||
       misaligned(state_in, sh.elt) || misaligned(state_out, sh.elt) || misaligned(h_out, sh.elt))
     return fail(PRN_ERR_INVALID_ARG, "a tensor pointer is not aligned to its element size");
@@ -794,10 +800,14 @@ prn_status prn_decode_step(const void* x, const void* W, const float* bias, cons
   };
   using F32 = std::integral_constant<int, prn::kF32>;
   using BF16 = std::integral_constant<int, prn::kBF16>;
-  if (p->cell == PRN_CELL_DIAG_GRU) {
-    if (p->dtype == PRN_F32) go(prn::CellGRU{}, F32{}); else go(prn::CellGRU{}, BF16{});
-  } else {
-    if (p->dtype == PRN_F32) go(prn::CellLSTM{}, F32{}); else go(prn::CellLSTM{}, BF16{});
+  auto typed = [&](auto cell) {
+    if (p->dtype == PRN_F32) go(cell, F32{}); else go(cell, BF16{});
+  };
+  switch (p->cell) {
+    case PRN_CELL_DIAG_GRU: typed(prn::CellGRU{}); break;
+    case PRN_CELL_DIAG_LSTM: typed(prn::CellLSTM{}); break;
+    case PRN_CELL_GATED: typed(prn::CellGated<2>{}); break;
+    default: typed(prn::CellGated<3>{}); break;
   }
   return launched("prn_decode_step");
 }
@@ -953,7 +963,7 @@ prn_status prn_sequential_forward(const void* xproj, const prn_params* p, const 
 
 prn_status prn_input_proj(const void* x, const void* W, const float* bias, const prn_params* p, void* xproj_out) {
   Shape sh;
-  prn_status s = check_common(p, &sh);
+  prn_status s = check_common(p, &sh, true);
   if (s != PRN_OK) return s;
   if (p->d_in < 1) return fail(PRN_ERR_INVALID_ARG, "d_in must be >= 1");
   const int64_t M = p->B * p->T, N = sh.G * p->d_h, Kd = p->d_in;
@@ -974,7 +984,7 @@ prn_status prn_input_proj(const void* x, const void* W, const float* bias, const
 size_t prn_input_proj_backward_workspace_bytes(const prn_params* p) {
   g_err.clear();  // a 0 result with no message means no workspace is needed
   Shape sh;
-  if (check_common(p, &sh) != PRN_OK) return 0;
+  if (check_common(p, &sh, true) != PRN_OK) return 0;
   if (p->d_in < 1) {
     fail(PRN_ERR_INVALID_ARG, "d_in must be >= 1");
     return 0;
@@ -985,7 +995,7 @@ size_t prn_input_proj_backward_workspace_bytes(const prn_params* p) {
 prn_status prn_input_proj_backward(const void* dxproj, const void* x, const void* W, const prn_params* p,
                                    void* dx_out, void* dW_out, float* dbias_out) {
   Shape sh;
-  prn_status s = check_common(p, &sh);
+  prn_status s = check_common(p, &sh, true);
   if (s != PRN_OK) return s;
   if (sh.ragged) return fail(PRN_ERR_INVALID_ARG, "the projection's backward takes (B, T) rows, n_seqs must be 0");
   if (p->d_in < 1) return fail(PRN_ERR_INVALID_ARG, "d_in must be >= 1");

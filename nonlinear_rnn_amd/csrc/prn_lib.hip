@@ -3,11 +3,17 @@
 // share the thread's error message and the argument helpers.
 //
 // Here: argument checks, workspace checks and launches of prn_embed*,
-// prn_block_norm* and prn_vocab_loss*.
+// prn_block_norm*, prn_vocab_loss*, prn_gated_scan*, prn_gated_ffn* and
+// prn_dropout.
+#include <cmath>
+
 #include "prn_api.hip"
 
 #include "block_norm.h"
+#include "dropout.h"
 #include "embed.h"
+#include "gated_ffn.h"
+#include "gated_scan.h"
 #include "vocab_loss.h"
 
 namespace {
@@ -86,6 +92,51 @@ prn_status loss_args(const prn_vocab_loss_params* p, prn::LossArgs* a) {
   if (!prn::loss_fits(*a)) return fail(PRN_ERR_UNSUPPORTED, "too many tiles for one launch: N=%lld V=%lld",
                                        (long long)p->N, (long long)p->V);
   return PRN_OK;
+}
+
+prn_status scan_args(const prn_params* p, prn::GatedScanArgs* a) {
+  Shape sh;
+  if (prn_status s = check_common(p, &sh, true); s != PRN_OK) return s;
+  if (!gated_cell(p->cell)) return fail(PRN_ERR_UNSUPPORTED, "prn_gated_scan takes the gated linear cells, not cell %d", p->cell);
+  if (p->T > kMaxRows) return fail(PRN_ERR_UNSUPPORTED, "T below 2^31; got T=%lld", (long long)p->T);
+  *a = prn::GatedScanArgs{};
+  a->bf16 = p->dtype == PRN_BF16;
+  a->G = sh.G;
+  a->B = p->B, a->T = p->T, a->d = p->d_h, a->n_seqs = p->n_seqs;
+  a->last = p->state_last_out;
+  a->ws = static_cast<uint8_t*>(p->workspace);
+  a->stream = static_cast<hipStream_t>(p->stream);
+  return PRN_OK;
+}
+prn_status scan_pack(const prn_params* p, const int32_t* cu) {
+  if (p->n_seqs > 0 && !cu) return fail(PRN_ERR_INVALID_ARG, "n_seqs > 0 but cu_seqlens is NULL");
+  if (p->n_seqs == 0 && cu) return fail(PRN_ERR_INVALID_ARG, "cu_seqlens given but n_seqs == 0");
+  if (misaligned(cu, 4)) return fail(PRN_ERR_INVALID_ARG, "cu_seqlens is not 4-byte aligned");
+  return PRN_OK;
+}
+
+prn_status ffn_args(const prn_gated_ffn_params* p, prn::GatedFfnArgs* a) {
+  if (!p) return fail(PRN_ERR_INVALID_ARG, "params is NULL");
+  if (prn_status s = check_dtype(p->dtype); s != PRN_OK) return s;
+  if (p->act != PRN_ACT_SILU && p->act != PRN_ACT_SIGMOID)
+    return fail(PRN_ERR_INVALID_ARG, "unknown gate activation %d", p->act);
+  if (p->N < 0 || p->d < 1 || p->F < 1)
+    return fail(PRN_ERR_INVALID_ARG, "bad sizes N=%lld d=%lld F=%lld", (long long)p->N, (long long)p->d, (long long)p->F);
+  *a = {p->dtype == PRN_BF16, p->act == PRN_ACT_SILU, p->N, p->d, p->F, static_cast<uint8_t*>(p->workspace),
+        static_cast<hipStream_t>(p->stream)};
+  if (p->N > kMaxRows || !prn::gated_ffn_fits(*a))
+    return fail(PRN_ERR_UNSUPPORTED, "N below 2^31, 2 F d below 2^32, N F below 2^37; got N=%lld d=%lld F=%lld",
+                (long long)p->N, (long long)p->d, (long long)p->F);
+  return PRN_OK;
+}
+// the projection whose gradients dz -> dx, dW are: 2 F columns of d
+prn_params ffn_projection(const prn_gated_ffn_params* p) {
+  prn_params q{};
+  q.cell = PRN_CELL_GATED;
+  q.dtype = p->dtype;
+  q.B = 1, q.T = p->N, q.d_in = p->d, q.d_h = p->F;
+  q.stream = p->stream;
+  return q;
 }
 
 }  // namespace
@@ -217,6 +268,117 @@ prn_status prn_vocab_loss_backward(const void* x, const void* W, const void* tar
   if (!dx && !dW) return PRN_OK;
   prn::launch_loss_backward(a, x, W, targets, lse, dloss, dlse, dx, dW);
   return launched("prn_vocab_loss_backward");
+}
+
+size_t prn_gated_scan_workspace_bytes(const prn_params* p) {
+  g_err.clear();
+  prn::GatedScanArgs a;
+  if (scan_args(p, &a) != PRN_OK) return 0;
+  return prn::gated_scan_workspace(a);
+}
+
+prn_status prn_gated_scan(const void* xproj, const prn_params* p, const void* h0, const int32_t* cu, void* H_out) {
+  prn::GatedScanArgs a;
+  if (prn_status s = scan_args(p, &a); s != PRN_OK) return s;
+  if (a.T && (!xproj || !H_out)) return fail(PRN_ERR_INVALID_ARG, "xproj or H_out is NULL");
+  if (prn_status s = scan_pack(p, cu); s != PRN_OK) return s;
+  if (misaligned(xproj, 16) || misaligned(h0, 16) || misaligned(H_out, 16) || misaligned(a.last, 16))
+    return fail(PRN_ERR_INVALID_ARG, "xproj, h0, H_out and state_last_out must be 16-byte aligned");
+  if (prn_status s = check_scratch(p->workspace, p->workspace_bytes, prn::gated_scan_workspace(a)); s != PRN_OK) return s;
+  a.xproj = xproj, a.h0 = h0, a.cu = cu, a.H = H_out;
+  prn::launch_gated_scan(a);
+  return launched("prn_gated_scan");
+}
+
+size_t prn_gated_scan_backward_workspace_bytes(const prn_params* p) {
+  g_err.clear();
+  prn::GatedScanArgs a;
+  if (scan_args(p, &a) != PRN_OK) return 0;
+  return prn::gated_scan_backward_workspace(a);
+}
+
+prn_status prn_gated_scan_backward(const void* xproj, const prn_params* p, const void* h0, const int32_t* cu, const void* H,
+                                   const void* dH, const void* dstate_last, void* dxproj, void* dh0) {
+  prn::GatedScanArgs a;
+  if (prn_status s = scan_args(p, &a); s != PRN_OK) return s;
+  if (a.T && (!xproj || !H || !dH || !dxproj)) return fail(PRN_ERR_INVALID_ARG, "xproj, H, dH or dxproj_out is NULL");
+  if (prn_status s = scan_pack(p, cu); s != PRN_OK) return s;
+  if (misaligned(xproj, 16) || misaligned(h0, 16) || misaligned(H, 16) || misaligned(dH, 16) || misaligned(dstate_last, 16) ||
+      misaligned(dxproj, 16) || misaligned(dh0, 16))
+    return fail(PRN_ERR_INVALID_ARG, "the tensors must be 16-byte aligned");
+  if (prn_status s = check_scratch(p->workspace, p->workspace_bytes, prn::gated_scan_backward_workspace(a)); s != PRN_OK)
+    return s;
+  a.xproj = xproj, a.h0 = h0, a.cu = cu, a.H = const_cast<void*>(H);
+  a.dH = dH, a.dlast = dstate_last, a.dxproj = dxproj, a.dh0 = dh0;
+  prn::launch_gated_scan_backward(a);
+  return launched("prn_gated_scan_backward");
+}
+
+size_t prn_gated_ffn_workspace_bytes(const prn_gated_ffn_params* p) {
+  g_err.clear();
+  prn::GatedFfnArgs a;
+  if (ffn_args(p, &a) != PRN_OK) return 0;
+  return prn::gated_ffn_workspace(a);
+}
+
+prn_status prn_gated_ffn(const void* x, const void* W, const prn_gated_ffn_params* p, void* out) {
+  prn::GatedFfnArgs a;
+  if (prn_status s = ffn_args(p, &a); s != PRN_OK) return s;
+  if (a.N && (!x || !W || !out)) return fail(PRN_ERR_INVALID_ARG, "x, W or out is NULL");
+  if (misaligned(x, 16) || misaligned(W, 16) || misaligned(out, 16))
+    return fail(PRN_ERR_INVALID_ARG, "x, W and out must be 16-byte aligned");
+  if (prn_status s = check_scratch(p->workspace, p->workspace_bytes, prn::gated_ffn_workspace(a)); s != PRN_OK) return s;
+  if (!a.N) return PRN_OK;
+  prn::launch_gated_ffn(a, x, W, out);
+  return launched("prn_gated_ffn");
+}
+
+size_t prn_gated_ffn_backward_workspace_bytes(const prn_gated_ffn_params* p) {
+  g_err.clear();
+  prn::GatedFfnArgs a;
+  if (ffn_args(p, &a) != PRN_OK) return 0;
+  size_t dz;
+  const size_t own = prn::gated_ffn_dz_workspace(a, &dz);
+  const prn_params q = ffn_projection(p);
+  const size_t proj = prn_input_proj_backward_workspace_bytes(&q);
+  return g_err.empty() ? own + proj : 0;
+}
+
+prn_status prn_gated_ffn_backward(const void* x, const void* W, const void* dout, const prn_gated_ffn_params* p, void* dx,
+                                  void* dW) {
+  prn::GatedFfnArgs a;
+  if (prn_status s = ffn_args(p, &a); s != PRN_OK) return s;
+  if (a.N && (!x || !W || !dout)) return fail(PRN_ERR_INVALID_ARG, "x, W or dout is NULL");
+  if (misaligned(x, 16) || misaligned(W, 16) || misaligned(dout, 16) || misaligned(dx, 16) || misaligned(dW, 16))
+    return fail(PRN_ERR_INVALID_ARG, "x, W, dout, dx_out and dW_out must be 16-byte aligned");
+  const size_t need = prn_gated_ffn_backward_workspace_bytes(p);
+  if (!g_err.empty()) return PRN_ERR_UNSUPPORTED;
+  if (prn_status s = check_scratch(p->workspace, p->workspace_bytes, need); s != PRN_OK) return s;
+  if (!dx && !dW) return PRN_OK;
+  size_t dz;
+  const size_t own = prn::gated_ffn_dz_workspace(a, &dz);
+  prn_params q = ffn_projection(p);
+  q.workspace = a.ws + own;
+  q.workspace_bytes = need - own;
+  if (a.N) prn::launch_gated_ffn_dz(a, x, W, dout);
+  return prn_input_proj_backward(a.ws + dz, x, W, &q, dx, dW, nullptr);
+}
+
+prn_status prn_dropout(const void* x, const void* residual, const prn_dropout_params* p, void* out) {
+  if (!p) return fail(PRN_ERR_INVALID_ARG, "params is NULL");
+  if (prn_status s = check_dtype(p->dtype); s != PRN_OK) return s;
+  if (p->n < 0 || p->n > (int64_t(1) << 40)) return fail(PRN_ERR_INVALID_ARG, "n must be in 0 .. 2^40, got %lld", (long long)p->n);
+  if (!(p->p >= 0.0 && p->p <= 1.0)) return fail(PRN_ERR_INVALID_ARG, "p must be in 0 .. 1, got %g", p->p);
+  if (p->n && (!x || !out)) return fail(PRN_ERR_INVALID_ARG, "x or out is NULL");
+  if (misaligned(x, 16) || misaligned(residual, 16) || misaligned(out, 16))
+    return fail(PRN_ERR_INVALID_ARG, "x, residual and out must be 16-byte aligned");
+  if (misaligned(p->state, 8)) return fail(PRN_ERR_INVALID_ARG, "state is not 8-byte aligned");
+  if (!p->n) return PRN_OK;
+  const uint32_t drop = uint32_t(std::nearbyint(p->p * 65536.0));
+  const prn::DropoutArgs a{p->dtype == PRN_BF16, p->n, drop, drop < 65536 ? 65536.0f / float(65536 - drop) : 0.0f, p->seed,
+                           p->offset, p->state, static_cast<hipStream_t>(p->stream)};
+  prn::launch_dropout(a, x, residual, out);
+  return launched("prn_dropout");
 }
 
 }  // extern "C"

@@ -16,6 +16,18 @@ namespace prn {
 void launch_proj(bool bf16, const void* A, const void* B, const float* bias, void* C, int64_t M, int64_t N,
                  int64_t K, hipStream_t stream);
 
+// A gated product: W holds F gate rows and F up rows, the sums g and u of each
+// pair meet in the epilogue.  Without dout out = act(g) u (M x F), with dout
+// (M x F) the gradients of the sums, [dout u act'(g) | dout act(g)] (M x 2 F).
+// The products, requirements and rounding are launch_proj's.
+struct GatedProj {
+  const void* dout;
+  int64_t F;
+  bool silu;   // g s(g); else s(g)
+};
+void launch_proj_gated(bool bf16, const void* x, const void* W, void* out, int64_t M, int64_t K, const GatedProj& gp,
+                       hipStream_t stream);
+
 // The same product without bias, with operand rows lda / ldb bytes apart
 // (16-byte multiples, at least K elements).
 void launch_proj_ld(bool bf16, const void* A, int64_t lda, const void* B, int64_t ldb, void* C, int64_t M,

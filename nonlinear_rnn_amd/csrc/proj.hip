@@ -58,6 +58,8 @@
 #include <type_traits>
 
 #include "bf16split.h"
+#include "gated_cell.h"
+#include "grid_rows.h"
 #include "proj.h"
 
 namespace prn {
@@ -121,15 +123,39 @@ struct Tile {
   static_assert(STAGE % (1024 * NW) == 0, "a stage must split evenly over the waves");
 };
 
+// GATED: the columns are pairs, gate and up, of a feed-forward product: B holds
+// gp.F gate rows and gp.F up rows, and every 64 columns of a wave are 32 of
+// each, so that a lane has both sums of its 16 rows and one pair of columns.
+// kGatedOut stores act(gate) up, M x F; kGatedBack the gradients of the two
+// sums from dout (M x F), M x 2 F.  N is 2 F (rounded up to whole pairs of
+// blocks, 64).
+//
 // OUTF32: store the fp32 sums as they are (no bias, no rounding), for the
 // split-K partial products of the weight gradient.  Operand rows are lda /
 // ldb bytes apart (16-byte multiples); slice z = blockIdx.y of a split-K
 // launch starts K elements into every operand row and writes its own M x N
 // block of C.
-template <bool BF16, bool EDGE, int WR, int WC, bool OUTF32, int WM, int WN>
+enum { kPlain = 0, kGatedOut = 1, kGatedBack = 2 };
+// g s(g), or s(g), and its derivative
+__device__ __forceinline__ float gated_value(bool silu, float g) {
+  const float on = gate_of(g).on;
+  return silu ? g * on : on;
+}
+__device__ __forceinline__ float gated_slope(bool silu, float g) {
+  const Gate s = gate_of(g);
+  return silu ? s.on * fmaf(g, s.off, 1.0f) : s.on * s.off;
+}
+// column c of a gated product: its row of B (columns past the last pair: the last one's)
+__device__ __forceinline__ int64_t gated_row(int64_t c, int64_t F) {
+  const int64_t f = (c >> 6) * 32 + (c & 31);
+  return (f < F ? f : F - 1) + ((c >> 5) & 1) * F;
+}
+
+template <bool BF16, bool EDGE, int WR, int WC, bool OUTF32, int WM, int WN, int GATED = kPlain>
 __global__ void __launch_bounds__(64 * WR * WC)
 k_proj(const uint8_t* __restrict__ A, const uint8_t* __restrict__ B, const float* __restrict__ bias,
-       uint8_t* __restrict__ C, int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int n_tiles_n, int remap) {
+       uint8_t* __restrict__ C, int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int n_tiles_n, int remap,
+       GatedProj gp) {
   using Tl = Tile<WR, WC, WM, WN>;
   constexpr int BM = Tl::BM, BN = Tl::BN, IPW = Tl::IPW, STAGE = Tl::STAGE;
   constexpr int ELT = BF16 ? 2 : 4;
@@ -176,11 +202,11 @@ k_proj(const uint8_t* __restrict__ A, const uint8_t* __restrict__ B, const float
     if constexpr (EDGE) {
       kvb[p] = lds_pos(r, q) * 16;
       int64_t g = r < BM ? m0 + r : n0 + r - BM;
-      g = r < BM ? (g < M ? g : M - 1) : (g < N ? g : N - 1);
+      g = r < BM ? (g < M ? g : M - 1) : GATED ? gated_row(g, gp.F) : (g < N ? g : N - 1);
       src[p] = (r < BM ? A + g * lda : B + g * ldb) + kvb[p];
     } else {
       const int r0 = (wave * IPW + p) * (64 / CPR);
-      gbase[p] = r0 < BM ? A + (m0 + r0) * lda : B + (n0 + r0 - BM) * ldb;
+      gbase[p] = r0 < BM ? A + (m0 + r0) * lda : B + (GATED ? gated_row(n0 + r0 - BM, gp.F) : n0 + r0 - BM) * ldb;
       voff[p] = static_cast<uint32_t>((r - r0) * (r0 < BM ? lda : ldb) + lds_pos(r, q) * 16);
     }
   }
@@ -305,7 +331,10 @@ k_proj(const uint8_t* __restrict__ A, const uint8_t* __restrict__ B, const float
       const int r = v / SCPR, q = v % SCPR;
       kvb2[p] = fpos(r, q) * 16;
       int64_t g = r < BM ? m0 + r : n0 + r - BM;
-      if (EDGE) g = r < BM ? (g < M ? g : M - 1) : (g < N ? g : N - 1);
+      if (GATED && r >= BM)
+        g = gated_row(g, gp.F);
+      else if (EDGE)
+        g = r < BM ? (g < M ? g : M - 1) : (g < N ? g : N - 1);
       src2[p] = (r < BM ? A + g * lda : B + g * ldb) + kvb2[p];
     }
     auto issue2 = [&](int64_t kt, int buf) {
@@ -381,6 +410,37 @@ k_proj(const uint8_t* __restrict__ A, const uint8_t* __restrict__ B, const float
     }
   }
 
+  if constexpr (GATED != kPlain) {
+    static_assert(WN == 2 && !OUTF32, "a gate and an up block");
+    using T = std::conditional_t<BF16, uint16_t, float>;
+    auto pack = [](float v) {
+      if constexpr (BF16) return bf16_rne(v); else return v;
+    };
+    const int64_t f = ((n0 >> 6) + wc) * 32 + l32;
+#pragma unroll
+    for (int i = 0; i < WM; ++i) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int64_t gm = m0 + wr * WM * 32 + i * 32 + 8 * (r >> 2) + 4 * half + (r & 3);
+        if (EDGE && (gm >= M || f >= gp.F)) continue;
+        const float g = acc[i][0][r], u = acc[i][1][r];
+        if constexpr (GATED == kGatedOut) {
+          reinterpret_cast<T*>(C)[gm * gp.F + f] = pack(gated_value(gp.silu, g) * u);
+        } else {
+          float d;
+          if constexpr (BF16)
+            d = __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(gp.dout)[gm * gp.F + f]) << 16);
+          else
+            d = static_cast<const float*>(gp.dout)[gm * gp.F + f];
+          T* const to = reinterpret_cast<T*>(C) + gm * 2 * gp.F + f;
+          to[0] = pack(d * u * gated_slope(gp.silu, g));
+          to[gp.F] = pack(d * gated_value(gp.silu, g));
+        }
+      }
+    }
+    return;
+  }
+
   // epilogue: bias, round to the storage dtype, store.  The bias of this
   // lane's columns is loaded here, before the first store (not held in
   // registers through the main loop, nor awaited between stores)
@@ -424,7 +484,7 @@ void launch_tiles(bool bf16, const void* A, const void* B, const float* bias, vo
   auto go = [&](auto bf, auto ed) {
     k_proj<decltype(bf)::value, decltype(ed)::value, WR, WC, OUTF32, WM, WN><<<grid, Tl::NTHR, 0, stream>>>(
         static_cast<const uint8_t*>(A), static_cast<const uint8_t*>(B), bias, static_cast<uint8_t*>(C), M, N, K,
-        lda, ldb, int(tn), remap);
+        lda, ldb, int(tn), remap, GatedProj{});
   };
   using T_ = std::true_type;
   using F_ = std::false_type;
@@ -635,6 +695,36 @@ void launch_proj(bool bf16, const void* A, const void* B, const float* bias, voi
     launch_tiles<2, 2, false>(bf16, A, B, bias, C, M, N, K, ld, ld, 1, stream);
 }
 
+void launch_proj_gated(bool bf16, const void* x, const void* W, void* out, int64_t M, int64_t K, const GatedProj& gp,
+                       hipStream_t stream) {
+  using Large = Tile<4, 4>;
+  const int64_t N = (gp.F + 31) / 32 * 64, ld = K * (bf16 ? 2 : 4);
+  auto run = [&](auto waves, auto bf, auto ed, auto kind) {
+    constexpr int WV = decltype(waves)::value;
+    using Tl = Tile<WV, WV>;
+    const int64_t tn = (N + Tl::BN - 1) / Tl::BN, nb = ((M + Tl::BM - 1) / Tl::BM) * tn;
+    k_proj<decltype(bf)::value, decltype(ed)::value, WV, WV, false, 2, 2, decltype(kind)::value>
+        <<<unsigned(nb), Tl::NTHR, 0, stream>>>(static_cast<const uint8_t*>(x), static_cast<const uint8_t*>(W), nullptr,
+                                                static_cast<uint8_t*>(out), M, N, K, ld, ld, int(tn), nb % NXCD == 0, gp);
+  };
+  auto kinds = [&](auto waves, auto bf, auto ed) {
+    if (gp.dout)
+      run(waves, bf, ed, std::integral_constant<int, kGatedBack>{});
+    else
+      run(waves, bf, ed, std::integral_constant<int, kGatedOut>{});
+  };
+  auto edges = [&](auto waves, auto bf) {
+    constexpr int BN = decltype(waves)::value * 64;
+    const bool edge = M % BN != 0 || 2 * gp.F % BN != 0 || ld % ROWB != 0;
+    if (edge) kinds(waves, bf, std::true_type{}); else kinds(waves, bf, std::false_type{});
+  };
+  auto types = [&](auto waves) {
+    if (bf16) edges(waves, std::true_type{}); else edges(waves, std::false_type{});
+  };
+  const int64_t large = ((M + Large::BM - 1) / Large::BM) * ((N + Large::BN - 1) / Large::BN);
+  if (large >= kLargeTiles) types(std::integral_constant<int, 4>{}); else types(std::integral_constant<int, 2>{});
+}
+
 void launch_proj_ld(bool bf16, const void* A, int64_t lda, const void* B, int64_t ldb, void* C, int64_t M,
                     int64_t N, int64_t K, hipStream_t stream) {
   using Large = Tile<4, 4>;
@@ -703,7 +793,7 @@ __global__ void __launch_bounds__(256) k_transpose(const typename Elt<BF16>::T* 
 template <bool BF16>
 __global__ void __launch_bounds__(256) k_pad_rows(const typename Elt<BF16>::T* __restrict__ in, int64_t R, int64_t C,
                                                   typename Elt<BF16>::T* __restrict__ out, int64_t Cp) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t i = block_in_rows() * 256 + threadIdx.x;
   if (i >= R * Cp) return;
   const int64_t r = i / Cp, c = i - r * Cp;
   out[i] = c < C ? in[r * C + c] : Elt<BF16>::st(0.0f);
@@ -914,7 +1004,7 @@ void launch_transpose(bool bf16, const void* in, int64_t R, int64_t C, int64_t l
 }
 
 void launch_pad_rows(bool bf16, const void* in, int64_t R, int64_t C, void* out, int64_t Cp, hipStream_t stream) {
-  const dim3 grid(static_cast<unsigned>((R * Cp + 255) / 256));
+  const dim3 grid = rows_of_blocks((R * Cp + 255) / 256);
   if (bf16)
     k_pad_rows<true><<<grid, 256, 0, stream>>>(static_cast<const uint16_t*>(in), R, C, static_cast<uint16_t*>(out), Cp);
   else

@@ -1,6 +1,7 @@
 """A token model around the recurrence: the embedding lookup, the norms at a
-block boundary with their gate and residual scale, and the softmax cross
-entropy over a vocabulary, each with its gradient.
+block boundary with their gate and residual scale, the gated feed-forward
+product, dropout, and the softmax cross entropy over a vocabulary, each with
+its gradient.
 
 As in ``api``: strided views (and views that do not start on 16 bytes) are
 copied to a dense layout first, outputs and workspaces are allocated here, the
@@ -13,6 +14,7 @@ from __future__ import annotations
 import torch
 
 from . import binding as B_
+from .autograd import first as _first
 
 
 def _rows(t):
@@ -51,29 +53,6 @@ def _shaped(shape, **tensors):
 
 def _scratch(n: int, device) -> torch.Tensor:
     return torch.empty(max(n, 1), dtype=torch.uint8, device=device)
-
-
-class _FirstDerivatives(torch.autograd.Function):
-    """Copies of gradients, and an error where a derivative of theirs is asked for."""
-
-    @staticmethod
-    def forward(ctx, count, *tensors):
-        return tuple(t.clone() for t in tensors[:count])
-
-    @staticmethod
-    def backward(ctx, *_):
-        raise RuntimeError("the token-model operators have first derivatives only")
-
-
-def _first(grads, *sources):
-    """A backward pass's gradients.  Under create_graph they would come without a graph, and a derivative of theirs
-    would silently lack this operator's part: it raises instead."""
-    sources = [s for s in sources if s is not None and s.requires_grad]
-    if not torch.is_grad_enabled() or not sources:
-        return grads
-    given = [g for g in grads if g is not None]
-    tied = iter(_FirstDerivatives.apply(len(given), *given, *sources))
-    return tuple(None if g is None else next(tied) for g in grads)
 
 
 # ------------------------------------------------------------------ embedding lookup ---
@@ -255,3 +234,113 @@ class _VocabLossFunction(torch.autograd.Function):
 def vocab_loss_apply(x, W, targets, *, scale: float = 1.0, ignore_index: int = -100):
     """Differentiable vocab_loss: gradients of loss and lse reach x and W."""
     return _VocabLossFunction.apply(x, W, targets, float(scale), int(ignore_index))
+
+
+# ------------------------------------------------------------------ feed-forward ---
+
+def _dense(t):
+    """t as a dense tensor that starts on 16 bytes: itself where it is that already."""
+    if not t.is_contiguous():
+        t = t.contiguous()
+    return t.clone() if t.data_ptr() % 16 else t
+
+
+def gated_ffn(x, W, *, act: str = "silu") -> torch.Tensor:
+    """act(x Wg^T) * (x Wu^T) in one kernel: x (..., d), W (2 F, d) = [Wg; Wu]; (..., F).  act "silu" or "sigmoid"."""
+    if W.dim() != 2 or W.shape[0] % 2 or W.shape[1] != x.shape[-1]:
+        raise ValueError(f"W must be (2 F, {x.shape[-1]}), got {tuple(W.shape)}")
+    x2, W = _rows(x), _dense(W)
+    N, d, F = *x2.shape, W.shape[0] // 2
+    out = x2.new_empty((N, F))
+    n = B_.prn_gated_ffn_workspace_bytes(x2.dtype, N, d, F)
+    B_.prn_gated_ffn(x2, W, out, act=act, workspace=_scratch(n, x2.device) if n else None)
+    return out if x.dim() == 2 else out.view(*x.shape[:-1], F)
+
+
+def gated_ffn_backward(dout, x, W, *, act: str = "silu", want_x: bool = True, want_W: bool = True):
+    """Gradients (dx, dW) of gated_ffn from dout (..., F); each only if wanted, else None.  The sums are formed
+    again: nothing but x and W is kept between the passes."""
+    if W.dim() != 2 or W.shape[0] % 2 or W.shape[1] != x.shape[-1]:
+        raise ValueError(f"W must be (2 F, {x.shape[-1]}), got {tuple(W.shape)}")
+    F = W.shape[0] // 2
+    _shaped((*x.shape[:-1], F), dout=dout)
+    x2, W, dout2 = _rows(x), _dense(W), _rows(dout)
+    dx = torch.empty_like(x2) if want_x else None
+    dW = torch.empty_like(W) if want_W else None
+    ws = _scratch(B_.prn_gated_ffn_backward_workspace_bytes(x2.dtype, *x2.shape, F), x2.device)
+    B_.prn_gated_ffn_backward(x2, W, dout2, act=act, dx_out=dx, dW_out=dW, workspace=ws)
+    return (None if dx is None else dx.view(x.shape)), dW
+
+
+class _GatedFfnFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, W, act):
+        ctx.save_for_backward(x, W)
+        ctx.act = act
+        return gated_ffn(x, W, act=act)
+
+    @staticmethod
+    def backward(ctx, dout):
+        x, W = ctx.saved_tensors
+        dx, dW = gated_ffn_backward(dout.to(x.dtype), x, W, act=ctx.act, want_x=ctx.needs_input_grad[0],
+                                    want_W=ctx.needs_input_grad[1])
+        return *_first((dx, dW), dout, x, W), None
+
+
+def gated_ffn_apply(x, W, *, act: str = "silu") -> torch.Tensor:
+    """Differentiable gated_ffn."""
+    return _GatedFfnFunction.apply(x, W, act)
+
+
+# ------------------------------------------------------------------ dropout ---
+
+def dropout(x, p: float, *, seed, offset: int = 0, residual=None) -> torch.Tensor:
+    """residual + x / (1 - q) where x stays and residual (or 0) where it is dropped, a share q = p rounded to 2^-16
+    of the elements.  Which ones is a function of (seed, offset, the element's index) alone: another offset for
+    every use of a seed.  seed may be an int64 tensor (seed, offset) on the device, read when the kernel runs, so
+    that a captured graph draws anew after it is changed."""
+    _shaped(x.shape, residual=residual)
+    x2 = _dense(x)
+    r2 = None if residual is None else _dense(residual)
+    out = torch.empty(x2.shape, dtype=x2.dtype, device=x2.device)
+    if isinstance(seed, torch.Tensor):
+        if offset:
+            raise ValueError("a seed on the device holds its offset itself")
+        B_.prn_dropout(x2, out, p=p, state=seed, residual=r2)
+    else:
+        B_.prn_dropout(x2, out, p=p, seed=seed, offset=offset, residual=r2)
+    return out
+
+
+def dropout_backward(dout, p: float, *, seed, offset: int = 0) -> torch.Tensor:
+    """The gradient of dropout at x, from the gradient dout at its result (residual's is dout itself): dout / (1 - q)
+    where x stayed, zero where it was dropped, by the same seed and offset."""
+    return dropout(dout, p, seed=seed, offset=offset)
+
+
+class _DropoutFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, p, seed, offset):
+        state = isinstance(seed, torch.Tensor)
+        if state:   # the backward's numbers are this call's, whatever the tensor holds by then
+            seed = seed.clone()
+        ctx.save_for_backward(*((seed,) if state else ()))
+        ctx.args = (p, None if state else seed, offset)
+        ctx.dtype, ctx.kept = x.dtype, residual is not None
+        return dropout(x, p, seed=seed, offset=offset, residual=residual)
+
+    @staticmethod
+    def backward(ctx, dout):
+        p, seed, offset = ctx.args
+        if ctx.saved_tensors:
+            seed, = ctx.saved_tensors
+        dout = dout.to(ctx.dtype)
+        dx = None
+        if ctx.needs_input_grad[0]:
+            dx, = _first((dropout_backward(dout, p, seed=seed, offset=offset),), dout)
+        return dx, dout if ctx.kept else None, None, None, None
+
+
+def dropout_apply(x, p: float, *, seed, offset: int = 0, residual=None) -> torch.Tensor:
+    """Differentiable dropout: the mask is drawn again in the backward pass, nothing is kept but the seed."""
+    return _DropoutFunction.apply(x, residual, float(p), seed, int(offset))

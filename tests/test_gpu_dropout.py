@@ -1,0 +1,118 @@
+"""Dropout on the GPU against oracle.gated: the same elements, bit for bit, and
+their values to the roundings of a product and a sum in fp32 and the output's."""
+import numpy as np
+import pytest
+import torch
+
+import nonlinear_rnn_amd as prn
+from nonlinear_rnn_amd import binding as B
+from oracle import gated
+
+pytestmark = pytest.mark.gpu
+
+HALF = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8}
+SEEDS = [(0, 0), (1, 5), ((1 << 63) + 12345, (1 << 40) + 3), (-1, -1)]
+
+
+def _np(t):
+    return t.detach().double().cpu().numpy()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n", [1, 7, 8, 9, 2047, 2048, 2049, 20011])
+@pytest.mark.parametrize("p", [0.0, 0.1, 0.5, 1.0, 1.0 / 65536, 65535 / 65536])
+def test_elements_and_values(n, p, dtype):
+    g = torch.Generator().manual_seed(n)
+    x, r = (torch.randn(n, generator=g).to(dtype).cuda() for _ in range(2))
+    seed, offset = SEEDS[n % len(SEEDS)]
+    m = (1 << 64) - 1
+    keep = gated.kept(n, p, seed & m, offset & m)
+    ones = prn.dropout(torch.ones_like(x), p, seed=seed, offset=offset)
+    assert ((_np(ones) != 0) == keep).all()
+    for res in (None, r):
+        want = gated.dropout(_np(x), p, seed & m, offset & m, None if res is None else _np(res))
+        got = _np(prn.dropout(x, p, seed=seed, offset=offset, residual=res))
+        part = np.abs(want - (0.0 if res is None else _np(r)))
+        tol = 2 * 2.0 ** -24 * (part + np.abs(want)) * (1 + HALF[dtype]) + HALF[dtype] * np.abs(want)
+        assert (np.abs(got - want) <= tol).all()
+        if res is not None:
+            assert (got[~keep] == _np(r)[~keep]).all()
+
+
+def test_the_mask_is_the_same_for_every_type_shape_and_direction():
+    x = torch.rand(6, 35, 11, device="cuda") + 1.0
+    a = prn.dropout(x, 0.3, seed=9, offset=2)
+    b = prn.dropout(x.bfloat16().view(-1), 0.3, seed=9, offset=2).view_as(x)
+    c = prn.dropout_backward(x.transpose(0, 2).contiguous().transpose(0, 2), 0.3, seed=9, offset=2)
+    assert torch.equal(a != 0, b != 0) and torch.equal(a, c)
+    for other in (dict(seed=10, offset=2), dict(seed=9, offset=3), dict(seed=9 + (1 << 32), offset=2),
+                  dict(seed=9, offset=2 + (1 << 32))):
+        assert not torch.equal(prn.dropout(x, 0.3, **other) != 0, a != 0)
+
+
+def test_what_is_dropped_does_not_count():
+    x = torch.full((4000,), float("nan"), device="cuda")
+    x[::2] = float("inf")
+    r = torch.randn(4000, device="cuda")
+    keep = torch.from_numpy(gated.kept(4000, 0.4, 3, 1)).cuda()
+    out = prn.dropout(x, 0.4, seed=3, offset=1, residual=r)
+    assert torch.equal(out[~keep], r[~keep]) and not torch.isfinite(out[keep]).any()
+
+
+def test_in_place_through_the_binding():
+    x, r = torch.randn(5000, device="cuda"), torch.randn(5000, device="cuda")
+    want = prn.dropout(x, 0.2, seed=4, residual=r)
+    for out in (x.clone(), r.clone()):
+        a, b = (out, r) if torch.equal(out, x) else (x, out)
+        B.prn_dropout(a, out, p=0.2, seed=4, residual=b)
+        assert torch.equal(out, want)
+
+
+def test_a_seed_on_the_device():
+    x = torch.randn(3000, device="cuda")
+    state = torch.tensor([11, 0], device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    prn.dropout(x, 0.5, seed=state)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        out = prn.dropout(x, 0.5, seed=state)
+    for k in range(4):
+        state[1] = k
+        want = prn.dropout(x, 0.5, seed=11, offset=k)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want), k
+
+
+def test_autograd():
+    x, r = (torch.randn(40, 33, device="cuda", requires_grad=True) for _ in range(2))
+    w = torch.randn(40, 33, device="cuda")
+    state = torch.tensor([5, 6], device="cuda")
+    for kw in (dict(seed=5, offset=6), dict(seed=state)):
+        state[0], state[1] = 5, 6
+        y = prn.dropout_apply(x, 0.25, residual=r, **kw)
+        state[1] = 99   # the backward pass is of the call as it was
+        dx, dr = torch.autograd.grad((y * w).sum(), (x, r))
+        assert torch.equal(dx, prn.dropout(w, 0.25, seed=5, offset=6)) and torch.equal(dr, w)
+    g, = torch.autograd.grad(prn.dropout_apply(x, 0.5, seed=1).square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="first derivatives only"):
+        g.square().sum().backward()
+
+
+def test_nothing_and_refusals():
+    x = torch.zeros(4, 8, device="cuda")
+    assert prn.dropout(x[:0], 0.5, seed=1).shape == (0, 8)
+    for p in (-0.1, 1.1, float("nan")):
+        with pytest.raises(B.PrnError):
+            prn.dropout(x, p, seed=1)
+    with pytest.raises(ValueError):
+        prn.dropout(x, 0.5, seed=1, residual=torch.zeros(8, 4, device="cuda"))
+    with pytest.raises(TypeError):
+        prn.dropout(x, 0.5, seed=1, residual=x.bfloat16())
+    with pytest.raises(TypeError):
+        prn.dropout(x.half(), 0.5, seed=1)
+    with pytest.raises(TypeError):
+        prn.dropout(x, 0.5, seed=torch.tensor([1, 2], dtype=torch.int32, device="cuda"))
+    with pytest.raises(ValueError):
+        prn.dropout(x, 0.5, seed=torch.tensor([1, 2], device="cuda"), offset=1)

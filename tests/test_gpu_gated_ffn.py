@@ -1,0 +1,167 @@
+"""The gated feed-forward product on the GPU against oracle.gated in float64.
+
+Tolerances are the oracle's elementwise bounds (gated_ffn_bounds) and the
+output's own rounding; the gradients of the sums are stored once in between.
+"""
+import numpy as np
+import pytest
+import torch
+
+import nonlinear_rnn_amd as prn
+from nonlinear_rnn_amd import binding as B
+from oracle import gated
+
+pytestmark = pytest.mark.gpu
+
+HALF = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8}
+
+
+def _np(t):
+    return t.detach().double().cpu().numpy()
+
+
+def _case(N, d, F, dtype, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    new = lambda *s: torch.randn(*s, generator=g)   # noqa: E731
+    return new(N, d).to(dtype).cuda(), (new(2 * F, d) * (1.5 / d ** 0.5)).to(dtype).cuda(), new(N, F).to(dtype).cuda()
+
+
+def _close(name, got, want, bound, dtype):
+    got = _np(got)
+    tol = bound * (1 + HALF[dtype]) + HALF[dtype] * np.abs(want) + 1e-30
+    bad = ~(np.abs(got - want) <= tol)
+    worst = (np.abs(got - want) / tol).max() if got.size else 0.0
+    print(f"  {name}: worst {worst:.3f} of its tolerance", flush=True)
+    assert not bad.any(), (name, np.argwhere(bad)[:5], got[bad][:5], want[bad][:5], tol[bad][:5])
+
+
+def _check(x, W, dout, kind, dtype):
+    xd, Wd, gd = _np(x), _np(W), _np(dout)
+    out = prn.gated_ffn(x, W, act=kind)
+    dx, dW = prn.gated_ffn_backward(dout, x, W, act=kind)
+    b_out, b_dx, b_dW = gated.gated_ffn_bounds(xd, Wd, kind, gd, HALF[dtype])
+    want_dx, want_dW = gated.gated_ffn_backward(xd, Wd, gd, kind)
+    _close("out", out, gated.gated_ffn(xd, Wd, kind), b_out, dtype)
+    _close("dx", dx, want_dx, b_dx, dtype)
+    _close("dW", dW, want_dW, b_dW, dtype)
+
+
+SIZES = [(1, 1, 1), (1, 8, 32), (2, 7, 3), (3, 64, 31), (16, 128, 64), (17, 130, 65), (33, 40, 200), (64, 512, 96),
+         (65, 100, 129), (127, 16, 64), (128, 64, 128), (129, 72, 130), (256, 256, 128), (300, 200, 100), (520, 24, 257),
+         (1030, 96, 70)]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("kind", ["silu", "sigmoid"])
+@pytest.mark.parametrize("N,d,F", SIZES)
+def test_sizes(N, d, F, kind, dtype):
+    _check(*_case(N, d, F, dtype, seed=N + d + F), kind, dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("N,d,F", [(4096, 32, 1536), (5000, 40, 1300), (12800, 24, 520)])
+def test_large_tiles(N, d, F, dtype):
+    _check(*_case(N, d, F, dtype), "silu", dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_values_far_apart(dtype):
+    """A large token, a large row of W, and zeros, each held to its own size."""
+    x, W, dout = _case(100, 48, 40, dtype)
+    x[3] *= 2.0 ** 20
+    W[7] *= 2.0 ** 15
+    x[5] = 0
+    W[50] = 0
+    dout[9] *= 2.0 ** -30
+    dout[11] = 0
+    _check(x, W, dout, "sigmoid", dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("N", [5, 150])
+def test_what_is_not_finite_stays_in_its_row(dtype, N):
+    x, W, dout = _case(N, 40, 24, dtype)
+    out, (dx, _) = prn.gated_ffn(x, W), prn.gated_ffn_backward(dout, x, W)
+    for bad in (float("nan"), float("inf"), float("-inf")):
+        y = x.clone()
+        y[3, 5] = bad
+        out2, (dx2, _) = prn.gated_ffn(y, W), prn.gated_ffn_backward(dout, y, W)
+        rest = [n for n in range(N) if n != 3]
+        assert torch.equal(out2[rest], out[rest]) and torch.equal(dx2[rest], dx[rest])
+        assert not torch.isfinite(out2[3]).all()
+
+
+def test_no_rows():
+    x, W = torch.empty(0, 24, device="cuda"), torch.randn(16, 24, device="cuda")
+    assert prn.gated_ffn(x, W).shape == (0, 8)
+    dx, dW = prn.gated_ffn_backward(torch.empty(0, 8, device="cuda"), x, W)
+    assert dx.shape == (0, 24) and (dW == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_shapes_layouts_and_the_same_bits(dtype):
+    x, W, dout = _case(210, 36, 40, dtype)
+    out, (dx, dW) = prn.gated_ffn(x, W), prn.gated_ffn_backward(dout, x, W)
+    wide = torch.empty(210, 37, dtype=dtype, device="cuda")
+    wide[:, 1:] = x
+    Wt = W.t().contiguous().t()
+    y, g = wide[:, 1:].unflatten(0, (3, 70)), dout.view(3, 70, 40)
+    assert torch.equal(prn.gated_ffn(y, Wt), out.view(3, 70, 40))
+    dx2, dW2 = prn.gated_ffn_backward(g, y, Wt)
+    assert torch.equal(dx2, dx.view(3, 70, 36)) and torch.equal(dW2, dW)
+    only = prn.gated_ffn_backward(dout, x, W, want_W=False)
+    assert torch.equal(only[0], dx) and only[1] is None
+    only = prn.gated_ffn_backward(dout, x, W, want_x=False)
+    assert torch.equal(only[1], dW) and only[0] is None
+
+
+def test_autograd():
+    x, W, dout = _case(50, 24, 16, torch.float32)
+    x.requires_grad_(), W.requires_grad_()
+    dx, dW = torch.autograd.grad((prn.gated_ffn_apply(x, W, act="sigmoid") * dout).sum(), (x, W))
+    want = prn.gated_ffn_backward(dout, x, W, act="sigmoid")
+    assert torch.equal(dx, want[0]) and torch.equal(dW, want[1])
+    g, = torch.autograd.grad(prn.gated_ffn_apply(x, W).sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="first derivatives only"):
+        g.square().sum().backward()
+
+
+@pytest.mark.parametrize("N", [3, 400])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_captured_and_replayed(N, dtype):
+    x, W, dout = _case(N, 52, 70, dtype)
+    both = lambda: (prn.gated_ffn(x, W), *prn.gated_ffn_backward(dout, x, W))   # noqa: E731
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        both()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = both()
+    for k in range(4):
+        for t, new in zip((x, W, dout), _case(N, 52, 70, dtype, seed=k + 1)):
+            t.copy_(new)
+        want = [t.clone() for t in both()]
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want)), k
+
+
+def test_refusals():
+    x, W = torch.zeros(4, 8, device="cuda"), torch.zeros(6, 8, device="cuda")
+    for bad in (W[:5], W[:, :4], W[0]):
+        with pytest.raises(ValueError):
+            prn.gated_ffn(x, bad)
+    with pytest.raises(ValueError):
+        prn.gated_ffn(x, W, act="tanh")
+    with pytest.raises(TypeError):
+        prn.gated_ffn(x, W.bfloat16())
+    with pytest.raises(TypeError):
+        prn.gated_ffn(x.half(), W.half())
+    with pytest.raises(ValueError):
+        prn.gated_ffn_backward(torch.zeros(3, 4, device="cuda"), x, W)   # rows and columns the wrong way round
+    with pytest.raises(ValueError):
+        prn.gated_ffn_backward(torch.zeros(4, 2, device="cuda"), x, W)
+    assert B.lib() is not None
