@@ -50,6 +50,21 @@ def test_the_mask_is_the_same_for_every_type_shape_and_direction():
         assert not torch.equal(prn.dropout(x, 0.3, **other) != 0, a != 0)
 
 
+@pytest.mark.parametrize("dtype,n", [(torch.float32, (1 << 25) + 13), (torch.bfloat16, (1 << 26) + 5)])
+def test_large_tensors(dtype, n):
+    """Past 128 MB, against pieces of the same numbers: a piece that starts at a block has the blocks from there on."""
+    x, r = torch.randn(n, device="cuda").to(dtype), torch.randn(n, device="cuda").to(dtype)
+    out, dx = prn.dropout(x, 0.3, seed=21, offset=4, residual=r), prn.dropout_backward(x, 0.3, seed=21, offset=4)
+    small = prn.dropout(x[:1 << 20], 0.3, seed=21, offset=4, residual=r[:1 << 20])
+    assert torch.equal(out[:1 << 20], small)
+    for lo in (0, 8 * ((n - 3000) // 8)):   # the first and the last blocks, one by one
+        hi = min(n, lo + 3000)
+        halves = gated.philox(np.arange(lo // 8, (hi + 7) // 8), 4, 21)
+        keep = np.stack([halves & 0xFFFF, halves >> 16], -1).reshape(-1)[:hi - lo] >= round(0.3 * 65536)
+        assert ((_np(dx[lo:hi]) != 0) == keep).all()
+        assert (_np(out[lo:hi])[~keep] == _np(r[lo:hi])[~keep]).all()
+
+
 def test_what_is_dropped_does_not_count():
     x = torch.full((4000,), float("nan"), device="cuda")
     x[::2] = float("inf")
