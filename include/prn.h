@@ -502,9 +502,9 @@ size_t prn_vocab_loss_backward_workspace_bytes(const prn_vocab_loss_params* para
 /* ---- Gated linear recurrence over time ---------------------------------
  * h_t = f_t h_{t-1} + in_t v_t for the cells PRN_CELL_GATED and
  * PRN_CELL_GATED_INPUT above, the state and its maps in fp32, every output
- * rounded once.  Two calls with the same arguments give the same bits.  No
- * workgroup waits for another (there is no error_out), no memory has to be
- * cleared: a call can be captured in a HIP graph with its buffers pinned.
+ * rounded once.  Two calls with the same arguments give the same bits.  A call
+ * can be captured in a HIP graph with its buffers pinned; calls that may overlap
+ * need workspaces of their own.
  *   xproj      (B, T, G, d_h) storage dtype, biases included
  *   h0         (rows, d_h) storage dtype or NULL for zeros; rows = B, or n_seqs
  *              for a ragged pack
@@ -514,8 +514,11 @@ size_t prn_vocab_loss_backward_workspace_bytes(const prn_vocab_loss_params* para
  *   H_out      (B, T, d_h) storage dtype
  * params: cell, dtype, B, T (below 2^31), d_h, n_seqs, state_last_out
  * ((rows, d_h) or NULL; an empty sequence's is its h0), workspace (at least
- * prn_gated_scan_workspace_bytes(params)), stream; a, states_out, picard_iters
- * and error_out are not used.  Tensors must be 16-byte aligned. */
+ * prn_gated_scan_workspace_bytes(params)), stream, error_out (as for
+ * prn_newton_forward: few and long chains run as chunks that wait for the ones
+ * before them; after a wait that gave up the results are NaN from the chunk on);
+ * a, states_out and picard_iters are not used.  PRN_SPIN_LIMIT is read as there.
+ * Tensors must be 16-byte aligned. */
 prn_status prn_gated_scan(const void* xproj, const prn_params* params, const void* h0, const int32_t* cu_seqlens,
                           void* H_out);
 size_t prn_gated_scan_workspace_bytes(const prn_params* params);
@@ -530,7 +533,7 @@ size_t prn_gated_scan_workspace_bytes(const prn_params* params);
  *   dstate_last  (rows, d_h) storage dtype, or NULL for zero
  *   dxproj_out   (B, T, G, d_h) storage dtype
  *   dh0_out      (rows, d_h) storage dtype, or NULL
- * The states are formed again in fp32, from H at every 64th step.  params as for
+ * The states are formed again in fp32, from H at every 64th or 128th step.  params as for
  * the forward, its workspace prn_gated_scan_backward_workspace_bytes(params). */
 prn_status prn_gated_scan_backward(const void* xproj, const prn_params* params, const void* h0, const int32_t* cu_seqlens,
                                    const void* H, const void* dH, const void* dstate_last, void* dxproj_out,
@@ -547,7 +550,8 @@ typedef struct {
   int32_t act;             /* PRN_ACT_SILU | PRN_ACT_SIGMOID                            */
   int64_t N;               /* rows, below 2^31                                          */
   int64_t d;               /* input channels                                            */
-  int64_t F;               /* output channels; 2 F d below 2^32                         */
+  int64_t F;               /* output channels; 2 (F + 256) (d + 64) below 2^31, N F and
+                              N d below 2^36                                            */
   void* workspace;         /* 256-byte aligned scratch                                  */
   size_t workspace_bytes;  /* >= prn_gated_ffn_workspace_bytes(params), backward:
                               >= prn_gated_ffn_backward_workspace_bytes(params)         */

@@ -364,7 +364,8 @@ def input_proj_apply(x, W, bias=None, *, cell: str):
 
 # ------------------------------------------------------------------ gated linear recurrence ---
 # The recurrence that is linear in its state needs no Newton iteration: one scan, exact, without a residual to
-# gate and without a wait that can time out, so no host synchronisation either.
+# gate, and so without a host synchronisation.  (Where a wait of few long chains for the chunk before gives up, as
+# LookbackTimeoutError has it, the results are NaN from there on; binding.prn_gated_scan's error_out tells.)
 
 def _aligned(t):
     """t as a dense tensor that starts on 16 bytes (None for None)."""

@@ -508,29 +508,23 @@ def prn_decode_step(x, W, bias, a, state_out, *, cell: str, state_in=None, h_out
     """One T = 1 step for B slots: x (B, d_in), W (G*d_h, d_in), bias (G*d_h) fp32 or None,
     state_in / state_out (B, S, d_h) (distinct buffers), h_out (B, d_h) or None.
     The gated linear cells have no a (None)."""
-    _dev(x, "x")
-    _dev(W, "W", x.dtype)
-    _dev(bias, "bias", torch.float32)
-    _dev(a, "a", torch.float32)
-    _dev(state_out, "state_out", x.dtype)
-    _dev(state_in, "state_in", x.dtype)
-    _dev(h_out, "h_out", x.dtype)
+    dev, code = _lead(x, "x", 2)
+    _lead(W, "W", 2)
+    if cell not in CELLS:
+        raise ValueError(f"unknown cell {cell!r}")
     Bn, d_in = x.shape
-    G, S = GATES[cell], STATE[cell]
+    G, S, dt, f32 = GATES[cell], STATE[cell], x.dtype, torch.float32
     d_h = W.shape[0] // G
-    if W.shape != (G * d_h, d_in) or (a is not None and a.shape != (G, d_h)) or state_out.shape != (Bn, S, d_h):
-        raise ValueError(f"shape mismatch: x {tuple(x.shape)} W {tuple(W.shape)} state_out {tuple(state_out.shape)}")
     if a is None and cell not in GATED_CELLS:
         raise ValueError(f"the cell {cell!r} has recurrent weights a")
-    if bias is not None and bias.shape != (G * d_h,):
-        raise ValueError("bias must have G*d_h entries")
-    if state_in is not None and state_in.shape != (Bn, S, d_h):
-        raise ValueError("state_in must match state_out")
-    if h_out is not None and h_out.shape != (Bn, d_h):
-        raise ValueError("h_out must be (B, d_h)")
-    p = make_params(cell, x.dtype, Bn, 1, d_h, d_in=d_in, a=a, stream=stream)
-    _check(lib().prn_decode_step(_ptr(x), _ptr(W), _ptr(bias), ctypes.byref(p), _ptr(state_in), _ptr(state_out),
-                                 _ptr(h_out)))
+    state = (Bn, S, d_h)
+    p = prn_params(CELLS[cell], code, Bn, 1, d_in, d_h, 0, _arg(a, "a", f32, (G, d_h), dev), None, None, 0,
+                   _handle(stream, dev))
+    with _On(dev):
+        _check(lib().prn_decode_step(
+            _arg(x, "x", dt, (Bn, d_in), dev), _arg(W, "W", dt, (G * d_h, d_in), dev),
+            _arg(bias, "bias", f32, (G * d_h,), dev), p, _arg(state_in, "state_in", dt, state, dev),
+            _arg(state_out, "state_out", dt, state, dev), _arg(h_out, "h_out", dt, (Bn, d_h), dev)))
 
 
 def _head_common(xproj, A, H_out, h0, state_last_out, d_head):
@@ -582,6 +576,25 @@ def prn_head_sequential_forward(xproj, A, H_out, *, d_head: int = 16, h0=None, s
 # that is not.
 
 _raw_stream = torch._C._cuda_getCurrentRawStream   # the handle alone, without a Stream object
+
+
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+class _On:
+    """Makes a device the current one for a launch, where it is not: a stream belongs to its device."""
+    __slots__ = ("guard",)
+
+    def __init__(self, dev):
+        self.guard = None if _current_device() == dev else torch.cuda.device(dev)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *reason):
+        if self.guard is not None:
+            self.guard.__exit__(*reason)
 
 
 def _refuse(t, name, dtype, shape, dev) -> None:
@@ -767,22 +780,7 @@ def prn_vocab_loss_backward(x, W, targets, lse, dloss, *, dlse=None, scale: floa
         _arg(dx_out, "dx_out", dt, (N, d), dev), _arg(dW_out, "dW_out", dt, (V, d), dev)))
 
 
-class _On:
-    """Makes a device the current one for a launch, where it is not: a stream belongs to its device."""
-
-    def __init__(self, dev):
-        self.guard = None if torch.cuda.current_device() == dev else torch.cuda.device(dev)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *reason):
-        if self.guard is not None:
-            self.guard.__exit__(*reason)
-
-
-def _scan_params(xproj, cell: str, cu_seqlens, state_last_out, workspace, stream):
+def _scan_params(xproj, cell: str, cu_seqlens, state_last_out, workspace, stream, error_out):
     """(device, parameters, the shape of per-sequence states)"""
     dev, code = _lead(xproj, "xproj", 4)
     if cell not in GATED_CELLS:
@@ -801,6 +799,7 @@ def _scan_params(xproj, cell: str, cu_seqlens, state_last_out, workspace, stream
     p.state_last_out = _arg(state_last_out, "state_last_out", xproj.dtype, rows, dev)
     p.workspace, p.workspace_bytes = _scratch(workspace, dev)
     p.stream = _handle(stream, dev)
+    p.error_out = _arg(error_out, "error_out", torch.int32, (1,), dev)
     return dev, p, rows
 
 
@@ -810,9 +809,10 @@ def prn_gated_scan_workspace_bytes(cell: str, dtype: torch.dtype, B: int, T: int
 
 
 def prn_gated_scan(xproj, H_out, *, cell: str, h0=None, cu_seqlens=None, state_last_out=None, workspace=None,
-                   stream=None) -> None:
-    """H_out (B, T, d) of the gated linear recurrence over xproj (B, T, G, d); h0 and state_last_out (rows, 1, d)."""
-    dev, p, rows = _scan_params(xproj, cell, cu_seqlens, state_last_out, workspace, stream)
+                   stream=None, error_out=None) -> None:
+    """H_out (B, T, d) of the gated linear recurrence over xproj (B, T, G, d); h0 and state_last_out (rows, 1, d); error_out
+    one int32."""
+    dev, p, rows = _scan_params(xproj, cell, cu_seqlens, state_last_out, workspace, stream, error_out)
     Bn, T, _, d = xproj.shape
     dt = xproj.dtype
     with _On(dev):
@@ -829,10 +829,10 @@ def prn_gated_scan_backward_workspace_bytes(cell: str, dtype: torch.dtype, B: in
 
 
 def prn_gated_scan_backward(xproj, H, dH, dxproj_out, *, cell: str, h0=None, cu_seqlens=None, dstate_last=None,
-                            dh0_out=None, workspace=None, stream=None) -> None:
+                            dh0_out=None, workspace=None, stream=None, error_out=None) -> None:
     """dxproj_out (B, T, G, d) and, optional, dh0_out (rows, 1, d) from dH (B, T, d) and dstate_last (rows, 1, d)
     or None; H (B, T, d) the forward's."""
-    dev, p, rows = _scan_params(xproj, cell, cu_seqlens, None, workspace, stream)
+    dev, p, rows = _scan_params(xproj, cell, cu_seqlens, None, workspace, stream, error_out)
     Bn, T, _, d = xproj.shape
     dt, states = xproj.dtype, (Bn, T, d)
     with _On(dev):

@@ -18,7 +18,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libprn.so")
 SOURCES = ["prn_lib.hip", "proj.hip", "embed.hip", "block_norm.hip", "vocab_loss.hip",
-           "gated_scan.hip", "gated_ffn.hip", "dropout.hip"]
+           "gated_scan.hip", "gated_ffn.hip", "gated_few.hip", "dropout.hip"]
 ARCH = os.environ.get("PRN_OFFLOAD_ARCH", "gfx950")
 
 # Packed fp32 VALU instructions are disabled: plain fp32 code only.

@@ -12,14 +12,13 @@
 // all, through cross-lane swaps and DPP, not LDS) leaves lane l with the
 // complete sum of output l.
 // The sum gets its bias, is rounded to the storage dtype (as the
-// projection's output would be; the gated linear cells take it as it is), and
-// lanes 0..15 gather their slot's gates and step the cell from the carry.  Waves are independent: no LDS, no
+// projection's output would be), and lanes 0..15 gather their slot's gates
+// and step the cell from the carry.  Waves are independent: no LDS, no
 // barrier.
 #pragma once
 
 #include <type_traits>
 
-#include "gated_cell.h"
 #include "newton_kernels.h"
 
 namespace prn {
@@ -50,7 +49,7 @@ k_decode(const typename Storage<DT>::T* __restrict__ x, const typename Storage<D
   const int g_l = lane / SB;
   const float bv = (bias && g_l < G) ? bias[g_l * d_h + ch] : 0.0f;
   ChanCoef<C> cf;
-  if constexpr (!IsGated<C>::value) cf.load(a, d_h, ch);
+  cf.load(a, d_h, ch);
   const int64_t slot = s0 + imin(lane & (SB - 1), n_s - 1);
   float s[S];
 #pragma unroll
@@ -127,7 +126,7 @@ k_decode(const typename Storage<DT>::T* __restrict__ x, const typename Storage<D
   float v = p[0];
   if (g_l < G) {
     if (bias) v += bv;
-    if constexpr (!IsGated<C>::value) v = ST::round(v);
+    v = ST::round(v);
   }
   float xs[G];
 #pragma unroll

@@ -1,7 +1,5 @@
-// The step of the gated linear recurrence, for its scan and its decode step.
+// The gates of the linear recurrence and the feed-forward product.
 #pragma once
-
-#include <type_traits>
 
 #include "prn_device.h"
 
@@ -20,22 +18,5 @@ __device__ __forceinline__ Gate gate_of(float x) {
   const float lo = open ? e * r : r, hi = 1.0f - lo;   // (x = -inf: e = inf, r = 0)
   return {open ? hi : lo, open ? lo : hi};
 }
-
-// The cells of prn_decode_step: x the projected values [f | v] or [f | i | v].
-// They are not rounded to the storage type on the way.
-template <int G_>
-struct CellGated {
-  static constexpr int G = G_, S = 1;
-  static constexpr __host__ __device__ float scale(int) { return 1.0f; }
-  static __device__ __forceinline__ void f(const float* x, const float* s, const float* /*as*/, const float* /*a*/, float* out) {
-    const Gate f = gate_of(x[0]);
-    const float in = G == 2 ? f.off : gate_of(x[1]).on;
-    out[0] = fmaf(f.on, s[0], in * x[G - 1]);
-  }
-};
-
-// cells without recurrent weights, whose projected values stay in fp32
-template <class C> struct IsGated : std::false_type {};
-template <int G> struct IsGated<CellGated<G>> : std::true_type {};
 
 }  // namespace prn

@@ -14,13 +14,12 @@ struct GatedFfnArgs {
   hipStream_t stream;
 };
 
-// do the launches fit their grids?
+// do the launches fit their grids and offsets?
 bool gated_ffn_fits(const GatedFfnArgs& a);
 size_t gated_ffn_workspace(const GatedFfnArgs& a);
 void launch_gated_ffn(const GatedFfnArgs& a, const void* x, const void* W, void* out);
-// the workspace of the gradients of the sums, N x 2 F; dz_at: where in it they lie
-size_t gated_ffn_dz_workspace(const GatedFfnArgs& a, size_t* dz_at);
-// the gradients of the sums, [gate | up], from dout
-void launch_gated_ffn_dz(const GatedFfnArgs& a, const void* x, const void* W, const void* dout);
+// dx / dW may be null
+size_t gated_ffn_backward_workspace(const GatedFfnArgs& a);
+void launch_gated_ffn_backward(const GatedFfnArgs& a, const void* x, const void* W, const void* dout, void* dx, void* dW);
 
 }  // namespace prn

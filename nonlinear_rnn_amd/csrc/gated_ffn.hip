@@ -1,100 +1,570 @@
-// Gated feed-forward product, and the gradients of its sums.
+// Gated feed-forward product, and its gradients.
 //
 //   g = x Wg^T    u = x Wu^T    out = act(g) u        W = [Wg; Wu], 2 F x d
-//   dg = dout u act'(g)         du = dout act(g)      (dx = [dg | du] W, dW = [dg | du]^T x)
+//   dg = dout u act'(g)         du = dout act(g)      dx = [dg | du] W      dW = [dg | du]^T x
 //
-// One kernel has both products: a tile's columns are pairs of a gate and an up
-// row of W, so that the two sums of a pair meet in one lane's accumulators,
-// in fp32, and only the result is stored.  The backward pass forms the sums
-// again (4 N F d operations) instead of reading 2 N F stored values.
+// One kernel has both products: a tile of W is pairs of blocks of 32 rows, 32
+// gate rows and the 32 up rows of the same outputs, so that the two sums of an
+// output meet in one lane's accumulators, in fp32, and only the result is
+// stored.  The backward pass forms the sums again (4 N F d operations) instead
+// of reading 2 N F stored values, and stores dz = [dg | du], rounded once to
+// bf16 (dx and dW are sums over many of its entries, whose roundings meet at
+// random: their error against float64 goes from 0.0017 of their root mean
+// square, that of the result's own rounding, to 0.0023), with its columns in
+// the same pairs of blocks: 64 consecutive columns are 32 of dg and their 32
+// of du.
+//
+// bf16 products run on the tiles of mm_tile.h, 256 x 256 in persistent
+// workgroups, where there are enough of them; fewer tokens on the projection's
+// 128 x 128 tiles (proj.hip); fp32 on the projection's tiles as well.
 #include "gated_ffn.h"
 
 #include <algorithm>
+#include <type_traits>
 
+#include "gated_cell.h"
+#include "gated_few.h"
 #include "grid_rows.h"
+#include "mm_plan.h"
+#include "mm_tile.h"
+#include "prn_device.h"
 #include "proj.h"
 
 namespace prn {
 namespace {
 
-size_t up(size_t x) { return (x + 255) / 256 * 256; }
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+// 8 waves, 256 x 256, 128 KB; 8 waves, 256 x 192, 112 KB (mm_tile.h)
+using Big = MmTile<2, 4, 4, 2, 64, 2>;
+using Wide = MmTile<4, 2, 2, 3, 64, 2>;
 
-// A copy of rows of d values as rows of ldp, zeros past d; a thread per 16 bytes.
+// A copy of rows of d values as rows of ldp, zeros past d and past row R, of
+// Rp rows; parts of R rows each, one after the other.  A thread per 16 bytes.
 template <class T>
-__global__ void __launch_bounds__(256) k_ffn_pad(const T* __restrict__ in, int64_t R, int64_t d, int64_t ldp,
-                                                 T* __restrict__ out) {
+__global__ void __launch_bounds__(256) k_ffn_pad(const T* __restrict__ in, int64_t parts, int64_t R, int64_t Rp, int64_t d,
+                                                 int64_t ldp, T* __restrict__ out) {
   constexpr int V = 16 / sizeof(T);
   const int64_t C = ldp / V, i = block_in_rows() * 256 + threadIdx.x;
-  if (i >= R * C) return;
-  const int64_t r = i / C, c0 = (i - r * C) * V;
+  if (i >= parts * Rp * C) return;
+  const int64_t to = i / C, c0 = (i - to * C) * V, part = to / Rp, r = to - part * Rp;
+  const T* const from = in + (part * R + r) * d + c0;
   T v[V];
-  if (c0 + V <= d) {
-    __builtin_memcpy(v, in + r * d + c0, sizeof(v));   // aligned or not
+  if (r < R && c0 + V <= d) {
+    __builtin_memcpy(v, from, sizeof(v));   // aligned or not
   } else {
 #pragma unroll
-    for (int e = 0; e < V; ++e) v[e] = c0 + e < d ? in[r * d + c0 + e] : T(0);
+    for (int e = 0; e < V; ++e) v[e] = r < R && c0 + e < d ? from[e] : T(0);
   }
-  __builtin_memcpy(__builtin_assume_aligned(out + r * ldp + c0, 16), v, sizeof(v));
+  __builtin_memcpy(__builtin_assume_aligned(out + to * ldp + c0, 16), v, sizeof(v));
 }
 
-// rows of d that are no multiple of 16 bytes are laid out anew
-struct Plan {
-  bool pad;
-  int64_t ldp;
-  size_t x_off, w_off, end;
+// ---------------------------------------------------- blocks of values ----
+// A block of 32 x 32 values of the accumulators (lane l: column l % 32, a token;
+// value 4 q + e: row 8 q + 4 (l / 32) + e, an output) as bf16 in two registers
+// of 16 bytes a lane, as memory has them: register k, lane l: token 16 k + l / 4,
+// outputs 8 (l % 4) .. + 7, so that four lanes have 64 bytes of a token.  Swaps
+// of the wave's halves and quarters put eight outputs of a token into one lane,
+// a permutation of the lanes puts a token's four side by side; each is its own
+// inverse but the last.
+__device__ __forceinline__ int quarter(int c) { return c == 1 ? 2 : c == 2 ? 1 : c; }
+
+struct Packed {
+  mm_u32x4 o[2];
 };
-Plan plan_of(const GatedFfnArgs& a) {
+__device__ __forceinline__ Packed to_rows(const float (&v)[16]) {
+  const int l = threadIdx.x & 63, from = 4 * ((l >> 2) + 16 * quarter(l & 3));
+  uint32_t w[4][2];
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      typedef __attribute__((ext_vector_type(2))) __bf16 b2;
+      w[q][e] = __builtin_bit_cast(uint32_t, b2{static_cast<__bf16>(v[4 * q + 2 * e]), static_cast<__bf16>(v[4 * q + 2 * e + 1])});
+    }
+  Packed p;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const auto a = __builtin_amdgcn_permlane32_swap(w[0][e], w[1][e], false, false);
+    const auto b = __builtin_amdgcn_permlane32_swap(w[2][e], w[3][e], false, false);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const auto f = __builtin_amdgcn_permlane16_swap(a[h], b[h], false, false);
+      p.o[0][2 * h + e] = f[0];
+      p.o[1][2 * h + e] = f[1];
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) p.o[k][e] = __builtin_amdgcn_ds_bpermute(from, p.o[k][e]);
+  return p;
+}
+__device__ __forceinline__ void from_rows(Packed p, float (&v)[16]) {
+  const int l = threadIdx.x & 63, from = 4 * (4 * (l & 15) + quarter(l >> 4));
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) p.o[k][e] = __builtin_amdgcn_ds_bpermute(from, p.o[k][e]);
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    uint32_t a[2], b[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const auto f = __builtin_amdgcn_permlane16_swap(p.o[0][2 * h + e], p.o[1][2 * h + e], false, false);
+      a[h] = f[0];
+      b[h] = f[1];
+    }
+    const auto lo = __builtin_amdgcn_permlane32_swap(a[0], a[1], false, false);
+    const auto hi = __builtin_amdgcn_permlane32_swap(b[0], b[1], false, false);
+    const uint32_t w[4] = {lo[0], lo[1], hi[0], hi[1]};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      v[4 * q + 2 * e] = __uint_as_float(w[q] << 16);
+      v[4 * q + 2 * e + 1] = __uint_as_float(w[q] & 0xffff0000u);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- sums ----
+
+// The tiles of g and u, 128 outputs x 256 tokens each; out (N x F), or with BACK
+// dz (N x 2 Fp in pairs of blocks, rows ldz apart, zeros past F).  W has Fw gate
+// rows, then Fw up rows.  A group of 8 tiles of outputs by all tokens, walked
+// down the outputs first, is a share of an XCD, whose L2 then holds the group's
+// W.  (32768 x 512 x 2048: 152 us, dz 186; two workgroups a CU of 256 x 128, one's
+// products under the other's epilogue: 158 and 197.)
+template <class Tl, bool BACK>
+__global__ void __launch_bounds__(Tl::NTHR, 2) k_ffn_sums(MmOperand W, MmOperand X, int64_t N, int64_t F, int64_t Fw, int64_t K,
+                                                          bool silu, const uint16_t* __restrict__ dout,
+                                                          uint16_t* __restrict__ out, int64_t ldo) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[Tl::LDS];
+  static_assert(Tl::WM % 2 == 0, "pairs of blocks");
+  constexpr int kPairs = Tl::BM / 2;   // outputs of a tile
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wr = wave / Tl::WC, wc = wave % Tl::WC;
+  const uint32_t f_tiles = static_cast<uint32_t>((F + kPairs - 1) / kPairs), n_tok = static_cast<uint32_t>((N + Tl::BN - 1) / Tl::BN);
+  constexpr uint32_t kGroup = 8;
+  Tl tile;
+  tile.open(lds, W, 2 * Fw, X, N, 0, K);
+  Units lu(f_tiles * n_tok), cu(lu);
+  auto go_to = [&]() {
+    uint32_t ft, tok;
+    tile_of(lu.u, f_tiles, n_tok, kGroup, ft, tok);
+    const int64_t f0 = static_cast<int64_t>(ft) * kPairs, n0 = static_cast<int64_t>(tok) * Tl::BN;
+    tile.template seek<false, false>(0, n0);
+    tile.ab = reinterpret_cast<const uint8_t*>(W.base + f0 * W.ld);
+    const int lim = static_cast<int>(imin(Fw - 1 - f0, kPairs));
+#pragma unroll
+    for (int p = 0; p < Tl::NLA; ++p) {   // rows in pairs of blocks; past the last output, the last one's
+      int s, f;
+      Tl::template source<false, Tl::BM>(wave * Tl::NLA + p, lane, s, f);
+      const int row = min((s >> 6) * 32 + (s & 31), lim);
+      tile.offa[p] = static_cast<uint32_t>((((s >> 5) & 1) * Fw + row) * W.ld + f) * 2;
+    }
+  };
+  auto next = [&]() {
+    lu.advance();
+    if (lu.valid()) go_to();
+  };
+  if (!lu.valid()) return;
+  go_to();
+  tile.template prime<false, false>(next);
+  constexpr int kStores = Tl::WN * Tl::WM * (BACK ? 2 : 1);   // of a wave and whole tile
+  bool whole = false;   // the tile before was
+  for (; cu.valid(); cu.advance()) {
+    uint32_t ft, tok;
+    tile_of(cu.u, f_tiles, n_tok, kGroup, ft, tok);
+    const int64_t f0 = static_cast<int64_t>(ft) * kPairs, n0 = static_cast<int64_t>(tok) * Tl::BN;
+    tile.template multiply<false, false, false, false, kStores>(next, whole);
+    const int f_left = static_cast<int>(imin(F - f0, kPairs)), toks = static_cast<int>(imin(N - n0, Tl::BN));
+    // opaque, so that what follows from it is not kept in registers over the tiles
+    int el = lane;
+    asm volatile("" : "+v"(el));
+    const int fe = 8 * (el & 3), te = el >> 2;   // this lane's place in a block as memory has it
+    auto finish = [&](auto edge) {
+      constexpr bool EDGE = decltype(edge)::value;
+#pragma unroll
+      for (int j = 0; j < Tl::WN; ++j) {
+        const int t0 = (wc * Tl::WN + j) * 32 + te;
+        Packed dp[Tl::WM / 2];
+        if constexpr (BACK) {   // all of dout before the first use
+#pragma unroll
+          for (int i = 0; i < Tl::WM / 2; ++i) {
+            const int fb = (wr * (Tl::WM / 2) + i) * 32 + fe;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int t = t0 + 16 * k;
+              const uint16_t* const at = dout + (n0 + t) * F + f0 + fb;
+              if (!EDGE || (t < toks && fb + 8 <= f_left)) {
+                __builtin_memcpy(&dp[i].o[k], at, 16);   // aligned or not
+              } else {
+                uint16_t e8[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) e8[e] = t < toks && fb + e < f_left ? at[e] : uint16_t(0);
+                __builtin_memcpy(&dp[i].o[k], e8, 16);
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < Tl::WM / 2; ++i) {
+          const int fb = (wr * (Tl::WM / 2) + i) * 32;
+          const mm_f32x16 g = tile.acc[2 * i][j], u = tile.acc[2 * i + 1][j];
+          float a[16], b[16];
+          if constexpr (BACK) {
+            from_rows(dp[i], a);
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+              const float e = ex2(-kLog2e * g[r]), on = rcp(1.0f + e), off = e < __builtin_inff() ? e * on : 1.0f;
+              const float d = a[r], value = silu ? g[r] * on : on;
+              const float slope = silu ? on * fmaf(g[r], off, 1.0f) : on * off;
+              a[r] = d * u[r] * slope;
+              b[r] = d * value;
+            }
+            if (EDGE && fb + 32 > f_left) {   // dx sums over these columns
+              const int rest = f_left - fb - 4 * (el >> 5);
+#pragma unroll
+              for (int r = 0; r < 16; ++r)
+                if (8 * (r >> 2) + (r & 3) >= rest) a[r] = b[r] = 0.0f;
+            }
+          } else {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+              const float s = rcp(1.0f + ex2(-kLog2e * g[r]));
+              a[r] = (silu ? g[r] * s : s) * u[r];
+            }
+          }
+          if (EDGE && fb >= f_left) continue;
+          const Packed pa = to_rows(a), pb = BACK ? to_rows(b) : pa;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int t = t0 + 16 * k;
+            if (EDGE && t >= toks) continue;
+            if constexpr (BACK) {
+              uint16_t* const to = out + (n0 + t) * ldo + 2 * (f0 + fb) + fe;
+              gstore(reinterpret_cast<mm_u32x4*>(to), pa.o[k]);
+              gstore(reinterpret_cast<mm_u32x4*>(to + 32), pb.o[k]);
+            } else {
+              uint16_t* const to = out + (n0 + t) * ldo + f0 + fb + fe;
+              if (!EDGE || fb + fe + 8 <= f_left) {
+                __builtin_memcpy(to, &pa.o[k], 16);   // aligned or not
+              } else {
+                uint16_t e8[8];
+                __builtin_memcpy(e8, &pa.o[k], 16);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                  if (fb + fe + e < f_left) to[e] = e8[e];
+              }
+            }
+          }
+        }
+      }
+    };
+    whole = f_left == kPairs && toks == Tl::BN;
+    if (whole) finish(std::false_type{}); else finish(std::true_type{});
+  }
+}
+
+// ----------------------------------------------------------- dx and dW ----
+
+// P[z][r][c] = sum over k of slice z of A(r, k) B(c, k), fp32, C columns, or with
+// `out` the sums rounded once.  TA: dW, A(r, k) = dz(k, r), the rows r in pairs
+// of blocks: of `out`, row (r / 32 % 2) F + r / 64 * 32 + r % 32, if below F in
+// its half.  Otherwise dx, k in pairs of blocks: B's rows (W) are half a stage
+// of 64 from the gate's, half from the up rows Fw further on.  One workgroup per
+// tile and slice, neighbours on one XCD.
+template <class Tl, bool TA>
+__global__ void __launch_bounds__(Tl::NTHR, 2) k_ffn_mm(MmOperand A, MmOperand B, int64_t R, int64_t C, int64_t K, int64_t k_slice,
+                                                        int n_col, int slices, int64_t F, int64_t Fw, int64_t row0,
+                                                        float* __restrict__ P, uint16_t* __restrict__ out) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[Tl::LDS];
+  const uint32_t u = Units(gridDim.x).u, tiles = gridDim.x / slices, z = u / tiles, ti = u - z * tiles;
+  const int64_t c0 = static_cast<int64_t>(ti % n_col) * Tl::BN, r0 = static_cast<int64_t>(ti / n_col) * Tl::BM;
+  const int64_t k0 = static_cast<int64_t>(z) * k_slice, k1 = imin(k0 + k_slice, K);
+  const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, l32 = lane & 31;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wr = wave / Tl::WC, wc = wave % Tl::WC;
+  Tl tile;
+  tile.open(lds, A, R, B, C, k0, k1);
+  auto next = []() {};
+  tile.template seek<TA, true>(r0, c0);
+  if constexpr (!TA) {
+    static_assert(Tl::KS == 64, "a stage is a pair of blocks");
+    tile.bb = reinterpret_cast<const uint8_t*>(B.base + k0 / 2 * B.ld + c0);
+#pragma unroll
+    for (int p = 0; p < Tl::NLB; ++p) {
+      int s, f;
+      Tl::template source<true, Tl::BN>(wave * Tl::NLB + p, lane, s, f);
+      if (s >= 32) tile.offb[p] += static_cast<uint32_t>((Fw - 32) * B.ld * 2);
+    }
+    tile.B.ld = B.ld / 2;   // a stage goes on by 32 rows of either half
+  }
+  tile.clear();
+  tile.template prime<TA, true>(next);
+  tile.template multiply<TA, true>(next);
+  const int rows = static_cast<int>(imin(R - r0, Tl::BM)), cols = static_cast<int>(imin(C - c0, Tl::BN));
+  const int rl = wr * Tl::WM * 32 + 4 * half, cl = wc * Tl::WN * 32 + l32;
+#pragma unroll
+  for (int i = 0; i < Tl::WM; ++i) {
+    // the block's first row of `out`, and how many of its rows are there
+    const int64_t rb = row0 + r0 + (wr * Tl::WM + i) * 32, f = rb / 64 * 32;
+    const int64_t ob = TA ? ((rb >> 5) & 1) * F + f : rb;
+    const int there = TA ? static_cast<int>(imin(F - f, 32)) : 32;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const int ri = 8 * (r >> 2) + (r & 3);
+#pragma unroll
+      for (int j = 0; j < Tl::WN; ++j) {
+        if (rl + 32 * i + ri >= rows || cl + 32 * j >= cols) continue;
+        if (out) {
+          if (4 * half + ri < there)
+            out[(ob + 4 * half + ri) * C + c0 + cl + 32 * j] = Storage<kBF16>::pack(tile.acc[i][j][r]);
+        } else {
+          P[(z * R + r0 + rl + 32 * i + ri) * C + c0 + cl + 32 * j] = tile.acc[i][j][r];
+        }
+      }
+    }
+  }
+}
+
+// out = the sum over z, in order, of P[z], rounded once; dW's rows as in k_ffn_mm
+template <bool IS_W>
+__global__ void __launch_bounds__(256) k_ffn_join(const float* __restrict__ P, int S, int64_t R, int64_t C, int64_t F,
+                                                  int64_t row0, uint16_t* __restrict__ out) {
+  const int64_t i = block_in_rows() * 256 + threadIdx.x, n = R * C;
+  if (i >= n) return;
+  const int64_t r = i / C, c = i - r * C, rb = row0 + r, f = rb / 64 * 32 + rb % 32;
+  if (IS_W && f >= F) return;
+  float sum = 0.0f;
+  for (int z = 0; z < S; ++z) sum += P[z * n + i];
+  out[(IS_W ? ((rb >> 5) & 1) * F + f : rb) * C + c] = Storage<kBF16>::pack(sum);
+}
+
+// zeros in columns c0 .. of rows of ld values
+template <class T>
+__global__ void __launch_bounds__(256) k_ffn_zero(T* __restrict__ out, int64_t R, int64_t c0, int64_t ld) {
+  const int64_t i = block_in_rows() * 256 + threadIdx.x, w = ld - c0, r = i / w;
+  if (r < R) out[r * ld + c0 + i - r * w] = T(0);
+}
+
+// ---------------------------------------------------------------- plan ----
+
+size_t up(size_t x) { return (x + 255) / 256 * 256; }
+
+// Few rows are gated_few.hip's: as many of its workgroups of 64 rows and 16 outputs
+// as one round of the device takes (bf16) or two (fp32, which takes the
+// projection's tiles longer).  us, few and the tiles: 65 x 512 x 1408 bf16 6.8 and
+// 10.0; 65 x 1024 x 4096 bf16 18 and 15; 256 x 512 x 1408 fp32 20 and 25.
+bool few_rows(const GatedFfnArgs& a) { return cdiv(a.N, 64) * cdiv(a.F, 16) <= (a.bf16 ? kCus : 2 * kCus); }
+
+// The 256 x 256 tiles where at least 128 of them keep the device busy: below, the
+// projection's quarter tiles.
+bool big_tiles(const GatedFfnArgs& a) { return a.bf16 && cdiv(a.N, Big::BN) * cdiv(a.F, Big::BM / 2) >= 128; }
+
+struct Plan {
+  bool tiles;             // of mm_tile.h
+  bool pad_x, pad_w;      // x and W laid out anew: rows that are no multiple of 16 bytes; for dx W's halves of Fw rows
+  int64_t ldp, Fw;
+  size_t x_off, w_off;
+  // backward
+  int64_t Fp, ldz;        // dz: columns of either kind, elements from row to row
+  int64_t cols;           // tile columns of dx and dW
+  Cut x, w;               // of their sums
+  bool tn;
+  size_t z_off, px_off, pw_off, wt_off, zt_off, xt_off, total;
+};
+
+Plan plan_of(const GatedFfnArgs& a, bool back) {
   Plan p{};
   const int64_t vec = a.bf16 ? 8 : 4, elt = a.bf16 ? 2 : 4;
-  p.pad = a.d % vec != 0;
+  p.tiles = big_tiles(a);
   p.ldp = cdiv(a.d, vec) * vec;
-  if (p.pad) {
-    p.w_off = up(size_t(a.N) * p.ldp * elt);
-    p.end = p.w_off + up(size_t(2 * a.F) * p.ldp * elt);
+  p.Fp = cdiv(a.F, 32) * 32;
+  p.pad_x = a.d != p.ldp;
+  p.pad_w = p.pad_x || (back && p.tiles && a.F != p.Fp);
+  p.Fw = back && p.tiles ? p.Fp : a.F;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off += up(bytes);
+    return at;
+  };
+  if (p.pad_x) p.x_off = take(size_t(a.N) * p.ldp * elt);
+  if (p.pad_w) p.w_off = take(size_t(2) * p.Fw * p.ldp * elt);
+  if (back && p.tiles) {
+    p.ldz = 2 * p.Fp + 64;   // rows are no power of two apart: they would fall on few memory channels
+    double best = -1;
+    for (int64_t bn : {int64_t(Big::BN), int64_t(Wide::BN)}) {
+      double tx, tw;
+      const Cut x = cut_of(a.N, 2 * p.Fp, a.d, 1, bn, &tx), w = cut_of(2 * p.Fp, a.N, a.d, 1, bn, &tw);
+      if (best >= 0 && tx + tw >= best) continue;
+      best = tx + tw;
+      p.cols = bn, p.x = x, p.w = w;
+    }
+    auto sums = [&](int64_t rows, const Cut& c) { return c.s > 1 ? size_t(c.s) * (rows - c.head) * a.d * 4 : 0; };
+    p.z_off = take(size_t(a.N) * p.ldz * 2);
+    p.px_off = take(sums(a.N, p.x));
+    p.pw_off = take(sums(2 * p.Fp, p.w));
+  } else if (back) {
+    // The projection's tiles take operands in rows of the summed index.  A sum is
+    // cut into slices where there are too few tiles for the device, of equal
+    // length where half as many slices allow it (what is left over is zeros).
+    auto cut = [&](int64_t rows, int64_t cols, int64_t K, Cut& c) {
+      const int64_t want = std::max<int64_t>(1, std::min<int64_t>({cdiv(512, cdiv(rows, 128) * cdiv(cols, 128)), K / 128, 64}));
+      for (int64_t n = want; n >= (want + 1) / 2; --n)
+        if (K % (n * vec) == 0) {
+          c.s = n, c.len = K / n;
+          return;
+        }
+      c.len = want > 1 ? cdiv(cdiv(K, want), 64) * 64 : cdiv(K, vec) * vec;
+      c.s = cdiv(K, c.len);
+    };
+    cut(a.N, a.d, 2 * a.F, p.x);
+    p.ldz = p.x.s * p.x.len;
+    p.z_off = take(size_t(a.N) * p.ldz * elt);
+    p.wt_off = take(size_t(a.d) * p.ldz * elt);
+    p.tn = 2 * a.F % 256 == 0 && a.d % 256 == 0;   // or both operands of dW in rows of their own
+    if (p.tn) {
+      const int64_t s = std::max<int64_t>(1, std::min<int64_t>(kCus / ((2 * a.F / 256) * (a.d / 256)), cdiv(a.N, 256)));
+      p.w.len = cdiv(cdiv(a.N, s), 256) * 256;
+      p.w.s = cdiv(a.N, p.w.len);
+    } else {
+      cut(2 * a.F, a.d, a.N, p.w);
+      p.zt_off = take(size_t(2) * a.F * p.w.s * p.w.len * elt);
+      p.xt_off = take(size_t(a.d) * p.w.s * p.w.len * elt);
+    }
+    p.px_off = take(p.x.s > 1 ? size_t(p.x.s) * a.N * a.d * 4 : 0);
+    p.pw_off = take(p.tn || p.w.s > 1 ? size_t(p.w.s) * 2 * a.F * a.d * 4 : 0);
   }
+  p.total = off;
   return p;
 }
 
-void product(const GatedFfnArgs& a, const Plan& p, const void* x, const void* W, const void* dout, void* out) {
-  auto padded = [&](const void* in, int64_t R, size_t off) {
+struct Operands {
+  const void *x, *W;
+};
+Operands lay_out(const GatedFfnArgs& a, const Plan& p, const void* x, const void* W) {
+  auto pad = [&](const void* in, int64_t parts, int64_t R, int64_t Rp, size_t off) {
     void* const to = a.ws + off;
-    const dim3 grid = rows_of_blocks(cdiv(R * (p.ldp / (a.bf16 ? 8 : 4)), 256));
+    const dim3 grid = rows_of_blocks(cdiv(parts * Rp * (p.ldp / (a.bf16 ? 8 : 4)), 256));
     if (a.bf16)
-      k_ffn_pad<uint16_t><<<grid, 256, 0, a.stream>>>(static_cast<const uint16_t*>(in), R, a.d, p.ldp, static_cast<uint16_t*>(to));
+      k_ffn_pad<uint16_t><<<grid, 256, 0, a.stream>>>(static_cast<const uint16_t*>(in), parts, R, Rp, a.d, p.ldp, static_cast<uint16_t*>(to));
     else
-      k_ffn_pad<float><<<grid, 256, 0, a.stream>>>(static_cast<const float*>(in), R, a.d, p.ldp, static_cast<float*>(to));
+      k_ffn_pad<float><<<grid, 256, 0, a.stream>>>(static_cast<const float*>(in), parts, R, Rp, a.d, p.ldp, static_cast<float*>(to));
     return to;
   };
-  if (p.pad) {
-    x = padded(x, a.N, p.x_off);
-    W = padded(W, 2 * a.F, p.w_off);
+  return {p.pad_x ? pad(x, 1, a.N, a.N, p.x_off) : x, p.pad_w ? pad(W, 2, a.F, p.Fw, p.w_off) : W};
+}
+
+void fill_zero(const GatedFfnArgs& a, void* out, int64_t R, int64_t c0, int64_t ld) {
+  const dim3 grid = rows_of_blocks(cdiv(R * (ld - c0), 256));
+  if (a.bf16)
+    k_ffn_zero<uint16_t><<<grid, 256, 0, a.stream>>>(static_cast<uint16_t*>(out), R, c0, ld);
+  else
+    k_ffn_zero<float><<<grid, 256, 0, a.stream>>>(static_cast<float*>(out), R, c0, ld);
+}
+
+// out, or with dout dz
+void sums(const GatedFfnArgs& a, const Plan& p, const Operands& o, const void* dout, void* out, int64_t ldo) {
+  if (!p.tiles) {
+    launch_proj_gated(a.bf16, o.x, o.W, out, a.N, p.ldp, GatedProj{dout, a.F, dout ? ldo : 0, a.silu}, a.stream);
+    return;
   }
-  launch_proj_gated(a.bf16, x, W, out, a.N, p.ldp, GatedProj{dout, a.F, a.silu}, a.stream);
+  const MmOperand W{static_cast<const uint16_t*>(o.W), p.ldp}, X{static_cast<const uint16_t*>(o.x), p.ldp};
+  const unsigned grid = unsigned(std::min(cdiv(a.N, Big::BN) * cdiv(a.F, Big::BM / 2), kCus));
+  auto go = [&](auto back) {
+    k_ffn_sums<Big, decltype(back)::value><<<grid, Big::NTHR, 0, a.stream>>>(
+        W, X, a.N, a.F, p.Fw, p.ldp, a.silu, static_cast<const uint16_t*>(dout), static_cast<uint16_t*>(out), ldo);
+  };
+  if (dout) go(std::true_type{}); else go(std::false_type{});
 }
 
 }  // namespace
 
 bool gated_ffn_fits(const GatedFfnArgs& a) {
-  // tiles of 128 x 128, 256 threads each, below 2^32 threads
-  return double(cdiv(a.N, 128)) * double(cdiv(a.F, 64)) < double(1 << 24) && 2.0 * double(a.F) * double(a.d) < 4294967296.0;
+  const double N = double(a.N), d = double(a.d), F = double(a.F), most = double(1 << 22);
+  // byte offsets into W of 32 bits; launches below 2^32 threads, also with tiles of 128 x 128
+  return 2 * (F + 256) * (d + 64) < 2147483648.0 && (N / 256 + 1) * (F / 128 + 1) < most && (N / 256 + 1) * (d / 128 + 1) < most;
 }
 
-size_t gated_ffn_workspace(const GatedFfnArgs& a) { return a.N ? plan_of(a).end : 0; }
+size_t gated_ffn_workspace(const GatedFfnArgs& a) { return a.N == 0 || few_rows(a) ? 0 : plan_of(a, false).total; }
 
 void launch_gated_ffn(const GatedFfnArgs& a, const void* x, const void* W, void* out) {
-  product(a, plan_of(a), x, W, nullptr, out);
+  if (few_rows(a)) {
+    launch_few_ffn(GatedFewArgs{a.bf16, a.N, a.F, a.d, x, W, a.stream}, a.silu, out);
+    return;
+  }
+  const Plan p = plan_of(a, false);
+  sums(a, p, lay_out(a, p, x, W), nullptr, out, a.F);
 }
 
-size_t gated_ffn_dz_workspace(const GatedFfnArgs& a, size_t* dz_at) {
-  const Plan p = plan_of(a);
-  *dz_at = p.end;
-  return p.end + up(size_t(a.N) * 2 * a.F * (a.bf16 ? 2 : 4));
-}
+size_t gated_ffn_backward_workspace(const GatedFfnArgs& a) { return a.N ? plan_of(a, true).total : 0; }
 
-void launch_gated_ffn_dz(const GatedFfnArgs& a, const void* x, const void* W, const void* dout) {
-  const Plan p = plan_of(a);
-  product(a, p, x, W, dout, a.ws + p.end);
+void launch_gated_ffn_backward(const GatedFfnArgs& a, const void* x, const void* W, const void* dout, void* dx, void* dW) {
+  if (a.N == 0) {   // no row: dW is zero
+    if (dW) fill_zero(a, dW, 1, 0, 2 * a.F * a.d);
+    return;
+  }
+  const Plan p = plan_of(a, true);
+  const Operands o = lay_out(a, p, x, W);
+  void* const dz = a.ws + p.z_off;
+  float *const px = reinterpret_cast<float*>(a.ws + p.px_off), *const pw = reinterpret_cast<float*>(a.ws + p.pw_off);
+  sums(a, p, o, dout, dz, p.ldz);
+  if (!p.tiles) {
+    const int64_t elt = a.bf16 ? 2 : 4, Z = 2 * a.F;
+    if (dx && p.ldz > Z) fill_zero(a, dz, a.N, Z, p.ldz);
+    if (dx) {
+      void* const wt = a.ws + p.wt_off;
+      launch_transpose(a.bf16, W, Z, a.d, a.d, wt, p.ldz, nullptr, a.stream);
+      if (p.x.s > 1) {
+        launch_proj_splitk(a.bf16, dz, p.ldz * elt, wt, p.ldz * elt, px, a.N, a.d, p.x.len, int(p.x.s), a.stream);
+        launch_splitk_sum(a.bf16, px, int(p.x.s), a.N * a.d, dx, a.stream);
+      } else {
+        launch_proj_ld(a.bf16, dz, p.ldz * elt, wt, p.ldz * elt, dx, a.N, a.d, p.x.len, a.stream);
+      }
+    }
+    if (dW && p.tn) {
+      launch_proj_tn(a.bf16, dz, p.ldz * elt, x, a.d * elt, pw, a.N, Z, a.d, p.w.len, int(p.w.s), nullptr, a.stream);
+      launch_splitk_sum(a.bf16, pw, int(p.w.s), Z * a.d, dW, a.stream);
+    } else if (dW) {
+      void *const zt = a.ws + p.zt_off, *const xt = a.ws + p.xt_off;
+      const int64_t ld = p.w.s * p.w.len;
+      launch_transpose(a.bf16, dz, a.N, Z, p.ldz, zt, ld, nullptr, a.stream);
+      launch_transpose(a.bf16, x, a.N, a.d, a.d, xt, ld, nullptr, a.stream);
+      if (p.w.s > 1) {
+        launch_proj_splitk(a.bf16, zt, ld * elt, xt, ld * elt, pw, Z, a.d, p.w.len, int(p.w.s), a.stream);
+        launch_splitk_sum(a.bf16, pw, int(p.w.s), Z * a.d, dW, a.stream);
+      } else {
+        launch_proj_ld(a.bf16, zt, ld * elt, xt, ld * elt, dW, Z, a.d, ld, a.stream);
+      }
+    }
+    return;
+  }
+  const MmOperand Z{static_cast<const uint16_t*>(dz), p.ldz}, X{static_cast<const uint16_t*>(o.x), p.ldp},
+      Wo{static_cast<const uint16_t*>(o.W), p.ldp};
+  // the head's rows, then the rest
+  auto product = [&](auto ta, const Cut& c, const MmOperand& B, int64_t rows, int64_t K, float* P, void* to) {
+    constexpr bool TA = decltype(ta)::value;
+    uint16_t* const out = static_cast<uint16_t*>(to);
+    auto part = [&](int64_t r0, int64_t n, int64_t s, int64_t len) {
+      if (n <= 0) return;
+      MmOperand A = Z;
+      A.base += r0 * (TA ? 1 : p.ldz);
+      auto run = [&](auto tl) {
+        using Tl = decltype(tl);
+        const int64_t n_col = cdiv(a.d, Tl::BN);
+        k_ffn_mm<Tl, TA><<<unsigned(cdiv(n, Tl::BM) * n_col * s), Tl::NTHR, 0, a.stream>>>(
+            A, B, n, a.d, K, len, int(n_col), int(s), a.F, p.Fw, r0, P, s == 1 ? out : nullptr);
+      };
+      if (p.cols == Big::BN) run(Big{}); else run(Wide{});
+      if (s > 1) k_ffn_join<TA><<<rows_of_blocks(cdiv(n * a.d, 256)), 256, 0, a.stream>>>(P, int(s), n, a.d, a.F, r0, out);
+    };
+    const int64_t head = std::min(c.head, rows);
+    part(0, head, 1, cdiv(K, 64) * 64);
+    part(head, rows - head, c.s, c.len);
+  };
+  if (dx) product(std::false_type{}, p.x, Wo, a.N, 2 * p.Fp, px, dx);
+  if (dW) product(std::true_type{}, p.w, X, 2 * p.Fp, a.N, pw, dW);
 }
 
 }  // namespace prn

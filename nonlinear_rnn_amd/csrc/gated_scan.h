@@ -18,10 +18,14 @@ struct GatedScanArgs {
   // backward (H is read)
   const void *dH, *dlast;    // dlast may be null
   void *dxproj, *dh0;        // dh0 may be null
+  unsigned* error;           // device word for a wait that gave up, or null
+  unsigned spin_limit;       // polls after which one does
   uint8_t* ws;
   hipStream_t stream;
 };
 
+// does the launch fit one grid?
+bool gated_scan_fits(const GatedScanArgs& a);
 size_t gated_scan_workspace(const GatedScanArgs& a);
 void launch_gated_scan(const GatedScanArgs& a);
 size_t gated_scan_backward_workspace(const GatedScanArgs& a);

@@ -8,25 +8,23 @@
 // Every step is an affine map of the state, per channel, so a stretch of time
 // is one too: (a, b) with h_out = a h_in + b.  Backwards, with m_t the gradient
 // that arrives at h_t from the steps after it, m_{t-1} = f_t (dH_t + m_t) is
-// another.  A chain is one row and 64 V channels (a lane has V of them).
+// another.  A chain is one row and 64 V channels (a lane has V of them).  A
+// workgroup has a chunk of its chain, NW waves x LS steps, LS a wave, in
+// registers: every wave takes the map of its steps, the maps meet in LDS, and
+// each wave walks its steps from its own carry.  Every value is read and
+// written once.
 //
-//   k_scan_map    where there are fewer chains than the device takes, time is
-//                 cut in ranges and the map of each range is taken first
-//   k_scan_walk   a workgroup walks its range in chunks of kWaves x kSteps
-//                 steps, kSteps a wave: every wave takes the map of its steps
-//                 (held in registers), the maps meet in LDS, and each wave
-//                 walks its steps from its own carry.  The next chunk's loads
-//                 are in flight meanwhile.  The range's own carry is the maps
-//                 of the ranges before it, applied to h0.
-//
-// Nothing waits for another workgroup, no memory has to be cleared first, and
-// every sum has a fixed order.  The walk reads and writes each value once; the
-// maps read the gates (and v or dH) once more, of which up to 256 MB come from
-// the memory-side cache.  Bound: memory traffic.
+//   k_scan_walk   where there are chains enough for the device: a workgroup
+//                 walks its chain chunk after chunk, the next one's loads under
+//                 way meanwhile.
+//   k_scan_pass   else: chunks run side by side and get the state before them
+//                 from the chunks before (look_back).
+// and the same two backwards.  Bound: memory traffic (long chains: the look-back
+// besides).
 //
 // The gradient needs h_{t-1}: it is formed again from x and the stored H of
-// the step before a chunk (so only one step in kWaves kSteps sees H's
-// rounding), which reads a value per step less than stored states would.
+// the step before a chunk (so only one step of a chunk sees H's rounding),
+// which reads a value per step less than stored states would.
 //
 // A sequence's first step in a pack cuts the map: h_in does not count, whatever
 // it is (a NaN of the sequence before stays there).  Since a >= 0 otherwise,
@@ -43,8 +41,6 @@
 namespace prn {
 namespace {
 
-constexpr int kWaves = 8, kSteps = 8;    // of a workgroup, of a wave and chunk
-constexpr int kChunk = kWaves * kSteps;
 constexpr float kCut = -0.0f;
 
 __device__ __forceinline__ bool is_cut(float a) { return __float_as_uint(a) == 0x80000000u; }
@@ -76,16 +72,17 @@ struct Chans {
 
 // Where the sequences of a pack begin and end among a wave's steps: bit j of
 // head / tail, and the sequence of step j.
+template <int LS>
 struct Cuts {
   uint32_t head, tail;
-  int32_t seg[kSteps];
+  int32_t seg[LS];
   __device__ __forceinline__ void find(const int32_t* cu, int64_t n_seqs, int64_t t0, int n, int64_t T) {
     head = tail = 0;
     if (n <= 0) return;
     SegTracker s;
     s.init_wave(cu, n_seqs, 0, t0);
 #pragma unroll
-    for (int j = 0; j < kSteps; ++j) {
+    for (int j = 0; j < LS; ++j) {
       if (j < n) {
         if (s.at(t0 + j)) head |= 1u << j;
         if (s.last(t0 + j, T)) tail |= 1u << j;
@@ -95,363 +92,441 @@ struct Cuts {
   }
 };
 
-// A workgroup's place: chain (row, channel tile) and range of time.
+// the tensors of a call, and its sizes
+template <int DT>
+struct Tensors {
+  using T = typename Storage<DT>::T;
+  const T *x, *h0, *dH, *dlast;
+  T *H, *last, *dx, *dh0;
+  const int32_t* cu;
+  int64_t n_seqs, B, T_, d;
+  int64_t chains, chunks;
+};
+
+// ------------------------------------------------------------ look-back ----
+
+// Chunk c of a chain publishes its map, and, once it has the state before it,
+// the state after it.  Its own carry is defined one chunk after another, E(c + 1)
+// = map_c(E(c)); a chunk that finds the state after an earlier chunk p behind
+// an unbroken run of published maps takes it through map_{p+1} .. map_{c-1} in
+// that order: the same operations, so the bits do not depend on which state it
+// found.  Workgroups take their chunks by ticket, the chunks of a chain in the
+// order of its walk, so a chunk waits for chunks with smaller tickets only,
+// which have started.  Every wait ends: after spin_limit polls without progress
+// the carry is NaN, the error word is set, and the chunk goes on.
+//
+// A record's words are written and read at the device's coherence point (relaxed
+// atomics of agent scope); a wave's stores have been acknowledged before it
+// stores the status that announces them, and a reader loads them after it has
+// the status.
+struct Records {
+  unsigned* ticket;
+  unsigned* error;
+  unsigned* status;   // [chain][chunk]: kNone, kMap, kState
+  float* maps;        // [chain][chunk][a, b][V][64]
+  float* states;      // [chain][chunk][V][64]
+};
+constexpr unsigned kNone = 0, kMap = 1, kState = 2;
+
+__device__ __forceinline__ void put(float* p, float v) { __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+__device__ __forceinline__ float get(const float* p) {
+  return __hip_atomic_load(const_cast<float*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void announce(unsigned* status, unsigned v, int lane) {
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  if (lane == 0) __hip_atomic_store(status, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// the state before chunk c > 0 of the chain whose records begin at `base`, by a whole wave
+template <int V>
+__device__ __forceinline__ void look_back(const Records& rec, int64_t base, int64_t c, const Map (&own)[V], int lane,
+                                          unsigned spin_limit, bool map_first, float (&e)[V]) {
+  constexpr int kAhead = 16 / V;   // maps under way at once
+  float* const mine = rec.maps + (base + c) * 2 * V * 64 + lane;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    put(mine + v * 64, own[v].a);
+    put(mine + (V + v) * 64, own[v].b);
+  }
+  bool announced = false;
+  unsigned spins = 0;
+  int64_t at = c - 1;   // lane i looks at chunk at - i
+  while (true) {
+    if (spins >= spin_limit) {
+      if (lane == 0) atomicOr(rec.error, 1u);
+      if (!announced) announce(rec.status + base + c, kMap, lane);
+#pragma unroll
+      for (int v = 0; v < V; ++v) e[v] = __builtin_nanf("");
+      return;
+    }
+    const int64_t j = at - lane;
+    const unsigned st =
+        j >= 0 ? __hip_atomic_load(rec.status + base + j, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : kNone;
+    const unsigned long long there = __ballot(st != kNone), state = __ballot(st == kState);
+    const int run = ~there ? __builtin_ctzll(~there) : 64, first = state ? __builtin_ctzll(state) : 64;
+    const bool hit = first < run;
+    // (the poll's wait has covered the stores of the map)
+    if ((map_first || !hit) && !announced) {
+      announce(rec.status + base + c, kMap, lane);
+      announced = true;
+    }
+    if (hit) {
+      const int64_t p = at - first;
+      const int n = static_cast<int>(c - 1 - p);
+      const float* const from = rec.states + (base + p) * V * 64 + lane;
+#pragma unroll
+      for (int v = 0; v < V; ++v) e[v] = get(from + v * 64);
+      for (int r = 0; r < n; r += kAhead) {
+        Map m[kAhead][V];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const float* const q = rec.maps + (base + p + 1 + min(r + k, n - 1)) * 2 * V * 64 + lane;
+#pragma unroll
+          for (int v = 0; v < V; ++v) m[k][v] = {get(q + v * 64), get(q + (V + v) * 64)};
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+          if (r + k < n) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) e[v] = through(m[k][v], e[v]);
+          }
+      }
+      return;
+    }
+    if (run == 64) {   // maps only: look further back
+      at -= 64;
+      continue;
+    }
+    ++spins;
+    __builtin_amdgcn_s_sleep(1);
+  }
+}
+
+// clears the words that a call's records begin with
+__global__ void __launch_bounds__(256) k_scan_clear(unsigned* __restrict__ words, int64_t n) {
+  const int64_t i = block_in_rows() * 256 + threadIdx.x;
+  if (i < n) words[i] = 0;
+}
+
+// A workgroup's place: its lane's channels and its wave's steps are of chain
+// (row, tile of channels).
 template <int V>
 struct Place {
   int lane, wave;
-  int64_t row, chain, c0;   // c0: this lane's first channel, kept in range
+  int64_t chain, row, c0;   // c0: this lane's first channel, kept in range
   bool live;                // has this lane channels of its own?
-  int64_t range, t0, t1;
-  bool there;               // is this workgroup one of the launch's (rows_of_blocks)?
-  __device__ __forceinline__ Place(int64_t B, int64_t d, int64_t T, int ranges, int64_t per) {
+  __device__ __forceinline__ Place(int64_t d, int64_t chain_) {
     lane = threadIdx.x & 63;
     wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t tiles = (d + 64 * V - 1) / (64 * V), b = block_in_rows();
-    there = b < B * tiles * ranges;
-    chain = b / ranges;
-    range = b - chain * ranges;
+    const int64_t tiles = (d + 64 * V - 1) / (64 * V);
+    chain = chain_;
     row = chain / tiles;
     c0 = (chain - row * tiles) * 64 * V + lane * V;
     live = c0 < d;
     if (!live) c0 = d - V;
-    t0 = range * per;
-    t1 = imin(t0 + per, T);
   }
 };
 
-// the maps of a chain's ranges, in the order they are walked: [chain][range][a, b][V][64]
-template <int V>
-__device__ __forceinline__ float* map_at(float* maps, int64_t chain, int ranges, int64_t range) {
-  return maps + ((chain * ranges + range) * 2 * V) * 64;
-}
+// -------------------------------------------------------------- forward ----
 
-// The map of ranges [0, n) of a chain: wave w joins its share of them, and the
-// shares meet in `part`.  Every wave has it after the call.
-template <int V>
-__device__ __forceinline__ void maps_before(const float* maps, int64_t chain, int ranges, int n, int lane, int wave,
-                                            Map (*part)[V][64], Map (&out)[V]) {
-  constexpr int kAhead = 8;
-  const int per = (n + kWaves - 1) / kWaves, i0 = min(wave * per, n), i1 = min(i0 + per, n);
-  Map m[V];
-#pragma unroll
-  for (int c = 0; c < V; ++c) m[c] = {1.0f, 0.0f};
-  for (int i = i0; i < i1; i += kAhead) {
-    Map q[kAhead][V];
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const float* p = map_at<V>(const_cast<float*>(maps), chain, ranges, min(i + k, i1 - 1)) + lane;
-#pragma unroll
-      for (int c = 0; c < V; ++c) q[k][c] = {p[c * 64], p[(V + c) * 64]};
-    }
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-      if (i + k < i1) {
-#pragma unroll
-        for (int c = 0; c < V; ++c) m[c] = then(m[c], q[k][c]);
-      }
-  }
-#pragma unroll
-  for (int c = 0; c < V; ++c) part[wave][c][lane] = m[c];
-  lds_barrier();
-#pragma unroll
-  for (int c = 0; c < V; ++c) out[c] = part[0][c][lane];
-#pragma unroll
-  for (int w = 1; w < kWaves; ++w)
-#pragma unroll
-    for (int c = 0; c < V; ++c) out[c] = then(out[c], part[w][c][lane]);
-  lds_barrier();   // part is free again
-}
-
-// --------------------------------------------------------------- maps ----
-
-// A range's map: wave w takes the w-th eighth of it.  BACK: of the gradient,
-// from the last step to the first, the maps stored in that order.
-template <int DT, int G, int V, bool RAGGED, bool BACK>
-__global__ void __launch_bounds__(64 * kWaves) k_scan_map(const typename Storage<DT>::T* __restrict__ x,
-                                                          const typename Storage<DT>::T* __restrict__ h0,
-                                                          const typename Storage<DT>::T* __restrict__ dH,
-                                                          const typename Storage<DT>::T* __restrict__ dlast,
-                                                          const int32_t* __restrict__ cu, int64_t n_seqs, int64_t B,
-                                                          int64_t T, int64_t d, int ranges, int64_t per, float* __restrict__ maps) {
+// a wave's LS steps from s0 on
+template <int DT, int G, int V, int LS, bool RAGGED>
+struct Fore {
   using C = Chans<DT, V>;
-  __shared__ Map part[kWaves][V][64];
-  const Place<V> at(B, d, T, ranges, per);
-  if (!at.there) return;
-  const int64_t share = (per + kWaves - 1) / kWaves;
-  const int64_t s0 = imin(at.t0 + at.wave * share, at.t1), s1 = imin(s0 + share, at.t1);
-  constexpr int R = BACK ? 2 : G;   // values read of a step: f and dH, or all of x
-  auto read = [&](int64_t t, C (&q)[R]) {
-    const typename Storage<DT>::T* p = x + ((at.row * T + t) * G) * d + at.c0;
-    if constexpr (BACK) {
-      q[0].load(p);
-      q[1].load(dH + (at.row * T + t) * d + at.c0);
-    } else {
-#pragma unroll
-      for (int g = 0; g < G; ++g) q[g].load(p + g * d);
-    }
-  };
-  Map m[V];
-#pragma unroll
-  for (int c = 0; c < V; ++c) m[c] = {1.0f, 0.0f};
-  const int blocks = static_cast<int>((s1 - s0 + kSteps - 1) / kSteps);
-  // step j of block k, in the order of the walk (a step past the end: the last one, not used)
-  auto step_at = [&](int k, int j) {
-    const int64_t i = static_cast<int64_t>(k) * kSteps + j;
-    return BACK ? imax(s1 - 1 - i, s0) : imin(s0 + i, s1 - 1);
-  };
-  C q[2][kSteps][R];
-  auto load_block = [&](int k, C (&to)[kSteps][R]) {
-#pragma unroll
-    for (int j = 0; j < kSteps; ++j) read(step_at(k, j), to[j]);
-  };
-  auto use_block = [&](int k, const C (&v)[kSteps][R]) {
-    const int n = static_cast<int>(imin(kSteps, s1 - s0 - static_cast<int64_t>(k) * kSteps));
-    Cuts cut;
-    const int64_t first = BACK ? step_at(k, n - 1) : step_at(k, 0);
-    if constexpr (RAGGED) cut.find(cu, n_seqs, first, n, T);
-#pragma unroll
-    for (int j = 0; j < kSteps; ++j) {
-      if (j >= n) break;
-      const int bit = BACK ? n - 1 - j : j;
-      const bool here = RAGGED && (((BACK ? cut.tail : cut.head) >> bit) & 1);
-#pragma unroll
-      for (int c = 0; c < V; ++c) {
-        const Gate f = gate_of(v[j][0].at(c));
-        Map s;
-        if constexpr (BACK) {
-          float g = v[j][1].at(c);
-          if (RAGGED ? here : step_at(k, j) == T - 1) {
-            if (dlast) g += Storage<DT>::load(dlast + (RAGGED ? cut.seg[bit] : at.row) * d + at.c0 + c);
-          }
-          s = {here ? kCut : f.on, f.on * g};
-        } else {
-          s = {f.on, (G == 2 ? f.off : gate_of(v[j][1].at(c)).on) * v[j][R - 1].at(c)};
-          if (here) {
-            if (h0) s.b = fmaf(s.a, Storage<DT>::load(h0 + static_cast<int64_t>(cut.seg[bit]) * d + at.c0 + c), s.b);
-            s.a = kCut;
-          }
-        }
-        m[c] = then(m[c], s);
-      }
-    }
-  };
-  if (blocks > 0) load_block(0, q[0]);
-  for (int k = 0; k < blocks; k += 2) {
-    if (k + 1 < blocks) load_block(k + 1, q[1]);
-    use_block(k, q[0]);
-    if (k + 1 >= blocks) break;
-    if (k + 2 < blocks) load_block(k + 2, q[0]);
-    use_block(k + 1, q[1]);
-  }
-#pragma unroll
-  for (int c = 0; c < V; ++c) part[at.wave][c][at.lane] = m[c];
-  lds_barrier();
-  if (at.wave != 0) return;
-#pragma unroll
-  for (int c = 0; c < V; ++c) {
-    Map t = part[BACK ? kWaves - 1 : 0][c][at.lane];
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w) t = then(t, part[BACK ? kWaves - 1 - w : w][c][at.lane]);
-    float* p = map_at<V>(maps, at.chain, ranges, BACK ? ranges - 1 - at.range : at.range) + at.lane;
-    p[c * 64] = t.a;
-    p[(V + c) * 64] = t.b;
-  }
-}
+  C q[LS][G];
+  Map s[LS][V];
+  Cuts<LS> cut;
+  int64_t s0;
+  int n;
 
-// ------------------------------------------------------------- forward ----
-
-template <int DT, int G, int V, bool RAGGED>
-__global__ void __launch_bounds__(64 * kWaves) k_scan_walk(const typename Storage<DT>::T* __restrict__ x,
-                                                           const typename Storage<DT>::T* __restrict__ h0,
-                                                           const int32_t* __restrict__ cu, int64_t n_seqs, int64_t B,
-                                                           int64_t T, int64_t d, int ranges, int64_t per,
-                                                           const float* __restrict__ maps,
-                                                           typename Storage<DT>::T* __restrict__ H,
-                                                           typename Storage<DT>::T* __restrict__ last) {
-  using C = Chans<DT, V>;
-  __shared__ Map part[2][kWaves][V][64];
-  const Place<V> at(B, d, T, ranges, per);
-  if (!at.there) return;
-  const typename Storage<DT>::T* const xr = x + at.row * T * G * d + at.c0;
-  typename Storage<DT>::T* const Hr = H + at.row * T * d + at.c0;
-  const int chunks = static_cast<int>((at.t1 - at.t0 + kChunk - 1) / kChunk);
-  C q[2][kSteps][G];
-  auto load_chunk = [&](int k, C (&to)[kSteps][G]) {
-    const int64_t s0 = at.t0 + static_cast<int64_t>(k) * kChunk + at.wave * kSteps;
+  __device__ __forceinline__ void load(const Tensors<DT>& t, const Place<V>& at, int64_t first) {
+    s0 = first + at.wave * LS;
+    n = static_cast<int>(imax(imin(LS, t.T_ - s0), 0));
+    const typename C::T* const x = t.x + at.row * t.T_ * G * t.d + at.c0;
 #pragma unroll
-    for (int j = 0; j < kSteps; ++j) {
-      const int64_t t = imin(s0 + j, at.t1 - 1);
+    for (int j = 0; j < LS; ++j) {
+      const int64_t step = imin(s0 + j, t.T_ - 1);   // past the end: the last one, not used
 #pragma unroll
-      for (int g = 0; g < G; ++g) to[j][g].load(xr + (t * G + g) * d);
+      for (int g = 0; g < G; ++g) q[j][g].load(x + (step * G + g) * t.d);
     }
-  };
-  load_chunk(0, q[0]);
-  float h[V];   // the state before the chunk
-#pragma unroll
-  for (int c = 0; c < V; ++c) h[c] = !RAGGED && h0 ? Storage<DT>::load(h0 + at.row * d + at.c0 + c) : 0.0f;
-  if (at.range > 0) {
-    Map m[V];
-    maps_before<V>(maps, at.chain, ranges, static_cast<int>(at.range), at.lane, at.wave, part[0], m);
-#pragma unroll
-    for (int c = 0; c < V; ++c) h[c] = through(m[c], h[c]);
   }
-  auto use_chunk = [&](int k, const C (&v)[kSteps][G]) {
-    const int64_t s0 = at.t0 + static_cast<int64_t>(k) * kChunk + at.wave * kSteps;
-    const int n = static_cast<int>(imax(imin(kSteps, at.t1 - s0), 0));
-    Cuts cut;
-    if constexpr (RAGGED) cut.find(cu, n_seqs, s0, n, T);
-    Map s[kSteps][V], m[V];
+  // the steps' maps, and the map of them all
+  __device__ __forceinline__ void maps(const Tensors<DT>& t, const Place<V>& at, Map (&m)[V]) {
+    if constexpr (RAGGED) cut.find(t.cu, t.n_seqs, s0, n, t.T_);
 #pragma unroll
     for (int c = 0; c < V; ++c) m[c] = {1.0f, 0.0f};
 #pragma unroll
-    for (int j = 0; j < kSteps; ++j) {
+    for (int j = 0; j < LS; ++j) {
       const bool here = RAGGED && j < n && ((cut.head >> j) & 1);
 #pragma unroll
       for (int c = 0; c < V; ++c) {
-        const Gate f = gate_of(v[j][0].at(c));
-        s[j][c] = {f.on, (G == 2 ? f.off : gate_of(v[j][1].at(c)).on) * v[j][G - 1].at(c)};
+        const Gate f = gate_of(q[j][0].at(c));
+        s[j][c] = {f.on, (G == 2 ? f.off : gate_of(q[j][1].at(c)).on) * q[j][G - 1].at(c)};
         if (here) {
-          if (h0) s[j][c].b = fmaf(f.on, Storage<DT>::load(h0 + static_cast<int64_t>(cut.seg[j]) * d + at.c0 + c), s[j][c].b);
+          if (t.h0) s[j][c].b = fmaf(f.on, Storage<DT>::load(t.h0 + static_cast<int64_t>(cut.seg[j]) * t.d + at.c0 + c), s[j][c].b);
           s[j][c].a = kCut;
         }
         if (j < n) m[c] = then(m[c], s[j][c]);
       }
     }
+  }
+  // the states from the one before the steps
+  __device__ __forceinline__ void walk(const Tensors<DT>& t, const Place<V>& at, float (&h)[V]) {
+    typename C::T* const H = t.H + at.row * t.T_ * t.d + at.c0;
+#pragma unroll
+    for (int j = 0; j < LS; ++j) {
+      if (j >= n) continue;
+      C o;
+#pragma unroll
+      for (int c = 0; c < V; ++c) {
+        h[c] = through(s[j][c], h[c]);
+        o.set(c, h[c]);
+      }
+      if (at.live) {
+        o.store(H + (s0 + j) * t.d);
+        if (t.last && (RAGGED ? (cut.tail >> j) & 1 : s0 + j == t.T_ - 1))
+          o.store(t.last + (RAGGED ? cut.seg[j] : at.row) * t.d + at.c0);
+      }
+    }
+  }
+  // the state before the row
+  static __device__ __forceinline__ void start(const Tensors<DT>& t, const Place<V>& at, float (&h)[V]) {
+#pragma unroll
+    for (int c = 0; c < V; ++c) h[c] = !RAGGED && t.h0 ? Storage<DT>::load(t.h0 + at.row * t.d + at.c0 + c) : 0.0f;
+  }
+};
+
+template <int DT, int G, int V, int LS, int NW, bool RAGGED>
+__global__ void __launch_bounds__(64 * NW) k_scan_walk(Tensors<DT> t) {
+  using W = Fore<DT, G, V, LS, RAGGED>;
+  __shared__ Map part[2][NW][V][64];
+  const int64_t b = block_in_rows();
+  if (b >= t.chains) return;
+  const Place<V> at(t.d, b);
+  W w[2];
+  w[0].load(t, at, 0);
+  float h[V];   // the state before the chunk
+  W::start(t, at, h);
+  auto chunk = [&](W& now, W& next, int64_t k) {
+    if (k + 1 < t.chunks) next.load(t, at, (k + 1) * (NW * LS));
+    Map m[V];
+    now.maps(t, at, m);
     Map(*const p)[V][64] = part[k & 1];
 #pragma unroll
     for (int c = 0; c < V; ++c) p[at.wave][c][at.lane] = m[c];
     lds_barrier();
     float mine[V];
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
+    for (int v = 0; v < NW; ++v) {
 #pragma unroll
       for (int c = 0; c < V; ++c) {
-        if (w == at.wave) mine[c] = h[c];
-        h[c] = through(p[w][c][at.lane], h[c]);
+        if (v == at.wave) mine[c] = h[c];
+        h[c] = through(p[v][c][at.lane], h[c]);
       }
     }
-#pragma unroll
-    for (int j = 0; j < kSteps; ++j) {
-      if (j >= n) break;
-      C o;
-#pragma unroll
-      for (int c = 0; c < V; ++c) {
-        mine[c] = through(s[j][c], mine[c]);
-        o.set(c, mine[c]);
-      }
-      if (at.live) {
-        o.store(Hr + (s0 + j) * d);
-        if (last && (RAGGED ? (cut.tail >> j) & 1 : s0 + j == T - 1))
-          o.store(last + (RAGGED ? cut.seg[j] : at.row) * d + at.c0);
-      }
-    }
+    now.walk(t, at, mine);
   };
-  for (int k = 0; k < chunks; k += 2) {
-    if (k + 1 < chunks) load_chunk(k + 1, q[1]);
-    use_chunk(k, q[0]);
-    if (k + 1 >= chunks) break;
-    if (k + 2 < chunks) load_chunk(k + 2, q[0]);
-    use_chunk(k + 1, q[1]);
+  for (int64_t k = 0; k < t.chunks; k += 2) {
+    chunk(w[0], w[1], k);
+    if (k + 1 < t.chunks) chunk(w[1], w[0], k + 1);
   }
 }
 
-// ------------------------------------------------------------ backward ----
+// A ticket's chunk, in the order of the walk, of its chain
+__device__ __forceinline__ int64_t take_ticket(unsigned* ticket, unsigned* shared) {
+  if (threadIdx.x == 0) *shared = atomicAdd(ticket, 1u);
+  __syncthreads();
+  return static_cast<unsigned>(__builtin_amdgcn_readfirstlane(*shared));
+}
 
-// what a step of the backward reads
-template <int DT, int G, int V>
-struct BackStep {
-  Chans<DT, V> x[G], g;
-};
+// What the last wave does for all: the waves' maps in `part` (in the order of the
+// walk: order(0), order(1), ..) become their carries (the first number of their
+// slots), and the chunk's records are published; e: the carry of a chain's first
+// chunk.  The state's status goes out by announce after the barrier that follows.
+template <int V, int NW, class Order>
+__device__ __forceinline__ void join(const Records& rec, int64_t base, int64_t c, int lane, unsigned spin_limit,
+                                     bool map_first, Map (*part)[V][64], float (&e)[V], Order order) {
+  Map tot[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) tot[v] = part[order(0)][v][lane];
+#pragma unroll
+  for (int w = 1; w < NW; ++w)
+#pragma unroll
+    for (int v = 0; v < V; ++v) tot[v] = then(tot[v], part[order(w)][v][lane]);
+  if (c > 0) look_back<V>(rec, base, c, tot, lane, spin_limit, map_first, e);
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    put(rec.states + (base + c) * V * 64 + v * 64 + lane, through(tot[v], e[v]));
+    float h = e[v];
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      Map& slot = part[order(w)][v][lane];
+      const Map m = slot;
+      slot.a = h;
+      h = through(m, h);
+    }
+  }
+}
 
-template <int DT, int G, int V, bool RAGGED>
-__global__ void __launch_bounds__(64 * kWaves) k_scan_walk_back(
-    const typename Storage<DT>::T* __restrict__ x, const typename Storage<DT>::T* __restrict__ h0,
-    const typename Storage<DT>::T* __restrict__ H, const typename Storage<DT>::T* __restrict__ dH,
-    const typename Storage<DT>::T* __restrict__ dlast, const int32_t* __restrict__ cu, int64_t n_seqs, int64_t B,
-    int64_t T, int64_t d, int ranges, int64_t per, const float* __restrict__ maps, typename Storage<DT>::T* __restrict__ dx,
-    typename Storage<DT>::T* __restrict__ dh0) {
+template <int DT, int G, int V, int LS, int NW, bool RAGGED>
+__global__ void __launch_bounds__(64 * NW) k_scan_pass(Tensors<DT> t, Records rec, unsigned spin_limit, bool map_first) {
+  using W = Fore<DT, G, V, LS, RAGGED>;
+  __shared__ Map part[NW][V][64];
+  __shared__ unsigned tk;
+  const int64_t ticket = take_ticket(rec.ticket, &tk), c = ticket / t.chains;
+  if (c >= t.chunks) return;
+  const Place<V> at(t.d, ticket - c * t.chains);
+  W w;
+  w.load(t, at, c * (NW * LS));
+  Map m[V];
+  w.maps(t, at, m);
+#pragma unroll
+  for (int v = 0; v < V; ++v) part[at.wave][v][at.lane] = m[v];
+  lds_barrier();
+  const int64_t base = at.chain * t.chunks;
+  if (at.wave == NW - 1) {
+    float e[V];
+    W::start(t, at, e);
+    join<V, NW>(rec, base, c, at.lane, spin_limit, map_first, part, e, [](int k) { return k; });
+  }
+  lds_barrier();
+  if (at.wave == NW - 1) announce(rec.status + base + c, kState, at.lane);
+  float h[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) h[v] = part[at.wave][v][at.lane].a;
+  w.walk(t, at, h);
+}
+
+// ------------------------------------------------------------- backward ----
+
+template <int DT, int G, int V, int LS, bool RAGGED>
+struct Back {
   using ST = Storage<DT>;
   using C = Chans<DT, V>;
-  using Step = BackStep<DT, G, V>;
-  __shared__ Map fore[2][kWaves][V][64], back[2][kWaves][V][64];
-  const Place<V> at(B, d, T, ranges, per);
-  if (!at.there) return;
-  const typename ST::T* const xr = x + at.row * T * G * d + at.c0;
-  typename ST::T* const dxr = dx + at.row * T * G * d + at.c0;
-  const typename ST::T* const Hr = H + at.row * T * d + at.c0;
-  const typename ST::T* const gr = dH + at.row * T * d + at.c0;
-  const int chunks = static_cast<int>((at.t1 - at.t0 + kChunk - 1) / kChunk);
-  // chunk k from the end of the range; `start` the state before it
-  Step q[2][kSteps];
-  C start[2];
-  auto first_of = [&](int k) { return at.t0 + static_cast<int64_t>(chunks - 1 - k) * kChunk; };
-  auto load_chunk = [&](int k, Step (&to)[kSteps], C& st) {
-    const int64_t f0 = first_of(k), s0 = f0 + at.wave * kSteps;
+  C x[LS][G], dh[LS], before;   // before: the state before the chunk
+  Gate f[LS][V], i[LS][V];
+  float g[LS][V];               // the gradient that arrives at a state from outside
+  Cuts<LS> cut;
+  int64_t s0;
+  int n;
+
+  __device__ __forceinline__ bool head(int j) const { return RAGGED && ((cut.head >> j) & 1); }
+  __device__ __forceinline__ bool tail(int j) const { return RAGGED && ((cut.tail >> j) & 1); }
+  __device__ __forceinline__ int64_t seg(int j, const Place<V>& at) const { return RAGGED ? static_cast<int64_t>(cut.seg[j]) : at.row; }
+
+  __device__ __forceinline__ void load(const Tensors<DT>& t, const Place<V>& at, int64_t first) {
+    s0 = first + at.wave * LS;
+    n = static_cast<int>(imax(imin(LS, t.T_ - s0), 0));
+    const int64_t row = at.row * t.T_;
 #pragma unroll
-    for (int j = 0; j < kSteps; ++j) {
-      const int64_t t = imin(s0 + j, at.t1 - 1);
+    for (int j = 0; j < LS; ++j) {
+      const int64_t step = row + imin(s0 + j, t.T_ - 1);   // past the end: the last one, not used
 #pragma unroll
-      for (int g = 0; g < G; ++g) to[j].x[g].load(xr + (t * G + g) * d);
-      to[j].g.load(gr + t * d);
+      for (int k = 0; k < G; ++k) x[j][k].load(t.x + (step * G + k) * t.d + at.c0);
+      dh[j].load(t.dH + step * t.d + at.c0);
     }
-    if (f0 > 0) {
-      st.load(Hr + (f0 - 1) * d);
-    } else if (!RAGGED && h0) {
-      st.load(h0 + at.row * d + at.c0);
+    if (first > 0) {
+      before.load(t.H + (row + first - 1) * t.d + at.c0);
+    } else if (!RAGGED && t.h0) {
+      before.load(t.h0 + at.row * t.d + at.c0);
     } else {
 #pragma unroll
-      for (int c = 0; c < V; ++c) st.set(c, 0.0f);
+      for (int c = 0; c < V; ++c) before.set(c, 0.0f);
     }
-  };
-  load_chunk(0, q[0], start[0]);
+  }
+  // the maps of the states over the steps, and of the gradient back over them
+  __device__ __forceinline__ void maps(const Tensors<DT>& t, const Place<V>& at, Map (&fore)[V], Map (&back)[V]) {
+    if constexpr (RAGGED) cut.find(t.cu, t.n_seqs, s0, n, t.T_);
+#pragma unroll
+    for (int c = 0; c < V; ++c) fore[c] = back[c] = {1.0f, 0.0f};
+#pragma unroll
+    for (int j = 0; j < LS; ++j) {
+#pragma unroll
+      for (int c = 0; c < V; ++c) {
+        f[j][c] = gate_of(x[j][0].at(c));
+        i[j][c] = G == 2 ? Gate{f[j][c].off, f[j][c].on} : gate_of(x[j][1].at(c));
+        g[j][c] = dh[j].at(c);
+        if (j < n && t.dlast && (RAGGED ? tail(j) : s0 + j == t.T_ - 1)) g[j][c] += ST::load(t.dlast + seg(j, at) * t.d + at.c0 + c);
+        Map m = {f[j][c].on, i[j][c].on * x[j][G - 1].at(c)};
+        if (RAGGED && j < n && head(j)) {
+          if (t.h0) m.b = fmaf(m.a, ST::load(t.h0 + seg(j, at) * t.d + at.c0 + c), m.b);
+          m.a = kCut;
+        }
+        if (j < n) fore[c] = then(fore[c], m);
+      }
+    }
+#pragma unroll
+    for (int j = LS - 1; j >= 0; --j) {
+      if (j >= n) continue;
+#pragma unroll
+      for (int c = 0; c < V; ++c) back[c] = then(back[c], Map{tail(j) ? kCut : f[j][c].on, f[j][c].on * g[j][c]});
+    }
+  }
+  // the gradients, from the state before the steps and the gradient that arrives at their last state from after it
+  __device__ __forceinline__ void walk(const Tensors<DT>& t, const Place<V>& at, float (&h)[V], float (&m)[V]) {
+    float prev[LS][V];
+#pragma unroll
+    for (int j = 0; j < LS; ++j) {
+      if (j >= n) continue;
+#pragma unroll
+      for (int c = 0; c < V; ++c) {
+        if (head(j)) h[c] = t.h0 ? ST::load(t.h0 + seg(j, at) * t.d + at.c0 + c) : 0.0f;
+        prev[j][c] = h[c];
+        h[c] = fmaf(f[j][c].on, h[c], i[j][c].on * x[j][G - 1].at(c));
+      }
+    }
+    typename ST::T* const dx = t.dx + at.row * t.T_ * G * t.d + at.c0;
+#pragma unroll
+    for (int j = LS - 1; j >= 0; --j) {
+      if (j >= n) continue;
+      C o[G], out;
+#pragma unroll
+      for (int c = 0; c < V; ++c) {
+        const float lam = tail(j) ? g[j][c] : g[j][c] + m[c], val = x[j][G - 1].at(c);
+        o[0].set(c, lam * (G == 2 ? prev[j][c] - val : prev[j][c]) * (f[j][c].on * f[j][c].off));
+        if constexpr (G == 3) o[1].set(c, lam * val * (i[j][c].on * i[j][c].off));
+        o[G - 1].set(c, lam * i[j][c].on);
+        m[c] = f[j][c].on * lam;
+        out.set(c, m[c]);
+      }
+      if (at.live) {
+#pragma unroll
+        for (int k = 0; k < G; ++k) o[k].store(dx + ((s0 + j) * G + k) * t.d);
+        if (t.dh0 && (RAGGED ? head(j) : s0 + j == 0)) out.store(t.dh0 + seg(j, at) * t.d + at.c0);
+      }
+    }
+  }
+  // the state before this wave's steps, through the waves' maps before it
+  template <int NW>
+  __device__ __forceinline__ void entry(const Place<V>& at, const Map (*fore)[V][64], float (&h)[V]) const {
+#pragma unroll
+    for (int c = 0; c < V; ++c) h[c] = before.at(c);
+#pragma unroll
+    for (int w = 0; w < NW - 1; ++w) {
+      if (w >= at.wave) break;
+#pragma unroll
+      for (int c = 0; c < V; ++c) h[c] = through(fore[w][c][at.lane], h[c]);
+    }
+  }
+};
+
+template <int DT, int G, int V, int LS, int NW, bool RAGGED>
+__global__ void __launch_bounds__(64 * NW) k_scan_walk_back(Tensors<DT> t) {
+  using W = Back<DT, G, V, LS, RAGGED>;
+  __shared__ Map fore[2][NW][V][64], back[2][NW][V][64];
+  const int64_t b = block_in_rows();
+  if (b >= t.chains) return;
+  const Place<V> at(t.d, b);
+  auto first = [&](int64_t k) { return (t.chunks - 1 - k) * (NW * LS); };   // chunk k from the end
+  W w[2];
+  w[0].load(t, at, first(0));
   float mu[V];   // the gradient that arrives at the chunk's last state from the steps after it
 #pragma unroll
   for (int c = 0; c < V; ++c) mu[c] = 0.0f;
-  if (at.range + 1 < ranges) {
-    Map m[V];
-    maps_before<V>(maps, at.chain, ranges, static_cast<int>(ranges - 1 - at.range), at.lane, at.wave, back[0], m);
-#pragma unroll
-    for (int c = 0; c < V; ++c) mu[c] = through(m[c], 0.0f);
-  }
-  auto use_chunk = [&](int k, const Step (&v)[kSteps], const C& st) {
-    const int64_t s0 = first_of(k) + at.wave * kSteps;
-    const int n = static_cast<int>(imax(imin(kSteps, at.t1 - s0), 0));
-    Cuts cut;
-    if constexpr (RAGGED) cut.find(cu, n_seqs, s0, n, T);
-    auto head = [&](int j) { return RAGGED && ((cut.head >> j) & 1); };
-    auto tail = [&](int j) { return RAGGED && ((cut.tail >> j) & 1); };
-    auto seg = [&](int j) { return RAGGED ? static_cast<int64_t>(cut.seg[j]) : at.row; };
-    // the forward map of a step, and the gradient that arrives at its state from outside
-    auto forward = [&](int j, int c, const Gate& f, const Gate& i) {
-      Map m = {f.on, i.on * v[j].x[G - 1].at(c)};
-      if (head(j)) {
-        if (h0) m.b = fmaf(f.on, ST::load(h0 + seg(j) * d + at.c0 + c), m.b);
-        m.a = kCut;
-      }
-      return m;
-    };
-    float g[kSteps][V];
-    Gate f[kSteps][V], i[kSteps][V];
+  auto chunk = [&](W& now, W& next, int64_t k) {
+    if (k + 1 < t.chunks) next.load(t, at, first(k + 1));
     Map mf[V], mb[V];
-#pragma unroll
-    for (int c = 0; c < V; ++c) mf[c] = mb[c] = {1.0f, 0.0f};
-#pragma unroll
-    for (int j = 0; j < kSteps; ++j) {
-#pragma unroll
-      for (int c = 0; c < V; ++c) {
-        f[j][c] = gate_of(v[j].x[0].at(c));
-        i[j][c] = G == 2 ? Gate{f[j][c].off, f[j][c].on} : gate_of(v[j].x[1].at(c));
-        g[j][c] = v[j].g.at(c);
-        if (j < n && dlast && (RAGGED ? tail(j) : s0 + j == T - 1)) g[j][c] += ST::load(dlast + seg(j) * d + at.c0 + c);
-        if (j < n) mf[c] = then(mf[c], forward(j, c, f[j][c], i[j][c]));
-      }
-    }
-#pragma unroll
-    for (int j = kSteps - 1; j >= 0; --j) {
-      if (j >= n) continue;
-#pragma unroll
-      for (int c = 0; c < V; ++c) mb[c] = then(mb[c], Map{tail(j) ? kCut : f[j][c].on, f[j][c].on * g[j][c]});
-    }
+    now.maps(t, at, mf, mb);
     Map(*const pf)[V][64] = fore[k & 1], (*const pb)[V][64] = back[k & 1];
 #pragma unroll
     for (int c = 0; c < V; ++c) {
@@ -460,61 +535,53 @@ __global__ void __launch_bounds__(64 * kWaves) k_scan_walk_back(
     }
     lds_barrier();
     float h[V], m[V];
+    now.template entry<NW>(at, pf, h);
 #pragma unroll
-    for (int c = 0; c < V; ++c) h[c] = st.at(c);
-#pragma unroll
-    for (int w = 0; w < kWaves - 1; ++w) {
-      if (w >= at.wave) break;
-#pragma unroll
-      for (int c = 0; c < V; ++c) h[c] = through(pf[w][c][at.lane], h[c]);
-    }
-#pragma unroll
-    for (int w = kWaves - 1; w >= 0; --w) {
+    for (int v = NW - 1; v >= 0; --v) {
 #pragma unroll
       for (int c = 0; c < V; ++c) {
-        if (w == at.wave) m[c] = mu[c];
-        mu[c] = through(pb[w][c][at.lane], mu[c]);
+        if (v == at.wave) m[c] = mu[c];
+        mu[c] = through(pb[v][c][at.lane], mu[c]);
       }
     }
-    float prev[kSteps][V];
-#pragma unroll
-    for (int j = 0; j < kSteps; ++j) {
-      if (j >= n) break;
-#pragma unroll
-      for (int c = 0; c < V; ++c) {
-        if (head(j)) h[c] = h0 ? ST::load(h0 + seg(j) * d + at.c0 + c) : 0.0f;
-        prev[j][c] = h[c];
-        h[c] = fmaf(f[j][c].on, h[c], i[j][c].on * v[j].x[G - 1].at(c));
-      }
-    }
-#pragma unroll
-    for (int j = kSteps - 1; j >= 0; --j) {
-      if (j >= n) continue;
-      C o[G], first;
-#pragma unroll
-      for (int c = 0; c < V; ++c) {
-        const float lam = tail(j) ? g[j][c] : g[j][c] + m[c], val = v[j].x[G - 1].at(c);
-        const float df = f[j][c].on * f[j][c].off;
-        o[0].set(c, lam * (G == 2 ? prev[j][c] - val : prev[j][c]) * df);
-        if constexpr (G == 3) o[1].set(c, lam * val * (i[j][c].on * i[j][c].off));
-        o[G - 1].set(c, lam * i[j][c].on);
-        m[c] = f[j][c].on * lam;
-        first.set(c, m[c]);
-      }
-      if (at.live) {
-#pragma unroll
-        for (int e = 0; e < G; ++e) o[e].store(dxr + ((s0 + j) * G + e) * d);
-        if (dh0 && (RAGGED ? head(j) : s0 + j == 0)) first.store(dh0 + seg(j) * d + at.c0);
-      }
-    }
+    now.walk(t, at, h, m);
   };
-  for (int k = 0; k < chunks; k += 2) {
-    if (k + 1 < chunks) load_chunk(k + 1, q[1], start[1]);
-    use_chunk(k, q[0], start[0]);
-    if (k + 1 >= chunks) break;
-    if (k + 2 < chunks) load_chunk(k + 2, q[0], start[0]);
-    use_chunk(k + 1, q[1], start[1]);
+  for (int64_t k = 0; k < t.chunks; k += 2) {
+    chunk(w[0], w[1], k);
+    if (k + 1 < t.chunks) chunk(w[1], w[0], k + 1);
   }
+}
+
+template <int DT, int G, int V, int LS, int NW, bool RAGGED>
+__global__ void __launch_bounds__(64 * NW) k_scan_pass_back(Tensors<DT> t, Records rec, unsigned spin_limit, bool map_first) {
+  using W = Back<DT, G, V, LS, RAGGED>;
+  __shared__ Map fore[NW][V][64], back[NW][V][64];
+  __shared__ unsigned tk;
+  const int64_t ticket = take_ticket(rec.ticket, &tk), c = ticket / t.chains;   // c: from the end
+  if (c >= t.chunks) return;
+  const Place<V> at(t.d, ticket - c * t.chains);
+  W w;
+  w.load(t, at, (t.chunks - 1 - c) * (NW * LS));
+  Map mf[V], mb[V];
+  w.maps(t, at, mf, mb);
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    fore[at.wave][v][at.lane] = mf[v];
+    back[at.wave][v][at.lane] = mb[v];
+  }
+  lds_barrier();
+  const int64_t base = at.chain * t.chunks;
+  if (at.wave == NW - 1) {
+    float e[V] = {};
+    join<V, NW>(rec, base, c, at.lane, spin_limit, map_first, back, e, [](int k) { return NW - 1 - k; });
+  }
+  lds_barrier();
+  if (at.wave == NW - 1) announce(rec.status + base + c, kState, at.lane);
+  float h[V], m[V];
+  w.template entry<NW>(at, fore, h);
+#pragma unroll
+  for (int v = 0; v < V; ++v) m[v] = back[at.wave][v][at.lane].a;
+  w.walk(t, at, h, m);
 }
 
 // out[j] = in[j] (0 without in) of the sequences of a pack that have no step,
@@ -532,26 +599,62 @@ __global__ void __launch_bounds__(256) k_scan_empty(const int32_t* __restrict__ 
 // ---------------------------------------------------------------- plan ----
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+size_t up(size_t x) { return (x + 255) / 256 * 256; }
 
-// workgroups that fill the device
-constexpr int64_t kFill = 512;
+// Chains from which a workgroup each fills the device, and steps up to which a
+// few chunks one after another take no longer than the look-back and the launch
+// that clears its records.  (Before the look-back the maps of 512 stretches of
+// time were taken by a kernel of their own, which reads the inputs twice: 43 and
+// 65 us for 8 x 4096 x 512 bf16, 284 and 400 for 2 x 131072 x 256 fp32, where it
+// takes 34 and 54, 186 and 285.)
+constexpr int64_t kEnough = 256, kShort = 256;
+// Steps of a wave and waves of a workgroup.  A longer chunk means fewer
+// look-backs in a row, as long as the registers allow a workgroup of it, and
+// two of the smaller ones, on a CU.  us, glr, 2 x 131072 x 256 fp32 and 8 x 4096 x
+// 512 bf16, steps x waves:
+//   forward   16 x 16 186 and 34, 12 x 16 207 and 36, 8 x 16 241 and 38, 16 x 12 205
+//             and 36, 24 x 8 196 and 40, 16 x 8 207 and 38
+//   backward  16 x 8 285 and 58, 12 x 8 308 and 63, 8 x 16 305 and 54, 8 x 8 355 and 56,
+//             4 x 16 443 and 67; glri fp32, a pack of 20011 x 250: 8 x 16 50, 16 x 8 58
+// and where a workgroup has its chain (64 x 1024 x 512 bf16, glr):
+//   forward   8 x 8 54, 8 x 16 53, 4 x 16 61, 16 x 8 62; glri 69, 76, 73, 79
+//   backward  8 x 8 82, 4 x 12 87, 4 x 8 98, 8 x 4 113
+struct Shape {
+  int steps, waves;
+  constexpr int chunk() const { return steps * waves; }
+};
+template <int G, int V>
+constexpr Shape shape_of(bool back, bool pass) {
+  if (!pass) return {8, 8};
+  if (!back) return {16, 16};
+  if (V == 1) return G == 2 ? Shape{16, 8} : Shape{8, 16};
+  return G == 2 ? Shape{8, 16} : Shape{8, 8};   // (glri of two channels a lane: more than 128 registers)
+}
+Shape shape_of(int G, int V, bool back, bool pass) {
+  if (G == 2) return V == 1 ? shape_of<2, 1>(back, pass) : shape_of<2, 2>(back, pass);
+  return V == 1 ? shape_of<3, 1>(back, pass) : shape_of<3, 2>(back, pass);
+}
 
 struct Plan {
   int V;
-  int64_t chains, per;
-  int ranges;
-  size_t total;
+  bool pass;
+  int64_t chains, chunks;
+  size_t words, maps_off, states_off, total;
 };
-Plan plan_of(const GatedScanArgs& a) {
+Plan plan_of(const GatedScanArgs& a, bool back) {
   Plan p{};
   if (a.T == 0) return p;
   p.V = a.bf16 && a.d % 2 == 0 ? 2 : 1;   // 4 bytes a lane where the rows allow it
   p.chains = a.B * cdiv(a.d, 64 * p.V);
-  const int64_t chunks = cdiv(a.T, kChunk);
-  const int64_t want = std::max<int64_t>(1, std::min(chunks, kFill / std::max<int64_t>(1, p.chains)));
-  p.per = cdiv(chunks, want) * kChunk;
-  p.ranges = static_cast<int>(std::max<int64_t>(1, cdiv(a.T, p.per)));
-  p.total = p.ranges > 1 ? size_t(p.chains) * p.ranges * 2 * p.V * 64 * sizeof(float) : 0;
+  p.pass = p.chains < kEnough && a.T > kShort;
+  p.chunks = cdiv(a.T, shape_of(a.G, p.V, back, p.pass).chunk());
+  if (p.pass) {
+    const size_t n = size_t(p.chains) * p.chunks, line = size_t(p.V) * 64 * sizeof(float);
+    p.words = 2 + n;   // ticket, error, statuses
+    p.maps_off = up(p.words * sizeof(unsigned));
+    p.states_off = p.maps_off + up(n * 2 * line);
+    p.total = p.states_off + up(n * line);
+  }
   return p;
 }
 
@@ -581,48 +684,63 @@ void fill_empty(const GatedScanArgs& a, const void* in, void* out) {
     k_scan_empty<float><<<grid, 256, 0, a.stream>>>(a.cu, rows, a.d, static_cast<const float*>(in), static_cast<float*>(out));
 }
 
+template <int DT>
+Tensors<DT> tensors_of(const GatedScanArgs& a, const Plan& p) {
+  using T = typename Storage<DT>::T;
+  return {static_cast<const T*>(a.xproj), static_cast<const T*>(a.h0), static_cast<const T*>(a.dH), static_cast<const T*>(a.dlast),
+          static_cast<T*>(a.H), static_cast<T*>(a.last), static_cast<T*>(a.dxproj), static_cast<T*>(a.dh0),
+          a.cu, a.n_seqs, a.B, a.T, a.d, p.chains, p.chunks};
+}
+
+Records records_of(const GatedScanArgs& a, const Plan& p) {
+  unsigned* const words = reinterpret_cast<unsigned*>(a.ws);
+  k_scan_clear<<<rows_of_blocks(cdiv(p.words, 256)), 256, 0, a.stream>>>(words, p.words);
+  return {words, a.error ? a.error : words + 1, words + 2, reinterpret_cast<float*>(a.ws + p.maps_off),
+          reinterpret_cast<float*>(a.ws + p.states_off)};
+}
+
 }  // namespace
 
-size_t gated_scan_workspace(const GatedScanArgs& a) { return plan_of(a).total; }
-size_t gated_scan_backward_workspace(const GatedScanArgs& a) { return plan_of(a).total; }
+bool gated_scan_fits(const GatedScanArgs& a) {
+  // a ticket counts the chunks of all chains; a chunk has 64 steps or more
+  return double(a.B) * (double(a.d) / 64 + 1) * (double(a.T) / 64 + 1) < 4194304.0 * 512;
+}
+size_t gated_scan_workspace(const GatedScanArgs& a) { return plan_of(a, false).total; }
+size_t gated_scan_backward_workspace(const GatedScanArgs& a) { return plan_of(a, true).total; }
 
 void launch_gated_scan(const GatedScanArgs& a) {
   if (a.last && (a.n_seqs > 0 || a.T == 0)) fill_empty(a, a.h0, a.last);
   if (a.T == 0) return;
-  const Plan p = plan_of(a);
-  float* const maps = reinterpret_cast<float*>(a.ws);
-  const dim3 grid = rows_of_blocks(p.chains * p.ranges);
+  const Plan p = plan_of(a, false);
+  const Records rec = p.pass ? records_of(a, p) : Records{};
   typed(a, p.V, [&](auto dt, auto g, auto v, auto ragged) {
     constexpr int DT = decltype(dt)::value, G = decltype(g)::value, V = decltype(v)::value;
     constexpr bool RAGGED = decltype(ragged)::value;
-    using T = typename Storage<DT>::T;
-    const T *x = static_cast<const T*>(a.xproj), *h0 = static_cast<const T*>(a.h0);
-    if (p.ranges > 1)
-      k_scan_map<DT, G, V, RAGGED, false><<<grid, 64 * kWaves, 0, a.stream>>>(x, h0, nullptr, nullptr, a.cu, a.n_seqs, a.B, a.T, a.d,
-                                                                              p.ranges, p.per, maps);
-    k_scan_walk<DT, G, V, RAGGED><<<grid, 64 * kWaves, 0, a.stream>>>(x, h0, a.cu, a.n_seqs, a.B, a.T, a.d, p.ranges, p.per, maps,
-                                                                      static_cast<T*>(a.H), static_cast<T*>(a.last));
+    const Tensors<DT> t = tensors_of<DT>(a, p);
+    constexpr Shape pass = shape_of<G, V>(false, true), walk = shape_of<G, V>(false, false);
+    if (p.pass)
+      k_scan_pass<DT, G, V, pass.steps, pass.waves, RAGGED><<<rows_of_blocks(p.chains * p.chunks), 64 * pass.waves, 0, a.stream>>>(
+          t, rec, a.spin_limit, p.chains < 64);
+    else
+      k_scan_walk<DT, G, V, walk.steps, walk.waves, RAGGED><<<rows_of_blocks(p.chains), 64 * walk.waves, 0, a.stream>>>(t);
   });
 }
 
 void launch_gated_scan_backward(const GatedScanArgs& a) {
   if (a.dh0 && (a.n_seqs > 0 || a.T == 0)) fill_empty(a, a.dlast, a.dh0);
   if (a.T == 0) return;
-  const Plan p = plan_of(a);
-  float* const maps = reinterpret_cast<float*>(a.ws);
-  const dim3 grid = rows_of_blocks(p.chains * p.ranges);
+  const Plan p = plan_of(a, true);
+  const Records rec = p.pass ? records_of(a, p) : Records{};
   typed(a, p.V, [&](auto dt, auto g, auto v, auto ragged) {
     constexpr int DT = decltype(dt)::value, G = decltype(g)::value, V = decltype(v)::value;
     constexpr bool RAGGED = decltype(ragged)::value;
-    using T = typename Storage<DT>::T;
-    const T *x = static_cast<const T*>(a.xproj), *h0 = static_cast<const T*>(a.h0), *H = static_cast<const T*>(a.H),
-            *dH = static_cast<const T*>(a.dH), *dlast = static_cast<const T*>(a.dlast);
-    if (p.ranges > 1)
-      k_scan_map<DT, G, V, RAGGED, true><<<grid, 64 * kWaves, 0, a.stream>>>(x, h0, dH, dlast, a.cu, a.n_seqs, a.B, a.T, a.d,
-                                                                             p.ranges, p.per, maps);
-    k_scan_walk_back<DT, G, V, RAGGED><<<grid, 64 * kWaves, 0, a.stream>>>(x, h0, H, dH, dlast, a.cu, a.n_seqs, a.B, a.T, a.d,
-                                                                           p.ranges, p.per, maps,
-                                                                           static_cast<T*>(a.dxproj), static_cast<T*>(a.dh0));
+    const Tensors<DT> t = tensors_of<DT>(a, p);
+    constexpr Shape pass = shape_of<G, V>(true, true), walk = shape_of<G, V>(true, false);
+    if (p.pass)
+      k_scan_pass_back<DT, G, V, pass.steps, pass.waves, RAGGED><<<rows_of_blocks(p.chains * p.chunks), 64 * pass.waves, 0, a.stream>>>(
+          t, rec, a.spin_limit, p.chains < 64);
+    else
+      k_scan_walk_back<DT, G, V, walk.steps, walk.waves, RAGGED><<<rows_of_blocks(p.chains), 64 * walk.waves, 0, a.stream>>>(t);
   });
 }
 

@@ -16,6 +16,7 @@
 
 #include "backward.h"
 #include "decode.h"
+#include "gated_few.h"
 #include "headmix.h"
 #include "newton_kernels.h"
 #include "newton_sp.h"
@@ -800,14 +801,13 @@ prn_status prn_decode_step(const void* x, const void* W, const float* bias, cons
   };
   using F32 = std::integral_constant<int, prn::kF32>;
   using BF16 = std::integral_constant<int, prn::kBF16>;
-  auto typed = [&](auto cell) {
-    if (p->dtype == PRN_F32) go(cell, F32{}); else go(cell, BF16{});
-  };
-  switch (p->cell) {
-    case PRN_CELL_DIAG_GRU: typed(prn::CellGRU{}); break;
-    case PRN_CELL_DIAG_LSTM: typed(prn::CellLSTM{}); break;
-    case PRN_CELL_GATED: typed(prn::CellGated<2>{}); break;
-    default: typed(prn::CellGated<3>{}); break;
+  if (gated_cell(p->cell)) {
+    const prn::GatedFewArgs a{p->dtype == PRN_BF16, p->B, p->d_h, p->d_in, x, W, st};
+    prn::launch_few_step(a, sh.G, bias, state_in, state_out, h_out);
+  } else if (p->cell == PRN_CELL_DIAG_GRU) {
+    if (p->dtype == PRN_F32) go(prn::CellGRU{}, F32{}); else go(prn::CellGRU{}, BF16{});
+  } else {
+    if (p->dtype == PRN_F32) go(prn::CellLSTM{}, F32{}); else go(prn::CellLSTM{}, BF16{});
   }
   return launched("prn_decode_step");
 }

@@ -104,14 +104,19 @@ prn_status scan_args(const prn_params* p, prn::GatedScanArgs* a) {
   a->G = sh.G;
   a->B = p->B, a->T = p->T, a->d = p->d_h, a->n_seqs = p->n_seqs;
   a->last = p->state_last_out;
+  a->error = static_cast<unsigned*>(p->error_out);
+  a->spin_limit = spin_limit();
   a->ws = static_cast<uint8_t*>(p->workspace);
   a->stream = static_cast<hipStream_t>(p->stream);
+  if (!prn::gated_scan_fits(*a)) return fail(PRN_ERR_UNSUPPORTED, "too many chunks for one launch: B=%lld T=%lld d_h=%lld",
+                                             (long long)p->B, (long long)p->T, (long long)p->d_h);
   return PRN_OK;
 }
 prn_status scan_pack(const prn_params* p, const int32_t* cu) {
   if (p->n_seqs > 0 && !cu) return fail(PRN_ERR_INVALID_ARG, "n_seqs > 0 but cu_seqlens is NULL");
   if (p->n_seqs == 0 && cu) return fail(PRN_ERR_INVALID_ARG, "cu_seqlens given but n_seqs == 0");
-  if (misaligned(cu, 4)) return fail(PRN_ERR_INVALID_ARG, "cu_seqlens is not 4-byte aligned");
+  if (misaligned(cu, 4) || misaligned(p->error_out, 4))
+    return fail(PRN_ERR_INVALID_ARG, "cu_seqlens or error_out is not 4-byte aligned");
   return PRN_OK;
 }
 
@@ -125,18 +130,9 @@ prn_status ffn_args(const prn_gated_ffn_params* p, prn::GatedFfnArgs* a) {
   *a = {p->dtype == PRN_BF16, p->act == PRN_ACT_SILU, p->N, p->d, p->F, static_cast<uint8_t*>(p->workspace),
         static_cast<hipStream_t>(p->stream)};
   if (p->N > kMaxRows || !prn::gated_ffn_fits(*a))
-    return fail(PRN_ERR_UNSUPPORTED, "N below 2^31, 2 F d below 2^32, N F below 2^37; got N=%lld d=%lld F=%lld",
+    return fail(PRN_ERR_UNSUPPORTED, "N below 2^31, 2 (F + 256) (d + 64) below 2^31, N F and N d below 2^36; got N=%lld d=%lld F=%lld",
                 (long long)p->N, (long long)p->d, (long long)p->F);
   return PRN_OK;
-}
-// the projection whose gradients dz -> dx, dW are: 2 F columns of d
-prn_params ffn_projection(const prn_gated_ffn_params* p) {
-  prn_params q{};
-  q.cell = PRN_CELL_GATED;
-  q.dtype = p->dtype;
-  q.B = 1, q.T = p->N, q.d_in = p->d, q.d_h = p->F;
-  q.stream = p->stream;
-  return q;
 }
 
 }  // namespace
@@ -337,11 +333,7 @@ size_t prn_gated_ffn_backward_workspace_bytes(const prn_gated_ffn_params* p) {
   g_err.clear();
   prn::GatedFfnArgs a;
   if (ffn_args(p, &a) != PRN_OK) return 0;
-  size_t dz;
-  const size_t own = prn::gated_ffn_dz_workspace(a, &dz);
-  const prn_params q = ffn_projection(p);
-  const size_t proj = prn_input_proj_backward_workspace_bytes(&q);
-  return g_err.empty() ? own + proj : 0;
+  return prn::gated_ffn_backward_workspace(a);
 }
 
 prn_status prn_gated_ffn_backward(const void* x, const void* W, const void* dout, const prn_gated_ffn_params* p, void* dx,
@@ -351,17 +343,11 @@ prn_status prn_gated_ffn_backward(const void* x, const void* W, const void* dout
   if (a.N && (!x || !W || !dout)) return fail(PRN_ERR_INVALID_ARG, "x, W or dout is NULL");
   if (misaligned(x, 16) || misaligned(W, 16) || misaligned(dout, 16) || misaligned(dx, 16) || misaligned(dW, 16))
     return fail(PRN_ERR_INVALID_ARG, "x, W, dout, dx_out and dW_out must be 16-byte aligned");
-  const size_t need = prn_gated_ffn_backward_workspace_bytes(p);
-  if (!g_err.empty()) return PRN_ERR_UNSUPPORTED;
-  if (prn_status s = check_scratch(p->workspace, p->workspace_bytes, need); s != PRN_OK) return s;
+  if (prn_status s = check_scratch(p->workspace, p->workspace_bytes, prn::gated_ffn_backward_workspace(a)); s != PRN_OK)
+    return s;
   if (!dx && !dW) return PRN_OK;
-  size_t dz;
-  const size_t own = prn::gated_ffn_dz_workspace(a, &dz);
-  prn_params q = ffn_projection(p);
-  q.workspace = a.ws + own;
-  q.workspace_bytes = need - own;
-  if (a.N) prn::launch_gated_ffn_dz(a, x, W, dout);
-  return prn_input_proj_backward(a.ws + dz, x, W, &q, dx, dW, nullptr);
+  prn::launch_gated_ffn_backward(a, x, W, dout, dx, dW);
+  return launched("prn_gated_ffn_backward");
 }
 
 prn_status prn_dropout(const void* x, const void* residual, const prn_dropout_params* p, void* out) {

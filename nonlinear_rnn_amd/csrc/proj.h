@@ -18,11 +18,12 @@ void launch_proj(bool bf16, const void* A, const void* B, const float* bias, voi
 
 // A gated product: W holds F gate rows and F up rows, the sums g and u of each
 // pair meet in the epilogue.  Without dout out = act(g) u (M x F), with dout
-// (M x F) the gradients of the sums, [dout u act'(g) | dout act(g)] (M x 2 F).
+// (M x F) the gradients of the sums, [dout u act'(g) | dout act(g)], in rows ldz
+// apart.
 // The products, requirements and rounding are launch_proj's.
 struct GatedProj {
   const void* dout;
-  int64_t F;
+  int64_t F, ldz;
   bool silu;   // g s(g); else s(g)
 };
 void launch_proj_gated(bool bf16, const void* x, const void* W, void* out, int64_t M, int64_t K, const GatedProj& gp,

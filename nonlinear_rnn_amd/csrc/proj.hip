@@ -127,7 +127,7 @@ struct Tile {
 // gp.F gate rows and gp.F up rows, and every 64 columns of a wave are 32 of
 // each, so that a lane has both sums of its 16 rows and one pair of columns.
 // kGatedOut stores act(gate) up, M x F; kGatedBack the gradients of the two
-// sums from dout (M x F), M x 2 F.  N is 2 F (rounded up to whole pairs of
+// sums from dout (M x F), in rows of gp.ldz.  N is 2 F (rounded up to whole pairs of
 // blocks, 64).
 //
 // OUTF32: store the fp32 sums as they are (no bias, no rounding), for the
@@ -432,7 +432,7 @@ k_proj(const uint8_t* __restrict__ A, const uint8_t* __restrict__ B, const float
             d = __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(gp.dout)[gm * gp.F + f]) << 16);
           else
             d = static_cast<const float*>(gp.dout)[gm * gp.F + f];
-          T* const to = reinterpret_cast<T*>(C) + gm * 2 * gp.F + f;
+          T* const to = reinterpret_cast<T*>(C) + gm * gp.ldz + f;
           to[0] = pack(d * u * gated_slope(gp.silu, g));
           to[gp.F] = pack(d * gated_value(gp.silu, g));
         }

@@ -103,8 +103,8 @@ def test_the_newton_entry_points_refuse_the_gated_cells():
     (dict(N=1 << 31), {}, UNSUP), (dict(F=1 << 20, d=1 << 12), {}, UNSUP), (dict(N=(1 << 31) - 1, F=1 << 10), {}, UNSUP),
     (dict(), dict(x=None), BAD), (dict(), dict(W=None), BAD), (dict(), dict(g=None), BAD), (dict(), dict(x=FAKE + 8), BAD),
     (dict(), dict(W=FAKE + 4), BAD), (dict(), dict(g=FAKE + 2), BAD),
-    (dict(d=7, workspace=None, workspace_bytes=0), {}, WS), (dict(d=7, workspace_bytes=64), {}, WS),
-    (dict(d=7, workspace=FAKE + 16), {}, WS),
+    (dict(N=1000, F=800, d=7, workspace=None, workspace_bytes=0), {}, WS), (dict(N=1000, F=800, d=7, workspace_bytes=64), {}, WS),
+    (dict(N=1000, F=800, d=7, workspace=FAKE + 16), {}, WS),
 ])
 def test_ffn_refusals(kw, args, status):
     a = dict(x=FAKE, W=FAKE, g=FAKE)

@@ -59,7 +59,8 @@ def test_sizes(N, d, F, kind, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
-@pytest.mark.parametrize("N,d,F", [(4096, 32, 1536), (5000, 40, 1300), (12800, 24, 520)])
+@pytest.mark.parametrize("N,d,F", [(4096, 32, 1536), (5000, 40, 1300), (12800, 24, 520), (8200, 7, 515), (2500, 130, 1999),
+                                   (33000, 16, 33)])
 def test_large_tiles(N, d, F, dtype):
     _check(*_case(N, d, F, dtype), "silu", dtype)
 

@@ -93,6 +93,49 @@ def test_many_sequences(cell):
     _check(cell, _case(cell, 1, 3000, 20, torch.float32, cu), torch.float32)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("cell", ["glr", "glri"])
+@pytest.mark.parametrize("Bn,T,d", [(300, 150, 20), (130, 70, 260), (260, 1, 64), (256, 129, 64), (3, 256, 40), (3, 257, 40),
+                                    (1, 2049, 7), (2, 513, 128)])
+def test_on_either_side_of_a_limit(cell, Bn, T, d, dtype):
+    """Chains enough for a workgroup each, or not, and lengths about the chunks of both ways."""
+    _check(cell, _case(cell, Bn, T, d, dtype, h0=Bn % 2 == 0, seed=T), dtype)
+
+
+def test_a_long_chain():
+    """Hundreds of chunks of one chain: the look-back over more than 64 of them."""
+    for cell, dtype in (("glr", torch.float32), ("glri", torch.bfloat16)):
+        c = _case(cell, 1, 60000, 3, dtype)
+        _check(cell, c, dtype)
+
+
+def test_a_wait_that_gives_up(monkeypatch):
+    """PRN_SPIN_LIMIT=0: every wait gives up at once.  The kernel ends, the error word is set, what has no wait
+    before it is right and the rest NaN; without the limit the same call is right again and the word stays."""
+    c = _case("glr", 1, 3000, 64, torch.float32)
+    H, err = torch.empty(1, 3000, 64, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    n = max(f("glr", torch.float32, 1, 3000, 64) for f in (B.prn_gated_scan_workspace_bytes,
+                                                           B.prn_gated_scan_backward_workspace_bytes))
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    want = prn.gated_scan(c["x"], cell="glr", h0=c["h0"])
+    want_dx, _ = prn.gated_scan_backward(c["dH"], c["x"], want, cell="glr", h0=c["h0"])
+    dx = torch.empty_like(c["x"])
+    kw = dict(cell="glr", h0=c["h0"], workspace=ws, error_out=err)
+    monkeypatch.setenv("PRN_SPIN_LIMIT", "0")
+    B.prn_gated_scan(c["x"], H, **kw)
+    assert err.item() == B.PRN_FAULT_LOOKBACK
+    assert torch.equal(H[0, :256], want[0, :256]) and torch.isnan(H[0, 256:]).all()
+    err.zero_()
+    B.prn_gated_scan_backward(c["x"], want, c["dH"], dx, **kw)
+    assert err.item() == B.PRN_FAULT_LOOKBACK
+    last = 3000 // 128 * 128   # the last chunk's first step
+    assert torch.equal(dx[0, last:], want_dx[0, last:]) and torch.isnan(dx[0, :last]).all()
+    monkeypatch.delenv("PRN_SPIN_LIMIT")
+    B.prn_gated_scan(c["x"], H, **kw)
+    B.prn_gated_scan_backward(c["x"], H, c["dH"], dx, **kw)
+    assert torch.equal(H, want) and torch.equal(dx, want_dx) and err.item() == B.PRN_FAULT_LOOKBACK
+
+
 def test_no_step_and_no_row():
     """T = 0: the final state is the initial one, its gradient passes through."""
     for cu in (None, [0, 0, 0]):
