@@ -10,6 +10,7 @@ fails loudly (there is no fallback).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -803,6 +804,7 @@ def _scan_params(xproj, cell: str, cu_seqlens, state_last_out, workspace, stream
     return dev, p, rows
 
 
+@functools.lru_cache(maxsize=1024)   # of the sizes alone
 def prn_gated_scan_workspace_bytes(cell: str, dtype: torch.dtype, B: int, T: int, d_h: int, n_seqs: int = 0) -> int:
     p = prn_params(CELLS[cell], _storage(dtype), B, T, 0, d_h, n_seqs)
     return _bytes(lib().prn_gated_scan_workspace_bytes, p)
@@ -822,6 +824,7 @@ def prn_gated_scan(xproj, H_out, *, cell: str, h0=None, cu_seqlens=None, state_l
             _arg(H_out, "H_out", dt, (Bn, T, d), dev)))
 
 
+@functools.lru_cache(maxsize=1024)   # of the sizes alone
 def prn_gated_scan_backward_workspace_bytes(cell: str, dtype: torch.dtype, B: int, T: int, d_h: int,
                                             n_seqs: int = 0) -> int:
     p = prn_params(CELLS[cell], _storage(dtype), B, T, 0, d_h, n_seqs)
@@ -857,6 +860,7 @@ def _ffn_params(x, W, act: str, workspace, stream):
     return dev, prn_gated_ffn_params(code, ACTS[act], N, d, F, ws, ws_bytes, _handle(stream, dev)), N, d, F
 
 
+@functools.lru_cache(maxsize=1024)   # of the sizes alone
 def prn_gated_ffn_workspace_bytes(dtype: torch.dtype, N: int, d: int, F: int) -> int:
     return _bytes(lib().prn_gated_ffn_workspace_bytes, prn_gated_ffn_params(_storage(dtype), 0, N, d, F))
 
@@ -870,6 +874,7 @@ def prn_gated_ffn(x, W, out, *, act: str = "silu", workspace=None, stream=None) 
                                    _arg(out, "out", dt, (N, F), dev)))
 
 
+@functools.lru_cache(maxsize=1024)   # of the sizes alone
 def prn_gated_ffn_backward_workspace_bytes(dtype: torch.dtype, N: int, d: int, F: int) -> int:
     return _bytes(lib().prn_gated_ffn_backward_workspace_bytes, prn_gated_ffn_params(_storage(dtype), 0, N, d, F))
 

@@ -37,24 +37,30 @@ namespace {
 using Big = MmTile<2, 4, 4, 2, 64, 2>;
 using Wide = MmTile<4, 2, 2, 3, 64, 2>;
 
-// A copy of rows of d values as rows of ldp, zeros past d and past row R, of
-// Rp rows; parts of R rows each, one after the other.  A thread per 16 bytes.
+// Copies of rows of d values as rows of ldp, zeros past d, a thread per 16 bytes:
+// x (N rows) to xp, then W (two halves of F rows) to wp, the halves Fw rows each,
+// zeros past F.  Nx or Fw = 0: not that one.
 template <class T>
-__global__ void __launch_bounds__(256) k_ffn_pad(const T* __restrict__ in, int64_t parts, int64_t R, int64_t Rp, int64_t d,
-                                                 int64_t ldp, T* __restrict__ out) {
+__global__ void __launch_bounds__(256) k_ffn_pad(const T* __restrict__ x, int64_t Nx, const T* __restrict__ W, int64_t F,
+                                                 int64_t Fw, int64_t d, int64_t ldp, T* __restrict__ xp, T* __restrict__ wp) {
   constexpr int V = 16 / sizeof(T);
   const int64_t C = ldp / V, i = block_in_rows() * 256 + threadIdx.x;
-  if (i >= parts * Rp * C) return;
-  const int64_t to = i / C, c0 = (i - to * C) * V, part = to / Rp, r = to - part * Rp;
-  const T* const from = in + (part * R + r) * d + c0;
+  int64_t to = i / C;
+  const int64_t c0 = (i - to * C) * V;
+  const bool is_x = to < Nx;
+  if (!is_x) to -= Nx;
+  if (!is_x && to >= 2 * Fw) return;
+  const int64_t half = !is_x && to >= Fw, r = to - half * Fw;
+  const bool there = is_x || r < F;
+  const T* const from = is_x ? x + r * d + c0 : W + (half * F + r) * d + c0;
   T v[V];
-  if (r < R && c0 + V <= d) {
+  if (there && c0 + V <= d) {
     __builtin_memcpy(v, from, sizeof(v));   // aligned or not
   } else {
 #pragma unroll
-    for (int e = 0; e < V; ++e) v[e] = r < R && c0 + e < d ? from[e] : T(0);
+    for (int e = 0; e < V; ++e) v[e] = there && c0 + e < d ? from[e] : T(0);
   }
-  __builtin_memcpy(__builtin_assume_aligned(out + to * ldp + c0, 16), v, sizeof(v));
+  __builtin_memcpy(__builtin_assume_aligned((is_x ? xp : wp) + to * ldp + c0, 16), v, sizeof(v));
 }
 
 // ---------------------------------------------------- blocks of values ----
@@ -444,16 +450,18 @@ struct Operands {
   const void *x, *W;
 };
 Operands lay_out(const GatedFfnArgs& a, const Plan& p, const void* x, const void* W) {
-  auto pad = [&](const void* in, int64_t parts, int64_t R, int64_t Rp, size_t off) {
-    void* const to = a.ws + off;
-    const dim3 grid = rows_of_blocks(cdiv(parts * Rp * (p.ldp / (a.bf16 ? 8 : 4)), 256));
-    if (a.bf16)
-      k_ffn_pad<uint16_t><<<grid, 256, 0, a.stream>>>(static_cast<const uint16_t*>(in), parts, R, Rp, a.d, p.ldp, static_cast<uint16_t*>(to));
-    else
-      k_ffn_pad<float><<<grid, 256, 0, a.stream>>>(static_cast<const float*>(in), parts, R, Rp, a.d, p.ldp, static_cast<float*>(to));
-    return to;
+  void *const xp = a.ws + p.x_off, *const wp = a.ws + p.w_off;
+  const int64_t Nx = p.pad_x ? a.N : 0, Fw = p.pad_w ? p.Fw : 0;
+  const dim3 grid = rows_of_blocks(cdiv((Nx + 2 * Fw) * (p.ldp / (a.bf16 ? 8 : 4)), 256));
+  auto go = [&](auto zero) {
+    using T = decltype(zero);
+    k_ffn_pad<T><<<grid, 256, 0, a.stream>>>(static_cast<const T*>(x), Nx, static_cast<const T*>(W), a.F, Fw, a.d, p.ldp,
+                                             static_cast<T*>(xp), static_cast<T*>(wp));
   };
-  return {p.pad_x ? pad(x, 1, a.N, a.N, p.x_off) : x, p.pad_w ? pad(W, 2, a.F, p.Fw, p.w_off) : W};
+  if (Nx + Fw > 0) {
+    if (a.bf16) go(uint16_t(0)); else go(0.0f);
+  }
+  return {p.pad_x ? xp : x, p.pad_w ? wp : W};
 }
 
 void fill_zero(const GatedFfnArgs& a, void* out, int64_t R, int64_t c0, int64_t ld) {

@@ -202,12 +202,6 @@ __device__ __forceinline__ void look_back(const Records& rec, int64_t base, int6
   }
 }
 
-// clears the words that a call's records begin with
-__global__ void __launch_bounds__(256) k_scan_clear(unsigned* __restrict__ words, int64_t n) {
-  const int64_t i = block_in_rows() * 256 + threadIdx.x;
-  if (i < n) words[i] = 0;
-}
-
 // A workgroup's place: its lane's channels and its wave's steps are of chain
 // (row, tile of channels).
 template <int V>
@@ -584,12 +578,18 @@ __global__ void __launch_bounds__(64 * NW) k_scan_pass_back(Tensors<DT> t, Recor
   w.walk(t, at, h, m);
 }
 
-// out[j] = in[j] (0 without in) of the sequences of a pack that have no step,
-// or, without cu, of every row
+// What comes before: the words that a call's records begin with become zero, and
+// out[j] = in[j] (0 without in) for the sequences of a pack that have no step, or,
+// without cu, for every row.
 template <class T>
-__global__ void __launch_bounds__(256) k_scan_empty(const int32_t* __restrict__ cu, int64_t rows, int64_t d,
-                                                    const T* __restrict__ in, T* __restrict__ out) {
-  const int64_t i = block_in_rows() * 256 + threadIdx.x;
+__global__ void __launch_bounds__(256) k_scan_begin(unsigned* __restrict__ words, int64_t n, const int32_t* __restrict__ cu,
+                                                    int64_t rows, int64_t d, const T* __restrict__ in, T* __restrict__ out) {
+  int64_t i = block_in_rows() * 256 + threadIdx.x;
+  if (i < n) {
+    words[i] = 0;
+    return;
+  }
+  i -= n;
   if (i >= rows * d) return;
   const int64_t j = i / d;
   if (cu && cu[j + 1] > cu[j]) return;
@@ -675,13 +675,20 @@ void typed(const GatedScanArgs& a, int V, F go) {
     gates(integral_constant<int, kBF16>{}, integral_constant<int, 1>{});
 }
 
-void fill_empty(const GatedScanArgs& a, const void* in, void* out) {
-  const int64_t rows = a.n_seqs > 0 ? a.n_seqs : a.B;
-  const dim3 grid = rows_of_blocks(cdiv(rows * a.d, 256));
-  if (a.bf16)
-    k_scan_empty<uint16_t><<<grid, 256, 0, a.stream>>>(a.cu, rows, a.d, static_cast<const uint16_t*>(in), static_cast<uint16_t*>(out));
-  else
-    k_scan_empty<float><<<grid, 256, 0, a.stream>>>(a.cu, rows, a.d, static_cast<const float*>(in), static_cast<float*>(out));
+// the records of a call that has some, and `out` of the sequences without a step
+Records begin(const GatedScanArgs& a, const Plan& p, const void* in, void* out) {
+  unsigned* const words = reinterpret_cast<unsigned*>(a.ws);
+  const int64_t rows = !out || (a.n_seqs == 0 && a.T > 0) ? 0 : a.n_seqs > 0 ? a.n_seqs : a.B;
+  const int64_t n = static_cast<int64_t>(p.words) + rows * a.d;
+  const dim3 grid = rows_of_blocks(cdiv(n, 256));
+  if (n > 0 && a.bf16)
+    k_scan_begin<uint16_t><<<grid, 256, 0, a.stream>>>(words, p.words, a.cu, rows, a.d, static_cast<const uint16_t*>(in),
+                                                       static_cast<uint16_t*>(out));
+  else if (n > 0)
+    k_scan_begin<float><<<grid, 256, 0, a.stream>>>(words, p.words, a.cu, rows, a.d, static_cast<const float*>(in),
+                                                    static_cast<float*>(out));
+  return {words, a.error ? a.error : words + 1, words + 2, reinterpret_cast<float*>(a.ws + p.maps_off),
+          reinterpret_cast<float*>(a.ws + p.states_off)};
 }
 
 template <int DT>
@@ -690,13 +697,6 @@ Tensors<DT> tensors_of(const GatedScanArgs& a, const Plan& p) {
   return {static_cast<const T*>(a.xproj), static_cast<const T*>(a.h0), static_cast<const T*>(a.dH), static_cast<const T*>(a.dlast),
           static_cast<T*>(a.H), static_cast<T*>(a.last), static_cast<T*>(a.dxproj), static_cast<T*>(a.dh0),
           a.cu, a.n_seqs, a.B, a.T, a.d, p.chains, p.chunks};
-}
-
-Records records_of(const GatedScanArgs& a, const Plan& p) {
-  unsigned* const words = reinterpret_cast<unsigned*>(a.ws);
-  k_scan_clear<<<rows_of_blocks(cdiv(p.words, 256)), 256, 0, a.stream>>>(words, p.words);
-  return {words, a.error ? a.error : words + 1, words + 2, reinterpret_cast<float*>(a.ws + p.maps_off),
-          reinterpret_cast<float*>(a.ws + p.states_off)};
 }
 
 }  // namespace
@@ -709,10 +709,9 @@ size_t gated_scan_workspace(const GatedScanArgs& a) { return plan_of(a, false).t
 size_t gated_scan_backward_workspace(const GatedScanArgs& a) { return plan_of(a, true).total; }
 
 void launch_gated_scan(const GatedScanArgs& a) {
-  if (a.last && (a.n_seqs > 0 || a.T == 0)) fill_empty(a, a.h0, a.last);
-  if (a.T == 0) return;
   const Plan p = plan_of(a, false);
-  const Records rec = p.pass ? records_of(a, p) : Records{};
+  const Records rec = begin(a, p, a.h0, a.last);
+  if (a.T == 0) return;
   typed(a, p.V, [&](auto dt, auto g, auto v, auto ragged) {
     constexpr int DT = decltype(dt)::value, G = decltype(g)::value, V = decltype(v)::value;
     constexpr bool RAGGED = decltype(ragged)::value;
@@ -727,10 +726,9 @@ void launch_gated_scan(const GatedScanArgs& a) {
 }
 
 void launch_gated_scan_backward(const GatedScanArgs& a) {
-  if (a.dh0 && (a.n_seqs > 0 || a.T == 0)) fill_empty(a, a.dlast, a.dh0);
-  if (a.T == 0) return;
   const Plan p = plan_of(a, true);
-  const Records rec = p.pass ? records_of(a, p) : Records{};
+  const Records rec = begin(a, p, a.dlast, a.dh0);
+  if (a.T == 0) return;
   typed(a, p.V, [&](auto dt, auto g, auto v, auto ragged) {
     constexpr int DT = decltype(dt)::value, G = decltype(g)::value, V = decltype(v)::value;
     constexpr bool RAGGED = decltype(ragged)::value;

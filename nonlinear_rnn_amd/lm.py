@@ -302,7 +302,7 @@ def dropout(x, p: float, *, seed, offset: int = 0, residual=None) -> torch.Tenso
     _shaped(x.shape, residual=residual)
     x2 = _dense(x)
     r2 = None if residual is None else _dense(residual)
-    out = torch.empty(x2.shape, dtype=x2.dtype, device=x2.device)
+    out = torch.empty_like(x2)
     if isinstance(seed, torch.Tensor):
         if offset:
             raise ValueError("a seed on the device holds its offset itself")
