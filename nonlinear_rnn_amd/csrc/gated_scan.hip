@@ -29,6 +29,11 @@
 // A sequence's first step in a pack cuts the map: h_in does not count, whatever
 // it is (a NaN of the sequence before stays there).  Since a >= 0 otherwise,
 // a = -0 says so, and stays -0 in every product with what comes after.
+//
+// Next to the memory traffic, what counts is the arithmetic: a gate is an
+// exponential and a quotient, 16 cycles of a wave each.  Rows are addressed from
+// scalar registers, batches without sequences do without cuts, and whole chunks
+// without bounds.
 #include "gated_scan.h"
 
 #include <algorithm>
@@ -48,10 +53,15 @@ __device__ __forceinline__ bool is_cut(float a) { return __float_as_uint(a) == 0
 struct Map {
   float a, b;
 };
-__device__ __forceinline__ float through(const Map& m, float h) { return is_cut(m.a) ? m.b : fmaf(m.a, h, m.b); }
+// CUTS: may the map be a cut (of a pack)?
+template <bool CUTS>
+__device__ __forceinline__ float through(const Map& m, float h) {
+  return CUTS && is_cut(m.a) ? m.b : fmaf(m.a, h, m.b);
+}
 // first m1, then m2
+template <bool CUTS>
 __device__ __forceinline__ Map then(const Map& m1, const Map& m2) {
-  return {is_cut(m2.a) ? kCut : m2.a * m1.a, through(m2, m1.b)};
+  return {CUTS && is_cut(m2.a) ? kCut : m2.a * m1.a, through<CUTS>(m2, m1.b)};
 }
 
 // a barrier for what waves hand over in LDS; global loads stay in flight
@@ -66,8 +76,24 @@ struct Chans {
   T v[V];
   __device__ __forceinline__ void load(const T* p) { __builtin_memcpy(v, __builtin_assume_aligned(p, V * sizeof(T)), sizeof(v)); }
   __device__ __forceinline__ void store(T* p) const { __builtin_memcpy(__builtin_assume_aligned(p, V * sizeof(T)), v, sizeof(v)); }
+  // of a row in scalar registers, from its element off on (32-bit byte offsets, as the instructions have them)
+  __device__ __forceinline__ void load(const T* row, uint32_t off) {
+    load(reinterpret_cast<const T*>(reinterpret_cast<const uint8_t*>(row) + off * static_cast<uint32_t>(sizeof(T))));
+  }
+  __device__ __forceinline__ void store(T* row, uint32_t off) const {
+    store(reinterpret_cast<T*>(reinterpret_cast<uint8_t*>(row) + off * static_cast<uint32_t>(sizeof(T))));
+  }
   __device__ __forceinline__ float at(int c) const { return Storage<DT>::load(&v[c]); }
-  __device__ __forceinline__ void set(int c, float x) { v[c] = Storage<DT>::pack(x); }
+  __device__ __forceinline__ void set(const float (&x)[V]) {
+    if constexpr (DT == kBF16 && V == 2) {   // one conversion of both
+      typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
+      const bf16x2 p{static_cast<__bf16>(x[0]), static_cast<__bf16>(x[1])};
+      __builtin_memcpy(v, &p, sizeof(v));
+    } else {
+#pragma unroll
+      for (int c = 0; c < V; ++c) v[c] = Storage<DT>::pack(x[c]);
+    }
+  }
 };
 
 // Where the sequences of a pack begin and end among a wave's steps: bit j of
@@ -138,7 +164,7 @@ __device__ __forceinline__ void announce(unsigned* status, unsigned v, int lane)
 }
 
 // the state before chunk c > 0 of the chain whose records begin at `base`, by a whole wave
-template <int V>
+template <int V, bool CUTS>
 __device__ __forceinline__ void look_back(const Records& rec, int64_t base, int64_t c, const Map (&own)[V], int lane,
                                           unsigned spin_limit, bool map_first, float (&e)[V]) {
   constexpr int kAhead = 16 / V;   // maps under way at once
@@ -188,7 +214,7 @@ __device__ __forceinline__ void look_back(const Records& rec, int64_t base, int6
         for (int k = 0; k < kAhead; ++k)
           if (r + k < n) {
 #pragma unroll
-            for (int v = 0; v < V; ++v) e[v] = through(m[k][v], e[v]);
+            for (int v = 0; v < V; ++v) e[v] = through<CUTS>(m[k][v], e[v]);
           }
       }
       return;
@@ -207,17 +233,20 @@ __device__ __forceinline__ void look_back(const Records& rec, int64_t base, int6
 template <int V>
 struct Place {
   int lane, wave;
-  int64_t chain, row, c0;   // c0: this lane's first channel, kept in range
-  bool live;                // has this lane channels of its own?
+  int64_t chain, row, tile;   // tile: its first channel
+  uint32_t off;               // this lane's first channel from there, kept in range
+  bool live;                  // has this lane channels of its own?
   __device__ __forceinline__ Place(int64_t d, int64_t chain_) {
     lane = threadIdx.x & 63;
     wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t tiles = (d + 64 * V - 1) / (64 * V);
     chain = chain_;
     row = chain / tiles;
-    c0 = (chain - row * tiles) * 64 * V + lane * V;
-    live = c0 < d;
-    if (!live) c0 = d - V;
+    tile = (chain - row * tiles) * 64 * V;
+    const uint32_t left = static_cast<uint32_t>(imin(d - tile, 64 * V));   // a multiple of V
+    off = lane * V;
+    live = off < left;
+    if (!live) off = left - V;
   }
 };
 
@@ -236,57 +265,66 @@ struct Fore {
   __device__ __forceinline__ void load(const Tensors<DT>& t, const Place<V>& at, int64_t first) {
     s0 = first + at.wave * LS;
     n = static_cast<int>(imax(imin(LS, t.T_ - s0), 0));
-    const typename C::T* const x = t.x + at.row * t.T_ * G * t.d + at.c0;
+    const typename C::T* const x = t.x + at.row * t.T_ * G * t.d + at.tile;
 #pragma unroll
     for (int j = 0; j < LS; ++j) {
       const int64_t step = imin(s0 + j, t.T_ - 1);   // past the end: the last one, not used
 #pragma unroll
-      for (int g = 0; g < G; ++g) q[j][g].load(x + (step * G + g) * t.d);
+      for (int g = 0; g < G; ++g) q[j][g].load(x + (step * G + g) * t.d, at.off);
     }
   }
-  // the steps' maps, and the map of them all
-  __device__ __forceinline__ void maps(const Tensors<DT>& t, const Place<V>& at, Map (&m)[V]) {
-    if constexpr (RAGGED) cut.find(t.cu, t.n_seqs, s0, n, t.T_);
-#pragma unroll
-    for (int c = 0; c < V; ++c) m[c] = {1.0f, 0.0f};
+  // the steps' maps, and the map of them all; ALL: n = LS
+  template <bool ALL>
+  __device__ __forceinline__ void maps_of(const Tensors<DT>& t, const Place<V>& at, Map (&m)[V]) {
 #pragma unroll
     for (int j = 0; j < LS; ++j) {
-      const bool here = RAGGED && j < n && ((cut.head >> j) & 1);
+      const bool here = RAGGED && (ALL || j < n) && ((cut.head >> j) & 1);
 #pragma unroll
       for (int c = 0; c < V; ++c) {
         const Gate f = gate_of(q[j][0].at(c));
         s[j][c] = {f.on, (G == 2 ? f.off : gate_of(q[j][1].at(c)).on) * q[j][G - 1].at(c)};
         if (here) {
-          if (t.h0) s[j][c].b = fmaf(f.on, Storage<DT>::load(t.h0 + static_cast<int64_t>(cut.seg[j]) * t.d + at.c0 + c), s[j][c].b);
+          if (t.h0) s[j][c].b = fmaf(f.on, Storage<DT>::load(t.h0 + static_cast<int64_t>(cut.seg[j]) * t.d + at.tile + at.off + c), s[j][c].b);
           s[j][c].a = kCut;
         }
-        if (j < n) m[c] = then(m[c], s[j][c]);
+        if (j == 0 && ALL)
+          m[c] = s[0][c];
+        else if (ALL || j < n)
+          m[c] = then<RAGGED>(m[c], s[j][c]);
       }
     }
   }
+  __device__ __forceinline__ void maps(const Tensors<DT>& t, const Place<V>& at, Map (&m)[V]) {
+    if constexpr (RAGGED) cut.find(t.cu, t.n_seqs, s0, n, t.T_);
+#pragma unroll
+    for (int c = 0; c < V; ++c) m[c] = {1.0f, 0.0f};
+    if (n == LS) maps_of<true>(t, at, m); else maps_of<false>(t, at, m);
+  }
   // the states from the one before the steps
-  __device__ __forceinline__ void walk(const Tensors<DT>& t, const Place<V>& at, float (&h)[V]) {
-    typename C::T* const H = t.H + at.row * t.T_ * t.d + at.c0;
+  template <bool ALL>
+  __device__ __forceinline__ void walk_of(const Tensors<DT>& t, const Place<V>& at, float (&h)[V]) {
+    typename C::T* const H = t.H + (at.row * t.T_ + s0) * t.d + at.tile;
 #pragma unroll
     for (int j = 0; j < LS; ++j) {
-      if (j >= n) continue;
+      if (!ALL && j >= n) continue;
       C o;
 #pragma unroll
-      for (int c = 0; c < V; ++c) {
-        h[c] = through(s[j][c], h[c]);
-        o.set(c, h[c]);
-      }
+      for (int c = 0; c < V; ++c) h[c] = through<RAGGED>(s[j][c], h[c]);
+      o.set(h);
       if (at.live) {
-        o.store(H + (s0 + j) * t.d);
+        o.store(H + j * t.d, at.off);
         if (t.last && (RAGGED ? (cut.tail >> j) & 1 : s0 + j == t.T_ - 1))
-          o.store(t.last + (RAGGED ? cut.seg[j] : at.row) * t.d + at.c0);
+          o.store(t.last + (RAGGED ? cut.seg[j] : at.row) * t.d + at.tile, at.off);
       }
     }
+  }
+  __device__ __forceinline__ void walk(const Tensors<DT>& t, const Place<V>& at, float (&h)[V]) {
+    if (n == LS) walk_of<true>(t, at, h); else walk_of<false>(t, at, h);
   }
   // the state before the row
   static __device__ __forceinline__ void start(const Tensors<DT>& t, const Place<V>& at, float (&h)[V]) {
 #pragma unroll
-    for (int c = 0; c < V; ++c) h[c] = !RAGGED && t.h0 ? Storage<DT>::load(t.h0 + at.row * t.d + at.c0 + c) : 0.0f;
+    for (int c = 0; c < V; ++c) h[c] = !RAGGED && t.h0 ? Storage<DT>::load(t.h0 + at.row * t.d + at.tile + at.off + c) : 0.0f;
   }
 };
 
@@ -315,7 +353,7 @@ __global__ void __launch_bounds__(64 * NW) k_scan_walk(Tensors<DT> t) {
 #pragma unroll
       for (int c = 0; c < V; ++c) {
         if (v == at.wave) mine[c] = h[c];
-        h[c] = through(p[v][c][at.lane], h[c]);
+        h[c] = through<RAGGED>(p[v][c][at.lane], h[c]);
       }
     }
     now.walk(t, at, mine);
@@ -337,7 +375,7 @@ __device__ __forceinline__ int64_t take_ticket(unsigned* ticket, unsigned* share
 // walk: order(0), order(1), ..) become their carries (the first number of their
 // slots), and the chunk's records are published; e: the carry of a chain's first
 // chunk.  The state's status goes out by announce after the barrier that follows.
-template <int V, int NW, class Order>
+template <int V, int NW, bool CUTS, class Order>
 __device__ __forceinline__ void join(const Records& rec, int64_t base, int64_t c, int lane, unsigned spin_limit,
                                      bool map_first, Map (*part)[V][64], float (&e)[V], Order order) {
   Map tot[V];
@@ -346,18 +384,18 @@ __device__ __forceinline__ void join(const Records& rec, int64_t base, int64_t c
 #pragma unroll
   for (int w = 1; w < NW; ++w)
 #pragma unroll
-    for (int v = 0; v < V; ++v) tot[v] = then(tot[v], part[order(w)][v][lane]);
-  if (c > 0) look_back<V>(rec, base, c, tot, lane, spin_limit, map_first, e);
+    for (int v = 0; v < V; ++v) tot[v] = then<CUTS>(tot[v], part[order(w)][v][lane]);
+  if (c > 0) look_back<V, CUTS>(rec, base, c, tot, lane, spin_limit, map_first, e);
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    put(rec.states + (base + c) * V * 64 + v * 64 + lane, through(tot[v], e[v]));
+    put(rec.states + (base + c) * V * 64 + v * 64 + lane, through<CUTS>(tot[v], e[v]));
     float h = e[v];
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
       Map& slot = part[order(w)][v][lane];
       const Map m = slot;
       slot.a = h;
-      h = through(m, h);
+      h = through<CUTS>(m, h);
     }
   }
 }
@@ -381,7 +419,7 @@ __global__ void __launch_bounds__(64 * NW) k_scan_pass(Tensors<DT> t, Records re
   if (at.wave == NW - 1) {
     float e[V];
     W::start(t, at, e);
-    join<V, NW>(rec, base, c, at.lane, spin_limit, map_first, part, e, [](int k) { return k; });
+    join<V, NW, RAGGED>(rec, base, c, at.lane, spin_limit, map_first, part, e, [](int k) { return k; });
   }
   lds_barrier();
   if (at.wave == NW - 1) announce(rec.status + base + c, kState, at.lane);
@@ -416,23 +454,23 @@ struct Back {
     for (int j = 0; j < LS; ++j) {
       const int64_t step = row + imin(s0 + j, t.T_ - 1);   // past the end: the last one, not used
 #pragma unroll
-      for (int k = 0; k < G; ++k) x[j][k].load(t.x + (step * G + k) * t.d + at.c0);
-      dh[j].load(t.dH + step * t.d + at.c0);
+      for (int k = 0; k < G; ++k) x[j][k].load(t.x + (step * G + k) * t.d + at.tile, at.off);
+      dh[j].load(t.dH + step * t.d + at.tile, at.off);
     }
     if (first > 0) {
-      before.load(t.H + (row + first - 1) * t.d + at.c0);
+      before.load(t.H + (row + first - 1) * t.d + at.tile, at.off);
     } else if (!RAGGED && t.h0) {
-      before.load(t.h0 + at.row * t.d + at.c0);
+      before.load(t.h0 + at.row * t.d + at.tile, at.off);
     } else {
-#pragma unroll
-      for (int c = 0; c < V; ++c) before.set(c, 0.0f);
+      before = {};
     }
   }
-  // the maps of the states over the steps, and of the gradient back over them
-  __device__ __forceinline__ void maps(const Tensors<DT>& t, const Place<V>& at, Map (&fore)[V], Map (&back)[V]) {
-    if constexpr (RAGGED) cut.find(t.cu, t.n_seqs, s0, n, t.T_);
-#pragma unroll
-    for (int c = 0; c < V; ++c) fore[c] = back[c] = {1.0f, 0.0f};
+  __device__ __forceinline__ float one(const typename C::T* states, int j, int c, const Tensors<DT>& t, const Place<V>& at) const {
+    return ST::load(states + seg(j, at) * t.d + at.tile + at.off + c);
+  }
+  // the maps of the states over the steps, and of the gradient back over them; ALL: n = LS
+  template <bool ALL>
+  __device__ __forceinline__ void maps_of(const Tensors<DT>& t, const Place<V>& at, Map (&fore)[V], Map (&back)[V]) {
 #pragma unroll
     for (int j = 0; j < LS; ++j) {
 #pragma unroll
@@ -440,55 +478,75 @@ struct Back {
         f[j][c] = gate_of(x[j][0].at(c));
         i[j][c] = G == 2 ? Gate{f[j][c].off, f[j][c].on} : gate_of(x[j][1].at(c));
         g[j][c] = dh[j].at(c);
-        if (j < n && t.dlast && (RAGGED ? tail(j) : s0 + j == t.T_ - 1)) g[j][c] += ST::load(t.dlast + seg(j, at) * t.d + at.c0 + c);
+        if (!ALL && j >= n) continue;
+        if (t.dlast && (RAGGED ? tail(j) : s0 + j == t.T_ - 1)) g[j][c] += one(t.dlast, j, c, t, at);
         Map m = {f[j][c].on, i[j][c].on * x[j][G - 1].at(c)};
-        if (RAGGED && j < n && head(j)) {
-          if (t.h0) m.b = fmaf(m.a, ST::load(t.h0 + seg(j, at) * t.d + at.c0 + c), m.b);
+        if (head(j)) {
+          if (t.h0) m.b = fmaf(m.a, one(t.h0, j, c, t, at), m.b);
           m.a = kCut;
         }
-        if (j < n) fore[c] = then(fore[c], m);
+        fore[c] = ALL && j == 0 ? m : then<RAGGED>(fore[c], m);
       }
     }
 #pragma unroll
     for (int j = LS - 1; j >= 0; --j) {
-      if (j >= n) continue;
+      if (!ALL && j >= n) continue;
 #pragma unroll
-      for (int c = 0; c < V; ++c) back[c] = then(back[c], Map{tail(j) ? kCut : f[j][c].on, f[j][c].on * g[j][c]});
+      for (int c = 0; c < V; ++c) {
+        const Map m = {tail(j) ? kCut : f[j][c].on, f[j][c].on * g[j][c]};
+        back[c] = ALL && j == LS - 1 ? m : then<RAGGED>(back[c], m);
+      }
     }
   }
+  __device__ __forceinline__ void maps(const Tensors<DT>& t, const Place<V>& at, Map (&fore)[V], Map (&back)[V]) {
+    if constexpr (RAGGED) cut.find(t.cu, t.n_seqs, s0, n, t.T_);
+#pragma unroll
+    for (int c = 0; c < V; ++c) fore[c] = back[c] = {1.0f, 0.0f};
+    if (n == LS) maps_of<true>(t, at, fore, back); else maps_of<false>(t, at, fore, back);
+  }
   // the gradients, from the state before the steps and the gradient that arrives at their last state from after it
-  __device__ __forceinline__ void walk(const Tensors<DT>& t, const Place<V>& at, float (&h)[V], float (&m)[V]) {
+  template <bool ALL>
+  __device__ __forceinline__ void walk_of(const Tensors<DT>& t, const Place<V>& at, float (&h)[V], float (&m)[V]) {
     float prev[LS][V];
 #pragma unroll
     for (int j = 0; j < LS; ++j) {
-      if (j >= n) continue;
+      if (!ALL && j >= n) continue;
 #pragma unroll
       for (int c = 0; c < V; ++c) {
-        if (head(j)) h[c] = t.h0 ? ST::load(t.h0 + seg(j, at) * t.d + at.c0 + c) : 0.0f;
+        if (head(j)) h[c] = t.h0 ? one(t.h0, j, c, t, at) : 0.0f;
         prev[j][c] = h[c];
         h[c] = fmaf(f[j][c].on, h[c], i[j][c].on * x[j][G - 1].at(c));
       }
     }
-    typename ST::T* const dx = t.dx + at.row * t.T_ * G * t.d + at.c0;
+    typename ST::T* const dx = t.dx + (at.row * t.T_ + s0) * G * t.d + at.tile;
 #pragma unroll
     for (int j = LS - 1; j >= 0; --j) {
-      if (j >= n) continue;
-      C o[G], out;
+      if (!ALL && j >= n) continue;
+      float o[G][V];
 #pragma unroll
       for (int c = 0; c < V; ++c) {
         const float lam = tail(j) ? g[j][c] : g[j][c] + m[c], val = x[j][G - 1].at(c);
-        o[0].set(c, lam * (G == 2 ? prev[j][c] - val : prev[j][c]) * (f[j][c].on * f[j][c].off));
-        if constexpr (G == 3) o[1].set(c, lam * val * (i[j][c].on * i[j][c].off));
-        o[G - 1].set(c, lam * i[j][c].on);
+        o[0][c] = lam * (G == 2 ? prev[j][c] - val : prev[j][c]) * (f[j][c].on * f[j][c].off);
+        if constexpr (G == 3) o[1][c] = lam * val * (i[j][c].on * i[j][c].off);
+        o[G - 1][c] = lam * i[j][c].on;
         m[c] = f[j][c].on * lam;
-        out.set(c, m[c]);
       }
       if (at.live) {
+        C out;
 #pragma unroll
-        for (int k = 0; k < G; ++k) o[k].store(dx + ((s0 + j) * G + k) * t.d);
-        if (t.dh0 && (RAGGED ? head(j) : s0 + j == 0)) out.store(t.dh0 + seg(j, at) * t.d + at.c0);
+        for (int k = 0; k < G; ++k) {
+          out.set(o[k]);
+          out.store(dx + (j * G + k) * t.d, at.off);
+        }
+        if (t.dh0 && (RAGGED ? head(j) : s0 + j == 0)) {
+          out.set(m);
+          out.store(t.dh0 + seg(j, at) * t.d + at.tile, at.off);
+        }
       }
     }
+  }
+  __device__ __forceinline__ void walk(const Tensors<DT>& t, const Place<V>& at, float (&h)[V], float (&m)[V]) {
+    if (n == LS) walk_of<true>(t, at, h, m); else walk_of<false>(t, at, h, m);
   }
   // the state before this wave's steps, through the waves' maps before it
   template <int NW>
@@ -499,7 +557,7 @@ struct Back {
     for (int w = 0; w < NW - 1; ++w) {
       if (w >= at.wave) break;
 #pragma unroll
-      for (int c = 0; c < V; ++c) h[c] = through(fore[w][c][at.lane], h[c]);
+      for (int c = 0; c < V; ++c) h[c] = through<RAGGED>(fore[w][c][at.lane], h[c]);
     }
   }
 };
@@ -535,7 +593,7 @@ __global__ void __launch_bounds__(64 * NW) k_scan_walk_back(Tensors<DT> t) {
 #pragma unroll
       for (int c = 0; c < V; ++c) {
         if (v == at.wave) m[c] = mu[c];
-        mu[c] = through(pb[v][c][at.lane], mu[c]);
+        mu[c] = through<RAGGED>(pb[v][c][at.lane], mu[c]);
       }
     }
     now.walk(t, at, h, m);
@@ -567,7 +625,7 @@ __global__ void __launch_bounds__(64 * NW) k_scan_pass_back(Tensors<DT> t, Recor
   const int64_t base = at.chain * t.chunks;
   if (at.wave == NW - 1) {
     float e[V] = {};
-    join<V, NW>(rec, base, c, at.lane, spin_limit, map_first, back, e, [](int k) { return NW - 1 - k; });
+    join<V, NW, RAGGED>(rec, base, c, at.lane, spin_limit, map_first, back, e, [](int k) { return NW - 1 - k; });
   }
   lds_barrier();
   if (at.wave == NW - 1) announce(rec.status + base + c, kState, at.lane);
@@ -603,22 +661,20 @@ size_t up(size_t x) { return (x + 255) / 256 * 256; }
 
 // Chains from which a workgroup each fills the device, and steps up to which a
 // few chunks one after another take no longer than the look-back and the launch
-// that clears its records.  (Before the look-back the maps of 512 stretches of
-// time were taken by a kernel of their own, which reads the inputs twice: 43 and
-// 65 us for 8 x 4096 x 512 bf16, 284 and 400 for 2 x 131072 x 256 fp32, where it
-// takes 34 and 54, 186 and 285.)
+// that clears its records.  (Taking the maps of 512 stretches of time first, by a
+// kernel of their own that reads the inputs once more, took 43 and 65 us for 8 x
+// 4096 x 512 bf16, 284 and 400 for 2 x 131072 x 256 fp32, where look-back takes 29
+// and 46, 174 and 272.  Tiles of 16 channels, so that every one of 8 x 512 has a
+// chain that fills the device: 40 and 73.)
 constexpr int64_t kEnough = 256, kShort = 256;
 // Steps of a wave and waves of a workgroup.  A longer chunk means fewer
-// look-backs in a row, as long as the registers allow a workgroup of it, and
-// two of the smaller ones, on a CU.  us, glr, 2 x 131072 x 256 fp32 and 8 x 4096 x
-// 512 bf16, steps x waves:
-//   forward   16 x 16 186 and 34, 12 x 16 207 and 36, 8 x 16 241 and 38, 16 x 12 205
-//             and 36, 24 x 8 196 and 40, 16 x 8 207 and 38
-//   backward  16 x 8 285 and 58, 12 x 8 308 and 63, 8 x 16 305 and 54, 8 x 8 355 and 56,
-//             4 x 16 443 and 67; glri fp32, a pack of 20011 x 250: 8 x 16 50, 16 x 8 58
-// and where a workgroup has its chain (64 x 1024 x 512 bf16, glr):
-//   forward   8 x 8 54, 8 x 16 53, 4 x 16 61, 16 x 8 62; glri 69, 76, 73, 79
-//   backward  8 x 8 82, 4 x 12 87, 4 x 8 98, 8 x 4 113
+// look-backs in a row, as long as the registers allow a workgroup of it, or two
+// of the smaller ones, on a CU.  us, glr, 2 x 131072 x 256 fp32 and 8 x 4096 x 512
+// bf16, steps x waves: forward 16 x 16 174 and 29, 12 x 16 187 and 32, 16 x 12 178 and
+// 32 (8 x 16 and 8 waves were 10 to 50% slower); backward 16 x 8 272, 8 x 16 46 (8 x 8
+// and 12 x 8 5 to 25% slower, 4 x 16 half as long again).  Where a workgroup has
+// its chain (64 x 1024 x 512 bf16), 8 x 8 took as long as 8 x 16 and 8 x 12 or less,
+// 4 x 8, 4 x 16 and 16 x 8 10 to 25% longer.
 struct Shape {
   int steps, waves;
   constexpr int chunk() const { return steps * waves; }
