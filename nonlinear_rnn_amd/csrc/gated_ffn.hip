@@ -7,16 +7,19 @@
 // gate rows and the 32 up rows of the same outputs, so that the two sums of an
 // output meet in one lane's accumulators, in fp32, and only the result is
 // stored.  The backward pass forms the sums again (4 N F d operations) instead
-// of reading 2 N F stored values, and stores dz = [dg | du], rounded once to
-// bf16 (dx and dW are sums over many of its entries, whose roundings meet at
-// random: their error against float64 goes from 0.0017 of their root mean
-// square, that of the result's own rounding, to 0.0023), with its columns in
-// the same pairs of blocks: 64 consecutive columns are 32 of dg and their 32
-// of du.
+// of reading 2 N F stored values, and stores dz = [dg | du], bf16: with its
+// columns in the same pairs of blocks, 64 consecutive columns are 32 of dg and
+// their 32 of du; dx and dW are one launch.
 //
 // bf16 products run on the tiles of mm_tile.h, 256 x 256 in persistent
-// workgroups, where there are enough of them; fewer tokens on the projection's
-// 128 x 128 tiles (proj.hip); fp32 on the projection's tiles as well.
+// workgroups where there are enough of them, else 128 x 128, two workgroups a
+// CU.  With the quarter tiles dz has two bf16 terms, v = hi + lo to 2^-16 |v|,
+// and dx and dW are as exact as their own rounding lets them be (0.00166 of
+// their root mean square against float64); the large ones round it once, and
+// the errors of its entries, which meet at random, make that 0.00235: the
+// second term would cost them most of a product's time (5003 x 517 x 1387:
+// backward 101 us, with two terms 143; 32768 x 512 x 2048: 451 and 901).
+// fp32 runs on the projection's tiles (proj.hip).
 #include "gated_ffn.h"
 
 #include <algorithm>
@@ -33,9 +36,10 @@
 namespace prn {
 namespace {
 
-// 8 waves, 256 x 256, 128 KB; 8 waves, 256 x 192, 112 KB (mm_tile.h)
+// 8 waves, 256 x 256, 128 KB; 8 waves, 256 x 192, 112 KB; 4 waves, 128 x 128, 64 KB, two workgroups a CU (mm_tile.h)
 using Big = MmTile<2, 4, 4, 2, 64, 2>;
 using Wide = MmTile<4, 2, 2, 3, 64, 2>;
+using Mid = MmTile<2, 2, 2, 2, 64, 2>;
 
 // Copies of rows of d values as rows of ldp, zeros past d, a thread per 16 bytes:
 // x (N rows) to xp, then W (two halves of F rows) to wp, the halves Fw rows each,
@@ -130,18 +134,26 @@ __device__ __forceinline__ void from_rows(Packed p, float (&v)[16]) {
   }
 }
 
+// what v is above its bf16 value, 0 where that is not finite
+__device__ __forceinline__ float second_term(float v) {
+  const float rest = v - static_cast<float>(static_cast<__bf16>(v));
+  return fabsf(rest) < __builtin_inff() ? rest : 0.0f;
+}
+
 // ---------------------------------------------------------------- sums ----
 
-// The tiles of g and u, 128 outputs x 256 tokens each; out (N x F), or with BACK
-// dz (N x 2 Fp in pairs of blocks, rows ldz apart, zeros past F).  W has Fw gate
+// The tiles of g and u, 128 outputs x 256 tokens each (quarter tiles: 64 x 128);
+// out (N x F), or dz in TERMS terms, `low` elements apart (N x 2 Fp in pairs of
+// blocks, rows ldo apart, zeros past F).  W has Fw gate
 // rows, then Fw up rows.  A group of 8 tiles of outputs by all tokens, walked
 // down the outputs first, is a share of an XCD, whose L2 then holds the group's
 // W.  (32768 x 512 x 2048: 152 us, dz 186; two workgroups a CU of 256 x 128, one's
 // products under the other's epilogue: 158 and 197.)
-template <class Tl, bool BACK>
+template <class Tl, int TERMS>
 __global__ void __launch_bounds__(Tl::NTHR, 2) k_ffn_sums(MmOperand W, MmOperand X, int64_t N, int64_t F, int64_t Fw, int64_t K,
                                                           bool silu, const uint16_t* __restrict__ dout,
-                                                          uint16_t* __restrict__ out, int64_t ldo) {
+                                                          uint16_t* __restrict__ out, int64_t ldo, int64_t low) {
+  constexpr bool BACK = TERMS > 0;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Tl::LDS];
   static_assert(Tl::WM % 2 == 0, "pairs of blocks");
   constexpr int kPairs = Tl::BM / 2;   // outputs of a tile
@@ -175,7 +187,7 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_ffn_sums(MmOperand W, MmOperand
   if (!lu.valid()) return;
   go_to();
   tile.template prime<false, false>(next);
-  constexpr int kStores = Tl::WN * Tl::WM * (BACK ? 2 : 1);   // of a wave and whole tile
+  constexpr int kStores = Tl::WN * Tl::WM * (BACK ? 2 * TERMS : 1);   // of a wave and whole tile
   bool whole = false;   // the tile before was
   for (; cu.valid(); cu.advance()) {
     uint32_t ft, tok;
@@ -241,16 +253,28 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_ffn_sums(MmOperand W, MmOperand
             }
           }
           if (EDGE && fb >= f_left) continue;
-          const Packed pa = to_rows(a), pb = BACK ? to_rows(b) : pa;
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int t = t0 + 16 * k;
-            if (EDGE && t >= toks) continue;
-            if constexpr (BACK) {
-              uint16_t* const to = out + (n0 + t) * ldo + 2 * (f0 + fb) + fe;
+          for (int term = 0; BACK && term < TERMS; ++term) {
+            if (term == 1) {
+#pragma unroll
+              for (int r = 0; r < 16; ++r) a[r] = second_term(a[r]), b[r] = second_term(b[r]);
+            }
+            const Packed pa = to_rows(a), pb = to_rows(b);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int t = t0 + 16 * k;
+              if (EDGE && t >= toks) continue;
+              uint16_t* const to = out + term * low + (n0 + t) * ldo + 2 * (f0 + fb) + fe;
               gstore(reinterpret_cast<mm_u32x4*>(to), pa.o[k]);
               gstore(reinterpret_cast<mm_u32x4*>(to + 32), pb.o[k]);
-            } else {
+            }
+          }
+          if constexpr (!BACK) {
+            const Packed pa = to_rows(a);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int t = t0 + 16 * k;
+              if (EDGE && t >= toks) continue;
               uint16_t* const to = out + (n0 + t) * ldo + f0 + fb + fe;
               if (!EDGE || fb + fe + 8 <= f_left) {
                 __builtin_memcpy(to, &pa.o[k], 16);   // aligned or not
@@ -273,47 +297,71 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_ffn_sums(MmOperand W, MmOperand
 
 // ----------------------------------------------------------- dx and dW ----
 
-// P[z][r][c] = sum over k of slice z of A(r, k) B(c, k), fp32, C columns, or with
+// One of the two products, C columns: tiles x slices of its sum over K.  Block b
+// of its own: a tile and a slice, neighbours on one XCD (blocks are dealt to the
+// XCDs in turn).
+struct FfnProduct {
+  MmOperand A, B;
+  int64_t R, K, len;
+  uint32_t slices, blocks;
+  float* P;        // the slices' sums, R x C each
+  uint16_t* out;   // one slice: the result
+  __device__ __forceinline__ uint32_t unit(uint32_t b) const {
+    const uint32_t x = b % kXcd;
+    return x * (blocks / kXcd) + min(x, blocks % kXcd) + b / kXcd;
+  }
+};
+
+// P[z][r][c] = sum over k of slice z of A(r, k) B(c, k), fp32, or with one slice
 // `out` the sums rounded once.  TA: dW, A(r, k) = dz(k, r), the rows r in pairs
 // of blocks: of `out`, row (r / 32 % 2) F + r / 64 * 32 + r % 32, if below F in
 // its half.  Otherwise dx, k in pairs of blocks: B's rows (W) are half a stage
-// of 64 from the gate's, half from the up rows Fw further on.  One workgroup per
-// tile and slice, neighbours on one XCD.
-template <class Tl, bool TA>
-__global__ void __launch_bounds__(Tl::NTHR, 2) k_ffn_mm(MmOperand A, MmOperand B, int64_t R, int64_t C, int64_t K, int64_t k_slice,
-                                                        int n_col, int slices, int64_t F, int64_t Fw, int64_t row0,
-                                                        float* __restrict__ P, uint16_t* __restrict__ out) {
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[Tl::LDS];
-  const uint32_t u = Units(gridDim.x).u, tiles = gridDim.x / slices, z = u / tiles, ti = u - z * tiles;
+// of 64 from the gate's, half from the up rows Fw further on.  TERMS = 2: A's
+// second terms, `low` elements further on, go over the same B.
+template <class Tl, bool TA, int TERMS>
+__device__ __forceinline__ void ffn_product(uint8_t* lds, const FfnProduct& p, uint32_t u, int64_t C, int64_t F, int64_t Fw,
+                                            int64_t low) {
+  const uint32_t n_col = static_cast<uint32_t>((C + Tl::BN - 1) / Tl::BN), tiles = p.blocks / p.slices, z = u / tiles, ti = u - z * tiles;
   const int64_t c0 = static_cast<int64_t>(ti % n_col) * Tl::BN, r0 = static_cast<int64_t>(ti / n_col) * Tl::BM;
-  const int64_t k0 = static_cast<int64_t>(z) * k_slice, k1 = imin(k0 + k_slice, K);
+  const int64_t k0 = static_cast<int64_t>(z) * p.len, k1 = imin(k0 + p.len, p.K), R = p.R;
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, l32 = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wr = wave / Tl::WC, wc = wave % Tl::WC;
   Tl tile;
-  tile.open(lds, A, R, B, C, k0, k1);
-  auto next = []() {};
-  tile.template seek<TA, true>(r0, c0);
-  if constexpr (!TA) {
-    static_assert(Tl::KS == 64, "a stage is a pair of blocks");
-    tile.bb = reinterpret_cast<const uint8_t*>(B.base + k0 / 2 * B.ld + c0);
+  tile.open(lds, p.A, R, p.B, C, k0, k1);
+  auto go_to = [&]() {
+    tile.B = p.B;
+    tile.template seek<TA, true>(r0, c0);
+    if constexpr (!TA) {
+      static_assert(Tl::KS == 64, "a stage is a pair of blocks");
+      tile.bb = reinterpret_cast<const uint8_t*>(p.B.base + k0 / 2 * p.B.ld + c0);
 #pragma unroll
-    for (int p = 0; p < Tl::NLB; ++p) {
-      int s, f;
-      Tl::template source<true, Tl::BN>(wave * Tl::NLB + p, lane, s, f);
-      if (s >= 32) tile.offb[p] += static_cast<uint32_t>((Fw - 32) * B.ld * 2);
+      for (int q = 0; q < Tl::NLB; ++q) {
+        int s, f;
+        Tl::template source<true, Tl::BN>(wave * Tl::NLB + q, lane, s, f);
+        if (s >= 32) tile.offb[q] += static_cast<uint32_t>((Fw - 32) * p.B.ld * 2);
+      }
+      tile.B.ld = p.B.ld / 2;   // a stage goes on by 32 rows of either half
     }
-    tile.B.ld = B.ld / 2;   // a stage goes on by 32 rows of either half
-  }
+  };
+  int term = 0;
+  auto next = [&]() {
+    if (++term < TERMS) {
+      tile.A.base += low;
+      go_to();
+    }
+  };
+  go_to();
   tile.clear();
   tile.template prime<TA, true>(next);
   tile.template multiply<TA, true>(next);
+  if constexpr (TERMS == 2) tile.template multiply<TA, true, true>(next);
   const int rows = static_cast<int>(imin(R - r0, Tl::BM)), cols = static_cast<int>(imin(C - c0, Tl::BN));
   const int rl = wr * Tl::WM * 32 + 4 * half, cl = wc * Tl::WN * 32 + l32;
 #pragma unroll
   for (int i = 0; i < Tl::WM; ++i) {
     // the block's first row of `out`, and how many of its rows are there
-    const int64_t rb = row0 + r0 + (wr * Tl::WM + i) * 32, f = rb / 64 * 32;
+    const int64_t rb = r0 + (wr * Tl::WM + i) * 32, f = rb / 64 * 32;
     const int64_t ob = TA ? ((rb >> 5) & 1) * F + f : rb;
     const int there = TA ? static_cast<int>(imin(F - f, 32)) : 32;
 #pragma unroll
@@ -322,28 +370,43 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_ffn_mm(MmOperand A, MmOperand B
 #pragma unroll
       for (int j = 0; j < Tl::WN; ++j) {
         if (rl + 32 * i + ri >= rows || cl + 32 * j >= cols) continue;
-        if (out) {
+        if (p.slices == 1) {
           if (4 * half + ri < there)
-            out[(ob + 4 * half + ri) * C + c0 + cl + 32 * j] = Storage<kBF16>::pack(tile.acc[i][j][r]);
+            p.out[(ob + 4 * half + ri) * C + c0 + cl + 32 * j] = Storage<kBF16>::pack(tile.acc[i][j][r]);
         } else {
-          P[(z * R + r0 + rl + 32 * i + ri) * C + c0 + cl + 32 * j] = tile.acc[i][j][r];
+          p.P[(z * R + r0 + rl + 32 * i + ri) * C + c0 + cl + 32 * j] = tile.acc[i][j][r];
         }
       }
     }
   }
 }
 
-// out = the sum over z, in order, of P[z], rounded once; dW's rows as in k_ffn_mm
-template <bool IS_W>
-__global__ void __launch_bounds__(256) k_ffn_join(const float* __restrict__ P, int S, int64_t R, int64_t C, int64_t F,
-                                                  int64_t row0, uint16_t* __restrict__ out) {
-  const int64_t i = block_in_rows() * 256 + threadIdx.x, n = R * C;
-  if (i >= n) return;
-  const int64_t r = i / C, c = i - r * C, rb = row0 + r, f = rb / 64 * 32 + rb % 32;
-  if (IS_W && f >= F) return;
+// dx and dW in one launch, the longer units first (w_first: dW's)
+template <class Tl, int TERMS>
+__global__ void __launch_bounds__(Tl::NTHR, 2) k_ffn_grads(FfnProduct x, FfnProduct w, bool w_first, int64_t C, int64_t F,
+                                                           int64_t Fw, int64_t low) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[Tl::LDS];
+  const uint32_t b = blockIdx.x, first = w_first ? w.blocks : x.blocks;
+  if ((b < first) == w_first)
+    ffn_product<Tl, true, TERMS>(lds, w, w.unit(w_first ? b : b - first), C, F, Fw, low);
+  else
+    ffn_product<Tl, false, TERMS>(lds, x, x.unit(w_first ? b - first : b), C, F, Fw, low);
+}
+
+// out = the sum over z, in order, of P[z], rounded once, of either product with
+// more than one slice (nx, nw values, or 0); dW's rows as in ffn_product
+__global__ void __launch_bounds__(256) k_ffn_join(FfnProduct x, int64_t nx, FfnProduct w, int64_t nw, int64_t C, int64_t F) {
+  int64_t i = block_in_rows() * 256 + threadIdx.x;
+  if (i >= nx + nw) return;
+  const bool is_w = i >= nx;
+  if (is_w) i -= nx;
+  const int64_t n = is_w ? nw : nx, r = i / C, c = i - r * C, f = r / 64 * 32 + r % 32;
+  if (is_w && f >= F) return;
+  const float* const P = is_w ? w.P : x.P;
+  const int S = static_cast<int>(is_w ? w.slices : x.slices);
   float sum = 0.0f;
   for (int z = 0; z < S; ++z) sum += P[z * n + i];
-  out[(IS_W ? ((rb >> 5) & 1) * F + f : rb) * C + c] = Storage<kBF16>::pack(sum);
+  (is_w ? w.out : x.out)[(is_w ? ((r >> 5) & 1) * F + f : r) * C + c] = Storage<kBF16>::pack(sum);
 }
 
 // zeros in columns c0 .. of rows of ld values
@@ -353,29 +416,123 @@ __global__ void __launch_bounds__(256) k_ffn_zero(T* __restrict__ out, int64_t R
   if (r < R) out[r * ld + c0 + i - r * w] = T(0);
 }
 
+// ---------------------------------------------------------------- fp32 ----
+
+// out (C x ld) = the transpose of in (R x C), zeros past R.  The first's n0 blocks, the second's n1.
+struct FfnTurn {
+  const float* in;
+  int64_t R, C;
+  float* out;
+  int64_t ld;
+  __host__ __device__ int64_t blocks() const { return (ld + 63) / 64 * ((C + 63) / 64); }
+};
+__global__ void __launch_bounds__(256) k_ffn_turn(FfnTurn first, int64_t n0, FfnTurn second, int64_t n1) {
+  __shared__ float tile[64][65];
+  int64_t b = block_in_rows();
+  const bool one = b < n0;
+  const FfnTurn t = one ? first : second;
+  if (!one && (b -= n0) >= n1) return;
+  const int64_t across = (t.C + 63) / 64, r0 = b / across * 64, c0 = b % across * 64;
+  const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int64_t r = r0 + ty + 4 * i, c = c0 + tx;
+    tile[ty + 4 * i][tx] = r < t.R && c < t.C ? t.in[r * t.C + c] : 0.0f;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int64_t c = c0 + ty + 4 * i, r = r0 + tx;
+    if (c < t.C && r < t.ld) t.out[c * t.ld + r] = tile[tx][ty + 4 * i];
+  }
+}
+
+// out = the sum over z, in order, of P[z], of dx (nx values) and dW (nw)
+__global__ void __launch_bounds__(256) k_ffn_add(const float* __restrict__ px, int sx, int64_t nx, float* __restrict__ dx,
+                                                 const float* __restrict__ pw, int sw, int64_t nw, float* __restrict__ dW) {
+  int64_t i = block_in_rows() * 256 + threadIdx.x;
+  const bool is_w = i >= nx;
+  if (is_w) i -= nx;
+  const int64_t n = is_w ? nw : nx;
+  if (i >= n) return;
+  const float* const P = is_w ? pw : px;
+  float sum = 0.0f;
+  for (int z = 0, S = is_w ? sw : sx; z < S; ++z) sum += P[z * n + i];
+  (is_w ? dW : dx)[i] = sum;
+}
+
 // ---------------------------------------------------------------- plan ----
+
+constexpr int kBigTerms = 1;
 
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
 
 // Few rows are gated_few.hip's: as many of its workgroups of 64 rows and 16 outputs
 // as one round of the device takes (bf16) or two (fp32, which takes the
-// projection's tiles longer).  us, few and the tiles: 65 x 512 x 1408 bf16 6.8 and
+// tiles longer).  us, few and the tiles: 65 x 512 x 1408 bf16 6.8 and
 // 10.0; 65 x 1024 x 4096 bf16 18 and 15; 256 x 512 x 1408 fp32 20 and 25.
 bool few_rows(const GatedFfnArgs& a) { return cdiv(a.N, 64) * cdiv(a.F, 16) <= (a.bf16 ? kCus : 2 * kCus); }
 
-// The 256 x 256 tiles where at least 128 of them keep the device busy: below, the
-// projection's quarter tiles.
-bool big_tiles(const GatedFfnArgs& a) { return a.bf16 && cdiv(a.N, Big::BN) * cdiv(a.F, Big::BM / 2) >= 128; }
+// The 256 x 256 tiles where at least 128 of them keep the device busy, or the
+// quarter tiles.  us, quarter and large: 3000 x 512 x 1408 (132 tiles) out 17 and
+// 18, the gradients (two terms of dz) 80 and 65; 8192 x 512 x 1408 gradients 147 and 107.
+bool big_tiles(const GatedFfnArgs& a) { return cdiv(a.N, Big::BN) * cdiv(a.F, Big::BM / 2) >= 128; }
+
+// How dx and dW, whose units share a launch, are cut: tiles of BM x BN, and slices of their sums.
+struct Slices {
+  int64_t s, len;
+};
+struct Split {
+  Slices x, w;
+  bool w_first;
+};
+template <class Tl>
+Split split_of(int64_t N, int64_t Z, int64_t d, int terms, double* us) {
+  // Microseconds of a unit over k of the sum, as in cut_of (the device at 1.05
+  // PFLOP/s, 256 x 192 tiles at less), and 2 to begin and end; of storing the
+  // slices' sums and reading them again, at 4 TB/s and half as much again.
+  constexpr int64_t kSlots = kCus * 8 / Tl::NW;
+  auto unit = [&](int64_t k) { return 2 + double(k) * terms * Tl::BM * Tl::BN * (Tl::BN == Wide::BN ? 1.12 : 1.0) * 2 * (kSlots / kCus) / 4.1e6; };
+  auto join = [&](int64_t rows, int64_t s) { return s > 1 ? double(s) * rows * d * 8 * 1.5 / 4e6 : 0.0; };
+  const int64_t n_col = cdiv(d, Tl::BN), tx = cdiv(N, Tl::BM) * n_col, tw = cdiv(Z, Tl::BM) * n_col;
+  constexpr int64_t kCounts[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 20, 24, 32};
+  auto cut = [](int64_t K, int64_t want) {
+    const int64_t len = cdiv(cdiv(K, want), 64) * 64;
+    return Slices{cdiv(K, len), len};
+  };
+  Split best{};
+  *us = -1;
+  for (int64_t a : kCounts) {
+    if (a > 1 && Z / a < 128) break;
+    const Slices x = cut(Z, a);
+    for (int64_t b : kCounts) {
+      if (b > 1 && N / b < 128) break;
+      const Slices w = cut(N, b);
+      const int64_t nx = tx * x.s, nw = tw * w.s;
+      const double ux = unit(x.len), uw = unit(w.len), longer = std::max(ux, uw), all = (nx * ux + nw * uw) / kSlots;
+      // whole rounds of equal units, or about half of one unit's time is lost at the end
+      const double run = nx + nw <= kSlots ? longer : std::max(all + std::min(ux, uw) / 2, longer);
+      const double t = run + (x.s > 1 || w.s > 1 ? 4 : 0) + join(N, x.s) + join(Z, w.s);
+      if (*us >= 0 && t >= *us) continue;
+      *us = t;
+      best = {x, w, uw > ux};
+    }
+  }
+  return best;
+}
 
 struct Plan {
-  bool tiles;             // of mm_tile.h
+  bool big;               // bf16: the large tiles
   bool pad_x, pad_w;      // x and W laid out anew: rows that are no multiple of 16 bytes; for dx W's halves of Fw rows
   int64_t ldp, Fw;
   size_t x_off, w_off;
   // backward
   int64_t Fp, ldz;        // dz: columns of either kind, elements from row to row
-  int64_t cols;           // tile columns of dx and dW
-  Cut x, w;               // of their sums
+  int terms;              // of dz
+  int64_t low;            // elements from its first to its second
+  bool wide;              // 256 x 192 for dx and dW
+  Slices x, w;            // of their sums
+  bool w_first;
   bool tn;
   size_t z_off, px_off, pw_off, wt_off, zt_off, xt_off, total;
 };
@@ -383,12 +540,12 @@ struct Plan {
 Plan plan_of(const GatedFfnArgs& a, bool back) {
   Plan p{};
   const int64_t vec = a.bf16 ? 8 : 4, elt = a.bf16 ? 2 : 4;
-  p.tiles = big_tiles(a);
+  p.big = a.bf16 && big_tiles(a);
   p.ldp = cdiv(a.d, vec) * vec;
   p.Fp = cdiv(a.F, 32) * 32;
   p.pad_x = a.d != p.ldp;
-  p.pad_w = p.pad_x || (back && p.tiles && a.F != p.Fp);
-  p.Fw = back && p.tiles ? p.Fp : a.F;
+  p.pad_w = p.pad_x || (back && a.bf16 && a.F != p.Fp);
+  p.Fw = back && a.bf16 ? p.Fp : a.F;
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t at = off;
@@ -397,25 +554,28 @@ Plan plan_of(const GatedFfnArgs& a, bool back) {
   };
   if (p.pad_x) p.x_off = take(size_t(a.N) * p.ldp * elt);
   if (p.pad_w) p.w_off = take(size_t(2) * p.Fw * p.ldp * elt);
-  if (back && p.tiles) {
+  if (back && a.bf16) {
     p.ldz = 2 * p.Fp + 64;   // rows are no power of two apart: they would fall on few memory channels
-    double best = -1;
-    for (int64_t bn : {int64_t(Big::BN), int64_t(Wide::BN)}) {
-      double tx, tw;
-      const Cut x = cut_of(a.N, 2 * p.Fp, a.d, 1, bn, &tx), w = cut_of(2 * p.Fp, a.N, a.d, 1, bn, &tw);
-      if (best >= 0 && tx + tw >= best) continue;
-      best = tx + tw;
-      p.cols = bn, p.x = x, p.w = w;
+    p.terms = p.big ? kBigTerms : 2;
+    const int64_t Z = 2 * p.Fp;
+    double us, us_wide = -1;
+    Split cut = p.big ? split_of<Big>(a.N, Z, a.d, p.terms, &us) : split_of<Mid>(a.N, Z, a.d, p.terms, &us);
+    if (p.big) {
+      const Split wide = split_of<Wide>(a.N, Z, a.d, p.terms, &us_wide);
+      p.wide = us_wide < us;
+      if (p.wide) cut = wide;
     }
-    auto sums = [&](int64_t rows, const Cut& c) { return c.s > 1 ? size_t(c.s) * (rows - c.head) * a.d * 4 : 0; };
-    p.z_off = take(size_t(a.N) * p.ldz * 2);
+    p.x = cut.x, p.w = cut.w, p.w_first = cut.w_first;
+    auto sums = [&](int64_t rows, const Slices& c) { return c.s > 1 ? size_t(c.s) * rows * a.d * 4 : 0; };
+    p.low = a.N * p.ldz;
+    p.z_off = take(size_t(p.terms) * p.low * 2);
     p.px_off = take(sums(a.N, p.x));
-    p.pw_off = take(sums(2 * p.Fp, p.w));
+    p.pw_off = take(sums(Z, p.w));
   } else if (back) {
     // The projection's tiles take operands in rows of the summed index.  A sum is
     // cut into slices where there are too few tiles for the device, of equal
     // length where half as many slices allow it (what is left over is zeros).
-    auto cut = [&](int64_t rows, int64_t cols, int64_t K, Cut& c) {
+    auto cut = [&](int64_t rows, int64_t cols, int64_t K, Slices& c) {
       const int64_t want = std::max<int64_t>(1, std::min<int64_t>({cdiv(512, cdiv(rows, 128) * cdiv(cols, 128)), K / 128, 64}));
       for (int64_t n = want; n >= (want + 1) / 2; --n)
         if (K % (n * vec) == 0) {
@@ -427,8 +587,8 @@ Plan plan_of(const GatedFfnArgs& a, bool back) {
     };
     cut(a.N, a.d, 2 * a.F, p.x);
     p.ldz = p.x.s * p.x.len;
-    p.z_off = take(size_t(a.N) * p.ldz * elt);
-    p.wt_off = take(size_t(a.d) * p.ldz * elt);
+    p.z_off = take(size_t(a.N) * p.ldz * 4);
+    p.wt_off = take(size_t(a.d) * p.ldz * 4);
     p.tn = 2 * a.F % 256 == 0 && a.d % 256 == 0;   // or both operands of dW in rows of their own
     if (p.tn) {
       const int64_t s = std::max<int64_t>(1, std::min<int64_t>(kCus / ((2 * a.F / 256) * (a.d / 256)), cdiv(a.N, 256)));
@@ -436,8 +596,8 @@ Plan plan_of(const GatedFfnArgs& a, bool back) {
       p.w.s = cdiv(a.N, p.w.len);
     } else {
       cut(2 * a.F, a.d, a.N, p.w);
-      p.zt_off = take(size_t(2) * a.F * p.w.s * p.w.len * elt);
-      p.xt_off = take(size_t(a.d) * p.w.s * p.w.len * elt);
+      p.zt_off = take(size_t(2) * a.F * p.w.s * p.w.len * 4);
+      p.xt_off = take(size_t(a.d) * p.w.s * p.w.len * 4);
     }
     p.px_off = take(p.x.s > 1 ? size_t(p.x.s) * a.N * a.d * 4 : 0);
     p.pw_off = take(p.tn || p.w.s > 1 ? size_t(p.w.s) * 2 * a.F * a.d * 4 : 0);
@@ -472,19 +632,19 @@ void fill_zero(const GatedFfnArgs& a, void* out, int64_t R, int64_t c0, int64_t 
     k_ffn_zero<float><<<grid, 256, 0, a.stream>>>(static_cast<float*>(out), R, c0, ld);
 }
 
-// out, or with dout dz
+// bf16: out, or with dout dz
 void sums(const GatedFfnArgs& a, const Plan& p, const Operands& o, const void* dout, void* out, int64_t ldo) {
-  if (!p.tiles) {
-    launch_proj_gated(a.bf16, o.x, o.W, out, a.N, p.ldp, GatedProj{dout, a.F, dout ? ldo : 0, a.silu}, a.stream);
-    return;
-  }
   const MmOperand W{static_cast<const uint16_t*>(o.W), p.ldp}, X{static_cast<const uint16_t*>(o.x), p.ldp};
-  const unsigned grid = unsigned(std::min(cdiv(a.N, Big::BN) * cdiv(a.F, Big::BM / 2), kCus));
-  auto go = [&](auto back) {
-    k_ffn_sums<Big, decltype(back)::value><<<grid, Big::NTHR, 0, a.stream>>>(
-        W, X, a.N, a.F, p.Fw, p.ldp, a.silu, static_cast<const uint16_t*>(dout), static_cast<uint16_t*>(out), ldo);
+  auto go = [&](auto tl, auto terms) {
+    using Tl = decltype(tl);
+    const unsigned grid = unsigned(std::min(cdiv(a.N, Tl::BN) * cdiv(a.F, Tl::BM / 2), kCus * 8 / Tl::NW));
+    k_ffn_sums<Tl, decltype(terms)::value><<<grid, Tl::NTHR, 0, a.stream>>>(
+        W, X, a.N, a.F, p.Fw, p.ldp, a.silu, static_cast<const uint16_t*>(dout), static_cast<uint16_t*>(out), ldo, p.low);
   };
-  if (dout) go(std::true_type{}); else go(std::false_type{});
+  auto kind = [&](auto tl, auto back) {
+    if (dout) go(tl, back); else go(tl, std::integral_constant<int, 0>{});
+  };
+  if (p.big) kind(Big{}, std::integral_constant<int, kBigTerms>{}); else kind(Mid{}, std::integral_constant<int, 2>{});
 }
 
 }  // namespace
@@ -503,7 +663,12 @@ void launch_gated_ffn(const GatedFfnArgs& a, const void* x, const void* W, void*
     return;
   }
   const Plan p = plan_of(a, false);
-  sums(a, p, lay_out(a, p, x, W), nullptr, out, a.F);
+  const Operands o = lay_out(a, p, x, W);
+  if (a.bf16)
+    sums(a, p, o, nullptr, out, a.F);
+  else
+    launch_proj_gated(static_cast<const float*>(o.x), static_cast<const float*>(o.W), static_cast<float*>(out), a.N, p.ldp,
+                      GatedProj{nullptr, a.F, 0, a.silu, nullptr, 0}, a.stream);
 }
 
 size_t gated_ffn_backward_workspace(const GatedFfnArgs& a) { return a.N ? plan_of(a, true).total : 0; }
@@ -517,62 +682,48 @@ void launch_gated_ffn_backward(const GatedFfnArgs& a, const void* x, const void*
   const Operands o = lay_out(a, p, x, W);
   void* const dz = a.ws + p.z_off;
   float *const px = reinterpret_cast<float*>(a.ws + p.px_off), *const pw = reinterpret_cast<float*>(a.ws + p.pw_off);
-  sums(a, p, o, dout, dz, p.ldz);
-  if (!p.tiles) {
-    const int64_t elt = a.bf16 ? 2 : 4, Z = 2 * a.F;
-    if (dx && p.ldz > Z) fill_zero(a, dz, a.N, Z, p.ldz);
-    if (dx) {
-      void* const wt = a.ws + p.wt_off;
-      launch_transpose(a.bf16, W, Z, a.d, a.d, wt, p.ldz, nullptr, a.stream);
-      if (p.x.s > 1) {
-        launch_proj_splitk(a.bf16, dz, p.ldz * elt, wt, p.ldz * elt, px, a.N, a.d, p.x.len, int(p.x.s), a.stream);
-        launch_splitk_sum(a.bf16, px, int(p.x.s), a.N * a.d, dx, a.stream);
-      } else {
-        launch_proj_ld(a.bf16, dz, p.ldz * elt, wt, p.ldz * elt, dx, a.N, a.d, p.x.len, a.stream);
-      }
-    }
-    if (dW && p.tn) {
-      launch_proj_tn(a.bf16, dz, p.ldz * elt, x, a.d * elt, pw, a.N, Z, a.d, p.w.len, int(p.w.s), nullptr, a.stream);
-      launch_splitk_sum(a.bf16, pw, int(p.w.s), Z * a.d, dW, a.stream);
-    } else if (dW) {
-      void *const zt = a.ws + p.zt_off, *const xt = a.ws + p.xt_off;
-      const int64_t ld = p.w.s * p.w.len;
-      launch_transpose(a.bf16, dz, a.N, Z, p.ldz, zt, ld, nullptr, a.stream);
-      launch_transpose(a.bf16, x, a.N, a.d, a.d, xt, ld, nullptr, a.stream);
-      if (p.w.s > 1) {
-        launch_proj_splitk(a.bf16, zt, ld * elt, xt, ld * elt, pw, Z, a.d, p.w.len, int(p.w.s), a.stream);
-        launch_splitk_sum(a.bf16, pw, int(p.w.s), Z * a.d, dW, a.stream);
-      } else {
-        launch_proj_ld(a.bf16, zt, ld * elt, xt, ld * elt, dW, Z, a.d, ld, a.stream);
-      }
-    }
+  if (!a.bf16) {
+    const int64_t Z = 2 * a.F, bz = p.ldz * 4, ldt = p.w.s * p.w.len;
+    const bool turned = dW && !p.tn;   // dW's operands
+    const float* const xf = static_cast<const float*>(x);
+    float *const z = static_cast<float*>(dz), *const wt = reinterpret_cast<float*>(a.ws + p.wt_off);
+    float *const zt = reinterpret_cast<float*>(a.ws + p.zt_off), *const xt = reinterpret_cast<float*>(a.ws + p.xt_off);
+    float *const dxf = static_cast<float*>(dx), *const dWf = static_cast<float*>(dW);
+    const FfnTurn turn_w{static_cast<const float*>(W), Z, a.d, wt, p.ldz}, turn_x{xf, a.N, a.d, xt, ldt};
+    const int64_t bw = dx ? turn_w.blocks() : 0, bx = turned ? turn_x.blocks() : 0;
+    if (bw + bx > 0) k_ffn_turn<<<rows_of_blocks(bw + bx), 256, 0, a.stream>>>(turn_w, bw, turn_x, bx);
+    launch_proj_gated(static_cast<const float*>(o.x), static_cast<const float*>(o.W), z, a.N, p.ldp,
+                      GatedProj{static_cast<const float*>(dout), a.F, p.ldz, a.silu, turned ? zt : nullptr, ldt}, a.stream);
+    if (dx && p.ldz > Z) fill_zero(a, z, a.N, Z, p.ldz);
+    if (turned && ldt > a.N) fill_zero(a, zt, Z, a.N, ldt);
+    const int64_t nx = dx && p.x.s > 1 ? a.N * a.d : 0, nw = dW && (p.tn || p.w.s > 1) ? Z * a.d : 0;
+    if (nx) launch_proj_splitk(false, z, bz, wt, bz, px, a.N, a.d, p.x.len, int(p.x.s), a.stream);
+    else if (dx) launch_proj_ld(false, z, bz, wt, bz, dxf, a.N, a.d, p.x.len, a.stream);
+    if (dW && p.tn) launch_proj_tn(false, z, bz, xf, a.d * 4, pw, a.N, Z, a.d, p.w.len, int(p.w.s), nullptr, a.stream);
+    else if (nw) launch_proj_splitk(false, zt, ldt * 4, xt, ldt * 4, pw, Z, a.d, p.w.len, int(p.w.s), a.stream);
+    else if (dW) launch_proj_ld(false, zt, ldt * 4, xt, ldt * 4, dWf, Z, a.d, ldt, a.stream);
+    if (nx + nw > 0)
+      k_ffn_add<<<rows_of_blocks(cdiv(nx + nw, 256)), 256, 0, a.stream>>>(px, int(p.x.s), nx, dxf, pw, int(p.w.s), nw, dWf);
     return;
   }
+  sums(a, p, o, dout, dz, p.ldz);
   const MmOperand Z{static_cast<const uint16_t*>(dz), p.ldz}, X{static_cast<const uint16_t*>(o.x), p.ldp},
       Wo{static_cast<const uint16_t*>(o.W), p.ldp};
-  // the head's rows, then the rest
-  auto product = [&](auto ta, const Cut& c, const MmOperand& B, int64_t rows, int64_t K, float* P, void* to) {
-    constexpr bool TA = decltype(ta)::value;
-    uint16_t* const out = static_cast<uint16_t*>(to);
-    auto part = [&](int64_t r0, int64_t n, int64_t s, int64_t len) {
-      if (n <= 0) return;
-      MmOperand A = Z;
-      A.base += r0 * (TA ? 1 : p.ldz);
-      auto run = [&](auto tl) {
-        using Tl = decltype(tl);
-        const int64_t n_col = cdiv(a.d, Tl::BN);
-        k_ffn_mm<Tl, TA><<<unsigned(cdiv(n, Tl::BM) * n_col * s), Tl::NTHR, 0, a.stream>>>(
-            A, B, n, a.d, K, len, int(n_col), int(s), a.F, p.Fw, r0, P, s == 1 ? out : nullptr);
-      };
-      if (p.cols == Big::BN) run(Big{}); else run(Wide{});
-      if (s > 1) k_ffn_join<TA><<<rows_of_blocks(cdiv(n * a.d, 256)), 256, 0, a.stream>>>(P, int(s), n, a.d, a.F, r0, out);
-    };
-    const int64_t head = std::min(c.head, rows);
-    part(0, head, 1, cdiv(K, 64) * 64);
-    part(head, rows - head, c.s, c.len);
+  const int64_t Zp = 2 * p.Fp;
+  FfnProduct to_x{Z, Wo, a.N, Zp, p.x.len, uint32_t(p.x.s), 0, px, static_cast<uint16_t*>(dx)};
+  FfnProduct to_w{Z, X, Zp, a.N, p.w.len, uint32_t(p.w.s), 0, pw, static_cast<uint16_t*>(dW)};
+  auto run = [&](auto tl, auto terms) {
+    using Tl = decltype(tl);
+    const int64_t n_col = cdiv(a.d, Tl::BN);
+    if (dx) to_x.blocks = uint32_t(cdiv(a.N, Tl::BM) * n_col * p.x.s);
+    if (dW) to_w.blocks = uint32_t(cdiv(Zp, Tl::BM) * n_col * p.w.s);
+    k_ffn_grads<Tl, decltype(terms)::value><<<to_x.blocks + to_w.blocks, Tl::NTHR, 0, a.stream>>>(to_x, to_w, p.w_first, a.d, a.F,
+                                                                                                  p.Fw, p.low);
   };
-  if (dx) product(std::false_type{}, p.x, Wo, a.N, 2 * p.Fp, px, dx);
-  if (dW) product(std::true_type{}, p.w, X, 2 * p.Fp, a.N, pw, dW);
+  constexpr std::integral_constant<int, kBigTerms> of_big{};
+  if (!p.big) run(Mid{}, std::integral_constant<int, 2>{}); else if (p.wide) run(Wide{}, of_big); else run(Big{}, of_big);
+  const int64_t nx = dx && p.x.s > 1 ? a.N * a.d : 0, nw = dW && p.w.s > 1 ? Zp * a.d : 0;
+  if (nx + nw > 0) k_ffn_join<<<rows_of_blocks(cdiv(nx + nw, 256)), 256, 0, a.stream>>>(to_x, nx, to_w, nw, a.d, a.F);
 }
 
 }  // namespace prn

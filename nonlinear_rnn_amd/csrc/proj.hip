@@ -411,30 +411,40 @@ k_proj(const uint8_t* __restrict__ A, const uint8_t* __restrict__ B, const float
   }
 
   if constexpr (GATED != kPlain) {
-    static_assert(WN == 2 && !OUTF32, "a gate and an up block");
-    using T = std::conditional_t<BF16, uint16_t, float>;
-    auto pack = [](float v) {
-      if constexpr (BF16) return bf16_rne(v); else return v;
-    };
+    static_assert(WN == 2 && !OUTF32 && !BF16, "a gate and an up block");
     const int64_t f = ((n0 >> 6) + wc) * 32 + l32;
+    float* const out = reinterpret_cast<float*>(C);
 #pragma unroll
     for (int i = 0; i < WM; ++i) {
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int64_t gm = m0 + wr * WM * 32 + i * 32 + 8 * (r >> 2) + 4 * half + (r & 3);
+      for (int q = 0; q < 4; ++q) {
+        const int64_t gm = m0 + wr * WM * 32 + i * 32 + 8 * q + 4 * half;
         if (EDGE && (gm >= M || f >= gp.F)) continue;
-        const float g = acc[i][0][r], u = acc[i][1][r];
-        if constexpr (GATED == kGatedOut) {
-          reinterpret_cast<T*>(C)[gm * gp.F + f] = pack(gated_value(gp.silu, g) * u);
-        } else {
-          float d;
-          if constexpr (BF16)
-            d = __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(gp.dout)[gm * gp.F + f]) << 16);
-          else
-            d = static_cast<const float*>(gp.dout)[gm * gp.F + f];
-          T* const to = reinterpret_cast<T*>(C) + gm * gp.ldz + f;
-          to[0] = pack(d * u * gated_slope(gp.silu, g));
-          to[gp.F] = pack(d * gated_value(gp.silu, g));
+        f32x4 zg, zu;
+        const int n = EDGE ? static_cast<int>(M - gm < 4 ? M - gm : 4) : 4;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (EDGE && e >= n) continue;
+          const float g = acc[i][0][4 * q + e], u = acc[i][1][4 * q + e];
+          if constexpr (GATED == kGatedOut) {
+            out[(gm + e) * gp.F + f] = gated_value(gp.silu, g) * u;
+          } else {
+            const float d = gp.dout[(gm + e) * gp.F + f];
+            float* const to = out + (gm + e) * gp.ldz + f;
+            to[0] = zg[e] = d * u * gated_slope(gp.silu, g);
+            to[gp.F] = zu[e] = d * gated_value(gp.silu, g);
+          }
+        }
+        if (GATED == kGatedBack && gp.zt) {
+          float* const to = gp.zt + f * gp.ldt + gm;
+          if (n == 4) {
+            *reinterpret_cast<f32x4*>(to) = zg;
+            *reinterpret_cast<f32x4*>(to + gp.F * gp.ldt) = zu;
+          } else {
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+              if (e < n) to[e] = zg[e], to[gp.F * gp.ldt + e] = zu[e];
+          }
         }
       }
     }
@@ -695,34 +705,31 @@ void launch_proj(bool bf16, const void* A, const void* B, const float* bias, voi
     launch_tiles<2, 2, false>(bf16, A, B, bias, C, M, N, K, ld, ld, 1, stream);
 }
 
-void launch_proj_gated(bool bf16, const void* x, const void* W, void* out, int64_t M, int64_t K, const GatedProj& gp,
+void launch_proj_gated(const float* x, const float* W, float* out, int64_t M, int64_t K, const GatedProj& gp,
                        hipStream_t stream) {
   using Large = Tile<4, 4>;
-  const int64_t N = (gp.F + 31) / 32 * 64, ld = K * (bf16 ? 2 : 4);
-  auto run = [&](auto waves, auto bf, auto ed, auto kind) {
+  const int64_t N = (gp.F + 31) / 32 * 64, ld = K * 4;
+  auto run = [&](auto waves, auto ed, auto kind) {
     constexpr int WV = decltype(waves)::value;
     using Tl = Tile<WV, WV>;
     const int64_t tn = (N + Tl::BN - 1) / Tl::BN, nb = ((M + Tl::BM - 1) / Tl::BM) * tn;
-    k_proj<decltype(bf)::value, decltype(ed)::value, WV, WV, false, 2, 2, decltype(kind)::value>
-        <<<unsigned(nb), Tl::NTHR, 0, stream>>>(static_cast<const uint8_t*>(x), static_cast<const uint8_t*>(W), nullptr,
-                                                static_cast<uint8_t*>(out), M, N, K, ld, ld, int(tn), nb % NXCD == 0, gp);
+    k_proj<false, decltype(ed)::value, WV, WV, false, 2, 2, decltype(kind)::value>
+        <<<unsigned(nb), Tl::NTHR, 0, stream>>>(reinterpret_cast<const uint8_t*>(x), reinterpret_cast<const uint8_t*>(W), nullptr,
+                                                reinterpret_cast<uint8_t*>(out), M, N, K, ld, ld, int(tn), nb % NXCD == 0, gp);
   };
-  auto kinds = [&](auto waves, auto bf, auto ed) {
+  auto kinds = [&](auto waves, auto ed) {
     if (gp.dout)
-      run(waves, bf, ed, std::integral_constant<int, kGatedBack>{});
+      run(waves, ed, std::integral_constant<int, kGatedBack>{});
     else
-      run(waves, bf, ed, std::integral_constant<int, kGatedOut>{});
+      run(waves, ed, std::integral_constant<int, kGatedOut>{});
   };
-  auto edges = [&](auto waves, auto bf) {
+  auto edges = [&](auto waves) {
     constexpr int BN = decltype(waves)::value * 64;
     const bool edge = M % BN != 0 || 2 * gp.F % BN != 0 || ld % ROWB != 0;
-    if (edge) kinds(waves, bf, std::true_type{}); else kinds(waves, bf, std::false_type{});
-  };
-  auto types = [&](auto waves) {
-    if (bf16) edges(waves, std::true_type{}); else edges(waves, std::false_type{});
+    if (edge) kinds(waves, std::true_type{}); else kinds(waves, std::false_type{});
   };
   const int64_t large = ((M + Large::BM - 1) / Large::BM) * ((N + Large::BN - 1) / Large::BN);
-  if (large >= kLargeTiles) types(std::integral_constant<int, 4>{}); else types(std::integral_constant<int, 2>{});
+  if (large >= kLargeTiles) edges(std::integral_constant<int, 4>{}); else edges(std::integral_constant<int, 2>{});
 }
 
 void launch_proj_ld(bool bf16, const void* A, int64_t lda, const void* B, int64_t ldb, void* C, int64_t M,

@@ -65,6 +65,18 @@ def test_large_tiles(N, d, F, dtype):
     _check(*_case(N, d, F, dtype), "silu", dtype)
 
 
+@pytest.mark.parametrize("N,d,F", [(3, 64, 96), (65, 100, 129), (300, 72, 77), (1030, 96, 250), (2000, 31, 64)])
+def test_bf16_gradients_of_few_tiles_round_once(N, d, F):
+    """The gradients of the sums have two bf16 terms in between: off by 2^-16 of themselves, no more."""
+    x, W, dout = _case(N, d, F, torch.bfloat16, seed=7)
+    xd, Wd, gd = _np(x), _np(W), _np(dout)
+    dx, dW = prn.gated_ffn_backward(dout, x, W)
+    _, b_dx, b_dW = gated.gated_ffn_bounds(xd, Wd, "silu", gd, 2.0 ** -16)
+    want_dx, want_dW = gated.gated_ffn_backward(xd, Wd, gd, "silu")
+    _close("dx", dx, want_dx, b_dx, torch.bfloat16)
+    _close("dW", dW, want_dW, b_dW, torch.bfloat16)
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_values_far_apart(dtype):
     """A large token, a large row of W, and zeros, each held to its own size."""
