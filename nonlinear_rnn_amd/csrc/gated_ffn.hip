@@ -11,20 +11,28 @@
 // columns in the same pairs of blocks, 64 consecutive columns are 32 of dg and
 // their 32 of du; dx and dW are one launch.
 //
-// bf16 products run on the tiles of mm_tile.h, 256 x 256 in persistent
-// workgroups where there are enough of them, else 128 x 128, two workgroups a
-// CU.  With the quarter tiles dz has two bf16 terms, v = hi + lo to 2^-16 |v|,
+// Products run on the tiles of mm_tile.h, 256 x 256 in persistent workgroups
+// where there are enough of them, else 128 x 128, two workgroups a CU.
+//
+// bf16: with the quarter tiles dz has two bf16 terms, v = hi + lo to 2^-16 |v|,
 // and dx and dW are as exact as their own rounding lets them be (0.00166 of
 // their root mean square against float64); the large ones round it once, and
 // the errors of its entries, which meet at random, make that 0.00235: the
-// second term would cost them most of a product's time (5003 x 517 x 1387:
-// backward 101 us, with two terms 143; 32768 x 512 x 2048: 451 and 901).
-// fp32 runs on the projection's tiles (proj.hip).
+// second term would cost them a good part of a product's time (gradients of
+// 5003 x 517 x 1387: 86 us, with two terms 119; of 32768 x 512 x 2048: 440 and 759).
+//
+// fp32: x, W and dz as three bf16 terms each, laid out before the products, six
+// products of terms (bf16split.h), one pass of a tile over the sum each.  The
+// forward runs on the projection's tiles, which split what they have in
+// registers: one product alone does not pay for the layout (4096 x 256 x 704: 27
+// us, in terms 38), three and their operands of either orientation do (the
+// gradients 93 us; on the projection's tiles, with transposed copies, 118).
 #include "gated_ffn.h"
 
 #include <algorithm>
 #include <type_traits>
 
+#include "bf16split.h"
 #include "gated_cell.h"
 #include "gated_few.h"
 #include "grid_rows.h"
@@ -66,6 +74,44 @@ __global__ void __launch_bounds__(256) k_ffn_pad(const T* __restrict__ x, int64_
   }
   __builtin_memcpy(__builtin_assume_aligned((is_x ? xp : wp) + to * ldp + c0, 16), v, sizeof(v));
 }
+
+// fp32 rows as three bf16 terms (bf16split.h), planes Nx ldp of x apart, 2 Fw ldp of
+// W; rows and zeros as above, a thread per eight values
+__global__ void __launch_bounds__(256) k_ffn_terms(const float* __restrict__ x, int64_t Nx, const float* __restrict__ W, int64_t F,
+                                                   int64_t Fw, int64_t d, int64_t ldp, uint16_t* __restrict__ xp,
+                                                   uint16_t* __restrict__ wp) {
+  const int64_t C = ldp / 8, i = block_in_rows() * 256 + threadIdx.x;
+  int64_t to = i / C;
+  const int64_t c0 = (i - to * C) * 8;
+  const bool is_x = to < Nx;
+  if (!is_x) to -= Nx;
+  if (!is_x && to >= 2 * Fw) return;
+  const int64_t half = !is_x && to >= Fw, r = to - half * Fw;
+  const bool there = is_x || r < F;
+  const float* const from = is_x ? x + r * d + c0 : W + (half * F + r) * d + c0;
+  sp_f32x4 a, b;
+  if (there && c0 + 8 <= d) {
+    __builtin_memcpy(&a, from, 16);   // aligned or not
+    __builtin_memcpy(&b, from + 4, 16);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      a[e] = there && c0 + e < d ? from[e] : 0.0f;
+      b[e] = there && c0 + 4 + e < d ? from[4 + e] : 0.0f;
+    }
+  }
+  sp_bf16x8 t[3];
+  split3(a, b, t[0], t[1], t[2]);
+#pragma unroll
+  for (int k = 0; k < 3; ++k)
+    *reinterpret_cast<sp_bf16x8*>((is_x ? xp + k * Nx * ldp : wp + k * 2 * Fw * ldp) + to * ldp + c0) = t[k];
+}
+
+// The passes of a product over its operands' terms (kSplitU, kSplitV), two bits each
+__device__ __forceinline__ int term_of_a(int pass) { return 0x910 >> 2 * pass & 3; }
+__device__ __forceinline__ int term_of_b(int pass) { return 0x184 >> 2 * pass & 3; }
+static_assert(kSplitU[2] == 1 && kSplitU[4] == 1 && kSplitU[5] == 2 && kSplitU[0] + kSplitU[1] + kSplitU[3] == 0, "0x910");
+static_assert(kSplitV[1] == 1 && kSplitV[3] == 2 && kSplitV[4] == 1 && kSplitV[0] + kSplitV[2] + kSplitV[5] == 0, "0x184");
 
 // ---------------------------------------------------- blocks of values ----
 // A block of 32 x 32 values of the accumulators (lane l: column l % 32, a token;
@@ -143,17 +189,22 @@ __device__ __forceinline__ float second_term(float v) {
 // ---------------------------------------------------------------- sums ----
 
 // The tiles of g and u, 128 outputs x 256 tokens each (quarter tiles: 64 x 128);
-// out (N x F), or dz in TERMS terms, `low` elements apart (N x 2 Fp in pairs of
+// TERMS = 0: out (N x F), bf16; else dz in TERMS bf16 terms (3: of fp32 data,
+// W and X in terms too, w_low and x_low apart), `low` elements apart (N x 2 Fp in pairs of
 // blocks, rows ldo apart, zeros past F).  W has Fw gate
 // rows, then Fw up rows.  A group of 8 tiles of outputs by all tokens, walked
 // down the outputs first, is a share of an XCD, whose L2 then holds the group's
 // W.  (32768 x 512 x 2048: 152 us, dz 186; two workgroups a CU of 256 x 128, one's
 // products under the other's epilogue: 158 and 197.)
 template <class Tl, int TERMS>
-__global__ void __launch_bounds__(Tl::NTHR, 2) k_ffn_sums(MmOperand W, MmOperand X, int64_t N, int64_t F, int64_t Fw, int64_t K,
-                                                          bool silu, const uint16_t* __restrict__ dout,
-                                                          uint16_t* __restrict__ out, int64_t ldo, int64_t low) {
-  constexpr bool BACK = TERMS > 0;
+__global__ void __launch_bounds__(Tl::NTHR, 2) k_ffn_sums(MmOperand W, int64_t w_low, MmOperand X, int64_t x_low, int64_t N,
+                                                          int64_t F, int64_t Fw, int64_t K, bool silu,
+                                                          const void* __restrict__ dout_, void* __restrict__ out_, int64_t ldo,
+                                                          int64_t low) {
+  constexpr bool BACK = TERMS > 0, FP32 = TERMS == 3;
+  using T = std::conditional_t<FP32, float, uint16_t>;
+  constexpr int kPasses = FP32 ? 6 : 1;
+  const T* const dout = static_cast<const T*>(dout_);
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Tl::LDS];
   static_assert(Tl::WM % 2 == 0, "pairs of blocks");
   constexpr int kPairs = Tl::BM / 2;   // outputs of a tile
@@ -165,12 +216,14 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_ffn_sums(MmOperand W, MmOperand
   Tl tile;
   tile.open(lds, W, 2 * Fw, X, N, 0, K);
   Units lu(f_tiles * n_tok), cu(lu);
+  int pass = 0;
   auto go_to = [&]() {
     uint32_t ft, tok;
     tile_of(lu.u, f_tiles, n_tok, kGroup, ft, tok);
     const int64_t f0 = static_cast<int64_t>(ft) * kPairs, n0 = static_cast<int64_t>(tok) * Tl::BN;
+    if constexpr (kPasses > 1) tile.B.base = X.base + term_of_b(pass) * x_low;
     tile.template seek<false, false>(0, n0);
-    tile.ab = reinterpret_cast<const uint8_t*>(W.base + f0 * W.ld);
+    tile.ab = reinterpret_cast<const uint8_t*>(W.base + (kPasses > 1 ? term_of_a(pass) * w_low : 0) + f0 * W.ld);
     const int lim = static_cast<int>(imin(Fw - 1 - f0, kPairs));
 #pragma unroll
     for (int p = 0; p < Tl::NLA; ++p) {   // rows in pairs of blocks; past the last output, the last one's
@@ -181,7 +234,10 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_ffn_sums(MmOperand W, MmOperand
     }
   };
   auto next = [&]() {
-    lu.advance();
+    if (kPasses == 1 || ++pass == kPasses) {
+      pass = 0;
+      lu.advance();
+    }
     if (lu.valid()) go_to();
   };
   if (!lu.valid()) return;
@@ -193,7 +249,12 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_ffn_sums(MmOperand W, MmOperand
     uint32_t ft, tok;
     tile_of(cu.u, f_tiles, n_tok, kGroup, ft, tok);
     const int64_t f0 = static_cast<int64_t>(ft) * kPairs, n0 = static_cast<int64_t>(tok) * Tl::BN;
-    tile.template multiply<false, false, false, false, kStores>(next, whole);
+    if constexpr (kPasses == 1) {
+      tile.template multiply<false, false, false, false, kStores>(next, whole);
+    } else {
+      tile.clear();
+      for (int t = 0; t < kPasses; ++t) tile.template multiply<false, false, true, false, kStores>(next, t == 0 && whole);
+    }
     const int f_left = static_cast<int>(imin(F - f0, kPairs)), toks = static_cast<int>(imin(N - n0, Tl::BN));
     // opaque, so that what follows from it is not kept in registers over the tiles
     int el = lane;
@@ -204,15 +265,17 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_ffn_sums(MmOperand W, MmOperand
 #pragma unroll
       for (int j = 0; j < Tl::WN; ++j) {
         const int t0 = (wc * Tl::WN + j) * 32 + te;
+        // fp32 data as the accumulators have it
+        const int tf = (wc * Tl::WN + j) * 32 + (el & 31), ff = 4 * (el >> 5);
         Packed dp[Tl::WM / 2];
-        if constexpr (BACK) {   // all of dout before the first use
+        if constexpr (BACK && !FP32) {   // all of dout before the first use
 #pragma unroll
           for (int i = 0; i < Tl::WM / 2; ++i) {
             const int fb = (wr * (Tl::WM / 2) + i) * 32 + fe;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               const int t = t0 + 16 * k;
-              const uint16_t* const at = dout + (n0 + t) * F + f0 + fb;
+              const T* const at = dout + (n0 + t) * F + f0 + fb;
               if (!EDGE || (t < toks && fb + 8 <= f_left)) {
                 __builtin_memcpy(&dp[i].o[k], at, 16);   // aligned or not
               } else {
@@ -230,7 +293,21 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_ffn_sums(MmOperand W, MmOperand
           const mm_f32x16 g = tile.acc[2 * i][j], u = tile.acc[2 * i + 1][j];
           float a[16], b[16];
           if constexpr (BACK) {
-            from_rows(dp[i], a);
+            if constexpr (FP32) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const int f = fb + 8 * q + ff;
+                const T* const at = dout + (n0 + tf) * F + f0 + f;
+                if (!EDGE || (tf < toks && f + 4 <= f_left)) {
+                  __builtin_memcpy(&a[4 * q], at, 16);   // aligned or not
+                } else {
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) a[4 * q + e] = tf < toks && f + e < f_left ? at[e] : 0.0f;
+                }
+              }
+            } else {
+              from_rows(dp[i], a);
+            }
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
               const float e = ex2(-kLog2e * g[r]), on = rcp(1.0f + e), off = e < __builtin_inff() ? e * on : 1.0f;
@@ -255,7 +332,7 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_ffn_sums(MmOperand W, MmOperand
           if (EDGE && fb >= f_left) continue;
 #pragma unroll
           for (int term = 0; BACK && term < TERMS; ++term) {
-            if (term == 1) {
+            if (term > 0) {
 #pragma unroll
               for (int r = 0; r < 16; ++r) a[r] = second_term(a[r]), b[r] = second_term(b[r]);
             }
@@ -264,7 +341,7 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_ffn_sums(MmOperand W, MmOperand
             for (int k = 0; k < 2; ++k) {
               const int t = t0 + 16 * k;
               if (EDGE && t >= toks) continue;
-              uint16_t* const to = out + term * low + (n0 + t) * ldo + 2 * (f0 + fb) + fe;
+              uint16_t* const to = static_cast<uint16_t*>(out_) + term * low + (n0 + t) * ldo + 2 * (f0 + fb) + fe;
               gstore(reinterpret_cast<mm_u32x4*>(to), pa.o[k]);
               gstore(reinterpret_cast<mm_u32x4*>(to + 32), pb.o[k]);
             }
@@ -275,7 +352,7 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_ffn_sums(MmOperand W, MmOperand
             for (int k = 0; k < 2; ++k) {
               const int t = t0 + 16 * k;
               if (EDGE && t >= toks) continue;
-              uint16_t* const to = out + (n0 + t) * ldo + f0 + fb + fe;
+              uint16_t* const to = static_cast<uint16_t*>(out_) + (n0 + t) * ldo + f0 + fb + fe;
               if (!EDGE || fb + fe + 8 <= f_left) {
                 __builtin_memcpy(to, &pa.o[k], 16);   // aligned or not
               } else {
@@ -302,10 +379,10 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_ffn_sums(MmOperand W, MmOperand
 // XCDs in turn).
 struct FfnProduct {
   MmOperand A, B;
-  int64_t R, K, len;
+  int64_t b_low, R, K, len;
   uint32_t slices, blocks;
   float* P;        // the slices' sums, R x C each
-  uint16_t* out;   // one slice: the result
+  void* out;       // one slice: the result
   __device__ __forceinline__ uint32_t unit(uint32_t b) const {
     const uint32_t x = b % kXcd;
     return x * (blocks / kXcd) + min(x, blocks % kXcd) + b / kXcd;
@@ -316,11 +393,13 @@ struct FfnProduct {
 // `out` the sums rounded once.  TA: dW, A(r, k) = dz(k, r), the rows r in pairs
 // of blocks: of `out`, row (r / 32 % 2) F + r / 64 * 32 + r % 32, if below F in
 // its half.  Otherwise dx, k in pairs of blocks: B's rows (W) are half a stage
-// of 64 from the gate's, half from the up rows Fw further on.  TERMS = 2: A's
-// second terms, `low` elements further on, go over the same B.
+// of 64 from the gate's, half from the up rows Fw further on.  dz has TERMS
+// terms, `low` elements apart; with three (fp32) B has as many, b_low apart.
 template <class Tl, bool TA, int TERMS>
 __device__ __forceinline__ void ffn_product(uint8_t* lds, const FfnProduct& p, uint32_t u, int64_t C, int64_t F, int64_t Fw,
                                             int64_t low) {
+  using S = Storage<TERMS == 3 ? kF32 : kBF16>;
+  using T = typename S::T;
   const uint32_t n_col = static_cast<uint32_t>((C + Tl::BN - 1) / Tl::BN), tiles = p.blocks / p.slices, z = u / tiles, ti = u - z * tiles;
   const int64_t c0 = static_cast<int64_t>(ti % n_col) * Tl::BN, r0 = static_cast<int64_t>(ti / n_col) * Tl::BM;
   const int64_t k0 = static_cast<int64_t>(z) * p.len, k1 = imin(k0 + p.len, p.K), R = p.R;
@@ -329,12 +408,16 @@ __device__ __forceinline__ void ffn_product(uint8_t* lds, const FfnProduct& p, u
   const int wr = wave / Tl::WC, wc = wave % Tl::WC;
   Tl tile;
   tile.open(lds, p.A, R, p.B, C, k0, k1);
+  constexpr int kPasses = TERMS == 3 ? 6 : TERMS;
+  int pass = 0;
   auto go_to = [&]() {
+    tile.A.base = p.A.base + (TERMS == 3 ? term_of_a(pass) : pass) * low;
     tile.B = p.B;
+    if constexpr (TERMS == 3) tile.B.base += term_of_b(pass) * p.b_low;
     tile.template seek<TA, true>(r0, c0);
     if constexpr (!TA) {
       static_assert(Tl::KS == 64, "a stage is a pair of blocks");
-      tile.bb = reinterpret_cast<const uint8_t*>(p.B.base + k0 / 2 * p.B.ld + c0);
+      tile.bb = reinterpret_cast<const uint8_t*>(tile.B.base + k0 / 2 * p.B.ld + c0);
 #pragma unroll
       for (int q = 0; q < Tl::NLB; ++q) {
         int s, f;
@@ -344,18 +427,16 @@ __device__ __forceinline__ void ffn_product(uint8_t* lds, const FfnProduct& p, u
       tile.B.ld = p.B.ld / 2;   // a stage goes on by 32 rows of either half
     }
   };
-  int term = 0;
   auto next = [&]() {
-    if (++term < TERMS) {
-      tile.A.base += low;
-      go_to();
-    }
+    if (++pass < kPasses) go_to();
   };
   go_to();
   tile.clear();
   tile.template prime<TA, true>(next);
-  tile.template multiply<TA, true>(next);
-  if constexpr (TERMS == 2) tile.template multiply<TA, true, true>(next);
+  if constexpr (kPasses == 1)
+    tile.template multiply<TA, true>(next);
+  else
+    for (int t = 0; t < kPasses; ++t) tile.template multiply<TA, true, true>(next);
   const int rows = static_cast<int>(imin(R - r0, Tl::BM)), cols = static_cast<int>(imin(C - c0, Tl::BN));
   const int rl = wr * Tl::WM * 32 + 4 * half, cl = wc * Tl::WN * 32 + l32;
 #pragma unroll
@@ -372,7 +453,7 @@ __device__ __forceinline__ void ffn_product(uint8_t* lds, const FfnProduct& p, u
         if (rl + 32 * i + ri >= rows || cl + 32 * j >= cols) continue;
         if (p.slices == 1) {
           if (4 * half + ri < there)
-            p.out[(ob + 4 * half + ri) * C + c0 + cl + 32 * j] = Storage<kBF16>::pack(tile.acc[i][j][r]);
+            static_cast<T*>(p.out)[(ob + 4 * half + ri) * C + c0 + cl + 32 * j] = S::pack(tile.acc[i][j][r]);
         } else {
           p.P[(z * R + r0 + rl + 32 * i + ri) * C + c0 + cl + 32 * j] = tile.acc[i][j][r];
         }
@@ -395,6 +476,7 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_ffn_grads(FfnProduct x, FfnProd
 
 // out = the sum over z, in order, of P[z], rounded once, of either product with
 // more than one slice (nx, nw values, or 0); dW's rows as in ffn_product
+template <bool FP32>
 __global__ void __launch_bounds__(256) k_ffn_join(FfnProduct x, int64_t nx, FfnProduct w, int64_t nw, int64_t C, int64_t F) {
   int64_t i = block_in_rows() * 256 + threadIdx.x;
   if (i >= nx + nw) return;
@@ -406,77 +488,36 @@ __global__ void __launch_bounds__(256) k_ffn_join(FfnProduct x, int64_t nx, FfnP
   const int S = static_cast<int>(is_w ? w.slices : x.slices);
   float sum = 0.0f;
   for (int z = 0; z < S; ++z) sum += P[z * n + i];
-  (is_w ? w.out : x.out)[(is_w ? ((r >> 5) & 1) * F + f : r) * C + c] = Storage<kBF16>::pack(sum);
+  using St = Storage<FP32 ? kF32 : kBF16>;
+  static_cast<typename St::T*>(is_w ? w.out : x.out)[(is_w ? ((r >> 5) & 1) * F + f : r) * C + c] = St::pack(sum);
 }
 
-// zeros in columns c0 .. of rows of ld values
 template <class T>
-__global__ void __launch_bounds__(256) k_ffn_zero(T* __restrict__ out, int64_t R, int64_t c0, int64_t ld) {
-  const int64_t i = block_in_rows() * 256 + threadIdx.x, w = ld - c0, r = i / w;
-  if (r < R) out[r * ld + c0 + i - r * w] = T(0);
-}
-
-// ---------------------------------------------------------------- fp32 ----
-
-// out (C x ld) = the transpose of in (R x C), zeros past R.  The first's n0 blocks, the second's n1.
-struct FfnTurn {
-  const float* in;
-  int64_t R, C;
-  float* out;
-  int64_t ld;
-  __host__ __device__ int64_t blocks() const { return (ld + 63) / 64 * ((C + 63) / 64); }
-};
-__global__ void __launch_bounds__(256) k_ffn_turn(FfnTurn first, int64_t n0, FfnTurn second, int64_t n1) {
-  __shared__ float tile[64][65];
-  int64_t b = block_in_rows();
-  const bool one = b < n0;
-  const FfnTurn t = one ? first : second;
-  if (!one && (b -= n0) >= n1) return;
-  const int64_t across = (t.C + 63) / 64, r0 = b / across * 64, c0 = b % across * 64;
-  const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int64_t r = r0 + ty + 4 * i, c = c0 + tx;
-    tile[ty + 4 * i][tx] = r < t.R && c < t.C ? t.in[r * t.C + c] : 0.0f;
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int64_t c = c0 + ty + 4 * i, r = r0 + tx;
-    if (c < t.C && r < t.ld) t.out[c * t.ld + r] = tile[tx][ty + 4 * i];
-  }
-}
-
-// out = the sum over z, in order, of P[z], of dx (nx values) and dW (nw)
-__global__ void __launch_bounds__(256) k_ffn_add(const float* __restrict__ px, int sx, int64_t nx, float* __restrict__ dx,
-                                                 const float* __restrict__ pw, int sw, int64_t nw, float* __restrict__ dW) {
-  int64_t i = block_in_rows() * 256 + threadIdx.x;
-  const bool is_w = i >= nx;
-  if (is_w) i -= nx;
-  const int64_t n = is_w ? nw : nx;
-  if (i >= n) return;
-  const float* const P = is_w ? pw : px;
-  float sum = 0.0f;
-  for (int z = 0, S = is_w ? sw : sx; z < S; ++z) sum += P[z * n + i];
-  (is_w ? dW : dx)[i] = sum;
+__global__ void __launch_bounds__(256) k_ffn_zero(T* __restrict__ out, int64_t n) {
+  const int64_t i = block_in_rows() * 256 + threadIdx.x;
+  if (i < n) out[i] = T(0);
 }
 
 // ---------------------------------------------------------------- plan ----
 
-constexpr int kBigTerms = 1;
-
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
 
 // Few rows are gated_few.hip's: as many of its workgroups of 64 rows and 16 outputs
-// as one round of the device takes (bf16) or two (fp32, which takes the
-// tiles longer).  us, few and the tiles: 65 x 512 x 1408 bf16 6.8 and
+// as one round of the device takes (bf16) or two (fp32, which takes the tiles
+// longer).  us, few and the tiles: 65 x 512 x 1408 bf16 6.8 and
 // 10.0; 65 x 1024 x 4096 bf16 18 and 15; 256 x 512 x 1408 fp32 20 and 25.
 bool few_rows(const GatedFfnArgs& a) { return cdiv(a.N, 64) * cdiv(a.F, 16) <= (a.bf16 ? kCus : 2 * kCus); }
 
 // The 256 x 256 tiles where at least 128 of them keep the device busy, or the
 // quarter tiles.  us, quarter and large: 3000 x 512 x 1408 (132 tiles) out 17 and
-// 18, the gradients (two terms of dz) 80 and 65; 8192 x 512 x 1408 gradients 147 and 107.
-bool big_tiles(const GatedFfnArgs& a) { return cdiv(a.N, Big::BN) * cdiv(a.F, Big::BM / 2) >= 128; }
+// 18, the gradients (two terms of dz) 80 and 63; 8192 x 512 x 1408 gradients 147
+// and 107.  fp32: from 192 on, and where a pass is long enough to hide the start
+// of the next: 5003 x 517 x 1387 377 and 304, 16384 x 512 x 1024 663 and 582, but
+// 8192 x 512 x 512 (128 tiles) 173 and 203, 16384 x 256 x 512 191 and 212.
+bool big_tiles(const GatedFfnArgs& a) {
+  const int64_t tiles = cdiv(a.N, Big::BN) * cdiv(a.F, Big::BM / 2);
+  return a.bf16 ? tiles >= 128 : tiles >= 192 && a.d > 256;
+}
 
 // How dx and dW, whose units share a launch, are cut: tiles of BM x BN, and slices of their sums.
 struct Slices {
@@ -522,30 +563,29 @@ Split split_of(int64_t N, int64_t Z, int64_t d, int terms, double* us) {
 }
 
 struct Plan {
-  bool big;               // bf16: the large tiles
-  bool pad_x, pad_w;      // x and W laid out anew: rows that are no multiple of 16 bytes; for dx W's halves of Fw rows
+  bool big;               // the large tiles
+  bool pad_x, pad_w;      // x and W laid out anew: rows that are no multiple of 16 bytes; fp32: in terms; for dx W's halves of Fw rows
   int64_t ldp, Fw;
   size_t x_off, w_off;
   // backward
   int64_t Fp, ldz;        // dz: columns of either kind, elements from row to row
-  int terms;              // of dz
-  int64_t low;            // elements from its first to its second
+  int64_t low;            // elements from a term to the next
   bool wide;              // 256 x 192 for dx and dW
   Slices x, w;            // of their sums
   bool w_first;
-  bool tn;
-  size_t z_off, px_off, pw_off, wt_off, zt_off, xt_off, total;
+  size_t z_off, px_off, pw_off, total;
 };
 
 Plan plan_of(const GatedFfnArgs& a, bool back) {
   Plan p{};
-  const int64_t vec = a.bf16 ? 8 : 4, elt = a.bf16 ? 2 : 4;
-  p.big = a.bf16 && big_tiles(a);
+  // bytes of x and W laid out: fp32 for the backward, three terms
+  const int64_t vec = a.bf16 || back ? 8 : 4, elt = a.bf16 ? 2 : back ? 6 : 4;
+  p.big = big_tiles(a);
   p.ldp = cdiv(a.d, vec) * vec;
   p.Fp = cdiv(a.F, 32) * 32;
-  p.pad_x = a.d != p.ldp;
-  p.pad_w = p.pad_x || (back && a.bf16 && a.F != p.Fp);
-  p.Fw = back && a.bf16 ? p.Fp : a.F;
+  p.pad_x = elt == 6 || a.d != p.ldp;
+  p.pad_w = p.pad_x || (back && a.F != p.Fp);
+  p.Fw = back ? p.Fp : a.F;
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t at = off;
@@ -554,97 +594,82 @@ Plan plan_of(const GatedFfnArgs& a, bool back) {
   };
   if (p.pad_x) p.x_off = take(size_t(a.N) * p.ldp * elt);
   if (p.pad_w) p.w_off = take(size_t(2) * p.Fw * p.ldp * elt);
-  if (back && a.bf16) {
+  if (back) {
     p.ldz = 2 * p.Fp + 64;   // rows are no power of two apart: they would fall on few memory channels
-    p.terms = p.big ? kBigTerms : 2;
     const int64_t Z = 2 * p.Fp;
+    const int terms = !a.bf16 ? 3 : p.big ? 1 : 2, passes = a.bf16 ? terms : 6;
     double us, us_wide = -1;
-    Split cut = p.big ? split_of<Big>(a.N, Z, a.d, p.terms, &us) : split_of<Mid>(a.N, Z, a.d, p.terms, &us);
+    Split cut = p.big ? split_of<Big>(a.N, Z, a.d, passes, &us) : split_of<Mid>(a.N, Z, a.d, passes, &us);
     if (p.big) {
-      const Split wide = split_of<Wide>(a.N, Z, a.d, p.terms, &us_wide);
+      const Split wide = split_of<Wide>(a.N, Z, a.d, passes, &us_wide);
       p.wide = us_wide < us;
       if (p.wide) cut = wide;
     }
     p.x = cut.x, p.w = cut.w, p.w_first = cut.w_first;
     auto sums = [&](int64_t rows, const Slices& c) { return c.s > 1 ? size_t(c.s) * rows * a.d * 4 : 0; };
     p.low = a.N * p.ldz;
-    p.z_off = take(size_t(p.terms) * p.low * 2);
+    p.z_off = take(size_t(terms) * p.low * 2);
     p.px_off = take(sums(a.N, p.x));
     p.pw_off = take(sums(Z, p.w));
-  } else if (back) {
-    // The projection's tiles take operands in rows of the summed index.  A sum is
-    // cut into slices where there are too few tiles for the device, of equal
-    // length where half as many slices allow it (what is left over is zeros).
-    auto cut = [&](int64_t rows, int64_t cols, int64_t K, Slices& c) {
-      const int64_t want = std::max<int64_t>(1, std::min<int64_t>({cdiv(512, cdiv(rows, 128) * cdiv(cols, 128)), K / 128, 64}));
-      for (int64_t n = want; n >= (want + 1) / 2; --n)
-        if (K % (n * vec) == 0) {
-          c.s = n, c.len = K / n;
-          return;
-        }
-      c.len = want > 1 ? cdiv(cdiv(K, want), 64) * 64 : cdiv(K, vec) * vec;
-      c.s = cdiv(K, c.len);
-    };
-    cut(a.N, a.d, 2 * a.F, p.x);
-    p.ldz = p.x.s * p.x.len;
-    p.z_off = take(size_t(a.N) * p.ldz * 4);
-    p.wt_off = take(size_t(a.d) * p.ldz * 4);
-    p.tn = 2 * a.F % 256 == 0 && a.d % 256 == 0;   // or both operands of dW in rows of their own
-    if (p.tn) {
-      const int64_t s = std::max<int64_t>(1, std::min<int64_t>(kCus / ((2 * a.F / 256) * (a.d / 256)), cdiv(a.N, 256)));
-      p.w.len = cdiv(cdiv(a.N, s), 256) * 256;
-      p.w.s = cdiv(a.N, p.w.len);
-    } else {
-      cut(2 * a.F, a.d, a.N, p.w);
-      p.zt_off = take(size_t(2) * a.F * p.w.s * p.w.len * 4);
-      p.xt_off = take(size_t(a.d) * p.w.s * p.w.len * 4);
-    }
-    p.px_off = take(p.x.s > 1 ? size_t(p.x.s) * a.N * a.d * 4 : 0);
-    p.pw_off = take(p.tn || p.w.s > 1 ? size_t(p.w.s) * 2 * a.F * a.d * 4 : 0);
   }
   p.total = off;
   return p;
 }
 
 struct Operands {
-  const void *x, *W;
+  MmOperand x, W;         // fp32: the first of three terms,
+  int64_t x_low, w_low;   // this far apart
 };
 Operands lay_out(const GatedFfnArgs& a, const Plan& p, const void* x, const void* W) {
-  void *const xp = a.ws + p.x_off, *const wp = a.ws + p.w_off;
+  uint16_t *const xp = reinterpret_cast<uint16_t*>(a.ws + p.x_off), *const wp = reinterpret_cast<uint16_t*>(a.ws + p.w_off);
   const int64_t Nx = p.pad_x ? a.N : 0, Fw = p.pad_w ? p.Fw : 0;
-  const dim3 grid = rows_of_blocks(cdiv((Nx + 2 * Fw) * (p.ldp / (a.bf16 ? 8 : 4)), 256));
-  auto go = [&](auto zero) {
-    using T = decltype(zero);
-    k_ffn_pad<T><<<grid, 256, 0, a.stream>>>(static_cast<const T*>(x), Nx, static_cast<const T*>(W), a.F, Fw, a.d, p.ldp,
-                                             static_cast<T*>(xp), static_cast<T*>(wp));
-  };
-  if (Nx + Fw > 0) {
-    if (a.bf16) go(uint16_t(0)); else go(0.0f);
+  const dim3 grid = rows_of_blocks(cdiv((Nx + 2 * Fw) * (p.ldp / 8), 256));
+  if (!a.bf16)
+    k_ffn_terms<<<grid, 256, 0, a.stream>>>(static_cast<const float*>(x), Nx, static_cast<const float*>(W), a.F, Fw, a.d, p.ldp, xp, wp);
+  else if (Nx + Fw > 0)
+    k_ffn_pad<<<grid, 256, 0, a.stream>>>(static_cast<const uint16_t*>(x), Nx, static_cast<const uint16_t*>(W), a.F, Fw, a.d,
+                                          p.ldp, xp, wp);
+  return {{p.pad_x ? xp : static_cast<const uint16_t*>(x), p.ldp}, {p.pad_w ? wp : static_cast<const uint16_t*>(W), p.ldp},
+          a.N * p.ldp, 2 * p.Fw * p.ldp};
+}
+
+// fp32 out: the projection's tiles
+void out_fp32(const GatedFfnArgs& a, const Plan& p, const float* x, const float* W, float* out) {
+  float *const xp = reinterpret_cast<float*>(a.ws + p.x_off), *const wp = reinterpret_cast<float*>(a.ws + p.w_off);
+  if (p.pad_x) {
+    k_ffn_pad<<<rows_of_blocks(cdiv((a.N + 2 * a.F) * (p.ldp / 4), 256)), 256, 0, a.stream>>>(x, a.N, W, a.F, a.F, a.d, p.ldp, xp, wp);
+    x = xp, W = wp;
   }
-  return {p.pad_x ? xp : x, p.pad_w ? wp : W};
+  launch_proj_gated(x, W, out, a.N, p.ldp, a.F, a.silu, a.stream);
 }
 
-void fill_zero(const GatedFfnArgs& a, void* out, int64_t R, int64_t c0, int64_t ld) {
-  const dim3 grid = rows_of_blocks(cdiv(R * (ld - c0), 256));
+void fill_zero(const GatedFfnArgs& a, void* out, int64_t n) {
+  const dim3 grid = rows_of_blocks(cdiv(n, 256));
   if (a.bf16)
-    k_ffn_zero<uint16_t><<<grid, 256, 0, a.stream>>>(static_cast<uint16_t*>(out), R, c0, ld);
+    k_ffn_zero<<<grid, 256, 0, a.stream>>>(static_cast<uint16_t*>(out), n);
   else
-    k_ffn_zero<float><<<grid, 256, 0, a.stream>>>(static_cast<float*>(out), R, c0, ld);
+    k_ffn_zero<<<grid, 256, 0, a.stream>>>(static_cast<float*>(out), n);
 }
 
-// bf16: out, or with dout dz
+// out (bf16), or with dout dz
 void sums(const GatedFfnArgs& a, const Plan& p, const Operands& o, const void* dout, void* out, int64_t ldo) {
-  const MmOperand W{static_cast<const uint16_t*>(o.W), p.ldp}, X{static_cast<const uint16_t*>(o.x), p.ldp};
   auto go = [&](auto tl, auto terms) {
     using Tl = decltype(tl);
     const unsigned grid = unsigned(std::min(cdiv(a.N, Tl::BN) * cdiv(a.F, Tl::BM / 2), kCus * 8 / Tl::NW));
-    k_ffn_sums<Tl, decltype(terms)::value><<<grid, Tl::NTHR, 0, a.stream>>>(
-        W, X, a.N, a.F, p.Fw, p.ldp, a.silu, static_cast<const uint16_t*>(dout), static_cast<uint16_t*>(out), ldo, p.low);
+    k_ffn_sums<Tl, decltype(terms)::value><<<grid, Tl::NTHR, 0, a.stream>>>(o.W, o.w_low, o.x, o.x_low, a.N, a.F, p.Fw, p.ldp, a.silu,
+                                                                            dout, out, ldo, p.low);
   };
-  auto kind = [&](auto tl, auto back) {
-    if (dout) go(tl, back); else go(tl, std::integral_constant<int, 0>{});
-  };
-  if (p.big) kind(Big{}, std::integral_constant<int, kBigTerms>{}); else kind(Mid{}, std::integral_constant<int, 2>{});
+  constexpr std::integral_constant<int, 0> none{};
+  constexpr std::integral_constant<int, 1> one{};
+  constexpr std::integral_constant<int, 2> two{};
+  constexpr std::integral_constant<int, 3> three{};
+  if (!dout) {
+    if (p.big) go(Big{}, none); else go(Mid{}, none);
+  } else if (a.bf16) {
+    if (p.big) go(Big{}, one); else go(Mid{}, two);
+  } else {
+    if (p.big) go(Big{}, three); else go(Mid{}, three);
+  }
 }
 
 }  // namespace
@@ -663,55 +688,28 @@ void launch_gated_ffn(const GatedFfnArgs& a, const void* x, const void* W, void*
     return;
   }
   const Plan p = plan_of(a, false);
-  const Operands o = lay_out(a, p, x, W);
   if (a.bf16)
-    sums(a, p, o, nullptr, out, a.F);
+    sums(a, p, lay_out(a, p, x, W), nullptr, out, a.F);
   else
-    launch_proj_gated(static_cast<const float*>(o.x), static_cast<const float*>(o.W), static_cast<float*>(out), a.N, p.ldp,
-                      GatedProj{nullptr, a.F, 0, a.silu, nullptr, 0}, a.stream);
+    out_fp32(a, p, static_cast<const float*>(x), static_cast<const float*>(W), static_cast<float*>(out));
 }
 
 size_t gated_ffn_backward_workspace(const GatedFfnArgs& a) { return a.N ? plan_of(a, true).total : 0; }
 
 void launch_gated_ffn_backward(const GatedFfnArgs& a, const void* x, const void* W, const void* dout, void* dx, void* dW) {
   if (a.N == 0) {   // no row: dW is zero
-    if (dW) fill_zero(a, dW, 1, 0, 2 * a.F * a.d);
+    if (dW) fill_zero(a, dW, 2 * a.F * a.d);
     return;
   }
   const Plan p = plan_of(a, true);
   const Operands o = lay_out(a, p, x, W);
-  void* const dz = a.ws + p.z_off;
+  uint16_t* const dz = reinterpret_cast<uint16_t*>(a.ws + p.z_off);
   float *const px = reinterpret_cast<float*>(a.ws + p.px_off), *const pw = reinterpret_cast<float*>(a.ws + p.pw_off);
-  if (!a.bf16) {
-    const int64_t Z = 2 * a.F, bz = p.ldz * 4, ldt = p.w.s * p.w.len;
-    const bool turned = dW && !p.tn;   // dW's operands
-    const float* const xf = static_cast<const float*>(x);
-    float *const z = static_cast<float*>(dz), *const wt = reinterpret_cast<float*>(a.ws + p.wt_off);
-    float *const zt = reinterpret_cast<float*>(a.ws + p.zt_off), *const xt = reinterpret_cast<float*>(a.ws + p.xt_off);
-    float *const dxf = static_cast<float*>(dx), *const dWf = static_cast<float*>(dW);
-    const FfnTurn turn_w{static_cast<const float*>(W), Z, a.d, wt, p.ldz}, turn_x{xf, a.N, a.d, xt, ldt};
-    const int64_t bw = dx ? turn_w.blocks() : 0, bx = turned ? turn_x.blocks() : 0;
-    if (bw + bx > 0) k_ffn_turn<<<rows_of_blocks(bw + bx), 256, 0, a.stream>>>(turn_w, bw, turn_x, bx);
-    launch_proj_gated(static_cast<const float*>(o.x), static_cast<const float*>(o.W), z, a.N, p.ldp,
-                      GatedProj{static_cast<const float*>(dout), a.F, p.ldz, a.silu, turned ? zt : nullptr, ldt}, a.stream);
-    if (dx && p.ldz > Z) fill_zero(a, z, a.N, Z, p.ldz);
-    if (turned && ldt > a.N) fill_zero(a, zt, Z, a.N, ldt);
-    const int64_t nx = dx && p.x.s > 1 ? a.N * a.d : 0, nw = dW && (p.tn || p.w.s > 1) ? Z * a.d : 0;
-    if (nx) launch_proj_splitk(false, z, bz, wt, bz, px, a.N, a.d, p.x.len, int(p.x.s), a.stream);
-    else if (dx) launch_proj_ld(false, z, bz, wt, bz, dxf, a.N, a.d, p.x.len, a.stream);
-    if (dW && p.tn) launch_proj_tn(false, z, bz, xf, a.d * 4, pw, a.N, Z, a.d, p.w.len, int(p.w.s), nullptr, a.stream);
-    else if (nw) launch_proj_splitk(false, zt, ldt * 4, xt, ldt * 4, pw, Z, a.d, p.w.len, int(p.w.s), a.stream);
-    else if (dW) launch_proj_ld(false, zt, ldt * 4, xt, ldt * 4, dWf, Z, a.d, ldt, a.stream);
-    if (nx + nw > 0)
-      k_ffn_add<<<rows_of_blocks(cdiv(nx + nw, 256)), 256, 0, a.stream>>>(px, int(p.x.s), nx, dxf, pw, int(p.w.s), nw, dWf);
-    return;
-  }
   sums(a, p, o, dout, dz, p.ldz);
-  const MmOperand Z{static_cast<const uint16_t*>(dz), p.ldz}, X{static_cast<const uint16_t*>(o.x), p.ldp},
-      Wo{static_cast<const uint16_t*>(o.W), p.ldp};
+  const MmOperand Z{dz, p.ldz};
   const int64_t Zp = 2 * p.Fp;
-  FfnProduct to_x{Z, Wo, a.N, Zp, p.x.len, uint32_t(p.x.s), 0, px, static_cast<uint16_t*>(dx)};
-  FfnProduct to_w{Z, X, Zp, a.N, p.w.len, uint32_t(p.w.s), 0, pw, static_cast<uint16_t*>(dW)};
+  FfnProduct to_x{Z, o.W, o.w_low, a.N, Zp, p.x.len, uint32_t(p.x.s), 0, px, dx};
+  FfnProduct to_w{Z, o.x, o.x_low, Zp, a.N, p.w.len, uint32_t(p.w.s), 0, pw, dW};
   auto run = [&](auto tl, auto terms) {
     using Tl = decltype(tl);
     const int64_t n_col = cdiv(a.d, Tl::BN);
@@ -720,10 +718,21 @@ void launch_gated_ffn_backward(const GatedFfnArgs& a, const void* x, const void*
     k_ffn_grads<Tl, decltype(terms)::value><<<to_x.blocks + to_w.blocks, Tl::NTHR, 0, a.stream>>>(to_x, to_w, p.w_first, a.d, a.F,
                                                                                                   p.Fw, p.low);
   };
-  constexpr std::integral_constant<int, kBigTerms> of_big{};
-  if (!p.big) run(Mid{}, std::integral_constant<int, 2>{}); else if (p.wide) run(Wide{}, of_big); else run(Big{}, of_big);
+  constexpr std::integral_constant<int, 1> one{};
+  constexpr std::integral_constant<int, 2> two{};
+  constexpr std::integral_constant<int, 3> three{};
+  if (a.bf16) {
+    if (!p.big) run(Mid{}, two); else if (p.wide) run(Wide{}, one); else run(Big{}, one);
+  } else {
+    if (!p.big) run(Mid{}, three); else if (p.wide) run(Wide{}, three); else run(Big{}, three);
+  }
   const int64_t nx = dx && p.x.s > 1 ? a.N * a.d : 0, nw = dW && p.w.s > 1 ? Zp * a.d : 0;
-  if (nx + nw > 0) k_ffn_join<<<rows_of_blocks(cdiv(nx + nw, 256)), 256, 0, a.stream>>>(to_x, nx, to_w, nw, a.d, a.F);
+  if (nx + nw == 0) return;
+  const dim3 grid = rows_of_blocks(cdiv(nx + nw, 256));
+  if (a.bf16)
+    k_ffn_join<false><<<grid, 256, 0, a.stream>>>(to_x, nx, to_w, nw, a.d, a.F);
+  else
+    k_ffn_join<true><<<grid, 256, 0, a.stream>>>(to_x, nx, to_w, nw, a.d, a.F);
 }
 
 }  // namespace prn

@@ -1,5 +1,5 @@
 // Matrix-core tiles over bf16 or fp16 operands of either orientation, for the
-// vocabulary loss: acc = sum over k of A(r, k) B(c, k).
+// vocabulary loss and the feed-forward product: acc = sum over k of A(r, k) B(c, k).
 //
 // Each wave owns WM x WN blocks of 32 x 32; WR x WC waves make a workgroup's
 // tile of BM x BN.  K is walked in stages of BK values, NST stages in LDS,

@@ -16,19 +16,10 @@ namespace prn {
 void launch_proj(bool bf16, const void* A, const void* B, const float* bias, void* C, int64_t M, int64_t N,
                  int64_t K, hipStream_t stream);
 
-// A gated product of fp32 data: W holds F gate rows and F up rows, the sums g and
-// u of each pair meet in the epilogue.  Without dout out = act(g) u (M x F), with
-// dout (M x F) the gradients of the sums, [dout u act'(g) | dout act(g)], in rows
-// ldz apart, and with zt their transpose as well, in rows ldt apart (a multiple
-// of 4, at least M).  The products and requirements are launch_proj's.
-struct GatedProj {
-  const float* dout;
-  int64_t F, ldz;
-  bool silu;   // g s(g); else s(g)
-  float* zt;
-  int64_t ldt;
-};
-void launch_proj_gated(const float* x, const float* W, float* out, int64_t M, int64_t K, const GatedProj& gp,
+// out = act(x Wg^T) (x Wu^T), fp32, M x F: W holds F gate rows, then F up rows;
+// both sums of a pair meet in the epilogue.  act: g s(g) (silu) or s(g).  The
+// products and requirements are launch_proj's.
+void launch_proj_gated(const float* x, const float* W, float* out, int64_t M, int64_t K, int64_t F, bool silu,
                        hipStream_t stream);
 
 // The same product without bias, with operand rows lda / ldb bytes apart

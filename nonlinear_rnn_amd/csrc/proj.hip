@@ -59,7 +59,6 @@
 
 #include "bf16split.h"
 #include "gated_cell.h"
-#include "grid_rows.h"
 #include "proj.h"
 
 namespace prn {
@@ -123,35 +122,27 @@ struct Tile {
   static_assert(STAGE % (1024 * NW) == 0, "a stage must split evenly over the waves");
 };
 
-// GATED: the columns are pairs, gate and up, of a feed-forward product: B holds
-// gp.F gate rows and gp.F up rows, and every 64 columns of a wave are 32 of
-// each, so that a lane has both sums of its 16 rows and one pair of columns.
-// kGatedOut stores act(gate) up, M x F; kGatedBack the gradients of the two
-// sums from dout (M x F), in rows of gp.ldz.  N is 2 F (rounded up to whole pairs of
-// blocks, 64).
+// GATED (fp32): the columns are pairs, gate and up, of a feed-forward product: B
+// holds gp.F gate rows and gp.F up rows, and every 64 columns of a wave are 32 of
+// each, so that a lane has both sums of its 16 rows and one pair of columns;
+// act(gate) up is stored, M x F.  N is 2 F (rounded up to whole pairs of blocks, 64).
 //
 // OUTF32: store the fp32 sums as they are (no bias, no rounding), for the
 // split-K partial products of the weight gradient.  Operand rows are lda /
 // ldb bytes apart (16-byte multiples); slice z = blockIdx.y of a split-K
 // launch starts K elements into every operand row and writes its own M x N
 // block of C.
-enum { kPlain = 0, kGatedOut = 1, kGatedBack = 2 };
-// g s(g), or s(g), and its derivative
-__device__ __forceinline__ float gated_value(bool silu, float g) {
-  const float on = gate_of(g).on;
-  return silu ? g * on : on;
-}
-__device__ __forceinline__ float gated_slope(bool silu, float g) {
-  const Gate s = gate_of(g);
-  return silu ? s.on * fmaf(g, s.off, 1.0f) : s.on * s.off;
-}
+struct GatedProj {
+  int64_t F;
+  bool silu;
+};
 // column c of a gated product: its row of B (columns past the last pair: the last one's)
 __device__ __forceinline__ int64_t gated_row(int64_t c, int64_t F) {
   const int64_t f = (c >> 6) * 32 + (c & 31);
   return (f < F ? f : F - 1) + ((c >> 5) & 1) * F;
 }
 
-template <bool BF16, bool EDGE, int WR, int WC, bool OUTF32, int WM, int WN, int GATED = kPlain>
+template <bool BF16, bool EDGE, int WR, int WC, bool OUTF32, int WM, int WN, bool GATED = false>
 __global__ void __launch_bounds__(64 * WR * WC)
 k_proj(const uint8_t* __restrict__ A, const uint8_t* __restrict__ B, const float* __restrict__ bias,
        uint8_t* __restrict__ C, int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int n_tiles_n, int remap,
@@ -410,42 +401,17 @@ k_proj(const uint8_t* __restrict__ A, const uint8_t* __restrict__ B, const float
     }
   }
 
-  if constexpr (GATED != kPlain) {
+  if constexpr (GATED) {
     static_assert(WN == 2 && !OUTF32 && !BF16, "a gate and an up block");
     const int64_t f = ((n0 >> 6) + wc) * 32 + l32;
-    float* const out = reinterpret_cast<float*>(C);
 #pragma unroll
     for (int i = 0; i < WM; ++i) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int64_t gm = m0 + wr * WM * 32 + i * 32 + 8 * q + 4 * half;
+      for (int r = 0; r < 16; ++r) {
+        const int64_t gm = m0 + wr * WM * 32 + i * 32 + 8 * (r >> 2) + 4 * half + (r & 3);
         if (EDGE && (gm >= M || f >= gp.F)) continue;
-        f32x4 zg, zu;
-        const int n = EDGE ? static_cast<int>(M - gm < 4 ? M - gm : 4) : 4;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (EDGE && e >= n) continue;
-          const float g = acc[i][0][4 * q + e], u = acc[i][1][4 * q + e];
-          if constexpr (GATED == kGatedOut) {
-            out[(gm + e) * gp.F + f] = gated_value(gp.silu, g) * u;
-          } else {
-            const float d = gp.dout[(gm + e) * gp.F + f];
-            float* const to = out + (gm + e) * gp.ldz + f;
-            to[0] = zg[e] = d * u * gated_slope(gp.silu, g);
-            to[gp.F] = zu[e] = d * gated_value(gp.silu, g);
-          }
-        }
-        if (GATED == kGatedBack && gp.zt) {
-          float* const to = gp.zt + f * gp.ldt + gm;
-          if (n == 4) {
-            *reinterpret_cast<f32x4*>(to) = zg;
-            *reinterpret_cast<f32x4*>(to + gp.F * gp.ldt) = zu;
-          } else {
-#pragma unroll
-            for (int e = 0; e < 3; ++e)
-              if (e < n) to[e] = zg[e], to[gp.F * gp.ldt + e] = zu[e];
-          }
-        }
+        const float g = acc[i][0][r], on = gate_of(g).on;
+        reinterpret_cast<float*>(C)[gm * gp.F + f] = (gp.silu ? g * on : on) * acc[i][1][r];
       }
     }
     return;
@@ -705,28 +671,22 @@ void launch_proj(bool bf16, const void* A, const void* B, const float* bias, voi
     launch_tiles<2, 2, false>(bf16, A, B, bias, C, M, N, K, ld, ld, 1, stream);
 }
 
-void launch_proj_gated(const float* x, const float* W, float* out, int64_t M, int64_t K, const GatedProj& gp,
+void launch_proj_gated(const float* x, const float* W, float* out, int64_t M, int64_t K, int64_t F, bool silu,
                        hipStream_t stream) {
   using Large = Tile<4, 4>;
-  const int64_t N = (gp.F + 31) / 32 * 64, ld = K * 4;
-  auto run = [&](auto waves, auto ed, auto kind) {
+  const int64_t N = (F + 31) / 32 * 64, ld = K * 4;
+  auto run = [&](auto waves, auto ed) {
     constexpr int WV = decltype(waves)::value;
     using Tl = Tile<WV, WV>;
     const int64_t tn = (N + Tl::BN - 1) / Tl::BN, nb = ((M + Tl::BM - 1) / Tl::BM) * tn;
-    k_proj<false, decltype(ed)::value, WV, WV, false, 2, 2, decltype(kind)::value>
-        <<<unsigned(nb), Tl::NTHR, 0, stream>>>(reinterpret_cast<const uint8_t*>(x), reinterpret_cast<const uint8_t*>(W), nullptr,
-                                                reinterpret_cast<uint8_t*>(out), M, N, K, ld, ld, int(tn), nb % NXCD == 0, gp);
-  };
-  auto kinds = [&](auto waves, auto ed) {
-    if (gp.dout)
-      run(waves, ed, std::integral_constant<int, kGatedBack>{});
-    else
-      run(waves, ed, std::integral_constant<int, kGatedOut>{});
+    k_proj<false, decltype(ed)::value, WV, WV, false, 2, 2, true><<<unsigned(nb), Tl::NTHR, 0, stream>>>(
+        reinterpret_cast<const uint8_t*>(x), reinterpret_cast<const uint8_t*>(W), nullptr, reinterpret_cast<uint8_t*>(out), M, N, K,
+        ld, ld, int(tn), nb % NXCD == 0, GatedProj{F, silu});
   };
   auto edges = [&](auto waves) {
     constexpr int BN = decltype(waves)::value * 64;
-    const bool edge = M % BN != 0 || 2 * gp.F % BN != 0 || ld % ROWB != 0;
-    if (edge) kinds(waves, std::true_type{}); else kinds(waves, std::false_type{});
+    const bool edge = M % BN != 0 || 2 * F % BN != 0 || ld % ROWB != 0;
+    if (edge) run(waves, std::true_type{}); else run(waves, std::false_type{});
   };
   const int64_t large = ((M + Large::BM - 1) / Large::BM) * ((N + Large::BN - 1) / Large::BN);
   if (large >= kLargeTiles) edges(std::integral_constant<int, 4>{}); else edges(std::integral_constant<int, 2>{});
@@ -800,7 +760,7 @@ __global__ void __launch_bounds__(256) k_transpose(const typename Elt<BF16>::T* 
 template <bool BF16>
 __global__ void __launch_bounds__(256) k_pad_rows(const typename Elt<BF16>::T* __restrict__ in, int64_t R, int64_t C,
                                                   typename Elt<BF16>::T* __restrict__ out, int64_t Cp) {
-  const int64_t i = block_in_rows() * 256 + threadIdx.x;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (i >= R * Cp) return;
   const int64_t r = i / Cp, c = i - r * Cp;
   out[i] = c < C ? in[r * C + c] : Elt<BF16>::st(0.0f);
@@ -1011,7 +971,7 @@ void launch_transpose(bool bf16, const void* in, int64_t R, int64_t C, int64_t l
 }
 
 void launch_pad_rows(bool bf16, const void* in, int64_t R, int64_t C, void* out, int64_t Cp, hipStream_t stream) {
-  const dim3 grid = rows_of_blocks((R * Cp + 255) / 256);
+  const dim3 grid(static_cast<unsigned>((R * Cp + 255) / 256));
   if (bf16)
     k_pad_rows<true><<<grid, 256, 0, stream>>>(static_cast<const uint16_t*>(in), R, C, static_cast<uint16_t*>(out), Cp);
   else
