@@ -509,8 +509,10 @@ size_t prn_vocab_loss_backward_workspace_bytes(const prn_vocab_loss_params* para
  *   h0         (rows, d_h) storage dtype or NULL for zeros; rows = B, or n_seqs
  *              for a ragged pack
  *   cu_seqlens NULL, or a ragged pack's (n_seqs + 1) int32 offsets, as for
- *              prn_newton_forward.  Whatever a sequence holds, infinities and
- *              NaN included, reaches no other one
+ *              prn_newton_forward, except that cu[n_seqs] may be below T: the
+ *              steps behind it belong to no sequence, their H_out and dxproj_out
+ *              are zeros, whatever the inputs hold there.  Whatever a sequence
+ *              holds, infinities and NaN included, reaches no other one
  *   H_out      (B, T, d_h) storage dtype
  * params: cell, dtype, B, T (below 2^31), d_h, n_seqs, state_last_out
  * ((rows, d_h) or NULL; an empty sequence's is its h0), workspace (at least

@@ -380,6 +380,8 @@ def _pack_offsets(cu_seqlens, T: int, device):
     if cu_seqlens is None:
         return None
     if isinstance(cu_seqlens, torch.Tensor) and cu_seqlens.device == device and cu_seqlens.dtype == torch.int32:
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+            raise ValueError("cu_seqlens must be 1-D with at least 2 entries")
         return cu_seqlens.contiguous()
     return validate_cu_seqlens(cu_seqlens, T, device)
 
@@ -403,7 +405,8 @@ def gated_scan(xproj, *, cell: str, h0=None, cu_seqlens=None, return_state=False
 
     s the logistic function.  H (B, T, d), with return_state also the final states (rows, 1, d); h0 (rows, 1, d)
     or None for zeros.  A ragged pack has B = 1 and cu_seqlens: int32 offsets on the device are used without a look
-    at them, anything else is validated first.  The state is fp32 within a call."""
+    at them (they may end before T, as in a pack of a fixed size: H is zero behind them), anything else is validated
+    first.  The state is fp32 within a call."""
     _check_gated(xproj, cell)
     xproj, h0 = _aligned(xproj), _aligned(h0)
     Bn, T, _, d = xproj.shape

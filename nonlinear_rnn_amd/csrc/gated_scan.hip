@@ -28,7 +28,8 @@
 //
 // A sequence's first step in a pack cuts the map: h_in does not count, whatever
 // it is (a NaN of the sequence before stays there).  Since a >= 0 otherwise,
-// a = -0 says so, and stays -0 in every product with what comes after.
+// a = -0 says so, and stays -0 in every product with what comes after.  Steps
+// behind the last sequence get zeros.
 //
 // Next to the memory traffic, what counts is the arithmetic: a gate is an
 // exponential and a quotient, 16 cycles of a wave each.  Rows are addressed from
@@ -102,7 +103,7 @@ template <int LS>
 struct Cuts {
   uint32_t head, tail;
   int32_t seg[LS];
-  __device__ __forceinline__ void find(const int32_t* cu, int64_t n_seqs, int64_t t0, int n, int64_t T) {
+  __device__ __forceinline__ void find(const int32_t* cu, int64_t n_seqs, int64_t t0, int n, int64_t end) {
     head = tail = 0;
     if (n <= 0) return;
     SegTracker s;
@@ -111,7 +112,7 @@ struct Cuts {
     for (int j = 0; j < LS; ++j) {
       if (j < n) {
         if (s.at(t0 + j)) head |= 1u << j;
-        if (s.last(t0 + j, T)) tail |= 1u << j;
+        if (s.last(t0 + j, end)) tail |= 1u << j;
         seg[j] = static_cast<int32_t>(s.seg);
       }
     }
@@ -127,6 +128,11 @@ struct Tensors {
   const int32_t* cu;
   int64_t n_seqs, B, T_, d;
   int64_t chains, chunks;
+  // the steps of a row that belong to a sequence: a pack may end before its tensor
+  template <bool RAGGED>
+  __device__ __forceinline__ int64_t end() const {
+    return RAGGED ? imin(imax(static_cast<int64_t>(cu[n_seqs]), 0), T_) : T_;
+  }
 };
 
 // ------------------------------------------------------------ look-back ----
@@ -264,7 +270,7 @@ struct Fore {
 
   __device__ __forceinline__ void load(const Tensors<DT>& t, const Place<V>& at, int64_t first) {
     s0 = first + at.wave * LS;
-    n = static_cast<int>(imax(imin(LS, t.T_ - s0), 0));
+    n = static_cast<int>(imax(imin(LS, t.template end<RAGGED>() - s0), 0));
     const typename C::T* const x = t.x + at.row * t.T_ * G * t.d + at.tile;
 #pragma unroll
     for (int j = 0; j < LS; ++j) {
@@ -295,7 +301,7 @@ struct Fore {
     }
   }
   __device__ __forceinline__ void maps(const Tensors<DT>& t, const Place<V>& at, Map (&m)[V]) {
-    if constexpr (RAGGED) cut.find(t.cu, t.n_seqs, s0, n, t.T_);
+    if constexpr (RAGGED) cut.find(t.cu, t.n_seqs, s0, n, t.template end<RAGGED>());
 #pragma unroll
     for (int c = 0; c < V; ++c) m[c] = {1.0f, 0.0f};
     if (n == LS) maps_of<true>(t, at, m); else maps_of<false>(t, at, m);
@@ -306,7 +312,10 @@ struct Fore {
     typename C::T* const H = t.H + (at.row * t.T_ + s0) * t.d + at.tile;
 #pragma unroll
     for (int j = 0; j < LS; ++j) {
-      if (!ALL && j >= n) continue;
+      if (!ALL && j >= n) {
+        if (RAGGED && s0 + j < t.T_ && at.live) C{}.store(H + j * t.d, at.off);
+        continue;
+      }
       C o;
 #pragma unroll
       for (int c = 0; c < V; ++c) h[c] = through<RAGGED>(s[j][c], h[c]);
@@ -448,7 +457,7 @@ struct Back {
 
   __device__ __forceinline__ void load(const Tensors<DT>& t, const Place<V>& at, int64_t first) {
     s0 = first + at.wave * LS;
-    n = static_cast<int>(imax(imin(LS, t.T_ - s0), 0));
+    n = static_cast<int>(imax(imin(LS, t.template end<RAGGED>() - s0), 0));
     const int64_t row = at.row * t.T_;
 #pragma unroll
     for (int j = 0; j < LS; ++j) {
@@ -499,7 +508,7 @@ struct Back {
     }
   }
   __device__ __forceinline__ void maps(const Tensors<DT>& t, const Place<V>& at, Map (&fore)[V], Map (&back)[V]) {
-    if constexpr (RAGGED) cut.find(t.cu, t.n_seqs, s0, n, t.T_);
+    if constexpr (RAGGED) cut.find(t.cu, t.n_seqs, s0, n, t.template end<RAGGED>());
 #pragma unroll
     for (int c = 0; c < V; ++c) fore[c] = back[c] = {1.0f, 0.0f};
     if (n == LS) maps_of<true>(t, at, fore, back); else maps_of<false>(t, at, fore, back);
@@ -521,7 +530,12 @@ struct Back {
     typename ST::T* const dx = t.dx + (at.row * t.T_ + s0) * G * t.d + at.tile;
 #pragma unroll
     for (int j = LS - 1; j >= 0; --j) {
-      if (!ALL && j >= n) continue;
+      if (!ALL && j >= n) {
+#pragma unroll
+        for (int k = 0; k < G; ++k)
+          if (RAGGED && s0 + j < t.T_ && at.live) C{}.store(dx + (j * G + k) * t.d, at.off);
+        continue;
+      }
       float o[G][V];
 #pragma unroll
       for (int c = 0; c < V; ++c) {

@@ -174,6 +174,25 @@ def test_one_sequence_is_not_anothers(T, dtype):
                 assert torch.equal(dx2[0, keep], dx[0, keep]) and torch.equal(dh2[rest], dh0[rest])
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("cell", ["glr", "glri"])
+@pytest.mark.parametrize("cu,T", [([0, 3, 90], 250), ([0, 5, 5, 300, 700], 1000), ([0, 0, 512], 2000), ([0, 0], 300), ([0, 0], 30)])
+def test_steps_behind_the_last_sequence(cu, T, cell, dtype):
+    """A pack of a fixed size that ends early: the sequences' results to the bit, zeros behind, whatever is there."""
+    c, n = _case(cell, 1, T, 40, dtype, cu), cu[-1]
+    for t in (c["x"], c["dH"]):
+        t[:, n:] = float("nan")
+    kw = dict(cell=cell, h0=c["h0"], cu_seqlens=c["cu"])
+    H, last = prn.gated_scan(c["x"], return_state=True, **kw)
+    dx, dh0 = prn.gated_scan_backward(c["dH"], c["x"], H, dstate=c["dlast"], **kw)
+    x, dH = (t[:, :n].contiguous() for t in (c["x"], c["dH"]))
+    want_H, want_last = prn.gated_scan(x, return_state=True, **kw)
+    want_dx, want_dh0 = prn.gated_scan_backward(dH, x, want_H, dstate=c["dlast"], **kw)
+    assert torch.equal(H[:, :n], want_H) and torch.equal(last, want_last)
+    assert torch.equal(dx[:, :n], want_dx) and torch.equal(dh0, want_dh0)
+    assert (H[:, n:] == 0).all() and (dx[:, n:] == 0).all()
+
+
 def test_a_nan_reaches_all_that_comes_after_it():
     c = _case("glr", 1, 4000, 64, torch.float32, h0=False)
     c["x"][0, 100, 1, 7] = float("nan")
@@ -367,6 +386,10 @@ def test_projection_gradients(cell):
 def test_refusals():
     x = torch.zeros(2, 4, 2, 8, device="cuda")
     H = torch.zeros(2, 4, 8, device="cuda")
+    pack = torch.zeros(1, 6, 2, 8, device="cuda")
+    for bad in ([0], [], [[0, 6]]):
+        with pytest.raises(ValueError):
+            prn.gated_scan(pack, cell="glr", cu_seqlens=torch.tensor(bad, dtype=torch.int32, device="cuda"))
     with pytest.raises(ValueError):
         prn.gated_scan(x, cell="gru")
     with pytest.raises(ValueError):
