@@ -127,6 +127,8 @@ def load_table(cell: str) -> dict:
     """The committed per-T table of a cell ({T: K}), for resolve_k."""
     with open(TABLE_PATH) as f:
         data = json.load(f)
+    if cell not in data["tables"]:
+        raise ValueError(f"no table of K for the cell {cell!r}")
     return {int(k): int(v) for k, v in data["tables"][cell].items()}
 
 

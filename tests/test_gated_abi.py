@@ -167,3 +167,9 @@ def test_python_refusals_without_a_gpu():
         prn.dropout(torch.zeros(8), 0.5, seed=1)
     with pytest.raises(ValueError):
         prn.dropout(torch.zeros(8), 0.5, seed=1, residual=torch.zeros(2, 4))
+
+
+def test_no_table_of_iterations_for_the_gated_cells():
+    from nonlinear_rnn_amd import kstar
+    with pytest.raises(ValueError, match="no table"):
+        kstar.load_table("glr")
