@@ -1,10 +1,11 @@
-"""Parallel Newton forward of diagonal GRU / LSTM recurrences on AMD MI355X.
+"""Parallel evaluation of recurrences (diagonal GRU / LSTM by Newton iterations, gated linear ones by one scan) on AMD MI355X.
 
 The compute lives in libprn.so (HIP, gfx950; C ABI in include/prn.h).
 ``binding`` marshals torch tensors into that ABI under the same names;
 ``api`` adds allocation, contiguity, K schedules, the residual gate and the
 agreement check; ``lm`` has the operators of a token model around the
-recurrence (embedding lookup, block-boundary norms, vocabulary loss).
+recurrence (embedding lookup, block-boundary norms, vocabulary loss, gated
+feed-forward product, dropout).
 """
 from .binding import (  # noqa: F401
     EXPORTS, PrnError, PrnUnsupportedError, lib, prn_backward_workspace_bytes, prn_input_proj, prn_last_error, prn_newton_backward,

@@ -504,14 +504,14 @@ size_t up(size_t x) { return (x + 255) / 256 * 256; }
 
 // Few rows are gated_few.hip's: as many of its workgroups of 64 rows and 16 outputs
 // as one round of the device takes (bf16) or two (fp32, which takes the tiles
-// longer).  us, few and the tiles: 65 x 512 x 1408 bf16 6.8 and
-// 10.0; 65 x 1024 x 4096 bf16 18 and 15; 256 x 512 x 1408 fp32 20 and 25.
+// longer).  us, few and the tiles: 64 x 512 x 1408 bf16 5.4 and 8.1, 128 tokens 7.4
+// and 7.9, 192 10.6 and 8.2; fp32 64 tokens 7.6 and 29, 256 20 and 26, 512 27 and 27.
 bool few_rows(const GatedFfnArgs& a) { return cdiv(a.N, 64) * cdiv(a.F, 16) <= (a.bf16 ? kCus : 2 * kCus); }
 
 // The 256 x 256 tiles where at least 128 of them keep the device busy, or the
-// quarter tiles.  us, quarter and large: 3000 x 512 x 1408 (132 tiles) out 17 and
-// 18, the gradients (two terms of dz) 80 and 63; 8192 x 512 x 1408 gradients 147
-// and 107.  fp32: from 192 on, and where a pass is long enough to hide the start
+// quarter tiles.  us, quarter and large: 3000 x 512 x 1408 (132 tiles) out 17.5
+// and 18.2, the gradients (with two terms of dz and one) 79 and 64; 8192 x 512 x
+// 1408 31 and 33, 164 and 109; 5003 x 517 x 1387 36 and 33, 130 and 87.  fp32: from 192 on, and where a pass is long enough to hide the start
 // of the next: 5003 x 517 x 1387 377 and 304, 16384 x 512 x 1024 663 and 582, but
 // 8192 x 512 x 512 (128 tiles) 173 and 203, 16384 x 256 x 512 191 and 212.
 bool big_tiles(const GatedFfnArgs& a) {
