@@ -131,3 +131,13 @@ def test_nothing_and_refusals():
         prn.dropout(x, 0.5, seed=torch.tensor([1, 2], dtype=torch.int32, device="cuda"))
     with pytest.raises(ValueError):
         prn.dropout(x, 0.5, seed=torch.tensor([1, 2], device="cuda"), offset=1)
+
+
+def test_offsets_past_32_bits():
+    """2^32 + 12345 elements: the last ones' numbers are those of their own index."""
+    n = 2 ** 32 + 12345
+    out = prn.dropout(torch.ones(n, dtype=torch.bfloat16, device="cuda"), 0.25, seed=11, offset=3)
+    for at in (2 ** 31, 2 ** 32, n - n % 8 - 64):
+        words = gated.philox(np.arange(at // 8, at // 8 + 8, dtype=np.int64), 3, 11)
+        keep = np.stack([words & 0xFFFF, words >> 16], -1).reshape(-1) >= round(0.25 * 65536)
+        assert np.array_equal(out[at:at + 64].float().cpu().numpy() != 0, keep)

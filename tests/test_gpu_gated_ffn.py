@@ -178,3 +178,28 @@ def test_refusals():
     with pytest.raises(ValueError):
         prn.gated_ffn_backward(torch.zeros(4, 2, device="cuda"), x, W)
     assert B.lib() is not None
+
+
+def test_offsets_past_32_bits():
+    """2^20 + 77 rows of 2100 outputs: the last rows are those of a call of their own size."""
+    N, d, F = 2 ** 20 + 77, 16, 2100
+    g = torch.Generator(device="cuda").manual_seed(1)
+    new = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()   # noqa: E731
+    x, W, dout = new(N, d), new(2 * F, d), new(N, F)
+    few = slice(N - 4096, N)   # of the same kind of tiles
+    out = prn.gated_ffn(x, W)
+    assert torch.equal(out[few], prn.gated_ffn(x[few].contiguous(), W))
+    del out
+    dx, _ = prn.gated_ffn_backward(dout, x, W, want_W=False)
+    want, _ = prn.gated_ffn_backward(dout[few].contiguous(), x[few].contiguous(), W, want_W=False)
+    # the sums may be cut in other slices: fp32 sums of 2 F products, and the result's rounding
+    bound = HALF[torch.bfloat16] * want.double().abs() * 2 + 8 * F * 2.0 ** -24 * _magnitude(x[few], W, dout[few])
+    assert ((dx[few].double() - want.double()).abs() <= bound).all()
+
+
+def _magnitude(x, W, dout):
+    """A bound of the sum of |dz| |W| for each entry of dx: |act'| <= 1.1, |act| <= |g| (silu)."""
+    z = x.double().abs() @ W.double().abs().t()
+    F = W.shape[0] // 2
+    dz = torch.cat([1.1 * dout.double().abs() * z[:, F:], dout.double().abs() * z[:, :F]], 1)
+    return dz @ W.double().abs()

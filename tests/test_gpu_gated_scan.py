@@ -414,3 +414,31 @@ def test_refusals():
         prn.sequential_forward(x, torch.zeros(2, 8, device="cuda"), cell="glr")
     with pytest.raises(B.PrnError, match="gated linear cells"):
         prn.newton_forward(x, torch.zeros(2, 8, device="cuda"), 2, cell="glr")
+
+
+@pytest.mark.parametrize("cu", [None, [0, 5, 4000001, 4300007]])
+def test_offsets_past_32_bits(cu):
+    """4300007 steps of 2 x 258 values: past the start, the last steps are those of a call that begins there."""
+    T, d, cut = 4300007, 258, 4200000
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(1, T, 2, d, generator=g, device="cuda", dtype=torch.bfloat16)
+    dH = torch.randn(1, T, d, generator=g, device="cuda", dtype=torch.bfloat16)
+    x[:, cut - 1, 0] = -200.0   # this step's state is its input: what came before has no part in what follows
+    if cu is not None:
+        cu = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    H, last = prn.gated_scan(x, cell="glr", cu_seqlens=cu, return_state=True)
+    dx, _ = prn.gated_scan_backward(dH, x, H, cell="glr", cu_seqlens=cu)
+    end = slice(cut - 1, T)
+    y, e = x[:, end].contiguous(), dH[:, end].contiguous()
+    want, want_last = prn.gated_scan(y, cell="glr", return_state=True)
+    want_dx, _ = prn.gated_scan_backward(e, y, want, cell="glr")
+    # the chunks begin elsewhere: fp32 maps in another order, a bf16 value next to the other's
+    near = lambda got, ref: (got.double() - ref.double()).abs() - 2.0 ** -7 * ref.double().abs()   # noqa: E731
+    got_dx, want_dx = dx[:, end][:, 1:], want_dx[:, 1:]
+    for got, ref in ((H[:, end], want), (last[-1:], want_last), (got_dx[:, :, 1], want_dx[:, :, 1])):
+        assert (near(got, ref) <= 2.0 ** -12).all()
+    # dx_f = lam (h - v) f (1 - f), h off by half a step of the state that its chunk starts from, in either call
+    off = torch.sigmoid(-y[:, 1:, 0].double())
+    lam = want_dx[:, :, 1].double().abs() / off
+    bound = 2 * HALF[torch.bfloat16] * want.double().abs().max() * lam * off * (1 - off) * 1.01 + 2.0 ** -12
+    assert (near(got_dx[:, :, 0], want_dx[:, :, 0]) <= bound).all()
