@@ -475,21 +475,52 @@ __global__ void __launch_bounds__(Tl::NTHR, 2) k_ffn_grads(FfnProduct x, FfnProd
 }
 
 // out = the sum over z, in order, of P[z], rounded once, of either product with
-// more than one slice (nx, nw values, or 0); dW's rows as in ffn_product
+// more than one slice (nx, nw values, or 0), four values a thread; dW's rows as in
+// ffn_product.  Blocks [0, bx) dx.
 template <bool FP32>
-__global__ void __launch_bounds__(256) k_ffn_join(FfnProduct x, int64_t nx, FfnProduct w, int64_t nw, int64_t C, int64_t F) {
-  int64_t i = block_in_rows() * 256 + threadIdx.x;
-  if (i >= nx + nw) return;
-  const bool is_w = i >= nx;
-  if (is_w) i -= nx;
-  const int64_t n = is_w ? nw : nx, r = i / C, c = i - r * C, f = r / 64 * 32 + r % 32;
-  if (is_w && f >= F) return;
-  const float* const P = is_w ? w.P : x.P;
-  const int S = static_cast<int>(is_w ? w.slices : x.slices);
-  float sum = 0.0f;
-  for (int z = 0; z < S; ++z) sum += P[z * n + i];
+__global__ void __launch_bounds__(256) k_ffn_join(FfnProduct x, int64_t nx, int64_t bx, FfnProduct w, int64_t nw, int64_t C,
+                                                  int64_t F) {
   using St = Storage<FP32 ? kF32 : kBF16>;
-  static_cast<typename St::T*>(is_w ? w.out : x.out)[(is_w ? ((r >> 5) & 1) * F + f : r) * C + c] = St::pack(sum);
+  using T = typename St::T;
+  const int64_t b = block_in_rows();
+  const bool is_w = b >= bx;
+  const int64_t n = is_w ? nw : nx, i = 4 * ((is_w ? b - bx : b) * 256 + threadIdx.x);
+  if (i >= n) return;
+  const float* const P = (is_w ? w.P : x.P) + i;
+  T* const out = static_cast<T*>(is_w ? w.out : x.out);
+  const int S = static_cast<int>(is_w ? w.slices : x.slices), left = static_cast<int>(imin(n - i, 4));
+  float sum[4] = {};
+  for (int z = 0; z < S; ++z) {
+    float v[4];
+    if (left == 4) {
+      __builtin_memcpy(v, P + z * n, 16);   // aligned or not
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = e < left ? P[z * n + e] : 0.0f;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum[e] += v[e];
+  }
+  T o[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) o[e] = St::pack(sum[e]);
+  if (!is_w) {
+    if (left == 4) {
+      __builtin_memcpy(__builtin_assume_aligned(out + i, sizeof(o)), o, sizeof(o));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (e < left) out[i + e] = o[e];
+    }
+    return;
+  }
+  int64_t r = i < (int64_t(1) << 32) ? static_cast<uint32_t>(i) / static_cast<uint32_t>(C) : i / C, c = i - r * C;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int64_t f = r / 64 * 32 + r % 32;
+    if (e < left && f < F) out[(((r >> 5) & 1) * F + f) * C + c] = o[e];
+    if (++c == C) c = 0, ++r;
+  }
 }
 
 template <class T>
@@ -728,11 +759,12 @@ void launch_gated_ffn_backward(const GatedFfnArgs& a, const void* x, const void*
   }
   const int64_t nx = dx && p.x.s > 1 ? a.N * a.d : 0, nw = dW && p.w.s > 1 ? Zp * a.d : 0;
   if (nx + nw == 0) return;
-  const dim3 grid = rows_of_blocks(cdiv(nx + nw, 256));
+  const int64_t bx = cdiv(nx, 1024);
+  const dim3 grid = rows_of_blocks(bx + cdiv(nw, 1024));
   if (a.bf16)
-    k_ffn_join<false><<<grid, 256, 0, a.stream>>>(to_x, nx, to_w, nw, a.d, a.F);
+    k_ffn_join<false><<<grid, 256, 0, a.stream>>>(to_x, nx, bx, to_w, nw, a.d, a.F);
   else
-    k_ffn_join<true><<<grid, 256, 0, a.stream>>>(to_x, nx, to_w, nw, a.d, a.F);
+    k_ffn_join<true><<<grid, 256, 0, a.stream>>>(to_x, nx, bx, to_w, nw, a.d, a.F);
 }
 
 }  // namespace prn
