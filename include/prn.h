@@ -535,7 +535,7 @@ size_t prn_gated_scan_workspace_bytes(const prn_params* params);
  *   dstate_last  (rows, d_h) storage dtype, or NULL for zero
  *   dxproj_out   (B, T, G, d_h) storage dtype
  *   dh0_out      (rows, d_h) storage dtype, or NULL
- * The states are formed again in fp32, from H at every 64th or 128th step.  params as for
+ * The states are formed again in fp32, from H at every 64th to 160th step.  params as for
  * the forward, its workspace prn_gated_scan_backward_workspace_bytes(params). */
 prn_status prn_gated_scan_backward(const void* xproj, const prn_params* params, const void* h0, const int32_t* cu_seqlens,
                                    const void* H, const void* dH, const void* dstate_last, void* dxproj_out,

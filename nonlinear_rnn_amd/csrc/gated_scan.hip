@@ -680,7 +680,7 @@ size_t up(size_t x) { return (x + 255) / 256 * 256; }
 // 4096 x 512 bf16, 284 and 400 for 2 x 131072 x 256 fp32, where look-back takes 29
 // and 46, 174 and 272.  Tiles of 16 channels, so that every one of 8 x 512 has a
 // chain that fills the device: 40 and 73.)
-constexpr int64_t kEnough = 256, kShort = 256;
+constexpr int64_t kEnough = 256, kShort = 256, kCus = 256;
 // Steps of a wave and waves of a workgroup.  A longer chunk means fewer
 // look-backs in a row, as long as the registers allow a workgroup of it, or two
 // of the smaller ones, on a CU.  us, glr, 2 x 131072 x 256 fp32 and 8 x 4096 x 512
@@ -700,6 +700,21 @@ constexpr Shape shape_of(bool back, bool pass) {
   if (V == 1) return G == 2 ? Shape{16, 8} : Shape{8, 16};
   return G == 2 ? Shape{8, 16} : Shape{8, 8};   // (glri of two channels a lane: more than 128 registers)
 }
+// A longer one for rows of one channel a lane, of as many waves: such a workgroup
+// has a CU to itself, so it is taken where it makes fewer steps of rounds of the
+// device.  us, 20011 x 250 fp32 glri in 37 sequences (four chains): forward 20 steps, one round,
+// 26, 16 steps, two, 35; backward 10 steps, two rounds, 43, 8 steps, three, 48.
+// (24 steps 35; 12 steps backward 57.)
+template <int G, int V>
+constexpr Shape longer_of(bool back) {
+  const Shape s = shape_of<G, V>(back, true);
+  if (V > 1) return s;
+  return back ? G == 3 ? Shape{10, s.waves} : s : Shape{20, s.waves};
+}
+Shape longer_of(int G, int V, bool back) {
+  if (V > 1) return G == 2 ? longer_of<2, 2>(back) : longer_of<3, 2>(back);
+  return G == 2 ? longer_of<2, 1>(back) : longer_of<3, 1>(back);
+}
 Shape shape_of(int G, int V, bool back, bool pass) {
   if (G == 2) return V == 1 ? shape_of<2, 1>(back, pass) : shape_of<2, 2>(back, pass);
   return V == 1 ? shape_of<3, 1>(back, pass) : shape_of<3, 2>(back, pass);
@@ -707,7 +722,7 @@ Shape shape_of(int G, int V, bool back, bool pass) {
 
 struct Plan {
   int V;
-  bool pass;
+  bool pass, longer;
   int64_t chains, chunks;
   size_t words, maps_off, states_off, total;
 };
@@ -717,7 +732,14 @@ Plan plan_of(const GatedScanArgs& a, bool back) {
   p.V = a.bf16 && a.d % 2 == 0 ? 2 : 1;   // 4 bytes a lane where the rows allow it
   p.chains = a.B * cdiv(a.d, 64 * p.V);
   p.pass = p.chains < kEnough && a.T > kShort;
-  p.chunks = cdiv(a.T, shape_of(a.G, p.V, back, p.pass).chunk());
+  Shape s = shape_of(a.G, p.V, back, p.pass);
+  if (p.pass) {
+    const Shape l = longer_of(a.G, p.V, back);
+    auto steps = [&](const Shape& k) { return cdiv(p.chains * cdiv(a.T, k.chunk()), kCus) * k.steps; };
+    p.longer = steps(l) < steps(s);
+    if (p.longer) s = l;
+  }
+  p.chunks = cdiv(a.T, s.chunk());
   if (p.pass) {
     const size_t n = size_t(p.chains) * p.chunks, line = size_t(p.V) * 64 * sizeof(float);
     p.words = 2 + n;   // ticket, error, statuses
@@ -786,8 +808,11 @@ void launch_gated_scan(const GatedScanArgs& a) {
     constexpr int DT = decltype(dt)::value, G = decltype(g)::value, V = decltype(v)::value;
     constexpr bool RAGGED = decltype(ragged)::value;
     const Tensors<DT> t = tensors_of<DT>(a, p);
-    constexpr Shape pass = shape_of<G, V>(false, true), walk = shape_of<G, V>(false, false);
-    if (p.pass)
+    constexpr Shape pass = shape_of<G, V>(false, true), longer = longer_of<G, V>(false), walk = shape_of<G, V>(false, false);
+    if (longer.steps > pass.steps && p.longer)
+      k_scan_pass<DT, G, V, longer.steps, longer.waves, RAGGED>
+          <<<rows_of_blocks(p.chains * p.chunks), 64 * longer.waves, 0, a.stream>>>(t, rec, a.spin_limit, p.chains < 64);
+    else if (p.pass)
       k_scan_pass<DT, G, V, pass.steps, pass.waves, RAGGED><<<rows_of_blocks(p.chains * p.chunks), 64 * pass.waves, 0, a.stream>>>(
           t, rec, a.spin_limit, p.chains < 64);
     else
@@ -803,8 +828,11 @@ void launch_gated_scan_backward(const GatedScanArgs& a) {
     constexpr int DT = decltype(dt)::value, G = decltype(g)::value, V = decltype(v)::value;
     constexpr bool RAGGED = decltype(ragged)::value;
     const Tensors<DT> t = tensors_of<DT>(a, p);
-    constexpr Shape pass = shape_of<G, V>(true, true), walk = shape_of<G, V>(true, false);
-    if (p.pass)
+    constexpr Shape pass = shape_of<G, V>(true, true), longer = longer_of<G, V>(true), walk = shape_of<G, V>(true, false);
+    if (longer.steps > pass.steps && p.longer)
+      k_scan_pass_back<DT, G, V, longer.steps, longer.waves, RAGGED>
+          <<<rows_of_blocks(p.chains * p.chunks), 64 * longer.waves, 0, a.stream>>>(t, rec, a.spin_limit, p.chains < 64);
+    else if (p.pass)
       k_scan_pass_back<DT, G, V, pass.steps, pass.waves, RAGGED><<<rows_of_blocks(p.chains * p.chunks), 64 * pass.waves, 0, a.stream>>>(
           t, rec, a.spin_limit, p.chains < 64);
     else

@@ -102,6 +102,13 @@ def test_on_either_side_of_a_limit(cell, Bn, T, d, dtype):
     _check(cell, _case(cell, Bn, T, d, dtype, h0=Bn % 2 == 0, seed=T), dtype)
 
 
+@pytest.mark.parametrize("cu", [None, [0, 0, 321, 9000, 17003]])
+@pytest.mark.parametrize("cell,d,dtype", [("glr", 250, torch.float32), ("glri", 250, torch.float32), ("glri", 251, torch.bfloat16)])
+def test_chunks_by_rounds(cell, d, dtype, cu):
+    """More chunks than a round of the device has, and longer ones in one round less."""
+    _check(cell, _case(cell, 1, 17003, d, dtype, cu), dtype)
+
+
 def test_a_long_chain():
     """Hundreds of chunks of one chain: the look-back over more than 64 of them."""
     for cell, dtype in (("glr", torch.float32), ("glri", torch.bfloat16)):
