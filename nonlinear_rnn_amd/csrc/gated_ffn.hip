@@ -188,14 +188,14 @@ __device__ __forceinline__ float second_term(float v) {
 
 // ---------------------------------------------------------------- sums ----
 
-// The tiles of g and u, 128 outputs x 256 tokens each (quarter tiles: 64 x 128);
-// TERMS = 0: out (N x F), bf16; else dz in TERMS bf16 terms (3: of fp32 data,
-// W and X in terms too, w_low and x_low apart), `low` elements apart (N x 2 Fp in pairs of
-// blocks, rows ldo apart, zeros past F).  W has Fw gate
-// rows, then Fw up rows.  A group of 8 tiles of outputs by all tokens, walked
-// down the outputs first, is a share of an XCD, whose L2 then holds the group's
-// W.  (32768 x 512 x 2048: 152 us, dz 186; two workgroups a CU of 256 x 128, one's
-// products under the other's epilogue: 158 and 197.)
+// The tiles of g and u, 128 outputs x 256 tokens each (quarter tiles: 64 x 128).
+// TERMS = 0: out (N x F), bf16.  Else dz in TERMS bf16 terms, `low` elements apart
+// (N x 2 Fp in pairs of blocks, rows ldo apart, zeros past F); with three the data
+// is fp32, W and X in terms w_low and x_low apart.  W has Fw gate rows, then Fw up
+// rows.  A group of 8 tiles of outputs by all tokens, walked down the outputs
+// first, is a share of an XCD, whose L2 then holds the group's W.  (32768 x 512 x
+// 2048: 152 us, dz 186; two workgroups a CU of 256 x 128, one's products under the
+// other's epilogue: 158 and 197.)
 template <class Tl, int TERMS>
 __global__ void __launch_bounds__(Tl::NTHR, 2) k_ffn_sums(MmOperand W, int64_t w_low, MmOperand X, int64_t x_low, int64_t N,
                                                           int64_t F, int64_t Fw, int64_t K, bool silu,
