@@ -14,7 +14,7 @@ struct Gate {
 };
 __device__ __forceinline__ Gate gate_of(float x) {
   const float e = ex2(-kLog2e * x), r = rcp(1.0f + e);
-  const float off = e < __builtin_inff() ? e * r : 1.0f;
+  const float off = e == __builtin_inff() ? 1.0f : e * r;   // of NaN: NaN, both
   return {e <= 1.0f ? 1.0f - off : r, off};
 }
 

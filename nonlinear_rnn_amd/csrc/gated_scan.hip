@@ -289,8 +289,9 @@ struct Fore {
       for (int c = 0; c < V; ++c) {
         const Gate f = gate_of(q[j][0].at(c));
         s[j][c] = {f.on, (G == 2 ? f.off : gate_of(q[j][1].at(c)).on) * q[j][G - 1].at(c)};
-        if (here) {
-          if (t.h0) s[j][c].b = fmaf(f.on, Storage<DT>::load(t.h0 + static_cast<int64_t>(cut.seg[j]) * t.d + at.tile + at.off + c), s[j][c].b);
+        if (here) {   // without h0 from zero, which a NaN gate does not keep either
+          const float h0 = t.h0 ? Storage<DT>::load(t.h0 + static_cast<int64_t>(cut.seg[j]) * t.d + at.tile + at.off + c) : 0.0f;
+          s[j][c].b = fmaf(f.on, h0, s[j][c].b);
           s[j][c].a = kCut;
         }
         if (j == 0 && ALL)
@@ -491,7 +492,7 @@ struct Back {
         if (t.dlast && (RAGGED ? tail(j) : s0 + j == t.T_ - 1)) g[j][c] += one(t.dlast, j, c, t, at);
         Map m = {f[j][c].on, i[j][c].on * x[j][G - 1].at(c)};
         if (head(j)) {
-          if (t.h0) m.b = fmaf(m.a, one(t.h0, j, c, t, at), m.b);
+          m.b = fmaf(m.a, t.h0 ? one(t.h0, j, c, t, at) : 0.0f, m.b);
           m.a = kCut;
         }
         fore[c] = ALL && j == 0 ? m : then<RAGGED>(fore[c], m);

@@ -449,3 +449,33 @@ def test_offsets_past_32_bits(cu):
     lam = want_dx[:, :, 1].double().abs() / off
     bound = 2 * HALF[torch.bfloat16] * want.double().abs().max() * lam * off * (1 - off) * 1.01 + 2.0 ** -12
     assert (near(got_dx[:, :, 0], want_dx[:, :, 0]) <= bound).all()
+
+
+# ------------------------------------------------------------------ gates at their ends ---
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("cell", ["glr", "glri"])
+@pytest.mark.parametrize("h0", [False, True])
+@pytest.mark.parametrize("cu,T", [(None, 1), (None, 40), (None, 3000), ([0, 7, 7, 40], 40), ([0, 1, 1000, 3000], 3000)])
+def test_a_gate_that_is_nan(cu, T, h0, cell, dtype):
+    """A NaN forget gate at a sequence's first step or inside one: NaN where the definition has it, in states, final
+    states and gradients, whatever the layout, and every other value to the bit."""
+    for at in sorted({0, T // 2, T - 1, *(cu[:-1] if cu else ())}):
+        c = _case(cell, 1, T, 40, dtype, cu, h0=h0, seed=at)
+        kw = dict(cell=cell, h0=c["h0"], cu_seqlens=c["cu"])
+        H, last = prn.gated_scan(c["x"], return_state=True, **kw)
+        dx, dh0 = prn.gated_scan_backward(c["dH"], c["x"], H, dstate=c["dlast"], **kw)
+        x = c["x"].clone()
+        x[0, at, 0, 11] = float("nan")
+        H2, last2 = prn.gated_scan(x, return_state=True, **kw)
+        dx2, dh2 = prn.gated_scan_backward(c["dH"], x, H2, dstate=c["dlast"], **kw)
+        want_H, want_last = gated.gated_scan(cell, _np(x), _np(c["h0"]), cu)
+        want_dx, want_dh0 = gated.gated_scan_backward(cell, _np(x), _np(c["dH"]), _np(c["h0"]), cu, _np(c["dlast"]))
+        assert np.isnan(want_H[0, at, 11])
+        for name, got, clean, want in (("H", H2, H, want_H), ("last", last2, last, want_last), ("dxproj", dx2, dx, want_dx),
+                                       ("dh0", dh2, dh0, want_dh0)):
+            if got is None:
+                continue
+            nan = torch.from_numpy(np.isnan(want)).cuda()
+            assert torch.equal(torch.isnan(got), nan), (name, at)
+            assert torch.equal(got[~nan], clean[~nan]), (name, at)
