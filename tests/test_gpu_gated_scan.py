@@ -479,3 +479,49 @@ def test_a_gate_that_is_nan(cu, T, h0, cell, dtype):
             nan = torch.from_numpy(np.isnan(want)).cuda()
             assert torch.equal(torch.isnan(got), nan), (name, at)
             assert torch.equal(got[~nan], clean[~nan]), (name, at)
+
+
+def _nearly_shut(dtype):
+    """Logits of gates from 1.6e-38 (a normal number) down to 0, through those whose value is no normal fp32 number,
+    and which are those: from log(2^-126) = -87.3365 on."""
+    x = torch.tensor([-87.0, -87.25, -87.375, -87.5, -87.75, -88.0, -88.25, -88.5, -88.6875, -88.71875, -88.75, -89.0, -100.0, -104.0])
+    x = x.to(dtype).cuda()
+    return x, x < -87.3366
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T", [1, 20, 3000])
+def test_gates_too_small_for_a_normal_number(T, dtype):
+    """Where s(x_f) is below fp32's normal numbers 1 - s(x_f) is 1: the state is the input and the input's gradient
+    the state's, exactly (what is kept of a state of order one is below 2^-125, far below half a step).  The logits
+    before have 1 - s from a power and a quotient, within the oracle's bounds."""
+    xf, shut = _nearly_shut(dtype)
+    g = torch.Generator().manual_seed(T)
+    v = torch.randn(1, T, len(xf), generator=g).to(dtype).cuda()
+    x = torch.stack([xf.expand_as(v), v], 2).contiguous()
+    h0 = torch.ones(1, 1, len(xf), dtype=dtype, device="cuda")
+    dH = torch.randn(1, T, len(xf), generator=g).to(dtype).cuda()
+    pack = torch.tensor([0, T // 2, T], dtype=torch.int32, device="cuda")
+    H = prn.gated_scan(x, cell="glr", h0=h0)
+    for got in (H, prn.gated_scan(x, cell="glr", cu_seqlens=pack)):
+        assert torch.equal(got[..., shut], v[..., shut]), xf[(got != v).any(1)[0]]
+    dx, dh0 = prn.gated_scan_backward(dH, x, H, cell="glr", h0=h0)
+    assert torch.equal(dx[:, :, 1][..., shut], dH[..., shut])
+    want_dx, want_dh0 = gated.gated_scan_backward("glr", _np(x), _np(dH), _np(h0))
+    bounds = gated.gated_scan_bounds("glr", _np(x), _np(h0), None, _np(dH), start=HALF[dtype] / U24)
+    for name, got, want in (("H", H, gated.gated_scan("glr", _np(x), _np(h0))[0]), ("dxproj", dx, want_dx), ("dh0", dh0, want_dh0)):
+        _close(name, got, want, bounds[name], dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_a_step_whose_gate_is_too_small_for_a_normal_number(dtype):
+    xf, shut = _nearly_shut(dtype)
+    v = torch.linspace(-2.0, 2.0, len(xf)).to(dtype).cuda()
+    W = torch.cat([xf, v])[:, None].contiguous()
+    x = torch.ones(3, 1, dtype=dtype, device="cuda")
+    out = torch.empty(3, 1, len(xf), dtype=dtype, device="cuda")
+    B.prn_decode_step(x, W, None, None, out, cell="glr", state_in=torch.ones_like(out))
+    want = v.expand_as(out)
+    assert torch.equal(out[..., shut], want[..., shut])
+    z, one = torch.stack([xf, v]).expand(3, 1, 2, len(xf)), np.ones((3, 1, len(xf)))
+    _close("state", out, gated.gated_scan("glr", _np(z), one)[1], gated.gated_scan_bounds("glr", _np(z), one)["last"], dtype)
