@@ -569,8 +569,8 @@ prn_status prn_gated_ffn(const void* x, const void* W, const prn_gated_ffn_param
 /* Its gradients from dout (N, F): dz = [dout u act'(g) | dout act(g)], with g and u
  * formed again; dx_out (N, d) = dz W, dW_out (2 F, d) = dz^T x, each optional.
  * bf16: dz, in between, is off by 2^-8 of itself, below 128 tiles of 256 tokens x
- * 128 outputs by 2^-16.  The workspace holds dz.  Tensors must be
- * 16-byte aligned. */
+ * 128 outputs by 2^-16.  The workspace holds dz.  min(N, 256) (F + 64) is at most
+ * 2^30.  Tensors must be 16-byte aligned. */
 prn_status prn_gated_ffn_backward(const void* x, const void* W, const void* dout, const prn_gated_ffn_params* params,
                                   void* dx_out, void* dW_out);
 size_t prn_gated_ffn_workspace_bytes(const prn_gated_ffn_params* params);

@@ -16,6 +16,7 @@ struct GatedFfnArgs {
 
 // do the launches fit their grids and offsets?
 bool gated_ffn_fits(const GatedFfnArgs& a);
+bool gated_ffn_backward_fits(const GatedFfnArgs& a);   // those of the gradients alone
 size_t gated_ffn_workspace(const GatedFfnArgs& a);
 void launch_gated_ffn(const GatedFfnArgs& a, const void* x, const void* W, void* out);
 // dx / dW may be null

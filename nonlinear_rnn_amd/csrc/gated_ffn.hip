@@ -711,6 +711,11 @@ bool gated_ffn_fits(const GatedFfnArgs& a) {
   return 2 * (F + 256) * (d + 64) < 2147483648.0 && (N / 256 + 1) * (F / 128 + 1) < most && (N / 256 + 1) * (d / 128 + 1) < most;
 }
 
+bool gated_ffn_backward_fits(const GatedFfnArgs& a) {
+  // byte offsets of 32 bits into the rows of dz, fewer than 4 (F + 64) bytes, that a tile of dx reads
+  return std::min(a.N, kTileRows) * (a.F + 64) <= int64_t(1) << 30;
+}
+
 size_t gated_ffn_workspace(const GatedFfnArgs& a) { return a.N == 0 || few_rows(a) ? 0 : plan_of(a, false).total; }
 
 void launch_gated_ffn(const GatedFfnArgs& a, const void* x, const void* W, void* out) {

@@ -134,6 +134,13 @@ prn_status ffn_args(const prn_gated_ffn_params* p, prn::GatedFfnArgs* a) {
                 (long long)p->N, (long long)p->d, (long long)p->F);
   return PRN_OK;
 }
+prn_status ffn_backward_args(const prn_gated_ffn_params* p, prn::GatedFfnArgs* a) {
+  if (prn_status s = ffn_args(p, a); s != PRN_OK) return s;
+  if (!prn::gated_ffn_backward_fits(*a))
+    return fail(PRN_ERR_UNSUPPORTED, "gradients take min(N, 256) (F + 64) up to 2^30; got N=%lld F=%lld", (long long)p->N,
+                (long long)p->F);
+  return PRN_OK;
+}
 
 }  // namespace
 
@@ -332,14 +339,14 @@ prn_status prn_gated_ffn(const void* x, const void* W, const prn_gated_ffn_param
 size_t prn_gated_ffn_backward_workspace_bytes(const prn_gated_ffn_params* p) {
   g_err.clear();
   prn::GatedFfnArgs a;
-  if (ffn_args(p, &a) != PRN_OK) return 0;
+  if (ffn_backward_args(p, &a) != PRN_OK) return 0;
   return prn::gated_ffn_backward_workspace(a);
 }
 
 prn_status prn_gated_ffn_backward(const void* x, const void* W, const void* dout, const prn_gated_ffn_params* p, void* dx,
                                   void* dW) {
   prn::GatedFfnArgs a;
-  if (prn_status s = ffn_args(p, &a); s != PRN_OK) return s;
+  if (prn_status s = ffn_backward_args(p, &a); s != PRN_OK) return s;
   if (a.N && (!x || !W || !dout)) return fail(PRN_ERR_INVALID_ARG, "x, W or dout is NULL");
   if (misaligned(x, 16) || misaligned(W, 16) || misaligned(dout, 16) || misaligned(dx, 16) || misaligned(dW, 16))
     return fail(PRN_ERR_INVALID_ARG, "x, W, dout, dx_out and dW_out must be 16-byte aligned");

@@ -173,3 +173,24 @@ def test_no_table_of_iterations_for_the_gated_cells():
     from nonlinear_rnn_amd import kstar
     with pytest.raises(ValueError, match="no table"):
         kstar.load_table("glr")
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("N,d,F", [(256, 64, 5000000), (256, 128, 4300000), (128, 32, 9000000), (4096, 1, 1 << 22),
+                                   (256, 64, (1 << 22) - 63)])
+def test_ffn_gradients_of_rows_past_32_bits(N, d, F, dtype):
+    """A tile of dx reads up to 256 rows of dz, of 4 (F + 64) bytes each at most, by offsets of 32 bits: past them
+    the gradients are refused, the product itself is not."""
+    L, p = B.lib(), _p(B.prn_gated_ffn_params, {**FFN, **BIG}, N=N, d=d, F=F, dtype=dtype)
+    assert L.prn_gated_ffn_backward(FAKE, FAKE, FAKE, p, FAKE, FAKE) == UNSUP and "2^30" in B.prn_last_error()
+    with pytest.raises(B.PrnError, match="2\\^30"):
+        B.prn_gated_ffn_backward_workspace_bytes((torch.float32, torch.bfloat16)[dtype], N, d, F)
+    L.prn_gated_ffn_workspace_bytes(p)
+    assert B.prn_last_error() == ""
+
+
+@pytest.mark.parametrize("N,d,F", [(256, 64, (1 << 22) - 64), (100, 32, 9000000), (1, 32, 9000000)])
+def test_ffn_gradients_of_rows_within_32_bits(N, d, F):
+    assert min(N, 256) * 2 * (2 * ((F + 31) // 32 * 32) + 64) < 1 << 32   # rows of both halves, in blocks of 32, and 64 between
+    for dtype in (torch.float32, torch.bfloat16):
+        assert B.prn_gated_ffn_backward_workspace_bytes(dtype, N, d, F) > N * 4 * F

@@ -203,3 +203,16 @@ def _magnitude(x, W, dout):
     F = W.shape[0] // 2
     dz = torch.cat([1.1 * dout.double().abs() * z[:, F:], dout.double().abs() * z[:, :F]], 1)
     return dz @ W.double().abs()
+
+
+@pytest.mark.parametrize("N,F,dtype", [(256, 2 ** 22 - 64, torch.bfloat16), (128, 2 ** 23 - 64, torch.float32)])
+def test_gradients_of_the_longest_rows(N, F, dtype):
+    """The rows of a tile of dx reach as far as its offsets do: the tokens in the other order give the same bits."""
+    d = 8
+    g = torch.Generator(device="cuda").manual_seed(2)
+    new = lambda *s: torch.randn(*s, generator=g, device="cuda", dtype=dtype)   # noqa: E731
+    x, W, dout = new(N, d), new(2 * F, d) / F ** 0.5, new(N, F)
+    dx, _ = prn.gated_ffn_backward(dout, x, W, want_W=False)
+    other, _ = prn.gated_ffn_backward(dout.flip(0), x.flip(0), W, want_W=False)
+    assert torch.isfinite(dx).all() and torch.equal(dx, other.flip(0))
+    assert len(torch.unique(dx, dim=0)) == N
