@@ -550,10 +550,10 @@ size_t prn_gated_scan_backward_workspace_bytes(const prn_params* params);
 typedef struct {
   int32_t dtype;           /* PRN_F32 | PRN_BF16: every tensor                          */
   int32_t act;             /* PRN_ACT_SILU | PRN_ACT_SIGMOID                            */
-  int64_t N;               /* rows, below 2^31                                          */
+  int64_t N;               /* rows; (N + 256) (F + 128) and (N + 256) (d + 128) below
+                              2^37, so N is below 2^30                                  */
   int64_t d;               /* input channels                                            */
-  int64_t F;               /* output channels; 2 (F + 256) (d + 64) below 2^31, N F and
-                              N d below 2^36                                            */
+  int64_t F;               /* output channels; 2 (F + 256) (d + 64) below 2^31          */
   void* workspace;         /* 256-byte aligned scratch                                  */
   size_t workspace_bytes;  /* >= prn_gated_ffn_workspace_bytes(params), backward:
                               >= prn_gated_ffn_backward_workspace_bytes(params)         */

@@ -706,9 +706,9 @@ void sums(const GatedFfnArgs& a, const Plan& p, const Operands& o, const void* d
 }  // namespace
 
 bool gated_ffn_fits(const GatedFfnArgs& a) {
-  const double N = double(a.N), d = double(a.d), F = double(a.F), most = double(1 << 22);
-  // byte offsets into W of 32 bits; launches below 2^32 threads, also with tiles of 128 x 128
-  return 2 * (F + 256) * (d + 64) < 2147483648.0 && (N / 256 + 1) * (F / 128 + 1) < most && (N / 256 + 1) * (d / 128 + 1) < most;
+  const double N = double(a.N) + 256, d = double(a.d), F = double(a.F), most = double(int64_t(1) << 37);
+  // byte offsets into W of 32 bits; launches below 2^32 threads: 2^22 tiles of 256 x 128, also where they are of 128 x 128
+  return 2 * (F + 256) * (d + 64) < 2147483648.0 && N * (F + 128) < most && N * (d + 128) < most;
 }
 
 bool gated_ffn_backward_fits(const GatedFfnArgs& a) {

@@ -129,8 +129,9 @@ prn_status ffn_args(const prn_gated_ffn_params* p, prn::GatedFfnArgs* a) {
     return fail(PRN_ERR_INVALID_ARG, "bad sizes N=%lld d=%lld F=%lld", (long long)p->N, (long long)p->d, (long long)p->F);
   *a = {p->dtype == PRN_BF16, p->act == PRN_ACT_SILU, p->N, p->d, p->F, static_cast<uint8_t*>(p->workspace),
         static_cast<hipStream_t>(p->stream)};
-  if (p->N > kMaxRows || !prn::gated_ffn_fits(*a))
-    return fail(PRN_ERR_UNSUPPORTED, "N below 2^31, 2 (F + 256) (d + 64) below 2^31, N F and N d below 2^36; got N=%lld d=%lld F=%lld",
+  if (!prn::gated_ffn_fits(*a))
+    return fail(PRN_ERR_UNSUPPORTED,
+                "2 (F + 256) (d + 64) below 2^31, (N + 256) (F + 128) and (N + 256) (d + 128) below 2^37; got N=%lld d=%lld F=%lld",
                 (long long)p->N, (long long)p->d, (long long)p->F);
   return PRN_OK;
 }

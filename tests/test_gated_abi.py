@@ -194,3 +194,19 @@ def test_ffn_gradients_of_rows_within_32_bits(N, d, F):
     assert min(N, 256) * 2 * (2 * ((F + 31) // 32 * 32) + 64) < 1 << 32   # rows of both halves, in blocks of 32, and 64 between
     for dtype in (torch.float32, torch.bfloat16):
         assert B.prn_gated_ffn_backward_workspace_bytes(dtype, N, d, F) > N * 4 * F
+
+
+@pytest.mark.parametrize("N,d,F", [(1 << 30, 32, 32), ((1 << 31) - 1, 1, 1), (1 << 26, 32, 1 << 11), (1 << 26, 1 << 11, 32),
+                                   ((1 << 37) // 256 - 256, 128, 16), ((1 << 37) // 129 - 255, 1, 1)])
+def test_ffn_refuses_the_rows_that_its_limits_name(N, d, F):
+    """Both ways refuse (N + 256) (F + 128) or (N + 256) (d + 128) of 2^37 on, and say so; the size before is taken."""
+    L = B.lib()
+    widest = max(d, F) + 128
+    assert (N + 256) * widest >= 1 << 37
+    p = _p(B.prn_gated_ffn_params, {**FFN, **BIG}, N=N, d=d, F=F)
+    assert L.prn_gated_ffn(FAKE, FAKE, p, FAKE) == UNSUP and "2^37" in B.prn_last_error()
+    assert L.prn_gated_ffn_backward(FAKE, FAKE, FAKE, p, FAKE, FAKE) == UNSUP and "2^37" in B.prn_last_error()
+    most = ((1 << 37) - 1) // widest - 256
+    for dtype in (torch.float32, torch.bfloat16):
+        B.prn_gated_ffn_workspace_bytes(dtype, most, d, F)
+        assert B.prn_gated_ffn_backward_workspace_bytes(dtype, most, d, F) > most * 4 * F
