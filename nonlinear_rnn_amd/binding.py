@@ -506,7 +506,7 @@ def prn_newton_backward(xproj, a, states, dH, dxproj_out, da_out, *, cell: str, 
 
 
 def prn_decode_step(x, W, bias, a, state_out, *, cell: str, state_in=None, h_out=None, stream=None) -> None:
-    """One T = 1 step for B slots: x (B, d_in), W (G*d_h, d_in), bias (G*d_h) fp32 or None,
+    """One T = 1 step for B slots: x (B, d_in), W (G*d_h, d_in), bias (G*d_h) or (G, d_h) fp32 or None,
     state_in / state_out (B, S, d_h) (distinct buffers), h_out (B, d_h) or None.
     The gated linear cells have no a (None)."""
     dev, code = _lead(x, "x", 2)
@@ -518,6 +518,8 @@ def prn_decode_step(x, W, bias, a, state_out, *, cell: str, state_in=None, h_out
     d_h = W.shape[0] // G
     if a is None and cell not in GATED_CELLS:
         raise ValueError(f"the cell {cell!r} has recurrent weights a")
+    if isinstance(bias, torch.Tensor) and bias.dim() != 1 and bias.numel() == G * d_h and bias.is_contiguous():
+        bias = bias.view(-1)
     state = (Bn, S, d_h)
     p = prn_params(CELLS[cell], code, Bn, 1, d_in, d_h, 0, _arg(a, "a", f32, (G, d_h), dev), None, None, 0,
                    _handle(stream, dev))

@@ -166,3 +166,20 @@ def test_decode_steps_captured_in_a_graph(cell, dtype):
         torch.cuda.synchronize()
         assert torch.equal(got_h, hs) and torch.equal(got_c, carry[steps % 2]), rep
         say(f"  replay {rep}: equal to eager")
+
+
+@pytest.mark.parametrize("cell", ["gru", "lstm", "glr", "glri"])
+def test_a_bias_by_gates(cell):
+    """A bias of (G, d_h) is the one of G * d_h values; one of another count is refused."""
+    G, S, slots, d_in, d_h = B.GATES[cell], B.STATE[cell], 5, 24, 20
+    g = torch.Generator().manual_seed(3)
+    new = lambda *s: torch.randn(*s, generator=g).cuda()   # noqa: E731
+    x, W, bias, state = new(slots, d_in), new(G * d_h, d_in) / 5, new(G * d_h), new(slots, S, d_h)
+    a = None if cell in B.GATED_CELLS else new(G, d_h)
+    flat, by_gates = torch.empty_like(state), torch.empty_like(state)
+    B.prn_decode_step(x, W, bias, a, flat, cell=cell, state_in=state)
+    B.prn_decode_step(x, W, bias.view(G, d_h), a, by_gates, cell=cell, state_in=state)
+    assert torch.equal(flat, by_gates)
+    for bad in (bias[:-1], new(G * d_h + 1), bias.view(G, d_h).t()):
+        with pytest.raises(ValueError):
+            B.prn_decode_step(x, W, bad, a, flat, cell=cell, state_in=state)
