@@ -131,6 +131,7 @@ class LinearTokenModel(torch.nn.Module):
             layer.alpha = new(width, scale=0.3, kind=torch.float32)
             self.layers.append(layer)
         self.w_out = torch.nn.Parameter(torch.ones(width, device="cuda"))
+        self.register_buffer("waits", torch.zeros(1, dtype=torch.int32, device="cuda"), persistent=False)
 
     def _block(self, layer, x, h, n, seed, offset):
         """The rest of a block after its recurrence: the stream x behind it."""
@@ -145,7 +146,7 @@ class LinearTokenModel(torch.nn.Module):
         for i, layer in enumerate(self.layers):
             _, n = prn.block_norm_apply(x, w_pre=layer.w_pre)
             h = prn.gated_scan_apply(prn.input_proj_apply(n, layer.W, layer.bias, cell=self.cell), cell=self.cell,
-                                     cu_seqlens=cu_seqlens)
+                                     cu_seqlens=cu_seqlens, error_out=self.waits)
             x = self._block(layer, x, h, n, seed, step * len(self.layers) + i)
         return prn.block_norm_apply(x, w_pre=self.w_out)[1]
 
@@ -193,8 +194,10 @@ def train(model, tokens, targets, steps, lr=3e-3, log=None, seed=None):
         optimizer.zero_grad(set_to_none=True)
         loss = model.loss(tokens, targets, z_loss=1e-4, **({} if seed is None else dict(seed=seed, step=i)))
         loss.backward()
-        optimizer.step()
         losses.append(loss.item())
+        if isinstance(model, LinearTokenModel):
+            prn.check_waits(model.waits)   # a wait that gave up has left NaN (newton_apply raises by itself)
+        optimizer.step()
         if log and (i % 5 == 0 or i == steps - 1):
             log(f"step {i:3d}  loss {losses[-1]:.4f}")
     return losses

@@ -17,7 +17,7 @@ from .api import (  # noqa: F401
     RESIDUAL_WARN,
     forward, forward_fused, gate_residual, input_proj, input_proj_apply, newton_apply, newton_forward, resolve_k,
     sequential_forward, validate_cu_seqlens, verify_agreement,
-    gated_scan, gated_scan_apply, gated_scan_backward,
+    check_waits, gated_scan, gated_scan_apply, gated_scan_backward,
 )
 from .lm import (  # noqa: F401
     block_norm, block_norm_apply, block_norm_backward, embed, embed_apply, embed_backward, vocab_loss,

@@ -364,8 +364,14 @@ def input_proj_apply(x, W, bias=None, *, cell: str):
 
 # ------------------------------------------------------------------ gated linear recurrence ---
 # The recurrence that is linear in its state needs no Newton iteration: one scan, exact, without a residual to
-# gate, and so without a host synchronisation.  (Where a wait of few long chains for the chunk before gives up, as
-# LookbackTimeoutError has it, the results are NaN from there on; binding.prn_gated_scan's error_out tells.)
+# gate, and so without a host synchronisation.  Where a wait of few long chains for the chunk before gives up, as
+# LookbackTimeoutError has it, the results are NaN from there on and the call's error_out is set, if it has one: a
+# program looks at it where it waits for the device anyway (check_waits), before it uses the gradients.
+
+def check_waits(error_out, what: str = "gated_scan") -> None:
+    """Raises LookbackTimeoutError if the error word that gated scans were given is set.  Waits for the device."""
+    _check_error_word(int(error_out.item()), what)
+
 
 def _aligned(t):
     """t as a dense tensor that starts on 16 bytes (None for None)."""
@@ -397,7 +403,7 @@ def _scan_workspace(n: int, device):
     return torch.empty(n, dtype=torch.uint8, device=device) if n else None
 
 
-def gated_scan(xproj, *, cell: str, h0=None, cu_seqlens=None, return_state=False):
+def gated_scan(xproj, *, cell: str, h0=None, cu_seqlens=None, return_state=False, error_out=None):
     """The gated linear recurrence over projected inputs (B, T, G, d), from input_proj with the same cell:
 
         "glr"   G = 2, rows f, v:       h' = s(f) h + (1 - s(f)) v
@@ -406,7 +412,7 @@ def gated_scan(xproj, *, cell: str, h0=None, cu_seqlens=None, return_state=False
     s the logistic function.  H (B, T, d), with return_state also the final states (rows, 1, d); h0 (rows, 1, d)
     or None for zeros.  A ragged pack has B = 1 and cu_seqlens: int32 offsets on the device are used without a look
     at them (they may end before T, as in a pack of a fixed size: H is zero behind them), anything else is validated
-    first.  The state is fp32 within a call."""
+    first.  The state is fp32 within a call.  error_out: one int32 on the device, zero, or None (check_waits)."""
     _check_gated(xproj, cell)
     xproj, h0 = _aligned(xproj), _aligned(h0)
     Bn, T, _, d = xproj.shape
@@ -415,13 +421,14 @@ def gated_scan(xproj, *, cell: str, h0=None, cu_seqlens=None, return_state=False
     H = xproj.new_empty((Bn, T, d))
     last = xproj.new_empty((n_seqs or Bn, 1, d)) if return_state else None
     ws = _scan_workspace(B_.prn_gated_scan_workspace_bytes(cell, xproj.dtype, Bn, T, d, n_seqs), xproj.device)
-    B_.prn_gated_scan(xproj, H, cell=cell, h0=h0, cu_seqlens=cu, state_last_out=last, workspace=ws)
+    B_.prn_gated_scan(xproj, H, cell=cell, h0=h0, cu_seqlens=cu, state_last_out=last, workspace=ws, error_out=error_out)
     return (H, last) if return_state else H
 
 
-def gated_scan_backward(dH, xproj, H, *, cell: str, h0=None, cu_seqlens=None, dstate=None, want_h0: bool = True):
+def gated_scan_backward(dH, xproj, H, *, cell: str, h0=None, cu_seqlens=None, dstate=None, want_h0: bool = True,
+                        error_out=None):
     """Gradients (dxproj, dh0) of gated_scan from dH (B, T, d) and dstate (rows, 1, d), that of the final states, or
-    None for zero; H is the forward's.  dh0 is None without h0, or where it is not wanted."""
+    None for zero; H is the forward's.  dh0 is None without h0, or where it is not wanted.  error_out as there."""
     _check_gated(xproj, cell)
     xproj, h0, H, dH, dstate = (_aligned(t) for t in (xproj, h0, H, dH, dstate))
     Bn, T, _, d = xproj.shape
@@ -431,17 +438,17 @@ def gated_scan_backward(dH, xproj, H, *, cell: str, h0=None, cu_seqlens=None, ds
     dh0 = torch.empty_like(h0) if h0 is not None and want_h0 else None
     ws = _scan_workspace(B_.prn_gated_scan_backward_workspace_bytes(cell, xproj.dtype, Bn, T, d, n_seqs), xproj.device)
     B_.prn_gated_scan_backward(xproj, H, dH, dxproj, cell=cell, h0=h0, cu_seqlens=cu, dstate_last=dstate, dh0_out=dh0,
-                               workspace=ws)
+                               workspace=ws, error_out=error_out)
     return dxproj, dh0
 
 
 class _GatedScanFunction(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, xproj, h0, cell, cu, with_state):
-        out = gated_scan(xproj, cell=cell, h0=h0, cu_seqlens=cu, return_state=with_state)
+    def forward(ctx, xproj, h0, cell, cu, with_state, error_out):
+        out = gated_scan(xproj, cell=cell, h0=h0, cu_seqlens=cu, return_state=with_state, error_out=error_out)
         H = out[0] if with_state else out
         ctx.save_for_backward(xproj, h0, H, cu)
-        ctx.cell = cell
+        ctx.cell, ctx.error_out = cell, error_out
         ctx.set_materialize_grads(False)
         return out
 
@@ -451,12 +458,13 @@ class _GatedScanFunction(torch.autograd.Function):
         dH = torch.zeros_like(H) if dH is None else dH.to(xproj.dtype)
         dstate = None if dstate is None else dstate.to(xproj.dtype)
         dxproj, dh0 = gated_scan_backward(dH, xproj, H, cell=ctx.cell, h0=h0, cu_seqlens=cu, dstate=dstate,
-                                          want_h0=ctx.needs_input_grad[1])
-        return *_first((dxproj, dh0), dH, dstate, xproj, h0), None, None, None
+                                          want_h0=ctx.needs_input_grad[1], error_out=ctx.error_out)
+        return *_first((dxproj, dh0), dH, dstate, xproj, h0), None, None, None, None
 
 
-def gated_scan_apply(xproj, *, cell: str, h0=None, cu_seqlens=None, return_state=False):
-    """Differentiable gated_scan: gradients of H and of the final states reach xproj and h0."""
+def gated_scan_apply(xproj, *, cell: str, h0=None, cu_seqlens=None, return_state=False, error_out=None):
+    """Differentiable gated_scan: gradients of H and of the final states reach xproj and h0.  error_out is set by
+    the waits of both passes."""
     _check_gated(xproj, cell)
     cu = _pack_offsets(cu_seqlens, xproj.shape[1], xproj.device)
-    return _GatedScanFunction.apply(xproj, h0, cell, cu, bool(return_state))
+    return _GatedScanFunction.apply(xproj, h0, cell, cu, bool(return_state), error_out)

@@ -163,3 +163,35 @@ def test_a_captured_training_step():
         torch.cuda.synchronize()
         assert torch.equal(out, want), k
         assert all(torch.equal(held[n], eager[n]) for n in held), k
+
+
+def test_a_wait_that_gives_up_raises(monkeypatch):
+    """PRN_SPIN_LIMIT=0: every wait of both passes gives up at once.  The call's error word is set, check_waits raises,
+    and a training step ends there, with the weights as they were."""
+    ex = _example()
+    prn = ex.prn
+    g = torch.Generator(device="cuda").manual_seed(9)
+    x = torch.randn(1, 3000, 2, 64, generator=g, device="cuda").requires_grad_()
+    words = [torch.zeros(1, dtype=torch.int32, device="cuda") for _ in range(3)]
+    torch.manual_seed(7)
+    model = ex.LinearTokenModel(100, 32, 1, 48)
+    before = [p.detach().clone() for p in model.parameters()]
+    tokens, targets = ex.chain(1, 1000, 100, g)
+    H = prn.gated_scan_apply(x, cell="glr", error_out=words[0])
+    torch.autograd.grad(H.sum(), x)
+    prn.check_waits(words[0])
+
+    H = prn.gated_scan_apply(x, cell="glr", error_out=words[0])
+    monkeypatch.setenv("PRN_SPIN_LIMIT", "0")
+    torch.autograd.grad(H.sum(), x)   # of the backward pass
+    prn.gated_scan_apply(x, cell="glr", error_out=words[1])
+    prn.gated_scan_backward(torch.ones_like(H), x.detach(), H.detach(), cell="glr", error_out=words[2])
+    for word in words:
+        with pytest.raises(prn.LookbackTimeoutError, match="gated_scan"):
+            prn.check_waits(word)
+    with pytest.raises(prn.LookbackTimeoutError):
+        ex.train(model, tokens, targets, 2, seed=1)
+    assert all(torch.equal(p, q) for p, q in zip(model.parameters(), before))
+    monkeypatch.delenv("PRN_SPIN_LIMIT")
+    model.waits.zero_()
+    ex.train(model, tokens, targets, 2, seed=1)
