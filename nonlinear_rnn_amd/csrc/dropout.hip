@@ -78,11 +78,11 @@ struct Eight {
   }
 };
 
+// out may be x or residual: an element is read and written by one thread, which reads first
 template <int DT, bool RES, bool PAST>
-__global__ void __launch_bounds__(256) k_dropout(const typename Storage<DT>::T* __restrict__ x,
-                                                 const typename Storage<DT>::T* __restrict__ residual, int64_t n,
-                                                 uint32_t drop, float scale, uint64_t seed, uint64_t offset,
-                                                 const int64_t* __restrict__ state, typename Storage<DT>::T* __restrict__ out) {
+__global__ void __launch_bounds__(256) k_dropout(const typename Storage<DT>::T* x, const typename Storage<DT>::T* residual,
+                                                 int64_t n, uint32_t drop, float scale, uint64_t seed, uint64_t offset,
+                                                 const int64_t* __restrict__ state, typename Storage<DT>::T* out) {
   using ST = Storage<DT>;
   using E = Eight<typename ST::T>;
   const int64_t block = block_in_rows() * 256 + threadIdx.x, i0 = 8 * block, left = n - i0;

@@ -141,3 +141,24 @@ def test_offsets_past_32_bits():
         words = gated.philox(np.arange(at // 8, at // 8 + 8, dtype=np.int64), 3, 11)
         keep = np.stack([words & 0xFFFF, words >> 16], -1).reshape(-1) >= round(0.25 * 65536)
         assert np.array_equal(out[at:at + 64].float().cpu().numpy() != 0, keep)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n", [1, 8, 13, 5003, 1 << 20, (1 << 26) + 5])
+def test_in_place_over_every_operand(n, dtype):
+    """The result over x, over the residual, and over a tensor that is both, for each launch there is."""
+    g = torch.Generator(device="cuda").manual_seed(n)
+    x, r = (torch.randn(n, generator=g, device="cuda").to(dtype) for _ in range(2))
+    want, alone, both = (prn.dropout(x, 0.3, seed=6, residual=q) for q in (r, None, x))
+    out = x.clone()
+    B.prn_dropout(out, out, p=0.3, seed=6, residual=r)
+    assert torch.equal(out, want)
+    out.copy_(r)
+    B.prn_dropout(x, out, p=0.3, seed=6, residual=out)
+    assert torch.equal(out, want)
+    out.copy_(x)
+    B.prn_dropout(out, out, p=0.3, seed=6)
+    assert torch.equal(out, alone)
+    out.copy_(x)
+    B.prn_dropout(out, out, p=0.3, seed=6, residual=out)
+    assert torch.equal(out, both)
