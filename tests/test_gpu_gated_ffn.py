@@ -216,3 +216,39 @@ def test_gradients_of_the_longest_rows(N, F, dtype):
     other, _ = prn.gated_ffn_backward(dout.flip(0), x.flip(0), W, want_W=False)
     assert torch.isfinite(dx).all() and torch.equal(dx, other.flip(0))
     assert len(torch.unique(dx, dim=0)) == N
+
+
+# fp32 with more than 256 channels and at least 192 tiles of 256 tokens x 128 outputs: the gradients' 256-row tiles,
+# 192 columns wide, and (500 and 512 channels) 256
+LARGE_FP32 = [(5003, 517, 1387), (6144, 264, 1024), (12289, 260, 513), (3333, 384, 1900), (49157, 257, 33), (6200, 500, 1000),
+              (6144, 512, 1024)]
+
+
+@pytest.mark.parametrize("N,d,F", LARGE_FP32)
+def test_large_tiles_of_fp32(N, d, F):
+    _check(*_case(N, d, F, torch.float32, seed=d), "silu", torch.float32)
+
+
+@pytest.mark.parametrize("d", [264, 505])   # 192 columns and 256
+def test_what_is_not_finite_on_large_tiles_of_fp32(d):
+    N, F = 6151, 1030
+    x, W, dout = _case(N, d, F, torch.float32)
+    out, (dx, dW) = prn.gated_ffn(x, W), prn.gated_ffn_backward(dout, x, W)
+    for bad in (float("nan"), float("inf"), float("-inf")):
+        y, g, V = x.clone(), dout.clone(), W.clone()
+        y[300, 5] = bad
+        out2, (dx2, _) = prn.gated_ffn(y, W), prn.gated_ffn_backward(dout, y, W)
+        rest = torch.arange(N, device="cuda") != 300
+        assert torch.equal(out2[rest], out[rest]) and torch.equal(dx2[rest], dx[rest])
+        assert not torch.isfinite(out2[300]).all() and not torch.isfinite(dx2[300]).all()
+        g[6150, 1029] = bad   # the last output of the last token
+        dx2, dW2 = prn.gated_ffn_backward(g, x, W)
+        assert torch.equal(dx2[:-1], dx[:-1]) and not torch.isfinite(dx2[-1]).any()
+        same = torch.ones(2 * F, dtype=torch.bool, device="cuda")
+        same[1029] = same[F + 1029] = False
+        assert torch.equal(dW2[same], dW[same]) and not torch.isfinite(dW2[~same]).any()
+        V[700, 100] = bad   # an output's gate
+        out2, (_, dW2) = prn.gated_ffn(x, V), prn.gated_ffn_backward(dout, x, V)
+        same[:] = True
+        same[700] = same[F + 700] = False
+        assert torch.equal(out2[:, same[:F]], out[:, same[:F]]) and torch.equal(dW2[same], dW[same])
