@@ -525,3 +525,27 @@ def test_a_step_whose_gate_is_too_small_for_a_normal_number(dtype):
     assert torch.equal(out[..., shut], want[..., shut])
     z, one = torch.stack([xf, v]).expand(3, 1, 2, len(xf)), np.ones((3, 1, len(xf)))
     _close("state", out, gated.gated_scan("glr", _np(z), one)[1], gated.gated_scan_bounds("glr", _np(z), one)["last"], dtype)
+
+
+# ------------------------------------------------------------------ projections in bf16 ---
+
+@pytest.mark.parametrize("cell", ["glr", "glri"])
+@pytest.mark.parametrize("Bn,T,d_in,d", [(2, 50, 32, 24), (1, 300, 72, 40), (3, 129, 16, 7), (1, 4096, 64, 128)])
+def test_projection_in_bf16_both_ways(cell, Bn, T, d_in, d):
+    """Products of bf16 values are exact in fp32, a sum of n of them is off by (n + 8) 2^-24 of their magnitudes, and
+    every result but the bias's gradient is rounded once to bf16."""
+    g = torch.Generator().manual_seed(T)
+    new = lambda *s: torch.randn(*s, generator=g)   # noqa: E731
+    x, W = new(Bn, T, d_in).bfloat16().cuda().requires_grad_(), (new(G[cell] * d, d_in) / d_in ** 0.5).bfloat16().cuda().requires_grad_()
+    bias, dz = new(G[cell] * d).cuda().requires_grad_(), new(Bn, T, G[cell], d).bfloat16().cuda()
+    z = prn.input_proj_apply(x, W, bias, cell=cell)
+    dx, dW, db = torch.autograd.grad(z, (x, W, bias), dz)
+    M = Bn * T
+    xd, Wd, bd, dzd = _np(x).reshape(M, -1), _np(W), _np(bias), _np(dz).reshape(M, -1)
+    ax, aW, adz = np.abs(xd), np.abs(Wd), np.abs(dzd)
+    for name, got, want, size, n, dtype in (
+            ("z", z, xd @ Wd.T + bd, ax @ aW.T + np.abs(bd), d_in + 1, torch.bfloat16),
+            ("dx", dx, dzd @ Wd, adz @ aW, G[cell] * d, torch.bfloat16),
+            ("dW", dW, dzd.T @ xd, adz.T @ ax, M, torch.bfloat16),
+            ("dbias", db, dzd.sum(0), adz.sum(0), M, torch.float32)):
+        _close(name, got.reshape(want.shape), want, (n + 8) * size, dtype)
