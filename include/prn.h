@@ -318,7 +318,8 @@ size_t prn_backward_workspace_bytes(const prn_params* params);
  * its buffers pinned.  The result equals prn_input_proj + prn_sequential_forward
  * on the same token up to the summation order of the projection.  The gated
  * linear cells take the projected values in fp32, without rounding them to the
- * storage dtype in between (a gate next to 1 would lose most of 1 - f).
+ * storage dtype in between, as prn_input_proj and prn_gated_scan do: with bf16
+ * the gates of the two differ by up to 2^-8 |x_f| of 1 - f.
  * Errors (nothing is launched): PRN_ERR_INVALID_ARG for T != 1, a ragged pack
  * (n_seqs > 0), d_in < 1, NULL x / W / a / state_out, a pointer not aligned
  * to its element size, or state_in == state_out. */
@@ -535,8 +536,9 @@ size_t prn_gated_scan_workspace_bytes(const prn_params* params);
  *   dstate_last  (rows, d_h) storage dtype, or NULL for zero
  *   dxproj_out   (B, T, G, d_h) storage dtype
  *   dh0_out      (rows, d_h) storage dtype, or NULL
- * The states are formed again in fp32, from H at every 64th to 160th step.  params as for
- * the forward, its workspace prn_gated_scan_backward_workspace_bytes(params). */
+ * The states are formed again in fp32, from H at every 64th to 160th step: with bf16
+ * h_{t-1} is off by that H's rounding as far as the gates since have kept it.  params as
+ * for the forward, its workspace prn_gated_scan_backward_workspace_bytes(params). */
 prn_status prn_gated_scan_backward(const void* xproj, const prn_params* params, const void* h0, const int32_t* cu_seqlens,
                                    const void* H, const void* dH, const void* dstate_last, void* dxproj_out,
                                    void* dh0_out);

@@ -23,8 +23,11 @@
 // besides).
 //
 // The gradient needs h_{t-1}: it is formed again from x and the stored H of
-// the step before a chunk (so only one step of a chunk sees H's rounding),
-// which reads a value per step less than stored states would.
+// the step before a chunk, which reads a value per step less than stored states
+// would.  That H's rounding (bf16: 2^-8 of it at most) stays in the chunk's
+// states as long as the gates keep it, so dx_f = lam (h_{t-1} - v) f (1 - f) is off
+// by the same lam f (1 - f) times what is left of it, with one sign over 64 to 160
+// steps; stored states of H's type would each have a rounding of their own.
 //
 // A sequence's first step in a pack cuts the map: h_in does not count, whatever
 // it is (a NaN of the sequence before stays there).  Since a >= 0 otherwise,
@@ -144,8 +147,9 @@ struct Tensors {
 // that order: the same operations, so the bits do not depend on which state it
 // found.  Workgroups take their chunks by ticket, the chunks of a chain in the
 // order of its walk, so a chunk waits for chunks with smaller tickets only,
-// which have started.  Every wait ends: after spin_limit polls without progress
-// the carry is NaN, the error word is set, and the chunk goes on.
+// which have started.  Every wait ends: after spin_limit polls in all that found
+// a chunk without a record (looking further back is none of them) the carry is
+// NaN, the error word is set, and the chunk goes on.
 //
 // A record's words are written and read at the device's coherence point (relaxed
 // atomics of agent scope); a wave's stores have been acknowledged before it
@@ -705,7 +709,7 @@ constexpr Shape shape_of(bool back, bool pass) {
 // has a CU to itself, so it is taken where it makes fewer steps of rounds of the
 // device.  us, 20011 x 250 fp32 glri in 37 sequences (four chains): forward 20 steps, one round,
 // 26, 16 steps, two, 35; backward 10 steps, two rounds, 43, 8 steps, three, 48.
-// (24 steps 35; 12 steps backward 57.)
+// (24 steps 35; 12 steps backward 57.)  The two lengths are of this shape alone.
 template <int G, int V>
 constexpr Shape longer_of(bool back) {
   const Shape s = shape_of<G, V>(back, true);
